@@ -303,6 +303,81 @@ int decode_attn_read_error(const da_plan* plan, int32_t* code, void* stream);
 int decode_attn_copy_plan(const da_plan* plan, int32_t* n_splits, int32_t* split_begin,
                           int32_t* n_work, int32_t* work, void* stream);
 
+/* ---- writing the caches ---------------------------------------------- */
+
+#define DA_X_F32 0  /* projections given as fp32 */
+#define DA_X_BF16 1 /* projections given as bf16 */
+
+/* Rotation of queries and keys by their positions.  For a token at position p
+ * every pair j = 0 .. dim/2 - 1 of the rotated dims of a head is turned by the
+ * angle p * inv_freq[j] (the exact product of the integer and the fp32 number;
+ * reduced in fp64, so far positions lose nothing):
+ *     a' = gain * (a cos - b sin),   b' = gain * (b cos + a sin)    (fp32)
+ * with (a, b) = dims (offset + j, offset + dim/2 + j), or, interleaved,
+ * (offset + 2j, offset + 2j + 1).  The head's other dims are copied. */
+typedef struct da_rope {
+  int32_t dim;           /* rotated dims: a multiple of 16; 0: no rotation    */
+  int32_t offset;        /* first of them within a head: a multiple of 8      */
+  int32_t interleaved;   /* 0 or 1: how dims pair up                          */
+  float gain;            /* finite; 1 for a plain rotation                    */
+  const float* inv_freq; /* device fp32 [dim / 2]                             */
+} da_rope;
+
+/* The new tokens of one decode_attn_append call.  Plain data. */
+typedef struct da_append {
+  int32_t n_tokens;         /* >= 0                                           */
+  int32_t x_dtype;          /* DA_X_* of k_new, v_new and q_new               */
+  const void* k_new;        /* [n_tokens, H_kv, D_qk]                         */
+  const void* v_new;        /* [n_tokens, H_kv, D_v]; NULL for a shared latent */
+  const void* q_new;        /* [n_tokens, H_q, D_qk], or NULL: no queries     */
+  int64_t k_stride;         /* elements from one token to the next, at least  */
+  int64_t v_stride;         /* a token's own, so that the three may be parts  */
+  int64_t q_stride;         /* of one fused projection's rows                 */
+  const int32_t* positions; /* int32 [n_tokens]                               */
+  const int32_t* rows;      /* int32 [n_tokens] or NULL (see below)           */
+  const int32_t* table;     /* paged: the page table that attention reads     */
+  void* k;                  /* the caches, as decode_attn_run takes them      */
+  void* v;
+  void* q_out;              /* bf16 [n_tokens, H_q, D_qk], contiguous         */
+  int32_t* err;             /* device word for DA_DEVERR_* bits, or NULL      */
+} da_append;
+
+/* Write new keys and values into the caches that decode_attn_run reads, keys
+ * rotated by `rope` (NULL: no rotation), and rotate the queries of the same
+ * tokens into q_out: the step of a decode or prompt pass between the
+ * projections and attention.  `prob` is the problem given to decode_attn_plan;
+ * it fixes head counts and dims, layout, page size, table width, cache size,
+ * element type and scales (its extra_* fields do not matter here: to write a
+ * second source's cache, describe that cache as an indexed problem).
+ *
+ * Where token i goes:
+ *   contiguous, paged: entry positions[i] of batch row rows[i] (rows NULL: row
+ *     i, then n_tokens <= batch), found like attention finds it;
+ *   indexed: slot rows[i] of the cache (rows required); positions[i] only
+ *     rotates.
+ * rows[i] < 0 marks a padded token: nothing is read from the table and nothing
+ * is written for it, its q_out row included.  The same is done, and a bit set
+ * in *err, for a negative position or one at or above the row's capacity
+ * (DA_DEVERR_LENGTH) and for a row, slot or page id out of range
+ * (DA_DEVERR_INDEX).  Bits are OR-ed into *err, never cleared.  Two tokens of a
+ * call must not go to the same entry: that entry's contents are unspecified.
+ *
+ * What is stored, from the fp32 values v (rotated or copied):
+ *   bf16:  v rounded to nearest even;
+ *   E4M3:  v / scale (fp32 division), rounded to nearest even, magnitudes above
+ *          448 stored as 448, NaN as NaN;
+ *   NVFP4: block scale s = e4m3(max|v| / (6 * scale)) over each 16 elements and
+ *          codes e2m1(v / (s * scale)), all fp32, rounded to nearest even and
+ *          saturated; a block whose s is 0 stores zero codes and one that holds
+ *          a NaN gets the NaN block scale.
+ * scale is k_scale for keys (and for a shared latent row) and v_scale for
+ * values.  A token's stored bytes and its q_out row depend on that token alone.
+ *
+ * Alignment: the five data pointers 16 bytes, strides multiples of 16 bytes.
+ * q_out must not overlap q_new.  One launch, no workspace. */
+int decode_attn_append(const da_problem* prob, const da_rope* rope, const da_append* args,
+                       void* stream);
+
 #ifdef __cplusplus
 }
 #endif

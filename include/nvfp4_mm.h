@@ -94,6 +94,106 @@ int nvfp4_mm(const void* x, int32_t x_dtype, const uint8_t* codes, const uint8_t
  * when its first kernel starts; reading clears it too). */
 int nvfp4_mm_read_error(void* ws, int32_t* code, void* stream);
 
+/* ---- low-rank adapters of many requests ------------------------------- */
+
+#define NVFP4_ADAPTER_MAX_RANK 128
+
+/* Device workspace bytes of one nvfp4_mm_adapters call (0: shape not
+ * supported): a 256-byte header and the fp32 products t.  Needs no
+ * initialisation. */
+size_t nvfp4_mm_adapters_workspace_bytes(int32_t n, int32_t N, int32_t K, int32_t n_adapters,
+                                         int32_t max_rank);
+
+/* Add each row's own low-rank adapter to the output of a matmul that all rows
+ * share (nvfp4_mm's y):
+ *
+ *     t[i, r]   = sum_k bf16(x[i, k]) * A[id, r, k]                  (fp32)
+ *     out[i, o] = y[i, o] + sum_{r < rank[id]} (scale[id] * t[i, r]) * B[id, o, r]
+ *
+ * with id = ids[i]; a row whose id is negative has no adapter, out = y.  Both
+ * sums run on the tensor cores with fp32 accumulation over exact products: t
+ * enters the second one as three bf16 terms that hold its 24 bits.  Orders are
+ * fixed by K and the rank alone, so a row's bits depend only on its own x, y
+ * and adapter, not on n, on its place or on the other rows.
+ *   x       [n, K], fp32 or bf16 as x_dtype (NVFP4_X_*) says, 16-byte aligned.
+ *   a       bf16 [n_adapters, max_rank, K], b  bf16 [n_adapters, N, max_rank],
+ *           16-byte aligned.
+ *   ranks   int32 [n_adapters] or NULL (all max_rank).  What a and b hold at or
+ *           beyond an adapter's rank has no effect on the result.
+ *   scales  fp32 [n_adapters] or NULL (all 1).
+ *   ids     int32 [n].
+ *   y, out  fp32 [n, N], 16-byte aligned; out may be y (rows without an adapter
+ *           are then not touched) but must not overlap it otherwise.
+ *   out_bf16  bf16 [n, N] or NULL, 8-byte aligned: out rounded to nearest even,
+ *           all rows.
+ *   ws      as for nvfp4_mm.
+ * An id at or above n_adapters counts as none and sets DA_DEVERR_INDEX, a rank
+ * outside [0, max_rank] is clamped and sets DA_DEVERR_LENGTH; read the bits of
+ * the last call with nvfp4_mm_read_error(ws, ...).
+ * Supported shapes: n >= 0, N a positive multiple of NVFP4_MM_TILE_N, K a
+ * positive multiple of 64, max_rank a multiple of 16 up to
+ * NVFP4_ADAPTER_MAX_RANK, n_adapters >= 1; n * K, n * N below 2^31. */
+int nvfp4_mm_adapters(const void* x, int32_t x_dtype, int32_t n, int32_t N, int32_t K,
+                      const void* a, const void* b, int32_t n_adapters, int32_t max_rank,
+                      const int32_t* ranks, const float* scales, const int32_t* ids,
+                      const float* y, float* out, void* out_bf16, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/* ---- logits ------------------------------------------------------------ */
+
+/* What a decode step does to the logits of its vocabulary projection (nvfp4_mm's
+ * y or y_bf16).  Plain data; a NULL list is an empty one. */
+typedef struct nvfp4_logits {
+  int32_t batch;             /* B >= 0 rows                                    */
+  int32_t vocab;             /* V tokens, 1 .. 2^30                              */
+  int32_t x_dtype;           /* NVFP4_X_* of x                                 */
+  const void* x;             /* [B, V], rows x_stride elements apart           */
+  int64_t x_stride;          /* >= V                                           */
+  const int32_t* prompt;     /* int32 [B, prompt_width]: the prompt's tokens   */
+  const int32_t* prompt_lens; /* int32 [B]                                     */
+  int32_t prompt_width;
+  const int32_t* output;     /* int32 [B, output_width]: tokens generated      */
+  const int32_t* output_lens; /* int32 [B]                                     */
+  int32_t output_width;
+  const float* repetition;   /* fp32 [B] or NULL (1): divides / multiplies     */
+  const float* frequency;    /* fp32 [B] or NULL (0): per occurrence           */
+  const float* presence;     /* fp32 [B] or NULL (0): once                     */
+  const int32_t* bias_tokens; /* int32 [B, bias_width]                         */
+  const float* bias_values;  /* fp32 [B, bias_width]                           */
+  const int32_t* bias_lens;  /* int32 [B]                                      */
+  int32_t bias_width;
+  const uint32_t* mask;      /* [n_masks, ceil(V / 32)]: bit v % 32 of word    */
+                             /* v / 32 set: token v may come                   */
+  const int32_t* mask_ids;   /* int32 [B]: the row's mask, negative: none;     */
+                             /* NULL: row b has mask b                         */
+  int32_t n_masks;
+  float* out;                /* fp32 [B, V], rows out_stride apart, or NULL    */
+  int64_t out_stride;        /* >= V                                           */
+  int32_t* tokens;           /* int32 [B] or NULL                              */
+  int32_t* err;              /* device word for DA_DEVERR_* bits, or NULL      */
+} nvfp4_logits;
+
+/* For every row b and token v, in fp32 with one rounding for each operation:
+ *
+ *     l = x[b, v]
+ *     v in the row's prompt or output:  l = l > 0 ? l / repetition : l * repetition
+ *     v in its output, c times:         l = l - frequency * c;  l = l - presence
+ *     v among its bias tokens:          l = l + (its bias values, added in order)
+ *     the row's mask has v's bit clear: l = -inf
+ *     out[b, v] = l
+ *     tokens[b] = the lowest v among those with the largest l > -inf, or -1 if
+ *                 there is none (every token masked, or -inf or NaN)
+ *
+ * A row's results depend on that row alone.  out may be x itself (fp32, same
+ * stride); any other overlap is not allowed.  List entries at or past a row's
+ * length are never read.  A length below 0 or above its width is clamped and
+ * sets DA_DEVERR_LENGTH; a token outside [0, V) is skipped and a mask id at or
+ * above n_masks counts as none, both set DA_DEVERR_INDEX.  Bits are OR-ed into
+ * *err, never cleared.  Alignment: that of the element types; rows that start
+ * on 16-byte boundaries (x, out) move in wider accesses.  One launch, no
+ * workspace. */
+int nvfp4_mm_logits(const nvfp4_logits* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

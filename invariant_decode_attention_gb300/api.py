@@ -35,11 +35,17 @@ EXPORTS = (
     "decode_attn_copy_plan", "decode_attn_forward_static", "decode_attn_plan_extra",
     "decode_attn_run_extra", "decode_attn_forward_extra",
     "nvfp4_mm_workspace_bytes", "nvfp4_mm", "nvfp4_mm_read_error",
+    "decode_attn_append", "nvfp4_mm_adapters_workspace_bytes", "nvfp4_mm_adapters",
+    "nvfp4_mm_logits",
 )
 
 # NVFP4 weight matmul (include/nvfp4_mm.h)
 NVFP4_TILE_N, NVFP4_ROW_TILE, NVFP4_K_CHUNK = 128, 32, 1024
 NVFP4_X_F32, NVFP4_X_BF16 = 0, 1
+
+# Cache append (include/decode_attn.h) and adapters (include/nvfp4_mm.h)
+X_F32, X_BF16 = 0, 1
+ADAPTER_MAX_RANK = 128
 
 # Size of the fixed device array decode_attn_forward_static uses as scratch.
 STATIC_WORKSPACE_BYTES = 64 << 20
@@ -88,6 +94,66 @@ class DaPlan(ctypes.Structure):
         ("off_item_desc", ctypes.c_uint64),
         ("off_lse_part", ctypes.c_uint64),
         ("off_o_part", ctypes.c_uint64),
+    ]
+
+
+class DaRope(ctypes.Structure):
+    _fields_ = [
+        ("dim", ctypes.c_int32),
+        ("offset", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("gain", ctypes.c_float),
+        ("inv_freq", ctypes.c_void_p),
+    ]
+
+
+class DaAppend(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32),
+        ("k_new", ctypes.c_void_p),
+        ("v_new", ctypes.c_void_p),
+        ("q_new", ctypes.c_void_p),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("q_stride", ctypes.c_int64),
+        ("positions", ctypes.c_void_p),
+        ("rows", ctypes.c_void_p),
+        ("table", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p),
+        ("err", ctypes.c_void_p),
+    ]
+
+
+class Nvfp4Logits(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("vocab", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32),
+        ("x", ctypes.c_void_p),
+        ("x_stride", ctypes.c_int64),
+        ("prompt", ctypes.c_void_p),
+        ("prompt_lens", ctypes.c_void_p),
+        ("prompt_width", ctypes.c_int32),
+        ("output", ctypes.c_void_p),
+        ("output_lens", ctypes.c_void_p),
+        ("output_width", ctypes.c_int32),
+        ("repetition", ctypes.c_void_p),
+        ("frequency", ctypes.c_void_p),
+        ("presence", ctypes.c_void_p),
+        ("bias_tokens", ctypes.c_void_p),
+        ("bias_values", ctypes.c_void_p),
+        ("bias_lens", ctypes.c_void_p),
+        ("bias_width", ctypes.c_int32),
+        ("mask", ctypes.c_void_p),
+        ("mask_ids", ctypes.c_void_p),
+        ("n_masks", ctypes.c_int32),
+        ("out", ctypes.c_void_p),
+        ("out_stride", ctypes.c_int64),
+        ("tokens", ctypes.c_void_p),
+        ("err", ctypes.c_void_p),
     ]
 
 
@@ -147,6 +213,15 @@ def lib():
     L.nvfp4_mm.argtypes = [vp, i32, vp, vp, ctypes.c_float, i32, i32, i32, vp, vp, vp, sz, vp]
     L.nvfp4_mm_read_error.restype = ctypes.c_int
     L.nvfp4_mm_read_error.argtypes = [vp, P(i32), vp]
+    L.decode_attn_append.restype = ctypes.c_int
+    L.decode_attn_append.argtypes = [P(DaProblem), P(DaRope), P(DaAppend), vp]
+    L.nvfp4_mm_adapters_workspace_bytes.restype = sz
+    L.nvfp4_mm_adapters_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    L.nvfp4_mm_adapters.restype = ctypes.c_int
+    L.nvfp4_mm_adapters.argtypes = [vp, i32, i32, i32, i32, vp, vp, i32, i32, vp, vp, vp, vp, vp,
+                                    vp, vp, sz, vp]
+    L.nvfp4_mm_logits.restype = ctypes.c_int
+    L.nvfp4_mm_logits.argtypes = [P(Nvfp4Logits), vp]
     _LIB = L
     return L
 
@@ -457,3 +532,266 @@ def run_nvfp4(m, ws=None, y=None, y_bf16=None, stream=None):
     """nvfp4_mm on a ``workloads.Nvfp4Matmul`` whose tensors are on the GPU."""
     return nvfp4_mm(m.x, m.codes, m.scales, m.global_scale, y=y, y_bf16=y_bf16, ws=ws,
                     stream=stream)
+
+
+# ------------------------------------------- around a decode step: append, adapters, logits
+
+_X_DTYPES = {torch.float32: X_F32, torch.bfloat16: X_BF16}
+
+
+def _addr(t, name, device, dtype, shape=None):
+    """Address of a contiguous tensor of `dtype` on `device` (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _launch(device, stream, call):
+    """call(stream handle) with `device` current; `stream` defaults to the
+    device's current torch stream."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, got {device} (no CPU path)")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    if torch.cuda.current_device() == device.index:
+        return call(stream.cuda_stream)
+    with torch.cuda.device(device):
+        return call(stream.cuda_stream)
+
+
+def rope(inv_freq: torch.Tensor, *, offset=0, interleaved=False, gain=1.0) -> DaRope:
+    """The rotation of a head's dims [offset, offset + 2 * len(inv_freq)): pair j
+    turns by position * inv_freq[j] (see da_rope).  inv_freq: fp32, on the
+    device; the returned description keeps it alive."""
+    if inv_freq.dim() != 1:
+        raise ValueError(f"inv_freq must be a vector, got {tuple(inv_freq.shape)}")
+    r = DaRope(2 * inv_freq.numel(), offset, int(bool(interleaved)), gain,
+               _addr(inv_freq, "inv_freq", inv_freq.device, torch.float32))
+    r.keep = inv_freq
+    return r
+
+
+def _head_rows(t, name, n, heads, dim, device, dtype):
+    """(address, token stride) of projections [n, heads, dim] whose tokens may
+    lie apart (a part of a fused projection's rows)."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype} like k_new, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.shape != (n, heads, dim):
+        raise ValueError(f"{name} must have shape {(n, heads, dim)}, got {tuple(t.shape)}")
+    token, head, one = t.stride()
+    if (one != 1 and dim > 1) or (head != dim and heads > 1):
+        raise ValueError(f"{name}: a token's heads must lie together, strides {t.stride()}")
+    return t.data_ptr(), token if n > 1 else heads * dim
+
+
+def _cache_addr(t, name, device, prob, entries, dim):
+    """Address of a cache of `entries` entries, checked for its type and size."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.dtype not in ((torch.bfloat16,) if prob.kv_dtype == KV_BF16 else _KV[1:]):
+        raise ValueError(f"{name} has the wrong element type {t.dtype}")
+    need = entries * prob.num_kv_heads * dim
+    have = t.numel()
+    if prob.kv_dtype == KV_NVFP4:  # codes; the block scales follow in the same storage
+        need = need // 2 + need // 16
+        have = t.untyped_storage().nbytes() - t.storage_offset()
+    if have < need:
+        raise ValueError(f"{name} holds {have} elements, the problem's cache has {need}")
+    return t.data_ptr()
+
+
+def append(prob: DaProblem, rope, k_new, v_new, k, v, positions, *, rows=None, table=None,
+           q_new=None, q_out=None, err=None, stream=None):
+    """New keys and values, keys rotated, into the caches that ``forward`` reads,
+    and the same tokens' queries rotated (decode_attn_append).
+
+    prob: the problem given to ``plan`` / ``forward``; rope: from ``rope()`` or
+    None; k_new, v_new: fp32 or bf16 [n, H_kv, D] (v_new and v None for a shared
+    latent cache), q_new: [n, H_q, D] or None -- parts of a fused projection's
+    rows are taken as they lie; positions: int32 [n]; rows: int32 [n], the batch
+    row of each token (None: token i is row i) or, for the indexed layout, its
+    slot -- negative: a padded token, nothing is written; table: the page table;
+    err: int32 [1] that device error bits are OR-ed into.  Returns q_out (bf16
+    [n, H_q, D], made when not given; rows of padded tokens are not written) or
+    None without queries.
+    """
+    device = k_new.device
+    n, dtype = k_new.shape[0], k_new.dtype
+    x_dtype = _X_DTYPES.get(dtype)
+    if x_dtype is None:
+        raise ValueError(f"k_new must be float32 or bfloat16, got {dtype}")
+    if (v_new is None) != bool(prob.shared_latent) or (v is None) != (v_new is None):
+        raise ValueError("v_new and v: both for separate caches, none for a shared latent one")
+    if q_new is None and q_out is not None:
+        raise ValueError("q_out without q_new")
+    D, Hkv = prob.head_dim_qk, prob.num_kv_heads
+    entries = (prob.batch * prob.width if prob.layout == CONTIGUOUS else
+               prob.num_blocks * prob.page_size if prob.layout == PAGED else prob.num_blocks)
+    a = DaAppend(n_tokens=n, x_dtype=x_dtype)
+    a.k_new, a.k_stride = _head_rows(k_new, "k_new", n, Hkv, D, device, dtype)
+    a.k = _cache_addr(k, "k", device, prob, entries, D)
+    if v_new is not None:
+        a.v_new, a.v_stride = _head_rows(v_new, "v_new", n, Hkv, prob.head_dim_v, device, dtype)
+        a.v = _cache_addr(v, "v", device, prob, entries, prob.head_dim_v)
+    if q_new is not None:
+        shape = (n, prob.num_q_heads, D)
+        a.q_new, a.q_stride = _head_rows(q_new, "q_new", *shape, device, dtype)
+        if q_out is None:
+            q_out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        a.q_out = _addr(q_out, "q_out", device, torch.bfloat16, shape)
+    a.positions = _addr(positions, "positions", device, torch.int32, (n,))
+    a.rows = _addr(rows, "rows", device, torch.int32, (n,))
+    if prob.layout == PAGED:
+        if table is None:
+            raise ValueError("a paged cache needs its table")
+        a.table = _addr(table, "table", device, torch.int32, (prob.batch, prob.width))
+    a.err = _addr(err, "err", device, torch.int32)
+    if rope is not None and rope.keep.device != device:
+        raise ValueError(f"inv_freq is on {rope.keep.device}, expected {device}")
+    _check(_launch(device, stream, lambda s: lib().decode_attn_append(prob, rope, a, s)), "append")
+    return q_out
+
+
+class Adapters:
+    """Low-rank adapters held side by side: a bf16 [count, max_rank, K], b bf16
+    [count, N, max_rank], ranks int32 [count] (None: all max_rank), scales fp32
+    [count] (None: all 1).  Checked once, here."""
+
+    def __init__(self, a, b, ranks=None, scales=None):
+        if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+            raise ValueError(f"a {tuple(a.shape)} and b {tuple(b.shape)} must be [count, max_rank, "
+                             "K] and [count, N, max_rank]")
+        self.device = a.device
+        self.count, self.max_rank, self.K = a.shape
+        self.N = b.shape[1]
+        self.a, self.b, self.ranks, self.scales = a, b, ranks, scales  # kept alive
+        self.ptrs = (_addr(a, "a", self.device, torch.bfloat16),
+                     _addr(b, "b", self.device, torch.bfloat16), self.count, self.max_rank,
+                     _addr(ranks, "ranks", self.device, torch.int32, (self.count,)),
+                     _addr(scales, "scales", self.device, torch.float32, (self.count,)))
+
+
+def adapters_workspace_bytes(n: int, N: int, K: int, count: int, max_rank: int) -> int:
+    """Workspace bytes of one ``nvfp4_adapters`` call (0: shape not supported)."""
+    return int(lib().nvfp4_mm_adapters_workspace_bytes(n, N, K, count, max_rank))
+
+
+def adapters_workspace(n: int, N: int, K: int, adapters: Adapters) -> torch.Tensor:
+    nb = adapters_workspace_bytes(n, N, K, adapters.count, adapters.max_rank)
+    if nb == 0:
+        raise DecodeAttnError(ERR_UNSUPPORTED, f"adapters shape n={n} N={N} K={K} "
+                              f"max_rank={adapters.max_rank}")
+    return torch.empty(nb, dtype=torch.uint8, device=adapters.device)
+
+
+def nvfp4_adapters(x, adapters: Adapters, ids, y, *, out=None, out_bf16=None, ws=None, stream=None):
+    """out = y + each row's own low-rank adapter of x (nvfp4_mm_adapters).
+
+    x: fp32 or bf16 [n, K], what ``nvfp4_mm`` got; y: fp32 [n, N], what it
+    returned; ids: int32 [n], negative: no adapter; out: None writes into y;
+    out_bf16: also filled when given.  Returns out.  A row's bits depend on its
+    own x, y and adapter only.  Device error bits: ``nvfp4_read_error(ws)``.
+    """
+    n, K = x.shape
+    device, N = adapters.device, adapters.N
+    x_dtype = _X_DTYPES.get(x.dtype)
+    if x_dtype is None:
+        raise ValueError(f"x must be float32 or bfloat16, got {x.dtype}")
+    if K != adapters.K:
+        raise ValueError(f"x has {K} columns, the adapters {adapters.K}")
+    if out is None:
+        out = y
+    if ws is None:
+        ws = adapters_workspace(n, N, K, adapters)
+    shape = (n, N)
+    args = (_addr(x, "x", device, x.dtype), x_dtype, n, N, K, *adapters.ptrs,
+            _addr(ids, "ids", device, torch.int32, (n,)),
+            _addr(y, "y", device, torch.float32, shape),
+            _addr(out, "out", device, torch.float32, shape),
+            _addr(out_bf16, "out_bf16", device, torch.bfloat16, shape),
+            _addr(ws, "ws", device, torch.uint8), ws.numel())
+    _check(_launch(device, stream, lambda s: lib().nvfp4_mm_adapters(*args, s)), "nvfp4_adapters")
+    return out
+
+
+def _rows_of(t, name, B, V, device, dtype):
+    """(address, row stride) of a [B, V] tensor whose rows are contiguous."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.shape != (B, V):
+        raise ValueError(f"{name} must have shape {(B, V)}, got {tuple(t.shape)}")
+    if t.stride(1) != 1 and V > 1:
+        raise ValueError(f"{name}: rows must be contiguous, strides {t.stride()}")
+    return t.data_ptr(), t.stride(0) if B > 1 else V
+
+
+def nvfp4_logits(x, *, prompt=None, prompt_lens=None, output=None, output_lens=None,
+                 repetition=None, frequency=None, presence=None, bias_tokens=None,
+                 bias_values=None, bias_lens=None, mask=None, mask_ids=None, out=None,
+                 tokens=None, err=None, stream=None):
+    """Penalties, biases and masks on logits, and the greedy token of each row
+    (nvfp4_mm_logits; the order of the steps is stated there).
+
+    x: fp32 or bf16 [B, V], rows may lie apart; prompt, output, bias_tokens:
+    int32 [B, width] with their int32 [B] lengths; repetition, frequency,
+    presence: fp32 [B]; bias_values fp32 [B, width]; mask: int32 or uint32
+    [n_masks, ceil(V / 32)] bits of the tokens that may come, mask_ids int32 [B]
+    (negative: any token; None: row b has mask b); out: fp32 [B, V], may be x;
+    None: the adjusted logits are not written.  Returns tokens, int32 [B] (made
+    when not given), -1 where no token may come.
+    """
+    B, V = x.shape
+    device = x.device
+    x_dtype = _X_DTYPES.get(x.dtype)
+    if x_dtype is None:
+        raise ValueError(f"x must be float32 or bfloat16, got {x.dtype}")
+    if tokens is None:
+        tokens = torch.empty(B, dtype=torch.int32, device=device)
+    g = Nvfp4Logits(batch=B, vocab=V, x_dtype=x_dtype)
+    g.x, g.x_stride = _rows_of(x, "x", B, V, device, x.dtype)
+    for name, t, lens in (("prompt", prompt, prompt_lens), ("output", output, output_lens),
+                          ("bias", bias_tokens, bias_lens)):
+        if t is None and lens is None:
+            continue
+        if t is None or lens is None:
+            raise ValueError(f"{name}: tokens and lengths belong together")
+        width = t.shape[-1]
+        setattr(g, name + ("_tokens" if name == "bias" else ""),
+                _addr(t, name, device, torch.int32, (B, width)))
+        setattr(g, name + "_lens", _addr(lens, name + "_lens", device, torch.int32, (B,)))
+        setattr(g, name + "_width", width)
+    if (bias_values is None) != (bias_tokens is None):
+        raise ValueError("bias_tokens and bias_values belong together")
+    if bias_values is not None:
+        g.bias_values = _addr(bias_values, "bias_values", device, torch.float32, bias_tokens.shape)
+    g.repetition = _addr(repetition, "repetition", device, torch.float32, (B,))
+    g.frequency = _addr(frequency, "frequency", device, torch.float32, (B,))
+    g.presence = _addr(presence, "presence", device, torch.float32, (B,))
+    if mask is not None:
+        if mask.dtype not in (torch.int32, torch.uint32) or mask.dim() != 2:
+            raise ValueError("mask must be a matrix of 32-bit words")
+        g.n_masks = mask.shape[0]
+        g.mask = _addr(mask, "mask", device, mask.dtype, (g.n_masks, -(-V // 32)))
+    g.mask_ids = _addr(mask_ids, "mask_ids", device, torch.int32, (B,))
+    if out is not None:
+        g.out, g.out_stride = _rows_of(out, "out", B, V, device, torch.float32)
+    g.tokens = _addr(tokens, "tokens", device, torch.int32, (B,))
+    g.err = _addr(err, "err", device, torch.int32)
+    _check(_launch(device, stream, lambda s: lib().nvfp4_mm_logits(g, s)), "nvfp4_logits")
+    return tokens

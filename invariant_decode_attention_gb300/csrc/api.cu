@@ -7,6 +7,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "append.cuh"
 #include "common.cuh"
 #include "merge.cuh"
 
@@ -489,6 +490,105 @@ int decode_attn_copy_plan(const da_plan* plan, int32_t* n_splits, int32_t* split
     e = cudaMemcpyAsync(work, ws + plan->off_work, 4 * B * ms, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   return e == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}
+
+int decode_attn_append(const da_problem* prob, const da_rope* rope, const da_append* args,
+                       void* stream) {
+  int rc = check_problem(prob);
+  if (rc != DA_OK) return rc;
+  if (!args || args->n_tokens < 0) return DA_ERR_INVALID_ARG;
+  if (args->x_dtype != DA_X_F32 && args->x_dtype != DA_X_BF16) return DA_ERR_INVALID_ARG;
+  const bool turns = rope && rope->dim != 0;
+  if (rope) {
+    if (rope->dim < 0 || rope->dim % 16 || rope->offset < 0 || rope->offset % 8 ||
+        rope->dim > prob->head_dim_qk - rope->offset)
+      return DA_ERR_INVALID_ARG;
+    if ((rope->interleaved != 0 && rope->interleaved != 1) || !std::isfinite(rope->gain))
+      return DA_ERR_INVALID_ARG;
+    if (turns && (!rope->inv_freq || !aligned(rope->inv_freq, 4))) return DA_ERR_INVALID_ARG;
+  }
+  Variant var;  // only what a kernel of this library reads can be written
+  da_problem one = *prob;
+  one.extra_width = 0;
+  rc = select_variant(&one, &var);
+  if (rc != DA_OK) return rc;
+  const da_append& a = *args;
+  if (a.n_tokens == 0) return DA_OK;
+  const bool latent = prob->shared_latent != 0;
+  const long long n = a.n_tokens, D = prob->head_dim_qk;
+  const long long q_row = prob->num_q_heads * D, kv_row = prob->num_kv_heads * D;
+  const long long esize = a.x_dtype == DA_X_BF16 ? 2 : 4;
+  if (!a.k_new || !a.k || !a.positions || latent != (a.v_new == nullptr) ||
+      (!latent && !a.v) || (a.q_new != nullptr) != (a.q_out != nullptr))
+    return DA_ERR_INVALID_ARG;
+  if (prob->layout == DA_KV_PAGED && !a.table) return DA_ERR_INVALID_ARG;
+  if (prob->layout == DA_KV_INDEXED && !a.rows) return DA_ERR_INVALID_ARG;
+  if (!a.rows && a.n_tokens > prob->batch) return DA_ERR_INVALID_ARG;
+  const void* ptr16[6] = {a.k_new, a.v_new, a.q_new, a.k, a.v, a.q_out};
+  for (const void* q : ptr16)
+    if (q && !aligned(q, 16)) return DA_ERR_INVALID_ARG;
+  if (!aligned(a.positions, 4) || (a.rows && !aligned(a.rows, 4)) ||
+      (a.table && !aligned(a.table, 4)) || (a.err && !aligned(a.err, 4)))
+    return DA_ERR_INVALID_ARG;
+  const long long strides[3] = {a.k_stride, a.v_new ? a.v_stride : kv_row,
+                                a.q_new ? a.q_stride : q_row};
+  const long long least[3] = {kv_row, kv_row, q_row};
+  for (int i = 0; i < 3; ++i) {
+    if (strides[i] < least[i] || strides[i] > (1LL << 40)) return DA_ERR_INVALID_ARG;
+    if (strides[i] * esize % 16) return DA_ERR_INVALID_ARG;
+  }
+  if (a.q_new) {  // other threads read what a rotated element's thread writes
+    const uintptr_t src = reinterpret_cast<uintptr_t>(a.q_new);
+    const uintptr_t dst = reinterpret_cast<uintptr_t>(a.q_out);
+    const uintptr_t src_end = src + ((n - 1) * a.q_stride + q_row) * esize;
+    if (dst < src_end && src < dst + n * q_row * 2) return DA_ERR_INVALID_ARG;
+  }
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DA_ERR_CUDA;
+  const int sms = sm_count(dev);
+  if (sms <= 0) return DA_ERR_CUDA;
+  AppendLaunch L;
+  std::memset(&L, 0, sizeof(L));
+  L.k_new = a.k_new;
+  L.v_new = a.v_new;
+  L.q_new = a.q_new;
+  L.k_stride = a.k_stride;
+  L.v_stride = a.v_stride;
+  L.q_stride = a.q_stride;
+  L.positions = a.positions;
+  L.rows = a.rows;
+  L.table = a.table;
+  L.k = a.k;
+  L.v = a.v;
+  L.q_out = static_cast<__nv_bfloat16*>(a.q_out);
+  L.err = a.err;
+  L.num_blocks = prob->num_blocks;
+  L.capacity = row_capacity(prob->layout, prob->width, prob->page_size);
+  L.kv_rows = (prob->layout == DA_KV_CONTIGUOUS) ? (long long)prob->batch * prob->width
+              : (prob->layout == DA_KV_PAGED)    ? prob->num_blocks * prob->page_size
+                                                 : prob->num_blocks;
+  L.n_tokens = a.n_tokens;
+  L.x_bf16 = a.x_dtype == DA_X_BF16;
+  L.B = prob->batch;
+  L.H_q = prob->num_q_heads;
+  L.H_kv = prob->num_kv_heads;
+  L.D = prob->head_dim_qk;
+  L.layout = prob->layout;
+  L.page_size = prob->page_size;
+  L.width = prob->width;
+  L.kv_type = prob->kv_dtype;
+  L.gain = 1.f;
+  if (turns) {
+    L.rope_dim = rope->dim;
+    L.rope_offset = rope->offset;
+    L.interleaved = rope->interleaved;
+    L.gain = rope->gain;
+    L.inv_freq = rope->inv_freq;
+  }
+  L.k_scale = prob->k_scale;
+  L.v_scale = prob->v_scale;
+  return launch_append(L, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DA_OK
+                                                                                 : DA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -30,6 +30,10 @@ What it computes and where that is stated:
   ``bf16(x) @ W^T`` that both kernel shapes of a weight matmul agree on.
   Source: "Greedy outputs depend on batch composition" (gllm issue #98),
   Candidate cause and Next steps.
+* ``step`` -- what surrounds attention in a decode step: rotation and storage of
+  new keys and values, low-rank adapters beside a weight matmul, and the
+  adjustment of logits with the greedy pick (plain definitions of the library's
+  own operators; the pages have no counterpart).
 * ``bf16`` -- exact fp64 -> bf16 round-to-nearest-even, used to state the
   output rounding and the tolerance in units of bf16 ULP (same page,
   Measurement: "1-2 ULP of bf16 near 1.0").
@@ -38,4 +42,4 @@ Parity pins (``tests/test_oracle_*.py``) tie every function to closed forms,
 brute force and invariants; no function here is "parity unpinned".
 """
 
-from . import attention, plan, bf16, fp8, nvfp4  # noqa: F401
+from . import attention, plan, bf16, fp8, nvfp4, step  # noqa: F401
