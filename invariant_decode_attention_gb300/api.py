@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -214,14 +215,14 @@ def lib():
     L.nvfp4_mm_read_error.restype = ctypes.c_int
     L.nvfp4_mm_read_error.argtypes = [vp, P(i32), vp]
     L.decode_attn_append.restype = ctypes.c_int
-    L.decode_attn_append.argtypes = [P(DaProblem), P(DaRope), P(DaAppend), vp]
+    L.decode_attn_append.argtypes = [vp, vp, vp, vp]  # addresses, or packed bytes
     L.nvfp4_mm_adapters_workspace_bytes.restype = sz
     L.nvfp4_mm_adapters_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
     L.nvfp4_mm_adapters.restype = ctypes.c_int
     L.nvfp4_mm_adapters.argtypes = [vp, i32, i32, i32, i32, vp, vp, i32, i32, vp, vp, vp, vp, vp,
                                     vp, vp, sz, vp]
     L.nvfp4_mm_logits.restype = ctypes.c_int
-    L.nvfp4_mm_logits.argtypes = [P(Nvfp4Logits), vp]
+    L.nvfp4_mm_logits.argtypes = [vp, vp]
     _LIB = L
     return L
 
@@ -536,37 +537,67 @@ def run_nvfp4(m, ws=None, y=None, y_bf16=None, stream=None):
 
 # ------------------------------------------- around a decode step: append, adapters, logits
 
+# These calls sit between small kernels of a decode step, so their host time
+# counts: arguments are checked with few attribute reads (the reason for a
+# refusal is looked for only once there is one), descriptors are packed in one
+# go, and the stream comes as a raw handle.  Measured on the GPU host, append of
+# one token: 15.6 us a call with a ctypes field per argument and
+# torch.cuda.current_stream(), see _APPEND below for the packed form.
+
 _X_DTYPES = {torch.float32: X_F32, torch.bfloat16: X_BF16}
+_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+# da_append and nvfp4_logits, field by field, with C's alignment
+_APPEND = struct.Struct("@iiPPPqqqPPPPPPP")
+_LOGITS = struct.Struct("@iiiPqPPiPPiPPPPPPiPPiPqPP")
 
 
-def _addr(t, name, device, dtype, shape=None):
-    """Address of a contiguous tensor of `dtype` on `device` (None stays None)."""
-    if t is None:
-        return None
+def _where(dev):
+    return f"cuda:{dev}" if dev >= 0 else "the CPU"
+
+
+def _refuse(t, name, dev, dtype, shape):
+    """Raise for a tensor that is not what a call takes."""
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {_where(dev)}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} has strides that the call does not take: {t.stride()} (most tensors "
+                     "must be contiguous; a token's heads and a row of logits must lie together)")
 
 
-def _launch(device, stream, call):
-    """call(stream handle) with `device` current; `stream` defaults to the
-    device's current torch stream."""
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be on a CUDA device, got {device} (no CPU path)")
+def _addr(t, name, dev, dtype, shape=None):
+    """Address of a contiguous tensor of `dtype` on device `dev` (None: 0)."""
+    if t is None:
+        return 0
+    if (t.dtype is dtype and t.get_device() == dev and (shape is None or t.shape == shape)
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, name, dev, dtype, shape)
+
+
+def _call(fn, where, dev, stream, *args):
+    """fn(*args, stream) with device `dev` current; the default is the device's
+    current torch stream."""
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device (no CPU path)")
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    if torch.cuda.current_device() == device.index:
-        return call(stream.cuda_stream)
-    with torch.cuda.device(device):
-        return call(stream.cuda_stream)
+        handle = _raw_stream(dev)
+    elif stream.device.index == dev:
+        handle = stream.cuda_stream
+    else:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {_where(dev)}")
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, handle)
+    if status != OK:
+        raise DecodeAttnError(status, where)
 
 
 def rope(inv_freq: torch.Tensor, *, offset=0, interleaved=False, gain=1.0) -> DaRope:
@@ -576,39 +607,35 @@ def rope(inv_freq: torch.Tensor, *, offset=0, interleaved=False, gain=1.0) -> Da
     if inv_freq.dim() != 1:
         raise ValueError(f"inv_freq must be a vector, got {tuple(inv_freq.shape)}")
     r = DaRope(2 * inv_freq.numel(), offset, int(bool(interleaved)), gain,
-               _addr(inv_freq, "inv_freq", inv_freq.device, torch.float32))
+               _addr(inv_freq, "inv_freq", inv_freq.get_device(), _F32))
     r.keep = inv_freq
     return r
 
 
-def _head_rows(t, name, n, heads, dim, device, dtype):
+def _heads(t, name, dev, dtype, shape):
     """(address, token stride) of projections [n, heads, dim] whose tokens may
     lie apart (a part of a fused projection's rows)."""
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype} like k_new, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.shape != (n, heads, dim):
-        raise ValueError(f"{name} must have shape {(n, heads, dim)}, got {tuple(t.shape)}")
-    token, head, one = t.stride()
-    if (one != 1 and dim > 1) or (head != dim and heads > 1):
-        raise ValueError(f"{name}: a token's heads must lie together, strides {t.stride()}")
-    return t.data_ptr(), token if n > 1 else heads * dim
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape:
+        n, heads, dim = shape
+        token, head, one = t.stride()
+        if (one == 1 or dim == 1) and (head == dim or heads == 1):
+            return t.data_ptr(), token if n > 1 else heads * dim
+    _refuse(t, name, dev, dtype, shape)
 
 
-def _cache_addr(t, name, device, prob, entries, dim):
-    """Address of a cache of `entries` entries, checked for its type and size."""
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+def _cache(t, name, dev, kv_dtype, need):
+    """Address of a cache of at least `need` elements of the problem's type."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {_where(dev)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.dtype not in ((torch.bfloat16,) if prob.kv_dtype == KV_BF16 else _KV[1:]):
+    if (t.dtype is not _BF16) if kv_dtype == KV_BF16 else (t.dtype not in _KV[1:]):
         raise ValueError(f"{name} has the wrong element type {t.dtype}")
-    need = entries * prob.num_kv_heads * dim
-    have = t.numel()
-    if prob.kv_dtype == KV_NVFP4:  # codes; the block scales follow in the same storage
+    if kv_dtype == KV_NVFP4:  # codes; the block scales follow in the same storage
         need = need // 2 + need // 16
         have = t.untyped_storage().nbytes() - t.storage_offset()
+    else:
+        have = t.numel()
     if have < need:
         raise ValueError(f"{name} holds {have} elements, the problem's cache has {need}")
     return t.data_ptr()
@@ -629,40 +656,49 @@ def append(prob: DaProblem, rope, k_new, v_new, k, v, positions, *, rows=None, t
     [n, H_q, D], made when not given; rows of padded tokens are not written) or
     None without queries.
     """
-    device = k_new.device
-    n, dtype = k_new.shape[0], k_new.dtype
+    dev, dtype, n = k_new.get_device(), k_new.dtype, k_new.shape[0]
     x_dtype = _X_DTYPES.get(dtype)
     if x_dtype is None:
         raise ValueError(f"k_new must be float32 or bfloat16, got {dtype}")
-    if (v_new is None) != bool(prob.shared_latent) or (v is None) != (v_new is None):
-        raise ValueError("v_new and v: both for separate caches, none for a shared latent one")
-    if q_new is None and q_out is not None:
-        raise ValueError("q_out without q_new")
-    D, Hkv = prob.head_dim_qk, prob.num_kv_heads
-    entries = (prob.batch * prob.width if prob.layout == CONTIGUOUS else
-               prob.num_blocks * prob.page_size if prob.layout == PAGED else prob.num_blocks)
-    a = DaAppend(n_tokens=n, x_dtype=x_dtype)
-    a.k_new, a.k_stride = _head_rows(k_new, "k_new", n, Hkv, D, device, dtype)
-    a.k = _cache_addr(k, "k", device, prob, entries, D)
-    if v_new is not None:
-        a.v_new, a.v_stride = _head_rows(v_new, "v_new", n, Hkv, prob.head_dim_v, device, dtype)
-        a.v = _cache_addr(v, "v", device, prob, entries, prob.head_dim_v)
+    D, heads, layout, kv_dtype = prob.head_dim_qk, prob.num_kv_heads, prob.layout, prob.kv_dtype
+    entries = (prob.num_blocks * prob.page_size if layout == PAGED else
+               prob.batch * prob.width if layout == CONTIGUOUS else prob.num_blocks)
+    shape = (n, heads, D)
+    k_ptr, k_stride = _heads(k_new, "k_new", dev, dtype, shape)
+    kc_ptr = _cache(k, "k", dev, kv_dtype, entries * heads * D)
+    if prob.shared_latent:
+        if v_new is not None or v is not None:
+            raise ValueError("v_new and v: none for a shared latent cache")
+        v_ptr = v_stride = vc_ptr = 0
+    else:
+        if v_new is None or v is None:
+            raise ValueError("v_new and v: both for separate caches")
+        v_ptr, v_stride = _heads(v_new, "v_new", dev, dtype, shape)
+        vc_ptr = _cache(v, "v", dev, kv_dtype, entries * heads * D)
+    q_ptr = q_stride = qo_ptr = 0
     if q_new is not None:
         shape = (n, prob.num_q_heads, D)
-        a.q_new, a.q_stride = _head_rows(q_new, "q_new", *shape, device, dtype)
+        q_ptr, q_stride = _heads(q_new, "q_new", dev, dtype, shape)
         if q_out is None:
-            q_out = torch.empty(shape, dtype=torch.bfloat16, device=device)
-        a.q_out = _addr(q_out, "q_out", device, torch.bfloat16, shape)
-    a.positions = _addr(positions, "positions", device, torch.int32, (n,))
-    a.rows = _addr(rows, "rows", device, torch.int32, (n,))
-    if prob.layout == PAGED:
+            q_out = torch.empty(shape, dtype=_BF16, device=k_new.device)
+        qo_ptr = _addr(q_out, "q_out", dev, _BF16, shape)
+    elif q_out is not None:
+        raise ValueError("q_out without q_new")
+    t_ptr = 0
+    if layout == PAGED:
         if table is None:
             raise ValueError("a paged cache needs its table")
-        a.table = _addr(table, "table", device, torch.int32, (prob.batch, prob.width))
-    a.err = _addr(err, "err", device, torch.int32)
-    if rope is not None and rope.keep.device != device:
-        raise ValueError(f"inv_freq is on {rope.keep.device}, expected {device}")
-    _check(_launch(device, stream, lambda s: lib().decode_attn_append(prob, rope, a, s)), "append")
+        t_ptr = _addr(table, "table", dev, _I32, (prob.batch, prob.width))
+    rope_ptr = None
+    if rope is not None:
+        if rope.keep.get_device() != dev:
+            raise ValueError(f"inv_freq is on {rope.keep.device}, expected {_where(dev)}")
+        rope_ptr = ctypes.addressof(rope)
+    args = _APPEND.pack(n, x_dtype, k_ptr, v_ptr, q_ptr, k_stride, v_stride, q_stride,
+                        _addr(positions, "positions", dev, _I32, (n,)),
+                        _addr(rows, "rows", dev, _I32, (n,)), t_ptr, kc_ptr, vc_ptr, qo_ptr,
+                        _addr(err, "err", dev, _I32))
+    _call(lib().decode_attn_append, "append", dev, stream, ctypes.addressof(prob), rope_ptr, args)
     return q_out
 
 
@@ -675,14 +711,13 @@ class Adapters:
         if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
             raise ValueError(f"a {tuple(a.shape)} and b {tuple(b.shape)} must be [count, max_rank, "
                              "K] and [count, N, max_rank]")
-        self.device = a.device
+        dev = self.dev = a.get_device()
         self.count, self.max_rank, self.K = a.shape
         self.N = b.shape[1]
         self.a, self.b, self.ranks, self.scales = a, b, ranks, scales  # kept alive
-        self.ptrs = (_addr(a, "a", self.device, torch.bfloat16),
-                     _addr(b, "b", self.device, torch.bfloat16), self.count, self.max_rank,
-                     _addr(ranks, "ranks", self.device, torch.int32, (self.count,)),
-                     _addr(scales, "scales", self.device, torch.float32, (self.count,)))
+        self.ptrs = (_addr(a, "a", dev, _BF16), _addr(b, "b", dev, _BF16), self.count, self.max_rank,
+                     _addr(ranks, "ranks", dev, _I32, (self.count,)),
+                     _addr(scales, "scales", dev, _F32, (self.count,)))
 
 
 def adapters_workspace_bytes(n: int, N: int, K: int, count: int, max_rank: int) -> int:
@@ -695,7 +730,7 @@ def adapters_workspace(n: int, N: int, K: int, adapters: Adapters) -> torch.Tens
     if nb == 0:
         raise DecodeAttnError(ERR_UNSUPPORTED, f"adapters shape n={n} N={N} K={K} "
                               f"max_rank={adapters.max_rank}")
-    return torch.empty(nb, dtype=torch.uint8, device=adapters.device)
+    return torch.empty(nb, dtype=torch.uint8, device=adapters.a.device)
 
 
 def nvfp4_adapters(x, adapters: Adapters, ids, y, *, out=None, out_bf16=None, ws=None, stream=None):
@@ -707,10 +742,10 @@ def nvfp4_adapters(x, adapters: Adapters, ids, y, *, out=None, out_bf16=None, ws
     own x, y and adapter only.  Device error bits: ``nvfp4_read_error(ws)``.
     """
     n, K = x.shape
-    device, N = adapters.device, adapters.N
-    x_dtype = _X_DTYPES.get(x.dtype)
+    dev, N, dtype = adapters.dev, adapters.N, x.dtype
+    x_dtype = _X_DTYPES.get(dtype)
     if x_dtype is None:
-        raise ValueError(f"x must be float32 or bfloat16, got {x.dtype}")
+        raise ValueError(f"x must be float32 or bfloat16, got {dtype}")
     if K != adapters.K:
         raise ValueError(f"x has {K} columns, the adapters {adapters.K}")
     if out is None:
@@ -718,27 +753,31 @@ def nvfp4_adapters(x, adapters: Adapters, ids, y, *, out=None, out_bf16=None, ws
     if ws is None:
         ws = adapters_workspace(n, N, K, adapters)
     shape = (n, N)
-    args = (_addr(x, "x", device, x.dtype), x_dtype, n, N, K, *adapters.ptrs,
-            _addr(ids, "ids", device, torch.int32, (n,)),
-            _addr(y, "y", device, torch.float32, shape),
-            _addr(out, "out", device, torch.float32, shape),
-            _addr(out_bf16, "out_bf16", device, torch.bfloat16, shape),
-            _addr(ws, "ws", device, torch.uint8), ws.numel())
-    _check(_launch(device, stream, lambda s: lib().nvfp4_mm_adapters(*args, s)), "nvfp4_adapters")
+    _call(lib().nvfp4_mm_adapters, "nvfp4_adapters", dev, stream, _addr(x, "x", dev, dtype), x_dtype,
+          n, N, K, *adapters.ptrs, _addr(ids, "ids", dev, _I32, (n,)), _addr(y, "y", dev, _F32, shape),
+          _addr(out, "out", dev, _F32, shape), _addr(out_bf16, "out_bf16", dev, _BF16, shape),
+          _addr(ws, "ws", dev, torch.uint8), ws.numel())
     return out
 
 
-def _rows_of(t, name, B, V, device, dtype):
+def _logit_rows(t, name, dev, dtype, shape):
     """(address, row stride) of a [B, V] tensor whose rows are contiguous."""
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.shape != (B, V):
-        raise ValueError(f"{name} must have shape {(B, V)}, got {tuple(t.shape)}")
-    if t.stride(1) != 1 and V > 1:
-        raise ValueError(f"{name}: rows must be contiguous, strides {t.stride()}")
-    return t.data_ptr(), t.stride(0) if B > 1 else V
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape:
+        row, one = t.stride()
+        if one == 1 or shape[1] == 1:
+            return t.data_ptr(), row if shape[0] > 1 else shape[1]
+    _refuse(t, name, dev, dtype, shape)
+
+
+def _list(tokens, lens, name, dev, B):
+    """(tokens, lengths, width) of a ragged list per row, zeros for none."""
+    if tokens is None and lens is None:
+        return 0, 0, 0
+    if tokens is None or lens is None:
+        raise ValueError(f"{name}: tokens and lengths belong together")
+    width = tokens.shape[-1]
+    return (_addr(tokens, name, dev, _I32, (B, width)), _addr(lens, name + "_lens", dev, _I32, (B,)),
+            width)
 
 
 def nvfp4_logits(x, *, prompt=None, prompt_lens=None, output=None, output_lens=None,
@@ -756,42 +795,32 @@ def nvfp4_logits(x, *, prompt=None, prompt_lens=None, output=None, output_lens=N
     None: the adjusted logits are not written.  Returns tokens, int32 [B] (made
     when not given), -1 where no token may come.
     """
-    B, V = x.shape
-    device = x.device
-    x_dtype = _X_DTYPES.get(x.dtype)
+    dev, dtype, shape = x.get_device(), x.dtype, x.shape
+    B, V = shape
+    x_dtype = _X_DTYPES.get(dtype)
     if x_dtype is None:
-        raise ValueError(f"x must be float32 or bfloat16, got {x.dtype}")
+        raise ValueError(f"x must be float32 or bfloat16, got {dtype}")
     if tokens is None:
-        tokens = torch.empty(B, dtype=torch.int32, device=device)
-    g = Nvfp4Logits(batch=B, vocab=V, x_dtype=x_dtype)
-    g.x, g.x_stride = _rows_of(x, "x", B, V, device, x.dtype)
-    for name, t, lens in (("prompt", prompt, prompt_lens), ("output", output, output_lens),
-                          ("bias", bias_tokens, bias_lens)):
-        if t is None and lens is None:
-            continue
-        if t is None or lens is None:
-            raise ValueError(f"{name}: tokens and lengths belong together")
-        width = t.shape[-1]
-        setattr(g, name + ("_tokens" if name == "bias" else ""),
-                _addr(t, name, device, torch.int32, (B, width)))
-        setattr(g, name + "_lens", _addr(lens, name + "_lens", device, torch.int32, (B,)))
-        setattr(g, name + "_width", width)
+        tokens = torch.empty(B, dtype=_I32, device=x.device)
+    row = (B,)
     if (bias_values is None) != (bias_tokens is None):
         raise ValueError("bias_tokens and bias_values belong together")
-    if bias_values is not None:
-        g.bias_values = _addr(bias_values, "bias_values", device, torch.float32, bias_tokens.shape)
-    g.repetition = _addr(repetition, "repetition", device, torch.float32, (B,))
-    g.frequency = _addr(frequency, "frequency", device, torch.float32, (B,))
-    g.presence = _addr(presence, "presence", device, torch.float32, (B,))
+    n_masks = mask_ptr = 0
     if mask is not None:
-        if mask.dtype not in (torch.int32, torch.uint32) or mask.dim() != 2:
+        if mask.dtype not in (_I32, torch.uint32) or mask.dim() != 2:
             raise ValueError("mask must be a matrix of 32-bit words")
-        g.n_masks = mask.shape[0]
-        g.mask = _addr(mask, "mask", device, mask.dtype, (g.n_masks, -(-V // 32)))
-    g.mask_ids = _addr(mask_ids, "mask_ids", device, torch.int32, (B,))
-    if out is not None:
-        g.out, g.out_stride = _rows_of(out, "out", B, V, device, torch.float32)
-    g.tokens = _addr(tokens, "tokens", device, torch.int32, (B,))
-    g.err = _addr(err, "err", device, torch.int32)
-    _check(_launch(device, stream, lambda s: lib().nvfp4_mm_logits(g, s)), "nvfp4_logits")
+        n_masks = mask.shape[0]
+        mask_ptr = _addr(mask, "mask", dev, mask.dtype, (n_masks, -(-V // 32)))
+    out_ptr, out_stride = (0, 0) if out is None else _logit_rows(out, "out", dev, _F32, shape)
+    p_ptr, pl_ptr, p_width = _list(prompt, prompt_lens, "prompt", dev, B)
+    o_ptr, ol_ptr, o_width = _list(output, output_lens, "output", dev, B)
+    b_ptr, bl_ptr, b_width = _list(bias_tokens, bias_lens, "bias_tokens", dev, B)
+    args = _LOGITS.pack(
+        B, V, x_dtype, *_logit_rows(x, "x", dev, dtype, shape), p_ptr, pl_ptr, p_width, o_ptr, ol_ptr,
+        o_width, _addr(repetition, "repetition", dev, _F32, row),
+        _addr(frequency, "frequency", dev, _F32, row), _addr(presence, "presence", dev, _F32, row),
+        b_ptr, _addr(bias_values, "bias_values", dev, _F32, (B, b_width)), bl_ptr, b_width, mask_ptr,
+        _addr(mask_ids, "mask_ids", dev, _I32, row), n_masks, out_ptr, out_stride,
+        _addr(tokens, "tokens", dev, _I32, row), _addr(err, "err", dev, _I32))
+    _call(lib().nvfp4_mm_logits, "nvfp4_logits", dev, stream, args)
     return tokens

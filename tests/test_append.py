@@ -406,6 +406,11 @@ def _args(api, **kw):
     return api.DaAppend(**a)
 
 
+def _append(api, *structs):
+    at = [None if t is None else ctypes.addressof(t) for t in structs]
+    return api.lib().decode_attn_append(*at, None)
+
+
 def _rope(api, **kw):
     r = dict(dim=128, offset=0, interleaved=0, gain=1.0, inv_freq=1 << 20)
     r.update(kw)
@@ -421,8 +426,7 @@ def _prob(api, **kw):
 
 def test_argument_rules(api):
     def call(prob=None, rope=None, **kw):
-        return api.lib().decode_attn_append(prob or _prob(api), rope or _rope(api), _args(api, **kw),
-                                            None)
+        return _append(api, prob or _prob(api), rope or _rope(api), _args(api, **kw))
     bad = api.ERR_INVALID_ARG
     fake = 1 << 20
     assert call(n_tokens=-1) == bad
@@ -451,8 +455,17 @@ def test_argument_rules(api):
     assert call(prob=_prob(api, **latent)) == bad          # a latent cache has no values
     assert call(prob=_prob(api, head_dim_qk=96), rope=_rope(api, dim=64)) == api.ERR_UNSUPPORTED
     assert call(prob=_prob(api, **latent, kv_dtype=api.KV_NVFP4)) == api.ERR_UNSUPPORTED
-    assert api.lib().decode_attn_append(None, None, _args(api), None) == bad
-    assert api.lib().decode_attn_append(_prob(api), None, None, None) == bad
+    assert _append(api, None, None, _args(api)) == bad
+    assert _append(api, _prob(api), None, None) == bad
+
+
+def test_packed_descriptors_match_the_structures(api):
+    for packed, c in ((api._APPEND, api.DaAppend), (api._LOGITS, api.Nvfp4Logits)):
+        values = list(range(1, len(c._fields_) + 1))
+        data = packed.pack(*values)
+        assert len(data) == ctypes.sizeof(c)
+        s = c.from_buffer_copy(data)
+        assert [getattr(s, f[0]) for f in c._fields_] == values
 
 
 def test_python_refusals(api):
@@ -470,9 +483,10 @@ def test_python_refusals(api):
                        a.pop("positions"), **a)
     refused("CUDA device")  # nothing wrong but the place
     refused("float32 or bfloat16", k_new=t(n, 2, 128, dtype=torch.float16))
-    refused("like k_new", v_new=t(n, 2, 128, dtype=torch.float32))
+    refused("v_new", v_new=t(n, 2, 128, dtype=torch.float32))
     refused("shape", k_new=t(n, 2, 64))
     refused("lie together", k_new=t(n, 128, 2).transpose(1, 2))
+    refused("strides", k_new=t(n, 128, 2).transpose(1, 2))
     refused("element type", k=t(40, 16, 2, 128, dtype=torch.uint8))
     refused("holds", k=t(39, 16, 2, 128))
     refused("contiguous", k=t(80, 16, 2, 128)[::2])

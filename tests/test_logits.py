@@ -6,6 +6,8 @@ operations is off by at most 2^-24 of its result; with R the largest magnitude
 on the way (x times or over the repetition penalty, frequency times count, the
 bias), the sum is within 6 * 2^-24 * R."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -300,7 +302,8 @@ def test_argument_rules(api):
         a = dict(batch=2, vocab=1000, x_dtype=api.X_F32, x=fake, x_stride=1000, out=1 << 28,
                  out_stride=1000, tokens=fake)
         a.update(kw)
-        return api.lib().nvfp4_mm_logits(api.Nvfp4Logits(**a), None)
+        g = api.Nvfp4Logits(**a)
+        return api.lib().nvfp4_mm_logits(ctypes.addressof(g), None)
     bad = api.ERR_INVALID_ARG
     assert api.lib().nvfp4_mm_logits(None, None) == bad
     assert call(batch=-1) == bad and call(vocab=0) == bad and call(x_dtype=5) == bad
@@ -335,7 +338,7 @@ def test_python_refusals(api):
             api.nvfp4_logits(x, tokens=kw.pop("tokens", t(2, dtype=i32)), **kw)
     refused("CUDA device")
     refused("float32 or bfloat16", x=t(2, 50, dtype=torch.float16))
-    refused("rows must be contiguous", x=t(2, 100)[:, ::2])
+    refused("strides", x=t(2, 100)[:, ::2])
     refused("belong together", prompt=t(2, 5, dtype=i32))
     refused("belong together", bias_values=t(2, 5))
     refused("prompt", prompt=t(3, 5, dtype=i32), prompt_lens=t(2, dtype=i32))
