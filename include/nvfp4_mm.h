@@ -142,7 +142,8 @@ int nvfp4_mm_adapters(const void* x, int32_t x_dtype, int32_t n, int32_t N, int3
 /* ---- logits ------------------------------------------------------------ */
 
 /* What a decode step does to the logits of its vocabulary projection (nvfp4_mm's
- * y or y_bf16).  Plain data; a NULL list is an empty one. */
+ * y or y_bf16).  Plain data; a NULL list is an empty one; the three widths add
+ * up to 2^30 at most. */
 typedef struct nvfp4_logits {
   int32_t batch;             /* B >= 0 rows                                    */
   int32_t vocab;             /* V tokens, 1 .. 2^30                              */

@@ -2,21 +2,25 @@
 // token, in one pass over each row.
 //
 // A row of V logits is read once and written once (or not at all), so memory
-// bounds a large step and latency a small one.  A cluster of CTAs shares a row:
-// CTA r takes the slices r, r + R, ... of at most kSlice tokens.  For a slice it
-//   1. asks for its logits (they arrive while 2 and 3 run),
-//   2. clears a shared-memory word per token of the slice,
-//   3. goes through the row's prompt and output tokens and records those of the
-//      slice: bit 31 "in the prompt", the low bits the count in the output
-//      (integer atomics: their order does not show), bit 30 "has a bias",
-//   4. adjusts and writes the tokens without a bias, keeping the best,
-//   5. one thread for each bias token that is the first of its kind does the
-//      same for that token, with the values of all its entries added in order.
-// Every CTA of a row reads the row's lists; they come from L2 and are short
-// beside the logits unless the history is longer than the vocabulary.  Best
-// tokens meet as 64-bit keys (ordered value, then lowest token) by shuffles,
-// shared memory, and the cluster's distributed shared memory, so there is no
-// workspace, and the maximum of the keys does not depend on the order.
+// bounds a large step and latency a small one.  One CTA takes a row, or a cluster
+// of CTAs when there are few rows; in each round a CTA takes one slice of up to
+// 32768 tokens,
+//   1. asks for its first logits (they arrive while 2 runs),
+//   2. goes through the row's prompt, output and bias tokens and records those of
+//      the slice in a word of shared memory per token: "in the prompt", the count
+//      in the output, "has a bias" (integer atomics: their order does not show),
+//      and lists them,
+//   3. masks, writes and compares the slice, kDepth loads of a thread in flight.
+//      Listed tokens are written but not compared,
+//   4. goes through the listed tokens: applies the penalties, adds the token's
+//      bias values in their order, writes and compares.
+// Step 4 apart from 3: a text's tokens spread over the vocabulary, and with the
+// penalties in the streaming loop nearly every warp went through them for one
+// lane (256 rows of 131072 tokens: 155 instructions per 128 tokens).  Every CTA
+// of a row reads the row's lists, from L2.
+// Best tokens meet as 64-bit keys (ordered value, then lowest token) by shuffles
+// and shared memory of the cluster, so there is no workspace, and the maximum of
+// the keys does not depend on the order.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -29,11 +33,58 @@ namespace da {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kSlice = 8192;    // tokens per slice at most: 32 KB of shared memory
-constexpr int kPer = kSlice / kThreads;
+constexpr int kTableBytes = 65536;   // shared memory for the words of a slice
+constexpr int kPlainBytes = 24 * 1024;  // with the static arrays: below 48 KB
+constexpr int kListed = 8192;       // tokens with a word that are listed at most
+constexpr int kDense = 3;            // list entries per so many tokens of a slice: many
+constexpr int kScan = 8;           // list entries a thread has in flight
 constexpr int kMaxVocab = 1 << 30;  // keeps token arithmetic in 32 bits
 constexpr int kCluster = 8;     // CTAs per row at most (the portable cluster size)
-constexpr uint32_t kInPrompt = 0x80000000u, kHasBias = 0x40000000u, kCount = 0x3fffffffu;
+
+// A token's word: "in the prompt", "has a bias", "is listed", and its count in
+// the output.  Two bytes do for outputs of up to 2^13 - 1 tokens and double a
+// slice.
+template <typename W>
+struct Word {
+  static constexpr uint32_t kInPrompt = 1u << (8 * sizeof(W) - 1);
+  static constexpr uint32_t kHasBias = kInPrompt >> 1, kListed = kInPrompt >> 2;
+  static constexpr uint32_t kCount = kListed - 1;
+  static constexpr int kMostOutput = (int)kCount;
+  static constexpr int kSlice = std::min<int>(kTableBytes / sizeof(W), 65536);
+
+  // by shared-memory address: the atomics act on the 32 bits around a word
+  static __device__ __forceinline__ void add(uint32_t at) {
+    asm volatile("red.relaxed.cta.shared::cta.add.u32 [%0], %1;" ::"r"(at & ~3u),
+                 "r"(1u << (at & 3u) * 8)
+                 : "memory");
+  }
+  static __device__ __forceinline__ void put(uint32_t at, uint32_t value) {
+    if constexpr (sizeof(W) == 2)
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((unsigned short)value) : "memory");
+    else
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(value) : "memory");
+  }
+  static __device__ __forceinline__ void flag(uint32_t at, uint32_t flags) {
+    asm volatile("red.relaxed.cta.shared::cta.or.b32 [%0], %1;" ::"r"(at & ~3u),
+                 "r"(flags << (at & 3u) * 8)
+                 : "memory");
+  }
+  // Sets `flags` and kListed; whether the token has just become listed, which is
+  // true for one caller only.  A plain look first: hot tokens repeat, and atomics
+  // on one word queue up.
+  static __device__ __forceinline__ bool set(uint32_t at, uint32_t flags) {
+    flags |= kListed;
+    const int shift = (at & 3u) * 8;
+    uint32_t old;
+    asm volatile("ld.volatile.shared::cta.u32 %0, [%1];" : "=r"(old) : "r"(at & ~3u) : "memory");
+    if (((old >> shift) & flags) == flags) return false;
+    asm volatile("atom.relaxed.cta.shared::cta.or.b32 %0, [%1], %2;"
+                 : "=r"(old)
+                 : "r"(at & ~3u), "r"(flags << shift)
+                 : "memory");
+    return !((old >> shift) & kListed);
+  }
+};
 
 struct Args {
   const void* x;
@@ -47,7 +98,7 @@ struct Args {
   const int32_t* mask_ids;
   float* out;
   int32_t *tokens, *err;
-  int V, slice, n_slices, prompt_width, output_width, bias_width, n_masks, mask_words;
+  int V, slice, prompt_width, output_width, bias_width, n_masks, mask_words;
 };
 
 // The key of token v with logit l > -inf (else 0): larger logits first, then
@@ -75,10 +126,12 @@ struct Row {
   float repetition, frequency, presence;
 };
 
-// The penalties on a logit whose token's table word is w.
+// The penalties on a logit whose token's word is w (not zero).
+template <typename W>
 __device__ __forceinline__ float penalised(float l, uint32_t w, const Row& r) {
-  if (w & (kInPrompt | kCount)) l = l > 0.f ? __fdiv_rn(l, r.repetition) : __fmul_rn(l, r.repetition);
-  const uint32_t c = w & kCount;
+  if (w & (Word<W>::kInPrompt | Word<W>::kCount))
+    l = l > 0.f ? __fdiv_rn(l, r.repetition) : __fmul_rn(l, r.repetition);
+  const uint32_t c = w & Word<W>::kCount;
   if (c) {
     l = __fsub_rn(l, __fmul_rn(r.frequency, (float)c));
     l = __fsub_rn(l, r.presence);
@@ -91,185 +144,350 @@ __device__ __forceinline__ float load_x(const void* x, long long i, bool bf16) {
               : static_cast<const float*>(x)[i];
 }
 
-// Logits of VEC consecutive tokens.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// VEC consecutive logits as they lie in memory.
 template <bool BF16, int VEC>
-__device__ __forceinline__ void load_group(const void* x, long long i, float (&l)[VEC]) {
-  if constexpr (VEC == 1) {
-    l[0] = load_x(x, i, BF16);
-  } else if constexpr (BF16) {
-    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(x) + i);
-    l[0] = bf16_lo(w.x), l[1] = bf16_hi(w.x), l[2] = bf16_lo(w.y), l[3] = bf16_hi(w.y);
+struct Group;
+
+template <>
+struct Group<false, 4> {
+  float4 raw;
+  __device__ __forceinline__ void load(const void* p) { raw = *static_cast<const float4*>(p); }
+  __device__ __forceinline__ void get(float (&l)[4]) const {
+    l[0] = raw.x, l[1] = raw.y, l[2] = raw.z, l[3] = raw.w;
+  }
+};
+
+template <>
+struct Group<true, 4> {
+  uint2 raw;
+  __device__ __forceinline__ void load(const void* p) { raw = *static_cast<const uint2*>(p); }
+  __device__ __forceinline__ void get(float (&l)[4]) const {
+    l[0] = bf16_lo(raw.x), l[1] = bf16_hi(raw.x), l[2] = bf16_lo(raw.y), l[3] = bf16_hi(raw.y);
+  }
+};
+
+template <bool BF16>
+struct Group<BF16, 1> {
+  float raw;
+  __device__ __forceinline__ void load(const void* p) { raw = load_x(p, 0, BF16); }
+  __device__ __forceinline__ void get(float (&l)[1]) const { l[0] = raw; }
+};
+
+// The words of VEC consecutive tokens from shared memory.
+template <typename W, int VEC>
+__device__ __forceinline__ void load_words(const W* at, uint32_t (&w)[VEC]) {
+  if constexpr (VEC == 4 && sizeof(W) == 4) {
+    const uint4 t = *reinterpret_cast<const uint4*>(at);
+    w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
+  } else if constexpr (VEC == 4) {
+    const uint2 t = *reinterpret_cast<const uint2*>(at);
+    w[0] = t.x & 0xffffu, w[1] = t.x >> 16, w[2] = t.y & 0xffffu, w[3] = t.y >> 16;
   } else {
-    const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + i);
-    l[0] = f.x, l[1] = f.y, l[2] = f.z, l[3] = f.w;
+    w[0] = *at;
   }
 }
 
-// Records the tokens of list[0, n) that fall into [v0, v0 + count) in the table.
-template <bool OUTPUT>
+// Goes through list[0, n) and calls put(s, address of its word) for every token
+// v0 + s of the slice [v0, v0 + count); kScan loads of a thread are in flight together.
+template <typename W, typename Put>
 __device__ __forceinline__ void record(const int32_t* list, int n, int v0, int count, int V,
-                                       uint32_t* table, int* bad) {
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int v = __ldg(list + i);
-    if ((unsigned)v >= (unsigned)V) *bad |= DA_DEVERR_INDEX;
-    const unsigned s = (unsigned)(v - v0);
-    if (s < (unsigned)count) {
-      if (OUTPUT)
-        atomicAdd(table + s, 1u);
-      else
-        atomicOr(table + s, kInPrompt);
+                                       uint32_t table, int* bad, Put put) {
+  for (int i0 = threadIdx.x; i0 < n; i0 += kThreads * kScan) {
+    int v[kScan];
+#pragma unroll
+    for (int u = 0; u < kScan; ++u) v[u] = __ldg(list + min(i0 + u * kThreads, n - 1));
+#pragma unroll
+    for (int u = 0; u < kScan; ++u) {
+      const unsigned s = (unsigned)(v[u] - v0);
+      if (i0 + u * kThreads >= n) break;
+      if ((unsigned)v[u] >= (unsigned)V) *bad |= DA_DEVERR_INDEX;
+      if (s < (unsigned)count) put((int)s, table + s * (uint32_t)sizeof(W));
     }
   }
 }
 
 // VEC 4: x, out and the strides allow groups of four tokens to move at once.
-template <bool BF16, int VEC>
-__global__ void __launch_bounds__(kThreads) logits_kernel(const Args a) {
-  __shared__ __align__(16) uint32_t table[kSlice];
+template <bool BF16, int VEC, typename W>
+__global__ void __launch_bounds__(kThreads, 2) logits_kernel(const Args a) {
+  constexpr int kElem = BF16 ? 2 : 4;
+  constexpr int kStep = kThreads * VEC;     // tokens of a step of the CTA
+  constexpr int kDepth = VEC == 4 ? 4 : 8;  // steps whose logits are on their way
+  extern __shared__ __align__(16) uint8_t smem[];
+  W* table = reinterpret_cast<W*>(smem);  // [slice]; all zero between slices
+  __shared__ uint16_t listed[kListed];  // tokens of the slice that have a word
+  __shared__ int n_listed;
   __shared__ unsigned long long warp_best[kThreads / 32], cta_best[kCluster];
   wait_prior_grid();
   uint32_t rank, ranks;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
-  // the cluster's first barrier: every CTA runs before any writes to another
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  const int b = blockIdx.x / ranks;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  cluster_arrive();
+  const int b = blockIdx.x / ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t words = smem_addr(table);
+  const int span = a.slice * (int)ranks;  // tokens of a round
+  const char* x = static_cast<const char*>(a.x) + (long long)b * a.x_stride * kElem;
+
+  Group<BF16, VEC> raw[kDepth];
+  uint32_t may[kDepth];  // their mask words
+  const uint32_t* mask = nullptr;
+  // Asks for step i of the slice at token v0.
+  auto load = [&](int d, int v0, int i) {
+    const long long v = v0 + (long long)i * kStep + tid * VEC;
+    raw[d].load(x + v * kElem);
+    if (mask) may[d] = __ldg(mask + (v >> 5));
+  };
+  auto load_first = [&](int v0) {
+    const int full = min(a.slice, max(0, a.V - v0)) / kStep;
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d)
+      if (d < full) load(d, v0, d);
+  };
 
   int bad = 0;
-  const int n_prompt = list_len(a.prompt_lens, a.prompt_width, b, &bad);
-  const int n_output = list_len(a.output_lens, a.output_width, b, &bad);
-  const int n_bias = list_len(a.bias_lens, a.bias_width, b, &bad);
-  const int32_t* prompt = a.prompt + (long long)b * a.prompt_width;
-  const int32_t* output = a.output + (long long)b * a.output_width;
-  const int32_t* bias_tokens = a.bias_tokens + (long long)b * a.bias_width;
-  const float* bias_values = a.bias_values + (long long)b * a.bias_width;
-  Row row;
-  row.repetition = a.repetition ? __ldg(a.repetition + b) : 1.f;
-  row.frequency = a.frequency ? __ldg(a.frequency + b) : 0.f;
-  row.presence = a.presence ? __ldg(a.presence + b) : 0.f;
-  const uint32_t* mask = nullptr;
   if (a.mask) {
     const int id = a.mask_ids ? __ldg(a.mask_ids + b) : b;
     if (id >= a.n_masks) bad |= DA_DEVERR_INDEX;
     if (id >= 0 && id < a.n_masks) mask = a.mask + (long long)id * a.mask_words;
   }
-  const long long x0 = (long long)b * a.x_stride;
+  const int n_prompt = list_len(a.prompt_lens, a.prompt_width, b, &bad);
+  const int n_output = list_len(a.output_lens, a.output_width, b, &bad);
+  const int n_bias = list_len(a.bias_lens, a.bias_width, b, &bad);
+  Row row;
+  row.repetition = a.repetition ? __ldg(a.repetition + b) : 1.f;
+  row.frequency = a.frequency ? __ldg(a.frequency + b) : 0.f;
+  row.presence = a.presence ? __ldg(a.presence + b) : 0.f;
+  load_first((int)rank * a.slice);
+  for (int i = tid; i < a.slice * (int)sizeof(W) / 16; i += kThreads)
+    reinterpret_cast<uint4*>(table)[i] = make_uint4(0, 0, 0, 0);
+  if (tid == 0) n_listed = 0;
+  __syncthreads();
+  const int32_t* bias_tokens = a.bias_tokens + (long long)b * a.bias_width;
+  const float* bias_values = a.bias_values + (long long)b * a.bias_width;
   float* out = a.out ? a.out + (long long)b * a.out_stride : nullptr;
-  auto allowed = [&](int v) { return !mask || ((__ldg(mask + (v >> 5)) >> (v & 31)) & 1u); };
 
-  unsigned long long best = 0;
-  for (int sl = rank; sl < a.n_slices; sl += ranks) {
-    const int v0 = sl * a.slice, count = min(a.slice, a.V - v0);
-    float l[kPer / VEC][VEC];
+  float best = -INFINITY;  // of this thread, whose tokens come in ascending order
+  int best_v = 0;
+  unsigned long long best_key = 0;  // of its last and its listed tokens
+  for (int r0 = 0; r0 < a.V; r0 += span) {
+    const int v0 = r0 + (int)rank * a.slice, count = min(a.slice, max(0, a.V - v0));
+    const int32_t* prompt = a.prompt + (long long)b * a.prompt_width;
+    const int32_t* output = a.output + (long long)b * a.output_width;
+    if ((long long)n_prompt + n_output + n_bias < count / kDense) {
+      // few entries: whoever touches a token first lists it
+      const auto list = [&](int s) {
+        const int at = atomicAdd(&n_listed, 1);
+        if (at < kListed) listed[at] = (uint16_t)s;
+      };
+      record<W>(prompt, n_prompt, v0, count, a.V, words, &bad, [&](int s, uint32_t at) {
+        if (Word<W>::set(at, Word<W>::kInPrompt)) list(s);
+      });
+      record<W>(output, n_output, v0, count, a.V, words, &bad, [&](int s, uint32_t at) {
+        if (Word<W>::set(at, 0)) list(s);
+        Word<W>::add(at);
+      });
+      record<W>(bias_tokens, n_bias, v0, count, a.V, words, &bad, [&](int s, uint32_t at) {
+        if (Word<W>::set(at, Word<W>::kHasBias)) list(s);
+      });
+    } else {
+      // many: record them with as few instructions as there are, then look
+      // through the words for the list
+      record<W>(prompt, n_prompt, v0, count, a.V, words, &bad,
+                [](int, uint32_t at) { Word<W>::put(at, Word<W>::kInPrompt); });
+      __syncthreads();
+      record<W>(output, n_output, v0, count, a.V, words, &bad,
+                [](int, uint32_t at) { Word<W>::add(at); });
+      record<W>(bias_tokens, n_bias, v0, count, a.V, words, &bad,
+                [](int, uint32_t at) { Word<W>::flag(at, Word<W>::kHasBias); });
+      __syncthreads();
+      constexpr int kWords = 16 / sizeof(W);
+      for (int s0 = (tid & ~31) * kWords; s0 < count; s0 += kThreads * kWords) {  // whole warps
+        const int s = s0 + lane * kWords;
+        W w[kWords] = {};
+        if (s < count)  // the table goes on past count, with zeros, to a multiple of 32
+          *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(table + s);
+        int mine = 0;
 #pragma unroll
-    for (int u = 0; u < kPer / VEC; ++u) {
-      const int s = (u * kThreads + threadIdx.x) * VEC;
-      if (VEC == 1 || s + VEC <= count) {
-        if (s < count) load_group<BF16, VEC>(a.x, x0 + v0 + s, l[u]);
-      } else {
+        for (int e = 0; e < kWords; ++e) mine += w[e] != 0;
+        int at = mine;  // this lane's place in the list: a prefix sum over the warp
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          if (s + e < count) l[u][e] = load_x(a.x, x0 + v0 + s + e, BF16);
-      }
-    }
-    __syncthreads();  // the previous slice's table is no longer read
-    for (int i = threadIdx.x; i < (count + 3) / 4; i += kThreads)
-      reinterpret_cast<uint4*>(table)[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    record<false>(prompt, n_prompt, v0, count, a.V, table, &bad);
-    record<true>(output, n_output, v0, count, a.V, table, &bad);
-    for (int i = threadIdx.x; i < n_bias; i += kThreads) {
-      const int v = __ldg(bias_tokens + i);
-      if ((unsigned)v >= (unsigned)a.V) bad |= DA_DEVERR_INDEX;
-      if ((unsigned)(v - v0) < (unsigned)count) atomicOr(table + (v - v0), kHasBias);
-    }
-    __syncthreads();
-
-#pragma unroll
-    for (int u = 0; u < kPer / VEC; ++u) {
-      const int s = (u * kThreads + threadIdx.x) * VEC;
-      if (s >= count) continue;
-      uint32_t w[VEC];
-      if constexpr (VEC == 4) {
-        const uint4 t = *reinterpret_cast<const uint4*>(table + s);
-        w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
-      } else {
-        w[0] = table[s];
-      }
-      bool whole = s + VEC <= count;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        if (s + e >= count) continue;
-        if (w[e] & kHasBias) {
-          whole = false;
-          continue;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int t = __shfl_up_sync(0xffffffffu, at, o);
+          if (lane >= o) at += t;
         }
-        if (w[e]) l[u][e] = penalised(l[u][e], w[e], row);
-        if (!allowed(v0 + s + e)) l[u][e] = -INFINITY;
-        best = max64(best, key_of(l[u][e], v0 + s + e));
+        int base = 0;
+        if (lane == 31 && at) base = atomicAdd(&n_listed, at);
+        at += __shfl_sync(0xffffffffu, base, 31) - mine;
+#pragma unroll
+        for (int e = 0; e < kWords; ++e)
+          if (w[e]) {
+            if (at < kListed) listed[at] = (uint16_t)(s + e);
+            ++at;
+          }
       }
-      if (!out) continue;
-      if constexpr (VEC == 4) {
-        if (whole) {
-          *reinterpret_cast<float4*>(out + v0 + s) =
-              make_float4(l[u][0], l[u][1], l[u][2], l[u][3]);
-          continue;
+    }
+    __syncthreads();
+
+    const int full = count / kStep;
+    for (int i0 = 0; i0 < full; i0 += kDepth) {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+        const int i = i0 + d;
+        if (i >= full) break;
+        const int s = i * kStep + tid * VEC;
+        float l[VEC];
+        uint32_t w[VEC];
+        raw[d].get(l);
+        load_words<W, VEC>(table + s, w);
+        if (mask) {
+          const uint32_t bits = may[d] >> ((v0 + s) & 31);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            if (!((bits >> e) & 1u)) l[e] = -INFINITY;
+        }
+        if (out) {
+          if constexpr (VEC == 4)
+            *reinterpret_cast<float4*>(out + v0 + s) = make_float4(l[0], l[1], l[2], l[3]);
+          else
+            out[v0 + s] = l[0];
+        }
+        if (i + kDepth < full) load(d, v0, i + kDepth);
+        uint32_t any = 0;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) any |= w[e];
+        if (any) {  // listed tokens compete later
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            if (w[e]) l[e] = -INFINITY;
+        }
+        float top = l[0];
+#pragma unroll
+        for (int e = 1; e < VEC; ++e) top = fmaxf(top, l[e]);
+        if (top > best) {
+          best = top;
+#pragma unroll
+          for (int e = VEC - 1; e >= 0; --e)
+            if (l[e] == top) best_v = v0 + s + e;
         }
       }
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        if (s + e < count && !(w[e] & kHasBias)) out[v0 + s + e] = l[u][e];
     }
+    for (int s = full * kStep + tid; s < count; s += kThreads) {  // what is left: one by one
+      float l = load_x(x, v0 + s, BF16);
+      if (mask && !((__ldg(mask + ((v0 + s) >> 5)) >> ((v0 + s) & 31)) & 1u)) l = -INFINITY;
+      if (out) out[v0 + s] = l;
+      if (!table[s]) best_key = max64(best_key, key_of(l, v0 + s));
+    }
+    if (r0 + span < a.V) load_first(v0 + span);
+    __syncthreads();  // the listed tokens' plain values are written
 
-    // tokens with a bias: untouched so far, also where out is x
-    for (int i = threadIdx.x; i < n_bias; i += kThreads) {
-      const int v = __ldg(bias_tokens + i);
-      if ((unsigned)(v - v0) >= (unsigned)count) continue;
-      bool first = true;
-      for (int j = 0; j < i && first; ++j) first = __ldg(bias_tokens + j) != v;
-      if (!first) continue;
-      float sum = __ldg(bias_values + i);
-      for (int j = i + 1; j < n_bias; ++j)
-        if (__ldg(bias_tokens + j) == v) sum = __fadd_rn(sum, __ldg(bias_values + j));
-      float lv = penalised(load_x(a.x, x0 + v, BF16), table[v - v0], row);
-      lv = __fadd_rn(lv, sum);
-      if (!allowed(v)) lv = -INFINITY;
-      best = max64(best, key_of(lv, v));
-      if (out) out[v] = lv;
+    // Where out is x, what is found there is still a listed token's logit, or
+    // -inf, which masks it anyway.
+    auto finish = [&](int s, float l, uint32_t w, uint32_t bits) {
+      const int v = v0 + s;
+      l = penalised<W>(l, w, row);
+      if (w & Word<W>::kHasBias) {
+        float sum = 0.f;
+        bool first = true;
+#pragma unroll 8
+        for (int j = 0; j < n_bias; ++j)
+          if (__ldg(bias_tokens + j) == v) {
+            const float value = __ldg(bias_values + j);
+            sum = first ? value : __fadd_rn(sum, value);
+            first = false;
+          }
+        l = __fadd_rn(l, sum);
+      }
+      if (!((bits >> (v & 31)) & 1u)) l = -INFINITY;
+      best_key = max64(best_key, key_of(l, v));
+      if (out) out[v] = l;
+    };
+    auto mask_word = [&](int s) { return mask ? __ldg(mask + ((v0 + s) >> 5)) : 0xffffffffu; };
+    const int n = n_listed;
+    if (n <= kListed) {
+      constexpr int kAhead = 4;  // tokens of a thread whose logits are on their way
+      for (int i0 = tid; i0 < n; i0 += kThreads * kAhead) {
+        int s[kAhead];
+        float l[kAhead];
+        uint32_t bits[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          s[u] = listed[min(i0 + u * kThreads, n - 1)];
+          l[u] = load_x(x, v0 + s[u], BF16);
+          bits[u] = mask_word(s[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          if (i0 + u * kThreads >= n) break;
+          finish(s[u], l[u], table[s[u]], bits[u]);
+          table[s[u]] = 0;
+        }
+      }
+    } else {  // more than the list holds: look for them
+      for (int s = tid; s < count; s += kThreads) {
+        const uint32_t w = table[s];
+        if (!w) continue;
+        finish(s, load_x(x, v0 + s, BF16), w, mask_word(s));
+        table[s] = 0;
+      }
     }
+    __syncthreads();  // the table is clear again
+    if (tid == 0) n_listed = 0;
+    __syncthreads();
   }
   if (bad && a.err) atomicOr(a.err, bad);
 
+  best_key = max64(best_key, key_of(best, best_v));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) best = max64(best, __shfl_xor_sync(0xffffffffu, best, o));
-  if (lane == 0) warp_best[warp] = best;
+  for (int o = 16; o > 0; o >>= 1)
+    best_key = max64(best_key, __shfl_xor_sync(0xffffffffu, best_key, o));
+  if (lane == 0) warp_best[warp] = best_key;
   __syncthreads();
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kThreads / 32; ++w) best = max64(best, warp_best[w]);
+  cluster_wait();  // every CTA of the cluster runs
+  if (tid == 0) {
+    for (int w = 1; w < kThreads / 32; ++w) best_key = max64(best_key, warp_best[w]);
     uint32_t to;  // cta_best[rank] of the cluster's first CTA
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
                  : "=r"(to)
                  : "r"(smem_addr(cta_best + rank)), "r"(0));
-    asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(to), "l"(best) : "memory");
+    asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(to), "l"(best_key) : "memory");
   }
   __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if (rank == 0 && threadIdx.x == 0 && a.tokens) {
-    for (uint32_t r = 0; r < ranks; ++r) best = max64(best, cta_best[r]);
-    a.tokens[b] = best ? (int32_t)~(uint32_t)best : -1;
+  cluster_arrive();
+  cluster_wait();
+  if (rank == 0 && tid == 0 && a.tokens) {
+    for (uint32_t r = 0; r < ranks; ++r) best_key = max64(best_key, cta_best[r]);
+    a.tokens[b] = best_key ? (int32_t)~(uint32_t)best_key : -1;
   }
 }
 
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-template <bool BF16, int VEC>
-cudaError_t launch_logits(const Args& a, int B, int ranks, cudaStream_t stream) {
+template <bool BF16, int VEC, typename W>
+cudaError_t launch_logits(Args& a, int B, int sms, cudaStream_t stream) {
+  // Every CTA of a row goes through its lists, so there are no more of them than
+  // fill the GPU twice over (two CTAs per SM run at once); slices are of equal
+  // length, a multiple of 32, so that they start on mask words.
+  int ranks = 1;
+  while (ranks < kCluster && 2LL * ranks * B <= 2LL * sms && ranks * kThreads * 4 < a.V) ranks *= 2;
+  const long long rounds = (a.V + ranks * Word<W>::kSlice - 1) / (ranks * Word<W>::kSlice);
+  a.slice = (int)(((a.V + ranks * rounds - 1) / (ranks * rounds) + 31) / 32 * 32);
+  const size_t bytes = (size_t)a.slice * sizeof(W);
+  if (bytes > kPlainBytes) {  // beyond what needs no consent; it holds per device
+    const cudaError_t e = cudaFuncSetAttribute(
+        logits_kernel<BF16, VEC, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTableBytes);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(B * ranks));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -280,7 +498,7 @@ cudaError_t launch_logits(const Args& a, int B, int ranks, cudaStream_t stream) 
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, logits_kernel<BF16, VEC>, a);
+  return cudaLaunchKernelEx(&cfg, logits_kernel<BF16, VEC, W>, a);
 }
 
 // A list is given whole or not at all (one without room needs no tokens).
@@ -316,6 +534,8 @@ extern "C" int nvfp4_mm_logits(const nvfp4_logits* g, void* stream) {
                           g->mask,       g->mask_ids,  g->tokens,   g->err};
   for (const void* w : words)
     if (!aligned_to(w, 4)) return DA_ERR_INVALID_ARG;
+  if ((long long)g->prompt_width + g->output_width + g->bias_width > kMaxVocab)
+    return DA_ERR_UNSUPPORTED;
   if (g->out) {  // in place row for row, or apart
     const uintptr_t x = reinterpret_cast<uintptr_t>(g->x);
     const uintptr_t o = reinterpret_cast<uintptr_t>(g->out);
@@ -350,24 +570,21 @@ extern "C" int nvfp4_mm_logits(const nvfp4_logits* g, void* stream) {
   a.bias_width = g->bias_width;
   a.n_masks = g->n_masks;
   a.mask_words = (g->vocab + 31) / 32;
-  // as many CTAs per row as the cluster allows, each with slices of equal
-  // length (a multiple of 32, so that slices start on mask words)
-  const int ranks = std::max(1, std::min(kCluster, (g->vocab + kThreads - 1) / kThreads));
-  const int rounds = (int)(((long long)g->vocab + (long long)ranks * kSlice - 1) /
-                           ((long long)ranks * kSlice));
-  const long long parts = (long long)ranks * rounds;
-  a.slice = (int)(((g->vocab + parts - 1) / parts + 31) / 32 * 32);
-  a.n_slices = (g->vocab + a.slice - 1) / a.slice;
-  if ((long long)g->batch * ranks > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
   const bool vec = aligned_to(g->x, bf16 ? 8 : 16) && g->x_stride % 4 == 0 &&
                    (!g->out || (aligned_to(g->out, 16) && g->out_stride % 4 == 0));
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (bf16)
-    e = vec ? launch_logits<true, 4>(a, g->batch, ranks, st)
-            : launch_logits<true, 1>(a, g->batch, ranks, st);
-  else
-    e = vec ? launch_logits<false, 4>(a, g->batch, ranks, st)
-            : launch_logits<false, 1>(a, g->batch, ranks, st);
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return DA_ERR_CUDA;
+  const bool narrow = g->output_width <= Word<uint16_t>::kMostOutput;
+  auto* launch = bf16 ? (vec ? (narrow ? launch_logits<true, 4, uint16_t>
+                                       : launch_logits<true, 4, uint32_t>)
+                             : (narrow ? launch_logits<true, 1, uint16_t>
+                                       : launch_logits<true, 1, uint32_t>))
+                      : (vec ? (narrow ? launch_logits<false, 4, uint16_t>
+                                       : launch_logits<false, 4, uint32_t>)
+                             : (narrow ? launch_logits<false, 1, uint16_t>
+                                       : launch_logits<false, 1, uint32_t>));
+  const cudaError_t e = launch(a, g->batch, sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }

@@ -111,6 +111,8 @@ class Case:
     (2, 65537, "fp32", dict(bias=300)), (3, 70000, "bf16", dict(prompt=0, bias=0)),
     (1, 200064, "bf16", dict(output=2000)), (300, 700, "fp32", dict(output=0)),
     (7, 513, "fp32", dict(prompt=0, output=0, bias=0)),
+    (2, 150001, "fp32", dict(prompt=60000, output=30000)), (1, 9000, "bf16", dict(prompt=40000)),
+    (160, 70001, "bf16", dict(prompt=300)),
 ])
 def test_against_oracle(api, B, V, x, kw):
     c = Case(B, V, x=x, seed=B + V, **kw)
@@ -195,9 +197,10 @@ def test_greedy_ties_masks_infinities_and_nan(api):
 
 
 @gpu
-def test_many_repeats_of_one_token(api):
-    # 70000 occurrences: counts do not spill into each other
-    V, L = 40, 70000
+@pytest.mark.parametrize("L", [8191, 8192, 70000])
+def test_many_repeats_of_one_token(api, L):
+    # counts do not spill into each other (L even: half the second row's)
+    V = 40
     o = torch.full((2, L), 3, dtype=torch.int32, device="cuda")
     o[1, ::2] = 4
     x = torch.zeros((2, V), device="cuda")
@@ -206,7 +209,7 @@ def test_many_repeats_of_one_token(api):
     api.nvfp4_logits(x, output=o, output_lens=torch.full((2,), L, dtype=torch.int32, device="cuda"),
                      frequency=one, presence=one, out=out)
     want = torch.zeros(2, V)
-    want[0, 3], want[1, 3], want[1, 4] = -70001.0, -35001.0, -35001.0
+    want[0, 3], want[1, 3], want[1, 4] = -L - 1.0, -(L // 2) - 1.0, -((L + 1) // 2) - 1.0
     assert torch.equal(out.cpu(), want)
 
 
