@@ -533,6 +533,7 @@ int decode_attn_append(const da_problem* prob, const da_rope* rope, const da_app
   const long long strides[3] = {a.k_stride, a.v_new ? a.v_stride : kv_row,
                                 a.q_new ? a.q_stride : q_row};
   const long long least[3] = {kv_row, kv_row, q_row};
+  if (q_row > (1 << 30)) return DA_ERR_UNSUPPORTED;  // a token's own offsets take 32 bits
   for (int i = 0; i < 3; ++i) {
     if (strides[i] < least[i] || strides[i] > (1LL << 40)) return DA_ERR_INVALID_ARG;
     if (strides[i] * esize % 16) return DA_ERR_INVALID_ARG;

@@ -2,15 +2,14 @@
 // the way.
 //
 // Pure data movement: each token's q, k and v are read once and written once,
-// so memory bounds a prompt's call and launch latency a decode step's.  A unit
-// of work is eight consecutive elements of a head (a "chunk": 16 or 32 bytes
-// read, 16, 8 or 4 written).  A warp takes a token, or a part of its chunks, and
-// computes the token's angles once for all its heads; the loads of its first
-// chunks are issued before the angles are needed, so one round trip to memory
-// covers both.  Warps do not wait for one another.  A rotated chunk whose pairs lie half a rotation apart reads its
-// partner chunk a second time (it comes from L1 or L2: the neighbouring lanes
-// have just asked for it), which costs less than an exchange between lanes whose
-// place depends on the rotation's size and offset.
+// so memory bounds a prompt's call and launch latency a decode step's.  A chunk
+// is eight consecutive elements of a head (16 or 32 bytes read, 16, 8 or 4
+// written); a unit of work is two chunks, the ones that the rotation of halves
+// mixes, so that each is read once and an angle serves both, or two neighbours.
+// A warp takes a token, or a part of its units, and computes the token's angles
+// once for all its heads; the loads of its first units are issued before the
+// angles are needed, so one round trip to memory covers both.  Warps do not wait
+// for one another.
 //
 // Angles: position * inv_freq is formed in fp64, where the product of a 31-bit
 // integer and a 24-bit fraction is exact up to 2^-53, and reduced by multiples
@@ -26,7 +25,10 @@ namespace {
 
 constexpr int kWarps = 4;       // per CTA; each works by itself
 constexpr int kMaxPairs = 288;  // rope_dim / 2 at most (576 / 2)
-constexpr int kBatch = 4;       // chunks a lane has in flight
+// Units that a lane has in flight (48 bytes or so a chunk pair of bf16; measured
+// on 16384 tokens of 32/8 heads: one 75, two 70, three 67 us).
+template <typename X>
+constexpr int kInFlight = sizeof(X) == 2 ? 3 : 2;
 
 template <typename X>
 struct Chunk;  // eight elements as loaded
@@ -116,13 +118,41 @@ __device__ __forceinline__ long long entry_of(const AppendLaunch& p, int i, int 
   return (long long)id * p.page_size + (pos - page * p.page_size);
 }
 
-enum { kQ = 0, kK = 1, kV = 2 };
+// Rotates the four pairs (a[0], a[1]), ... of a chunk, or half a group of pairs.
+__device__ __forceinline__ void turn_pairs(float (&f)[8], const float4* at, int groups) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float4 t = at[e * groups];
+    const float a0 = f[4 * e], b0 = f[4 * e + 1], a1 = f[4 * e + 2], b1 = f[4 * e + 3];
+    f[4 * e] = a0 * t.x - b0 * t.y;
+    f[4 * e + 1] = b0 * t.x + a0 * t.y;
+    f[4 * e + 2] = a1 * t.z - b1 * t.w;
+    f[4 * e + 3] = b1 * t.z + a1 * t.w;
+  }
+}
 
-// Warp w of the grid takes part w % parts of token w / parts: chunks [part *
-// per_part, + per_part) of the token's list q, k, v, 32 * kBatch at a time.
-template <typename X, int KT>
-__global__ void __launch_bounds__(kWarps * 32, sizeof(X) == 2 ? 7 : 5) append_kernel(const AppendLaunch p, int parts,
-                                                             int per_part) {
+// Rotates the eight pairs (a[i], b[i]) of a group.
+__device__ __forceinline__ void turn_halves(float (&a)[8], float (&b)[8], const float4* at,
+                                            int groups) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float4 t = at[e * groups];
+    const float a0 = a[2 * e], b0 = b[2 * e], a1 = a[2 * e + 1], b1 = b[2 * e + 1];
+    a[2 * e] = a0 * t.x - b0 * t.y;
+    b[2 * e] = b0 * t.x + a0 * t.y;
+    a[2 * e + 1] = a1 * t.z - b1 * t.w;
+    b[2 * e + 1] = b1 * t.z + a1 * t.w;
+  }
+}
+
+// Warp w of the grid takes part w % parts of token w / parts: units [part *
+// per_part, + per_part) of the token's heads q, k, v, 32 * kBatch at a time.
+template <typename X, int KT, int D>
+__global__ void __launch_bounds__(kWarps * 32, sizeof(X) == 2 ? 7 : 5)
+    append_kernel(const AppendLaunch p, int parts, int per_part) {
+  constexpr int kUnits = D / 16;                // units of a head
+  constexpr int kBatch = kInFlight<X>;
+  constexpr bool kBlocks = KT == DA_KV_NVFP4;   // a unit is always a block of 16
   // gain * (cos, sin) of the token's angles, for each warp: pairs 2i and 2i + 1
   // of group c (eight pairs) at [i * groups + c], so that neighbouring lanes,
   // which hold neighbouring groups, read neighbouring 16 bytes
@@ -133,33 +163,45 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(X) == 2 ? 7 : 5) append_ke
   const int token = (int)(task / parts), part = (int)(task - (long long)token * parts);
   if (token >= p.n_tokens) return;  // the whole warp
   float4* turn = turns[warp];
-  const int D = p.D, per_head = D >> 3, half = p.rope_dim >> 1, groups = half >> 3;
-  const int q_chunks = p.q_new ? p.H_q * per_head : 0, kv_chunks = p.H_kv * per_head;
-  const int total = q_chunks + kv_chunks * (p.v_new ? 2 : 1);  // even: D is a multiple of 16
-  const int end = min(total, (part + 1) * per_part);
+  const int half = p.rope_dim >> 1, groups = half >> 3;
+  const int skip = p.rope_offset >> 3;  // chunks before the rotated ones
+  const int hq = p.q_new ? p.H_q : 0, hk = hq + p.H_kv, heads = hk + (p.v_new ? p.H_kv : 0);
+  const int end = min(heads * kUnits, (part + 1) * per_part);
   const X* q_src = static_cast<const X*>(p.q_new) + token * p.q_stride;
   const X* k_src = static_cast<const X*>(p.k_new) + token * p.k_stride;
   const X* v_src = static_cast<const X*>(p.v_new) + token * p.v_stride;
+  const bool halves = !p.interleaved;
 
-  Chunk<X> own[kBatch], other[kBatch];
-  int what[kBatch], head[kBatch], dim0[kBatch];  // -1, kQ, kK or kV; its place
+  // A unit is two chunks of a head: the two that a rotation of halves mixes, or
+  // neighbours.  Its chunks' numbers within the head:
+  auto chunks_of = [&](int head, int i, int* c0, int* c1) {
+    if (kBlocks || !halves || head >= hk) {
+      *c0 = 2 * i;
+      *c1 = 2 * i + 1;
+    } else if (i < groups) {
+      *c0 = skip + i;
+      *c1 = skip + groups + i;
+    } else {  // what is not rotated, in order
+      const int m = 2 * (i - groups);
+      *c0 = m < skip ? m : m + 2 * groups;
+      *c1 = m + 1 < skip ? m + 1 : m + 1 + 2 * groups;
+    }
+  };
+  auto source = [&](int head) {
+    return head < hq ? q_src + head * D : head < hk ? k_src + (head - hq) * D : v_src + (head - hk) * D;
+  };
+  Chunk<X> lo[kBatch], hi[kBatch];
   auto load = [&](int first) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      int c = first + u * 32 + lane;
-      what[u] = -1;
-      head[u] = dim0[u] = 0;
-      if (c >= end) continue;
-      what[u] = c < q_chunks ? kQ : c < q_chunks + kv_chunks ? kK : kV;
-      c -= what[u] == kQ ? 0 : what[u] == kK ? q_chunks : q_chunks + kv_chunks;
-      head[u] = c / per_head;
-      dim0[u] = (c - head[u] * per_head) * 8;
-      const X* src = (what[u] == kQ ? q_src : what[u] == kK ? k_src : v_src) +
-                     (long long)head[u] * D + dim0[u];
-      own[u].load(src);
-      const int rel = dim0[u] - p.rope_offset;
-      if (what[u] != kV && !p.interleaved && rel >= 0 && rel < p.rope_dim)
-        other[u].load(rel < half ? src + half : src - half);
+      const int unit = first + u * 32 + lane;
+      if (unit >= end) continue;
+      const int head = unit / kUnits;
+      int c0, c1;
+      chunks_of(head, unit - head * kUnits, &c0, &c1);
+      const X* src = source(head);
+      lo[u].load(src + 8 * c0);
+      hi[u].load(src + 8 * c1);
     }
   };
   load(part * per_part);  // on their way while the place and the angles are found
@@ -182,74 +224,85 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(X) == 2 ? 7 : 5) append_ke
   }
   __syncwarp();
 
+  __nv_bfloat16* q_dst = p.q_out + (long long)token * p.H_q * D;
+  const long long at0 = entry * p.H_kv * D;  // first element of the entry in its caches
   for (int first = part * per_part;;) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      float f[8];
-      if (what[u] >= 0) {
-        own[u].get(f);
-        const int rel = dim0[u] - p.rope_offset;
-        if (what[u] != kV && rel >= 0 && rel < p.rope_dim) {
-          if (p.interleaved) {  // pairs rel / 2 .. + 3: half a group
-            const float4* at = turn + ((rel >> 3) & 1) * 2 * groups + (rel >> 4);
+      const int unit = first + u * 32 + lane;
+      if (unit >= end) continue;
+      const int head = unit / kUnits, i = unit - head * kUnits;
+      int c0, c1;
+      chunks_of(head, i, &c0, &c1);
+      float a[8], b[8];
+      lo[u].get(a);
+      hi[u].get(b);
+      if (head < hk) {
+        if (!halves) {
+          const int r0 = c0 - skip, r1 = c1 - skip;  // pairs 4 r .. 4 r + 3: half a group
+          if (r0 >= 0 && r0 < 2 * groups) turn_pairs(a, turn + (r0 & 1) * 2 * groups + (r0 >> 1), groups);
+          if (r1 >= 0 && r1 < 2 * groups) turn_pairs(b, turn + (r1 & 1) * 2 * groups + (r1 >> 1), groups);
+        } else if (!kBlocks) {
+          if (i < groups) turn_halves(a, b, turn + i, groups);
+        } else {
+          // a block's chunks have their partners elsewhere: they are read again
+          // (from L1 or L2), which costs less than an exchange between lanes whose
+          // place depends on the rotation
+          const X* src = source(head);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float4 t = at[e * groups];
-              const float a0 = f[4 * e], b0 = f[4 * e + 1], a1 = f[4 * e + 2], b1 = f[4 * e + 3];
-              f[4 * e] = a0 * t.x - b0 * t.y;
-              f[4 * e + 1] = b0 * t.x + a0 * t.y;
-              f[4 * e + 2] = a1 * t.z - b1 * t.w;
-              f[4 * e + 3] = b1 * t.z + a1 * t.w;
-            }
-          } else {
+          for (int h = 0; h < 2; ++h) {
+            float(&own)[8] = h ? b : a;
+            const int r = (h ? c1 : c0) - skip;
+            if (r < 0 || r >= 2 * groups) continue;
+            Chunk<X> other;
+            other.load(src + 8 * (skip + (r < groups ? r + groups : r - groups)));
             float g[8];
-            other[u].get(g);
-            const bool lower = rel < half;
-            const float4* at = turn + ((lower ? rel : rel - half) >> 3);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float4 t = at[e * groups];
-              f[2 * e] = f[2 * e] * t.x + g[2 * e] * (lower ? -t.y : t.y);
-              f[2 * e + 1] = f[2 * e + 1] * t.z + g[2 * e + 1] * (lower ? -t.w : t.w);
-            }
+            other.get(g);
+            if (r < groups)
+              turn_halves(own, g, turn + r, groups);
+            else
+              turn_halves(g, own, turn + (r - groups), groups);
           }
         }
-        if (what[u] == kQ)
-          *reinterpret_cast<uint4*>(p.q_out + ((long long)token * p.H_q + head[u]) * D + dim0[u]) =
-              to_bf16x8(f);
       }
-      const bool kv = what[u] == kK || what[u] == kV;
-      uint8_t* cache = static_cast<uint8_t*>(what[u] == kV ? p.v : p.k);
-      const float scale = what[u] == kV ? p.v_scale : p.k_scale;
-      const long long at = (entry * p.H_kv + head[u]) * D + dim0[u];  // element of the cache
+      if (head < hq) {
+        __nv_bfloat16* dst = q_dst + head * D;
+        *reinterpret_cast<uint4*>(dst + 8 * c0) = to_bf16x8(a);
+        *reinterpret_cast<uint4*>(dst + 8 * c1) = to_bf16x8(b);
+        continue;
+      }
+      const bool is_v = head >= hk;
+      uint8_t* cache = static_cast<uint8_t*>(is_v ? p.v : p.k);
+      const float scale = is_v ? p.v_scale : p.k_scale;
+      const long long at = at0 + (head - (is_v ? hk : hq)) * D;  // the head's first element
       if constexpr (KT == DA_KV_BF16) {
-        if (kv) *reinterpret_cast<uint4*>(cache + 2 * at) = to_bf16x8(f);
+        *reinterpret_cast<uint4*>(cache + 2 * (at + 8 * c0)) = to_bf16x8(a);
+        *reinterpret_cast<uint4*>(cache + 2 * (at + 8 * c1)) = to_bf16x8(b);
       } else if constexpr (KT == DA_KV_FP8_E4M3) {
-        if (kv) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float(&f)[8] = h ? b : a;
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             w[e] = e4m3x2(__fdiv_rn(f[2 * e], scale), __fdiv_rn(f[2 * e + 1], scale));
-          *reinterpret_cast<uint2*>(cache + at) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+          *reinterpret_cast<uint2*>(cache + at + 8 * (h ? c1 : c0)) =
+              make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
         }
-      } else if (__any_sync(0xffffffffu, kv)) {
-        // a block of 16 is this lane's chunk and its neighbour's (chunks come in
-        // pairs: D is a multiple of 16 and every list starts on an even chunk)
+      } else {
         float m = 0.f;
-        if (kv) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(f[e]));
-        }
-        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        if (kv) {
-          const uint32_t s = e4m3x2(__fdiv_rn(m, 6.f * scale), 0.f) & 0xffu;
-          const float step = __half2float(__ushort_as_half((unsigned short)(
-                                 e4m3x2_to_f16x2(s) & 0xffffu))) * scale;
+        for (int e = 0; e < 8; ++e) m = max_nan(m, max_nan(fabsf(a[e]), fabsf(b[e])));
+        const uint32_t s = e4m3x2(__fdiv_rn(m, 6.f * scale), 0.f) & 0xffu;
+        const float step = __half2float(__ushort_as_half((unsigned short)(
+                               e4m3x2_to_f16x2(s) & 0xffffu))) * scale;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = s ? __fdiv_rn(f[e], step) : 0.f;
-          *reinterpret_cast<uint32_t*>(cache + at / 2) = e2m1x8(f);
-          if (!(dim0[u] & 8)) cache[p.kv_rows * p.H_kv * (D / 2) + at / 16] = (uint8_t)s;
+        for (int e = 0; e < 8; ++e) {
+          a[e] = s ? __fdiv_rn(a[e], step) : 0.f;
+          b[e] = s ? __fdiv_rn(b[e], step) : 0.f;
         }
+        *reinterpret_cast<uint2*>(cache + (at >> 1) + 8 * i) = make_uint2(e2m1x8(a), e2m1x8(b));
+        cache[p.kv_rows * p.H_kv * (D / 2) + (at >> 4) + i] = (uint8_t)s;
       }
     }
     first += 32 * kBatch;
@@ -258,28 +311,40 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(X) == 2 ? 7 : 5) append_ke
   }
 }
 
-template <typename X, int KT>
-cudaError_t launch_typed(const AppendLaunch& p, int sms, cudaStream_t stream) {
-  const int chunks = (p.D >> 3) * ((p.q_new ? p.H_q : 0) + p.H_kv * (p.v_new ? 2 : 1));
+template <typename X, int KT, int D>
+cudaError_t launch_dim(const AppendLaunch& p, int sms, cudaStream_t stream) {
+  const int units = (D / 16) * ((p.q_new ? p.H_q : 0) + p.H_kv * (p.v_new ? 2 : 1));
   // a warp takes a whole token once there are enough of them; fewer tokens are
-  // cut, down to one load a lane, so that all SMs have work
-  const long long want = 64LL * sms;  // warps
+  // cut, down to one unit a lane, so that all SMs have work (64 tokens of 128
+  // heads of 576: 5.2 us with 32 warps per SM, 7.3 with 64)
+  const long long want = 32LL * sms;  // warps
   long long parts = std::max<long long>(1, want / p.n_tokens);
-  parts = std::min<long long>(parts, (chunks + 31) / 32);
-  const int per_part = (int)(((chunks + parts - 1) / parts + 31) / 32 * 32);
-  parts = (chunks + per_part - 1) / per_part;
+  parts = std::min<long long>(parts, (units + 31) / 32);
+  const int per_part = (int)(((units + parts - 1) / parts + 31) / 32 * 32);
+  parts = (units + per_part - 1) / per_part;
   const long long grid = (p.n_tokens * parts + kWarps - 1) / kWarps;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_after(append_kernel<X, KT>, dim3((unsigned)grid), dim3(kWarps * 32), 0, stream, p,
+  return launch_after(append_kernel<X, KT, D>, dim3((unsigned)grid), dim3(kWarps * 32), 0, stream, p,
                       (int)parts, per_part);
+}
+
+template <typename X, int KT>
+cudaError_t launch_kv(const AppendLaunch& p, int sms, cudaStream_t stream) {
+  switch (p.D) {
+    case 64: return launch_dim<X, KT, 64>(p, sms, stream);
+    case 128: return launch_dim<X, KT, 128>(p, sms, stream);
+    case 576:
+      if constexpr (KT != DA_KV_NVFP4) return launch_dim<X, KT, 576>(p, sms, stream);
+  }
+  return cudaErrorInvalidValue;  // no kernel reads such a cache
 }
 
 template <typename X>
 cudaError_t launch_x(const AppendLaunch& p, int sms, cudaStream_t stream) {
   switch (p.kv_type) {
-    case DA_KV_FP8_E4M3: return launch_typed<X, DA_KV_FP8_E4M3>(p, sms, stream);
-    case DA_KV_NVFP4: return launch_typed<X, DA_KV_NVFP4>(p, sms, stream);
-    default: return launch_typed<X, DA_KV_BF16>(p, sms, stream);
+    case DA_KV_FP8_E4M3: return launch_kv<X, DA_KV_FP8_E4M3>(p, sms, stream);
+    case DA_KV_NVFP4: return launch_kv<X, DA_KV_NVFP4>(p, sms, stream);
+    default: return launch_kv<X, DA_KV_BF16>(p, sms, stream);
   }
 }
 
