@@ -2,27 +2,34 @@
 //     t[i, :] = bf16(x[i, :]) A_id^T,   out[i, :] = y[i, :] + (scale_id t[i, :]) B_id^T
 // with each row's own id, every row's bits independent of the batch.
 //
-// Rows are taken 32 at a time in batch order (a "tile", one lane of a warp per
-// row); the rows of a tile that share an adapter form a group, found by a match
-// across the lanes, and the members of a group are the columns of the matrix
-// products.  Prompts, whose rows come in runs, give one group of 32 per tile;
-// decode steps give many small ones.  No list is built or sorted on the device.
+// Three kernels:
+//   plan  groups the rows of a window of 512 by adapter and cuts the groups into
+//         tiles of at most 32 rows (the columns of the matrix products).  Prompts,
+//         whose rows come in runs, give full tiles; a decode step's scattered rows
+//         meet their adapter's others anywhere in the window, so an adapter's
+//         weights are read once per 32 rows that use it.
+//   down  t: D[rank, member] += A[rank, k] x[member, k] on the tensor cores
+//         (tcgen05, M = 128 of which the adapter's ranks count, N = 32, fp32 in
+//         tensor memory).  K is cut into the chunks of nvfp4_mm (1024), each
+//         summed from zero in K order; a unit of work is a tile and a chunk.
+//   up    out: D[feature, member] += B[feature, r] t[member, r], M = 128 features,
+//         N = 32.  The chunk sums of t are added in order, scaled, and split into
+//         three bf16 terms that hold their 24 bits; their products with B are
+//         exact, so out keeps fp32 accuracy.  A unit is a tile and 128 features;
+//         a thread of the epilogue holds one feature, so a warp reads y and writes
+//         out in whole 128-byte lines, a row at a time.
+// The orders of all sums depend on K and the rank alone.  A column of an MMA does
+// not depend on the other columns, so neither do a row's bits.
 //
-// Two kernels on the warp-level tensor cores (m16n8k16, bf16 x bf16 products
-// exact, fp32 accumulation):
-//   down: t.  M = ranks, N = group members, K along x.  Operand fragments come
-//     straight from global memory, 16 bytes a lane: a fragment's K order may be
-//     any permutation as long as both operands use the same, so lane q of a row
-//     quad takes K 8q .. 8q + 7 of each 32.  K is cut into chunks of kChunk that
-//     one warp sums from zero, four chunks make a K group, added in order, and
-//     the groups are added in order: ((g0 + g1) + g2) ...; a large call lets one
-//     CTA walk all groups of a tile, a small one gives every group its own CTA
-//     and the second kernel adds them, the same additions either way.
-//   up: out.  M = output features, N = group members, K = ranks.  t is scaled
-//     and split into three bf16 terms that hold its 24 bits (their products
-//     with B are exact, so out keeps fp32 accuracy); rows of the M tiles are
-//     assigned to features so that a lane ends up with four consecutive ones:
-//     y and out move 16 bytes a lane, whole 128-byte lines a quad of lanes.
+// Both matmul kernels are persistent with one CTA per SM and run the same roles:
+// producer warps bring operands into a ring of stages with 16-byte cp.async (rows
+// may lie anywhere, and a copy may end inside 16 bytes, zeros beyond: what memory
+// holds past an adapter's rank is never multiplied) in the 128-byte-swizzled
+// K-major layout; one thread issues the MMAs; epilogue warps drain accumulators.
+// Every wait is bounded; on time-out the kernel records DA_DEVERR_TIMEOUT, all
+// roles leave their loops, copies and tensor-core work are drained and tensor
+// memory is freed.
+//
 // y and out (8 N bytes a row) bound a prompt, the adapters' weights and launch
 // latency a decode step.
 #include <cuda_bf16.h>
@@ -32,20 +39,19 @@
 
 #include "common.cuh"
 #include "nvfp4_mm.h"
+#include "tcgen05.cuh"
 
 namespace da {
 namespace {
 
-constexpr int kTile = 32;                     // rows per tile
-constexpr int kChunk = 128;                   // K that one warp sums from zero
-constexpr int kWarps = 4;                     // warps of a down CTA = chunks of a K group
-constexpr int kGroupK = kChunk * kWarps;      // 512
-constexpr int kDownThreads = kWarps * 32;
+constexpr int kTile = 32;                  // rows per tile (MMA N)
+constexpr int kWindow = 512;               // rows that are grouped together
+constexpr int kSlab = 512 * kWindow;       // rows of one set of launches
 constexpr int kMaxRank = NVFP4_ADAPTER_MAX_RANK;
-constexpr int kUpWarps = 8;
-constexpr int kUpThreads = kUpWarps * 32;
-constexpr int kWarpN = 32;                    // features of a warp's step
+constexpr int kKChunk = NVFP4_MM_K_CHUNK;  // K summed from zero
+constexpr int kFeat = NVFP4_MM_TILE_N;     // features per unit (MMA M)
 constexpr unsigned kFull = 0xffffffffu;
+constexpr uint32_t kIdesc = umma::idesc_bf16_f32(128, kTile, false);
 
 struct Args {
   const void* x;
@@ -58,20 +64,24 @@ struct Args {
   float* out;
   __nv_bfloat16* out_bf16;
   int32_t* hdr;
-  float* t;  // [n_parts][n][max_rank]: one part (all K), or one per K group
-  int n, N, K, n_adapters, max_rank;
-  int n_groups;   // K groups
-  int n_parts;    // 1 or n_groups
-  int n_step;     // up: features of a CTA (a multiple of 128)
+  int32_t* tiles_in;   // [windows] tiles of a window; window w's start at slot 512 w
+  int32_t* tile_id;    // [rows] adapter, or -1: rows that are only copied
+  int32_t* tile_count; // [rows] members
+  int32_t* tile_rows;  // [rows][32] their rows, then -1
+  float* t;            // [chunks][n][max_rank]
+  int n, N, K, n_adapters, max_rank, n_chunks, windows;
+  int copy;            // 1: rows without an adapter are written as well
+  int first;           // 1: the call's first slab
 };
 
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                    uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ void fence_proxy_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// 16 bytes of which the first `bytes` are copied and the others are zero.
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -79,326 +89,698 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&b);
 }
 
-// The groups of a tile as every lane of a warp sees them.
-struct Groups {
-  int id;            // this lane's row's adapter, -1 if none
-  unsigned peers;    // lanes whose row has the same adapter
-  unsigned leaders;  // lowest lane of each group
-  int bad;           // error bits of this lane's row
-};
-
-__device__ __forceinline__ Groups groups_of(const Args& g, int row0, int lane) {
-  Groups r;
-  const int row = row0 + lane;
-  r.id = row < g.n ? __ldg(g.ids + row) : -1;
-  r.bad = 0;
-  if (r.id >= g.n_adapters) {
-    r.bad = DA_DEVERR_INDEX;
-    r.id = -1;
-  }
-  if (r.id < 0) r.id = -1;
-  r.peers = __match_any_sync(kFull, r.id);
-  r.leaders = __ballot_sync(kFull, r.id >= 0 && lane == __ffs(r.peers) - 1);
-  return r;
+__device__ __forceinline__ int rank_of(const Args& g, int id) {
+  return g.ranks ? clamp_len(__ldg(g.ranks + id), g.max_rank) : g.max_rank;
 }
 
-__device__ __forceinline__ int rank_of(const Args& g, int id, int* bad) {
-  if (!g.ranks) return g.max_rank;
-  const int r = __ldg(g.ranks + id), c = clamp_len(r, g.max_rank);
-  if (c != r) *bad |= DA_DEVERR_LENGTH;
-  return c;
-}
+// ---------------------------------------------------------------- plan
 
-// The rows of the group `members`, in order, then -1: written by one warp.
-__device__ __forceinline__ void list_members(int (&list)[kTile], unsigned members, int row0,
-                                             int lane) {
-  const int before = __popc(members & ((1u << lane) - 1u));
-  if ((members >> lane) & 1u) list[before] = row0 + lane;
-  if (lane >= __popc(members)) list[lane] = -1;
-}
-
-// Eight consecutive activations as bf16 pairs (round to nearest even).
-template <bool BF16>
-__device__ __forceinline__ uint4 load_x8(const void* x, long long i) {
-  if constexpr (BF16) {
-    return __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) + i));
-  } else {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + i);
-    const float4 u = __ldg(p), v = __ldg(p + 1);
-    return make_uint4(pack_bf16(u.x, u.y), pack_bf16(u.z, u.w), pack_bf16(v.x, v.y),
-                      pack_bf16(v.z, v.w));
-  }
-}
-
-// ---------------------------------------------------------------- down
-// Grid (K groups or 1, tiles, Z): CTA (p, tile, z) takes the tile's groups z,
-// z + Z, ...; rank blocks of 64 one after the other.
-template <bool BF16>
-__global__ void __launch_bounds__(kDownThreads) down_kernel(const Args g) {
-  // a K group's chunk sums: [warp][rank of 64][member]
-  __shared__ float part[kWarps][64][kTile + 1];
-  __shared__ int member[kTile];
+// One CTA per window, one thread per row.
+__global__ void __launch_bounds__(kWindow) plan_kernel(const Args g) {
+  __shared__ __align__(16) int id[kWindow];
+  __shared__ int pos[kWindow], leader[kWindow], before[kWindow / 32 + 1];
   wait_prior_grid();
   allow_next_grid();  // after the wait: what ran before this call has finished
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int q = lane & 3, row8 = lane >> 2;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0)
-    g.hdr[kHdrError] = 0;  // errors of this call only: the second kernel sets them
-  const int row0 = blockIdx.y * kTile;
-  const Groups gr = groups_of(g, row0, lane);
-  unsigned left = gr.leaders;
-  for (int j = 0; left; ++j) {
-    const int lead = __ffs(left) - 1;
-    left &= left - 1;
-    if (j % (int)gridDim.z != (int)blockIdx.z) continue;
-    const int id = __shfl_sync(kFull, gr.id, lead);
-    const unsigned members = __shfl_sync(kFull, gr.peers, lead);
-    const int count = __popc(members);
-    int ignore = 0;
-    const int rank = rank_of(g, id, &ignore);
-    __syncthreads();  // the previous group's list has been read
-    if (warp == 0) list_members(member, members, row0, lane);
-    __syncthreads();
-    // this lane's columns: members row8, row8 + 8, ...
-    long long xrow[4];
-#pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-      const int row = member[nt * 8 + row8];
-      xrow[nt] = row < 0 ? -1 : (long long)row * g.K;
+  const int i = threadIdx.x, lane = i & 31, line = i >> 5;
+  const int r0 = blockIdx.x * kWindow, count = min(kWindow, g.n - r0);
+  if (blockIdx.x == 0 && i == 0 && g.first) g.hdr[kHdrError] = 0;  // errors of this call only
+  int v = -2;  // no row, or one that nothing is done for
+  if (i < count) {
+    v = __ldg(g.ids + r0 + i);
+    if (v < 0 || v >= g.n_adapters || rank_of(g, v) == 0) v = g.copy ? -1 : -2;
+  }
+  id[i] = v;
+  __syncthreads();
+  // this row's place among the rows of its group: those of earlier lines, then
+  // of its own
+  int p = 0;
+  for (int j = 0; j < line * 32; j += 4) {
+    const int4 o = *reinterpret_cast<const int4*>(id + j);
+    p += (o.x == v) + (o.y == v) + (o.z == v) + (o.w == v);
+  }
+  p += __popc(__match_any_sync(kFull, v) & ((1u << lane) - 1u));
+  pos[i] = p;
+  // every 32nd row of a group leads a tile; tiles are numbered in row order
+  const unsigned leads = __ballot_sync(kFull, v != -2 && p % kTile == 0);
+  if (lane == 0) before[line + 1] = __popc(leads);
+  if (i == 0) before[0] = 0;
+  __syncthreads();
+  if (i == 0)
+    for (int l = 1; l <= kWindow / 32; ++l) before[l] += before[l - 1];
+  __syncthreads();
+  if ((leads >> lane) & 1u) leader[before[line] + __popc(leads & ((1u << lane) - 1u))] = i;
+  __syncthreads();
+  const int tiles = before[kWindow / 32];
+  if (i == 0) g.tiles_in[blockIdx.x] = tiles;
+  for (int t = line; t < tiles; t += kWindow / 32) {  // a warp per tile
+    const int lead = leader[t], tv = id[lead], tp = pos[lead];
+    const long long slot = r0 + t;
+    int found = 0;
+    for (int j = lead & ~31; j < count && found < kTile; j += 32) {
+      const int r = j + lane, q = pos[r] - tp;
+      const bool mine = id[r] == tv && q >= 0 && q < kTile;
+      if (mine) g.tile_rows[slot * kTile + q] = r0 + r;
+      found += __popc(__ballot_sync(kFull, mine));
     }
-    const int n_nt = (count + 7) >> 3;
-    const int p0 = g.n_parts == 1 ? 0 : (int)blockIdx.x;
-    const int p1 = g.n_parts == 1 ? g.n_groups : p0 + 1;
-    for (int r0 = 0; r0 < rank; r0 += 64) {
-      const int n_mt = min(4, (rank - r0 + 15) >> 4);
-      const __nv_bfloat16* arow = g.a + ((long long)id * g.max_rank + r0 + row8) * g.K + 8 * q;
-      // sums of this thread's share of (64 ranks) x (32 members)
-      constexpr int kMine = 64 * kTile / kDownThreads;
-      float sum[kMine];
-      for (int p = p0; p < p1; ++p) {
-        float acc[4][4][4];
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-          for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
-        const int k0 = p * kGroupK + warp * kChunk, k1 = min(k0 + kChunk, g.K);
-#pragma unroll 2
-        for (int k = k0; k < k1; k += 32) {
-          uint4 xv[4];
-#pragma unroll
-          for (int nt = 0; nt < 4; ++nt) {
-            xv[nt] = make_uint4(0, 0, 0, 0);
-            if (nt < n_nt && xrow[nt] >= 0) xv[nt] = load_x8<BF16>(g.x, xrow[nt] + k + 8 * q);
-          }
-#pragma unroll
-          for (int mt = 0; mt < 4; ++mt) {
-            if (mt >= n_mt) break;
-            const uint4 lo = __ldg(reinterpret_cast<const uint4*>(arow + (long long)mt * 16 * g.K + k));
-            const uint4 hi =
-                __ldg(reinterpret_cast<const uint4*>(arow + (long long)(mt * 16 + 8) * g.K + k));
-            const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-              if (nt >= n_nt) break;
-              mma(acc[mt][nt], a0, xv[nt].x, xv[nt].y);
-              mma(acc[mt][nt], a1, xv[nt].z, xv[nt].w);
-            }
-          }
-        }
-        __syncthreads();  // the previous sums have been read
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-          for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              part[warp][mt * 16 + row8 + (e >> 1) * 8][nt * 8 + 2 * q + (e & 1)] = acc[mt][nt][e];
-        __syncthreads();
-        // chunks past the end of K are zero: adding them changes nothing but a
-        // -0, so they take part whatever K is
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          const int r = (int)threadIdx.x & 63, c = i * (kDownThreads / 64) + ((int)threadIdx.x >> 6);
-          const float s = ((part[0][r][c] + part[1][r][c]) + part[2][r][c]) + part[3][r][c];
-          sum[i] = p == p0 ? s : sum[i] + s;
-        }
-      }
-      float* t = g.t + (long long)p0 * g.n * g.max_rank;
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        const int r = (int)threadIdx.x & 63, c = i * (kDownThreads / 64) + ((int)threadIdx.x >> 6);
-        if (c < count && r0 + r < rank)
-          t[(long long)member[c] * g.max_rank + r0 + r] = sum[i];
+    if (lane >= found) g.tile_rows[slot * kTile + lane] = -1;
+    if (lane == 0) {
+      g.tile_id[slot] = tv;
+      g.tile_count[slot] = found;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- shared by the matmul kernels
+
+struct Ctx {
+  uint32_t sbase, bars;  // shared memory, and its mbarriers
+  volatile int* abort_flag;
+  int32_t* hdr;
+};
+
+__device__ __forceinline__ uint32_t bar_at(const Ctx& c, int i) { return c.bars + 8 * i; }
+
+// Bounded wait that also gives up once another role has aborted.
+__device__ __forceinline__ bool wait_bar(const Ctx& c, int i, uint32_t parity) {
+  const uint32_t bar = bar_at(c, i);
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      if (*c.abort_flag) return false;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        set_error(c.hdr, DA_DEVERR_TIMEOUT);
+        *c.abort_flag = 1;
+        return false;
       }
     }
+  }
+}
+
+// The same for a whole warp: one lane polls.
+__device__ __forceinline__ bool wait_warp(const Ctx& c, int i, uint32_t parity) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = wait_bar(c, i, parity) ? 1 : 0;
+  ok = __shfl_sync(kFull, ok, 0);
+  __syncwarp();
+  return ok != 0;
+}
+
+// Windows' tiles counted up: start[w] is the number of tiles before window w.
+// Called by all threads; returns the total.
+__device__ int count_tiles(const Args& g, int* start) {
+  for (int w = threadIdx.x; w < g.windows; w += blockDim.x) start[w + 1] = __ldcg(g.tiles_in + w);
+  if (threadIdx.x == 0) start[0] = 0;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    int run = 0;
+    for (int w0 = 0; w0 < g.windows; w0 += 32) {
+      const int w = w0 + (int)threadIdx.x;
+      int s = w < g.windows ? start[w + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, s, o);
+        if ((int)threadIdx.x >= o) s += u;
+      }
+      if (w < g.windows) start[w + 1] = run + s;
+      run += __shfl_sync(kFull, s, 31);
+    }
+  }
+  __syncthreads();
+  return start[g.windows];
+}
+
+// Slot of the call's tile number t.
+__device__ __forceinline__ long long slot_of(const int* start, int windows, int t) {
+  int lo = 0, hi = windows;  // start[lo] <= t < start[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= t) lo = mid; else hi = mid;
+  }
+  return (long long)lo * kWindow + (t - start[lo]);
+}
+
+// The arrive of a tcgen05.commit lands some time after the work it tracks; the
+// last one on each of `slots` barriers from `first` on, which `commits` commits
+// went to in turn, must have landed before the CTA's shared memory is handed on.
+__device__ __forceinline__ void drain_commits(const Ctx& c, int first, int slots, int commits) {
+  for (int s = 0; s < slots && s < commits; ++s) {
+    const int rounds = (commits - 1 - s) / slots;  // of barrier s, before its last
+    if (!mbar_wait(bar_at(c, first + s), rounds & 1)) set_error(c.hdr, DA_DEVERR_TIMEOUT);
+  }
+}
+
+// What the MMA thread committed to barriers that nobody waits for at the end.
+struct Commits {
+  int ring = 0, terms = 0;
+};
+
+// ---------------------------------------------------------------- down
+
+constexpr int kStepK = 256, kRegionK = 64;         // K of a stage, and of a 128-byte swizzle row
+constexpr int kXRegion = kTile * kRegionK * 2;     // 4 KB
+constexpr int kXStage = (kStepK / kRegionK) * kXRegion;
+constexpr int kDownEpWarps = 4, kDownProdWarp0 = 4, kDownProdWarps = 8, kDownMmaWarp = 12;
+constexpr int kDownThreads = (kDownMmaWarp + 1) * 32;
+constexpr int kDownStages = 4;
+// mbarriers: stage full and empty, accumulator full and empty, drain
+enum { kFull0 = 0, kEmpty0 = kFull0 + kDownStages, kDFull0 = kEmpty0 + kDownStages,
+       kDEmpty0 = kDFull0 + 2, kDownDrain = kDEmpty0 + 2, kDownBars };
+constexpr uint32_t kDownCols = 64;                 // two accumulators
+
+__host__ __device__ constexpr int down_stage_bytes(int max_rank) {
+  return max_rank * kStepK * 2 + kXStage;
+}
+__host__ __device__ constexpr int down_stages(int max_rank) { return max_rank <= 64 ? 4 : 2; }
+
+struct DownUnit {
+  long long slot;
+  int id, count, rank, k0, k_len, chunk;
+};
+
+// Units of the CTA, one after the other; all roles walk them alike.  Tiles that
+// are only copied have none.
+struct DownWalk {
+  const Args& g;
+  const int* start;
+  int u, total;
+  __device__ __forceinline__ bool next(DownUnit* d) {
+    for (; u < total; u += gridDim.x) {
+      const int tile = u / g.n_chunks;
+      d->slot = slot_of(start, g.windows, tile);
+      d->id = __ldcg(g.tile_id + d->slot);
+      if (d->id < 0) continue;
+      d->count = __ldcg(g.tile_count + d->slot);
+      d->rank = rank_of(g, d->id);
+      d->chunk = u - tile * g.n_chunks;
+      d->k0 = d->chunk * kKChunk;
+      d->k_len = min(g.K, d->k0 + kKChunk) - d->k0;
+      u += gridDim.x;
+      return true;
+    }
+    return false;
+  }
+};
+
+// Producer warp w brings rows w, w + 8, ... of A and of the members' x; a lane
+// copies 16 bytes of K, a warp 512 bytes of one row.
+template <bool BF16, int S>
+__device__ void down_produce(const Ctx& c, const Args& g, DownWalk walk) {
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kDownProdWarp0;
+  const int stage_bytes = down_stage_bytes(g.max_rank), a_region = g.max_rank * 128;
+  const uint32_t chunk16 = lane & 7, region = lane >> 3;  // of this lane's 16 bytes
+  int step = 0;
+  bool ok = true;
+  auto signal = [&](int s) {  // stage s % S has landed
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_at(c, kFull0 + s % S));
+  };
+  DownUnit d;
+  while (ok && walk.next(&d)) {
+    const int my_row = __ldcg(g.tile_rows + d.slot * kTile + lane);
+    const int rows_a = (d.rank + 15) & ~15;
+    const __nv_bfloat16* a = g.a + (long long)d.id * g.max_rank * g.K + d.k0 + 8 * lane;
+    for (int k = 0; k < d.k_len; k += kStepK, ++step) {
+      const bool live = k + 8 * lane < d.k_len;  // K is a multiple of 64: whole regions
+      uint4 v[kTile / kDownProdWarps];
+      if constexpr (!BF16) {  // fp32 rows are rounded on the way; their loads come first
+#pragma unroll
+        for (int i = 0; i < kTile / kDownProdWarps; ++i) {
+          const int m = w + i * kDownProdWarps;
+          const int row = __shfl_sync(kFull, my_row, m);
+          if (m < d.count && live) {
+            const float4* p = reinterpret_cast<const float4*>(
+                static_cast<const float*>(g.x) + (long long)row * g.K + d.k0 + k + 8 * lane);
+            const float4 e = __ldg(p), f = __ldg(p + 1);
+            v[i] = make_uint4(pack_bf16(e.x, e.y), pack_bf16(e.z, e.w), pack_bf16(f.x, f.y),
+                              pack_bf16(f.z, f.w));
+          }
+        }
+      }
+      if (step >= S && !wait_warp(c, kEmpty0 + step % S, (step / S - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      const uint32_t stage = c.sbase + (step % S) * stage_bytes;
+      if (live) {
+        for (int r = w; r < rows_a; r += kDownProdWarps)
+          cp_async16(stage + region * a_region + r * 128 + ((chunk16 ^ (r & 7)) << 4),
+                     a + (long long)r * g.K + k);
+      }
+      const uint32_t xs = stage + 4 * a_region;
+#pragma unroll
+      for (int i = 0; i < kTile / kDownProdWarps; ++i) {
+        const int m = w + i * kDownProdWarps;
+        const int row = __shfl_sync(kFull, my_row, m);
+        if (m >= d.count || !live) continue;
+        const uint32_t at = xs + region * kXRegion + m * 128 + ((chunk16 ^ (m & 7)) << 4);
+        if constexpr (BF16)
+          cp_async16(at, static_cast<const __nv_bfloat16*>(g.x) + (long long)row * g.K + d.k0 + k +
+                             8 * lane);
+        else
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[i].x), "r"(v[i].y),
+                       "r"(v[i].z), "r"(v[i].w)
+                       : "memory");
+      }
+      cp_async_commit();
+      if (step >= S - 1) {
+        cp_async_wait<S - 1>();
+        signal(step - (S - 1));
+      }
+    }
+  }
+  cp_async_wait<0>();  // what is left has landed as well
+  if (ok)
+    for (int s = max(0, step - (S - 1)); s < step; ++s) signal(s);
+}
+
+template <int S>
+__device__ Commits down_mma(const Ctx& c, const Args& g, DownWalk walk, uint32_t tmem) {
+  const int stage_bytes = down_stage_bytes(g.max_rank), a_region = g.max_rank * 128;
+  const uint64_t base = umma::smem_desc(c.sbase, 16, 1024, umma::kSwizzle128B);
+  Commits done;
+  int& step = done.ring;
+  int k_unit = 0;
+  DownUnit d;
+  for (; walk.next(&d); ++k_unit) {
+    const int tb = k_unit & 1;
+    if (k_unit >= 2 && !wait_bar(c, kDEmpty0 + tb, ((k_unit >> 1) - 1) & 1)) return done;
+    umma::fence_after_sync();
+    for (int k = 0; k < d.k_len; k += kStepK, ++step) {
+      if (!wait_bar(c, kFull0 + step % S, (step / S) & 1)) return done;
+      umma::fence_after_sync();
+      const int n_mma = min(kStepK, d.k_len - k) / 16;
+      const uint32_t stage = (step % S) * stage_bytes;
+      for (int j = 0; j < n_mma; ++j) {
+        const uint32_t ra = stage + (j >> 2) * a_region + (j & 3) * 32;
+        const uint32_t rx = stage + 4 * a_region + (j >> 2) * kXRegion + (j & 3) * 32;
+        umma::mma_bf16(tmem + tb * kTile, base + (ra >> 4), base + (rx >> 4), kIdesc, k || j);
+      }
+      umma::commit(bar_at(c, kEmpty0 + step % S));
+    }
+    umma::commit(bar_at(c, kDFull0 + tb));
+  }
+  return done;
+}
+
+// Warp q: ranks 32 q .. 32 q + 31, one a lane.
+__device__ void down_epilogue(const Ctx& c, const Args& g, DownWalk walk, uint32_t tmem) {
+  const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
+  int k_unit = 0;
+  DownUnit d;
+  for (; walk.next(&d); ++k_unit) {
+    const int my_row = __ldcg(g.tile_rows + d.slot * kTile + lane), tb = k_unit & 1;
+    if (!wait_warp(c, kDFull0 + tb, (k_unit >> 1) & 1)) return;
+    umma::fence_after_sync();
+    float v[kTile];
+    umma::ld_32x32b_x32(tmem + ((uint32_t)(q * 32) << 16) + tb * kTile, v);
+    umma::wait_ld();
+    umma::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_at(c, kDEmpty0 + tb));
+    const int r = 32 * q + lane;
+    float* t = g.t + (long long)d.chunk * g.n * g.max_rank + r;
+#pragma unroll
+    for (int i = 0; i < kTile; ++i) {
+      const int row = __shfl_sync(kFull, my_row, i);
+      if (i < d.count && r < d.rank) t[(long long)row * g.max_rank] = v[i];
+    }
+  }
+}
+
+template <bool BF16, int S>
+__global__ void __launch_bounds__(kDownThreads, 1) down_kernel(const Args g) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ int start[kSlab / kWindow + 1];
+  __shared__ __align__(8) uint64_t bars[kDownBars];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  wait_prior_grid();
+  allow_next_grid();
+  Ctx c;
+  c.sbase = smem_addr(smem);
+  c.bars = smem_addr(bars);
+  c.abort_flag = &abort_word;
+  c.hdr = g.hdr;
+  const int warp = threadIdx.x >> 5;
+  if (c.sbase & 1023u) {  // the swizzled layout needs 1024-byte-aligned shared memory
+    if (threadIdx.x == 0) set_error(g.hdr, DA_DEVERR_TIMEOUT);
+    return;
+  }
+  // input checks, spread over the grid
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < g.n; i += gridDim.x * blockDim.x) {
+    const int v = __ldg(g.ids + i);
+    if (v >= g.n_adapters) set_error(g.hdr, DA_DEVERR_INDEX);
+    if (v >= 0 && v < g.n_adapters && g.ranks) {
+      const int r = __ldg(g.ranks + v);
+      if (r < 0 || r > g.max_rank) set_error(g.hdr, DA_DEVERR_LENGTH);
+    }
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kDownBars; ++i) {
+      uint32_t count = 1;  // tcgen05.commit
+      if (i < kEmpty0) count = kDownProdWarps;
+      if (i == kDEmpty0 || i == kDEmpty0 + 1) count = kDownEpWarps;
+      mbar_init(c.bars + 8 * i, count);
+    }
+    abort_word = 0;
+    fence_mbar_init();
+  }
+  if (warp == kDownMmaWarp) {
+    umma::tmem_alloc(smem_addr(&tmem_slot), kDownCols);
+    umma::tmem_relinquish();
+  }
+  umma::fence_before_sync();
+  const int tiles = count_tiles(g, start);  // holds CTA barriers
+  umma::fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
+  DownWalk walk{g, start, (int)blockIdx.x, tiles * g.n_chunks};
+  Commits done;
+  if (warp == kDownMmaWarp) {
+    if ((threadIdx.x & 31) == 0) {
+      done = down_mma<S>(c, g, walk, tmem);
+      umma::commit(bar_at(c, kDownDrain));  // arrives once every MMA above has completed
+    }
+  } else if (warp < kDownEpWarps) {
+    down_epilogue(c, g, walk, tmem);
+  } else {
+    down_produce<BF16, S>(c, g, walk);
+  }
+  umma::fence_before_sync();
+  __syncthreads();
+  if (warp == kDownMmaWarp) {
+    umma::fence_after_sync();
+    if ((threadIdx.x & 31) == 0) {
+      drain_commits(c, kDownDrain, 1, 1);
+      drain_commits(c, kEmpty0, S, done.ring);
+    }
+    __syncwarp();
+    umma::tmem_dealloc(tmem, kDownCols);
   }
 }
 
 // ---------------------------------------------------------------- up
-// Bytes between the rows of a term of t in shared memory: 2 * 16 * blocks
-// rounded to an odd multiple of 32, which spreads the 8-byte reads of four
-// neighbouring rows over all banks.
-__host__ __device__ constexpr int t_stride(int max_rank) {
-  const int b = 2 * max_rank;
-  return (b / 32) % 2 ? b : b + 32;
+
+constexpr int kGroups = 4;                  // epilogue groups of four warps, one accumulator each
+constexpr int kUpProdWarp0 = 16, kUpProdWarps = 4, kUpTWarp0 = 20, kUpTWarps = 4, kUpMmaWarp = 24;
+constexpr int kUpThreads = (kUpMmaWarp + 1) * 32;
+constexpr int kBRegion = kFeat * 128;       // 16 KB: 128 features x 64 ranks
+constexpr int kTRegion = kTile * 128;       // 4 KB: 32 members x 64 ranks
+constexpr int kBSlots = 8;                  // regions of the B ring
+constexpr int kTOff = kBSlots * kBRegion;   // 131072: two slots of three terms
+constexpr int kTSlot = 3 * 2 * kTRegion;
+constexpr int kUpSmem = kTOff + 2 * kTSlot; // 180224
+enum { kBFull0 = 0, kBEmpty0 = kBFull0 + kBSlots, kUDFull0 = kBEmpty0 + kBSlots,
+       kUDEmpty0 = kUDFull0 + kGroups, kTFull0 = kUDEmpty0 + kGroups, kTEmpty0 = kTFull0 + 2,
+       kUpDrain = kTEmpty0 + 2, kUpBars };
+constexpr uint32_t kUpCols = kGroups * kTile;
+static_assert(2 * (kUpSmem + 1024) > 233472, "one CTA per SM");
+
+// The CTA's units [first, last): tile u / blocks, features (u % blocks) * 128.
+struct UpWalk {
+  const Args& g;
+  const int* start;
+  int u, last, blocks;
+  int tile = -1;       // of the last unit returned
+  long long slot = 0;
+  int id = 0, count = 0, rank = 0, f0 = 0;
+  bool fresh = false;  // the unit is its tile's first in this CTA
+  bool ends = false;   // ... and its last
+  __device__ __forceinline__ bool next() {
+    if (u >= last) return false;
+    const int t = u / blocks;
+    fresh = t != tile;
+    if (fresh) {
+      tile = t;
+      slot = slot_of(start, g.windows, t);
+      id = __ldcg(g.tile_id + slot);
+      count = __ldcg(g.tile_count + slot);
+      rank = id >= 0 ? rank_of(g, id) : 0;
+    }
+    f0 = (u - t * blocks) * kFeat;
+    ++u;
+    ends = u >= last || u / blocks != t;
+    return true;
+  }
+};
+
+// B, 128 features a unit: consecutive lanes take consecutive 16-byte chunks of a
+// row's ranks, then the next row's.
+template <int S>
+__device__ void up_produce(const Ctx& c, const Args& g, UpWalk walk) {
+  const int lane = threadIdx.x & 31, tid = threadIdx.x - kUpProdWarp0 * 32;
+  const int slot_bytes = (kBSlots / S) * kBRegion;
+  int k = 0;
+  bool ok = true;
+  auto signal = [&](int s) {
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_at(c, kBFull0 + s % S));
+  };
+  while (ok && walk.next()) {
+    if (walk.id < 0) continue;
+    if (k >= S && !wait_warp(c, kBEmpty0 + k % S, (k / S - 1) & 1)) {
+      ok = false;
+      break;
+    }
+    const uint32_t slot = c.sbase + (k % S) * slot_bytes;
+    const int nc = ((walk.rank + 15) >> 4) * 2;    // 16-byte chunks of a row: 2 .. 16
+    const uint32_t inv = 65536u / nc + 1;          // q / nc = q * inv >> 16 for q < 2048
+    const __nv_bfloat16* b = g.b + ((long long)walk.id * g.N + walk.f0) * g.max_rank;
+    for (int q = tid; q < kFeat * nc; q += kUpProdWarps * 32) {
+      const int row = (int)((uint32_t)q * inv >> 16), ch = q - row * nc;
+      const int bytes = min(16, max(0, (walk.rank - 8 * ch) * 2));
+      cp_async16_zfill(slot + (ch >> 3) * kBRegion + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                       b + (long long)row * g.max_rank + 8 * ch, bytes);
+    }
+    cp_async_commit();
+    if (k >= S - 1) {
+      cp_async_wait<S - 1>();
+      signal(k - (S - 1));
+    }
+    ++k;
+  }
+  cp_async_wait<0>();
+  if (ok)
+    for (int s = max(0, k - (S - 1)); s < k; ++s) signal(s);
 }
 
-// Four ranks of feature row `p` (ranks k .. k + 3 of which `left` are below the
-// adapter's rank); the others are zero whatever memory holds.
-__device__ __forceinline__ uint2 load_b4(const __nv_bfloat16* p, int left) {
-  uint2 w = make_uint2(0, 0);
-  if (left > 0) w = __ldg(reinterpret_cast<const uint2*>(p));
-  if (left < 4) {
-    if (left <= 2) w.y = 0;
-    if (left == 3) w.y &= 0xffffu;
-    if (left == 1) w.x &= 0xffffu;
-  }
-  return w;
-}
-
-// Grid (feature blocks, tiles, Z): CTA (f, tile, z) adds to the rows of the
-// tile's groups z, z + Z, ..., features [f * n_step, (f + 1) * n_step); the CTA
-// z = 0 also copies the rows without an adapter.
-__global__ void __launch_bounds__(kUpThreads) up_kernel(const Args g) {
-  extern __shared__ __align__(16) uint8_t smem[];  // [3 terms][32 members][t_stride]
-  __shared__ int member[kTile];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int q = lane & 3, row8 = lane >> 2;
-  const int ts = t_stride(g.max_rank);
-  const int row0 = blockIdx.y * kTile;
-  wait_prior_grid();
-  allow_next_grid();
-  Groups gr = groups_of(g, row0, lane);
-  const int f0 = blockIdx.x * g.n_step, f1 = min(f0 + g.n_step, g.N);
-
-  if (blockIdx.z == 0 && (g.out != g.y || g.out_bf16)) {
-    unsigned none = __ballot_sync(kFull, gr.id < 0 && row0 + lane < g.n);
-    for (; none; none &= none - 1) {
-      const long long at = (long long)(row0 + __ffs(none) - 1) * g.N;
-      for (int f = f0 + 4 * (int)threadIdx.x; f < f1; f += 4 * kUpThreads) {
-        const float4 v = *reinterpret_cast<const float4*>(g.y + at + f);
-        if (g.out != g.y) *reinterpret_cast<float4*>(g.out + at + f) = v;
-        if (g.out_bf16)
-          *reinterpret_cast<uint2*>(g.out_bf16 + at + f) =
-              make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-      }
-    }
-  }
-
-  unsigned left = gr.leaders;
-  for (int j = 0; left; ++j) {
-    const int lead = __ffs(left) - 1;
-    left &= left - 1;
-    if (j % (int)gridDim.z != (int)blockIdx.z) continue;
-    const int id = __shfl_sync(kFull, gr.id, lead);
-    const unsigned members = __shfl_sync(kFull, gr.peers, lead);
-    const int count = __popc(members);
-    const int rank = rank_of(g, id, &gr.bad);
-    const int n_k = (rank + 15) >> 4, n_nt = (count + 7) >> 3;
-    const float scale = g.scales ? __ldg(g.scales + id) : 1.f;
-
-    // t of the members, scaled, as three bf16 terms: hi + mid + lo = t up to
-    // 2^-24 of it (each term takes the next 8 bits); ranks at or beyond the
-    // adapter's, and members that do not exist, are zero
-    __syncthreads();  // the previous group's terms and list have been read
-    if (warp == 0) list_members(member, members, row0, lane);
-    __syncthreads();
-    for (int i = threadIdx.x; i < kTile * n_k * 16; i += kUpThreads) {
-      const int c = i / (n_k * 16), r = i - c * (n_k * 16);
-      float v = 0.f;
-      if (c < count && r < rank) {
-        const float* t = g.t + (long long)member[c] * g.max_rank + r;
-        v = __ldcg(t);
-        for (int p = 1; p < g.n_parts; ++p) v += __ldcg(t + (long long)p * g.n * g.max_rank);
-        v *= scale;
-      }
-      const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-      // nothing is left of an infinity (inf - inf would make it a NaN)
-      const float r1 = __hisinf(hi) ? 0.f : v - __bfloat162float(hi);
-      const __nv_bfloat16 mid = __float2bfloat16_rn(r1);
-      const __nv_bfloat16 lo = __float2bfloat16_rn(r1 - __bfloat162float(mid));
-      uint8_t* at = smem + c * ts + 2 * r;
-      *reinterpret_cast<__nv_bfloat16*>(at) = hi;
-      *reinterpret_cast<__nv_bfloat16*>(at + kTile * ts) = mid;
-      *reinterpret_cast<__nv_bfloat16*>(at + 2 * kTile * ts) = lo;
-    }
-    __syncthreads();
-
-    // rows of this lane's accumulator columns 2q, 2q + 1 of each block of 8
-    int mrow[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      mrow[i] = member[(i >> 1) * 8 + 2 * q + (i & 1)];
-    }
-    const __nv_bfloat16* bmat = g.b + (long long)id * g.N * g.max_rank;
-    for (int f = f0 + warp * kWarpN; f < f1; f += kUpWarps * kWarpN) {
-      const int feat = f + 4 * row8;  // this lane's four features
-      float4 yv[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (mrow[i] >= 0)
-          yv[i] = *reinterpret_cast<const float4*>(g.y + (long long)mrow[i] * g.N + feat);
-      // M tile 0: features 4 row8 (rows 0-7) and 4 row8 + 1 (rows 8-15);
-      // M tile 1: 4 row8 + 2 and 4 row8 + 3
-      float acc[2][4][4];
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
-      const __nv_bfloat16* brow = bmat + (long long)feat * g.max_rank + 4 * q;
-#pragma unroll 4
-      for (int kb = 0; kb < n_k; ++kb) {
-        const int have = rank - kb * 16 - 4 * q;
-        uint2 w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = load_b4(brow + (long long)i * g.max_rank + kb * 16, have);
-        const uint32_t a0[4] = {w[0].x, w[1].x, w[0].y, w[1].y};
-        const uint32_t a1[4] = {w[2].x, w[3].x, w[2].y, w[3].y};
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-          if (nt >= n_nt) break;
-          const uint8_t* at = smem + (nt * 8 + row8) * ts + 32 * kb + 8 * q;
-#pragma unroll
-          for (int term = 2; term >= 0; --term) {  // small terms first
-            const uint2 tv = *reinterpret_cast<const uint2*>(at + term * kTile * ts);
-            mma(acc[0][nt], a0, tv.x, tv.y);
-            mma(acc[1][nt], a1, tv.x, tv.y);
+// t of a tile's members: chunk sums added in order, scaled, split.  Warp w takes
+// members w, w + 4, ...; a lane two ranks of each 64.
+__device__ void up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kUpTWarp0;
+  const long long part = (long long)g.n * g.max_rank;
+  int k = 0;
+  while (walk.next()) {
+    if (!walk.fresh || walk.id < 0) continue;
+    const int my_row = __ldcg(g.tile_rows + walk.slot * kTile + lane);
+    const float scale = g.scales ? __ldg(g.scales + walk.id) : 1.f;
+    if (k >= 2 && !wait_warp(c, kTEmpty0 + (k & 1), ((k >> 1) - 1) & 1)) return;
+    const uint32_t slot = c.sbase + kTOff + (k & 1) * kTSlot;
+    for (int m = w; m < walk.count; m += kUpTWarps) {
+      const int row = __shfl_sync(kFull, my_row, m);
+      for (int r0 = 0; r0 < ((walk.rank + 15) & ~15); r0 += 64) {
+        const int r = r0 + 2 * lane;
+        float v[2] = {0.f, 0.f};
+        if (r < walk.rank) {  // the row is max_rank long, so r + 1 may be read
+          const float* t = g.t + (long long)row * g.max_rank + r;
+          float2 s = __ldcg(reinterpret_cast<const float2*>(t));
+          for (int p = 1; p < g.n_chunks; ++p) {
+            const float2 e = __ldcg(reinterpret_cast<const float2*>(t + p * part));
+            s.x += e.x;
+            s.y += e.y;
           }
+          v[0] = s.x * scale;
+          v[1] = r + 1 < walk.rank ? s.y * scale : 0.f;
+        }
+        const uint32_t at = slot + (r0 ? kTRegion : 0) + m * 128 +
+                            (((lane >> 2) ^ (m & 7)) << 4) + (lane & 3) * 4;
+#pragma unroll
+        for (int term = 0; term < 3; ++term) {  // each takes the next eight bits
+          __nv_bfloat16 h[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            h[e] = __float2bfloat16_rn(v[e]);
+            // nothing is left of an infinity (inf - inf would make it a NaN)
+            v[e] = __hisinf(h[e]) ? 0.f : v[e] - __bfloat162float(h[e]);
+          }
+          const uint32_t word = (uint32_t)__bfloat16_as_ushort(h[0]) |
+                                (uint32_t)__bfloat16_as_ushort(h[1]) << 16;
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + term * 2 * kTRegion), "r"(word)
+                       : "memory");
         }
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (mrow[i] < 0) continue;
-        const int nt = i >> 1, e = i & 1;
-        float4 v = yv[i];
-        v.x += acc[0][nt][e];
-        v.y += acc[0][nt][2 + e];
-        v.z += acc[1][nt][e];
-        v.w += acc[1][nt][2 + e];
-        const long long at = (long long)mrow[i] * g.N + feat;
-        *reinterpret_cast<float4*>(g.out + at) = v;
-        if (g.out_bf16)
-          *reinterpret_cast<uint2*>(g.out_bf16 + at) =
-              make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+    }
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_at(c, kTFull0 + (k & 1)));
+    ++k;
+  }
+}
+
+template <int S>
+__device__ Commits up_mma(const Ctx& c, const Args& g, UpWalk walk, uint32_t tmem) {
+  const int slot_bytes = (kBSlots / S) * kBRegion;
+  const uint64_t base = umma::smem_desc(c.sbase, 16, 1024, umma::kSwizzle128B);
+  Commits done;
+  int& k = done.ring;
+  int& tiles = done.terms;  // tiles begun; a tile is committed with its last unit
+  uint32_t used = 0;  // per group: how often its accumulator was filled, a parity bit each
+  uint32_t ever = 0;
+  for (int i = 0; walk.next(); ++i) {
+    const int e = i % kGroups;
+    if (walk.id < 0) continue;
+    if (walk.fresh) {
+      if (!wait_bar(c, kTFull0 + (tiles & 1), (tiles >> 1) & 1)) return done;
+      ++tiles;
+    }
+    bool ok = true;
+    if ((ever >> e) & 1u) ok = wait_bar(c, kUDEmpty0 + e, ((used >> e) & 1u) ^ 1u);
+    if (!ok || !wait_bar(c, kBFull0 + k % S, (k / S) & 1)) {
+      --tiles;  // its last unit will not be committed
+      return done;
+    }
+    umma::fence_after_sync();
+    const uint32_t bs = (k % S) * slot_bytes, ts = kTOff + ((tiles - 1) & 1) * kTSlot;
+    const int n_k = (walk.rank + 15) >> 4;
+    for (int term = 2; term >= 0; --term) {  // small terms first
+      for (int kb = 0; kb < n_k; ++kb) {
+        const uint32_t rb = bs + (kb >> 2) * kBRegion + (kb & 3) * 32;
+        const uint32_t rt = ts + term * 2 * kTRegion + (kb >> 2) * kTRegion + (kb & 3) * 32;
+        umma::mma_bf16(tmem + e * kTile, base + (rb >> 4), base + (rt >> 4), kIdesc,
+                       term != 2 || kb != 0);
       }
     }
+    umma::commit(bar_at(c, kBEmpty0 + k % S));
+    umma::commit(bar_at(c, kUDFull0 + e));
+    if (walk.ends) umma::commit(bar_at(c, kTEmpty0 + ((tiles - 1) & 1)));
+    ever |= 1u << e;
+    used ^= 1u << e;
+    ++k;
   }
-  if (gr.bad && blockIdx.x == 0 && warp == 0) set_error(g.hdr, gr.bad);
+  return done;
+}
+
+// Group e takes units e, e + 4, ... of the CTA; warp q of it features 32 q ..
+// + 31, one a lane; a member's line of y is asked for before the accumulator is.
+__device__ void up_epilogue(const Ctx& c, const Args& g, UpWalk walk, uint32_t tmem) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = warp & 3, e = warp >> 2;
+  uint32_t parity = 0;
+  for (int i = 0; walk.next(); ++i) {
+    if (i % kGroups != e) continue;
+    const int my_row = __ldcg(g.tile_rows + walk.slot * kTile + lane);
+    const int f = walk.f0 + 32 * q + lane;
+    const int count = walk.count;
+    float v[kTile];
+#pragma unroll
+    for (int m = 0; m < kTile; ++m) {
+      const int row = __shfl_sync(kFull, my_row, m);
+      if (m < count) v[m] = g.y[(long long)row * g.N + f];
+    }
+    if (walk.id >= 0) {
+      if (!wait_warp(c, kUDFull0 + e, parity)) return;
+      parity ^= 1u;
+      umma::fence_after_sync();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float d[16];
+        umma::ld_32x32b_x16(tmem + ((uint32_t)(q * 32) << 16) + e * kTile + 16 * h, d);
+        umma::wait_ld();
+#pragma unroll
+        for (int m = 0; m < 16; ++m) v[16 * h + m] += d[m];
+      }
+      umma::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_at(c, kUDEmpty0 + e));
+    }
+    const bool write = walk.id >= 0 || g.out != g.y;
+#pragma unroll
+    for (int m = 0; m < kTile; ++m) {
+      const int row = __shfl_sync(kFull, my_row, m);
+      if (m >= count) continue;
+      const long long at = (long long)row * g.N + f;
+      if (write) g.out[at] = v[m];
+      if (g.out_bf16) g.out_bf16[at] = __float2bfloat16_rn(v[m]);
+    }
+  }
+}
+
+template <int S>
+__global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ int start[kSlab / kWindow + 1];
+  __shared__ __align__(8) uint64_t bars[kUpBars];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  wait_prior_grid();
+  allow_next_grid();
+  Ctx c;
+  c.sbase = smem_addr(smem);
+  c.bars = smem_addr(bars);
+  c.abort_flag = &abort_word;
+  c.hdr = g.hdr;
+  const int warp = threadIdx.x >> 5;
+  if (c.sbase & 1023u) {
+    if (threadIdx.x == 0) set_error(g.hdr, DA_DEVERR_TIMEOUT);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kUpBars; ++i) {
+      uint32_t count = 1;  // tcgen05.commit
+      if (i < kBEmpty0) count = kUpProdWarps;
+      if (i >= kUDEmpty0 && i < kTFull0) count = 4;
+      if (i == kTFull0 || i == kTFull0 + 1) count = kUpTWarps;
+      mbar_init(c.bars + 8 * i, count);
+    }
+    abort_word = 0;
+    fence_mbar_init();
+  }
+  if (warp == kUpMmaWarp) {
+    umma::tmem_alloc(smem_addr(&tmem_slot), kUpCols);
+    umma::tmem_relinquish();
+  }
+  umma::fence_before_sync();
+  const int tiles = count_tiles(g, start);  // holds CTA barriers
+  umma::fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
+  const int blocks = g.N / kFeat;
+  const long long total = (long long)tiles * blocks;
+  UpWalk walk{g, start, (int)(total * blockIdx.x / gridDim.x),
+              (int)(total * (blockIdx.x + 1) / gridDim.x), blocks};
+  Commits done;
+  if (warp == kUpMmaWarp) {
+    if ((threadIdx.x & 31) == 0) {
+      done = up_mma<S>(c, g, walk, tmem);
+      umma::commit(bar_at(c, kUpDrain));
+    }
+  } else if (warp >= kUpTWarp0) {
+    up_make_t(c, g, walk);
+  } else if (warp >= kUpProdWarp0) {
+    up_produce<S>(c, g, walk);
+  } else {
+    up_epilogue(c, g, walk, tmem);
+  }
+  umma::fence_before_sync();
+  __syncthreads();
+  if (warp == kUpMmaWarp) {
+    umma::fence_after_sync();
+    if ((threadIdx.x & 31) == 0) {
+      drain_commits(c, kUpDrain, 1, 1);
+      drain_commits(c, kBEmpty0, S, done.ring);
+      drain_commits(c, kTEmpty0, 2, done.terms);
+    }
+    __syncwarp();
+    umma::tmem_dealloc(tmem, kUpCols);
+  }
 }
 
 // ---------------------------------------------------------------- host
 
 constexpr size_t kHdr = 256;
 
-int groups_of_k(int K) { return (K + kGroupK - 1) / kGroupK; }
-
-// A CTA per K group until the tiles alone fill the GPU about once; then one
-// walks all groups of its tile, and t is written once.
-int parts_of(int n, int K) { return n > 4096 ? 1 : groups_of_k(K); }
+size_t round_up(size_t v, size_t m) { return (v + m - 1) / m * m; }
 
 bool shape_ok(int n, int N, int K, int n_adapters, int max_rank) {
   if (n < 0 || N <= 0 || K <= 0 || N % NVFP4_MM_TILE_N || K % 64) return false;
@@ -407,6 +789,47 @@ bool shape_ok(int n, int N, int K, int n_adapters, int max_rank) {
 }
 
 bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+int chunks_of(int K) { return (K + kKChunk - 1) / kKChunk; }
+
+struct Layout {
+  size_t tiles_in, tile_id, tile_count, tile_rows, t, total;
+};
+
+Layout layout_of(int n, int K, int max_rank) {
+  const size_t rows = (size_t)std::min(n, kSlab);
+  Layout l;
+  l.tiles_in = kHdr;
+  l.tile_id = l.tiles_in + round_up((rows + kWindow - 1) / kWindow * 4, 256);
+  l.tile_count = l.tile_id + round_up(rows * 4, 256);
+  l.tile_rows = l.tile_count + round_up(rows * 4, 256);
+  l.t = l.tile_rows + rows * kTile * 4;
+  l.total = l.t + (size_t)chunks_of(K) * rows * max_rank * 4;
+  return l;
+}
+
+template <typename F>
+cudaError_t allow_smem(F* kernel, int bytes) {  // it holds per device, and is cheap
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <bool BF16, int S>
+cudaError_t launch_down(const Args& g, int sms, cudaStream_t st) {
+  // at least so much that a second CTA stays off the SM: one owns tensor memory
+  const int smem = std::max(S * down_stage_bytes(g.max_rank), 118 * 1024);
+  cudaError_t e = allow_smem(down_kernel<BF16, S>, smem);
+  if (e != cudaSuccess) return e;
+  const int grid = (int)std::min<long long>((long long)g.n * g.n_chunks, sms);
+  return launch_after(down_kernel<BF16, S>, dim3(grid), dim3(kDownThreads), (size_t)smem, st, g);
+}
+
+template <int S>
+cudaError_t launch_up(const Args& g, int sms, cudaStream_t st) {
+  cudaError_t e = allow_smem(up_kernel<S>, kUpSmem);
+  if (e != cudaSuccess) return e;
+  const int grid = (int)std::min<long long>((long long)g.n * (g.N / kFeat), sms);
+  return launch_after(up_kernel<S>, dim3(grid), dim3(kUpThreads), (size_t)kUpSmem, st, g);
+}
 
 }  // namespace
 }  // namespace da
@@ -418,7 +841,7 @@ extern "C" {
 size_t nvfp4_mm_adapters_workspace_bytes(int32_t n, int32_t N, int32_t K, int32_t n_adapters,
                                          int32_t max_rank) {
   if (!shape_ok(n, N, K, n_adapters, max_rank)) return 0;
-  return kHdr + (size_t)parts_of(n, K) * n * max_rank * sizeof(float);
+  return layout_of(n, K, max_rank).total;
 }
 
 int nvfp4_mm_adapters(const void* x, int32_t x_dtype, int32_t n, int32_t N, int32_t K,
@@ -440,48 +863,53 @@ int nvfp4_mm_adapters(const void* x, int32_t x_dtype, int32_t n, int32_t N, int3
   if (!ws || !aligned_to(ws, 256)) return DA_ERR_WORKSPACE;
   if (ws_bytes < nvfp4_mm_adapters_workspace_bytes(n, N, K, n_adapters, max_rank))
     return DA_ERR_WORKSPACE;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return DA_ERR_CUDA;
+  const Layout l = layout_of(n, K, max_rank);
+  uint8_t* base = static_cast<uint8_t*>(ws);
   Args g;
   std::memset(&g, 0, sizeof(g));
-  g.x = x;
   g.a = static_cast<const __nv_bfloat16*>(a);
   g.b = static_cast<const __nv_bfloat16*>(b);
   g.ranks = ranks;
   g.scales = scales;
-  g.ids = ids;
-  g.y = y;
-  g.out = out;
-  g.out_bf16 = static_cast<__nv_bfloat16*>(out_bf16);
   g.hdr = static_cast<int32_t*>(ws);
-  g.t = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kHdr);
-  g.n = n;
+  g.tiles_in = reinterpret_cast<int32_t*>(base + l.tiles_in);
+  g.tile_id = reinterpret_cast<int32_t*>(base + l.tile_id);
+  g.tile_count = reinterpret_cast<int32_t*>(base + l.tile_count);
+  g.tile_rows = reinterpret_cast<int32_t*>(base + l.tile_rows);
+  g.t = reinterpret_cast<float*>(base + l.t);
   g.N = N;
   g.K = K;
   g.n_adapters = n_adapters;
   g.max_rank = max_rank;
-  g.n_groups = groups_of_k(K);
-  g.n_parts = parts_of(n, K);
+  g.n_chunks = chunks_of(K);
+  g.copy = out != y || out_bf16;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int tiles = (n + kTile - 1) / kTile;
-  if (tiles > 65535) return DA_ERR_UNSUPPORTED;  // n * K and n * N already bound it far below
-  // a CTA per group of a tile while there are few CTAs without it
-  const auto spread = [&](long long ctas) {
-    return (unsigned)std::max<long long>(1, std::min<long long>({(long long)kTile, (long long)n,
-                                                                 (long long)n_adapters,
-                                                                 2048 / std::max(1ll, ctas)}));
-  };
-  const dim3 down((unsigned)g.n_parts, (unsigned)tiles, spread((long long)g.n_parts * tiles));
-  cudaError_t e = x_dtype == NVFP4_X_BF16
-                      ? launch_after(down_kernel<true>, down, dim3(kDownThreads), 0, st, g)
-                      : launch_after(down_kernel<false>, down, dim3(kDownThreads), 0, st, g);
-  if (e != cudaSuccess) return DA_ERR_CUDA;
-  // 256 features a CTA (one step of its warps) while that leaves few CTAs
-  g.n_step = kUpWarps * kWarpN;
-  while (g.n_step < 1024 && (long long)tiles * (N / g.n_step) > 2048) g.n_step *= 2;
-  const unsigned blocks = (unsigned)((N + g.n_step - 1) / g.n_step);
-  const size_t smem = 3 * (size_t)kTile * t_stride(max_rank);
-  e = launch_after(up_kernel, dim3(blocks, (unsigned)tiles, spread((long long)blocks * tiles)),
-                   dim3(kUpThreads), smem, st, g);
-  return e == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  const bool bf16 = x_dtype == NVFP4_X_BF16;
+  // four stages of up to 48 KB, or two of up to 80; B rows of up to 64 ranks take
+  // one region of the ring, longer ones two
+  auto* down = down_stages(max_rank) == 4 ? (bf16 ? launch_down<true, 4> : launch_down<false, 4>)
+                                          : (bf16 ? launch_down<true, 2> : launch_down<false, 2>);
+  auto* up = max_rank <= 64 ? launch_up<kBSlots> : launch_up<kBSlots / 2>;
+  for (int r0 = 0; r0 < n; r0 += kSlab) {
+    const size_t row = (size_t)r0;
+    g.n = std::min(kSlab, n - r0);
+    g.windows = (g.n + kWindow - 1) / kWindow;
+    g.first = r0 == 0;
+    g.x = static_cast<const uint8_t*>(x) + row * K * (bf16 ? 2 : 4);
+    g.ids = ids + row;
+    g.y = y + row * N;
+    g.out = out + row * N;
+    g.out_bf16 = out_bf16 ? static_cast<__nv_bfloat16*>(out_bf16) + row * N : nullptr;
+    if (launch_after(plan_kernel, dim3((unsigned)g.windows), dim3(kWindow), 0, st, g) != cudaSuccess)
+      return DA_ERR_CUDA;
+    if (down(g, sms, st) != cudaSuccess) return DA_ERR_CUDA;
+    if (up(g, sms, st) != cudaSuccess) return DA_ERR_CUDA;
+  }
+  return DA_OK;
 }
 
 }  // extern "C"
