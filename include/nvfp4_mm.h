@@ -124,7 +124,7 @@ size_t nvfp4_mm_adapters_workspace_bytes(int32_t n, int32_t N, int32_t K, int32_
  *   ids     int32 [n].
  *   y, out  fp32 [n, N], 16-byte aligned; out may be y (rows without an adapter
  *           are then not touched) but must not overlap it otherwise.
- *   out_bf16  bf16 [n, N] or NULL, 8-byte aligned: out rounded to nearest even,
+ *   out_bf16  bf16 [n, N] or NULL, 16-byte aligned: out rounded to nearest even,
  *           all rows.
  *   ws      as for nvfp4_mm.
  * An id at or above n_adapters counts as none and sets DA_DEVERR_INDEX, a rank

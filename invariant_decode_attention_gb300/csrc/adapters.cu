@@ -15,9 +15,10 @@
 //   up    out: D[feature, member] += B[feature, r] t[member, r], M = 128 features,
 //         N = 32.  The chunk sums of t are added in order, scaled, and split into
 //         three bf16 terms that hold their 24 bits; their products with B are
-//         exact, so out keeps fp32 accuracy.  A unit is a tile and 128 features;
-//         a thread of the epilogue holds one feature, so a warp reads y and writes
-//         out in whole 128-byte lines, a row at a time.
+//         exact, so out keeps fp32 accuracy.  A unit is a tile and 128 features.
+//         y arrives and out leaves by bulk copies of a member's 512 bytes (loads
+//         and stores by the epilogue's threads, 4 bytes a lane, took 4900
+//         instructions a unit and 267 us for 8192 rows of 8192).
 // The orders of all sums depend on K and the rank alone.  A column of an MMA does
 // not depend on the other columns, so neither do a row's bits.
 //
@@ -82,6 +83,22 @@ __device__ __forceinline__ void fence_proxy_async() {
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
+}
+
+// Bulk store of `bytes` (a multiple of 16, both addresses 16-byte aligned).
+__device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src),
+               "r"(bytes)
+               : "memory");
+}
+
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// Until this thread's bulk stores have read their shared memory.
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -288,6 +305,7 @@ struct DownWalk {
 template <bool BF16, int S>
 __device__ void down_produce(const Ctx& c, const Args& g, DownWalk walk) {
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kDownProdWarp0;
+  constexpr int kLag = S / 2;  // stages that are landing while others are multiplied
   const int stage_bytes = down_stage_bytes(g.max_rank), a_region = g.max_rank * 128;
   const uint32_t chunk16 = lane & 7, region = lane >> 3;  // of this lane's 16 bytes
   int step = 0;
@@ -345,15 +363,15 @@ __device__ void down_produce(const Ctx& c, const Args& g, DownWalk walk) {
                        : "memory");
       }
       cp_async_commit();
-      if (step >= S - 1) {
-        cp_async_wait<S - 1>();
-        signal(step - (S - 1));
+      if (step >= kLag) {
+        cp_async_wait<kLag>();
+        signal(step - kLag);
       }
     }
   }
   cp_async_wait<0>();  // what is left has landed as well
   if (ok)
-    for (int s = max(0, step - (S - 1)); s < step; ++s) signal(s);
+    for (int s = max(0, step - kLag); s < step; ++s) signal(s);
 }
 
 template <int S>
@@ -484,55 +502,71 @@ __global__ void __launch_bounds__(kDownThreads, 1) down_kernel(const Args g) {
 // ---------------------------------------------------------------- up
 
 constexpr int kGroups = 4;                  // epilogue groups of four warps, one accumulator each
-constexpr int kUpProdWarp0 = 16, kUpProdWarps = 4, kUpTWarp0 = 20, kUpTWarps = 4, kUpMmaWarp = 24;
-constexpr int kUpThreads = (kUpMmaWarp + 1) * 32;
+constexpr int kUpProdWarp0 = 16, kUpProdWarps = 4, kUpTWarp0 = 20, kUpTWarps = 4, kUpMmaWarp = 24,
+              kUpYWarp = 25;
+constexpr int kUpThreads = (kUpYWarp + 1) * 32;
 constexpr int kBRegion = kFeat * 128;       // 16 KB: 128 features x 64 ranks
 constexpr int kTRegion = kTile * 128;       // 4 KB: 32 members x 64 ranks
-constexpr int kBSlots = 8;                  // regions of the B ring
-constexpr int kTOff = kBSlots * kBRegion;   // 131072: two slots of three terms
-constexpr int kTSlot = 3 * 2 * kTRegion;
-constexpr int kUpSmem = kTOff + 2 * kTSlot; // 180224
-enum { kBFull0 = 0, kBEmpty0 = kBFull0 + kBSlots, kUDFull0 = kBEmpty0 + kBSlots,
+constexpr int kYRow = kFeat * 4;            // 512 bytes of a row of y
+constexpr int kYSlot = kTile * kYRow + kTile * kFeat * 2;  // y, then out as bf16: 24 KB
+
+// Shared memory by R, the 64-rank regions of an adapter of max_rank: four or two
+// slots of B, two of t's terms, five or four of y.
+template <int R>
+struct Up {
+  static constexpr int kBSlots = 4 / R, kYSlots = 6 - R;
+  static constexpr int kTOff = kBSlots * R * kBRegion;
+  static constexpr int kTSlot = 3 * R * kTRegion;
+  static constexpr int kYOff = kTOff + 2 * kTSlot;
+  static constexpr int kSmem = kYOff + kYSlots * kYSlot;
+  static_assert(kYOff % 1024 == 0 && kSmem <= 220 * 1024 && 2 * kSmem > 233472, "one CTA per SM");
+};
+constexpr int kMaxBSlots = 4, kMaxYSlots = 5;
+enum { kBFull0 = 0, kBEmpty0 = kBFull0 + kMaxBSlots, kYFull0 = kBEmpty0 + kMaxBSlots,
+       kYEmpty0 = kYFull0 + kMaxYSlots, kUDFull0 = kYEmpty0 + kMaxYSlots,
        kUDEmpty0 = kUDFull0 + kGroups, kTFull0 = kUDEmpty0 + kGroups, kTEmpty0 = kTFull0 + 2,
        kUpDrain = kTEmpty0 + 2, kUpBars };
 constexpr uint32_t kUpCols = kGroups * kTile;
-static_assert(2 * (kUpSmem + 1024) > 233472, "one CTA per SM");
 
 // The CTA's units [first, last): tile u / blocks, features (u % blocks) * 128.
 struct UpWalk {
   const Args& g;
   const int* start;
-  int u, last, blocks;
-  int tile = -1;       // of the last unit returned
+  int left, tile, block, blocks;  // units to come, and where the next one is
   long long slot = 0;
   int id = 0, count = 0, rank = 0, f0 = 0;
   bool fresh = false;  // the unit is its tile's first in this CTA
   bool ends = false;   // ... and its last
+  bool seen = false;
   __device__ __forceinline__ bool next() {
-    if (u >= last) return false;
-    const int t = u / blocks;
-    fresh = t != tile;
+    if (left == 0) return false;
+    --left;
+    fresh = !seen;
     if (fresh) {
-      tile = t;
-      slot = slot_of(start, g.windows, t);
+      slot = slot_of(start, g.windows, tile);
       id = __ldcg(g.tile_id + slot);
       count = __ldcg(g.tile_count + slot);
       rank = id >= 0 ? rank_of(g, id) : 0;
+      seen = true;
     }
-    f0 = (u - t * blocks) * kFeat;
-    ++u;
-    ends = u >= last || u / blocks != t;
+    f0 = block * kFeat;
+    if (++block == blocks) {
+      block = 0;
+      ++tile;
+      seen = false;
+    }
+    ends = left == 0 || !seen;
     return true;
   }
 };
 
-// B, 128 features a unit: consecutive lanes take consecutive 16-byte chunks of a
-// row's ranks, then the next row's.
-template <int S>
+// B, 128 features a unit: a thread keeps one 16-byte chunk of the ranks and steps
+// through the features, neighbours in a row taking neighbouring chunks.
+template <int R>
 __device__ void up_produce(const Ctx& c, const Args& g, UpWalk walk) {
+  constexpr int S = Up<R>::kBSlots, kLag = S / 2;
   const int lane = threadIdx.x & 31, tid = threadIdx.x - kUpProdWarp0 * 32;
-  const int slot_bytes = (kBSlots / S) * kBRegion;
-  int k = 0;
+  int k = 0, row0 = 0, rows = 1, ch = 0, bytes = 0;
   bool ok = true;
   auto signal = [&](int s) {
     fence_proxy_async();
@@ -541,34 +575,37 @@ __device__ void up_produce(const Ctx& c, const Args& g, UpWalk walk) {
   };
   while (ok && walk.next()) {
     if (walk.id < 0) continue;
+    if (walk.fresh) {
+      const int nc = ((walk.rank + 15) >> 4) * 2;  // 16-byte chunks of a row: 2 .. 16
+      rows = (kUpProdWarps * 32) / nc;             // features that the threads cover at once
+      row0 = tid / nc;
+      ch = tid - row0 * nc;
+      if (row0 >= rows) row0 = kFeat;              // left over: no part in it
+      bytes = min(16, max(0, (walk.rank - 8 * ch) * 2));
+    }
     if (k >= S && !wait_warp(c, kBEmpty0 + k % S, (k / S - 1) & 1)) {
       ok = false;
       break;
     }
-    const uint32_t slot = c.sbase + (k % S) * slot_bytes;
-    const int nc = ((walk.rank + 15) >> 4) * 2;    // 16-byte chunks of a row: 2 .. 16
-    const uint32_t inv = 65536u / nc + 1;          // q / nc = q * inv >> 16 for q < 2048
-    const __nv_bfloat16* b = g.b + ((long long)walk.id * g.N + walk.f0) * g.max_rank;
-    for (int q = tid; q < kFeat * nc; q += kUpProdWarps * 32) {
-      const int row = (int)((uint32_t)q * inv >> 16), ch = q - row * nc;
-      const int bytes = min(16, max(0, (walk.rank - 8 * ch) * 2));
-      cp_async16_zfill(slot + (ch >> 3) * kBRegion + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
-                       b + (long long)row * g.max_rank + 8 * ch, bytes);
-    }
+    const uint32_t to = c.sbase + (k % S) * (R * kBRegion) + (ch >> 3) * kBRegion;
+    const __nv_bfloat16* b = g.b + ((long long)walk.id * g.N + walk.f0) * g.max_rank + 8 * ch;
+    for (int row = row0; row < kFeat; row += rows)
+      cp_async16_zfill(to + row * 128 + (((ch & 7) ^ (row & 7)) << 4), b + row * g.max_rank, bytes);
     cp_async_commit();
-    if (k >= S - 1) {
-      cp_async_wait<S - 1>();
-      signal(k - (S - 1));
+    if (k >= kLag) {
+      cp_async_wait<kLag>();
+      signal(k - kLag);
     }
     ++k;
   }
   cp_async_wait<0>();
   if (ok)
-    for (int s = max(0, k - (S - 1)); s < k; ++s) signal(s);
+    for (int s = max(0, k - kLag); s < k; ++s) signal(s);
 }
 
 // t of a tile's members: chunk sums added in order, scaled, split.  Warp w takes
 // members w, w + 4, ...; a lane two ranks of each 64.
+template <int R>
 __device__ void up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kUpTWarp0;
   const long long part = (long long)g.n * g.max_rank;
@@ -578,15 +615,17 @@ __device__ void up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
     const int my_row = __ldcg(g.tile_rows + walk.slot * kTile + lane);
     const float scale = g.scales ? __ldg(g.scales + walk.id) : 1.f;
     if (k >= 2 && !wait_warp(c, kTEmpty0 + (k & 1), ((k >> 1) - 1) & 1)) return;
-    const uint32_t slot = c.sbase + kTOff + (k & 1) * kTSlot;
+    const uint32_t slot = c.sbase + Up<R>::kTOff + (k & 1) * Up<R>::kTSlot;
     for (int m = w; m < walk.count; m += kUpTWarps) {
       const int row = __shfl_sync(kFull, my_row, m);
-      for (int r0 = 0; r0 < ((walk.rank + 15) & ~15); r0 += 64) {
-        const int r = r0 + 2 * lane;
+#pragma unroll
+      for (int reg = 0; reg < R; ++reg) {
+        const int r = 64 * reg + 2 * lane;
         float v[2] = {0.f, 0.f};
         if (r < walk.rank) {  // the row is max_rank long, so r + 1 may be read
           const float* t = g.t + (long long)row * g.max_rank + r;
           float2 s = __ldcg(reinterpret_cast<const float2*>(t));
+#pragma unroll 4
           for (int p = 1; p < g.n_chunks; ++p) {
             const float2 e = __ldcg(reinterpret_cast<const float2*>(t + p * part));
             s.x += e.x;
@@ -595,8 +634,8 @@ __device__ void up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
           v[0] = s.x * scale;
           v[1] = r + 1 < walk.rank ? s.y * scale : 0.f;
         }
-        const uint32_t at = slot + (r0 ? kTRegion : 0) + m * 128 +
-                            (((lane >> 2) ^ (m & 7)) << 4) + (lane & 3) * 4;
+        const uint32_t at = slot + reg * kTRegion + m * 128 + (((lane >> 2) ^ (m & 7)) << 4) +
+                            (lane & 3) * 4;
 #pragma unroll
         for (int term = 0; term < 3; ++term) {  // each takes the next eight bits
           __nv_bfloat16 h[2];
@@ -608,7 +647,7 @@ __device__ void up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
           }
           const uint32_t word = (uint32_t)__bfloat16_as_ushort(h[0]) |
                                 (uint32_t)__bfloat16_as_ushort(h[1]) << 16;
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + term * 2 * kTRegion), "r"(word)
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + term * R * kTRegion), "r"(word)
                        : "memory");
         }
       }
@@ -620,14 +659,14 @@ __device__ void up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
   }
 }
 
-template <int S>
+template <int R>
 __device__ Commits up_mma(const Ctx& c, const Args& g, UpWalk walk, uint32_t tmem) {
-  const int slot_bytes = (kBSlots / S) * kBRegion;
+  constexpr int S = Up<R>::kBSlots;
   const uint64_t base = umma::smem_desc(c.sbase, 16, 1024, umma::kSwizzle128B);
   Commits done;
   int& k = done.ring;
   int& tiles = done.terms;  // tiles begun; a tile is committed with its last unit
-  uint32_t used = 0;  // per group: how often its accumulator was filled, a parity bit each
+  uint32_t used = 0;        // per group: how often its accumulator was filled, a parity bit each
   uint32_t ever = 0;
   for (int i = 0; walk.next(); ++i) {
     const int e = i % kGroups;
@@ -643,12 +682,12 @@ __device__ Commits up_mma(const Ctx& c, const Args& g, UpWalk walk, uint32_t tme
       return done;
     }
     umma::fence_after_sync();
-    const uint32_t bs = (k % S) * slot_bytes, ts = kTOff + ((tiles - 1) & 1) * kTSlot;
+    const uint32_t bs = (k % S) * (R * kBRegion), ts = Up<R>::kTOff + ((tiles - 1) & 1) * Up<R>::kTSlot;
     const int n_k = (walk.rank + 15) >> 4;
     for (int term = 2; term >= 0; --term) {  // small terms first
       for (int kb = 0; kb < n_k; ++kb) {
         const uint32_t rb = bs + (kb >> 2) * kBRegion + (kb & 3) * 32;
-        const uint32_t rt = ts + term * 2 * kTRegion + (kb >> 2) * kTRegion + (kb & 3) * 32;
+        const uint32_t rt = ts + (term * R + (kb >> 2)) * kTRegion + (kb & 3) * 32;
         umma::mma_bf16(tmem + e * kTile, base + (rb >> 4), base + (rt >> 4), kIdesc,
                        term != 2 || kb != 0);
       }
@@ -663,51 +702,95 @@ __device__ Commits up_mma(const Ctx& c, const Args& g, UpWalk walk, uint32_t tme
   return done;
 }
 
+// y, a member's 512 bytes by one bulk copy each: a lane per member.
+template <int R>
+__device__ void up_fetch_y(const Ctx& c, const Args& g, UpWalk walk) {
+  constexpr int S = Up<R>::kYSlots;
+  const int lane = threadIdx.x & 31;
+  const uint64_t policy = policy_evict_first();  // read once
+  int i = 0;
+  for (; walk.next(); ++i) {
+    const int row = __ldcg(g.tile_rows + walk.slot * kTile + lane);
+    if (i >= S && !wait_warp(c, kYEmpty0 + i % S, (i / S - 1) & 1)) break;
+    if (lane == 0) mbar_arrive_expect_tx(bar_at(c, kYFull0 + i % S), walk.count * kYRow);
+    __syncwarp();
+    if (lane < walk.count)
+      bulk_g2s(c.sbase + Up<R>::kYOff + (i % S) * kYSlot + lane * kYRow,
+               g.y + (long long)row * g.N + walk.f0, kYRow, bar_at(c, kYFull0 + i % S), policy);
+  }
+  // copies still in flight land before the shared memory goes away (normally the
+  // epilogue has waited for every one already)
+  for (int s = 0; s < S && s < i; ++s) {
+    if (lane == 0 && !mbar_wait(bar_at(c, kYFull0 + s), ((i - 1 - s) / S) & 1))
+      set_error(c.hdr, DA_DEVERR_TIMEOUT);
+  }
+  __syncwarp();
+}
+
 // Group e takes units e, e + 4, ... of the CTA; warp q of it features 32 q ..
-// + 31, one a lane; a member's line of y is asked for before the accumulator is.
-__device__ void up_epilogue(const Ctx& c, const Args& g, UpWalk walk, uint32_t tmem) {
+// + 31, one a lane.  The sum replaces y in shared memory and leaves by bulk
+// stores, a lane of one warp per member.
+template <int R>
+__device__ void up_epilogue(const Ctx& c, const Args& g, UpWalk walk, uint32_t tmem, uint8_t* smem) {
+  constexpr int S = Up<R>::kYSlots;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = warp & 3, e = warp >> 2;
+  const int f = 32 * q + lane;  // within the unit
   uint32_t parity = 0;
   for (int i = 0; walk.next(); ++i) {
     if (i % kGroups != e) continue;
-    const int my_row = __ldcg(g.tile_rows + walk.slot * kTile + lane);
-    const int f = walk.f0 + 32 * q + lane;
+    uint8_t* slot = smem + Up<R>::kYOff + (i % S) * kYSlot;
+    float* yv = reinterpret_cast<float*>(slot) + f;
+    __nv_bfloat16* half = reinterpret_cast<__nv_bfloat16*>(slot + kTile * kYRow) + f;
+    const int row = __ldcg(g.tile_rows + walk.slot * kTile + lane);
     const int count = walk.count;
-    float v[kTile];
-#pragma unroll
-    for (int m = 0; m < kTile; ++m) {
-      const int row = __shfl_sync(kFull, my_row, m);
-      if (m < count) v[m] = g.y[(long long)row * g.N + f];
-    }
+    bool ok = wait_warp(c, kYFull0 + i % S, (i / S) & 1);
     if (walk.id >= 0) {
-      if (!wait_warp(c, kUDFull0 + e, parity)) return;
+      ok = ok && wait_warp(c, kUDFull0 + e, parity);
       parity ^= 1u;
+    }
+    // all four warps leave together: they meet below
+    if (named_bar_or(1 + e, 128, !ok)) return;
+    if (walk.id >= 0) {
       umma::fence_after_sync();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float d[16];
         umma::ld_32x32b_x16(tmem + ((uint32_t)(q * 32) << 16) + e * kTile + 16 * h, d);
         umma::wait_ld();
+        if (h == 1) {
+          umma::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_at(c, kUDEmpty0 + e));
+        }
+        if (count <= 16 * h) continue;
 #pragma unroll
-        for (int m = 0; m < 16; ++m) v[16 * h + m] += d[m];
+        for (int m = 0; m < 16; ++m) {  // rows past count hold leftovers; none is stored
+          const float v = yv[(16 * h + m) * kFeat] + d[m];
+          yv[(16 * h + m) * kFeat] = v;
+          if (g.out_bf16) half[(16 * h + m) * kFeat] = __float2bfloat16_rn(v);
+        }
       }
-      umma::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_at(c, kUDEmpty0 + e));
+    } else if (g.out_bf16) {
+      for (int m = 0; m < count; ++m) half[m * kFeat] = __float2bfloat16_rn(yv[m * kFeat]);
     }
-    const bool write = walk.id >= 0 || g.out != g.y;
-#pragma unroll
-    for (int m = 0; m < kTile; ++m) {
-      const int row = __shfl_sync(kFull, my_row, m);
-      if (m >= count) continue;
-      const long long at = (long long)row * g.N + f;
-      if (write) g.out[at] = v[m];
-      if (g.out_bf16) g.out_bf16[at] = __float2bfloat16_rn(v[m]);
+    fence_proxy_async();
+    named_bar_sync(1 + e, 128);
+    if (q == 0) {
+      const long long at = (long long)row * g.N + walk.f0;
+      if (lane < count) {
+        if (walk.id >= 0 || g.out != g.y) bulk_s2g(g.out + at, smem_addr(slot) + lane * kYRow, kYRow);
+        if (g.out_bf16)
+          bulk_s2g(g.out_bf16 + at, smem_addr(slot) + kTile * kYRow + lane * kFeat * 2, kFeat * 2);
+      }
+      bulk_commit();
+      bulk_wait_read();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_at(c, kYEmpty0 + i % S));
     }
   }
 }
 
-template <int S>
+template <int R>
 __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int start[kSlab / kWindow + 1];
@@ -728,7 +811,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kUpBars; ++i) {
-      uint32_t count = 1;  // tcgen05.commit
+      uint32_t count = 1;  // tcgen05.commit, or one thread
       if (i < kBEmpty0) count = kUpProdWarps;
       if (i >= kUDEmpty0 && i < kTFull0) count = 4;
       if (i == kTFull0 || i == kTFull0 + 1) count = kUpTWarps;
@@ -747,20 +830,23 @@ __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
   const int blocks = g.N / kFeat;
   const long long total = (long long)tiles * blocks;
-  UpWalk walk{g, start, (int)(total * blockIdx.x / gridDim.x),
-              (int)(total * (blockIdx.x + 1) / gridDim.x), blocks};
+  const int first = (int)(total * blockIdx.x / gridDim.x);
+  const int last = (int)(total * (blockIdx.x + 1) / gridDim.x);
+  UpWalk walk{g, start, last - first, first / blocks, first % blocks, blocks};
   Commits done;
   if (warp == kUpMmaWarp) {
     if ((threadIdx.x & 31) == 0) {
-      done = up_mma<S>(c, g, walk, tmem);
+      done = up_mma<R>(c, g, walk, tmem);
       umma::commit(bar_at(c, kUpDrain));
     }
+  } else if (warp == kUpYWarp) {
+    up_fetch_y<R>(c, g, walk);
   } else if (warp >= kUpTWarp0) {
-    up_make_t(c, g, walk);
+    up_make_t<R>(c, g, walk);
   } else if (warp >= kUpProdWarp0) {
-    up_produce<S>(c, g, walk);
+    up_produce<R>(c, g, walk);
   } else {
-    up_epilogue(c, g, walk, tmem);
+    up_epilogue<R>(c, g, walk, tmem, smem);
   }
   umma::fence_before_sync();
   __syncthreads();
@@ -768,7 +854,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
     umma::fence_after_sync();
     if ((threadIdx.x & 31) == 0) {
       drain_commits(c, kUpDrain, 1, 1);
-      drain_commits(c, kBEmpty0, S, done.ring);
+      drain_commits(c, kBEmpty0, Up<R>::kBSlots, done.ring);
       drain_commits(c, kTEmpty0, 2, done.terms);
     }
     __syncwarp();
@@ -823,12 +909,12 @@ cudaError_t launch_down(const Args& g, int sms, cudaStream_t st) {
   return launch_after(down_kernel<BF16, S>, dim3(grid), dim3(kDownThreads), (size_t)smem, st, g);
 }
 
-template <int S>
+template <int R>
 cudaError_t launch_up(const Args& g, int sms, cudaStream_t st) {
-  cudaError_t e = allow_smem(up_kernel<S>, kUpSmem);
+  cudaError_t e = allow_smem(up_kernel<R>, Up<R>::kSmem);
   if (e != cudaSuccess) return e;
   const int grid = (int)std::min<long long>((long long)g.n * (g.N / kFeat), sms);
-  return launch_after(up_kernel<S>, dim3(grid), dim3(kUpThreads), (size_t)kUpSmem, st, g);
+  return launch_after(up_kernel<R>, dim3(grid), dim3(kUpThreads), (size_t)Up<R>::kSmem, st, g);
 }
 
 }  // namespace
@@ -854,7 +940,7 @@ int nvfp4_mm_adapters(const void* x, int32_t x_dtype, int32_t n, int32_t N, int3
   if (n == 0) return DA_OK;
   if (!x || !a || !b || !ids || !y || !out) return DA_ERR_INVALID_ARG;
   if (!aligned_to(x, 16) || !aligned_to(a, 16) || !aligned_to(b, 16) || !aligned_to(y, 16) ||
-      !aligned_to(out, 16) || !aligned_to(out_bf16, 8) || !aligned_to(ids, 4) ||
+      !aligned_to(out, 16) || !aligned_to(out_bf16, 16) || !aligned_to(ids, 4) ||
       !aligned_to(ranks, 4) || !aligned_to(scales, 4))
     return DA_ERR_INVALID_ARG;
   const uintptr_t y0 = reinterpret_cast<uintptr_t>(y), o0 = reinterpret_cast<uintptr_t>(out);
@@ -889,11 +975,11 @@ int nvfp4_mm_adapters(const void* x, int32_t x_dtype, int32_t n, int32_t N, int3
   g.copy = out != y || out_bf16;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf16 = x_dtype == NVFP4_X_BF16;
-  // four stages of up to 48 KB, or two of up to 80; B rows of up to 64 ranks take
-  // one region of the ring, longer ones two
+  // four stages of up to 48 KB, or two of up to 80; ranks of up to 64 take one
+  // region of a slot, higher ones two
   auto* down = down_stages(max_rank) == 4 ? (bf16 ? launch_down<true, 4> : launch_down<false, 4>)
                                           : (bf16 ? launch_down<true, 2> : launch_down<false, 2>);
-  auto* up = max_rank <= 64 ? launch_up<kBSlots> : launch_up<kBSlots / 2>;
+  auto* up = max_rank <= 64 ? launch_up<1> : launch_up<2>;
   for (int r0 = 0; r0 < n; r0 += kSlab) {
     const size_t row = (size_t)r0;
     g.n = std::min(kSlab, n - r0);

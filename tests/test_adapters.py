@@ -259,7 +259,7 @@ def test_argument_rules(api):
         assert call(**{name: (1 << 26) + 8}) == bad, name
     for name in ("ids", "ranks", "scales"):
         assert call(**{name: fake + 2}) == bad, name
-    assert call(ob=fake + 4) == bad
+    assert call(ob=fake + 8) == bad
     assert call(out=(1 << 24) + 512) == bad  # overlaps y
     assert call(ws=None) == api.ERR_WORKSPACE
     assert call(ws=fake + 16) == api.ERR_WORKSPACE
