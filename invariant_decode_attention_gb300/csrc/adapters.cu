@@ -16,9 +16,11 @@
 //         N = 32.  The chunk sums of t are added in order, scaled, and split into
 //         three bf16 terms that hold their 24 bits; their products with B are
 //         exact, so out keeps fp32 accuracy.  A unit is a tile and 128 features.
-//         y arrives and out leaves by bulk copies of a member's 512 bytes (loads
-//         and stores by the epilogue's threads, 4 bytes a lane, took 4900
-//         instructions a unit and 267 us for 8192 rows of 8192).
+//         y arrives through the ring as well; the epilogue adds the products to
+//         it in shared memory and writes a row's 512 bytes with one instruction
+//         (loads and stores of 4 bytes a lane took 4900 instructions a unit and
+//         267 us for 8192 rows of 8192; bulk copies of 512 bytes a row, 96 a
+//         unit, 200 us).
 // The orders of all sums depend on K and the rank alone.  A column of an MMA does
 // not depend on the other columns, so neither do a row's bits.
 //
@@ -83,22 +85,6 @@ __device__ __forceinline__ void fence_proxy_async() {
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
-}
-
-// Bulk store of `bytes` (a multiple of 16, both addresses 16-byte aligned).
-__device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src),
-               "r"(bytes)
-               : "memory");
-}
-
-__device__ __forceinline__ void bulk_commit() {
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-
-// Until this thread's bulk stores have read their shared memory.
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -503,25 +489,30 @@ __global__ void __launch_bounds__(kDownThreads, 1) down_kernel(const Args g) {
 
 constexpr int kGroups = 4;                  // epilogue groups of four warps, one accumulator each
 constexpr int kUpProdWarp0 = 16, kUpProdWarps = 4, kUpTWarp0 = 20, kUpTWarps = 4, kUpMmaWarp = 24,
-              kUpYWarp = 25;
-constexpr int kUpThreads = (kUpYWarp + 1) * 32;
+              kUpYWarp0 = 25, kUpYWarps = 4;
+constexpr int kUpThreads = (kUpYWarp0 + kUpYWarps) * 32;
 constexpr int kBRegion = kFeat * 128;       // 16 KB: 128 features x 64 ranks
 constexpr int kTRegion = kTile * 128;       // 4 KB: 32 members x 64 ranks
 constexpr int kYRow = kFeat * 4;            // 512 bytes of a row of y
-constexpr int kYSlot = kTile * kYRow + kTile * kFeat * 2;  // y, then out as bf16: 24 KB
+constexpr int kYSlot = kTile * kYRow;       // 16 KB
 
 // Shared memory by R, the 64-rank regions of an adapter of max_rank: four or two
-// slots of B, two of t's terms, five or four of y.
+// slots of B, two of t's terms, eight or four of y.
 template <int R>
 struct Up {
-  static constexpr int kBSlots = 4 / R, kYSlots = 6 - R;
+  static constexpr int kBSlots = 4 / R, kYSlots = 8 / R;
   static constexpr int kTOff = kBSlots * R * kBRegion;
   static constexpr int kTSlot = 3 * R * kTRegion;
   static constexpr int kYOff = kTOff + 2 * kTSlot;
   static constexpr int kSmem = kYOff + kYSlots * kYSlot;
+  // A parity tells a phase from the one before it only.  A slot of y must belong to
+  // one group, which waits for its phases one by one: a group that came to another
+  // group's slot could ask for a phase before the previous one has completed, and
+  // would be let through.
+  static_assert(kYSlots % kGroups == 0, "a slot of y belongs to one group");
   static_assert(kYOff % 1024 == 0 && kSmem <= 220 * 1024 && 2 * kSmem > 233472, "one CTA per SM");
 };
-constexpr int kMaxBSlots = 4, kMaxYSlots = 5;
+constexpr int kMaxBSlots = 4, kMaxYSlots = 8;
 enum { kBFull0 = 0, kBEmpty0 = kBFull0 + kMaxBSlots, kYFull0 = kBEmpty0 + kMaxBSlots,
        kYEmpty0 = kYFull0 + kMaxYSlots, kUDFull0 = kYEmpty0 + kMaxYSlots,
        kUDEmpty0 = kUDFull0 + kGroups, kTFull0 = kUDEmpty0 + kGroups, kTEmpty0 = kTFull0 + 2,
@@ -702,91 +693,97 @@ __device__ Commits up_mma(const Ctx& c, const Args& g, UpWalk walk, uint32_t tme
   return done;
 }
 
-// y, a member's 512 bytes by one bulk copy each: a lane per member.
+// y: warp w brings members w, w + 4, ..., 512 bytes of one each time.
 template <int R>
 __device__ void up_fetch_y(const Ctx& c, const Args& g, UpWalk walk) {
-  constexpr int S = Up<R>::kYSlots;
-  const int lane = threadIdx.x & 31;
-  const uint64_t policy = policy_evict_first();  // read once
-  int i = 0;
-  for (; walk.next(); ++i) {
-    const int row = __ldcg(g.tile_rows + walk.slot * kTile + lane);
-    if (i >= S && !wait_warp(c, kYEmpty0 + i % S, (i / S - 1) & 1)) break;
-    if (lane == 0) mbar_arrive_expect_tx(bar_at(c, kYFull0 + i % S), walk.count * kYRow);
+  constexpr int S = Up<R>::kYSlots, kLag = S / 2;
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kUpYWarp0;
+  int i = 0, my_row = -1;
+  bool ok = true;
+  auto signal = [&](int s) {
     __syncwarp();
-    if (lane < walk.count)
-      bulk_g2s(c.sbase + Up<R>::kYOff + (i % S) * kYSlot + lane * kYRow,
-               g.y + (long long)row * g.N + walk.f0, kYRow, bar_at(c, kYFull0 + i % S), policy);
+    if (lane == 0) mbar_arrive(bar_at(c, kYFull0 + s % S));
+  };
+  for (; ok && walk.next(); ++i) {
+    if (walk.fresh) my_row = __ldcg(g.tile_rows + walk.slot * kTile + lane);
+    if (i >= S && !wait_warp(c, kYEmpty0 + i % S, (i / S - 1) & 1)) {
+      ok = false;
+      break;
+    }
+    const uint32_t slot = c.sbase + Up<R>::kYOff + (i % S) * kYSlot + lane * 16;
+    const float* y = g.y + walk.f0 + 4 * lane;
+#pragma unroll
+    for (int j = 0; j < kTile / kUpYWarps; ++j) {
+      const int m = w + j * kUpYWarps;
+      const int row = __shfl_sync(kFull, my_row, m);
+      if (m < walk.count) cp_async16(slot + m * kYRow, y + (long long)row * g.N);
+    }
+    cp_async_commit();
+    if (i >= kLag) {
+      cp_async_wait<kLag>();
+      signal(i - kLag);
+    }
   }
-  // copies still in flight land before the shared memory goes away (normally the
-  // epilogue has waited for every one already)
-  for (int s = 0; s < S && s < i; ++s) {
-    if (lane == 0 && !mbar_wait(bar_at(c, kYFull0 + s), ((i - 1 - s) / S) & 1))
-      set_error(c.hdr, DA_DEVERR_TIMEOUT);
-  }
-  __syncwarp();
+  cp_async_wait<0>();
+  if (ok)
+    for (int s = max(0, i - kLag); s < i; ++s) signal(s);
 }
 
-// Group e takes units e, e + 4, ... of the CTA; warp q of it features 32 q ..
-// + 31, one a lane.  The sum replaces y in shared memory and leaves by bulk
-// stores, a lane of one warp per member.
+// Group e takes units e, e + 4, ... of the CTA.  Warp q of it first adds features
+// 32 q .. + 31, one a lane, to y in shared memory, then writes members q, q + 4,
+// ..., 16 bytes a lane.
 template <int R>
 __device__ void up_epilogue(const Ctx& c, const Args& g, UpWalk walk, uint32_t tmem, uint8_t* smem) {
   constexpr int S = Up<R>::kYSlots;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = warp & 3, e = warp >> 2;
-  const int f = 32 * q + lane;  // within the unit
   uint32_t parity = 0;
+  int my_row = -1;
   for (int i = 0; walk.next(); ++i) {
+    if (walk.fresh) my_row = __ldcg(g.tile_rows + walk.slot * kTile + lane);
     if (i % kGroups != e) continue;
     uint8_t* slot = smem + Up<R>::kYOff + (i % S) * kYSlot;
-    float* yv = reinterpret_cast<float*>(slot) + f;
-    __nv_bfloat16* half = reinterpret_cast<__nv_bfloat16*>(slot + kTile * kYRow) + f;
-    const int row = __ldcg(g.tile_rows + walk.slot * kTile + lane);
     const int count = walk.count;
     bool ok = wait_warp(c, kYFull0 + i % S, (i / S) & 1);
     if (walk.id >= 0) {
       ok = ok && wait_warp(c, kUDFull0 + e, parity);
       parity ^= 1u;
+      if (ok) {
+        float* yv = reinterpret_cast<float*>(slot) + 32 * q + lane;
+        umma::fence_after_sync();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float d[16];
+          umma::ld_32x32b_x16(tmem + ((uint32_t)(q * 32) << 16) + e * kTile + 16 * h, d);
+          umma::wait_ld();
+          if (h == 1) {
+            umma::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_at(c, kUDEmpty0 + e));
+          }
+          if (count <= 16 * h) continue;
+#pragma unroll
+          for (int m = 0; m < 16; ++m)  // members past count hold leftovers; none is stored
+            yv[(16 * h + m) * kFeat] += d[m];
+        }
+      }
     }
-    // all four warps leave together: they meet below
+    // the group's four warps meet, or leave together
     if (named_bar_or(1 + e, 128, !ok)) return;
-    if (walk.id >= 0) {
-      umma::fence_after_sync();
+    const bool write = walk.id >= 0 || g.out != g.y;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float d[16];
-        umma::ld_32x32b_x16(tmem + ((uint32_t)(q * 32) << 16) + e * kTile + 16 * h, d);
-        umma::wait_ld();
-        if (h == 1) {
-          umma::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_at(c, kUDEmpty0 + e));
-        }
-        if (count <= 16 * h) continue;
-#pragma unroll
-        for (int m = 0; m < 16; ++m) {  // rows past count hold leftovers; none is stored
-          const float v = yv[(16 * h + m) * kFeat] + d[m];
-          yv[(16 * h + m) * kFeat] = v;
-          if (g.out_bf16) half[(16 * h + m) * kFeat] = __float2bfloat16_rn(v);
-        }
-      }
-    } else if (g.out_bf16) {
-      for (int m = 0; m < count; ++m) half[m * kFeat] = __float2bfloat16_rn(yv[m * kFeat]);
+    for (int j = 0; j < kTile / 4; ++j) {
+      const int m = q + 4 * j;
+      const int row = __shfl_sync(kFull, my_row, m);
+      if (m >= count) continue;
+      const float4 v = *reinterpret_cast<const float4*>(slot + m * kYRow + 16 * lane);
+      const long long at = (long long)row * g.N + walk.f0 + 4 * lane;
+      if (write) *reinterpret_cast<float4*>(g.out + at) = v;
+      if (g.out_bf16)
+        *reinterpret_cast<uint2*>(g.out_bf16 + at) =
+            make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
     }
-    fence_proxy_async();
-    named_bar_sync(1 + e, 128);
-    if (q == 0) {
-      const long long at = (long long)row * g.N + walk.f0;
-      if (lane < count) {
-        if (walk.id >= 0 || g.out != g.y) bulk_s2g(g.out + at, smem_addr(slot) + lane * kYRow, kYRow);
-        if (g.out_bf16)
-          bulk_s2g(g.out_bf16 + at, smem_addr(slot) + kTile * kYRow + lane * kFeat * 2, kFeat * 2);
-      }
-      bulk_commit();
-      bulk_wait_read();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_at(c, kYEmpty0 + i % S));
-    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_at(c, kYEmpty0 + i % S));
   }
 }
 
@@ -813,6 +810,8 @@ __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
     for (int i = 0; i < kUpBars; ++i) {
       uint32_t count = 1;  // tcgen05.commit, or one thread
       if (i < kBEmpty0) count = kUpProdWarps;
+      if (i >= kYFull0 && i < kYEmpty0) count = kUpYWarps;
+      if (i >= kYEmpty0 && i < kUDFull0) count = 4;
       if (i >= kUDEmpty0 && i < kTFull0) count = 4;
       if (i == kTFull0 || i == kTFull0 + 1) count = kUpTWarps;
       mbar_init(c.bars + 8 * i, count);
@@ -839,7 +838,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
       done = up_mma<R>(c, g, walk, tmem);
       umma::commit(bar_at(c, kUpDrain));
     }
-  } else if (warp == kUpYWarp) {
+  } else if (warp >= kUpYWarp0) {
     up_fetch_y<R>(c, g, walk);
   } else if (warp >= kUpTWarp0) {
     up_make_t<R>(c, g, walk);
