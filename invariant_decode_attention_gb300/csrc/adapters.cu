@@ -376,11 +376,18 @@ __device__ Commits down_mma(const Ctx& c, const Args& g, DownWalk walk, uint32_t
       if (!wait_bar(c, kFull0 + step % S, (step / S) & 1)) return done;
       umma::fence_after_sync();
       const int n_mma = min(kStepK, d.k_len - k) / 16;
-      const uint32_t stage = (step % S) * stage_bytes;
-      for (int j = 0; j < n_mma; ++j) {
-        const uint32_t ra = stage + (j >> 2) * a_region + (j & 3) * 32;
-        const uint32_t rx = stage + 4 * a_region + (j >> 2) * kXRegion + (j & 3) * 32;
-        umma::mma_bf16(tmem + tb * kTile, base + (ra >> 4), base + (rx >> 4), kIdesc, k || j);
+      const uint64_t ad = base + (uint64_t)(((step % S) * stage_bytes) >> 4);
+      const uint64_t xd = ad + (uint64_t)((4 * a_region) >> 4);
+      const uint32_t acc = tmem + tb * kTile;
+#pragma unroll
+      for (int rg = 0; rg < kStepK / kRegionK; ++rg) {
+        if (4 * rg >= n_mma) break;
+        const uint64_t ar = ad + (uint64_t)((rg * a_region) >> 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          umma::mma_bf16(acc, ar + (uint64_t)((j * 32) >> 4),
+                         xd + (uint64_t)((rg * kXRegion + j * 32) >> 4), kIdesc,
+                         rg || j ? 1u : (uint32_t)(k != 0));
       }
       umma::commit(bar_at(c, kEmpty0 + step % S));
     }
@@ -488,9 +495,14 @@ __global__ void __launch_bounds__(kDownThreads, 1) down_kernel(const Args g) {
 // ---------------------------------------------------------------- up
 
 constexpr int kGroups = 4;                  // epilogue groups of four warps, one accumulator each
-constexpr int kUpProdWarp0 = 16, kUpProdWarps = 4, kUpTWarp0 = 20, kUpTWarps = 4, kUpMmaWarp = 24,
-              kUpYWarp0 = 25, kUpYWarps = 4;
-constexpr int kUpThreads = (kUpYWarp0 + kUpYWarps) * 32;
+// Warp w issues on scheduler w % 4.  The 16 epilogue warps take all four (a warp
+// reads the quarter w % 4 of tensor memory); of the others the MMA issuer has
+// scheduler 0, the twelve that bring operands share 1, 2 and 3 (warps 20, 24 and 28
+// are idle).
+constexpr int kUpMmaWarp = 16, kUpWarps = 32, kUpThreads = kUpWarps * 32;
+constexpr int kUpProdWarps = 4, kUpTWarps = 4, kUpYWarps = 4;
+// 0 .. 11 for the warps that bring operands: four each for B, t and y
+__device__ __forceinline__ int up_helper(int warp) { return (warp - 17) / 4 * 3 + (warp - 17) % 4; }
 constexpr int kBRegion = kFeat * 128;       // 16 KB: 128 features x 64 ranks
 constexpr int kTRegion = kTile * 128;       // 4 KB: 32 members x 64 ranks
 constexpr int kYRow = kFeat * 4;            // 512 bytes of a row of y
@@ -556,7 +568,7 @@ struct UpWalk {
 template <int R>
 __device__ void up_produce(const Ctx& c, const Args& g, UpWalk walk) {
   constexpr int S = Up<R>::kBSlots, kLag = S / 2;
-  const int lane = threadIdx.x & 31, tid = threadIdx.x - kUpProdWarp0 * 32;
+  const int lane = threadIdx.x & 31, tid = up_helper(threadIdx.x >> 5) * 32 + lane;
   int k = 0, row0 = 0, rows = 1, ch = 0, bytes = 0;
   bool ok = true;
   auto signal = [&](int s) {
@@ -598,7 +610,7 @@ __device__ void up_produce(const Ctx& c, const Args& g, UpWalk walk) {
 // members w, w + 4, ...; a lane two ranks of each 64.
 template <int R>
 __device__ void up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
-  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kUpTWarp0;
+  const int lane = threadIdx.x & 31, w = up_helper(threadIdx.x >> 5) - kUpProdWarps;
   const long long part = (long long)g.n * g.max_rank;
   int k = 0;
   while (walk.next()) {
@@ -673,14 +685,22 @@ __device__ Commits up_mma(const Ctx& c, const Args& g, UpWalk walk, uint32_t tme
       return done;
     }
     umma::fence_after_sync();
-    const uint32_t bs = (k % S) * (R * kBRegion), ts = Up<R>::kTOff + ((tiles - 1) & 1) * Up<R>::kTSlot;
+    // each MMA adds a constant to the operands' descriptors (K = 16 is 32 bytes of
+    // a 128-byte swizzle row; the address field holds bytes / 16 and does not carry
+    // out); a loop over them took 180 cycles an MMA
+    const uint64_t bd = base + (uint64_t)(((k % S) * (R * kBRegion)) >> 4);
+    const uint64_t td = base + (uint64_t)((Up<R>::kTOff + ((tiles - 1) & 1) * Up<R>::kTSlot) >> 4);
+    const uint32_t acc = tmem + e * kTile;
     const int n_k = (walk.rank + 15) >> 4;
+    umma::mma_bf16(acc, bd, td + (uint64_t)((2 * R * kTRegion) >> 4), kIdesc, 0u);
+#pragma unroll
     for (int term = 2; term >= 0; --term) {  // small terms first
-      for (int kb = 0; kb < n_k; ++kb) {
-        const uint32_t rb = bs + (kb >> 2) * kBRegion + (kb & 3) * 32;
-        const uint32_t rt = ts + (term * R + (kb >> 2)) * kTRegion + (kb & 3) * 32;
-        umma::mma_bf16(tmem + e * kTile, base + (rb >> 4), base + (rt >> 4), kIdesc,
-                       term != 2 || kb != 0);
+#pragma unroll
+      for (int kb = 0; kb < 4 * R; ++kb) {
+        if ((term == 2 && kb == 0) || kb >= n_k) continue;
+        umma::mma_bf16(acc, bd + (uint64_t)(((kb >> 2) * kBRegion + (kb & 3) * 32) >> 4),
+                       td + (uint64_t)(((term * R + (kb >> 2)) * kTRegion + (kb & 3) * 32) >> 4),
+                       kIdesc, 1u);
       }
     }
     umma::commit(bar_at(c, kBEmpty0 + k % S));
@@ -697,7 +717,7 @@ __device__ Commits up_mma(const Ctx& c, const Args& g, UpWalk walk, uint32_t tme
 template <int R>
 __device__ void up_fetch_y(const Ctx& c, const Args& g, UpWalk walk) {
   constexpr int S = Up<R>::kYSlots, kLag = S / 2;
-  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kUpYWarp0;
+  const int lane = threadIdx.x & 31, w = up_helper(threadIdx.x >> 5) - kUpProdWarps - kUpTWarps;
   int i = 0, my_row = -1;
   bool ok = true;
   auto signal = [&](int s) {
@@ -838,14 +858,16 @@ __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
       done = up_mma<R>(c, g, walk, tmem);
       umma::commit(bar_at(c, kUpDrain));
     }
-  } else if (warp >= kUpYWarp0) {
-    up_fetch_y<R>(c, g, walk);
-  } else if (warp >= kUpTWarp0) {
-    up_make_t<R>(c, g, walk);
-  } else if (warp >= kUpProdWarp0) {
-    up_produce<R>(c, g, walk);
-  } else {
+  } else if (warp < kUpMmaWarp) {
     up_epilogue<R>(c, g, walk, tmem, smem);
+  } else if (warp % 4) {
+    const int h = up_helper(warp);
+    if (h < kUpProdWarps)
+      up_produce<R>(c, g, walk);
+    else if (h < kUpProdWarps + kUpTWarps)
+      up_make_t<R>(c, g, walk);
+    else
+      up_fetch_y<R>(c, g, walk);
   }
   umma::fence_before_sync();
   __syncthreads();
