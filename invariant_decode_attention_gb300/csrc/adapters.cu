@@ -224,33 +224,43 @@ __device__ __forceinline__ long long slot_of(const int* start, int windows, int 
   return (long long)lo * kWindow + (t - start[lo]);
 }
 
-// The arrive of a tcgen05.commit lands some time after the work it tracks; the
-// last one on each of `slots` barriers from `first` on, which `commits` commits
-// went to in turn, must have landed before the CTA's shared memory is handed on.
-__device__ __forceinline__ void drain_commits(const Ctx& c, int first, int slots, int commits) {
-  for (int s = 0; s < slots && s < commits; ++s) {
-    const int rounds = (commits - 1 - s) / slots;  // of barrier s, before its last
-    if (!mbar_wait(bar_at(c, first + s), rounds & 1)) set_error(c.hdr, DA_DEVERR_TIMEOUT);
+// A set of barriers of which each has completed some number of phases: one bit
+// each for "any" and for the number's parity.
+struct Phases {
+  uint32_t any = 0, odd = 0;
+  __device__ __forceinline__ void add(int i) {
+    any |= 1u << i;
+    odd ^= 1u << i;
   }
-}
-
-// What the MMA thread committed to barriers that nobody waits for at the end.
-struct Commits {
-  int ring = 0, terms = 0;
+  __device__ __forceinline__ bool has(int i) const { return (any >> i) & 1u; }
+  __device__ __forceinline__ uint32_t next(int i) const { return (odd >> i) & 1u; }         // parity
+  __device__ __forceinline__ uint32_t last(int i) const { return ((odd >> i) & 1u) ^ 1u; }  // parity
 };
+
+// The arrive of a tcgen05.commit lands some time after the work it tracks; the
+// last one on each barrier first, first + 1, ... must have landed before the CTA's
+// shared memory is handed on.
+__device__ __forceinline__ void drain_commits(const Ctx& c, int first, const Phases& p) {
+  for (int i = 0; (p.any >> i) != 0; ++i)
+    if (p.has(i) && !mbar_wait(bar_at(c, first + i), p.last(i))) set_error(c.hdr, DA_DEVERR_TIMEOUT);
+}
 
 // ---------------------------------------------------------------- down
 
 constexpr int kStepK = 256, kRegionK = 64;         // K of a stage, and of a 128-byte swizzle row
 constexpr int kXRegion = kTile * kRegionK * 2;     // 4 KB
 constexpr int kXStage = (kStepK / kRegionK) * kXRegion;
-constexpr int kDownEpWarps = 4, kDownProdWarp0 = 4, kDownProdWarps = 8, kDownMmaWarp = 12;
-constexpr int kDownThreads = (kDownMmaWarp + 1) * 32;
+// Two threads issue the MMAs (one took 90 cycles an MMA and set the pace): the
+// even and the odd stages, each into an accumulator of its own that the epilogue
+// adds.  Which of the two a step goes to depends on what came before, but the sum
+// of two numbers does not.
+constexpr int kDownEpWarps = 4, kDownProdWarp0 = 4, kDownProdWarps = 8, kDownMmaWarp0 = 12;
+constexpr int kDownThreads = (kDownMmaWarp0 + 2) * 32;
 constexpr int kDownStages = 4;
 // mbarriers: stage full and empty, accumulator full and empty, drain
 enum { kFull0 = 0, kEmpty0 = kFull0 + kDownStages, kDFull0 = kEmpty0 + kDownStages,
-       kDEmpty0 = kDFull0 + 2, kDownDrain = kDEmpty0 + 2, kDownBars };
-constexpr uint32_t kDownCols = 64;                 // two accumulators
+       kDEmpty0 = kDFull0 + 2, kDownDrain = kDEmpty0 + 2, kDownBars = kDownDrain + 2 };
+constexpr uint32_t kDownCols = 4 * kTile;          // two units' two accumulators
 
 __host__ __device__ constexpr int down_stage_bytes(int max_rank) {
   return max_rank * kStepK * 2 + kXStage;
@@ -290,10 +300,16 @@ struct DownWalk {
 // copies 16 bytes of K, a warp 512 bytes of one row.
 template <bool BF16, int S>
 __device__ void down_produce(const Ctx& c, const Args& g, DownWalk walk) {
-  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kDownProdWarp0;
   constexpr int kLag = S / 2;  // stages that are landing while others are multiplied
+  constexpr int kMine = kTile / kDownProdWarps;
+  constexpr int kElem = BF16 ? 2 : 4;
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kDownProdWarp0;
   const int stage_bytes = down_stage_bytes(g.max_rank), a_region = g.max_rank * 128;
-  const uint32_t chunk16 = lane & 7, region = lane >> 3;  // of this lane's 16 bytes
+  // where this lane's 16 bytes go within a stage: rows w + 8 i differ by 1024 bytes
+  // and share the swizzle (w & 7)
+  const uint32_t swz = ((lane & 7) ^ (w & 7)) << 4;
+  const uint32_t a_at = (lane >> 3) * a_region + w * 128 + swz;
+  const uint32_t x_at = 4 * a_region + (lane >> 3) * kXRegion + w * 128 + swz;
   int step = 0;
   bool ok = true;
   auto signal = [&](int s) {  // stage s % S has landed
@@ -304,20 +320,27 @@ __device__ void down_produce(const Ctx& c, const Args& g, DownWalk walk) {
   DownUnit d;
   while (ok && walk.next(&d)) {
     const int my_row = __ldcg(g.tile_rows + d.slot * kTile + lane);
-    const int rows_a = (d.rank + 15) & ~15;
-    const __nv_bfloat16* a = g.a + (long long)d.id * g.max_rank * g.K + d.k0 + 8 * lane;
+    const char* xp[kMine];  // this lane's 8 elements of its rows' x, or null
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int row = __shfl_sync(kFull, my_row, w + i * kDownProdWarps);
+      xp[i] = row < 0 ? nullptr
+                      : static_cast<const char*>(g.x) +
+                            ((long long)row * g.K + d.k0 + 8 * lane) * kElem;
+    }
+    const int rows_a = (((d.rank + 15) & ~15) - w + kDownProdWarps - 1) / kDownProdWarps;
+    const char* ap = reinterpret_cast<const char*>(
+        g.a + ((long long)d.id * g.max_rank + w) * g.K + d.k0 + 8 * lane);
+    const long long a_step = (long long)kDownProdWarps * g.K * 2;
     for (int k = 0; k < d.k_len; k += kStepK, ++step) {
       const bool live = k + 8 * lane < d.k_len;  // K is a multiple of 64: whole regions
-      uint4 v[kTile / kDownProdWarps];
+      uint4 v[kMine];
       if constexpr (!BF16) {  // fp32 rows are rounded on the way; their loads come first
 #pragma unroll
-        for (int i = 0; i < kTile / kDownProdWarps; ++i) {
-          const int m = w + i * kDownProdWarps;
-          const int row = __shfl_sync(kFull, my_row, m);
-          if (m < d.count && live) {
-            const float4* p = reinterpret_cast<const float4*>(
-                static_cast<const float*>(g.x) + (long long)row * g.K + d.k0 + k + 8 * lane);
-            const float4 e = __ldg(p), f = __ldg(p + 1);
+        for (int i = 0; i < kMine; ++i) {
+          if (xp[i] && live) {
+            const float4* q = reinterpret_cast<const float4*>(xp[i] + k * kElem);
+            const float4 e = __ldg(q), f = __ldg(q + 1);
             v[i] = make_uint4(pack_bf16(e.x, e.y), pack_bf16(e.z, e.w), pack_bf16(f.x, f.y),
                               pack_bf16(f.z, f.w));
           }
@@ -329,24 +352,19 @@ __device__ void down_produce(const Ctx& c, const Args& g, DownWalk walk) {
       }
       const uint32_t stage = c.sbase + (step % S) * stage_bytes;
       if (live) {
-        for (int r = w; r < rows_a; r += kDownProdWarps)
-          cp_async16(stage + region * a_region + r * 128 + ((chunk16 ^ (r & 7)) << 4),
-                     a + (long long)r * g.K + k);
-      }
-      const uint32_t xs = stage + 4 * a_region;
+        const char* p = ap + k * 2;
+        uint32_t at = stage + a_at;
+        for (int i = 0; i < rows_a; ++i, p += a_step, at += 1024) cp_async16(at, p);
 #pragma unroll
-      for (int i = 0; i < kTile / kDownProdWarps; ++i) {
-        const int m = w + i * kDownProdWarps;
-        const int row = __shfl_sync(kFull, my_row, m);
-        if (m >= d.count || !live) continue;
-        const uint32_t at = xs + region * kXRegion + m * 128 + ((chunk16 ^ (m & 7)) << 4);
-        if constexpr (BF16)
-          cp_async16(at, static_cast<const __nv_bfloat16*>(g.x) + (long long)row * g.K + d.k0 + k +
-                             8 * lane);
-        else
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[i].x), "r"(v[i].y),
-                       "r"(v[i].z), "r"(v[i].w)
-                       : "memory");
+        for (int i = 0; i < kMine; ++i) {
+          if (!xp[i]) continue;
+          if constexpr (BF16)
+            cp_async16(stage + x_at + i * 1024, xp[i] + k * kElem);
+          else
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + x_at + i * 1024),
+                         "r"(v[i].x), "r"(v[i].y), "r"(v[i].z), "r"(v[i].w)
+                         : "memory");
+        }
       }
       cp_async_commit();
       if (step >= kLag) {
@@ -360,25 +378,28 @@ __device__ void down_produce(const Ctx& c, const Args& g, DownWalk walk) {
     for (int s = max(0, step - kLag); s < step; ++s) signal(s);
 }
 
+// Issuer `me` takes the steps of its parity; returns what it committed to the
+// stages' empty barriers.
 template <int S>
-__device__ Commits down_mma(const Ctx& c, const Args& g, DownWalk walk, uint32_t tmem) {
+__device__ Phases down_mma(const Ctx& c, const Args& g, DownWalk walk, uint32_t tmem, int me) {
   const int stage_bytes = down_stage_bytes(g.max_rank), a_region = g.max_rank * 128;
   const uint64_t base = umma::smem_desc(c.sbase, 16, 1024, umma::kSwizzle128B);
-  Commits done;
-  int& step = done.ring;
-  int k_unit = 0;
+  Phases done;
+  int step = 0, k_unit = 0;
   DownUnit d;
   for (; walk.next(&d); ++k_unit) {
     const int tb = k_unit & 1;
     if (k_unit >= 2 && !wait_bar(c, kDEmpty0 + tb, ((k_unit >> 1) - 1) & 1)) return done;
     umma::fence_after_sync();
+    const uint32_t acc = tmem + (2 * tb + me) * kTile;
+    bool first = true;
     for (int k = 0; k < d.k_len; k += kStepK, ++step) {
+      if ((step & 1) != me) continue;
       if (!wait_bar(c, kFull0 + step % S, (step / S) & 1)) return done;
       umma::fence_after_sync();
       const int n_mma = min(kStepK, d.k_len - k) / 16;
       const uint64_t ad = base + (uint64_t)(((step % S) * stage_bytes) >> 4);
       const uint64_t xd = ad + (uint64_t)((4 * a_region) >> 4);
-      const uint32_t acc = tmem + tb * kTile;
 #pragma unroll
       for (int rg = 0; rg < kStepK / kRegionK; ++rg) {
         if (4 * rg >= n_mma) break;
@@ -387,11 +408,13 @@ __device__ Commits down_mma(const Ctx& c, const Args& g, DownWalk walk, uint32_t
         for (int j = 0; j < 4; ++j)
           umma::mma_bf16(acc, ar + (uint64_t)((j * 32) >> 4),
                          xd + (uint64_t)((rg * kXRegion + j * 32) >> 4), kIdesc,
-                         rg || j ? 1u : (uint32_t)(k != 0));
+                         rg || j ? 1u : (uint32_t)!first);
       }
       umma::commit(bar_at(c, kEmpty0 + step % S));
+      done.add(step % S);
+      first = false;
     }
-    umma::commit(bar_at(c, kDFull0 + tb));
+    umma::commit(bar_at(c, kDFull0 + tb));  // also when it had no step of the unit
   }
   return done;
 }
@@ -399,25 +422,35 @@ __device__ Commits down_mma(const Ctx& c, const Args& g, DownWalk walk, uint32_t
 // Warp q: ranks 32 q .. 32 q + 31, one a lane.
 __device__ void down_epilogue(const Ctx& c, const Args& g, DownWalk walk, uint32_t tmem) {
   const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
-  int k_unit = 0;
+  int k_unit = 0, step = 0;
   DownUnit d;
   for (; walk.next(&d); ++k_unit) {
     const int my_row = __ldcg(g.tile_rows + d.slot * kTile + lane), tb = k_unit & 1;
+    const int steps = (d.k_len + kStepK - 1) / kStepK;
     if (!wait_warp(c, kDFull0 + tb, (k_unit >> 1) & 1)) return;
     umma::fence_after_sync();
-    float v[kTile];
-    umma::ld_32x32b_x32(tmem + ((uint32_t)(q * 32) << 16) + tb * kTile, v);
-    umma::wait_ld();
-    umma::fence_before_sync();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar_at(c, kDEmpty0 + tb));
     const int r = 32 * q + lane;
     float* t = g.t + (long long)d.chunk * g.n * g.max_rank + r;
+    const uint32_t from = tmem + ((uint32_t)(q * 32) << 16) + 2 * tb * kTile;
 #pragma unroll
-    for (int i = 0; i < kTile; ++i) {
-      const int row = __shfl_sync(kFull, my_row, i);
-      if (i < d.count && r < d.rank) t[(long long)row * g.max_rank] = v[i];
+    for (int h = 0; h < 2; ++h) {
+      float u[16], v[16];
+      umma::ld_32x32b_x16(from + (step & 1) * kTile + 16 * h, u);  // of the unit's first step
+      if (steps > 1) umma::ld_32x32b_x16(from + (~step & 1) * kTile + 16 * h, v);
+      umma::wait_ld();
+      if (h == 1) {
+        umma::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_at(c, kDEmpty0 + tb));
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int row = __shfl_sync(kFull, my_row, 16 * h + i);
+        if (row >= 0 && r < d.rank)
+          t[(long long)row * g.max_rank] = steps > 1 ? u[i] + v[i] : u[i];
+      }
     }
+    step += steps;
   }
 }
 
@@ -453,13 +486,14 @@ __global__ void __launch_bounds__(kDownThreads, 1) down_kernel(const Args g) {
     for (int i = 0; i < kDownBars; ++i) {
       uint32_t count = 1;  // tcgen05.commit
       if (i < kEmpty0) count = kDownProdWarps;
-      if (i == kDEmpty0 || i == kDEmpty0 + 1) count = kDownEpWarps;
+      if (i >= kDFull0 && i < kDEmpty0) count = 2;  // both issuers
+      if (i >= kDEmpty0 && i < kDownDrain) count = kDownEpWarps;
       mbar_init(c.bars + 8 * i, count);
     }
     abort_word = 0;
     fence_mbar_init();
   }
-  if (warp == kDownMmaWarp) {
+  if (warp == kDownMmaWarp0) {
     umma::tmem_alloc(smem_addr(&tmem_slot), kDownCols);
     umma::tmem_relinquish();
   }
@@ -468,11 +502,12 @@ __global__ void __launch_bounds__(kDownThreads, 1) down_kernel(const Args g) {
   umma::fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
   DownWalk walk{g, start, (int)blockIdx.x, tiles * g.n_chunks};
-  Commits done;
-  if (warp == kDownMmaWarp) {
+  Phases done;
+  const int me = warp - kDownMmaWarp0;  // of the issuers
+  if (me >= 0) {
     if ((threadIdx.x & 31) == 0) {
-      done = down_mma<S>(c, g, walk, tmem);
-      umma::commit(bar_at(c, kDownDrain));  // arrives once every MMA above has completed
+      done = down_mma<S>(c, g, walk, tmem, me);
+      umma::commit(bar_at(c, kDownDrain + me));  // arrives once every MMA above has completed
     }
   } else if (warp < kDownEpWarps) {
     down_epilogue(c, g, walk, tmem);
@@ -481,26 +516,28 @@ __global__ void __launch_bounds__(kDownThreads, 1) down_kernel(const Args g) {
   }
   umma::fence_before_sync();
   __syncthreads();
-  if (warp == kDownMmaWarp) {
-    umma::fence_after_sync();
-    if ((threadIdx.x & 31) == 0) {
-      drain_commits(c, kDownDrain, 1, 1);
-      drain_commits(c, kEmpty0, S, done.ring);
-    }
-    __syncwarp();
-    umma::tmem_dealloc(tmem, kDownCols);
+  umma::fence_after_sync();
+  if (me >= 0 && (threadIdx.x & 31) == 0) {
+    done.add(kDownDrain + me - kEmpty0);
+    drain_commits(c, kEmpty0, done);
   }
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  if (warp == kDownMmaWarp0) umma::tmem_dealloc(tmem, kDownCols);
 }
 
 // ---------------------------------------------------------------- up
 
 constexpr int kGroups = 4;                  // epilogue groups of four warps, one accumulator each
 // Warp w issues on scheduler w % 4.  The 16 epilogue warps take all four (a warp
-// reads the quarter w % 4 of tensor memory); of the others the MMA issuer has
-// scheduler 0, the twelve that bring operands share 1, 2 and 3 (warps 20, 24 and 28
-// are idle).
-constexpr int kUpMmaWarp = 16, kUpWarps = 32, kUpThreads = kUpWarps * 32;
+// reads the quarter w % 4 of tensor memory); of the others the two MMA issuers have
+// scheduler 0, the twelve that bring operands share 1, 2 and 3 (warps 24 and 28 are
+// idle).  The issuers take the even and the odd units (one alone took 78 cycles an
+// MMA, twelve a unit at rank 64, and set the pace).
+constexpr int kUpMmaWarp0 = 16, kUpMmaWarp1 = 20, kUpWarps = 32, kUpThreads = kUpWarps * 32;
 constexpr int kUpProdWarps = 4, kUpTWarps = 4, kUpYWarps = 4;
+constexpr int kUpTWarp = 22;  // one of those of t
 // 0 .. 11 for the warps that bring operands: four each for B, t and y
 __device__ __forceinline__ int up_helper(int warp) { return (warp - 17) / 4 * 3 + (warp - 17) % 4; }
 constexpr int kBRegion = kFeat * 128;       // 16 KB: 128 features x 64 ranks
@@ -528,7 +565,7 @@ constexpr int kMaxBSlots = 4, kMaxYSlots = 8;
 enum { kBFull0 = 0, kBEmpty0 = kBFull0 + kMaxBSlots, kYFull0 = kBEmpty0 + kMaxBSlots,
        kYEmpty0 = kYFull0 + kMaxYSlots, kUDFull0 = kYEmpty0 + kMaxYSlots,
        kUDEmpty0 = kUDFull0 + kGroups, kTFull0 = kUDEmpty0 + kGroups, kTEmpty0 = kTFull0 + 2,
-       kUpDrain = kTEmpty0 + 2, kUpBars };
+       kUpDrain = kTEmpty0 + 2, kUpBars = kUpDrain + 2 };
 constexpr uint32_t kUpCols = kGroups * kTile;
 
 // The CTA's units [first, last): tile u / blocks, features (u % blocks) * 128.
@@ -564,60 +601,68 @@ struct UpWalk {
 };
 
 // B, 128 features a unit: a thread keeps one 16-byte chunk of the ranks and steps
-// through the features, neighbours in a row taking neighbouring chunks.
+// through the features, neighbours in a row taking neighbouring chunks.  Slots go
+// by the unit's number, units that are only copied included, so that a slot
+// belongs to one issuer.
 template <int R>
 __device__ void up_produce(const Ctx& c, const Args& g, UpWalk walk) {
   constexpr int S = Up<R>::kBSlots, kLag = S / 2;
   const int lane = threadIdx.x & 31, tid = up_helper(threadIdx.x >> 5) * 32 + lane;
-  int k = 0, row0 = 0, rows = 1, ch = 0, bytes = 0;
+  int i = 0, row0 = 0, rows = 1, ch = 0, bytes = 0;
+  uint32_t real = 0;  // bit j: unit i - 1 - j has a product
+  Phases filled;
   bool ok = true;
   auto signal = [&](int s) {
     fence_proxy_async();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_at(c, kBFull0 + s % S));
   };
-  while (ok && walk.next()) {
-    if (walk.id < 0) continue;
-    if (walk.fresh) {
-      const int nc = ((walk.rank + 15) >> 4) * 2;  // 16-byte chunks of a row: 2 .. 16
-      rows = (kUpProdWarps * 32) / nc;             // features that the threads cover at once
-      row0 = tid / nc;
-      ch = tid - row0 * nc;
-      if (row0 >= rows) row0 = kFeat;              // left over: no part in it
-      bytes = min(16, max(0, (walk.rank - 8 * ch) * 2));
+  for (; walk.next(); ++i) {
+    if (walk.id >= 0) {
+      if (walk.fresh) {
+        const int nc = ((walk.rank + 15) >> 4) * 2;  // 16-byte chunks of a row: 2 .. 16
+        rows = (kUpProdWarps * 32) / nc;             // features that the threads cover at once
+        row0 = tid / nc;
+        ch = tid - row0 * nc;
+        if (row0 >= rows) row0 = kFeat;              // left over: no part in it
+        bytes = min(16, max(0, (walk.rank - 8 * ch) * 2));
+      }
+      if (filled.has(i % S) && !wait_warp(c, kBEmpty0 + i % S, filled.last(i % S))) {
+        ok = false;
+        break;
+      }
+      filled.add(i % S);
+      const uint32_t to = c.sbase + (i % S) * (R * kBRegion) + (ch >> 3) * kBRegion;
+      const __nv_bfloat16* b = g.b + ((long long)walk.id * g.N + walk.f0) * g.max_rank + 8 * ch;
+      for (int row = row0; row < kFeat; row += rows)
+        cp_async16_zfill(to + row * 128 + (((ch & 7) ^ (row & 7)) << 4), b + row * g.max_rank, bytes);
     }
-    if (k >= S && !wait_warp(c, kBEmpty0 + k % S, (k / S - 1) & 1)) {
-      ok = false;
-      break;
-    }
-    const uint32_t to = c.sbase + (k % S) * (R * kBRegion) + (ch >> 3) * kBRegion;
-    const __nv_bfloat16* b = g.b + ((long long)walk.id * g.N + walk.f0) * g.max_rank + 8 * ch;
-    for (int row = row0; row < kFeat; row += rows)
-      cp_async16_zfill(to + row * 128 + (((ch & 7) ^ (row & 7)) << 4), b + row * g.max_rank, bytes);
-    cp_async_commit();
-    if (k >= kLag) {
-      cp_async_wait<kLag>();
-      signal(k - kLag);
-    }
-    ++k;
+    cp_async_commit();  // an empty group where there is no product
+    real = real << 1 | (walk.id >= 0 ? 1u : 0u);
+    cp_async_wait<kLag>();
+    if (i >= kLag && ((real >> kLag) & 1u)) signal(i - kLag);
   }
   cp_async_wait<0>();
   if (ok)
-    for (int s = max(0, k - kLag); s < k; ++s) signal(s);
+    for (int s = max(0, i - kLag); s < i; ++s)
+      if ((real >> (i - 1 - s)) & 1u) signal(s);
 }
 
 // t of a tile's members: chunk sums added in order, scaled, split.  Warp w takes
-// members w, w + 4, ...; a lane two ranks of each 64.
+// members w, w + 4, ...; a lane two ranks of each 64.  Returns the tiles that went
+// through each slot.
 template <int R>
-__device__ void up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
+__device__ Phases up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
   const int lane = threadIdx.x & 31, w = up_helper(threadIdx.x >> 5) - kUpProdWarps;
   const long long part = (long long)g.n * g.max_rank;
+  Phases tiles;
   int k = 0;
   while (walk.next()) {
     if (!walk.fresh || walk.id < 0) continue;
     const int my_row = __ldcg(g.tile_rows + walk.slot * kTile + lane);
     const float scale = g.scales ? __ldg(g.scales + walk.id) : 1.f;
-    if (k >= 2 && !wait_warp(c, kTEmpty0 + (k & 1), ((k >> 1) - 1) & 1)) return;
+    if (k >= 2 && !wait_warp(c, kTEmpty0 + (k & 1), ((k >> 1) - 1) & 1)) return tiles;
+    tiles.add(k & 1);
     const uint32_t slot = c.sbase + Up<R>::kTOff + (k & 1) * Up<R>::kTSlot;
     for (int m = w; m < walk.count; m += kUpTWarps) {
       const int row = __shfl_sync(kFull, my_row, m);
@@ -660,57 +705,55 @@ __device__ void up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
     if (lane == 0) mbar_arrive(bar_at(c, kTFull0 + (k & 1)));
     ++k;
   }
+  return tiles;
 }
 
+// Issuer `me` takes the units of its parity.  Returns what it committed to the
+// slots of B.
 template <int R>
-__device__ Commits up_mma(const Ctx& c, const Args& g, UpWalk walk, uint32_t tmem) {
+__device__ Phases up_mma(const Ctx& c, const Args& g, UpWalk walk, uint32_t tmem, int me) {
   constexpr int S = Up<R>::kBSlots;
+  static_assert(S % 2 == 0 && kGroups % 2 == 0, "slots and accumulators belong to one issuer");
   const uint64_t base = umma::smem_desc(c.sbase, 16, 1024, umma::kSwizzle128B);
-  Commits done;
-  int& k = done.ring;
-  int& tiles = done.terms;  // tiles begun; a tile is committed with its last unit
-  uint32_t used = 0;        // per group: how often its accumulator was filled, a parity bit each
-  uint32_t ever = 0;
+  Phases slots, accs;
+  int tiles = 0;  // begun
   for (int i = 0; walk.next(); ++i) {
-    const int e = i % kGroups;
     if (walk.id < 0) continue;
     if (walk.fresh) {
-      if (!wait_bar(c, kTFull0 + (tiles & 1), (tiles >> 1) & 1)) return done;
+      if (!wait_bar(c, kTFull0 + (tiles & 1), (tiles >> 1) & 1)) return slots;
       ++tiles;
     }
-    bool ok = true;
-    if ((ever >> e) & 1u) ok = wait_bar(c, kUDEmpty0 + e, ((used >> e) & 1u) ^ 1u);
-    if (!ok || !wait_bar(c, kBFull0 + k % S, (k / S) & 1)) {
-      --tiles;  // its last unit will not be committed
-      return done;
-    }
-    umma::fence_after_sync();
-    // each MMA adds a constant to the operands' descriptors (K = 16 is 32 bytes of
-    // a 128-byte swizzle row; the address field holds bytes / 16 and does not carry
-    // out); a loop over them took 180 cycles an MMA
-    const uint64_t bd = base + (uint64_t)(((k % S) * (R * kBRegion)) >> 4);
-    const uint64_t td = base + (uint64_t)((Up<R>::kTOff + ((tiles - 1) & 1) * Up<R>::kTSlot) >> 4);
-    const uint32_t acc = tmem + e * kTile;
-    const int n_k = (walk.rank + 15) >> 4;
-    umma::mma_bf16(acc, bd, td + (uint64_t)((2 * R * kTRegion) >> 4), kIdesc, 0u);
+    if ((i & 1) == me) {
+      const int e = i % kGroups, s = i % S;
+      if (accs.has(e) && !wait_bar(c, kUDEmpty0 + e, accs.last(e))) return slots;
+      if (!wait_bar(c, kBFull0 + s, slots.next(s))) return slots;
+      umma::fence_after_sync();
+      // each MMA adds a constant to the operands' descriptors (K = 16 is 32 bytes of
+      // a 128-byte swizzle row; the address field holds bytes / 16 and does not
+      // carry out); a loop over them took 180 cycles an MMA
+      const uint64_t bd = base + (uint64_t)((s * (R * kBRegion)) >> 4);
+      const uint64_t td = base + (uint64_t)((Up<R>::kTOff + ((tiles - 1) & 1) * Up<R>::kTSlot) >> 4);
+      const uint32_t acc = tmem + e * kTile;
+      const int n_k = (walk.rank + 15) >> 4;
+      umma::mma_bf16(acc, bd, td + (uint64_t)((2 * R * kTRegion) >> 4), kIdesc, 0u);
 #pragma unroll
-    for (int term = 2; term >= 0; --term) {  // small terms first
+      for (int term = 2; term >= 0; --term) {  // small terms first
 #pragma unroll
-      for (int kb = 0; kb < 4 * R; ++kb) {
-        if ((term == 2 && kb == 0) || kb >= n_k) continue;
-        umma::mma_bf16(acc, bd + (uint64_t)(((kb >> 2) * kBRegion + (kb & 3) * 32) >> 4),
-                       td + (uint64_t)(((term * R + (kb >> 2)) * kTRegion + (kb & 3) * 32) >> 4),
-                       kIdesc, 1u);
+        for (int kb = 0; kb < 4 * R; ++kb) {
+          if ((term == 2 && kb == 0) || kb >= n_k) continue;
+          umma::mma_bf16(acc, bd + (uint64_t)(((kb >> 2) * kBRegion + (kb & 3) * 32) >> 4),
+                         td + (uint64_t)(((term * R + (kb >> 2)) * kTRegion + (kb & 3) * 32) >> 4),
+                         kIdesc, 1u);
+        }
       }
+      umma::commit(bar_at(c, kBEmpty0 + s));
+      umma::commit(bar_at(c, kUDFull0 + e));
+      slots.add(s);
+      accs.add(e);
     }
-    umma::commit(bar_at(c, kBEmpty0 + k % S));
-    umma::commit(bar_at(c, kUDFull0 + e));
-    if (walk.ends) umma::commit(bar_at(c, kTEmpty0 + ((tiles - 1) & 1)));
-    ever |= 1u << e;
-    used ^= 1u << e;
-    ++k;
+    if (walk.ends) umma::commit(bar_at(c, kTEmpty0 + ((tiles - 1) & 1)));  // both issuers do
   }
-  return done;
+  return slots;
 }
 
 // y: warp w brings members w, w + 4, ..., 512 bytes of one each time.
@@ -834,12 +877,13 @@ __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
       if (i >= kYEmpty0 && i < kUDFull0) count = 4;
       if (i >= kUDEmpty0 && i < kTFull0) count = 4;
       if (i == kTFull0 || i == kTFull0 + 1) count = kUpTWarps;
+      if (i == kTEmpty0 || i == kTEmpty0 + 1) count = 2;  // both issuers
       mbar_init(c.bars + 8 * i, count);
     }
     abort_word = 0;
     fence_mbar_init();
   }
-  if (warp == kUpMmaWarp) {
+  if (warp == kUpMmaWarp0) {
     umma::tmem_alloc(smem_addr(&tmem_slot), kUpCols);
     umma::tmem_relinquish();
   }
@@ -852,35 +896,39 @@ __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
   const int first = (int)(total * blockIdx.x / gridDim.x);
   const int last = (int)(total * (blockIdx.x + 1) / gridDim.x);
   UpWalk walk{g, start, last - first, first / blocks, first % blocks, blocks};
-  Commits done;
-  if (warp == kUpMmaWarp) {
+  Phases done;
+  const bool issuer = warp == kUpMmaWarp0 || warp == kUpMmaWarp1;
+  const int me = warp == kUpMmaWarp1;
+  if (issuer) {
     if ((threadIdx.x & 31) == 0) {
-      done = up_mma<R>(c, g, walk, tmem);
-      umma::commit(bar_at(c, kUpDrain));
+      done = up_mma<R>(c, g, walk, tmem, me);
+      umma::commit(bar_at(c, kUpDrain + me));
     }
-  } else if (warp < kUpMmaWarp) {
+  } else if (warp < kUpMmaWarp0) {
     up_epilogue<R>(c, g, walk, tmem, smem);
   } else if (warp % 4) {
     const int h = up_helper(warp);
     if (h < kUpProdWarps)
       up_produce<R>(c, g, walk);
     else if (h < kUpProdWarps + kUpTWarps)
-      up_make_t<R>(c, g, walk);
+      done = up_make_t<R>(c, g, walk);
     else
       up_fetch_y<R>(c, g, walk);
   }
   umma::fence_before_sync();
   __syncthreads();
-  if (warp == kUpMmaWarp) {
-    umma::fence_after_sync();
-    if ((threadIdx.x & 31) == 0) {
-      drain_commits(c, kUpDrain, 1, 1);
-      drain_commits(c, kBEmpty0, Up<R>::kBSlots, done.ring);
-      drain_commits(c, kTEmpty0, 2, done.terms);
-    }
-    __syncwarp();
-    umma::tmem_dealloc(tmem, kUpCols);
+  umma::fence_after_sync();
+  if (issuer && (threadIdx.x & 31) == 0) {
+    if (!mbar_wait(bar_at(c, kUpDrain + me), 0)) set_error(c.hdr, DA_DEVERR_TIMEOUT);
+    drain_commits(c, kBEmpty0, done);
   }
+  // t's slots are released by both issuers together, unless one of them gave up
+  if (warp == kUpTWarp && (threadIdx.x & 31) == 0 && !*c.abort_flag)
+    drain_commits(c, kTEmpty0, done);
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  if (warp == kUpMmaWarp0) umma::tmem_dealloc(tmem, kUpCols);
 }
 
 // ---------------------------------------------------------------- host
