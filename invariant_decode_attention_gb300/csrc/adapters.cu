@@ -2,25 +2,26 @@
 //     t[i, :] = bf16(x[i, :]) A_id^T,   out[i, :] = y[i, :] + (scale_id t[i, :]) B_id^T
 // with each row's own id, every row's bits independent of the batch.
 //
-// Three kernels:
+// Three parts:
 //   plan  groups the rows of a window of 512 by adapter and cuts the groups into
-//         tiles of at most 32 rows (the columns of the matrix products).  Prompts,
+//         tiles of at most 64 rows (the columns of the matrix products).  Prompts,
 //         whose rows come in runs, give full tiles; a decode step's scattered rows
 //         meet their adapter's others anywhere in the window, so an adapter's
-//         weights are read once per 32 rows that use it.
+//         weights are read once per 64 rows that use it.  A kernel of its own; with
+//         one window both matmul kernels make the plan for themselves instead.
 //   down  t: D[rank, member] += A[rank, k] x[member, k] on the tensor cores
-//         (tcgen05, M = 128 of which the adapter's ranks count, N = 32, fp32 in
-//         tensor memory).  K is cut into the chunks of nvfp4_mm (1024), each
-//         summed from zero in K order; a unit of work is a tile and a chunk.
+//         (tcgen05, M = 128 of which the adapter's ranks count, N = 64, fp32 in
+//         tensor memory).  K is cut into the chunks of nvfp4_mm (1024), each summed
+//         from zero by two issuing threads in turn; a unit of work is a tile and a chunk.
 //   up    out: D[feature, member] += B[feature, r] t[member, r], M = 128 features,
-//         N = 32.  The chunk sums of t are added in order, scaled, and split into
+//         N = 64.  The chunk sums of t are added in order, scaled, and split into
 //         three bf16 terms that hold their 24 bits; their products with B are
 //         exact, so out keeps fp32 accuracy.  A unit is a tile and 128 features.
-//         y arrives through the ring as well; the epilogue adds the products to
-//         it in shared memory and writes a row's 512 bytes with one instruction
-//         (loads and stores of 4 bytes a lane took 4900 instructions a unit and
-//         267 us for 8192 rows of 8192; bulk copies of 512 bytes a row, 96 a
-//         unit, 200 us).
+//         y arrives in shared memory, 16 rows at a time; the epilogue adds the
+//         products to it there and writes a row's 512 bytes with one instruction
+//         (loads and stores of 4 bytes a lane took 4900 instructions a unit of 32
+//         rows and 267 us for 8192 rows of 8192, bulk copies of 512 bytes 200 us, y
+//         in registers a quarter ahead 220 us).
 // The orders of all sums depend on K and the rank alone.  A column of an MMA does
 // not depend on the other columns, so neither do a row's bits.
 //
@@ -28,10 +29,14 @@
 // producer warps bring operands into a ring of stages with 16-byte cp.async (rows
 // may lie anywhere, and a copy may end inside 16 bytes, zeros beyond: what memory
 // holds past an adapter's rank is never multiplied) in the 128-byte-swizzled
-// K-major layout; one thread issues the MMAs; epilogue warps drain accumulators.
-// Every wait is bounded; on time-out the kernel records DA_DEVERR_TIMEOUT, all
-// roles leave their loops, copies and tensor-core work are drained and tensor
-// memory is freed.
+// K-major layout, whose landing arrives on the stage's barrier by itself; two threads issue the MMAs (one alone took 80 cycles an MMA and
+// set the pace); epilogue warps drain accumulators.  Every wait is bounded; on
+// time-out the kernel records DA_DEVERR_TIMEOUT, all roles leave their loops,
+// copies and tensor-core work are drained and tensor memory is freed.
+//
+// A parity tells a phase of a barrier from the one before it only, so every waiter
+// goes through all phases of the barriers it waits on, in order: a stage, a slot or
+// an accumulator has one issuer and one epilogue group.
 //
 // y and out (8 N bytes a row) bound a prompt, the adapters' weights and launch
 // latency a decode step.
@@ -47,11 +52,12 @@
 namespace da {
 namespace {
 
-constexpr int kTile = 32;                  // rows per tile (MMA N)
+constexpr int kTile = 64;                  // rows per tile (MMA N)
 constexpr int kWindow = 512;               // rows that are grouped together
+constexpr int kLines = kWindow / 32;
 constexpr int kSlab = 512 * kWindow;       // rows of one set of launches
 constexpr int kMaxRank = NVFP4_ADAPTER_MAX_RANK;
-constexpr int kKChunk = NVFP4_MM_K_CHUNK;  // K summed from zero
+constexpr int kKChunk = NVFP4_MM_K_CHUNK;  // 1024: K summed from zero
 constexpr int kFeat = NVFP4_MM_TILE_N;     // features per unit (MMA M)
 constexpr unsigned kFull = 0xffffffffu;
 constexpr uint32_t kIdesc = umma::idesc_bf16_f32(128, kTile, false);
@@ -67,14 +73,16 @@ struct Args {
   float* out;
   __nv_bfloat16* out_bf16;
   int32_t* hdr;
-  int32_t* tiles_in;   // [windows] tiles of a window; window w's start at slot 512 w
-  int32_t* tile_id;    // [rows] adapter, or -1: rows that are only copied
-  int32_t* tile_count; // [rows] members
-  int32_t* tile_rows;  // [rows][32] their rows, then -1
-  float* t;            // [chunks][n][max_rank]
+  // the plan, window w's tiles from slot 512 w on (several windows)
+  int32_t* tiles_in;    // [windows] tiles of a window
+  int32_t* tile_id;     // adapter, or -1: rows that are only copied
+  int32_t* tile_count;  // members
+  int32_t* tile_first;  // ... from here on in
+  int32_t* order;       // [rows] the rows, tile by tile
+  float* t;             // [chunks][n][max_rank]
   int n, N, K, n_adapters, max_rank, n_chunks, windows;
-  int copy;            // 1: rows without an adapter are written as well
-  int first;           // 1: the call's first slab
+  int copy;             // 1: rows without an adapter are written as well
+  int first;            // 1: the call's first slab
 };
 
 __device__ __forceinline__ void fence_proxy_async() {
@@ -98,62 +106,170 @@ __device__ __forceinline__ int rank_of(const Args& g, int id) {
 
 // ---------------------------------------------------------------- plan
 
-// One CTA per window, one thread per row.
+// The plan of one window, and what making it takes.
+struct Window {
+  int tile_id[kWindow], tile_count[kWindow], tile_first[kWindow], order[kWindow];
+  __align__(16) int id[kWindow];
+  int pos[kWindow], leader[kWindow], before[kLines + 1];
+};
+
+// Rows r0 .. r0 + count - 1, by all threads of the CTA; returns the tiles.
+__device__ int make_plan(const Args& g, int r0, int count, Window& s) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  for (int i = threadIdx.x; i < kWindow; i += blockDim.x) {
+    int v = -2;  // no row, or one that nothing is done for
+    if (i < count) {
+      v = __ldg(g.ids + r0 + i);
+      if (v < 0 || v >= g.n_adapters || rank_of(g, v) == 0) v = g.copy ? -1 : -2;
+    }
+    s.id[i] = v;
+  }
+  __syncthreads();
+  for (int line = warp; line < kLines; line += warps) {
+    const int i = line * 32 + lane, v = s.id[i];
+    unsigned leads = 0;
+    if (line * 32 < count) {
+      // a row's place among the rows of its group: those of earlier lines, then of
+      // its own; every kTile-th row leads a tile
+      int p = 0;
+      for (int j = 0; j < line * 32; j += 4) {
+        const int4 o = *reinterpret_cast<const int4*>(s.id + j);
+        p += (o.x == v) + (o.y == v) + (o.z == v) + (o.w == v);
+      }
+      p += __popc(__match_any_sync(kFull, v) & ((1u << lane) - 1u));
+      s.pos[i] = p;
+      leads = __ballot_sync(kFull, v != -2 && p % kTile == 0);
+    }
+    if (lane == 0) s.before[line + 1] = __popc(leads);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s.before[0] = 0;
+    for (int l = 1; l <= kLines; ++l) s.before[l] += s.before[l - 1];
+  }
+  __syncthreads();
+  for (int line = warp; line * 32 < count; line += warps) {  // tiles are numbered in row order
+    const int i = line * 32 + lane;
+    const bool lead = s.id[i] != -2 && s.pos[i] % kTile == 0;
+    const unsigned leads = __ballot_sync(kFull, lead);
+    if (lead) s.leader[s.before[line] + __popc(leads & ((1u << lane) - 1u))] = i;
+  }
+  __syncthreads();
+  const int tiles = s.before[kLines];
+  // the members of tile t are the rows of its leader's group from the leader's place
+  // on; first they are counted, then listed
+  auto members = [&](int t, int line, int* q) {
+    const int lead = s.leader[t], r = line * 32 + lane;
+    *q = s.pos[r] - s.pos[lead];
+    return r < count && s.id[r] == s.id[lead] && *q >= 0 && *q < kTile;
+  };
+  for (int t = warp; t < tiles; t += warps) {  // a warp per tile
+    int found = 0, q;
+    for (int line = s.leader[t] >> 5; line * 32 < count && found < kTile; ++line)
+      found += __popc(__ballot_sync(kFull, members(t, line, &q)));
+    if (lane == 0) {
+      s.tile_id[t] = s.id[s.leader[t]];
+      s.tile_count[t] = found;
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int run = 0;
+    for (int t0 = 0; t0 < tiles; t0 += 32) {
+      const int n = t0 + lane < tiles ? s.tile_count[t0 + lane] : 0;
+      int sum = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, sum, o);
+        if (lane >= o) sum += u;
+      }
+      if (t0 + lane < tiles) s.tile_first[t0 + lane] = run + sum - n;
+      run += __shfl_sync(kFull, sum, 31);
+    }
+  }
+  __syncthreads();
+  for (int t = warp; t < tiles; t += warps) {
+    int left = s.tile_count[t], q;
+    for (int line = s.leader[t] >> 5; left > 0; ++line) {
+      const bool mine = members(t, line, &q);
+      if (mine) s.order[s.tile_first[t] + q] = r0 + line * 32 + lane;
+      left -= __popc(__ballot_sync(kFull, mine));
+    }
+  }
+  __syncthreads();
+  return tiles;
+}
+
+// One CTA per window.
 __global__ void __launch_bounds__(kWindow) plan_kernel(const Args g) {
-  __shared__ __align__(16) int id[kWindow];
-  __shared__ int pos[kWindow], leader[kWindow], before[kWindow / 32 + 1];
+  __shared__ Window s;
   wait_prior_grid();
   allow_next_grid();  // after the wait: what ran before this call has finished
-  const int i = threadIdx.x, lane = i & 31, line = i >> 5;
-  const int r0 = blockIdx.x * kWindow, count = min(kWindow, g.n - r0);
+  const int i = threadIdx.x, r0 = blockIdx.x * kWindow, count = min(kWindow, g.n - r0);
   if (blockIdx.x == 0 && i == 0 && g.first) g.hdr[kHdrError] = 0;  // errors of this call only
-  int v = -2;  // no row, or one that nothing is done for
-  if (i < count) {
-    v = __ldg(g.ids + r0 + i);
-    if (v < 0 || v >= g.n_adapters || rank_of(g, v) == 0) v = g.copy ? -1 : -2;
-  }
-  id[i] = v;
-  __syncthreads();
-  // this row's place among the rows of its group: those of earlier lines, then
-  // of its own
-  int p = 0;
-  for (int j = 0; j < line * 32; j += 4) {
-    const int4 o = *reinterpret_cast<const int4*>(id + j);
-    p += (o.x == v) + (o.y == v) + (o.z == v) + (o.w == v);
-  }
-  p += __popc(__match_any_sync(kFull, v) & ((1u << lane) - 1u));
-  pos[i] = p;
-  // every 32nd row of a group leads a tile; tiles are numbered in row order
-  const unsigned leads = __ballot_sync(kFull, v != -2 && p % kTile == 0);
-  if (lane == 0) before[line + 1] = __popc(leads);
-  if (i == 0) before[0] = 0;
-  __syncthreads();
-  if (i == 0)
-    for (int l = 1; l <= kWindow / 32; ++l) before[l] += before[l - 1];
-  __syncthreads();
-  if ((leads >> lane) & 1u) leader[before[line] + __popc(leads & ((1u << lane) - 1u))] = i;
-  __syncthreads();
-  const int tiles = before[kWindow / 32];
+  const int tiles = make_plan(g, r0, count, s);
   if (i == 0) g.tiles_in[blockIdx.x] = tiles;
-  for (int t = line; t < tiles; t += kWindow / 32) {  // a warp per tile
-    const int lead = leader[t], tv = id[lead], tp = pos[lead];
-    const long long slot = r0 + t;
-    int found = 0;
-    for (int j = lead & ~31; j < count && found < kTile; j += 32) {
-      const int r = j + lane, q = pos[r] - tp;
-      const bool mine = id[r] == tv && q >= 0 && q < kTile;
-      if (mine) g.tile_rows[slot * kTile + q] = r0 + r;
-      found += __popc(__ballot_sync(kFull, mine));
-    }
-    if (lane >= found) g.tile_rows[slot * kTile + lane] = -1;
-    if (lane == 0) {
-      g.tile_id[slot] = tv;
-      g.tile_count[slot] = found;
-    }
+  if (i < tiles) {
+    g.tile_id[r0 + i] = s.tile_id[i];
+    g.tile_count[r0 + i] = s.tile_count[i];
+    g.tile_first[r0 + i] = r0 + s.tile_first[i];
   }
+  if (i < count) g.order[r0 + i] = s.order[i];
 }
 
 // ---------------------------------------------------------------- shared by the matmul kernels
+
+// The call's tiles as a matmul kernel sees them: its own plan or the plan kernel's.
+struct Tiles {
+  const int* start;  // [windows + 1] tiles before a window
+  const int *id, *count, *first, *order;
+  int windows, total;
+
+  // Slot of tile number t.
+  __device__ __forceinline__ int slot(int t) const {
+    int lo = 0, hi = windows;  // start[lo] <= t < start[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (start[mid] <= t) lo = mid; else hi = mid;
+    }
+    return lo * kWindow + (t - start[lo]);
+  }
+};
+
+// Gets the tiles; by all threads.  One window: planned here, in `own`.
+__device__ Tiles get_tiles(const Args& g, int* start, Window& own) {
+  Tiles r;
+  r.start = start;
+  r.windows = g.windows;
+  if (g.windows == 1) {
+    r.total = make_plan(g, 0, g.n, own);
+    if (threadIdx.x == 0) start[0] = 0, start[1] = r.total;
+    r.id = own.tile_id, r.count = own.tile_count, r.first = own.tile_first, r.order = own.order;
+    __syncthreads();
+    return r;
+  }
+  r.id = g.tile_id, r.count = g.tile_count, r.first = g.tile_first, r.order = g.order;
+  for (int w = threadIdx.x; w < g.windows; w += blockDim.x) start[w + 1] = g.tiles_in[w];
+  if (threadIdx.x == 0) start[0] = 0;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    int run = 0;
+    for (int w0 = 0; w0 < g.windows; w0 += 32) {
+      const int w = w0 + (int)threadIdx.x;
+      int s = w < g.windows ? start[w + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, s, o);
+        if ((int)threadIdx.x >= o) s += u;
+      }
+      if (w < g.windows) start[w + 1] = run + s;
+      run += __shfl_sync(kFull, s, 31);
+    }
+  }
+  __syncthreads();
+  r.total = start[g.windows];
+  return r;
+}
 
 struct Ctx {
   uint32_t sbase, bars;  // shared memory, and its mbarriers
@@ -190,40 +306,6 @@ __device__ __forceinline__ bool wait_warp(const Ctx& c, int i, uint32_t parity) 
   return ok != 0;
 }
 
-// Windows' tiles counted up: start[w] is the number of tiles before window w.
-// Called by all threads; returns the total.
-__device__ int count_tiles(const Args& g, int* start) {
-  for (int w = threadIdx.x; w < g.windows; w += blockDim.x) start[w + 1] = __ldcg(g.tiles_in + w);
-  if (threadIdx.x == 0) start[0] = 0;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    int run = 0;
-    for (int w0 = 0; w0 < g.windows; w0 += 32) {
-      const int w = w0 + (int)threadIdx.x;
-      int s = w < g.windows ? start[w + 1] : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(kFull, s, o);
-        if ((int)threadIdx.x >= o) s += u;
-      }
-      if (w < g.windows) start[w + 1] = run + s;
-      run += __shfl_sync(kFull, s, 31);
-    }
-  }
-  __syncthreads();
-  return start[g.windows];
-}
-
-// Slot of the call's tile number t.
-__device__ __forceinline__ long long slot_of(const int* start, int windows, int t) {
-  int lo = 0, hi = windows;  // start[lo] <= t < start[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (start[mid] <= t) lo = mid; else hi = mid;
-  }
-  return (long long)lo * kWindow + (t - start[lo]);
-}
-
 // A set of barriers of which each has completed some number of phases: one bit
 // each for "any" and for the number's parity.
 struct Phases {
@@ -247,93 +329,96 @@ __device__ __forceinline__ void drain_commits(const Ctx& c, int first, const Pha
 
 // ---------------------------------------------------------------- down
 
-constexpr int kStepK = 256, kRegionK = 64;         // K of a stage, and of a 128-byte swizzle row
-constexpr int kXRegion = kTile * kRegionK * 2;     // 4 KB
+constexpr int kStepK = 128, kRegionK = 64;         // K of a stage, and of a 128-byte swizzle row
+constexpr int kXRegion = kTile * kRegionK * 2;     // 8 KB
 constexpr int kXStage = (kStepK / kRegionK) * kXRegion;
-// Two threads issue the MMAs (one took 90 cycles an MMA and set the pace): the
-// even and the odd stages, each into an accumulator of its own that the epilogue
-// adds.  Which of the two a step goes to depends on what came before, but the sum
-// of two numbers does not.
 constexpr int kDownEpWarps = 4, kDownProdWarp0 = 4, kDownProdWarps = 8, kDownMmaWarp0 = 12;
 constexpr int kDownThreads = (kDownMmaWarp0 + 2) * 32;
-constexpr int kDownStages = 4;
-// mbarriers: stage full and empty, accumulator full and empty, drain
+constexpr int kDownStages = 6;                     // at most
+// Two threads issue the MMAs: the even and the odd steps, each into an accumulator
+// of its own that the epilogue adds.  Which of the two a step goes to depends on
+// what came before, but the sum of two numbers does not.
+// mbarriers: stage full and empty, accumulators full and empty, drain
 enum { kFull0 = 0, kEmpty0 = kFull0 + kDownStages, kDFull0 = kEmpty0 + kDownStages,
        kDEmpty0 = kDFull0 + 2, kDownDrain = kDEmpty0 + 2, kDownBars = kDownDrain + 2 };
 constexpr uint32_t kDownCols = 4 * kTile;          // two units' two accumulators
 
 __host__ __device__ constexpr int down_stage_bytes(int max_rank) {
-  return max_rank * kStepK * 2 + kXStage;
+  return max_rank * kStepK * 2 + kXStage;          // 32 KB at rank 64, 48 KB at 128
 }
-__host__ __device__ constexpr int down_stages(int max_rank) { return max_rank <= 64 ? 4 : 2; }
 
-struct DownUnit {
-  long long slot;
-  int id, count, rank, k0, k_len, chunk;
-};
-
-// Units of the CTA, one after the other; all roles walk them alike.  Tiles that
-// are only copied have none.
+// The CTA's units, tile by tile and chunk by chunk; all roles walk them alike.
+// Tiles that are only copied are passed over.
 struct DownWalk {
   const Args& g;
-  const int* start;
-  int u, total;
-  __device__ __forceinline__ bool next(DownUnit* d) {
-    for (; u < total; u += gridDim.x) {
-      const int tile = u / g.n_chunks;
-      d->slot = slot_of(start, g.windows, tile);
-      d->id = __ldcg(g.tile_id + d->slot);
-      if (d->id < 0) continue;
-      d->count = __ldcg(g.tile_count + d->slot);
-      d->rank = rank_of(g, d->id);
-      d->chunk = u - tile * g.n_chunks;
-      d->k0 = d->chunk * kKChunk;
-      d->k_len = min(g.K, d->k0 + kKChunk) - d->k0;
-      u += gridDim.x;
-      return true;
+  const Tiles& tiles;
+  int left, tile, chunk;  // units to come, and where the next one is
+  int id = 0, first = 0, count = 0, rank = 0, k0 = 0, k_len = 0;
+  bool seen = false, fresh = false;  // fresh: the unit is its tile's first in this CTA
+  __device__ __forceinline__ bool next() {
+    while (left > 0) {
+      fresh = !seen;
+      if (fresh) {
+        const int slot = tiles.slot(tile);
+        id = tiles.id[slot];
+        first = tiles.first[slot];
+        count = tiles.count[slot];
+        rank = id >= 0 ? rank_of(g, id) : 0;
+        seen = true;
+      }
+      if (id < 0) {  // the tile's other units too
+        const int skip = min(left, g.n_chunks - chunk);
+        left -= skip;
+        chunk += skip;
+      } else {
+        k0 = chunk * kKChunk;
+        k_len = min(g.K, k0 + kKChunk) - k0;
+        --left;
+        ++chunk;
+      }
+      if (chunk == g.n_chunks) {
+        chunk = 0;
+        ++tile;
+        seen = false;
+      }
+      if (id >= 0) return true;
     }
     return false;
   }
 };
 
-// Producer warp w brings rows w, w + 8, ... of A and of the members' x; a lane
-// copies 16 bytes of K, a warp 512 bytes of one row.
+// A warp's copy takes 256 bytes of two rows; warp w brings rows 2 w, 2 w + 1 of
+// every 16 of A and of the members' x.
 template <bool BF16, int S>
 __device__ void down_produce(const Ctx& c, const Args& g, DownWalk walk) {
-  constexpr int kLag = S / 2;  // stages that are landing while others are multiplied
-  constexpr int kMine = kTile / kDownProdWarps;
+  constexpr int kMine = kTile / 16;
   constexpr int kElem = BF16 ? 2 : 4;
-  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kDownProdWarp0;
+  const int lane = threadIdx.x & 31;
+  const int row0 = 2 * ((threadIdx.x >> 5) - kDownProdWarp0) + (lane >> 4), e0 = 8 * (lane & 15);
   const int stage_bytes = down_stage_bytes(g.max_rank), a_region = g.max_rank * 128;
-  // where this lane's 16 bytes go within a stage: rows w + 8 i differ by 1024 bytes
-  // and share the swizzle (w & 7)
-  const uint32_t swz = ((lane & 7) ^ (w & 7)) << 4;
-  const uint32_t a_at = (lane >> 3) * a_region + w * 128 + swz;
-  const uint32_t x_at = 4 * a_region + (lane >> 3) * kXRegion + w * 128 + swz;
+  // where this lane's 16 bytes go within a stage: rows row0 + 16 i differ by 2048
+  // bytes and share the swizzle
+  const int region = (lane & 15) >> 3;
+  const uint32_t at0 = row0 * 128 + (((lane & 7) ^ (row0 & 7)) << 4);
+  const uint32_t a_at = region * a_region + at0, x_at = 2 * a_region + region * kXRegion + at0;
   int step = 0;
   bool ok = true;
-  auto signal = [&](int s) {  // stage s % S has landed
-    fence_proxy_async();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar_at(c, kFull0 + s % S));
-  };
-  DownUnit d;
-  while (ok && walk.next(&d)) {
-    const int my_row = __ldcg(g.tile_rows + d.slot * kTile + lane);
-    const char* xp[kMine];  // this lane's 8 elements of its rows' x, or null
+  const char* xp[kMine];  // this lane's first 8 elements of its rows' x, or null
+  const char* ap = nullptr;
+  while (ok && walk.next()) {
+    if (walk.fresh) {
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      const int row = __shfl_sync(kFull, my_row, w + i * kDownProdWarps);
-      xp[i] = row < 0 ? nullptr
-                      : static_cast<const char*>(g.x) +
-                            ((long long)row * g.K + d.k0 + 8 * lane) * kElem;
+      for (int i = 0; i < kMine; ++i) {
+        const int m = row0 + 16 * i;
+        xp[i] = m < walk.count ? static_cast<const char*>(g.x) +
+                                     ((long long)walk.tiles.order[walk.first + m] * g.K + e0) * kElem
+                               : nullptr;
+      }
+      ap = reinterpret_cast<const char*>(g.a + ((long long)walk.id * g.max_rank + row0) * g.K + e0);
     }
-    const int rows_a = (((d.rank + 15) & ~15) - w + kDownProdWarps - 1) / kDownProdWarps;
-    const char* ap = reinterpret_cast<const char*>(
-        g.a + ((long long)d.id * g.max_rank + w) * g.K + d.k0 + 8 * lane);
-    const long long a_step = (long long)kDownProdWarps * g.K * 2;
-    for (int k = 0; k < d.k_len; k += kStepK, ++step) {
-      const bool live = k + 8 * lane < d.k_len;  // K is a multiple of 64: whole regions
+    const int passes = (walk.rank + 15) >> 4;
+    for (int k = walk.k0; k < walk.k0 + walk.k_len; k += kStepK, ++step) {
+      const bool live = k + e0 < walk.k0 + walk.k_len;  // K is a multiple of 64: whole regions
       uint4 v[kMine];
       if constexpr (!BF16) {  // fp32 rows are rounded on the way; their loads come first
 #pragma unroll
@@ -353,53 +438,53 @@ __device__ void down_produce(const Ctx& c, const Args& g, DownWalk walk) {
       const uint32_t stage = c.sbase + (step % S) * stage_bytes;
       if (live) {
         const char* p = ap + k * 2;
-        uint32_t at = stage + a_at;
-        for (int i = 0; i < rows_a; ++i, p += a_step, at += 1024) cp_async16(at, p);
+        for (int i = 0; i < passes; ++i) cp_async16(stage + a_at + i * 2048, p + (long long)i * 32 * g.K);
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
           if (!xp[i]) continue;
           if constexpr (BF16)
-            cp_async16(stage + x_at + i * 1024, xp[i] + k * kElem);
+            cp_async16(stage + x_at + i * 2048, xp[i] + k * kElem);
           else
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + x_at + i * 1024),
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + x_at + i * 2048),
                          "r"(v[i].x), "r"(v[i].y), "r"(v[i].z), "r"(v[i].w)
                          : "memory");
         }
       }
-      cp_async_commit();
-      if (step >= kLag) {
-        cp_async_wait<kLag>();
-        signal(step - kLag);
+      cp_async_mbar_arrive(bar_at(c, kFull0 + step % S));  // when this thread's copies have landed
+      if constexpr (!BF16) {  // and its stores
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_at(c, kFull0 + step % S));
       }
     }
   }
-  cp_async_wait<0>();  // what is left has landed as well
-  if (ok)
-    for (int s = max(0, step - kLag); s < step; ++s) signal(s);
+  cp_async_wait_all();  // nothing is in flight when the CTA ends
 }
 
 // Issuer `me` takes the steps of its parity; returns what it committed to the
 // stages' empty barriers.
 template <int S>
 __device__ Phases down_mma(const Ctx& c, const Args& g, DownWalk walk, uint32_t tmem, int me) {
+  static_assert(S % 2 == 0, "a stage belongs to one issuer");
   const int stage_bytes = down_stage_bytes(g.max_rank), a_region = g.max_rank * 128;
   const uint64_t base = umma::smem_desc(c.sbase, 16, 1024, umma::kSwizzle128B);
   Phases done;
   int step = 0, k_unit = 0;
-  DownUnit d;
-  for (; walk.next(&d); ++k_unit) {
+  for (; walk.next(); ++k_unit) {
     const int tb = k_unit & 1;
     if (k_unit >= 2 && !wait_bar(c, kDEmpty0 + tb, ((k_unit >> 1) - 1) & 1)) return done;
     umma::fence_after_sync();
     const uint32_t acc = tmem + (2 * tb + me) * kTile;
     bool first = true;
-    for (int k = 0; k < d.k_len; k += kStepK, ++step) {
+    for (int k = 0; k < walk.k_len; k += kStepK, ++step) {
       if ((step & 1) != me) continue;
       if (!wait_bar(c, kFull0 + step % S, (step / S) & 1)) return done;
+      fence_proxy_async();  // the copies wrote through the generic proxy, the MMAs do not read through it
       umma::fence_after_sync();
-      const int n_mma = min(kStepK, d.k_len - k) / 16;
+      const int n_mma = min(kStepK, walk.k_len - k) / 16;
+      // each MMA adds a constant to the operands' descriptors (K = 16 is 32 bytes of a
+      // 128-byte swizzle row; the address field holds bytes / 16 and does not carry out)
       const uint64_t ad = base + (uint64_t)(((step % S) * stage_bytes) >> 4);
-      const uint64_t xd = ad + (uint64_t)((4 * a_region) >> 4);
+      const uint64_t xd = ad + (uint64_t)((2 * a_region) >> 4);
 #pragma unroll
       for (int rg = 0; rg < kStepK / kRegionK; ++rg) {
         if (4 * rg >= n_mma) break;
@@ -422,34 +507,33 @@ __device__ Phases down_mma(const Ctx& c, const Args& g, DownWalk walk, uint32_t 
 // Warp q: ranks 32 q .. 32 q + 31, one a lane.
 __device__ void down_epilogue(const Ctx& c, const Args& g, DownWalk walk, uint32_t tmem) {
   const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
-  int k_unit = 0, step = 0;
-  DownUnit d;
-  for (; walk.next(&d); ++k_unit) {
-    const int my_row = __ldcg(g.tile_rows + d.slot * kTile + lane), tb = k_unit & 1;
-    const int steps = (d.k_len + kStepK - 1) / kStepK;
+  int k_unit = 0, step = 0, row_lo = 0, row_hi = 0;  // members lane and lane + 32
+  for (; walk.next(); ++k_unit) {
+    if (walk.fresh) {
+      if (lane < walk.count) row_lo = walk.tiles.order[walk.first + lane];
+      if (lane + 32 < walk.count) row_hi = walk.tiles.order[walk.first + lane + 32];
+    }
+    const int tb = k_unit & 1, steps = (walk.k_len + kStepK - 1) / kStepK;
     if (!wait_warp(c, kDFull0 + tb, (k_unit >> 1) & 1)) return;
     umma::fence_after_sync();
     const int r = 32 * q + lane;
-    float* t = g.t + (long long)d.chunk * g.n * g.max_rank + r;
+    float* t = g.t + (long long)(walk.k0 / kKChunk) * g.n * g.max_rank + r;
     const uint32_t from = tmem + ((uint32_t)(q * 32) << 16) + 2 * tb * kTile;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int m0 = 0; m0 < walk.count && 32 * q < walk.rank; m0 += 16) {
       float u[16], v[16];
-      umma::ld_32x32b_x16(from + (step & 1) * kTile + 16 * h, u);  // of the unit's first step
-      if (steps > 1) umma::ld_32x32b_x16(from + (~step & 1) * kTile + 16 * h, v);
+      umma::ld_32x32b_x16(from + (step & 1) * kTile + m0, u);  // of the unit's first step
+      if (steps > 1) umma::ld_32x32b_x16(from + (~step & 1) * kTile + m0, v);
       umma::wait_ld();
-      if (h == 1) {
-        umma::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_at(c, kDEmpty0 + tb));
-      }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int row = __shfl_sync(kFull, my_row, 16 * h + i);
-        if (row >= 0 && r < d.rank)
+        const int row = __shfl_sync(kFull, m0 < 32 ? row_lo : row_hi, (m0 + i) & 31);
+        if (m0 + i < walk.count && r < walk.rank)
           t[(long long)row * g.max_rank] = steps > 1 ? u[i] + v[i] : u[i];
       }
     }
+    umma::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_at(c, kDEmpty0 + tb));
     step += steps;
   }
 }
@@ -457,12 +541,11 @@ __device__ void down_epilogue(const Ctx& c, const Args& g, DownWalk walk, uint32
 template <bool BF16, int S>
 __global__ void __launch_bounds__(kDownThreads, 1) down_kernel(const Args g) {
   extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ Window own;
   __shared__ int start[kSlab / kWindow + 1];
   __shared__ __align__(8) uint64_t bars[kDownBars];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
-  wait_prior_grid();
-  allow_next_grid();
   Ctx c;
   c.sbase = smem_addr(smem);
   c.bars = smem_addr(bars);
@@ -470,22 +553,14 @@ __global__ void __launch_bounds__(kDownThreads, 1) down_kernel(const Args g) {
   c.hdr = g.hdr;
   const int warp = threadIdx.x >> 5;
   if (c.sbase & 1023u) {  // the swizzled layout needs 1024-byte-aligned shared memory
+    wait_prior_grid();
     if (threadIdx.x == 0) set_error(g.hdr, DA_DEVERR_TIMEOUT);
     return;
-  }
-  // input checks, spread over the grid
-  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < g.n; i += gridDim.x * blockDim.x) {
-    const int v = __ldg(g.ids + i);
-    if (v >= g.n_adapters) set_error(g.hdr, DA_DEVERR_INDEX);
-    if (v >= 0 && v < g.n_adapters && g.ranks) {
-      const int r = __ldg(g.ranks + v);
-      if (r < 0 || r > g.max_rank) set_error(g.hdr, DA_DEVERR_LENGTH);
-    }
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kDownBars; ++i) {
       uint32_t count = 1;  // tcgen05.commit
-      if (i < kEmpty0) count = kDownProdWarps;
+      if (i < kEmpty0) count = kDownProdWarps * (32 + (BF16 ? 0 : 1));
       if (i >= kDFull0 && i < kDEmpty0) count = 2;  // both issuers
       if (i >= kDEmpty0 && i < kDownDrain) count = kDownEpWarps;
       mbar_init(c.bars + 8 * i, count);
@@ -493,15 +568,42 @@ __global__ void __launch_bounds__(kDownThreads, 1) down_kernel(const Args g) {
     abort_word = 0;
     fence_mbar_init();
   }
-  if (warp == kDownMmaWarp0) {
+  wait_prior_grid();
+  allow_next_grid();  // after the wait: what ran before this call has finished
+  if (warp == kDownMmaWarp0) {  // not before: the previous kernel may own tensor memory
     umma::tmem_alloc(smem_addr(&tmem_slot), kDownCols);
     umma::tmem_relinquish();
   }
+  // input checks, spread over the grid; with one window CTA 0 makes them and its
+  // store also clears the word
+  int bad = 0;
+  if (g.windows > 1 || blockIdx.x == 0) {
+    const int stride = g.windows > 1 ? gridDim.x * blockDim.x : blockDim.x;
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < g.n; i += stride) {
+      const int v = __ldg(g.ids + i);
+      if (v >= g.n_adapters) bad |= DA_DEVERR_INDEX;
+      if (v >= 0 && v < g.n_adapters && g.ranks) {
+        const int r = __ldg(g.ranks + v);
+        if (r < 0 || r > g.max_rank) bad |= DA_DEVERR_LENGTH;
+      }
+    }
+    if (g.windows > 1) {
+      if (bad) set_error(g.hdr, bad);
+    } else {
+      const int index = __syncthreads_or(bad & DA_DEVERR_INDEX);
+      const int length = __syncthreads_or(bad & DA_DEVERR_LENGTH);
+      if (threadIdx.x == 0)
+        g.hdr[kHdrError] = (index ? DA_DEVERR_INDEX : 0) | (length ? DA_DEVERR_LENGTH : 0);
+    }
+  }
   umma::fence_before_sync();
-  const int tiles = count_tiles(g, start);  // holds CTA barriers
+  const Tiles tiles = get_tiles(g, start, own);  // holds CTA barriers
   umma::fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
-  DownWalk walk{g, start, (int)blockIdx.x, tiles * g.n_chunks};
+  const long long total = (long long)tiles.total * g.n_chunks;
+  const int first = (int)(total * blockIdx.x / gridDim.x);
+  const int last = (int)(total * (blockIdx.x + 1) / gridDim.x);
+  DownWalk walk{g, tiles, last - first, first / g.n_chunks, first % g.n_chunks};
   Phases done;
   const int me = warp - kDownMmaWarp0;  // of the issuers
   if (me >= 0) {
@@ -533,48 +635,44 @@ constexpr int kGroups = 4;                  // epilogue groups of four warps, on
 // Warp w issues on scheduler w % 4.  The 16 epilogue warps take all four (a warp
 // reads the quarter w % 4 of tensor memory); of the others the two MMA issuers have
 // scheduler 0, the twelve that bring operands share 1, 2 and 3 (warps 24 and 28 are
-// idle).  The issuers take the even and the odd units (one alone took 78 cycles an
-// MMA, twelve a unit at rank 64, and set the pace).
+// idle).  The issuers take the even and the odd units.
 constexpr int kUpMmaWarp0 = 16, kUpMmaWarp1 = 20, kUpWarps = 32, kUpThreads = kUpWarps * 32;
-constexpr int kUpProdWarps = 4, kUpTWarps = 4, kUpYWarps = 4;
+constexpr int kUpProdWarps = 4, kUpTWarps = 4;
 constexpr int kUpTWarp = 22;  // one of those of t
-// 0 .. 11 for the warps that bring operands: four each for B, t and y
+// 0 .. 11 for the warps that bring operands: four each for B and t, one for each
+// group's y
 __device__ __forceinline__ int up_helper(int warp) { return (warp - 17) / 4 * 3 + (warp - 17) % 4; }
 constexpr int kBRegion = kFeat * 128;       // 16 KB: 128 features x 64 ranks
-constexpr int kTRegion = kTile * 128;       // 4 KB: 32 members x 64 ranks
-constexpr int kYRow = kFeat * 4;            // 512 bytes of a row of y
-constexpr int kYSlot = kTile * kYRow;       // 16 KB
+constexpr int kTRegion = kTile * 128;       // 8 KB: 64 members x 64 ranks
+constexpr int kYRow = kFeat * 4;            // 512 bytes: a member's 128 features
+constexpr int kYSlot = 16 * kYRow;          // 8 KB: a quarter of a tile
+constexpr int kYSlots = 3;                  // of each epilogue group
 
 // Shared memory by R, the 64-rank regions of an adapter of max_rank: four or two
-// slots of B, two of t's terms, eight or four of y.
+// slots of B, two or one of t's terms, and the groups' y.
 template <int R>
 struct Up {
-  static constexpr int kBSlots = 4 / R, kYSlots = 8 / R;
+  static constexpr int kBSlots = 4 / R, kTSlots = 2 / R;
   static constexpr int kTOff = kBSlots * R * kBRegion;
   static constexpr int kTSlot = 3 * R * kTRegion;
-  static constexpr int kYOff = kTOff + 2 * kTSlot;
-  static constexpr int kSmem = kYOff + kYSlots * kYSlot;
-  // A parity tells a phase from the one before it only.  A slot of y must belong to
-  // one group, which waits for its phases one by one: a group that came to another
-  // group's slot could ask for a phase before the previous one has completed, and
-  // would be let through.
-  static_assert(kYSlots % kGroups == 0, "a slot of y belongs to one group");
-  static_assert(kYOff % 1024 == 0 && kSmem <= 220 * 1024 && 2 * kSmem > 233472, "one CTA per SM");
+  static constexpr int kYOff = kTOff + kTSlots * kTSlot;
+  static constexpr int kSmem = kYOff + kGroups * kYSlots * kYSlot;
+  static_assert(kBSlots % 2 == 0 && kGroups % 2 == 0, "slots and accumulators have one issuer");
+  static_assert(kYOff % 1024 == 0 && kSmem <= 209 * 1024 && 2 * kSmem > 233472, "one CTA per SM");
 };
-constexpr int kMaxBSlots = 4, kMaxYSlots = 8;
-enum { kBFull0 = 0, kBEmpty0 = kBFull0 + kMaxBSlots, kYFull0 = kBEmpty0 + kMaxBSlots,
-       kYEmpty0 = kYFull0 + kMaxYSlots, kUDFull0 = kYEmpty0 + kMaxYSlots,
+constexpr int kMaxBSlots = 4;
+enum { kBFull0 = 0, kBEmpty0 = kBFull0 + kMaxBSlots, kUDFull0 = kBEmpty0 + kMaxBSlots,
        kUDEmpty0 = kUDFull0 + kGroups, kTFull0 = kUDEmpty0 + kGroups, kTEmpty0 = kTFull0 + 2,
-       kUpDrain = kTEmpty0 + 2, kUpBars = kUpDrain + 2 };
+       kYFull0 = kTEmpty0 + 2, kYEmpty0 = kYFull0 + kGroups * kYSlots,
+       kUpDrain = kYEmpty0 + kGroups * kYSlots, kUpBars = kUpDrain + 2 };
 constexpr uint32_t kUpCols = kGroups * kTile;
 
-// The CTA's units [first, last): tile u / blocks, features (u % blocks) * 128.
+// The CTA's units: tile by tile, 128 features each.
 struct UpWalk {
   const Args& g;
-  const int* start;
+  const Tiles& tiles;
   int left, tile, block, blocks;  // units to come, and where the next one is
-  long long slot = 0;
-  int id = 0, count = 0, rank = 0, f0 = 0;
+  int id = 0, count = 0, first = 0, rank = 0, f0 = 0;
   bool fresh = false;  // the unit is its tile's first in this CTA
   bool ends = false;   // ... and its last
   bool seen = false;
@@ -583,9 +681,10 @@ struct UpWalk {
     --left;
     fresh = !seen;
     if (fresh) {
-      slot = slot_of(start, g.windows, tile);
-      id = __ldcg(g.tile_id + slot);
-      count = __ldcg(g.tile_count + slot);
+      const int slot = tiles.slot(tile);
+      id = tiles.id[slot];
+      count = tiles.count[slot];
+      first = tiles.first[slot];
       rank = id >= 0 ? rank_of(g, id) : 0;
       seen = true;
     }
@@ -606,46 +705,29 @@ struct UpWalk {
 // belongs to one issuer.
 template <int R>
 __device__ void up_produce(const Ctx& c, const Args& g, UpWalk walk) {
-  constexpr int S = Up<R>::kBSlots, kLag = S / 2;
+  constexpr int S = Up<R>::kBSlots;
   const int lane = threadIdx.x & 31, tid = up_helper(threadIdx.x >> 5) * 32 + lane;
-  int i = 0, row0 = 0, rows = 1, ch = 0, bytes = 0;
-  uint32_t real = 0;  // bit j: unit i - 1 - j has a product
+  int row0 = 0, rows = 1, ch = 0, bytes = 0;
   Phases filled;
-  bool ok = true;
-  auto signal = [&](int s) {
-    fence_proxy_async();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar_at(c, kBFull0 + s % S));
-  };
-  for (; walk.next(); ++i) {
-    if (walk.id >= 0) {
-      if (walk.fresh) {
-        const int nc = ((walk.rank + 15) >> 4) * 2;  // 16-byte chunks of a row: 2 .. 16
-        rows = (kUpProdWarps * 32) / nc;             // features that the threads cover at once
-        row0 = tid / nc;
-        ch = tid - row0 * nc;
-        if (row0 >= rows) row0 = kFeat;              // left over: no part in it
-        bytes = min(16, max(0, (walk.rank - 8 * ch) * 2));
-      }
-      if (filled.has(i % S) && !wait_warp(c, kBEmpty0 + i % S, filled.last(i % S))) {
-        ok = false;
-        break;
-      }
-      filled.add(i % S);
-      const uint32_t to = c.sbase + (i % S) * (R * kBRegion) + (ch >> 3) * kBRegion;
-      const __nv_bfloat16* b = g.b + ((long long)walk.id * g.N + walk.f0) * g.max_rank + 8 * ch;
-      for (int row = row0; row < kFeat; row += rows)
-        cp_async16_zfill(to + row * 128 + (((ch & 7) ^ (row & 7)) << 4), b + row * g.max_rank, bytes);
+  for (int i = 0; walk.next(); ++i) {
+    if (walk.id < 0) continue;
+    if (walk.fresh) {
+      const int nc = ((walk.rank + 15) >> 4) * 2;  // 16-byte chunks of a row: 2 .. 16
+      rows = (kUpProdWarps * 32) / nc;             // features that the threads cover at once
+      row0 = tid / nc;
+      ch = tid - row0 * nc;
+      if (row0 >= rows) row0 = kFeat;              // left over: no part in it
+      bytes = min(16, max(0, (walk.rank - 8 * ch) * 2));
     }
-    cp_async_commit();  // an empty group where there is no product
-    real = real << 1 | (walk.id >= 0 ? 1u : 0u);
-    cp_async_wait<kLag>();
-    if (i >= kLag && ((real >> kLag) & 1u)) signal(i - kLag);
+    if (filled.has(i % S) && !wait_warp(c, kBEmpty0 + i % S, filled.last(i % S))) break;
+    filled.add(i % S);
+    const uint32_t to = c.sbase + (i % S) * (R * kBRegion) + (ch >> 3) * kBRegion;
+    const __nv_bfloat16* b = g.b + ((long long)walk.id * g.N + walk.f0) * g.max_rank + 8 * ch;
+    for (int row = row0; row < kFeat; row += rows)
+      cp_async16_zfill(to + row * 128 + (((ch & 7) ^ (row & 7)) << 4), b + row * g.max_rank, bytes);
+    cp_async_mbar_arrive(bar_at(c, kBFull0 + i % S));
   }
-  cp_async_wait<0>();
-  if (ok)
-    for (int s = max(0, i - kLag); s < i; ++s)
-      if ((real >> (i - 1 - s)) & 1u) signal(s);
+  cp_async_wait_all();
 }
 
 // t of a tile's members: chunk sums added in order, scaled, split.  Warp w takes
@@ -653,56 +735,80 @@ __device__ void up_produce(const Ctx& c, const Args& g, UpWalk walk) {
 // through each slot.
 template <int R>
 __device__ Phases up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
+  constexpr int S = Up<R>::kTSlots;
   const int lane = threadIdx.x & 31, w = up_helper(threadIdx.x >> 5) - kUpProdWarps;
   const long long part = (long long)g.n * g.max_rank;
   Phases tiles;
   int k = 0;
   while (walk.next()) {
     if (!walk.fresh || walk.id < 0) continue;
-    const int my_row = __ldcg(g.tile_rows + walk.slot * kTile + lane);
     const float scale = g.scales ? __ldg(g.scales + walk.id) : 1.f;
-    if (k >= 2 && !wait_warp(c, kTEmpty0 + (k & 1), ((k >> 1) - 1) & 1)) return tiles;
-    tiles.add(k & 1);
-    const uint32_t slot = c.sbase + Up<R>::kTOff + (k & 1) * Up<R>::kTSlot;
-    for (int m = w; m < walk.count; m += kUpTWarps) {
-      const int row = __shfl_sync(kFull, my_row, m);
+    if (k >= S && !wait_warp(c, kTEmpty0 + k % S, (k / S - 1) & 1)) return tiles;
+    tiles.add(k % S);
+    const uint32_t slot = c.sbase + Up<R>::kTOff + (k % S) * Up<R>::kTSlot;
+    int row_lo = 0, row_hi = 0;  // members lane and lane + 32
+    if (lane < walk.count) row_lo = walk.tiles.order[walk.first + lane];
+    if (lane + 32 < walk.count) row_hi = walk.tiles.order[walk.first + lane + 32];
+    // kBatch members at once: their loads are in flight together (one by one a tile of
+    // 64 took 25 us)
+    constexpr int kBatch = 8;
+    for (int m0 = w; m0 < walk.count; m0 += kBatch * kUpTWarps) {
 #pragma unroll
       for (int reg = 0; reg < R; ++reg) {
         const int r = 64 * reg + 2 * lane;
-        float v[2] = {0.f, 0.f};
-        if (r < walk.rank) {  // the row is max_rank long, so r + 1 may be read
-          const float* t = g.t + (long long)row * g.max_rank + r;
-          float2 s = __ldcg(reinterpret_cast<const float2*>(t));
-#pragma unroll 4
-          for (int p = 1; p < g.n_chunks; ++p) {
-            const float2 e = __ldcg(reinterpret_cast<const float2*>(t + p * part));
-            s.x += e.x;
-            s.y += e.y;
-          }
-          v[0] = s.x * scale;
-          v[1] = r + 1 < walk.rank ? s.y * scale : 0.f;
+        const bool live = r < walk.rank;  // the row is max_rank long, so r + 1 may be read
+        const float* t[kBatch];
+        float2 sum[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int m = m0 + j * kUpTWarps;
+          const int row = __shfl_sync(kFull, m < 32 ? row_lo : row_hi, m & 31);
+          t[j] = g.t + (long long)row * g.max_rank + r;
+          sum[j] = make_float2(0.f, 0.f);
+          if (live && m < walk.count) sum[j] = __ldcg(reinterpret_cast<const float2*>(t[j]));
         }
-        const uint32_t at = slot + reg * kTRegion + m * 128 + (((lane >> 2) ^ (m & 7)) << 4) +
-                            (lane & 3) * 4;
+        for (int p = 1; p < g.n_chunks; ++p) {
+          float2 e[kBatch];
 #pragma unroll
-        for (int term = 0; term < 3; ++term) {  // each takes the next eight bits
-          __nv_bfloat16 h[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            h[e] = __float2bfloat16_rn(v[e]);
-            // nothing is left of an infinity (inf - inf would make it a NaN)
-            v[e] = __hisinf(h[e]) ? 0.f : v[e] - __bfloat162float(h[e]);
+          for (int j = 0; j < kBatch; ++j) {
+            e[j] = make_float2(0.f, 0.f);
+            if (live && m0 + j * kUpTWarps < walk.count)
+              e[j] = __ldcg(reinterpret_cast<const float2*>(t[j] + p * part));
           }
-          const uint32_t word = (uint32_t)__bfloat16_as_ushort(h[0]) |
-                                (uint32_t)__bfloat16_as_ushort(h[1]) << 16;
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + term * R * kTRegion), "r"(word)
-                       : "memory");
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            sum[j].x += e[j].x;
+            sum[j].y += e[j].y;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int m = m0 + j * kUpTWarps;
+          if (m >= walk.count) break;
+          float v[2] = {live ? sum[j].x * scale : 0.f,
+                        r + 1 < walk.rank ? sum[j].y * scale : 0.f};
+          const uint32_t at = slot + reg * kTRegion + m * 128 + (((lane >> 2) ^ (m & 7)) << 4) +
+                              (lane & 3) * 4;
+#pragma unroll
+          for (int term = 0; term < 3; ++term) {  // each takes the next eight bits
+            __nv_bfloat16 h[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              h[i] = __float2bfloat16_rn(v[i]);
+              // nothing is left of an infinity (inf - inf would make it a NaN)
+              v[i] = __hisinf(h[i]) ? 0.f : v[i] - __bfloat162float(h[i]);
+            }
+            const uint32_t word = (uint32_t)__bfloat16_as_ushort(h[0]) |
+                                  (uint32_t)__bfloat16_as_ushort(h[1]) << 16;
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + term * R * kTRegion), "r"(word)
+                         : "memory");
+          }
         }
       }
     }
     fence_proxy_async();
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar_at(c, kTFull0 + (k & 1)));
+    if (lane == 0) mbar_arrive(bar_at(c, kTFull0 + k % S));
     ++k;
   }
   return tiles;
@@ -712,27 +818,25 @@ __device__ Phases up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
 // slots of B.
 template <int R>
 __device__ Phases up_mma(const Ctx& c, const Args& g, UpWalk walk, uint32_t tmem, int me) {
-  constexpr int S = Up<R>::kBSlots;
-  static_assert(S % 2 == 0 && kGroups % 2 == 0, "slots and accumulators belong to one issuer");
+  constexpr int S = Up<R>::kBSlots, TS = Up<R>::kTSlots;
   const uint64_t base = umma::smem_desc(c.sbase, 16, 1024, umma::kSwizzle128B);
   Phases slots, accs;
   int tiles = 0;  // begun
   for (int i = 0; walk.next(); ++i) {
     if (walk.id < 0) continue;
     if (walk.fresh) {
-      if (!wait_bar(c, kTFull0 + (tiles & 1), (tiles >> 1) & 1)) return slots;
+      if (!wait_bar(c, kTFull0 + tiles % TS, (tiles / TS) & 1)) return slots;
       ++tiles;
     }
+    const int ts = (tiles - 1) % TS;
     if ((i & 1) == me) {
       const int e = i % kGroups, s = i % S;
       if (accs.has(e) && !wait_bar(c, kUDEmpty0 + e, accs.last(e))) return slots;
       if (!wait_bar(c, kBFull0 + s, slots.next(s))) return slots;
+      fence_proxy_async();  // as in down_mma
       umma::fence_after_sync();
-      // each MMA adds a constant to the operands' descriptors (K = 16 is 32 bytes of
-      // a 128-byte swizzle row; the address field holds bytes / 16 and does not
-      // carry out); a loop over them took 180 cycles an MMA
       const uint64_t bd = base + (uint64_t)((s * (R * kBRegion)) >> 4);
-      const uint64_t td = base + (uint64_t)((Up<R>::kTOff + ((tiles - 1) & 1) * Up<R>::kTSlot) >> 4);
+      const uint64_t td = base + (uint64_t)((Up<R>::kTOff + ts * Up<R>::kTSlot) >> 4);
       const uint32_t acc = tmem + e * kTile;
       const int n_k = (walk.rank + 15) >> 4;
       umma::mma_bf16(acc, bd, td + (uint64_t)((2 * R * kTRegion) >> 4), kIdesc, 0u);
@@ -751,133 +855,132 @@ __device__ Phases up_mma(const Ctx& c, const Args& g, UpWalk walk, uint32_t tmem
       slots.add(s);
       accs.add(e);
     }
-    if (walk.ends) umma::commit(bar_at(c, kTEmpty0 + ((tiles - 1) & 1)));  // both issuers do
+    if (walk.ends) umma::commit(bar_at(c, kTEmpty0 + ts));  // both issuers do
   }
   return slots;
 }
 
-// y: warp w brings members w, w + 4, ..., 512 bytes of one each time.
+// y of group e's units, a quarter of a tile at a time, a row's 512 bytes with one
+// instruction.
 template <int R>
 __device__ void up_fetch_y(const Ctx& c, const Args& g, UpWalk walk) {
-  constexpr int S = Up<R>::kYSlots, kLag = S / 2;
-  const int lane = threadIdx.x & 31, w = up_helper(threadIdx.x >> 5) - kUpProdWarps - kUpTWarps;
-  int i = 0, my_row = -1;
+  constexpr int S = kYSlots;
+  const int lane = threadIdx.x & 31, e = up_helper(threadIdx.x >> 5) - kUpProdWarps - kUpTWarps;
+  const int full = kYFull0 + e * S, empty = kYEmpty0 + e * S;
+  const uint32_t ring = c.sbase + Up<R>::kYOff + e * S * kYSlot + lane * 16;
+  int k = 0, row_lo = 0, row_hi = 0;  // members lane and lane + 32
   bool ok = true;
-  auto signal = [&](int s) {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar_at(c, kYFull0 + s % S));
-  };
-  for (; ok && walk.next(); ++i) {
-    if (walk.fresh) my_row = __ldcg(g.tile_rows + walk.slot * kTile + lane);
-    if (i >= S && !wait_warp(c, kYEmpty0 + i % S, (i / S - 1) & 1)) {
-      ok = false;
-      break;
+  for (int i = 0; ok && walk.next(); ++i) {
+    if (walk.fresh) {
+      if (lane < walk.count) row_lo = walk.tiles.order[walk.first + lane];
+      if (lane + 32 < walk.count) row_hi = walk.tiles.order[walk.first + lane + 32];
     }
-    const uint32_t slot = c.sbase + Up<R>::kYOff + (i % S) * kYSlot + lane * 16;
+    if (i % kGroups != e) continue;
     const float* y = g.y + walk.f0 + 4 * lane;
+    for (int m0 = 0; m0 < walk.count; m0 += 16, ++k) {
+      if (k >= S && !wait_warp(c, empty + k % S, (k / S - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      const uint32_t to = ring + (k % S) * kYSlot;
 #pragma unroll
-    for (int j = 0; j < kTile / kUpYWarps; ++j) {
-      const int m = w + j * kUpYWarps;
-      const int row = __shfl_sync(kFull, my_row, m);
-      if (m < walk.count) cp_async16(slot + m * kYRow, y + (long long)row * g.N);
-    }
-    cp_async_commit();
-    if (i >= kLag) {
-      cp_async_wait<kLag>();
-      signal(i - kLag);
+      for (int m = 0; m < 16; ++m) {
+        const int row = __shfl_sync(kFull, m0 < 32 ? row_lo : row_hi, (m0 + m) & 31);
+        if (m0 + m < walk.count) cp_async16(to + m * kYRow, y + (long long)row * g.N);
+      }
+      cp_async_mbar_arrive(bar_at(c, full + k % S));
     }
   }
-  cp_async_wait<0>();
-  if (ok)
-    for (int s = max(0, i - kLag); s < i; ++s) signal(s);
+  cp_async_wait_all();
 }
 
-// Group e takes units e, e + 4, ... of the CTA.  Warp q of it first adds features
-// 32 q .. + 31, one a lane, to y in shared memory, then writes members q, q + 4,
-// ..., 16 bytes a lane.
+// Group e takes units e, e + 4, ... of the CTA, a quarter of the members at a time:
+// warp q of it adds features 32 q .. + 31, one a lane, to y in shared memory, and
+// then writes members q, q + 4, ... of the quarter, 16 bytes a lane.
 template <int R>
 __device__ void up_epilogue(const Ctx& c, const Args& g, UpWalk walk, uint32_t tmem, uint8_t* smem) {
-  constexpr int S = Up<R>::kYSlots;
+  constexpr int S = kYSlots;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = warp & 3, e = warp >> 2;
+  uint8_t* ring = smem + Up<R>::kYOff + e * S * kYSlot;
   uint32_t parity = 0;
-  int my_row = -1;
+  int k = 0, my_row = 0;  // member q + 4 lane (lanes 0 .. 15)
   for (int i = 0; walk.next(); ++i) {
-    if (walk.fresh) my_row = __ldcg(g.tile_rows + walk.slot * kTile + lane);
+    if (walk.fresh && lane < 16 && q + 4 * lane < walk.count)
+      my_row = walk.tiles.order[walk.first + q + 4 * lane];
     if (i % kGroups != e) continue;
-    uint8_t* slot = smem + Up<R>::kYOff + (i % S) * kYSlot;
     const int count = walk.count;
-    bool ok = wait_warp(c, kYFull0 + i % S, (i / S) & 1);
-    if (walk.id >= 0) {
-      ok = ok && wait_warp(c, kUDFull0 + e, parity);
-      parity ^= 1u;
-      if (ok) {
-        float* yv = reinterpret_cast<float*>(slot) + 32 * q + lane;
-        umma::fence_after_sync();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
+    const bool product = walk.id >= 0, write = product || g.out != g.y;
+    for (int m0 = 0; m0 < count; m0 += 16, ++k) {
+      uint8_t* slot = ring + (k % S) * kYSlot;
+      bool ok = wait_warp(c, kYFull0 + e * S + k % S, (k / S) & 1);
+      if (product) {
+        if (m0 == 0) {
+          ok = ok && wait_warp(c, kUDFull0 + e, parity);
+          parity ^= 1u;
+        }
+        if (ok) {
+          umma::fence_after_sync();
           float d[16];
-          umma::ld_32x32b_x16(tmem + ((uint32_t)(q * 32) << 16) + e * kTile + 16 * h, d);
+          umma::ld_32x32b_x16(tmem + ((uint32_t)(q * 32) << 16) + e * kTile + m0, d);
           umma::wait_ld();
-          if (h == 1) {
+          if (m0 + 16 >= count) {
             umma::fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_at(c, kUDEmpty0 + e));
           }
-          if (count <= 16 * h) continue;
+          float* yv = reinterpret_cast<float*>(slot) + 32 * q + lane;
 #pragma unroll
-          for (int m = 0; m < 16; ++m)  // members past count hold leftovers; none is stored
-            yv[(16 * h + m) * kFeat] += d[m];
+          for (int m = 0; m < 16; ++m) yv[m * kFeat] += d[m];  // past count: leftovers, not stored
         }
       }
-    }
-    // the group's four warps meet, or leave together
-    if (named_bar_or(1 + e, 128, !ok)) return;
-    const bool write = walk.id >= 0 || g.out != g.y;
+      // the group's four warps meet, or leave together
+      if (named_bar_or(1 + e, 128, !ok)) return;
 #pragma unroll
-    for (int j = 0; j < kTile / 4; ++j) {
-      const int m = q + 4 * j;
-      const int row = __shfl_sync(kFull, my_row, m);
-      if (m >= count) continue;
-      const float4 v = *reinterpret_cast<const float4*>(slot + m * kYRow + 16 * lane);
-      const long long at = (long long)row * g.N + walk.f0 + 4 * lane;
-      if (write) *reinterpret_cast<float4*>(g.out + at) = v;
-      if (g.out_bf16)
-        *reinterpret_cast<uint2*>(g.out_bf16 + at) =
-            make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+      for (int j = 0; j < 4; ++j) {
+        const int m = q + 4 * j;
+        const int row = __shfl_sync(kFull, my_row, (m0 >> 2) + j);
+        if (m0 + m >= count) continue;
+        const float4 v = *reinterpret_cast<const float4*>(slot + m * kYRow + 16 * lane);
+        const long long at = (long long)row * g.N + walk.f0 + 4 * lane;
+        if (write) *reinterpret_cast<float4*>(g.out + at) = v;
+        if (g.out_bf16)
+          *reinterpret_cast<uint2*>(g.out_bf16 + at) =
+              make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_at(c, kYEmpty0 + e * S + k % S));
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar_at(c, kYEmpty0 + i % S));
   }
 }
 
 template <int R>
 __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
   extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ Window own;
   __shared__ int start[kSlab / kWindow + 1];
   __shared__ __align__(8) uint64_t bars[kUpBars];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
-  wait_prior_grid();
-  allow_next_grid();
   Ctx c;
   c.sbase = smem_addr(smem);
   c.bars = smem_addr(bars);
   c.abort_flag = &abort_word;
   c.hdr = g.hdr;
   const int warp = threadIdx.x >> 5;
-  if (c.sbase & 1023u) {
+  if (c.sbase & 1023u) {  // the swizzled layout needs 1024-byte-aligned shared memory
+    wait_prior_grid();
     if (threadIdx.x == 0) set_error(g.hdr, DA_DEVERR_TIMEOUT);
     return;
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kUpBars; ++i) {
-      uint32_t count = 1;  // tcgen05.commit, or one thread
-      if (i < kBEmpty0) count = kUpProdWarps;
-      if (i >= kYFull0 && i < kYEmpty0) count = kUpYWarps;
-      if (i >= kYEmpty0 && i < kUDFull0) count = 4;
+      uint32_t count = 1;  // tcgen05.commit
+      if (i < kBEmpty0) count = kUpProdWarps * 32;
+      if (i >= kYFull0 && i < kYEmpty0) count = 32;
       if (i >= kUDEmpty0 && i < kTFull0) count = 4;
       if (i == kTFull0 || i == kTFull0 + 1) count = kUpTWarps;
       if (i == kTEmpty0 || i == kTEmpty0 + 1) count = 2;  // both issuers
+      if (i >= kYEmpty0 && i < kUpDrain) count = 4;
       mbar_init(c.bars + 8 * i, count);
     }
     abort_word = 0;
@@ -888,14 +991,19 @@ __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
     umma::tmem_relinquish();
   }
   umma::fence_before_sync();
-  const int tiles = count_tiles(g, start);  // holds CTA barriers
+  // one window: the plan needs ids and ranks only, which were complete before the
+  // down kernel let this one start
+  if (g.windows > 1) wait_prior_grid();
+  const Tiles tiles = get_tiles(g, start, own);  // holds CTA barriers
+  if (g.windows == 1) wait_prior_grid();
+  allow_next_grid();
   umma::fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
   const int blocks = g.N / kFeat;
-  const long long total = (long long)tiles * blocks;
+  const long long total = (long long)tiles.total * blocks;
   const int first = (int)(total * blockIdx.x / gridDim.x);
   const int last = (int)(total * (blockIdx.x + 1) / gridDim.x);
-  UpWalk walk{g, start, last - first, first / blocks, first % blocks, blocks};
+  UpWalk walk{g, tiles, last - first, first / blocks, first % blocks, blocks};
   Phases done;
   const bool issuer = warp == kUpMmaWarp0 || warp == kUpMmaWarp1;
   const int me = warp == kUpMmaWarp1;
@@ -948,17 +1056,18 @@ bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p)
 int chunks_of(int K) { return (K + kKChunk - 1) / kKChunk; }
 
 struct Layout {
-  size_t tiles_in, tile_id, tile_count, tile_rows, t, total;
+  size_t tiles_in, tile_id, tile_count, tile_first, order, t, total;
 };
 
 Layout layout_of(int n, int K, int max_rank) {
-  const size_t rows = (size_t)std::min(n, kSlab);
+  const size_t rows = (size_t)std::min(n, kSlab), ints = round_up(rows * 4, 256);
   Layout l;
   l.tiles_in = kHdr;
   l.tile_id = l.tiles_in + round_up((rows + kWindow - 1) / kWindow * 4, 256);
-  l.tile_count = l.tile_id + round_up(rows * 4, 256);
-  l.tile_rows = l.tile_count + round_up(rows * 4, 256);
-  l.t = l.tile_rows + rows * kTile * 4;
+  l.tile_count = l.tile_id + ints;
+  l.tile_first = l.tile_count + ints;
+  l.order = l.tile_first + ints;
+  l.t = l.order + ints;
   l.total = l.t + (size_t)chunks_of(K) * rows * max_rank * 4;
   return l;
 }
@@ -1034,7 +1143,8 @@ int nvfp4_mm_adapters(const void* x, int32_t x_dtype, int32_t n, int32_t N, int3
   g.tiles_in = reinterpret_cast<int32_t*>(base + l.tiles_in);
   g.tile_id = reinterpret_cast<int32_t*>(base + l.tile_id);
   g.tile_count = reinterpret_cast<int32_t*>(base + l.tile_count);
-  g.tile_rows = reinterpret_cast<int32_t*>(base + l.tile_rows);
+  g.tile_first = reinterpret_cast<int32_t*>(base + l.tile_first);
+  g.order = reinterpret_cast<int32_t*>(base + l.order);
   g.t = reinterpret_cast<float*>(base + l.t);
   g.N = N;
   g.K = K;
@@ -1044,10 +1154,10 @@ int nvfp4_mm_adapters(const void* x, int32_t x_dtype, int32_t n, int32_t N, int3
   g.copy = out != y || out_bf16;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf16 = x_dtype == NVFP4_X_BF16;
-  // four stages of up to 48 KB, or two of up to 80; ranks of up to 64 take one
+  // six stages of up to 32 KB, or four of up to 48; ranks of up to 64 take one
   // region of a slot, higher ones two
-  auto* down = down_stages(max_rank) == 4 ? (bf16 ? launch_down<true, 4> : launch_down<false, 4>)
-                                          : (bf16 ? launch_down<true, 2> : launch_down<false, 2>);
+  auto* down = max_rank <= 64 ? (bf16 ? launch_down<true, 6> : launch_down<false, 6>)
+                              : (bf16 ? launch_down<true, 4> : launch_down<false, 4>);
   auto* up = max_rank <= 64 ? launch_up<1> : launch_up<2>;
   for (int r0 = 0; r0 < n; r0 += kSlab) {
     const size_t row = (size_t)r0;
@@ -1059,7 +1169,9 @@ int nvfp4_mm_adapters(const void* x, int32_t x_dtype, int32_t n, int32_t N, int3
     g.y = y + row * N;
     g.out = out + row * N;
     g.out_bf16 = out_bf16 ? static_cast<__nv_bfloat16*>(out_bf16) + row * N : nullptr;
-    if (launch_after(plan_kernel, dim3((unsigned)g.windows), dim3(kWindow), 0, st, g) != cudaSuccess)
+    if (g.windows > 1 &&
+        launch_after(plan_kernel, dim3((unsigned)g.windows), dim3(kWindow), 0, st, g) !=
+            cudaSuccess)
       return DA_ERR_CUDA;
     if (down(g, sms, st) != cudaSuccess) return DA_ERR_CUDA;
     if (up(g, sms, st) != cudaSuccess) return DA_ERR_CUDA;

@@ -95,7 +95,7 @@ def test_against_oracle(api, n, N, K, count, max_rank, x):
 @gpu
 def test_prompts_in_runs(api):
     # runs of rows that cross tiles, a run of one, rows without an adapter
-    ids = [0] * 70 + [3] * 33 + [-1] * 5 + [1] + [2] * 64 + [-1] * 40 + [0] * 3
+    ids = [0] * 140 + [3] * 33 + [-1] * 5 + [1] + [2] * 64 + [-1] * 40 + [0] * 3
     c = Case(api, len(ids), 256, 1024, 4, 64, ids=ids, ranks=None, seed=4)
     c.check(c.run())
 
@@ -122,11 +122,11 @@ def test_row_bits_do_not_depend_on_the_batch(api):
         rows = torch.randperm(200, generator=g)[:n]
         assert torch.equal(c.run(rows), full[rows]), n
     # all rows on one adapter, alone and together, at every place of a tile
-    d = Case(api, 40, 128, 640, 2, 32, ids=[1] * 40, ranks=None, seed=13)
+    d = Case(api, 80, 128, 640, 2, 32, ids=[1] * 80, ranks=None, seed=13)
     full = d.run()
-    for i in (0, 7, 8, 31, 32, 39):
+    for i in (0, 7, 8, 15, 16, 31, 32, 63, 64, 79):
         assert torch.equal(d.run([i])[0], full[i])
-    assert torch.equal(d.run(list(range(39, -1, -1))), full.flip(0))
+    assert torch.equal(d.run(list(range(79, -1, -1))), full.flip(0))
 
 
 @gpu
@@ -237,8 +237,9 @@ def test_argument_rules(api):
     L, vp = api.lib(), ctypes.c_void_p
     fake = 1 << 20  # never dereferenced: every case fails before any device work
     size = L.nvfp4_mm_adapters_workspace_bytes
-    # header, tiles per window, id and size of each tile, its rows, t per K chunk
-    assert size(4, 128, 1088, 3, 64) == 4 * 256 + 4 * 128 + 2 * 4 * 64 * 4
+    # header, tiles per window, the tiles' ids, sizes and places, the rows in their
+    # order, t per 1024 of K
+    assert size(4, 128, 1088, 3, 64) == 6 * 256 + 2 * 4 * 64 * 4
     assert size(1 << 19, 128, 64, 1, 16) == size(1 << 18, 128, 64, 1, 16)  # rows in slabs
     for shape in ((-1, 128, 64, 1, 16), (1, 100, 64, 1, 16), (1, 128, 96, 1, 16), (1, 128, 64, 0, 16),
                   (1, 128, 64, 1, 8), (1, 128, 64, 1, 144), (1, 128, 64, 1, 24), (1 << 20, 128, 2048, 1, 16)):
