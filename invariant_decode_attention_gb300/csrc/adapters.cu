@@ -18,7 +18,7 @@
 //         three bf16 terms that hold their 24 bits; their products with B are
 //         exact, so out keeps fp32 accuracy.  A unit is a tile and 128 features.
 //         y arrives in shared memory, 16 rows at a time; the epilogue adds the
-//         products to it there and writes a row's 512 bytes with one instruction
+//         products to it there and writes whole 128-byte lines, 16 bytes a lane
 //         (loads and stores of 4 bytes a lane took 4900 instructions a unit of 32
 //         rows and 267 us for 8192 rows of 8192, bulk copies of 512 bytes 200 us, y
 //         in registers a quarter ahead 220 us).
@@ -388,11 +388,12 @@ struct DownWalk {
 };
 
 // A warp's copy takes 256 bytes of two rows; warp w brings rows 2 w, 2 w + 1 of
-// every 16 of A and of the members' x.
+// every 16 of A and of the members' x.  fp32 rows of x are rounded on the way: a
+// lane keeps kAhead of their pieces (16 rows of a step) in registers, so that
+// several steps of a few rows, or one of many, are on their way.
 template <bool BF16, int S>
 __device__ void down_produce(const Ctx& c, const Args& g, DownWalk walk) {
-  constexpr int kMine = kTile / 16;
-  constexpr int kElem = BF16 ? 2 : 4;
+  constexpr int kElem = BF16 ? 2 : 4, kAhead = 4;
   const int lane = threadIdx.x & 31;
   const int row0 = 2 * ((threadIdx.x >> 5) - kDownProdWarp0) + (lane >> 4), e0 = 8 * (lane & 15);
   const int stage_bytes = down_stage_bytes(g.max_rank), a_region = g.max_rank * 128;
@@ -403,12 +404,12 @@ __device__ void down_produce(const Ctx& c, const Args& g, DownWalk walk) {
   const uint32_t a_at = region * a_region + at0, x_at = 2 * a_region + region * kXRegion + at0;
   int step = 0;
   bool ok = true;
-  const char* xp[kMine];  // this lane's first 8 elements of its rows' x, or null
+  const char* xp[kTile / 16];  // this lane's first 8 elements of its rows' x, or null
   const char* ap = nullptr;
   while (ok && walk.next()) {
     if (walk.fresh) {
 #pragma unroll
-      for (int i = 0; i < kMine; ++i) {
+      for (int i = 0; i < kTile / 16; ++i) {
         const int m = row0 + 16 * i;
         xp[i] = m < walk.count ? static_cast<const char*>(g.x) +
                                      ((long long)walk.tiles.order[walk.first + m] * g.K + e0) * kElem
@@ -416,44 +417,60 @@ __device__ void down_produce(const Ctx& c, const Args& g, DownWalk walk) {
       }
       ap = reinterpret_cast<const char*>(g.a + ((long long)walk.id * g.max_rank + row0) * g.K + e0);
     }
-    const int passes = (walk.rank + 15) >> 4;
-    for (int k = walk.k0; k < walk.k0 + walk.k_len; k += kStepK, ++step) {
-      const bool live = k + e0 < walk.k0 + walk.k_len;  // K is a multiple of 64: whole regions
-      uint4 v[kMine];
-      if constexpr (!BF16) {  // fp32 rows are rounded on the way; their loads come first
+    const int passes = (walk.rank + 15) >> 4, pieces = (walk.count + 15) >> 4;
+    const int k_end = walk.k0 + walk.k_len;
+    // K is a multiple of 64, so whole regions are live
+    auto begin = [&](int k) {  // the step's stage is free; A goes there
+      if (step >= S && !wait_warp(c, kEmpty0 + step % S, (step / S - 1) & 1)) return false;
+      if (k + e0 < k_end) {
+        const uint32_t to = c.sbase + (step % S) * stage_bytes + a_at;
+        for (int i = 0; i < passes; ++i) cp_async16(to + i * 2048, ap + 2 * (k + (long long)i * 16 * g.K));
+      }
+      return true;
+    };
+    if constexpr (BF16) {
+      for (int k = walk.k0; k < k_end; k += kStepK, ++step) {
+        if (!(ok = begin(k))) break;
+        const uint32_t to = c.sbase + (step % S) * stage_bytes + x_at;
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          if (xp[i] && live) {
-            const float4* q = reinterpret_cast<const float4*>(xp[i] + k * kElem);
-            const float4 e = __ldg(q), f = __ldg(q + 1);
-            v[i] = make_uint4(pack_bf16(e.x, e.y), pack_bf16(e.z, e.w), pack_bf16(f.x, f.y),
-                              pack_bf16(f.z, f.w));
+        for (int i = 0; i < kTile / 16; ++i)
+          if (xp[i] && k + e0 < k_end) cp_async16(to + i * 2048, xp[i] + k * kElem);
+        cp_async_mbar_arrive(bar_at(c, kFull0 + step % S));  // when this thread's copies have landed
+      }
+    } else {
+      float4 lo[kAhead], hi[kAhead];
+      int kf = walk.k0, pf = 0;  // step and piece to ask for next
+      auto fetch = [&](int u) {
+        const char* p = pf == 0 ? xp[0] : pf == 1 ? xp[1] : pf == 2 ? xp[2] : xp[3];
+        if (p && kf + e0 < k_end) {
+          lo[u] = __ldg(reinterpret_cast<const float4*>(p + kf * kElem));
+          hi[u] = __ldg(reinterpret_cast<const float4*>(p + kf * kElem) + 1);
+        }
+        if (++pf == pieces) pf = 0, kf += kStepK;
+      };
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) fetch(u);
+      for (int k = walk.k0, i = 0; ok && k < k_end;) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          if (k >= k_end || !ok) break;
+          if (i == 0 && !(ok = begin(k))) break;
+          if (row0 + 16 * i < walk.count && k + e0 < k_end)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             c.sbase + (step % S) * stage_bytes + x_at + i * 2048),
+                         "r"(pack_bf16(lo[u].x, lo[u].y)), "r"(pack_bf16(lo[u].z, lo[u].w)),
+                         "r"(pack_bf16(hi[u].x, hi[u].y)), "r"(pack_bf16(hi[u].z, hi[u].w))
+                         : "memory");
+          fetch(u);
+          if (++i == pieces) {
+            cp_async_mbar_arrive(bar_at(c, kFull0 + step % S));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_at(c, kFull0 + step % S));  // the stores
+            i = 0;
+            k += kStepK;
+            ++step;
           }
         }
-      }
-      if (step >= S && !wait_warp(c, kEmpty0 + step % S, (step / S - 1) & 1)) {
-        ok = false;
-        break;
-      }
-      const uint32_t stage = c.sbase + (step % S) * stage_bytes;
-      if (live) {
-        const char* p = ap + k * 2;
-        for (int i = 0; i < passes; ++i) cp_async16(stage + a_at + i * 2048, p + (long long)i * 32 * g.K);
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          if (!xp[i]) continue;
-          if constexpr (BF16)
-            cp_async16(stage + x_at + i * 2048, xp[i] + k * kElem);
-          else
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + x_at + i * 2048),
-                         "r"(v[i].x), "r"(v[i].y), "r"(v[i].z), "r"(v[i].w)
-                         : "memory");
-        }
-      }
-      cp_async_mbar_arrive(bar_at(c, kFull0 + step % S));  // when this thread's copies have landed
-      if constexpr (!BF16) {  // and its stores
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_at(c, kFull0 + step % S));
       }
     }
   }
@@ -894,54 +911,57 @@ __device__ void up_fetch_y(const Ctx& c, const Args& g, UpWalk walk) {
   cp_async_wait_all();
 }
 
-// Group e takes units e, e + 4, ... of the CTA, a quarter of the members at a time:
-// warp q of it adds features 32 q .. + 31, one a lane, to y in shared memory, and
-// then writes members q, q + 4, ... of the quarter, 16 bytes a lane.
+// Group e takes units e, e + 4, ... of the CTA, a quarter of the members at a time.
+// Warp q of it has features 32 q .. + 31 to itself: it adds the products, a feature
+// a lane, to y in shared memory, and writes the sums from there, 16 bytes a lane and
+// 128 of a row.  (Whole rows to a warp needed a barrier of the group per quarter.)
 template <int R>
 __device__ void up_epilogue(const Ctx& c, const Args& g, UpWalk walk, uint32_t tmem, uint8_t* smem) {
   constexpr int S = kYSlots;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = warp & 3, e = warp >> 2;
-  uint8_t* ring = smem + Up<R>::kYOff + e * S * kYSlot;
+  uint8_t* ring = smem + Up<R>::kYOff + e * S * kYSlot + 32 * q * 4;
   uint32_t parity = 0;
-  int k = 0, my_row = 0;  // member q + 4 lane (lanes 0 .. 15)
+  int k = 0, row_lo = 0, row_hi = 0;  // members lane and lane + 32
   for (int i = 0; walk.next(); ++i) {
-    if (walk.fresh && lane < 16 && q + 4 * lane < walk.count)
-      my_row = walk.tiles.order[walk.first + q + 4 * lane];
+    if (walk.fresh) {
+      if (lane < walk.count) row_lo = walk.tiles.order[walk.first + lane];
+      if (lane + 32 < walk.count) row_hi = walk.tiles.order[walk.first + lane + 32];
+    }
     if (i % kGroups != e) continue;
     const int count = walk.count;
     const bool product = walk.id >= 0, write = product || g.out != g.y;
+    const long long f = walk.f0 + 32 * q + 4 * (lane & 7);
     for (int m0 = 0; m0 < count; m0 += 16, ++k) {
       uint8_t* slot = ring + (k % S) * kYSlot;
-      bool ok = wait_warp(c, kYFull0 + e * S + k % S, (k / S) & 1);
       if (product) {
+        float d[16];
         if (m0 == 0) {
-          ok = ok && wait_warp(c, kUDFull0 + e, parity);
+          if (!wait_warp(c, kUDFull0 + e, parity)) return;
           parity ^= 1u;
-        }
-        if (ok) {
           umma::fence_after_sync();
-          float d[16];
-          umma::ld_32x32b_x16(tmem + ((uint32_t)(q * 32) << 16) + e * kTile + m0, d);
-          umma::wait_ld();
-          if (m0 + 16 >= count) {
-            umma::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_at(c, kUDEmpty0 + e));
-          }
-          float* yv = reinterpret_cast<float*>(slot) + 32 * q + lane;
-#pragma unroll
-          for (int m = 0; m < 16; ++m) yv[m * kFeat] += d[m];  // past count: leftovers, not stored
         }
+        umma::ld_32x32b_x16(tmem + ((uint32_t)(q * 32) << 16) + e * kTile + m0, d);
+        umma::wait_ld();
+        if (m0 + 16 >= count) {
+          umma::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_at(c, kUDEmpty0 + e));
+        }
+        if (!wait_warp(c, kYFull0 + e * S + k % S, (k / S) & 1)) return;
+        float* yv = reinterpret_cast<float*>(slot) + lane;
+#pragma unroll
+        for (int m = 0; m < 16; ++m) yv[m * kFeat] += d[m];  // past count: leftovers, not stored
+        __syncwarp();
+      } else if (!wait_warp(c, kYFull0 + e * S + k % S, (k / S) & 1)) {
+        return;
       }
-      // the group's four warps meet, or leave together
-      if (named_bar_or(1 + e, 128, !ok)) return;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int m = q + 4 * j;
-        const int row = __shfl_sync(kFull, my_row, (m0 >> 2) + j);
+        const int m = 4 * j + (lane >> 3);
+        const int row = __shfl_sync(kFull, m0 < 32 ? row_lo : row_hi, (m0 + m) & 31);
         if (m0 + m >= count) continue;
-        const float4 v = *reinterpret_cast<const float4*>(slot + m * kYRow + 16 * lane);
-        const long long at = (long long)row * g.N + walk.f0 + 4 * lane;
+        const float4 v = *reinterpret_cast<const float4*>(slot + m * kYRow + 16 * (lane & 7));
+        const long long at = (long long)row * g.N + f;
         if (write) *reinterpret_cast<float4*>(g.out + at) = v;
         if (g.out_bf16)
           *reinterpret_cast<uint2*>(g.out_bf16 + at) =
