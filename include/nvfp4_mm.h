@@ -97,6 +97,7 @@ int nvfp4_mm_read_error(void* ws, int32_t* code, void* stream);
 /* ---- low-rank adapters of many requests ------------------------------- */
 
 #define NVFP4_ADAPTER_MAX_RANK 128
+#define NVFP4_ADAPTER_MAX_K (1 << 22)
 
 /* Device workspace bytes of one nvfp4_mm_adapters call (0: shape not
  * supported): a 256-byte header and the fp32 products t.  Needs no
@@ -114,7 +115,8 @@ size_t nvfp4_mm_adapters_workspace_bytes(int32_t n, int32_t N, int32_t K, int32_
  * sums run on the tensor cores with fp32 accumulation over exact products: t
  * enters the second one as three bf16 terms that hold its 24 bits.  Orders are
  * fixed by K and the rank alone, so a row's bits depend only on its own x, y
- * and adapter, not on n, on its place or on the other rows.
+ * and adapter, not on n, on its place or on the other rows.  A t that overflows
+ * bf16's range is an infinity; where B is infinite out is an infinity or NaN.
  *   x       [n, K], fp32 or bf16 as x_dtype (NVFP4_X_*) says, 16-byte aligned.
  *   a       bf16 [n_adapters, max_rank, K], b  bf16 [n_adapters, N, max_rank],
  *           16-byte aligned.
@@ -123,16 +125,16 @@ size_t nvfp4_mm_adapters_workspace_bytes(int32_t n, int32_t N, int32_t K, int32_
  *   scales  fp32 [n_adapters] or NULL (all 1).
  *   ids     int32 [n].
  *   y, out  fp32 [n, N], 16-byte aligned; out may be y (rows without an adapter
- *           are then not touched) but must not overlap it otherwise.
+ *           are then not touched).
  *   out_bf16  bf16 [n, N] or NULL, 16-byte aligned: out rounded to nearest even,
- *           all rows.
+ *           all rows.  Otherwise out and out_bf16 overlap no other argument.
  *   ws      as for nvfp4_mm.
  * An id at or above n_adapters counts as none and sets DA_DEVERR_INDEX, a rank
  * outside [0, max_rank] is clamped and sets DA_DEVERR_LENGTH; read the bits of
  * the last call with nvfp4_mm_read_error(ws, ...).
  * Supported shapes: n >= 0, N a positive multiple of NVFP4_MM_TILE_N, K a
- * positive multiple of 64, max_rank a multiple of 16 up to
- * NVFP4_ADAPTER_MAX_RANK, n_adapters >= 1; n * K, n * N below 2^31. */
+ * positive multiple of 64 up to NVFP4_ADAPTER_MAX_K, max_rank a multiple of 16
+ * up to NVFP4_ADAPTER_MAX_RANK, n_adapters >= 1; n * K, n * N below 2^31. */
 int nvfp4_mm_adapters(const void* x, int32_t x_dtype, int32_t n, int32_t N, int32_t K,
                       const void* a, const void* b, int32_t n_adapters, int32_t max_rank,
                       const int32_t* ranks, const float* scales, const int32_t* ids,
@@ -141,9 +143,12 @@ int nvfp4_mm_adapters(const void* x, int32_t x_dtype, int32_t n, int32_t N, int3
 
 /* ---- logits ------------------------------------------------------------ */
 
+/* Entries of a row's bias list at most: each of its tokens is looked for in it. */
+#define NVFP4_LOGITS_MAX_BIAS 4096
+
 /* What a decode step does to the logits of its vocabulary projection (nvfp4_mm's
  * y or y_bf16).  Plain data; a NULL list is an empty one; the three widths add
- * up to 2^30 at most. */
+ * up to less than 2^29. */
 typedef struct nvfp4_logits {
   int32_t batch;             /* B >= 0 rows                                    */
   int32_t vocab;             /* V tokens, 1 .. 2^30                              */
@@ -162,7 +167,7 @@ typedef struct nvfp4_logits {
   const int32_t* bias_tokens; /* int32 [B, bias_width]                         */
   const float* bias_values;  /* fp32 [B, bias_width]                           */
   const int32_t* bias_lens;  /* int32 [B]                                      */
-  int32_t bias_width;
+  int32_t bias_width;        /* <= NVFP4_LOGITS_MAX_BIAS                       */
   const uint32_t* mask;      /* [n_masks, ceil(V / 32)]: bit v % 32 of word    */
                              /* v / 32 set: token v may come                   */
   const int32_t* mask_ids;   /* int32 [B]: the row's mask, negative: none;     */
@@ -186,7 +191,7 @@ typedef struct nvfp4_logits {
  *                 there is none (every token masked, or -inf or NaN)
  *
  * A row's results depend on that row alone.  out may be x itself (fp32, same
- * stride); any other overlap is not allowed.  List entries at or past a row's
+ * stride); otherwise out and tokens overlap no other argument.  List entries at or past a row's
  * length are never read.  A length below 0 or above its width is clamped and
  * sets DA_DEVERR_LENGTH; a token outside [0, V) is skipped and a mask id at or
  * above n_masks counts as none, both set DA_DEVERR_INDEX.  Bits are OR-ed into

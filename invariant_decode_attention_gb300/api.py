@@ -46,7 +46,7 @@ NVFP4_X_F32, NVFP4_X_BF16 = 0, 1
 
 # Cache append (include/decode_attn.h) and adapters (include/nvfp4_mm.h)
 X_F32, X_BF16 = 0, 1
-ADAPTER_MAX_RANK = 128
+ADAPTER_MAX_RANK, ADAPTER_MAX_K, LOGITS_MAX_BIAS = 128, 1 << 22, 4096
 
 # Size of the fixed device array decode_attn_forward_static uses as scratch.
 STATIC_WORKSPACE_BYTES = 64 << 20
@@ -540,9 +540,9 @@ def run_nvfp4(m, ws=None, y=None, y_bf16=None, stream=None):
 # These calls sit between small kernels of a decode step, so their host time
 # counts: arguments are checked with few attribute reads (the reason for a
 # refusal is looked for only once there is one), descriptors are packed in one
-# go, and the stream comes as a raw handle.  Measured on the GPU host, append of
+# go, and the stream comes as a raw handle.  Measured on a Grace host, append of
 # one token: 15.6 us a call with a ctypes field per argument and
-# torch.cuda.current_stream(), see _APPEND below for the packed form.
+# torch.cuda.current_stream(), 9.3 us like this, 2.0 us of it the C call.
 
 _X_DTYPES = {torch.float32: X_F32, torch.bfloat16: X_BF16}
 _I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
@@ -578,6 +578,15 @@ def _addr(t, name, dev, dtype, shape=None):
             and t.is_contiguous()):
         return t.data_ptr()
     _refuse(t, name, dev, dtype, shape)
+
+
+def _make(shape, dtype, device, stream):
+    """A tensor that a call on `stream` fills: from that stream's memory, so that
+    nothing else is still using it, and nothing gets it before the call is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _call(fn, where, dev, stream, *args):
@@ -680,7 +689,7 @@ def append(prob: DaProblem, rope, k_new, v_new, k, v, positions, *, rows=None, t
         shape = (n, prob.num_q_heads, D)
         q_ptr, q_stride = _heads(q_new, "q_new", dev, dtype, shape)
         if q_out is None:
-            q_out = torch.empty(shape, dtype=_BF16, device=k_new.device)
+            q_out = _make(shape, _BF16, k_new.device, stream)
         qo_ptr = _addr(q_out, "q_out", dev, _BF16, shape)
     elif q_out is not None:
         raise ValueError("q_out without q_new")
@@ -691,8 +700,9 @@ def append(prob: DaProblem, rope, k_new, v_new, k, v, positions, *, rows=None, t
         t_ptr = _addr(table, "table", dev, _I32, (prob.batch, prob.width))
     rope_ptr = None
     if rope is not None:
-        if rope.keep.get_device() != dev:
-            raise ValueError(f"inv_freq is on {rope.keep.device}, expected {_where(dev)}")
+        keep = getattr(rope, "keep", None)  # not there when filled in by hand
+        if keep is not None and keep.get_device() != dev:
+            raise ValueError(f"inv_freq is on {keep.device}, expected {_where(dev)}")
         rope_ptr = ctypes.addressof(rope)
     args = _APPEND.pack(n, x_dtype, k_ptr, v_ptr, q_ptr, k_stride, v_stride, q_stride,
                         _addr(positions, "positions", dev, _I32, (n,)),
@@ -725,12 +735,12 @@ def adapters_workspace_bytes(n: int, N: int, K: int, count: int, max_rank: int) 
     return int(lib().nvfp4_mm_adapters_workspace_bytes(n, N, K, count, max_rank))
 
 
-def adapters_workspace(n: int, N: int, K: int, adapters: Adapters) -> torch.Tensor:
+def adapters_workspace(n: int, N: int, K: int, adapters: Adapters, stream=None) -> torch.Tensor:
     nb = adapters_workspace_bytes(n, N, K, adapters.count, adapters.max_rank)
     if nb == 0:
         raise DecodeAttnError(ERR_UNSUPPORTED, f"adapters shape n={n} N={N} K={K} "
                               f"max_rank={adapters.max_rank}")
-    return torch.empty(nb, dtype=torch.uint8, device=adapters.a.device)
+    return _make((nb,), torch.uint8, adapters.a.device, stream)
 
 
 def nvfp4_adapters(x, adapters: Adapters, ids, y, *, out=None, out_bf16=None, ws=None, stream=None):
@@ -751,7 +761,7 @@ def nvfp4_adapters(x, adapters: Adapters, ids, y, *, out=None, out_bf16=None, ws
     if out is None:
         out = y
     if ws is None:
-        ws = adapters_workspace(n, N, K, adapters)
+        ws = adapters_workspace(n, N, K, adapters, stream)
     shape = (n, N)
     _call(lib().nvfp4_mm_adapters, "nvfp4_adapters", dev, stream, _addr(x, "x", dev, dtype), x_dtype,
           n, N, K, *adapters.ptrs, _addr(ids, "ids", dev, _I32, (n,)), _addr(y, "y", dev, _F32, shape),
@@ -801,7 +811,7 @@ def nvfp4_logits(x, *, prompt=None, prompt_lens=None, output=None, output_lens=N
     if x_dtype is None:
         raise ValueError(f"x must be float32 or bfloat16, got {dtype}")
     if tokens is None:
-        tokens = torch.empty(B, dtype=_I32, device=x.device)
+        tokens = _make((B,), _I32, x.device, stream)
     row = (B,)
     if (bias_values is None) != (bias_tokens is None):
         raise ValueError("bias_tokens and bias_values belong together")

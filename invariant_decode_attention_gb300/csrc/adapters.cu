@@ -29,8 +29,9 @@
 // producer warps bring operands into a ring of stages with 16-byte cp.async (rows
 // may lie anywhere, and a copy may end inside 16 bytes, zeros beyond: what memory
 // holds past an adapter's rank is never multiplied) in the 128-byte-swizzled
-// K-major layout, whose landing arrives on the stage's barrier by itself; two threads issue the MMAs (one alone took 80 cycles an MMA and
-// set the pace); epilogue warps drain accumulators.  Every wait is bounded; on
+// K-major layout, whose landing arrives on the stage's barrier by itself; two
+// threads issue the MMAs (one alone took 80 cycles an MMA and set the pace);
+// epilogue warps drain accumulators.  Every wait is bounded; on
 // time-out the kernel records DA_DEVERR_TIMEOUT, all roles leave their loops,
 // copies and tensor-core work are drained and tensor memory is freed.
 //
@@ -609,8 +610,11 @@ __global__ void __launch_bounds__(kDownThreads, 1) down_kernel(const Args g) {
     } else {
       const int index = __syncthreads_or(bad & DA_DEVERR_INDEX);
       const int length = __syncthreads_or(bad & DA_DEVERR_LENGTH);
-      if (threadIdx.x == 0)
-        g.hdr[kHdrError] = (index ? DA_DEVERR_INDEX : 0) | (length ? DA_DEVERR_LENGTH : 0);
+      if (threadIdx.x == 0) {  // a later slab keeps what the earlier ones recorded
+        const int found = (index ? DA_DEVERR_INDEX : 0) | (length ? DA_DEVERR_LENGTH : 0);
+        if (g.first) g.hdr[kHdrError] = found;
+        else if (found) set_error(g.hdr, found);
+      }
     }
   }
   umma::fence_before_sync();
@@ -1006,17 +1010,20 @@ __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
     abort_word = 0;
     fence_mbar_init();
   }
-  if (warp == kUpMmaWarp0) {
-    umma::tmem_alloc(smem_addr(&tmem_slot), kUpCols);
-    umma::tmem_relinquish();
-  }
-  umma::fence_before_sync();
   // one window: the plan needs ids and ranks only, which were complete before the
   // down kernel let this one start
   if (g.windows > 1) wait_prior_grid();
   const Tiles tiles = get_tiles(g, start, own);  // holds CTA barriers
   if (g.windows == 1) wait_prior_grid();
   allow_next_grid();
+  // not before the wait: a CTA that holds tensor memory waits for no other kernel,
+  // so kernels of two streams cannot wait for one another's
+  if (warp == kUpMmaWarp0) {
+    umma::tmem_alloc(smem_addr(&tmem_slot), kUpCols);
+    umma::tmem_relinquish();
+  }
+  umma::fence_before_sync();
+  __syncthreads();
   umma::fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
   const int blocks = g.N / kFeat;
@@ -1067,11 +1074,17 @@ size_t round_up(size_t v, size_t m) { return (v + m - 1) / m * m; }
 
 bool shape_ok(int n, int N, int K, int n_adapters, int max_rank) {
   if (n < 0 || N <= 0 || K <= 0 || N % NVFP4_MM_TILE_N || K % 64) return false;
+  if (K > NVFP4_ADAPTER_MAX_K) return false;
   if (n_adapters < 1 || max_rank < 16 || max_rank > kMaxRank || max_rank % 16) return false;
   return (long long)n * K < (1ll << 31) && (long long)n * N < (1ll << 31);
 }
 
 bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return p < q + b_bytes && q < p + a_bytes;
+}
 
 int chunks_of(int K) { return (K + kKChunk - 1) / kKChunk; }
 
@@ -1141,9 +1154,12 @@ int nvfp4_mm_adapters(const void* x, int32_t x_dtype, int32_t n, int32_t N, int3
       !aligned_to(out, 16) || !aligned_to(out_bf16, 16) || !aligned_to(ids, 4) ||
       !aligned_to(ranks, 4) || !aligned_to(scales, 4))
     return DA_ERR_INVALID_ARG;
-  const uintptr_t y0 = reinterpret_cast<uintptr_t>(y), o0 = reinterpret_cast<uintptr_t>(out);
-  const uintptr_t bytes = (uintptr_t)n * N * 4;
-  if (y0 != o0 && y0 < o0 + bytes && o0 < y0 + bytes) return DA_ERR_INVALID_ARG;
+  const size_t x_bytes = (size_t)n * K * (x_dtype == NVFP4_X_BF16 ? 2 : 4);
+  const size_t y_bytes = (size_t)n * N * 4, ob_bytes = out_bf16 ? y_bytes / 2 : 0;
+  if ((y != out && overlap(y, y_bytes, out, y_bytes)) || overlap(x, x_bytes, out, y_bytes) ||
+      overlap(x, x_bytes, out_bf16, ob_bytes) || overlap(y, y_bytes, out_bf16, ob_bytes) ||
+      overlap(out, y_bytes, out_bf16, ob_bytes))
+    return DA_ERR_INVALID_ARG;
   if (!ws || !aligned_to(ws, 256)) return DA_ERR_WORKSPACE;
   if (ws_bytes < nvfp4_mm_adapters_workspace_bytes(n, N, K, n_adapters, max_rank))
     return DA_ERR_WORKSPACE;

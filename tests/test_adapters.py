@@ -194,6 +194,41 @@ def test_error_bits(api):
 
 
 @gpu
+def test_more_rows_than_a_slab(api):
+    # two sets of launches, the second of one window: it keeps the first one's errors
+    slab = 1 << 18
+    n = slab + 300
+    ids = np.full(n, -1)
+    ids[[0, 700, 70000, slab - 1, slab, slab + 40, n - 1]] = [0, 1, 0, 1, 1, 0, 1]
+    ids[5] = 2  # there is none
+    c = Case(api, n, 128, 64, 2, 16, ids=ids, ranks=None, seed=31)
+    ws = api.adapters_workspace(n, 128, 64, c.handle)
+    out = c.run(ws=ws)
+    assert api.nvfp4_read_error(ws) == api.DEVERR_INDEX
+    rows = np.flatnonzero((ids == 0) | (ids == 1))
+    c.check(out[torch.as_tensor(rows, device="cuda")], rows)
+    assert torch.equal(c.run(rows), out[torch.as_tensor(rows, device="cuda")])
+    others = torch.as_tensor((ids < 0) | (ids == 2))
+    assert torch.equal(out.cpu()[others], c.y[others])
+
+
+@gpu
+def test_own_memory_on_another_stream(api):
+    # workspaces made by the call belong to its stream: calls in a row on two
+    # streams, without waiting for one another
+    c = Case(api, 90, 256, 1088, 6, 64, seed=18)
+    want = c.run()
+    x, ids, y = c.x.cuda(), c.ids.cuda(), c.y.cuda()
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.zeros_like(y) for _ in range(12)]
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        api.nvfp4_adapters(x, c.handle, ids, y, out=out, stream=sides[i % 2])
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, want) for out in outs)
+
+
+@gpu
 def test_repeats_stream_and_graph(api):
     c = Case(api, 90, 384, 1088, 6, 64, seed=17)
     ws = api.adapters_workspace(90, 384, 1088, c.handle)
@@ -242,7 +277,8 @@ def test_argument_rules(api):
     assert size(4, 128, 1088, 3, 64) == 6 * 256 + 2 * 4 * 64 * 4
     assert size(1 << 19, 128, 64, 1, 16) == size(1 << 18, 128, 64, 1, 16)  # rows in slabs
     for shape in ((-1, 128, 64, 1, 16), (1, 100, 64, 1, 16), (1, 128, 96, 1, 16), (1, 128, 64, 0, 16),
-                  (1, 128, 64, 1, 8), (1, 128, 64, 1, 144), (1, 128, 64, 1, 24), (1 << 20, 128, 2048, 1, 16)):
+                  (1, 128, 64, 1, 8), (1, 128, 64, 1, 144), (1, 128, 64, 1, 24), (1 << 20, 128, 2048, 1, 16),
+                  (1, 128, api.ADAPTER_MAX_K + 64, 1, 16)):
         assert size(*shape) == 0, shape
 
     def call(x=fake, xd=0, n=4, N=128, K=64, a=fake, b=fake, count=2, rank=16, ranks=fake, scales=fake,
@@ -262,6 +298,9 @@ def test_argument_rules(api):
         assert call(**{name: fake + 2}) == bad, name
     assert call(ob=fake + 8) == bad
     assert call(out=(1 << 24) + 512) == bad  # overlaps y
+    assert call(out=fake) == bad and call(ob=fake) == bad                       # over x
+    assert call(ob=1 << 24) == bad and call(ob=(1 << 28) + 1024) == bad         # over y, over out
+    assert call(xd=1, ob=fake + 512, wsb=0) == api.ERR_WORKSPACE                # just behind x
     assert call(ws=None) == api.ERR_WORKSPACE
     assert call(ws=fake + 16) == api.ERR_WORKSPACE
     assert call(wsb=100) == api.ERR_WORKSPACE
