@@ -374,7 +374,8 @@ typedef struct da_append {
  * values.  A token's stored bytes and its q_out row depend on that token alone.
  *
  * Alignment: the five data pointers 16 bytes, strides multiples of 16 bytes.
- * q_out must not overlap q_new.  One launch, no workspace. */
+ * Neither q_out nor the caches may overlap the new tokens.  One launch, no
+ * workspace. */
 int decode_attn_append(const da_problem* prob, const da_rope* rope, const da_append* args,
                        void* stream);
 

@@ -538,10 +538,12 @@ int decode_attn_append(const da_problem* prob, const da_rope* rope, const da_app
     if (strides[i] < least[i] || strides[i] > (1LL << 40)) return DA_ERR_INVALID_ARG;
     if (strides[i] * esize % 16) return DA_ERR_INVALID_ARG;
   }
-  if (a.q_new) {  // other threads read what a rotated element's thread writes
-    const uintptr_t src = reinterpret_cast<uintptr_t>(a.q_new);
+  const void* source[3] = {a.k_new, a.v_new, a.q_new};
+  for (int i = 0; i < 3 && a.q_out; ++i) {  // other threads read what q_out's threads write
+    if (!source[i]) continue;
+    const uintptr_t src = reinterpret_cast<uintptr_t>(source[i]);
     const uintptr_t dst = reinterpret_cast<uintptr_t>(a.q_out);
-    const uintptr_t src_end = src + ((n - 1) * a.q_stride + q_row) * esize;
+    const uintptr_t src_end = src + ((n - 1) * strides[i] + least[i]) * esize;
     if (dst < src_end && src < dst + n * q_row * 2) return DA_ERR_INVALID_ARG;
   }
   int dev = 0;

@@ -534,8 +534,9 @@ extern "C" int nvfp4_mm_logits(const nvfp4_logits* g, void* stream) {
                           g->mask,       g->mask_ids,  g->tokens,   g->err};
   for (const void* w : words)
     if (!aligned_to(w, 4)) return DA_ERR_INVALID_ARG;
-  if ((long long)g->prompt_width + g->output_width + g->bias_width > kMaxVocab)
-    return DA_ERR_UNSUPPORTED;
+  if (g->bias_width > NVFP4_LOGITS_MAX_BIAS ||
+      (long long)g->prompt_width + g->output_width + g->bias_width > Word<uint32_t>::kMostOutput)
+    return DA_ERR_UNSUPPORTED;  // (the count of a token in the output has 29 bits)
   if (g->out) {  // in place row for row, or apart
     const uintptr_t x = reinterpret_cast<uintptr_t>(g->x);
     const uintptr_t o = reinterpret_cast<uintptr_t>(g->out);

@@ -387,6 +387,23 @@ def test_other_stream_and_graph(api):
 
 
 @gpu
+def test_a_rotation_described_by_hand(api):
+    # da_rope is plain data: filled in field by field it does what rope() gives
+    prob = api.problem(batch=3, num_q_heads=4, num_kv_heads=2, head_dim_qk=64, layout="contiguous",
+                       scale=0.1, width=8)
+    k_new = torch.randn((3, 2, 64), device="cuda")
+    freq = torch.rand(32, device="cuda")
+    at = torch.tensor([5, 0, 7], dtype=torch.int32, device="cuda")
+    got = []
+    for rope in (api.rope(freq), api.DaRope(64, 0, 0, 1.0, freq.data_ptr())):
+        k, v = (torch.zeros((3, 8, 2, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        api.append(prob, rope, k_new, k_new, k, v, at)
+        got.append((k, v))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert got[0][0].any()
+
+
+@gpu
 def test_no_tokens(api):
     c = Case(api, n=3, rope=(128, 0, False))
     q = api.append(c.prob, c.rope, c.k_new[:0], c.v_new[:0], c.k, c.v, c.i32(c.pos)[:0],
@@ -444,6 +461,8 @@ def test_argument_rules(api):
     assert call(rows=None, n_tokens=5) == bad              # more tokens than rows
     assert call(q_out=fake) == bad                         # over its input
     assert call(q_out=fake + 2 * (3 * 1536 + 512)) == bad  # the input's last 1024 bytes
+    for name in ("k_new", "v_new"):                        # over the other inputs
+        assert call(**{name: (1 << 30) + 4096}) == bad, name
     for r in (dict(dim=8), dict(dim=-16), dict(offset=4), dict(offset=-8), dict(offset=8),
               dict(dim=144), dict(interleaved=2), dict(gain=float("nan")), dict(inv_freq=None),
               dict(inv_freq=fake + 1)):

@@ -167,6 +167,21 @@ def test_repeated_bias_tokens_add_up_in_order(api):
 
 
 @gpu
+def test_the_longest_bias_list(api):
+    V, W = 9000, api.LOGITS_MAX_BIAS
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn((2, V), generator=g)
+    at = torch.stack([torch.randperm(V, generator=g)[:W] for _ in range(2)]).to(torch.int32)
+    v = torch.randn((2, W), generator=g)
+    want = x.scatter_add(1, at.long(), v)  # distinct tokens: one addition each
+    out = torch.empty((2, V), device="cuda")
+    tokens = api.nvfp4_logits(x.cuda(), bias_tokens=at.cuda(), bias_values=v.cuda(), out=out,
+                              bias_lens=torch.full((2,), W, dtype=torch.int32, device="cuda"))
+    assert torch.equal(out.cpu(), want)
+    assert torch.equal(tokens.cpu().long(), want.argmax(1))
+
+
+@gpu
 def test_greedy_ties_masks_infinities_and_nan(api):
     nan, inf = float("nan"), float("inf")
     V = 9000  # several CTAs a row
@@ -322,6 +337,10 @@ def test_argument_rules(api):
         assert call(**{name: fake + 1, name + "_lens": fake, name + "_width": 4}) == bad
     assert call(bias_tokens=fake, bias_lens=fake, bias_width=3) == bad
     assert call(bias_values=fake, bias_width=3) == bad
+    wide = dict(bias_tokens=fake, bias_values=fake, bias_lens=fake)
+    assert call(**wide, bias_width=api.LOGITS_MAX_BIAS + 1) == api.ERR_UNSUPPORTED
+    wide = dict(prompt=fake, prompt_lens=fake, prompt_width=1 << 28, output=fake, output_lens=fake)
+    assert call(**wide, output_width=1 << 28) == api.ERR_UNSUPPORTED
     assert call(mask=fake, n_masks=0, mask_ids=fake) == bad
     assert call(mask=fake, n_masks=1) == bad           # two rows, no ids
     assert call(mask_ids=fake) == bad
