@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(X) == 2 ? 7 : 5)
     append_kernel(const AppendLaunch p, int parts, int per_part) {
   constexpr int kUnits = D / 16;                // units of a head
   constexpr int kBatch = kInFlight<X>;
-  constexpr bool kBlocks = KT == DA_KV_NVFP4;   // a unit is always a block of 16
+  constexpr bool kBlocks = KT == DA_KV_NVFP4;   // a unit of the cache is always a block of 16
   // gain * (cos, sin) of the token's angles, for each warp: pairs 2i and 2i + 1
   // of group c (eight pairs) at [i * groups + c], so that neighbouring lanes,
   // which hold neighbouring groups, read neighbouring 16 bytes
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(X) == 2 ? 7 : 5)
   // A unit is two chunks of a head: the two that a rotation of halves mixes, or
   // neighbours.  Its chunks' numbers within the head:
   auto chunks_of = [&](int head, int i, int* c0, int* c1) {
-    if (kBlocks || !halves || head >= hk) {
+    if (!halves || head >= (kBlocks ? hq : hk)) {
       *c0 = 2 * i;
       *c1 = 2 * i + 1;
     } else if (i < groups) {
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(X) == 2 ? 7 : 5)
           const int r0 = c0 - skip, r1 = c1 - skip;  // pairs 4 r .. 4 r + 3: half a group
           if (r0 >= 0 && r0 < 2 * groups) turn_pairs(a, turn + (r0 & 1) * 2 * groups + (r0 >> 1), groups);
           if (r1 >= 0 && r1 < 2 * groups) turn_pairs(b, turn + (r1 & 1) * 2 * groups + (r1 >> 1), groups);
-        } else if (!kBlocks) {
+        } else if (!kBlocks || head < hq) {
           if (i < groups) turn_halves(a, b, turn + i, groups);
         } else {
           // a block's chunks have their partners elsewhere: they are read again
