@@ -219,7 +219,7 @@ template <bool BF16, int VEC, typename W>
 __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const Args a) {
   constexpr int kElem = BF16 ? 2 : 4;
   constexpr int kStep = kThreads * VEC;     // tokens of a step of the CTA
-  constexpr int kDepth = VEC == 4 ? 4 : 8;  // steps whose logits are on their way
+  constexpr int kDepth = 4;                 // steps whose logits are on their way
   extern __shared__ __align__(16) uint8_t smem[];
   W* table = reinterpret_cast<W*>(smem);  // [slice]; all zero between slices
   __shared__ uint16_t listed[kListed];  // tokens of the slice that have a word
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const Args a) {
       for (int s0 = (tid & ~31) * kWords; s0 < count; s0 += kThreads * kWords) {  // whole warps
         const int s = s0 + lane * kWords;
         W w[kWords] = {};
-        if (s < count)  // the table goes on past count, with zeros, to a multiple of 32
+        if (s < count)  // the table goes on past count, with zeros, to a whole step
           *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(table + s);
         int mine = 0;
 #pragma unroll
@@ -378,11 +378,24 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const Args a) {
         }
       }
     }
-    for (int s = full * kStep + tid; s < count; s += kThreads) {  // what is left: one by one
-      float l = load_x(x, v0 + s, BF16);
-      if (mask && !((__ldg(mask + ((v0 + s) >> 5)) >> ((v0 + s) & 31)) & 1u)) l = -INFINITY;
-      if (out) out[v0 + s] = l;
-      if (!table[s]) best_key = max64(best_key, key_of(l, v0 + s));
+    if (full * kStep < count) {  // what is left (the row's last tokens): one by one
+      const int s0 = full * kStep + tid;
+      float l[VEC];
+      uint32_t bits[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const int v = v0 + min(s0 + e * kThreads, count - 1);
+        l[e] = load_x(x, v, BF16);
+        bits[e] = mask ? __ldg(mask + (v >> 5)) : 0xffffffffu;
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const int s = s0 + e * kThreads;
+        if (s >= count) break;
+        if (!((bits[e] >> ((v0 + s) & 31)) & 1u)) l[e] = -INFINITY;
+        if (out) out[v0 + s] = l[e];
+        if (!table[s]) best_key = max64(best_key, key_of(l[e], v0 + s));
+      }
     }
     if (r0 + span < a.V) load_first(v0 + span);
     __syncthreads();  // the listed tokens' plain values are written
@@ -473,11 +486,14 @@ template <bool BF16, int VEC, typename W>
 cudaError_t launch_logits(Args& a, int B, int sms, cudaStream_t stream) {
   // Every CTA of a row goes through its lists, so there are no more of them than
   // fill the GPU twice over (two CTAs per SM run at once); slices are of equal
-  // length, a multiple of 32, so that they start on mask words.
+  // length, a multiple of the steps of a CTA, so that only a row's last one ends
+  // inside a step.
   int ranks = 1;
-  while (ranks < kCluster && 2LL * ranks * B <= 2LL * sms && ranks * kThreads * 4 < a.V) ranks *= 2;
+  while (ranks < kCluster && (long long)ranks * B <= sms && ranks * kThreads * 4 < a.V) ranks *= 2;
   const long long rounds = (a.V + ranks * Word<W>::kSlice - 1) / (ranks * Word<W>::kSlice);
-  a.slice = (int)(((a.V + ranks * rounds - 1) / (ranks * rounds) + 31) / 32 * 32);
+  constexpr int kStep = kThreads * VEC;
+  static_assert(Word<W>::kSlice % kStep == 0, "a slice may be whole steps");
+  a.slice = (int)(((a.V + ranks * rounds - 1) / (ranks * rounds) + kStep - 1) / kStep * kStep);
   const size_t bytes = (size_t)a.slice * sizeof(W);
   if (bytes > kPlainBytes) {  // beyond what needs no consent; it holds per device
     const cudaError_t e = cudaFuncSetAttribute(
