@@ -29,6 +29,9 @@ constexpr int kMaxPairs = 288;  // rope_dim / 2 at most (576 / 2)
 // on 16384 tokens of 32/8 heads: one 75, two 70, three 67 us).
 template <typename X>
 constexpr int kInFlight = sizeof(X) == 2 ? 3 : 2;
+// CTAs that an SM holds at once (72 and 96 registers a thread).
+template <typename X>
+constexpr int kResident = sizeof(X) == 2 ? 7 : 5;
 
 template <typename X>
 struct Chunk;  // eight elements as loaded
@@ -148,7 +151,7 @@ __device__ __forceinline__ void turn_halves(float (&a)[8], float (&b)[8], const 
 // Warp w of the grid takes part w % parts of token w / parts: units [part *
 // per_part, + per_part) of the token's heads q, k, v, 32 * kBatch at a time.
 template <typename X, int KT, int D>
-__global__ void __launch_bounds__(kWarps * 32, sizeof(X) == 2 ? 7 : 5)
+__global__ void __launch_bounds__(kWarps * 32, kResident<X>)
     append_kernel(const AppendLaunch p, int parts, int per_part) {
   constexpr int kUnits = D / 16;                // units of a head
   constexpr int kBatch = kInFlight<X>;
@@ -315,9 +318,11 @@ template <typename X, int KT, int D>
 cudaError_t launch_dim(const AppendLaunch& p, int sms, cudaStream_t stream) {
   const int units = (D / 16) * ((p.q_new ? p.H_q : 0) + p.H_kv * (p.v_new ? 2 : 1));
   // a warp takes a whole token once there are enough of them; fewer tokens are
-  // cut, down to one unit a lane, so that all SMs have work (64 tokens of 128
-  // heads of 576: 5.2 us with 32 warps per SM, 7.3 with 64)
-  const long long want = 32LL * sms;  // warps
+  // cut, down to one unit a lane, so that all SMs have work, into no more parts than
+  // the GPU holds at once (64 tokens of 128 heads of 576: 5.3 us with these 28 warps
+  // per SM, 6.4 with 32, 7.8 with 64; 2047 tokens of 32/8 heads into NVFP4: 16.1,
+  // 16.1 and 19.5, with 20 warps 19.6)
+  const long long want = (long long)kResident<X> * kWarps * sms;  // warps
   long long parts = std::max<long long>(1, want / p.n_tokens);
   parts = std::min<long long>(parts, (units + 31) / 32);
   const int per_part = (int)(((units + parts - 1) / parts + 31) / 32 * 32);
