@@ -114,17 +114,52 @@ struct Window {
   int pos[kWindow], leader[kWindow], before[kLines + 1];
 };
 
-// Rows r0 .. r0 + count - 1, by all threads of the CTA; returns the tiles.
-__device__ int make_plan(const Args& g, int r0, int count, Window& s) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  for (int i = threadIdx.x; i < kWindow; i += blockDim.x) {
-    int v = -2;  // no row, or one that nothing is done for
-    if (i < count) {
-      v = __ldg(g.ids + r0 + i);
-      if (v < 0 || v >= g.n_adapters || rank_of(g, v) == 0) v = g.copy ? -1 : -2;
-    }
-    s.id[i] = v;
+// What the plan takes row i for: its adapter, -1 for a row that is only copied, -2
+// for one that nothing is done for.  *bad gets the error bits.
+__device__ __forceinline__ int planned_id(const Args& g, int i, int* bad) {
+  const int v = __ldg(g.ids + i);
+  int rank = 0;
+  if (v >= g.n_adapters) {
+    *bad |= DA_DEVERR_INDEX;
+  } else if (v >= 0) {
+    rank = rank_of(g, v);
+    if (g.ranks && __ldg(g.ranks + v) != rank) *bad |= DA_DEVERR_LENGTH;
   }
+  return rank ? v : g.copy ? -1 : -2;
+}
+
+// Rows r0 .. r0 + count - 1, by all threads of the CTA; returns the tiles.  *bad gets
+// the error bits of the rows that this thread has looked at.
+__device__ int make_plan(const Args& g, int r0, int count, Window& s, int* bad) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  if (count <= 32) {  // a decode step: one warp, a row a lane, without the barriers below
+    if (warp == 0) {
+      const int v = lane < count ? planned_id(g, r0 + lane, bad) : -2;
+      const unsigned peers = __match_any_sync(kFull, v), lower = (1u << lane) - 1u;
+      const bool lead = v != -2 && !(peers & lower);
+      const unsigned leads = __ballot_sync(kFull, lead);
+      const int size = lead ? __popc(peers) : 0;  // a group is one tile
+      int sum = size;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, sum, o);
+        if (lane >= o) sum += u;
+      }
+      const int first = __shfl_sync(kFull, sum - size, __ffs(peers) - 1);  // the group's
+      if (lead) {
+        const int t = __popc(leads & lower);
+        s.tile_id[t] = v;
+        s.tile_count[t] = size;
+        s.tile_first[t] = first;
+      }
+      if (v != -2) s.order[first + __popc(peers & lower)] = r0 + lane;
+      if (lane == 0) s.before[kLines] = __popc(leads);
+    }
+    __syncthreads();
+    return s.before[kLines];
+  }
+  for (int i = threadIdx.x; i < kWindow; i += blockDim.x)
+    s.id[i] = i < count ? planned_id(g, r0 + i, bad) : -2;
   __syncthreads();
   for (int line = warp; line < kLines; line += warps) {
     const int i = line * 32 + lane, v = s.id[i];
@@ -208,7 +243,8 @@ __global__ void __launch_bounds__(kWindow) plan_kernel(const Args g) {
   allow_next_grid();  // after the wait: what ran before this call has finished
   const int i = threadIdx.x, r0 = blockIdx.x * kWindow, count = min(kWindow, g.n - r0);
   if (blockIdx.x == 0 && i == 0 && g.first) g.hdr[kHdrError] = 0;  // errors of this call only
-  const int tiles = make_plan(g, r0, count, s);
+  int unused = 0;  // the down kernel records the error bits
+  const int tiles = make_plan(g, r0, count, s, &unused);
   if (i == 0) g.tiles_in[blockIdx.x] = tiles;
   if (i < tiles) {
     g.tile_id[r0 + i] = s.tile_id[i];
@@ -237,13 +273,14 @@ struct Tiles {
   }
 };
 
-// Gets the tiles; by all threads.  One window: planned here, in `own`.
-__device__ Tiles get_tiles(const Args& g, int* start, Window& own) {
+// Gets the tiles; by all threads.  One window: planned here, in `own`, and *bad gets
+// the error bits that this thread has seen.
+__device__ Tiles get_tiles(const Args& g, int* start, Window& own, int* bad) {
   Tiles r;
   r.start = start;
   r.windows = g.windows;
   if (g.windows == 1) {
-    r.total = make_plan(g, 0, g.n, own);
+    r.total = make_plan(g, 0, g.n, own, bad);
     if (threadIdx.x == 0) start[0] = 0, start[1] = r.total;
     r.id = own.tile_id, r.count = own.tile_count, r.first = own.tile_first, r.order = own.order;
     __syncthreads();
@@ -592,33 +629,22 @@ __global__ void __launch_bounds__(kDownThreads, 1) down_kernel(const Args g) {
     umma::tmem_alloc(smem_addr(&tmem_slot), kDownCols);
     umma::tmem_relinquish();
   }
-  // input checks, spread over the grid; with one window CTA 0 makes them and its
-  // store also clears the word
   int bad = 0;
-  if (g.windows > 1 || blockIdx.x == 0) {
-    const int stride = g.windows > 1 ? gridDim.x * blockDim.x : blockDim.x;
-    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < g.n; i += stride) {
-      const int v = __ldg(g.ids + i);
-      if (v >= g.n_adapters) bad |= DA_DEVERR_INDEX;
-      if (v >= 0 && v < g.n_adapters && g.ranks) {
-        const int r = __ldg(g.ranks + v);
-        if (r < 0 || r > g.max_rank) bad |= DA_DEVERR_LENGTH;
-      }
-    }
-    if (g.windows > 1) {
-      if (bad) set_error(g.hdr, bad);
-    } else {
-      const int index = __syncthreads_or(bad & DA_DEVERR_INDEX);
-      const int length = __syncthreads_or(bad & DA_DEVERR_LENGTH);
-      if (threadIdx.x == 0) {  // a later slab keeps what the earlier ones recorded
-        const int found = (index ? DA_DEVERR_INDEX : 0) | (length ? DA_DEVERR_LENGTH : 0);
-        if (g.first) g.hdr[kHdrError] = found;
-        else if (found) set_error(g.hdr, found);
-      }
-    }
+  if (g.windows > 1) {  // input checks, spread over the grid
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < g.n; i += gridDim.x * blockDim.x)
+      planned_id(g, i, &bad);
+    if (bad) set_error(g.hdr, bad);
   }
   umma::fence_before_sync();
-  const Tiles tiles = get_tiles(g, start, own);  // holds CTA barriers
+  const Tiles tiles = get_tiles(g, start, own, &bad);  // holds CTA barriers
+  if (g.windows == 1 && blockIdx.x == 0) {  // the plan has checked them
+    const int any = __syncthreads_or(bad);
+    if (threadIdx.x == 0 && g.first) g.hdr[kHdrError] = 0;  // a later slab keeps what is there
+    if (any) {
+      __syncthreads();
+      if (bad) set_error(g.hdr, bad);
+    }
+  }
   umma::fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
   const long long total = (long long)tiles.total * g.n_chunks;
@@ -770,9 +796,9 @@ __device__ Phases up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
     int row_lo = 0, row_hi = 0;  // members lane and lane + 32
     if (lane < walk.count) row_lo = walk.tiles.order[walk.first + lane];
     if (lane + 32 < walk.count) row_hi = walk.tiles.order[walk.first + lane + 32];
-    // kBatch members at once: their loads are in flight together (one by one a tile of
-    // 64 took 25 us)
-    constexpr int kBatch = 8;
+    // kBatch members and kDeep chunks at once: their loads are in flight together (one
+    // by one a tile of 64 took 25 us)
+    constexpr int kBatch = 4, kDeep = 2;
     for (int m0 = w; m0 < walk.count; m0 += kBatch * kUpTWarps) {
 #pragma unroll
       for (int reg = 0; reg < R; ++reg) {
@@ -784,23 +810,25 @@ __device__ Phases up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
         for (int j = 0; j < kBatch; ++j) {
           const int m = m0 + j * kUpTWarps;
           const int row = __shfl_sync(kFull, m < 32 ? row_lo : row_hi, m & 31);
-          t[j] = g.t + (long long)row * g.max_rank + r;
+          t[j] = live && m < walk.count ? g.t + (long long)row * g.max_rank + r : nullptr;
           sum[j] = make_float2(0.f, 0.f);
-          if (live && m < walk.count) sum[j] = __ldcg(reinterpret_cast<const float2*>(t[j]));
         }
-        for (int p = 1; p < g.n_chunks; ++p) {
-          float2 e[kBatch];
+        for (int p0 = 0; p0 < g.n_chunks; p0 += kDeep) {
+          float2 e[kDeep][kBatch];
 #pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            e[j] = make_float2(0.f, 0.f);
-            if (live && m0 + j * kUpTWarps < walk.count)
-              e[j] = __ldcg(reinterpret_cast<const float2*>(t[j] + p * part));
-          }
+          for (int p = 0; p < kDeep; ++p)
 #pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            sum[j].x += e[j].x;
-            sum[j].y += e[j].y;
-          }
+            for (int j = 0; j < kBatch; ++j)
+              if (t[j] && p0 + p < g.n_chunks)
+                e[p][j] = __ldcg(reinterpret_cast<const float2*>(t[j] + (p0 + p) * part));
+#pragma unroll
+          for (int p = 0; p < kDeep; ++p)
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+              if (t[j] && p0 + p < g.n_chunks) {
+                sum[j].x += e[p][j].x;
+                sum[j].y += e[p][j].y;
+              }
         }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
@@ -1013,7 +1041,8 @@ __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
   // one window: the plan needs ids and ranks only, which were complete before the
   // down kernel let this one start
   if (g.windows > 1) wait_prior_grid();
-  const Tiles tiles = get_tiles(g, start, own);  // holds CTA barriers
+  int unused = 0;  // the down kernel has recorded the error bits
+  const Tiles tiles = get_tiles(g, start, own, &unused);  // holds CTA barriers
   if (g.windows == 1) wait_prior_grid();
   allow_next_grid();
   // not before the wait: a CTA that holds tensor memory waits for no other kernel,
