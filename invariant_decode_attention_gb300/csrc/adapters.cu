@@ -168,6 +168,7 @@ __device__ int make_plan(const Args& g, int r0, int count, Window& s, int* bad) 
       // a row's place among the rows of its group: those of earlier lines, then of
       // its own; every kTile-th row leads a tile
       int p = 0;
+#pragma unroll 8
       for (int j = 0; j < line * 32; j += 4) {
         const int4 o = *reinterpret_cast<const int4*>(s.id + j);
         p += (o.x == v) + (o.y == v) + (o.z == v) + (o.w == v);
