@@ -9,7 +9,9 @@
 // A warp takes a token, or a part of its units, and computes the token's angles
 // once for all its heads; the loads of its first units are issued before the
 // angles are needed, so one round trip to memory covers both.  Warps do not wait
-// for one another.
+// for one another.  Measured: 16384 tokens of 32/8 heads of 128, bf16, 67 us (6.0
+// TB/s, 0.89 of a plain copy's rate); one token 2.9 us; 2047 tokens into an NVFP4
+// cache 16 us, bound by the divisions of its blocks.
 //
 // Angles: position * inv_freq is formed in fp64, where the product of a 31-bit
 // integer and a 24-bit fraction is exact up to 2^-53, and reduced by multiples

@@ -20,7 +20,10 @@
 // of a row reads the row's lists, from L2.
 // Best tokens meet as 64-bit keys (ordered value, then lowest token) by shuffles
 // and shared memory of the cluster, so there is no workspace, and the maximum of
-// the keys does not depend on the order.
+// the keys does not depend on the order.  Measured: 256 rows of 131072, everything
+// written, 64 us (4.2 TB/s, 0.63 of a plain copy's rate; 48 of 152 SMs have one row,
+// the others two); 64 rows of 32000 with 30000 tokens behind them 21 us, the list
+// scan; one row of 32000 5.1 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -485,7 +488,8 @@ bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p)
 template <bool BF16, int VEC, typename W>
 cudaError_t launch_logits(Args& a, int B, int sms, cudaStream_t stream) {
   // Every CTA of a row goes through its lists, so there are no more of them than
-  // fill the GPU twice over (two CTAs per SM run at once); slices are of equal
+  // run at once, two per SM (64 rows of 32000 with long lists: four CTAs a row 22
+  // us, eight 31; 256 rows of 131072: one 69 us, four 71, eight 89); slices are of equal
   // length, a multiple of the steps of a CTA, so that only a row's last one ends
   // inside a step.
   int ranks = 1;
