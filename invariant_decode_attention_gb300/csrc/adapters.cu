@@ -41,9 +41,9 @@
 //
 // y and out (8 N bytes a row) bound a prompt, the adapters' weights and launch
 // latency a decode step.  Measured, 4096 -> 8192 features: 8192 rows of rank 64 with
-// the bf16 copy 173 us (plan 8, down 28, up 133: 5.0 TB/s, 0.74 of a plain copy's
-// rate, hand-offs between roles set the pace); 67 rows with 24 adapters 29 us; one
-// row 15 us.
+// the bf16 copy 168 us (plan 8, down 28, up 133: 5.0 TB/s, 0.74 of a plain copy's
+// rate, hand-offs between roles set the pace); 67 rows with 24 adapters 28.7 us; one
+// row 13.2 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -791,9 +791,15 @@ __device__ Phases up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
   const long long part = (long long)g.n * g.max_rank;
   Phases tiles;
   int k = 0;
+  bool waited = false;
   while (walk.next()) {
     if (!walk.fresh || walk.id < 0) continue;
     const float scale = g.scales ? __ldg(g.scales + walk.id) : 1.f;
+    if (!waited) {
+      wait_prior_grid();  // for t
+      allow_next_grid();
+      waited = true;
+    }
     if (k >= S && !wait_warp(c, kTEmpty0 + k % S, (k / S - 1) & 1)) return tiles;
     tiles.add(k % S);
     const uint32_t slot = c.sbase + Up<R>::kTOff + (k % S) * Up<R>::kTSlot;
@@ -801,8 +807,10 @@ __device__ Phases up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
     if (lane < walk.count) row_lo = walk.tiles.order[walk.first + lane];
     if (lane + 32 < walk.count) row_hi = walk.tiles.order[walk.first + lane + 32];
     // kBatch members and kDeep chunks at once: their loads are in flight together (one
-    // by one a tile of 64 took 25 us)
-    constexpr int kBatch = 4, kDeep = 2;
+    // by one a tile of 64 took 25 us; with four members and two chunks one row takes
+    // 13.9 us for 13.2, 67 rows 30.1 for 28.7, 1910 rows of a single chunk 45 for 52; both
+    // forms side by side spill)
+    constexpr int kBatch = 2, kDeep = 4;
     for (int m0 = w; m0 < walk.count; m0 += kBatch * kUpTWarps) {
 #pragma unroll
       for (int reg = 0; reg < R; ++reg) {
@@ -864,6 +872,7 @@ __device__ Phases up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
     if (lane == 0) mbar_arrive(bar_at(c, kTFull0 + k % S));
     ++k;
   }
+  if (!waited) wait_prior_grid();  // this grid has not ended before the down kernel has
   return tiles;
 }
 
@@ -1042,23 +1051,12 @@ __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
     abort_word = 0;
     fence_mbar_init();
   }
-  // one window: the plan needs ids and ranks only, which were complete before the
-  // down kernel let this one start
+  // Only t comes from the down kernel.  ids, ranks, scales, B and y were complete before
+  // it let this one start, so with one window (the plan is made here) all roles start
+  // at once and those of t wait.
   if (g.windows > 1) wait_prior_grid();
   int unused = 0;  // the down kernel has recorded the error bits
   const Tiles tiles = get_tiles(g, start, own, &unused);  // holds CTA barriers
-  if (g.windows == 1) wait_prior_grid();
-  allow_next_grid();
-  // not before the wait: a CTA that holds tensor memory waits for no other kernel,
-  // so kernels of two streams cannot wait for one another's
-  if (warp == kUpMmaWarp0) {
-    umma::tmem_alloc(smem_addr(&tmem_slot), kUpCols);
-    umma::tmem_relinquish();
-  }
-  umma::fence_before_sync();
-  __syncthreads();
-  umma::fence_after_sync();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
   const int blocks = g.N / kFeat;
   const long long total = (long long)tiles.total * blocks;
   const int first = (int)(total * blockIdx.x / gridDim.x);
@@ -1067,6 +1065,20 @@ __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
   Phases done;
   const bool issuer = warp == kUpMmaWarp0 || warp == kUpMmaWarp1;
   const int me = warp == kUpMmaWarp1;
+  uint32_t tmem = 0;
+  if (issuer || warp < kUpMmaWarp0) {  // the roles that use tensor memory
+    if (warp == kUpMmaWarp0) {
+      // not before the wait: a CTA that holds tensor memory waits for no other kernel,
+      // so kernels of two streams cannot wait for one another's
+      wait_prior_grid();
+      umma::tmem_alloc(smem_addr(&tmem_slot), kUpCols);
+      umma::tmem_relinquish();
+    }
+    umma::fence_before_sync();
+    asm volatile("bar.sync 1, %0;" ::"n"((kUpMmaWarp0 + 2) * 32) : "memory");
+    umma::fence_after_sync();
+    tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
+  }
   if (issuer) {
     if ((threadIdx.x & 31) == 0) {
       done = up_mma<R>(c, g, walk, tmem, me);

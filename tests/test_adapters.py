@@ -261,6 +261,34 @@ def test_repeats_stream_and_graph(api):
 
 
 @gpu
+@pytest.mark.parametrize("n", [1, 20, 90])
+def test_replays_see_what_changed_between_them(api, n):
+    # parts of the second kernel start before the first one has ended: everything
+    # they read is what was there when the call began
+    c = Case(api, n, 1024, 1088, 6, 64, seed=n, garbage=False)
+    ws = api.adapters_workspace(n, 1024, 1088, c.handle)
+    x, ids, y = c.x.cuda(), c.ids.cuda(), c.y.cuda()
+    both = torch.empty((n, 1024), dtype=torch.bfloat16, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):  # in place: each call reads what the last one wrote
+            api.nvfp4_adapters(x, c.handle, ids, y, out_bf16=both, ws=ws)
+    g = torch.Generator().manual_seed(n)
+    for _ in range(6):
+        c.ids = torch.randint(-1, 6, (n,), generator=g, dtype=torch.int32)
+        c.ranks = torch.randint(0, 65, (6,), generator=g, dtype=torch.int32)
+        c.scales = torch.rand(6, generator=g) + 0.5
+        c.y = torch.randn((n, 1024), generator=g)
+        ids.copy_(c.ids), y.copy_(c.y), c.handle.ranks.copy_(c.ranks), c.handle.scales.copy_(c.scales)
+        graph.replay()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            c.y = c.run(ws=ws).cpu()
+            torch.cuda.synchronize()
+        assert torch.equal(y.cpu(), c.y) and torch.equal(both.cpu(), c.y.to(torch.bfloat16))
+
+
+@gpu
 def test_no_rows(api):
     c = Case(api, 3, 128, 64, 2, 16)
     assert c.run([]).shape == (0, 128)
