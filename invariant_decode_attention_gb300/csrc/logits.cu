@@ -163,6 +163,10 @@ template <>
 struct Group<false, 4> {
   float4 raw;
   __device__ __forceinline__ void load(const void* p) { raw = *static_cast<const float4*>(p); }
+  __device__ __forceinline__ void load_from(const void* p, int skip) {  // 1 .. 3 of them
+    const float* f = static_cast<const float*>(p);
+    raw = make_float4(0.f, skip > 1 ? 0.f : f[1], skip > 2 ? 0.f : f[2], f[3]);
+  }
   __device__ __forceinline__ void get(float (&l)[4]) const {
     l[0] = raw.x, l[1] = raw.y, l[2] = raw.z, l[3] = raw.w;
   }
@@ -172,6 +176,11 @@ template <>
 struct Group<true, 4> {
   uint2 raw;
   __device__ __forceinline__ void load(const void* p) { raw = *static_cast<const uint2*>(p); }
+  __device__ __forceinline__ void load_from(const void* p, int skip) {  // 1 .. 3 of them
+    const unsigned short* h = static_cast<const unsigned short*>(p);
+    raw.x = skip > 1 ? 0u : (uint32_t)h[1] << 16;
+    raw.y = (skip > 2 ? 0u : h[2]) | (uint32_t)h[3] << 16;
+  }
   __device__ __forceinline__ void get(float (&l)[4]) const {
     l[0] = bf16_lo(raw.x), l[1] = bf16_hi(raw.x), l[2] = bf16_lo(raw.y), l[3] = bf16_hi(raw.y);
   }
@@ -181,6 +190,7 @@ template <bool BF16>
 struct Group<BF16, 1> {
   float raw;
   __device__ __forceinline__ void load(const void* p) { raw = load_x(p, 0, BF16); }
+  __device__ __forceinline__ void load_from(const void*, int) {}
   __device__ __forceinline__ void get(float (&l)[1]) const { l[0] = raw; }
 };
 
@@ -211,14 +221,19 @@ __device__ __forceinline__ void record(const int32_t* list, int n, int v0, int c
     for (int u = 0; u < kScan; ++u) {
       const unsigned s = (unsigned)(v[u] - v0);
       if (i0 + u * kThreads >= n) break;
-      if ((unsigned)v[u] >= (unsigned)V) *bad |= DA_DEVERR_INDEX;
-      if (s < (unsigned)count) put((int)s, table + s * (uint32_t)sizeof(W));
+      if ((unsigned)v[u] >= (unsigned)V)
+        *bad |= DA_DEVERR_INDEX;
+      else if (s < (unsigned)count)
+        put((int)s, table + s * (uint32_t)sizeof(W));
     }
   }
 }
 
-// VEC 4: x, out and the strides allow groups of four tokens to move at once.
-template <bool BF16, int VEC, typename W>
+// VEC 4: groups of four tokens move at once.  They start at multiples of four tokens
+// or, if SHIFT, wherever x has its 16 (bf16: 8) byte boundaries, which differs from row
+// to row: slices begin `shift` tokens early, so that a row's first group may lie partly
+// before it, and its words and its places in the table are counted from there.
+template <bool BF16, int VEC, bool SHIFT, typename W>
 __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const Args a) {
   constexpr int kElem = BF16 ? 2 : 4;
   constexpr int kStep = kThreads * VEC;     // tokens of a step of the CTA
@@ -238,14 +253,20 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const Args a) {
   const int span = a.slice * (int)ranks;  // tokens of a round
   const char* x = static_cast<const char*>(a.x) + (long long)b * a.x_stride * kElem;
 
+  const int shift = SHIFT ? (int)(reinterpret_cast<uintptr_t>(x) / kElem & 3) : 0;
+  const int V = a.V + shift;  // of which the first `shift` do not exist
+
   Group<BF16, VEC> raw[kDepth];
   uint32_t may[kDepth];  // their mask words
   const uint32_t* mask = nullptr;
   // Asks for step i of the slice at token v0.
   auto load = [&](int d, int v0, int i) {
-    const long long v = v0 + (long long)i * kStep + tid * VEC;
-    raw[d].load(x + v * kElem);
-    if (mask) may[d] = __ldg(mask + (v >> 5));
+    const int v = v0 + i * kStep + tid * VEC;
+    if (SHIFT && v < 0)
+      raw[d].load_from(x + v * kElem, shift);
+    else
+      raw[d].load(x + (long long)v * kElem);
+    if (mask) may[d] = __ldg(mask + (SHIFT ? max(v, 0) >> 5 : v >> 5));
   };
   auto load_first = [&](int v0) {
     const int full = min(a.slice, max(0, a.V - v0)) / kStep;
@@ -267,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const Args a) {
   row.repetition = a.repetition ? __ldg(a.repetition + b) : 1.f;
   row.frequency = a.frequency ? __ldg(a.frequency + b) : 0.f;
   row.presence = a.presence ? __ldg(a.presence + b) : 0.f;
-  load_first((int)rank * a.slice);
+  load_first((int)rank * a.slice - shift);
   for (int i = tid; i < a.slice * (int)sizeof(W) / 16; i += kThreads)
     reinterpret_cast<uint4*>(table)[i] = make_uint4(0, 0, 0, 0);
   if (tid == 0) n_listed = 0;
@@ -279,8 +300,9 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const Args a) {
   float best = -INFINITY;  // of this thread, whose tokens come in ascending order
   int best_v = 0;
   unsigned long long best_key = 0;  // of its last and its listed tokens
-  for (int r0 = 0; r0 < a.V; r0 += span) {
-    const int v0 = r0 + (int)rank * a.slice, count = min(a.slice, max(0, a.V - v0));
+  for (int r0 = 0; r0 < V; r0 += span) {
+    // the slice's first token, and its length
+    const int v0 = r0 + (int)rank * a.slice - shift, count = min(a.slice, max(0, a.V - v0));
     const int32_t* prompt = a.prompt + (long long)b * a.prompt_width;
     const int32_t* output = a.output + (long long)b * a.output_width;
     if ((long long)n_prompt + n_output + n_bias < count / kDense) {
@@ -350,12 +372,22 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const Args a) {
         raw[d].get(l);
         load_words<W, VEC>(table + s, w);
         if (mask) {
-          const uint32_t bits = may[d] >> ((v0 + s) & 31);
+          uint32_t bits = may[d] >> ((v0 + s) & 31);
+          if (SHIFT) {  // a group that crosses a word's end: the next lane has the next word
+            const uint32_t next = __shfl_down_sync(0xffffffffu, may[d], 1);
+            bits = v0 + s < 0 ? may[d] << shift : __funnelshift_r(may[d], next, v0 + s);
+          }
 #pragma unroll
           for (int e = 0; e < VEC; ++e)
             if (!((bits >> e) & 1u)) l[e] = -INFINITY;
         }
-        if (out) {
+        if (SHIFT && v0 + s < 0) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            if (e < shift) l[e] = -INFINITY;
+            else if (out) out[v0 + s + e] = l[e];
+          }
+        } else if (out) {
           if constexpr (VEC == 4)
             *reinterpret_cast<float4*>(out + v0 + s) = make_float4(l[0], l[1], l[2], l[3]);
           else
@@ -387,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const Args a) {
       uint32_t bits[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const int v = v0 + min(s0 + e * kThreads, count - 1);
+        const int v = max(v0 + min(s0 + e * kThreads, count - 1), 0);
         l[e] = load_x(x, v, BF16);
         bits[e] = mask ? __ldg(mask + (v >> 5)) : 0xffffffffu;
       }
@@ -395,12 +427,13 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const Args a) {
       for (int e = 0; e < VEC; ++e) {
         const int s = s0 + e * kThreads;
         if (s >= count) break;
+        if (SHIFT && v0 + s < 0) continue;
         if (!((bits[e] >> ((v0 + s) & 31)) & 1u)) l[e] = -INFINITY;
         if (out) out[v0 + s] = l[e];
         if (!table[s]) best_key = max64(best_key, key_of(l[e], v0 + s));
       }
     }
-    if (r0 + span < a.V) load_first(v0 + span);
+    if (r0 + span < V) load_first(v0 + span);
     __syncthreads();  // the listed tokens' plain values are written
 
     // Where out is x, what is found there is still a listed token's logit, or
@@ -485,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const Args a) {
 
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-template <bool BF16, int VEC, typename W>
+template <bool BF16, int VEC, bool SHIFT, typename W>
 cudaError_t launch_logits(Args& a, int B, int sms, cudaStream_t stream) {
   // Every CTA of a row goes through its lists, so there are no more of them than
   // run at once, two per SM (64 rows of 32000 with long lists: four CTAs a row 22
@@ -494,14 +527,15 @@ cudaError_t launch_logits(Args& a, int B, int sms, cudaStream_t stream) {
   // inside a step.
   int ranks = 1;
   while (ranks < kCluster && (long long)ranks * B <= sms && ranks * kThreads * 4 < a.V) ranks *= 2;
-  const long long rounds = (a.V + ranks * Word<W>::kSlice - 1) / (ranks * Word<W>::kSlice);
+  const int V = a.V + (SHIFT ? 3 : 0);  // at most
+  const long long rounds = (V + ranks * Word<W>::kSlice - 1) / (ranks * Word<W>::kSlice);
   constexpr int kStep = kThreads * VEC;
   static_assert(Word<W>::kSlice % kStep == 0, "a slice may be whole steps");
-  a.slice = (int)(((a.V + ranks * rounds - 1) / (ranks * rounds) + kStep - 1) / kStep * kStep);
+  a.slice = (int)(((V + ranks * rounds - 1) / (ranks * rounds) + kStep - 1) / kStep * kStep);
   const size_t bytes = (size_t)a.slice * sizeof(W);
   if (bytes > kPlainBytes) {  // beyond what needs no consent; it holds per device
     const cudaError_t e = cudaFuncSetAttribute(
-        logits_kernel<BF16, VEC, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTableBytes);
+        logits_kernel<BF16, VEC, SHIFT, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTableBytes);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -518,7 +552,18 @@ cudaError_t launch_logits(Args& a, int B, int sms, cudaStream_t stream) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, logits_kernel<BF16, VEC, W>, a);
+  return cudaLaunchKernelEx(&cfg, logits_kernel<BF16, VEC, SHIFT, W>, a);
+}
+
+template <bool BF16, typename W>
+auto* pick(bool vec, bool shift) {
+  return !vec ? launch_logits<BF16, 1, false, W>
+              : shift ? launch_logits<BF16, 4, true, W> : launch_logits<BF16, 4, false, W>;
+}
+
+template <bool BF16>
+auto* pick(bool vec, bool shift, bool narrow) {
+  return narrow ? pick<BF16, uint16_t>(vec, shift) : pick<BF16, uint32_t>(vec, shift);
 }
 
 // A list is given whole or not at all (one without room needs no tokens).
@@ -591,21 +636,17 @@ extern "C" int nvfp4_mm_logits(const nvfp4_logits* g, void* stream) {
   a.bias_width = g->bias_width;
   a.n_masks = g->n_masks;
   a.mask_words = (g->vocab + 31) / 32;
-  const bool vec = aligned_to(g->x, bf16 ? 8 : 16) && g->x_stride % 4 == 0 &&
-                   (!g->out || (aligned_to(g->out, 16) && g->out_stride % 4 == 0));
+  // groups of four: x and out must have their boundaries at the same tokens of a row
+  const long long x_at = (long long)(reinterpret_cast<uintptr_t>(g->x) / (bf16 ? 2 : 4));
+  const long long out_at = (long long)(reinterpret_cast<uintptr_t>(g->out) / 4);
+  const bool vec = !g->out || ((x_at - out_at) % 4 == 0 && (g->x_stride - g->out_stride) % 4 == 0);
+  const bool shift = x_at % 4 != 0 || g->x_stride % 4 != 0;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return DA_ERR_CUDA;
   const bool narrow = g->output_width <= Word<uint16_t>::kMostOutput;
-  auto* launch = bf16 ? (vec ? (narrow ? launch_logits<true, 4, uint16_t>
-                                       : launch_logits<true, 4, uint32_t>)
-                             : (narrow ? launch_logits<true, 1, uint16_t>
-                                       : launch_logits<true, 1, uint32_t>))
-                      : (vec ? (narrow ? launch_logits<false, 4, uint16_t>
-                                       : launch_logits<false, 4, uint32_t>)
-                             : (narrow ? launch_logits<false, 1, uint16_t>
-                                       : launch_logits<false, 1, uint32_t>));
+  auto* launch = bf16 ? pick<true>(vec, shift, narrow) : pick<false>(vec, shift, narrow);
   const cudaError_t e = launch(a, g->batch, sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }

@@ -142,6 +142,44 @@ def test_strides_and_alignment(api, x, pad, lead):
 
 
 @gpu
+@pytest.mark.parametrize("x", ["fp32", "bf16"])
+@pytest.mark.parametrize("V,pad,lead,apart", [
+    (4099, 0, 0, 0), (10003, 0, 1, 0), (8192, 2, 3, 0), (2046, 1, 2, 0), (70001, 4, 1, 0),
+    (5000, 1, 0, 4), (40001, 0, 2, 1), (6145, 0, 3, None), (9, 2, 1, 0)])
+def test_rows_that_start_off_a_boundary(api, x, V, pad, lead, apart):
+    """Rows at every offset from a 16-byte boundary: x and out with the boundaries at the
+    same tokens (out `apart` elements on, a multiple of 4), at others, or no out;
+    the tokens before a row's first are nobody's."""
+    B = 5
+    c = Case(B, V, x=x, seed=V + lead, prompt=200, output=100)
+    prompt, lens = c.lists["prompt"]
+    prompt[:, :7] = [-1, -2, -3, 0, 1, 2, V]  # three in front of the row, one behind it
+    lens[:-1] = np.maximum(lens[:-1], 7)
+    size = B * (V + pad) + 64
+    store = torch.full((size,), 1e30, dtype=c.x.dtype, device="cuda")  # beats all if it is read
+    xs = store.as_strided((B, V), (V + pad, 1), 16 + lead)
+    xs.copy_(c.x)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    packed = torch.empty((B, V), device="cuda")
+    want = api.nvfp4_logits(c.x.cuda(), out=packed, **c.kwargs())
+    if apart is None:
+        tokens = api.nvfp4_logits(xs, err=err, **c.kwargs())
+    else:
+        outs = torch.full((size + 8,), 9.0, device="cuda")
+        out = outs.as_strided((B, V), (V + pad, 1), 16 + lead + apart)
+        tokens = api.nvfp4_logits(xs, out=out, err=err, **c.kwargs())
+        c.check(out, tokens)
+        assert torch.equal(out, packed)
+        touched = torch.zeros_like(outs, dtype=torch.bool)
+        touched.as_strided((B, V), (V + pad, 1), 16 + lead + apart).fill_(True)
+        assert torch.all(outs[~touched] == 9.0)
+        if x == "fp32" and apart == 0:  # in place
+            assert torch.equal(api.nvfp4_logits(xs, out=xs, **c.kwargs()), tokens)
+            assert torch.equal(xs, packed)
+    assert torch.equal(tokens, want) and int(err) == api.DEVERR_INDEX
+
+
+@gpu
 def test_in_place_and_tokens_only(api):
     c = Case(9, 3001, seed=31, repeat_bias=True, bias=40)
     x = c.x.cuda().contiguous()
