@@ -172,6 +172,60 @@ def test_an_infinite_low_rank_value_stays_infinite(api):
 
 
 @gpu
+@pytest.mark.parametrize("max_rank,K", [(16, 64), (64, 64), (64, 2176), (128, 2176)])
+def test_low_rank_values_keep_all_their_bits(api, max_rank, K):
+    """One-hot rows, so that out = fp32(scale * x) exactly: 24 bits need all three terms.
+    Every rank meets every place of a tile."""
+    g = torch.Generator().manual_seed(max_rank + K)
+    col = torch.arange(max_rank) * (K // max_rank)  # the column that rank r picks
+    a = torch.zeros((2, max_rank, K))
+    a[:, torch.arange(max_rank), col] = 1
+    N = 256
+    b = (torch.arange(N)[:, None] % max_rank == torch.arange(max_rank)).float().repeat(2, 1, 1)
+    scales = torch.tensor([1.9999998807907104, -1.4142135381698608])
+    handle = api.Adapters(a.to(torch.bfloat16).cuda(), b.to(torch.bfloat16).cuda(), None, scales.cuda())
+    rank = (torch.arange(64)[:, None] + torch.arange(0, max_rank, 16)).T.reshape(-1) % max_rank
+    rank = torch.cat([(rank + s) % max_rank for s in range(16)])
+    n = len(rank)
+    ids = (torch.arange(n) // 512 % 2).int()  # full tiles, whole windows of one adapter
+    x = torch.zeros((n, K))
+    value = torch.randn(n, generator=g).to(torch.bfloat16).float()
+    x[torch.arange(n), col[rank]] = value
+    out = api.nvfp4_adapters(x.cuda(), handle, ids.cuda(), torch.zeros((n, N), device="cuda"))
+    product = scales[ids.long()] * value
+    want = torch.where(torch.arange(N) % max_rank == rank[:, None], product[:, None], 0.0)
+    assert torch.equal(out.cpu(), want)
+    assert (product != product.to(torch.bfloat16).float()).float().mean() > 0.9
+
+
+@gpu
+@pytest.mark.parametrize("max_rank", [64, 128])
+@pytest.mark.parametrize("x", ["bf16", "fp32"])
+def test_many_full_tiles_for_each_cta(api, max_rank, x):
+    """More units than the CTAs have stages, slots and accumulators, at full tiles: 152
+    CTAs take eight units of 128 features, or eight of a tile and a part of K, from
+    four tiles.  Every element against fp64, and some rows bit for bit alone."""
+    n, N, K, count = 40000, 256, 1088, 5
+    ids = np.arange(n) * count // n
+    c = Case(api, n, N, K, count, max_rank, x=x, ids=ids, ranks=None, seed=max_rank)
+    both = torch.empty((n, N), dtype=torch.bfloat16, device="cuda")
+    out = c.run(out_bf16=both)
+    assert torch.equal(both, out.to(torch.bfloat16))
+    worst = 0.0
+    for d in range(count):
+        rows = torch.as_tensor(ids == d)
+        xr = c.x[rows].cuda().to(torch.bfloat16).double()
+        a, b, s = c.a[d].cuda().double(), c.b[d].cuda().double(), float(c.scales[d])
+        ref = c.y[rows].cuda().double() + s * (xr @ a.T) @ b.T
+        mag = s * (xr.abs() @ a.abs().T) @ b.abs().T
+        err = (out[rows.cuda()].double() - ref).abs()
+        worst = max(worst, float((err / (2.0 ** -24 * ref.abs() + 2.0 ** -15 * mag)).max()))
+    assert worst <= 1, worst
+    rows = [0, 63, 64, 511, 512, 7999, 8000, 20011, 39999]
+    assert torch.equal(c.run(rows), out[rows])
+
+
+@gpu
 def test_error_bits(api):
     c = Case(api, 40, 128, 256, 3, 16, ranks=None, seed=5)
     ws = api.adapters_workspace(40, 128, 256, c.handle)

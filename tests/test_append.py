@@ -228,6 +228,15 @@ def test_far_positions(api):
 
 
 @gpu
+@pytest.mark.parametrize("kv", KV)
+def test_prompts_of_many_tokens(api, kv):
+    c = Case(api, n=1500, kv=kv, heads=(20, 4, 128), rope=(96, 16, False), x="bf16", B=12, page=16,
+             seed=15)
+    c.check_q(c.run(api))
+    c.check_caches()
+
+
+@gpu
 @pytest.mark.parametrize("x", ["bf16", "fp32"])
 def test_copied_values_are_stored_like_torch_stores_them(api, x):
     """Without a rotation the stored bytes are those of torch's conversions."""

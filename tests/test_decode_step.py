@@ -13,6 +13,8 @@ import torch
 
 from invariant_decode_attention_gb300 import workloads as W
 from oracle import attention as A
+from oracle import fp8 as OF
+from oracle import nvfp4 as ON
 from oracle import step as OS
 
 pytestmark = pytest.mark.gpu
@@ -163,3 +165,36 @@ def test_a_captured_step_replays(api):
         torch.cuda.synchronize()
         for a, b in zip((*got, s.token), want[i]):
             assert torch.equal(a, b), i
+
+
+def test_nvfp4_caches_alone_and_together(api):
+    """The same over NVFP4 caches: codes of all entries, then their block scales, in
+    one buffer."""
+    s = Server(api, list(range(5)), api.KV_NVFP4)
+    solo = [Server(api, [b], api.KV_NVFP4) for b in range(5)]
+
+    def parts(server, t):
+        m, flat = server.prob.num_blocks * PAGE * H_KV * D, t.view(-1)
+        return (flat[:m // 2].view(-1, PAGE, H_KV, D // 2),
+                flat[m // 2:m // 2 + m // 16].view(-1, PAGE, H_KV, D // 16))
+
+    def values(t):
+        codes, scales = parts(s, t)
+        step = OF.decode_e4m3(scales.cpu().numpy()) / 32
+        return ON.decode_e2m1(ON.unpack(codes.cpu().numpy())) * np.repeat(step, 16, -1)
+    for _ in range(STEPS):
+        got = s.step()
+        ref, ref_lse = A.attend(got[0].double().cpu().numpy(), values(s.k), values(s.v),
+                                s.lengths.cpu().numpy(), scale=D ** -0.5, layout="paged",
+                                table=s.table.cpu().numpy(), page_size=PAGE, d_v=D)
+        out = got[1].double().cpu().numpy()
+        assert np.all(np.abs(out - ref) <= np.maximum(1e-2, 2.0 ** -8 * np.abs(ref)))
+        assert np.all(np.abs(got[2].double().cpu().numpy() - ref_lse) <= 1e-4)
+        assert np.abs(out).max() > 0.1
+        for b, one in enumerate(solo):
+            for a, t in zip(got, one.step()):
+                assert torch.equal(a[b], t[0]), b
+    for b, one in enumerate(solo):  # the same entries in other pages
+        for mine, theirs in ((s.k, one.k), (s.v, one.v)):
+            for x, y in zip(parts(s, mine), parts(one, theirs)):
+                assert torch.equal(x[s.table[b].long()], y[one.table[0].long()])
