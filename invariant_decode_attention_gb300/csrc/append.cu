@@ -15,9 +15,12 @@
 //
 // Angles: position * inv_freq is formed in fp64, where the product of a 31-bit
 // integer and a 24-bit fraction is exact up to 2^-53, and reduced by multiples
-// of 2 pi held as two fp64 terms (Cody and Waite's two-step reduction), so sin
-// and cos see an fp32 argument in [-pi, pi] whose error is that of its own
-// rounding, 2^-23, at any position.
+// of 2 pi held as two fp64 terms (Cody and Waite's two-step reduction).  sincospi
+// gets what is left in half turns of [-1, 1], rounded once to fp32 (an error of 2^-25
+// of them, less than 2^-23 in radians), and is itself off by two units in the last
+// place at most.  (The hardware's approximations of sine and cosine are off by
+// up to 2^-21 each: a component near zero beside a large partner lost bits that its
+// type holds.)
 #include "append.cuh"
 
 #include <algorithm>
@@ -222,8 +225,8 @@ __global__ void __launch_bounds__(kWarps * 32, kResident<X>)
     const double whole = rint(a * 0.15915494309189533577);  // 1 / (2 pi)
     double r = fma(-whole, 6.283185307179586477, a);         // 2 pi, fp64
     r = fma(-whole, 2.4492935982947064e-16, r);              // 2 pi less that
-    float sn, cs;  // |r| <= pi: off by less than 2^-21
-    __sincosf((float)r, &sn, &cs);
+    float sn, cs;
+    sincospif((float)(r * 0.31830988618379067154), &sn, &cs);  // 1 / pi
     reinterpret_cast<float2*>(turn + ((j & 7) >> 1) * groups + (j >> 3))[j & 1] =
         make_float2(p.gain * cs, p.gain * sn);
   }

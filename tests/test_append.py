@@ -228,6 +228,39 @@ def test_far_positions(api):
 
 
 @gpu
+@pytest.mark.parametrize("inter", [False, True])
+def test_sine_and_cosine_have_fp32_accuracy(api, inter):
+    """A vector (sin t, cos t) turned by t has a first component near zero, whose bf16
+    bits show the absolute error of the rotation that a result of ordinary size hides.
+
+    With |a|, |b| <= 1 and a sin t + b cos t = 1: the angle is rounded once to fp32, in
+    half turns of at most 1 (2^-25 of them: 0.80 * 2^-23 in radians); sine and
+    cosine are off by two units of 2^-24 at most, together sqrt(2) * 2^-23; the two products
+    of magnitude at most 1/2 by 2^-26 each.  Sum: 2.47 * 2^-23 < 1.25 * 2^-22."""
+    g = torch.Generator().manual_seed(5)
+    n, half = 64, 64
+    pos = torch.randint(0, 1 << 17, (n,), generator=g)
+    inv = torch.exp2(-13 * torch.rand(half, generator=g, dtype=torch.float64)).float()
+    t = pos.double().numpy().astype(np.longdouble)[:, None] * inv.numpy().astype(np.longdouble)
+    x = np.zeros((n, 1, 2 * half))
+    ia = 2 * np.arange(half) if inter else np.arange(half)
+    ib = ia + (1 if inter else half)
+    x[:, 0, ia], x[:, 0, ib] = np.sin(t), np.cos(t)
+    q = torch.from_numpy(x).float()
+    prob = api.problem(batch=1, num_q_heads=1, num_kv_heads=1, head_dim_qk=128, layout="indexed",
+                       scale=0.1, width=1, num_blocks=n)
+    k, v = (torch.zeros((n, 1, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = api.append(prob, api.rope(inv.cuda(), interleaved=inter), q.cuda(), q.cuda(), k, v,
+                     pos.to(**i32), rows=torch.arange(n, **i32), q_new=q.cuda())
+    ref = OS.rotate(q.double().numpy(), pos.numpy(), inv.numpy(), interleaved=inter)
+    tol = 2.0 ** -8 * np.abs(ref) + 1.25 * 2.0 ** -22
+    for got in (out, k):
+        err = np.abs(got.double().cpu().numpy() - ref)[:, 0, ia]
+        assert np.all(err <= tol[:, 0, ia]), float(err.max() * 2 ** 22)
+
+
+@gpu
 @pytest.mark.parametrize("kv", KV)
 def test_prompts_of_many_tokens(api, kv):
     c = Case(api, n=1500, kv=kv, heads=(20, 4, 128), rope=(96, 16, False), x="bf16", B=12, page=16,
