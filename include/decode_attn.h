@@ -310,8 +310,9 @@ int decode_attn_copy_plan(const da_plan* plan, int32_t* n_splits, int32_t* split
 
 /* Rotation of queries and keys by their positions.  For a token at position p
  * every pair j = 0 .. dim/2 - 1 of the rotated dims of a head is turned by the
- * angle p * inv_freq[j] (the exact product of the integer and the fp32 number;
- * reduced in fp64, so far positions lose nothing):
+ * angle p * inv_freq[j], the exact product of the integer and the fp32 number,
+ * less its whole turns, so that far positions lose nothing (magnitudes below 2^64;
+ * larger angles are unspecified); cos and sin are off by less than 2^-22:
  *     a' = gain * (a cos - b sin),   b' = gain * (b cos + a sin)    (fp32)
  * with (a, b) = dims (offset + j, offset + dim/2 + j), or, interleaved,
  * (offset + 2j, offset + 2j + 1).  The head's other dims are copied. */
@@ -320,7 +321,7 @@ typedef struct da_rope {
   int32_t offset;        /* first of them within a head: a multiple of 8      */
   int32_t interleaved;   /* 0 or 1: how dims pair up                          */
   float gain;            /* finite; 1 for a plain rotation                    */
-  const float* inv_freq; /* device fp32 [dim / 2]                             */
+  const float* inv_freq; /* device fp32 [dim / 2], finite                     */
 } da_rope;
 
 /* The new tokens of one decode_attn_append call.  Plain data. */

@@ -9,18 +9,21 @@
 // A warp takes a token, or a part of its units, and computes the token's angles
 // once for all its heads; the loads of its first units are issued before the
 // angles are needed, so one round trip to memory covers both.  Warps do not wait
-// for one another.  Measured: 16384 tokens of 32/8 heads of 128, bf16, 67 us (6.0
-// TB/s, 0.89 of a plain copy's rate); one token 2.9 us; 2047 tokens into an NVFP4
-// cache 16 us, bound by the divisions of its blocks.
+// for one another.  Measured: 16384 tokens of 32/8 heads of 128, bf16, 64 us (6.3
+// TB/s, 0.93 of a plain copy's rate); one token 2.5 us; 2047 tokens into an NVFP4
+// cache 15.7 us.
 //
-// Angles: position * inv_freq is formed in fp64, where the product of a 31-bit
-// integer and a 24-bit fraction is exact up to 2^-53, and reduced by multiples
-// of 2 pi held as two fp64 terms (Cody and Waite's two-step reduction).  sincospi
-// gets what is left in half turns of [-1, 1], rounded once to fp32 (an error of 2^-25
-// of them, less than 2^-23 in radians), and is itself off by two units in the last
-// place at most.  (The hardware's approximations of sine and cosine are off by
-// up to 2^-21 each: a component near zero beside a large partner lost bits that its
-// type holds.)
+// Angles: position * inv_freq is the product of a 31-bit integer, a 24-bit integer and
+// a power of two.  Multiplied by 2^128 / (2 pi) in integers, its whole turns are
+// the bits above a place that the exponent gives and go by themselves; the 64
+// below it are exact up to 2^-63 of a turn, at any position and frequency (Payne
+// and Hanek's reduction with a constant long enough for all of them).  The
+// multiplications of a warp's 32 angles take fewer cycles than one in fp64, whose
+// units are few (64 latent rows: 4.5 us, 5.9 in fp64).  sincospi gets half turns of [-1, 1],
+// rounded once to fp32 (an error of 2^-25 of them, less than 2^-23 in radians), and
+// is itself off by two units in the last place at most.  (The hardware's
+// approximations of sine and cosine are off by up to 2^-21 each: a component near
+// zero beside a large partner lost bits that its type holds.)
 #include "append.cuh"
 
 #include <algorithm>
@@ -126,6 +129,22 @@ __device__ __forceinline__ long long entry_of(const AppendLaunch& p, int i, int 
   return (long long)id * p.page_size + (pos - page * p.page_size);
 }
 
+// The angle pos * inv_freq in half turns, whole turns taken away: in [-1, 1].
+__device__ __forceinline__ float half_turns(uint32_t pos, float inv_freq) {
+  // 2^128 / (2 pi), from the value of pi
+  constexpr unsigned long long kHigh = 0x28be60db9391054aull, kLow = 0x7f09d5f47d4d3770ull;
+  const uint32_t bits = __float_as_uint(inv_freq), e = (bits >> 23) & 0xffu;
+  const unsigned long long m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u), n = m * pos;
+  const unsigned long long carry = __umul64hi(n, kLow), t1 = carry + n * kHigh;
+  const unsigned long long t2 = __umul64hi(n, kHigh) + (t1 < carry);
+  // turns = (t2, t1, n * kLow) * 2^(e - 150 - 128): 64 bits from bit `at` on
+  const int at = min(max(214 - (int)max(e, 1u), 0), 191), shift = at & 63;
+  const unsigned long long lo = at < 64 ? n * kLow : at < 128 ? t1 : t2;
+  const unsigned long long hi = at < 64 ? t1 : at < 128 ? t2 : 0;
+  const unsigned long long turn = (lo >> shift) | (hi << 1 << (63 - shift));
+  return __ll2float_rn((long long)(bits >> 31 ? 0 - turn : turn)) * 0x1p-63f;
+}
+
 // Rotates the four pairs (a[0], a[1]), ... of a chunk, or half a group of pairs.
 __device__ __forceinline__ void turn_pairs(float (&f)[8], const float4* at, int groups) {
 #pragma unroll
@@ -220,13 +239,10 @@ __global__ void __launch_bounds__(kWarps * 32, kResident<X>)
   if (bad && p.err && part == 0 && lane == 0) atomicOr(p.err, bad);
   if (entry < 0) return;  // the whole warp: one token
 
+#pragma unroll 2  // a head of 128's two angles of a lane at once (one by one: 72 us for 64)
   for (int j = lane; j < half; j += 32) {
-    const double a = (double)pos * (double)__ldg(p.inv_freq + j);
-    const double whole = rint(a * 0.15915494309189533577);  // 1 / (2 pi)
-    double r = fma(-whole, 6.283185307179586477, a);         // 2 pi, fp64
-    r = fma(-whole, 2.4492935982947064e-16, r);              // 2 pi less that
     float sn, cs;
-    sincospif((float)(r * 0.31830988618379067154), &sn, &cs);  // 1 / pi
+    sincospif(half_turns((uint32_t)pos, __ldg(p.inv_freq + j)), &sn, &cs);
     reinterpret_cast<float2*>(turn + ((j & 7) >> 1) * groups + (j >> 3))[j & 1] =
         make_float2(p.gain * cs, p.gain * sn);
   }

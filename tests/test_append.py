@@ -261,6 +261,17 @@ def test_sine_and_cosine_have_fp32_accuracy(api, inter):
 
 
 @gpu
+def test_angles_far_beyond_32_bits(api):
+    # the product of a position and a frequency is exact, whatever the frequency
+    pos = [1, 4095, (1 << 24) + 1, (1 << 30) + 12345, (1 << 31) - 1, (1 << 31) - 77]
+    c = Case(api, n=6, layout="indexed", rope=(128, 0, False), x="fp32", positions=pos)
+    c.inv = torch.exp2(torch.linspace(-4, 18, 64, dtype=torch.float64)).float()
+    c.rope = api.rope(c.inv.cuda())
+    c.check_q(c.run(api))
+    c.check_caches()
+
+
+@gpu
 @pytest.mark.parametrize("kv", KV)
 def test_prompts_of_many_tokens(api, kv):
     c = Case(api, n=1500, kv=kv, heads=(20, 4, 128), rope=(96, 16, False), x="bf16", B=12, page=16,
