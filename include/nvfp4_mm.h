@@ -99,6 +99,12 @@ int nvfp4_mm_read_error(void* ws, int32_t* code, void* stream);
 #define NVFP4_ADAPTER_MAX_RANK 128
 #define NVFP4_ADAPTER_MAX_K (1 << 22)
 
+/* Tests only: added to x_dtype of nvfp4_mm_adapters, one of them keeps the first stage
+ * of every CTA of the first or second matmul kernel from ever getting full and bounds
+ * waits to 2 ms, which drives that kernel's time-out path. */
+#define NVFP4_X_TEST_STALL_DOWN 0x100
+#define NVFP4_X_TEST_STALL_UP 0x200
+
 /* Device workspace bytes of one nvfp4_mm_adapters call (0: shape not
  * supported): a 256-byte header and the fp32 products t.  Needs no
  * initialisation. */
@@ -130,8 +136,9 @@ size_t nvfp4_mm_adapters_workspace_bytes(int32_t n, int32_t N, int32_t K, int32_
  *           all rows.  Otherwise out and out_bf16 overlap no other argument.
  *   ws      as for nvfp4_mm.
  * An id at or above n_adapters counts as none and sets DA_DEVERR_INDEX, a rank
- * outside [0, max_rank] is clamped and sets DA_DEVERR_LENGTH; read the bits of
- * the last call with nvfp4_mm_read_error(ws, ...).
+ * outside [0, max_rank] is clamped and sets DA_DEVERR_LENGTH; a pipeline wait that
+ * hits its time limit sets DA_DEVERR_TIMEOUT and the kernel returns, out and out_bf16
+ * are then undefined.  Read the bits of the last call with nvfp4_mm_read_error(ws, ...).
  * Supported shapes: n >= 0, N a positive multiple of NVFP4_MM_TILE_N, K a
  * positive multiple of 64 up to NVFP4_ADAPTER_MAX_K, max_rank a multiple of 16
  * up to NVFP4_ADAPTER_MAX_RANK, n_adapters >= 1; n * K, n * N below 2^31. */

@@ -47,6 +47,7 @@ NVFP4_X_F32, NVFP4_X_BF16 = 0, 1
 # Cache append (include/decode_attn.h) and adapters (include/nvfp4_mm.h)
 X_F32, X_BF16 = 0, 1
 ADAPTER_MAX_RANK, ADAPTER_MAX_K, LOGITS_MAX_BIAS = 128, 1 << 22, 4096
+X_TEST_STALL_DOWN, X_TEST_STALL_UP = 0x100, 0x200  # test hooks (see include/nvfp4_mm.h)
 
 # Size of the fixed device array decode_attn_forward_static uses as scratch.
 STATIC_WORKSPACE_BYTES = 64 << 20

@@ -87,6 +87,9 @@ struct Args {
   int n, N, K, n_adapters, max_rank, n_chunks, windows;
   int copy;             // 1: rows without an adapter are written as well
   int first;            // 1: the call's first slab
+  // time-out test hook: the first stage (1: of down, 2: of up) never gets full
+  int stall;
+  unsigned long long limit_ns;  // of a wait
 };
 
 __device__ __forceinline__ void fence_proxy_async() {
@@ -317,6 +320,7 @@ struct Ctx {
   uint32_t sbase, bars;  // shared memory, and its mbarriers
   volatile int* abort_flag;
   int32_t* hdr;
+  unsigned long long limit_ns;  // of a wait
 };
 
 __device__ __forceinline__ uint32_t bar_at(const Ctx& c, int i) { return c.bars + 8 * i; }
@@ -330,7 +334,7 @@ __device__ __forceinline__ bool wait_bar(const Ctx& c, int i, uint32_t parity) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 63u) == 0) {
       if (*c.abort_flag) return false;
-      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      if (globaltimer_ns() - t0 > c.limit_ns) {
         set_error(c.hdr, DA_DEVERR_TIMEOUT);
         *c.abort_flag = 1;
         return false;
@@ -363,8 +367,10 @@ struct Phases {
 
 // The arrive of a tcgen05.commit lands some time after the work it tracks; the
 // last one on each barrier first, first + 1, ... must have landed before the CTA's
-// shared memory is handed on.
-__device__ __forceinline__ void drain_commits(const Ctx& c, int first, const Phases& p) {
+// shared memory is handed on.  Every barrier that commits arrive on has one issuer,
+// which waits for its own here: after a time-out too, when nobody else may.  (Not
+// inlined: small calls pay for the instructions that they fetch, 0.4 us of one row's.)
+__device__ __noinline__ void drain_commits(Ctx c, int first, Phases p) {
   for (int i = 0; (p.any >> i) != 0; ++i)
     if (p.has(i) && !mbar_wait(bar_at(c, first + i), p.last(i))) set_error(c.hdr, DA_DEVERR_TIMEOUT);
 }
@@ -380,9 +386,10 @@ constexpr int kDownStages = 6;                     // at most
 // Two threads issue the MMAs: the even and the odd steps, each into an accumulator
 // of its own that the epilogue adds.  Which of the two a step goes to depends on
 // what came before, but the sum of two numbers does not.
-// mbarriers: stage full and empty, accumulators full and empty, drain
+// mbarriers: stage full; by tcgen05.commit: stage empty, each issuer's accumulators
+// full, drain; accumulators empty
 enum { kFull0 = 0, kEmpty0 = kFull0 + kDownStages, kDFull0 = kEmpty0 + kDownStages,
-       kDEmpty0 = kDFull0 + 2, kDownDrain = kDEmpty0 + 2, kDownBars = kDownDrain + 2 };
+       kDownDrain = kDFull0 + 4, kDEmpty0 = kDownDrain + 2, kDownBars = kDEmpty0 + 2 };
 constexpr uint32_t kDownCols = 4 * kTile;          // two units' two accumulators
 
 __host__ __device__ constexpr int down_stage_bytes(int max_rank) {
@@ -519,8 +526,8 @@ __device__ void down_produce(const Ctx& c, const Args& g, DownWalk walk) {
   cp_async_wait_all();  // nothing is in flight when the CTA ends
 }
 
-// Issuer `me` takes the steps of its parity; returns what it committed to the
-// stages' empty barriers.
+// Issuer `me` takes the steps of its parity; returns what it committed, by barrier
+// from kEmpty0 on.
 template <int S>
 __device__ Phases down_mma(const Ctx& c, const Args& g, DownWalk walk, uint32_t tmem, int me) {
   static_assert(S % 2 == 0, "a stage belongs to one issuer");
@@ -558,7 +565,8 @@ __device__ Phases down_mma(const Ctx& c, const Args& g, DownWalk walk, uint32_t 
       done.add(step % S);
       first = false;
     }
-    umma::commit(bar_at(c, kDFull0 + tb));  // also when it had no step of the unit
+    umma::commit(bar_at(c, kDFull0 + 2 * tb + me));  // also when it had no step of the unit
+    done.add(kDFull0 - kEmpty0 + 2 * tb + me);
   }
   return done;
 }
@@ -573,7 +581,9 @@ __device__ void down_epilogue(const Ctx& c, const Args& g, DownWalk walk, uint32
       if (lane + 32 < walk.count) row_hi = walk.tiles.order[walk.first + lane + 32];
     }
     const int tb = k_unit & 1, steps = (walk.k_len + kStepK - 1) / kStepK;
-    if (!wait_warp(c, kDFull0 + tb, (k_unit >> 1) & 1)) return;
+    if (!wait_warp(c, kDFull0 + 2 * tb, (k_unit >> 1) & 1) ||
+        !wait_warp(c, kDFull0 + 2 * tb + 1, (k_unit >> 1) & 1))
+      return;
     umma::fence_after_sync();
     const int r = 32 * q + lane;
     float* t = g.t + (long long)(walk.k0 / kKChunk) * g.n * g.max_rank + r;
@@ -610,6 +620,7 @@ __global__ void __launch_bounds__(kDownThreads, 1) down_kernel(const Args g) {
   c.bars = smem_addr(bars);
   c.abort_flag = &abort_word;
   c.hdr = g.hdr;
+  c.limit_ns = g.limit_ns;
   const int warp = threadIdx.x >> 5;
   if (c.sbase & 1023u) {  // the swizzled layout needs 1024-byte-aligned shared memory
     wait_prior_grid();
@@ -620,8 +631,8 @@ __global__ void __launch_bounds__(kDownThreads, 1) down_kernel(const Args g) {
     for (int i = 0; i < kDownBars; ++i) {
       uint32_t count = 1;  // tcgen05.commit
       if (i < kEmpty0) count = kDownProdWarps * (32 + (BF16 ? 0 : 1));
-      if (i >= kDFull0 && i < kDEmpty0) count = 2;  // both issuers
-      if (i >= kDEmpty0 && i < kDownDrain) count = kDownEpWarps;
+      if (i >= kDEmpty0) count = kDownEpWarps;
+      if (i == kFull0 && g.stall == 1) ++count;
       mbar_init(c.bars + 8 * i, count);
     }
     abort_word = 0;
@@ -689,7 +700,6 @@ constexpr int kGroups = 4;                  // epilogue groups of four warps, on
 // idle).  The issuers take the even and the odd units.
 constexpr int kUpMmaWarp0 = 16, kUpMmaWarp1 = 20, kUpWarps = 32, kUpThreads = kUpWarps * 32;
 constexpr int kUpProdWarps = 4, kUpTWarps = 4;
-constexpr int kUpTWarp = 22;  // one of those of t
 // 0 .. 11 for the warps that bring operands: four each for B and t, one for each
 // group's y
 __device__ __forceinline__ int up_helper(int warp) { return (warp - 17) / 4 * 3 + (warp - 17) % 4; }
@@ -712,10 +722,12 @@ struct Up {
   static_assert(kYOff % 1024 == 0 && kSmem <= 209 * 1024 && 2 * kSmem > 233472, "one CTA per SM");
 };
 constexpr int kMaxBSlots = 4;
+// mbarriers: B full; by tcgen05.commit: B empty, accumulators full, each issuer's t
+// empty, drain; accumulators empty, t full, y full and empty
 enum { kBFull0 = 0, kBEmpty0 = kBFull0 + kMaxBSlots, kUDFull0 = kBEmpty0 + kMaxBSlots,
-       kUDEmpty0 = kUDFull0 + kGroups, kTFull0 = kUDEmpty0 + kGroups, kTEmpty0 = kTFull0 + 2,
-       kYFull0 = kTEmpty0 + 2, kYEmpty0 = kYFull0 + kGroups * kYSlots,
-       kUpDrain = kYEmpty0 + kGroups * kYSlots, kUpBars = kUpDrain + 2 };
+       kTEmpty0 = kUDFull0 + kGroups, kUpDrain = kTEmpty0 + 4, kUDEmpty0 = kUpDrain + 2,
+       kTFull0 = kUDEmpty0 + kGroups, kYFull0 = kTFull0 + 2,
+       kYEmpty0 = kYFull0 + kGroups * kYSlots, kUpBars = kYEmpty0 + kGroups * kYSlots };
 constexpr uint32_t kUpCols = kGroups * kTile;
 
 // The CTA's units: tile by tile, 128 features each.
@@ -782,14 +794,12 @@ __device__ void up_produce(const Ctx& c, const Args& g, UpWalk walk) {
 }
 
 // t of a tile's members: chunk sums added in order, scaled, split.  Warp w takes
-// members w, w + 4, ...; a lane two ranks of each 64.  Returns the tiles that went
-// through each slot.
+// members w, w + 4, ...; a lane two ranks of each 64.
 template <int R>
-__device__ Phases up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
+__device__ void up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
   constexpr int S = Up<R>::kTSlots;
   const int lane = threadIdx.x & 31, w = up_helper(threadIdx.x >> 5) - kUpProdWarps;
   const long long part = (long long)g.n * g.max_rank;
-  Phases tiles;
   int k = 0;
   bool waited = false;
   while (walk.next()) {
@@ -800,8 +810,9 @@ __device__ Phases up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
       allow_next_grid();
       waited = true;
     }
-    if (k >= S && !wait_warp(c, kTEmpty0 + k % S, (k / S - 1) & 1)) return tiles;
-    tiles.add(k % S);
+    if (k >= S && (!wait_warp(c, kTEmpty0 + 2 * (k % S), (k / S - 1) & 1) ||
+                   !wait_warp(c, kTEmpty0 + 2 * (k % S) + 1, (k / S - 1) & 1)))
+      return;
     const uint32_t slot = c.sbase + Up<R>::kTOff + (k % S) * Up<R>::kTSlot;
     int row_lo = 0, row_hi = 0;  // members lane and lane + 32
     if (lane < walk.count) row_lo = walk.tiles.order[walk.first + lane];
@@ -873,28 +884,32 @@ __device__ Phases up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
     ++k;
   }
   if (!waited) wait_prior_grid();  // this grid has not ended before the down kernel has
-  return tiles;
 }
 
-// Issuer `me` takes the units of its parity.  Returns what it committed to the
-// slots of B.
+// What an issuer committed: to the slots of B, the accumulators and its barriers of
+// t's slots.
+struct UpDone {
+  Phases slots, accs, tiles;
+};
+
+// Issuer `me` takes the units of its parity.
 template <int R>
-__device__ Phases up_mma(const Ctx& c, const Args& g, UpWalk walk, uint32_t tmem, int me) {
+__device__ UpDone up_mma(const Ctx& c, const Args& g, UpWalk walk, uint32_t tmem, int me) {
   constexpr int S = Up<R>::kBSlots, TS = Up<R>::kTSlots;
   const uint64_t base = umma::smem_desc(c.sbase, 16, 1024, umma::kSwizzle128B);
-  Phases slots, accs;
+  UpDone done;
   int tiles = 0;  // begun
   for (int i = 0; walk.next(); ++i) {
     if (walk.id < 0) continue;
     if (walk.fresh) {
-      if (!wait_bar(c, kTFull0 + tiles % TS, (tiles / TS) & 1)) return slots;
+      if (!wait_bar(c, kTFull0 + tiles % TS, (tiles / TS) & 1)) return done;
       ++tiles;
     }
     const int ts = (tiles - 1) % TS;
     if ((i & 1) == me) {
       const int e = i % kGroups, s = i % S;
-      if (accs.has(e) && !wait_bar(c, kUDEmpty0 + e, accs.last(e))) return slots;
-      if (!wait_bar(c, kBFull0 + s, slots.next(s))) return slots;
+      if (done.accs.has(e) && !wait_bar(c, kUDEmpty0 + e, done.accs.last(e))) return done;
+      if (!wait_bar(c, kBFull0 + s, done.slots.next(s))) return done;
       fence_proxy_async();  // as in down_mma
       umma::fence_after_sync();
       const uint64_t bd = base + (uint64_t)((s * (R * kBRegion)) >> 4);
@@ -914,12 +929,15 @@ __device__ Phases up_mma(const Ctx& c, const Args& g, UpWalk walk, uint32_t tmem
       }
       umma::commit(bar_at(c, kBEmpty0 + s));
       umma::commit(bar_at(c, kUDFull0 + e));
-      slots.add(s);
-      accs.add(e);
+      done.slots.add(s);
+      done.accs.add(e);
     }
-    if (walk.ends) umma::commit(bar_at(c, kTEmpty0 + ts));  // both issuers do
+    if (walk.ends) {  // both issuers do
+      umma::commit(bar_at(c, kTEmpty0 + 2 * ts + me));
+      done.tiles.add(2 * ts + me);
+    }
   }
-  return slots;
+  return done;
 }
 
 // y of group e's units, a quarter of a tile at a time, a row's 512 bytes with one
@@ -1031,6 +1049,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
   c.bars = smem_addr(bars);
   c.abort_flag = &abort_word;
   c.hdr = g.hdr;
+  c.limit_ns = g.limit_ns;
   const int warp = threadIdx.x >> 5;
   if (c.sbase & 1023u) {  // the swizzled layout needs 1024-byte-aligned shared memory
     wait_prior_grid();
@@ -1044,8 +1063,8 @@ __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
       if (i >= kYFull0 && i < kYEmpty0) count = 32;
       if (i >= kUDEmpty0 && i < kTFull0) count = 4;
       if (i == kTFull0 || i == kTFull0 + 1) count = kUpTWarps;
-      if (i == kTEmpty0 || i == kTEmpty0 + 1) count = 2;  // both issuers
-      if (i >= kYEmpty0 && i < kUpDrain) count = 4;
+      if (i >= kYEmpty0) count = 4;
+      if (i == kBFull0 && g.stall == 2) ++count;
       mbar_init(c.bars + 8 * i, count);
     }
     abort_word = 0;
@@ -1062,7 +1081,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
   const int first = (int)(total * blockIdx.x / gridDim.x);
   const int last = (int)(total * (blockIdx.x + 1) / gridDim.x);
   UpWalk walk{g, tiles, last - first, first / blocks, first % blocks, blocks};
-  Phases done;
+  UpDone done;
   const bool issuer = warp == kUpMmaWarp0 || warp == kUpMmaWarp1;
   const int me = warp == kUpMmaWarp1;
   uint32_t tmem = 0;
@@ -1091,7 +1110,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
     if (h < kUpProdWarps)
       up_produce<R>(c, g, walk);
     else if (h < kUpProdWarps + kUpTWarps)
-      done = up_make_t<R>(c, g, walk);
+      up_make_t<R>(c, g, walk);
     else
       up_fetch_y<R>(c, g, walk);
   }
@@ -1100,11 +1119,11 @@ __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
   umma::fence_after_sync();
   if (issuer && (threadIdx.x & 31) == 0) {
     if (!mbar_wait(bar_at(c, kUpDrain + me), 0)) set_error(c.hdr, DA_DEVERR_TIMEOUT);
-    drain_commits(c, kBEmpty0, done);
+    drain_commits(c, kBEmpty0, done.slots);
+    drain_commits(c, kTEmpty0, done.tiles);
+    // the epilogue has waited for the accumulators' unless it gave up
+    if (*c.abort_flag) drain_commits(c, kUDFull0, done.accs);
   }
-  // t's slots are released by both issuers together, unless one of them gave up
-  if (warp == kUpTWarp && (threadIdx.x & 31) == 0 && !*c.abort_flag)
-    drain_commits(c, kTEmpty0, done);
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
@@ -1191,6 +1210,9 @@ int nvfp4_mm_adapters(const void* x, int32_t x_dtype, int32_t n, int32_t N, int3
                       const int32_t* ranks, const float* scales, const int32_t* ids,
                       const float* y, float* out, void* out_bf16, void* ws, size_t ws_bytes,
                       void* stream) {
+  const int stall = x_dtype / NVFP4_X_TEST_STALL_DOWN;  // tests only
+  x_dtype %= NVFP4_X_TEST_STALL_DOWN;
+  if (stall < 0 || stall > 2) return DA_ERR_INVALID_ARG;
   if (x_dtype != NVFP4_X_F32 && x_dtype != NVFP4_X_BF16) return DA_ERR_INVALID_ARG;
   if (!shape_ok(n, N, K, n_adapters, max_rank)) return DA_ERR_UNSUPPORTED;
   if (n == 0) return DA_OK;
@@ -1233,6 +1255,8 @@ int nvfp4_mm_adapters(const void* x, int32_t x_dtype, int32_t n, int32_t N, int3
   g.max_rank = max_rank;
   g.n_chunks = chunks_of(K);
   g.copy = out != y || out_bf16;
+  g.stall = stall;
+  g.limit_ns = stall ? kTestStallNs : kWaitLimitNs;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf16 = x_dtype == NVFP4_X_BF16;
   // six stages of up to 32 KB, or four of up to 48; ranks of up to 64 take one

@@ -81,3 +81,50 @@ def test_stall_times_out_and_context_stays_usable(api, kind):
         o, l = api.run_workload(g, ws=ws)
         torch.cuda.synchronize()
         assert torch.equal(o, o_ref) and torch.equal(l, l_ref)
+
+
+@gpu
+@pytest.mark.parametrize("n,max_rank,x_dtype", [(90, 64, 1), (90, 128, 0), (1300, 64, 0), (1300, 128, 1)])
+def test_stalled_adapters_time_out_and_the_next_call_is_clean(api, n, max_rank, x_dtype):
+    """nvfp4_mm_adapters with the first stage of one of its two matmul kernels never full:
+    one issuing thread waits for it (2 ms limit) while the other one goes on, with
+    commits to every kind of barrier behind it."""
+    g = torch.Generator().manual_seed(n + max_rank)
+    N, K, count = 1024, 2176, 3
+    x = torch.randn((n, K), generator=g).to(torch.bfloat16 if x_dtype else torch.float32).cuda()
+    y = torch.randn((n, N), generator=g).cuda()
+    a = (torch.randn((count, max_rank, K), generator=g) * K ** -0.5).to(torch.bfloat16).cuda()
+    b = torch.randn((count, N, max_rank), generator=g).to(torch.bfloat16).cuda()
+    ids = torch.sort(torch.randint(-1, count, (n,), generator=g, dtype=torch.int32))[0].cuda()
+    h = api.Adapters(a, b)
+    ws = api.adapters_workspace(n, N, K, h)
+    want = api.nvfp4_adapters(x, h, ids, y, out=torch.empty_like(y), ws=ws)
+    assert api.nvfp4_read_error(ws) == 0
+    out = torch.empty_like(y)
+
+    def call(flag):
+        status = api.lib().nvfp4_mm_adapters(
+            x.data_ptr(), x_dtype + flag, n, N, K, a.data_ptr(), b.data_ptr(), count, max_rank, None,
+            None, ids.data_ptr(), y.data_ptr(), out.data_ptr(), None, ws.data_ptr(), ws.numel(),
+            torch.cuda.current_stream().cuda_stream)
+        assert status == api.OK
+        return api.nvfp4_read_error(ws)
+    for flag in (api.X_TEST_STALL_DOWN, api.X_TEST_STALL_UP):
+        for _ in range(2):  # twice: the first stalled call left nothing behind
+            assert call(flag) == api.DEVERR_TIMEOUT
+        for _ in range(2):
+            out.fill_(float("nan"))
+            assert call(0) == 0
+            assert torch.equal(out, want)
+
+
+def test_adapters_flag_validation(api):
+    fake = 1 << 20  # never dereferenced: every case fails before any device work
+
+    def call(x_dtype):
+        return api.lib().nvfp4_mm_adapters(fake, x_dtype, 4, 128, 64, fake, fake, 2, 16, None, None,
+                                           fake, 1 << 24, 1 << 28, None, fake, 0, None)
+    for good in (0, 1, 0x100, 0x101, 0x200, 0x201):
+        assert call(good) == api.ERR_WORKSPACE, good
+    for bad in (2, 0x102, 0x202, 0x300, 0x301, -1, -256, -255):
+        assert call(bad) == api.ERR_INVALID_ARG, bad
