@@ -106,8 +106,8 @@ int nvfp4_mm_read_error(void* ws, int32_t* code, void* stream);
 #define NVFP4_X_TEST_STALL_UP 0x200
 
 /* Device workspace bytes of one nvfp4_mm_adapters call (0: shape not
- * supported): a 256-byte header and the fp32 products t.  Needs no
- * initialisation. */
+ * supported): a 256-byte header, the plan (which rows make a tile with which
+ * adapter) and the fp32 products t.  Needs no initialisation. */
 size_t nvfp4_mm_adapters_workspace_bytes(int32_t n, int32_t N, int32_t K, int32_t n_adapters,
                                          int32_t max_rank);
 
@@ -138,7 +138,8 @@ size_t nvfp4_mm_adapters_workspace_bytes(int32_t n, int32_t N, int32_t K, int32_
  * An id at or above n_adapters counts as none and sets DA_DEVERR_INDEX, a rank
  * outside [0, max_rank] is clamped and sets DA_DEVERR_LENGTH; a pipeline wait that
  * hits its time limit sets DA_DEVERR_TIMEOUT and the kernel returns, out and out_bf16
- * are then undefined.  Read the bits of the last call with nvfp4_mm_read_error(ws, ...).
+ * are then undefined.  Read the bits of the last call with nvfp4_mm_read_error(ws, ...);
+ * a call with n = 0 clears them and does nothing else (ws may be NULL).
  * Supported shapes: n >= 0, N a positive multiple of NVFP4_MM_TILE_N, K a
  * positive multiple of 64 up to NVFP4_ADAPTER_MAX_K, max_rank a multiple of 16
  * up to NVFP4_ADAPTER_MAX_RANK, n_adapters >= 1; n * K, n * N below 2^31. */

@@ -1215,7 +1215,12 @@ int nvfp4_mm_adapters(const void* x, int32_t x_dtype, int32_t n, int32_t N, int3
   if (stall < 0 || stall > 2) return DA_ERR_INVALID_ARG;
   if (x_dtype != NVFP4_X_F32 && x_dtype != NVFP4_X_BF16) return DA_ERR_INVALID_ARG;
   if (!shape_ok(n, N, K, n_adapters, max_rank)) return DA_ERR_UNSUPPORTED;
-  if (n == 0) return DA_OK;
+  if (n == 0) {  // nothing to do, and so no errors
+    if (!ws) return DA_OK;
+    if (!aligned_to(ws, 256) || ws_bytes < kHdr) return DA_ERR_WORKSPACE;
+    return cudaMemsetAsync(ws, 0, sizeof(int32_t), static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? DA_OK : DA_ERR_CUDA;
+  }
   if (!x || !a || !b || !ids || !y || !out) return DA_ERR_INVALID_ARG;
   if (!aligned_to(x, 16) || !aligned_to(a, 16) || !aligned_to(b, 16) || !aligned_to(y, 16) ||
       !aligned_to(out, 16) || !aligned_to(out_bf16, 16) || !aligned_to(ids, 4) ||

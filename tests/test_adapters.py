@@ -348,6 +348,20 @@ def test_no_rows(api):
     assert c.run([]).shape == (0, 128)
 
 
+@gpu
+def test_a_call_without_rows_has_no_errors(api):
+    # its workspace needs no initialisation either, and an earlier call's bits go
+    c = Case(api, 3, 128, 64, 2, 16, ranks=None)
+    ws = api.adapters_workspace(3, 128, 64, c.handle)
+    ws.fill_(255)
+    c.run([], ws=ws)
+    assert api.nvfp4_read_error(ws) == 0
+    c.ids[1] = 2
+    c.run(ws=ws)
+    c.run([], ws=ws)
+    assert api.nvfp4_read_error(ws) == 0
+
+
 # ------------------------------------------------------------------ refusals (no GPU)
 
 def test_argument_rules(api):
