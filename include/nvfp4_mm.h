@@ -121,8 +121,9 @@ size_t nvfp4_mm_adapters_workspace_bytes(int32_t n, int32_t N, int32_t K, int32_
  * sums run on the tensor cores with fp32 accumulation over exact products: t
  * enters the second one as three bf16 terms that hold its 24 bits.  Orders are
  * fixed by K and the rank alone, so a row's bits depend only on its own x, y
- * and adapter, not on n, on its place or on the other rows.  A t that overflows
- * bf16's range is an infinity; where B is infinite out is an infinity or NaN.
+ * and adapter, not on n, on its place or on the other rows.  Infinities, NaN and sums
+ * that overflow follow the formulas: a result that does not come out finite is formed
+ * again in plain fp32, in order of r.
  *   x       [n, K], fp32 or bf16 as x_dtype (NVFP4_X_*) says, 16-byte aligned.
  *   a       bf16 [n_adapters, max_rank, K], b  bf16 [n_adapters, N, max_rank],
  *           16-byte aligned.

@@ -172,6 +172,76 @@ def test_an_infinite_low_rank_value_stays_infinite(api):
 
 
 @gpu
+def test_an_infinite_weight_gives_what_the_formula_gives(api):
+    # t = 1.5 (its lower bf16 terms are zero) against an infinite B: an infinity of the
+    # product's sign; NaN only where t is zero or infinities of both signs meet
+    nan, inf = float("nan"), float("inf")
+    x = torch.zeros((3, 64), dtype=torch.bfloat16)
+    x[:, 0] = torch.tensor([1.5, -1.5, 0.0])
+    a = torch.zeros((1, 16, 64), dtype=torch.bfloat16)
+    a[0, :, 0] = 1
+    b = torch.ones((1, 128, 16), dtype=torch.bfloat16)
+    b[0, 3, 2], b[0, 4, 2], b[0, 5, 7], b[0, 5, 8], b[0, 6, 1] = inf, -inf, inf, -inf, nan
+    y = torch.full((3, 128), 0.25)
+    y[1, 7] = inf
+    out = api.nvfp4_adapters(x.cuda(), api.Adapters(a.cuda(), b.cuda()),
+                             torch.zeros(3, dtype=torch.int32, device="cuda"), y.cuda()).cpu()
+    want = torch.tensor([24.25, -23.75, 0.25])[:, None].repeat(1, 128)
+    want[0, 3:5], want[1, 3:5] = torch.tensor([inf, -inf]), torch.tensor([-inf, inf])
+    want[2, 3:5], want[:, 5:7], want[1, 7] = nan, nan, inf
+    assert torch.equal(torch.nan_to_num(out, 7e7, 8e8, -8e8), torch.nan_to_num(want, 7e7, 8e8, -8e8))
+
+
+@gpu
+def test_a_low_rank_value_between_the_largest_of_bf16_and_fp32(api):
+    # t = 2^127 (2 - 2^-7 + 1.5 * 2^-8): beyond bf16, a number in fp32
+    x = torch.zeros((2, 64), dtype=torch.bfloat16)
+    x[0, :2] = torch.tensor([torch.finfo(torch.bfloat16).max, 1.5 * 2.0 ** 119])
+    x[1, :2] = -x[0, :2]
+    a = torch.zeros((1, 16, 64), dtype=torch.bfloat16)
+    a[0, 5, :2] = 1
+    b = torch.zeros((1, 128, 16), dtype=torch.bfloat16)
+    b[0, :64, 5], b[0, 64:, 5] = 0.5, -0.25
+    y = torch.zeros((2, 128))
+    out = api.nvfp4_adapters(x.cuda(), api.Adapters(a.cuda(), b.cuda()),
+                             torch.zeros(2, dtype=torch.int32, device="cuda"), y.cuda()).cpu()
+    t = 2.0 ** 127 * (2 - 2.0 ** -7 + 1.5 * 2.0 ** -8)
+    assert torch.all(out[0, :64] == 0.5 * t) and torch.all(out[0, 64:] == -0.25 * t)
+    assert torch.equal(out[1], -out[0])
+
+
+@gpu
+@pytest.mark.parametrize("max_rank", [48, 112])
+def test_infinities_in_a_large_batch(api, max_rank):
+    # rows with infinite x and infinite weights of some adapters among others: the kinds
+    # of results are the formula's, all finite ones have the bits of a call without them
+    inf, n, N = float("inf"), 700, 256
+    c = Case(api, n, N, 2112, 4, max_rank, seed=71, garbage=False)
+    c.ranks = torch.tensor([max_rank, 1, 2, 17], dtype=torch.int32)
+    c.handle.ranks.copy_(c.ranks)
+    clean = c.run()
+    c.x[::9, 1500] = inf
+    c.x[4::27, 3] = -inf
+    c.b[1, 7, 0], c.b[1, 8, 0], c.b[3, 100, 16], c.b[0, 255, 5] = inf, -inf, inf, float("nan")
+    c.handle.b.copy_(c.b)
+    out = c.run().cpu()
+    hit = torch.zeros((n, N), dtype=torch.bool)
+    for i in range(n):
+        d = int(c.ids[i])
+        if d < 0:
+            continue
+        r = int(c.ranks[d])
+        t = c.a[d, :r].double() @ c.x[i].double()
+        want = c.y[i].double() + float(c.scales[d]) * (c.b[d, :, :r].double() * t).sum(1)
+        odd = ~torch.isfinite(want)
+        assert torch.equal(torch.isnan(out[i]), torch.isnan(want)), i
+        assert torch.equal(out[i][torch.isinf(want)].double(), want[torch.isinf(want)]), i
+        hit[i] = odd
+    assert torch.isinf(out[hit]).sum() > 1000 and torch.isnan(out[hit]).sum() > 1000
+    assert torch.equal(out[~hit], clean.cpu()[~hit])
+
+
+@gpu
 @pytest.mark.parametrize("max_rank,K", [(16, 64), (64, 64), (64, 2176), (128, 2176)])
 def test_low_rank_values_keep_all_their_bits(api, max_rank, K):
     """One-hot rows, so that out = fp32(scale * x) exactly: 24 bits need all three terms.
