@@ -200,8 +200,9 @@ typedef struct nvfp4_logits {
  *                 there is none (every token masked, or -inf or NaN)
  *
  * A row's results depend on that row alone.  out may be x itself (fp32, same
- * stride); otherwise out and tokens overlap no other argument.  List entries at or past a row's
- * length are never read.  A length below 0 or above its width is clamped and
+ * stride); otherwise out and tokens overlap no other argument (rows of x and out that
+ * lie in turn in one buffer need strides of the same size in bytes).  List entries at
+ * or past a row's length are never read.  A length below 0 or above its width is clamped and
  * sets DA_DEVERR_LENGTH; a token outside [0, V) is skipped and a mask id at or
  * above n_masks counts as none, both set DA_DEVERR_INDEX.  Bits are OR-ed into
  * *err, never cleared.  Alignment: that of the element types; rows that start

@@ -566,6 +566,21 @@ auto* pick(bool vec, bool shift, bool narrow) {
   return narrow ? pick<BF16, uint16_t>(vec, shift) : pick<BF16, uint32_t>(vec, shift);
 }
 
+// Whether `rows` rows of a_bytes at a and of b_bytes at b, strides apart, share a byte.
+// Rows with one stride may interleave; with two, nothing is told but that the buffers
+// lie apart.
+bool rows_overlap(uintptr_t a, long long a_bytes, long long a_stride, uintptr_t b, long long b_bytes,
+                  long long b_stride, long long rows) {
+  const uintptr_t a_end = a + (rows - 1) * a_stride + a_bytes;
+  const uintptr_t b_end = b + (rows - 1) * b_stride + b_bytes;
+  if (a >= b_end || b >= a_end) return false;
+  if (a_stride != b_stride) return true;
+  // rows i of a and j of b meet if b - a + (j - i) stride lies in (-b_bytes, a_bytes): with
+  // buffers that touch, one of the two values next to zero is taken by some i and j
+  const long long at = (long long)(b - a) % a_stride, on = at < 0 ? at + a_stride : at;
+  return on < a_bytes || on > a_stride - b_bytes;
+}
+
 // A list is given whole or not at all (one without room needs no tokens).
 bool list_ok(const int32_t* list, const int32_t* lens, int width) {
   if (width < 0 || (width > 0 && (list != nullptr) != (lens != nullptr))) return false;
@@ -605,10 +620,10 @@ extern "C" int nvfp4_mm_logits(const nvfp4_logits* g, void* stream) {
   if (g->out) {  // in place row for row, or apart
     const uintptr_t x = reinterpret_cast<uintptr_t>(g->x);
     const uintptr_t o = reinterpret_cast<uintptr_t>(g->out);
-    const uintptr_t x_end = x + ((g->batch - 1LL) * g->x_stride + g->vocab) * (bf16 ? 2 : 4);
-    const uintptr_t o_end = o + ((g->batch - 1LL) * g->out_stride + g->vocab) * 4;
     const bool same = x == o && !bf16 && g->x_stride == g->out_stride;
-    if (!same && x < o_end && o < x_end) return DA_ERR_INVALID_ARG;
+    const long long size = bf16 ? 2 : 4, V = g->vocab;
+    if (!same && rows_overlap(x, V * size, g->x_stride * size, o, V * 4, g->out_stride * 4, g->batch))
+      return DA_ERR_INVALID_ARG;
   }
   Args a;
   std::memset(&a, 0, sizeof(a));

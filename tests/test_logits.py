@@ -180,6 +180,25 @@ def test_rows_that_start_off_a_boundary(api, x, V, pad, lead, apart):
 
 
 @gpu
+@pytest.mark.parametrize("x", ["fp32", "bf16"])
+def test_rows_of_x_and_out_side_by_side(api, x):
+    # one buffer's rows hold both: they interleave and do not overlap
+    B, V = 5, 1500
+    c = Case(B, V, x=x, seed=6)
+    packed = torch.empty((B, V), device="cuda")
+    want = api.nvfp4_logits(c.x.cuda(), out=packed, **c.kwargs())
+    size = 4 if x == "fp32" else 2
+    for x_first in (True, False):
+        rows = torch.full((B, V * (size + 4)), 77, dtype=torch.uint8, device="cuda")
+        cut = V * (size if x_first else 4)
+        xs, out = (rows[:, :cut], rows[:, cut:]) if x_first else (rows[:, cut:], rows[:, :cut])
+        xs, out = xs.view(c.x.dtype), out.view(torch.float32)
+        xs.copy_(c.x)
+        assert torch.equal(api.nvfp4_logits(xs, out=out, **c.kwargs()), want)
+        assert torch.equal(out, packed) and torch.equal(xs, c.x.cuda())
+
+
+@gpu
 def test_in_place_and_tokens_only(api):
     c = Case(9, 3001, seed=31, repeat_bias=True, bias=40)
     x = c.x.cuda().contiguous()
@@ -387,6 +406,25 @@ def test_argument_rules(api):
     assert call(out=fake + 4000) == bad                # inside x
     assert call(out=fake, out_stride=1004) == bad      # in place, other rows
     assert call(x_dtype=api.X_BF16, out=fake) == bad   # in place, other type
+
+
+def test_rows_that_interleave_and_overlap(api):
+    fake = 1 << 20  # never dereferenced: every case is refused before any device work
+
+    def call(**kw):
+        a = dict(batch=3, vocab=1000, x_dtype=api.X_F32, x=fake, x_stride=2500, out_stride=2500,
+                 tokens=fake)
+        a.update(kw)
+        g = api.Nvfp4Logits(**a)
+        return api.lib().nvfp4_mm_logits(ctypes.addressof(g), None)
+    for at in (4, 999, 1501, 2499, 2500, 2501, 5000, 5999, -4, -999, -2500, -2501, -5999):
+        assert call(out=fake + 4 * at) == api.ERR_INVALID_ARG, at
+    # bf16 x, rows of the same size: 500 words of x to 1000 of out
+    half = dict(x_dtype=api.X_BF16, x_stride=5000)
+    for at in (0, 499, 1501, 2500, 2999, -1, -999, -2500, -5999):
+        assert call(out=fake + 4 * at, **half) == api.ERR_INVALID_ARG, at
+    # rows of two sizes: refused as soon as the two buffers touch
+    assert call(out=fake + 4000, out_stride=2504) == api.ERR_INVALID_ARG
 
 
 def test_python_refusals(api):
