@@ -796,7 +796,7 @@ __device__ void up_produce(const Ctx& c, const Args& g, UpWalk walk) {
 
 // t of a tile's members: chunk sums added in order, scaled, split.  Warp w takes
 // members w, w + 4, ...; a lane two ranks of each 64.
-template <int R>
+template <int R, bool WIDE>
 __device__ void up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
   constexpr int S = Up<R>::kTSlots;
   const int lane = threadIdx.x & 31, w = up_helper(threadIdx.x >> 5) - kUpProdWarps;
@@ -819,10 +819,8 @@ __device__ void up_make_t(const Ctx& c, const Args& g, UpWalk walk) {
     if (lane < walk.count) row_lo = walk.tiles.order[walk.first + lane];
     if (lane + 32 < walk.count) row_hi = walk.tiles.order[walk.first + lane + 32];
     // kBatch members and kDeep chunks at once: their loads are in flight together (one
-    // by one a tile of 64 took 25 us; with four members and two chunks one row takes
-    // 13.9 us for 13.2, 67 rows 30.1 for 28.7, 1910 rows of a single chunk 45 for 52; both
-    // forms side by side spill)
-    constexpr int kBatch = 2, kDeep = 4;
+    // by one a tile of 64 took 25 us; four of each spill)
+    constexpr int kBatch = WIDE ? 4 : 2, kDeep = WIDE ? 2 : 4;
     for (int m0 = w; m0 < walk.count; m0 += kBatch * kUpTWarps) {
 #pragma unroll
       for (int reg = 0; reg < R; ++reg) {
@@ -1084,7 +1082,7 @@ __device__ void up_epilogue(const Ctx& c, const Args& g, UpWalk walk, uint32_t t
   }
 }
 
-template <int R>
+template <int R, bool WIDE>
 __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Window own;
@@ -1158,7 +1156,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) up_kernel(const Args g) {
     if (h < kUpProdWarps)
       up_produce<R>(c, g, walk);
     else if (h < kUpProdWarps + kUpTWarps)
-      up_make_t<R>(c, g, walk);
+      up_make_t<R, WIDE>(c, g, walk);
     else
       up_fetch_y<R>(c, g, walk);
   }
@@ -1232,12 +1230,17 @@ cudaError_t launch_down(const Args& g, int sms, cudaStream_t st) {
   return launch_after(down_kernel<BF16, S>, dim3(grid), dim3(kDownThreads), (size_t)smem, st, g);
 }
 
-template <int R>
+// WIDE: t of twice as many members at once, two chunks of K at a time instead of four.
+// For K of up to two chunks, where the others would be empty, and rows for full tiles
+// (4096 features, us: 1910 rows of rank 64 and K = 1024 47.0, else 48.9, of rank 128
+// and K = 2048 63.4 and 67.1, 140 rows 26.8 and 27.7; K = 4096, 1910 rows of rank 64
+// 55.7 and 52.2; K = 1024, 67 rows of rank 64 19.6 and 19.2).
+template <int R, bool WIDE>
 cudaError_t launch_up(const Args& g, int sms, cudaStream_t st) {
-  cudaError_t e = allow_smem(up_kernel<R>, Up<R>::kSmem);
+  cudaError_t e = allow_smem(up_kernel<R, WIDE>, Up<R>::kSmem);
   if (e != cudaSuccess) return e;
   const int grid = (int)std::min<long long>((long long)g.n * (g.N / kFeat), sms);
-  return launch_after(up_kernel<R>, dim3(grid), dim3(kUpThreads), (size_t)Up<R>::kSmem, st, g);
+  return launch_after(up_kernel<R, WIDE>, dim3(grid), dim3(kUpThreads), (size_t)Up<R>::kSmem, st, g);
 }
 
 }  // namespace
@@ -1316,7 +1319,9 @@ int nvfp4_mm_adapters(const void* x, int32_t x_dtype, int32_t n, int32_t N, int3
   // region of a slot, higher ones two
   auto* down = max_rank <= 64 ? (bf16 ? launch_down<true, 6> : launch_down<false, 6>)
                               : (bf16 ? launch_down<true, 4> : launch_down<false, 4>);
-  auto* up = max_rank <= 64 ? launch_up<1> : launch_up<2>;
+  const bool wide = g.n_chunks <= 2 && n > 2 * kTile;
+  auto* up = max_rank <= 64 ? (wide ? launch_up<1, true> : launch_up<1, false>)
+                            : (wide ? launch_up<2, true> : launch_up<2, false>);
   for (int r0 = 0; r0 < n; r0 += kSlab) {
     const size_t row = (size_t)r0;
     g.n = std::min(kSlab, n - r0);

@@ -269,13 +269,13 @@ def test_low_rank_values_keep_all_their_bits(api, max_rank, K):
 
 
 @gpu
-@pytest.mark.parametrize("max_rank", [64, 128])
-@pytest.mark.parametrize("x", ["bf16", "fp32"])
-def test_many_full_tiles_for_each_cta(api, max_rank, x):
+@pytest.mark.parametrize("max_rank,x,K", [(64, "bf16", 1088), (64, "fp32", 1088), (128, "bf16", 1088),
+                                          (128, "fp32", 1088), (64, "fp32", 2112), (128, "bf16", 2112)])
+def test_many_full_tiles_for_each_cta(api, max_rank, x, K):
     """More units than the CTAs have stages, slots and accumulators, at full tiles: 152
     CTAs take eight units of 128 features, or eight of a tile and a part of K, from
     four tiles.  Every element against fp64, and some rows bit for bit alone."""
-    n, N, K, count = 40000, 256, 1088, 5
+    n, N, count = 40000, 256, 5
     ids = np.arange(n) * count // n
     c = Case(api, n, N, K, count, max_rank, x=x, ids=ids, ranks=None, seed=max_rank)
     both = torch.empty((n, N), dtype=torch.bfloat16, device="cuda")
