@@ -266,6 +266,7 @@ def test_angles_far_beyond_32_bits(api):
     pos = [1, 4095, (1 << 24) + 1, (1 << 30) + 12345, (1 << 31) - 1, (1 << 31) - 77]
     c = Case(api, n=6, layout="indexed", rope=(128, 0, False), x="fp32", positions=pos)
     c.inv = torch.exp2(torch.linspace(-4, 18, 64, dtype=torch.float64)).float()
+    c.inv[1::3] *= -1
     c.rope = api.rope(c.inv.cuda())
     c.check_q(c.run(api))
     c.check_caches()
@@ -278,6 +279,52 @@ def test_prompts_of_many_tokens(api, kv):
              seed=15)
     c.check_q(c.run(api))
     c.check_caches()
+
+
+@gpu
+def test_frequencies_at_the_ends_of_their_range(api):
+    # denormal and tiny ones turn by nothing, zero by nothing at all, in both directions
+    c = Case(api, n=5, layout="indexed", rope=(128, 0, True), x="fp32",
+             positions=[0, 1, 7, 1 << 20, (1 << 31) - 1])
+    c.inv = torch.cat([torch.tensor([0.0, -0.0, 1e-45, -1e-40, 2.0 ** -126, 2.0 ** -100, -(2.0 ** -64)]),
+                       torch.exp2(torch.linspace(-60, 17, 57, dtype=torch.float64)).float()])
+    c.rope = api.rope(c.inv.cuda(), interleaved=True)
+    c.check_q(c.run(api))
+    c.check_caches()
+
+
+@gpu
+@pytest.mark.parametrize("kv", KV)
+def test_entries_beyond_32_bits(api, kv):
+    """A cache of more than 2^32 elements: entries at both ends and around 2^31 and 2^32
+    elements get what the same tokens get in a small cache."""
+    n, H_kv, D = 7, 8, 128
+    slots = (1 << 22) + 5  # 1024 elements each
+    at = torch.tensor([0, (1 << 21) - 1, 1 << 21, (1 << 22) - 1, 1 << 22, slots - 2, slots - 1])
+    g = torch.Generator().manual_seed(7)
+    k_new, v_new = (torch.randn((n, H_kv, D), generator=g).cuda() for _ in range(2))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    rope = api.rope(torch.rand(64, generator=g).cuda())
+    got = []
+    for count, rows in ((n, torch.arange(n)), (slots, at)):
+        prob = api.problem(batch=1, num_q_heads=H_kv, num_kv_heads=H_kv, head_dim_qk=D, layout="indexed",
+                           scale=0.1, width=1, num_blocks=count, kv_dtype=KV.index(kv), k_scale=K_SCALE,
+                           v_scale=V_SCALE)
+        m = count * H_kv * D
+        size = {"bf16": 2 * m, "e4m3": m, "nvfp4": m // 2 + m // 16}[kv]
+        pair = [torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        k, v = (t.view(torch.bfloat16) if kv == "bf16" else t for t in pair)
+        api.append(prob, rope, k_new, v_new, k, v, torch.arange(n, **i32), rows=rows.to(**i32))
+        for t in pair:
+            parts = [t[:m // 2], t[m // 2:]] if kv == "nvfp4" else [t]
+            got.append([p.view(count, -1)[rows.cuda()] for p in parts])
+            written = sum(int(torch.count_nonzero(p.view(count, -1).view(torch.int32).any(1)))
+                          for p in parts)
+            assert written == n * len(parts)
+        del pair, k, v, t, parts
+    torch.cuda.empty_cache()
+    for small, large in ((got[0], got[2]), (got[1], got[3])):
+        assert all(torch.equal(a, b) for a, b in zip(small, large))
 
 
 @gpu
