@@ -199,6 +199,33 @@ def test_rows_of_x_and_out_side_by_side(api, x):
 
 
 @gpu
+@pytest.mark.parametrize("B,V", [(2, 1 << 30), (3, (1 << 30) - 1), (17000, 131073)])
+def test_offsets_beyond_32_bits(api, B, V):
+    """More than 2^31 logits: the largest vocabulary, and many rows."""
+    x = torch.zeros((B, V), device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    last = B - 1
+    x[0, V - 1], x[0, V - 2], x[last, V - 1], x[last, 5] = 5.0, 4.0, -1.0, 2.0
+    prompt = torch.full((B, 1), V - 1, **i32)
+    lens = torch.zeros(B, **i32)
+    lens[0] = lens[last] = 1
+    bias = torch.zeros((B, 1), **i32)
+    bias[last] = V - 7
+    out = torch.empty_like(x)
+    tokens = api.nvfp4_logits(x, prompt=prompt, prompt_lens=lens, out=out, bias_tokens=bias,
+                              repetition=torch.full((B,), 2.0, device="cuda"),
+                              bias_values=torch.full((B, 1), 3.0, device="cuda"),
+                              bias_lens=torch.where(torch.arange(B, device="cuda") == last, 1, 0).int())
+    x[0, V - 1], x[last, V - 1], x[last, V - 7] = 2.5, -2.0, 3.0
+    assert all(torch.equal(out[b0:b0 + 1000], x[b0:b0 + 1000]) for b0 in range(0, B, 1000))
+    want = torch.zeros(B, dtype=torch.int32)
+    want[0], want[last] = V - 2, V - 7
+    assert torch.equal(tokens.cpu(), want)
+    del x, out
+    torch.cuda.empty_cache()
+
+
+@gpu
 def test_in_place_and_tokens_only(api):
     c = Case(9, 3001, seed=31, repeat_bias=True, bias=40)
     x = c.x.cuda().contiguous()
