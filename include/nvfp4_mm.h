@@ -152,7 +152,9 @@ int nvfp4_mm_adapters(const void* x, int32_t x_dtype, int32_t n, int32_t N, int3
 
 /* ---- logits ------------------------------------------------------------ */
 
-/* Entries of a row's bias list at most: each of its tokens is looked for in it. */
+/* Entries of a row's bias list at most: each of its tokens is looked for in it, so
+ * that the work grows with the square (33 rows of 50001 tokens: 12 us with 40
+ * entries, 49 with 400, 657 with 4096). */
 #define NVFP4_LOGITS_MAX_BIAS 4096
 
 /* What a decode step does to the logits of its vocabulary projection (nvfp4_mm's

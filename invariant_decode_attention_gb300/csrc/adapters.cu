@@ -7,7 +7,9 @@
 //         tiles of at most 64 rows (the columns of the matrix products).  Prompts,
 //         whose rows come in runs, give full tiles; a decode step's scattered rows
 //         meet their adapter's others anywhere in the window, so an adapter's
-//         weights are read once per 64 rows that use it.  A kernel of its own; with
+//         weights are read once per 64 rows of a window that use it.  (Groups do not
+//         go beyond a window: 8192 rows that use 64 adapters in no order make 1024
+//         tiles of eight rows and take 540 us, in runs 161.)  A kernel of its own; with
 //         one window both matmul kernels make the plan for themselves instead.
 //   down  t: D[rank, member] += A[rank, k] x[member, k] on the tensor cores
 //         (tcgen05, M = 128 of which the adapter's ranks count, N = 64, fp32 in
@@ -16,7 +18,9 @@
 //   up    out: D[feature, member] += B[feature, r] t[member, r], M = 128 features,
 //         N = 64.  The chunk sums of t are added in order, scaled, and split into
 //         three bf16 terms that hold their 24 bits; their products with B are
-//         exact, so out keeps fp32 accuracy.  A unit is a tile and 128 features.
+//         exact, so out keeps fp32 accuracy (the tensor cores' accumulation of both
+//         products leaves an error of 5e-7 of a result's usual size at K = 4096; a
+//         library's fp32 products 1.6e-7).  A unit is a tile and 128 features.
 //         y arrives in shared memory, 16 rows at a time; the epilogue adds the
 //         products to it there and writes whole 128-byte lines, 16 bytes a lane
 //         (loads and stores of 4 bytes a lane took 4900 instructions a unit of 32
@@ -37,13 +41,14 @@
 //
 // A parity tells a phase of a barrier from the one before it only, so every waiter
 // goes through all phases of the barriers it waits on, in order: a stage, a slot or
-// an accumulator has one issuer and one epilogue group.
+// an accumulator has one issuer and one epilogue group; what both issuers release has
+// a barrier of each.
 //
 // y and out (8 N bytes a row) bound a prompt, the adapters' weights and launch
 // latency a decode step.  Measured, 4096 -> 8192 features: 8192 rows of rank 64 with
-// the bf16 copy 168 us (plan 8, down 28, up 133: 5.0 TB/s, 0.74 of a plain copy's
-// rate, hand-offs between roles set the pace); 67 rows with 24 adapters 28.7 us; one
-// row 13.2 us.
+// the bf16 copy 166 us (plan 8, down 27, up 132: 5.1 TB/s, 0.75 of a plain copy's
+// rate, hand-offs between roles set the pace); 67 rows with 24 adapters 29.2 us; one
+// row 13.1 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -10,8 +10,9 @@
 // once for all its heads; the loads of its first units are issued before the
 // angles are needed, so one round trip to memory covers both.  Warps do not wait
 // for one another.  Measured: 16384 tokens of 32/8 heads of 128, bf16, 64 us (6.3
-// TB/s, 0.93 of a plain copy's rate); one token 2.5 us; 2047 tokens into an NVFP4
-// cache 15.7 us.
+// TB/s, 0.93 of a plain copy's rate); one token 2.6 us; 2047 tokens into an NVFP4
+// cache 15.7 us (into E4M3 13.2, bf16 11.9: one wave of latency-bound warps, then
+// divisions, block scales and partners that are read a second time).
 //
 // Angles: position * inv_freq is the product of a 31-bit integer, a 24-bit integer and
 // a power of two.  Multiplied by 2^128 / (2 pi) in integers, its whole turns are
@@ -34,7 +35,7 @@ namespace {
 constexpr int kWarps = 4;       // per CTA; each works by itself
 constexpr int kMaxPairs = 288;  // rope_dim / 2 at most (576 / 2)
 // Units that a lane has in flight (48 bytes or so a chunk pair of bf16; measured
-// on 16384 tokens of 32/8 heads: one 75, two 70, three 67 us).
+// on 16384 tokens of 32/8 heads: one 71, two and three 64 us).
 template <typename X>
 constexpr int kInFlight = sizeof(X) == 2 ? 3 : 2;
 // CTAs that an SM holds at once (72 and 96 registers a thread).
@@ -340,9 +341,9 @@ cudaError_t launch_dim(const AppendLaunch& p, int sms, cudaStream_t stream) {
   const int units = (D / 16) * ((p.q_new ? p.H_q : 0) + p.H_kv * (p.v_new ? 2 : 1));
   // a warp takes a whole token once there are enough of them; fewer tokens are
   // cut, down to one unit a lane, so that all SMs have work, into no more parts than
-  // the GPU holds at once (64 tokens of 128 heads of 576: 5.3 us with these 28 warps
-  // per SM, 6.4 with 32, 7.8 with 64; 2047 tokens of 32/8 heads into NVFP4: 16.1,
-  // 16.1 and 19.5, with 20 warps 19.6)
+  // the GPU holds at once (64 tokens of 128 heads of 576: 4.6 us with these 28 warps
+  // per SM, 5.3 with 32, 6.2 with 64; 2047 tokens of 32/8 heads into NVFP4: 15.7,
+  // 15.7 and 18.4, with 20 warps 19.2)
   const long long want = (long long)kResident<X> * kWarps * sms;  // warps
   long long parts = std::max<long long>(1, want / p.n_tokens);
   parts = std::min<long long>(parts, (units + 31) / 32);
