@@ -165,7 +165,7 @@ typedef struct nvfp4_logits {
   int32_t vocab;             /* V tokens, 1 .. 2^30                              */
   int32_t x_dtype;           /* NVFP4_X_* of x                                 */
   const void* x;             /* [B, V], rows x_stride elements apart           */
-  int64_t x_stride;          /* >= V                                           */
+  int64_t x_stride;          /* V .. 2^40 (one row: >= V)                       */
   const int32_t* prompt;     /* int32 [B, prompt_width]: the prompt's tokens   */
   const int32_t* prompt_lens; /* int32 [B]                                     */
   int32_t prompt_width;
@@ -185,7 +185,7 @@ typedef struct nvfp4_logits {
                              /* NULL: row b has mask b                         */
   int32_t n_masks;
   float* out;                /* fp32 [B, V], rows out_stride apart, or NULL    */
-  int64_t out_stride;        /* >= V                                           */
+  int64_t out_stride;        /* V .. 2^40 (one row: >= V)                       */
   int32_t* tokens;           /* int32 [B] or NULL                              */
   int32_t* err;              /* device word for DA_DEVERR_* bits, or NULL      */
 } nvfp4_logits;

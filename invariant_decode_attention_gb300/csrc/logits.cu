@@ -43,6 +43,7 @@ constexpr int kDense = 3;            // list entries per so many tokens of a sli
 constexpr int kScan = 8;           // list entries a thread has in flight
 constexpr int kMaxVocab = 1 << 30;  // keeps token arithmetic in 32 bits
 constexpr int kCluster = 8;     // CTAs per row at most (the portable cluster size)
+constexpr long long kMaxStride = 1ll << 40;  // elements
 
 // A token's word: "in the prompt", "has a bias", "is listed", and its count in
 // the output.  Two bytes do for outputs of up to 2^13 - 1 tokens and double a
@@ -617,19 +618,23 @@ extern "C" int nvfp4_mm_logits(const nvfp4_logits* g, void* stream) {
   if (g->bias_width > NVFP4_LOGITS_MAX_BIAS ||
       (long long)g->prompt_width + g->output_width + g->bias_width > Word<uint32_t>::kMostOutput)
     return DA_ERR_UNSUPPORTED;  // (the count of a token in the output has 29 bits)
+  // one row has no stride; those of more rows stay where bytes can be counted
+  const long long V = g->vocab, x_stride = g->batch > 1 ? g->x_stride : V;
+  const long long out_stride = g->out && g->batch > 1 ? g->out_stride : V;
+  if (x_stride > kMaxStride || out_stride > kMaxStride) return DA_ERR_INVALID_ARG;
   if (g->out) {  // in place row for row, or apart
     const uintptr_t x = reinterpret_cast<uintptr_t>(g->x);
     const uintptr_t o = reinterpret_cast<uintptr_t>(g->out);
-    const bool same = x == o && !bf16 && g->x_stride == g->out_stride;
-    const long long size = bf16 ? 2 : 4, V = g->vocab;
-    if (!same && rows_overlap(x, V * size, g->x_stride * size, o, V * 4, g->out_stride * 4, g->batch))
+    const long long size = bf16 ? 2 : 4;
+    const bool same = x == o && !bf16 && x_stride == out_stride;
+    if (!same && rows_overlap(x, V * size, x_stride * size, o, V * 4, out_stride * 4, g->batch))
       return DA_ERR_INVALID_ARG;
   }
   Args a;
   std::memset(&a, 0, sizeof(a));
   a.x = g->x;
-  a.x_stride = g->x_stride;
-  a.out_stride = g->out_stride;
+  a.x_stride = x_stride;
+  a.out_stride = out_stride;
   a.prompt = g->prompt;
   a.prompt_lens = g->prompt_lens;
   a.output = g->output;
@@ -654,8 +659,8 @@ extern "C" int nvfp4_mm_logits(const nvfp4_logits* g, void* stream) {
   // groups of four: x and out must have their boundaries at the same tokens of a row
   const long long x_at = (long long)(reinterpret_cast<uintptr_t>(g->x) / (bf16 ? 2 : 4));
   const long long out_at = (long long)(reinterpret_cast<uintptr_t>(g->out) / 4);
-  const bool vec = !g->out || ((x_at - out_at) % 4 == 0 && (g->x_stride - g->out_stride) % 4 == 0);
-  const bool shift = x_at % 4 != 0 || g->x_stride % 4 != 0;
+  const bool vec = !g->out || ((x_at - out_at) % 4 == 0 && (x_stride - out_stride) % 4 == 0);
+  const bool shift = x_at % 4 != 0 || (g->batch > 1 && x_stride % 4 != 0);
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)

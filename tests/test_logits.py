@@ -454,6 +454,26 @@ def test_rows_that_interleave_and_overlap(api):
     assert call(out=fake + 4000, out_stride=2504) == api.ERR_INVALID_ARG
 
 
+def test_strides_without_end(api):
+    fake = 1 << 20  # never dereferenced: every case is refused before any device work
+
+    def call(**kw):
+        a = dict(batch=3, vocab=1000, x_dtype=api.X_F32, x=fake, x_stride=1000, out=1 << 28,
+                 out_stride=1000, tokens=fake)
+        a.update(kw)
+        g = api.Nvfp4Logits(**a)
+        return api.lib().nvfp4_mm_logits(ctypes.addressof(g), None)
+    for big in ((1 << 40) + 1, 1 << 61, 1 << 62, (1 << 63) - 1):
+        for x_dtype in (api.X_F32, api.X_BF16):
+            both = dict(x_stride=big, out_stride=big, x_dtype=x_dtype)
+            assert call(**both) == api.ERR_INVALID_ARG
+            assert call(**both, out=fake + 64) == api.ERR_INVALID_ARG
+            # one row's stride does not matter, but that it overlaps does
+            assert call(**both, batch=1, out=fake + 64) == api.ERR_INVALID_ARG
+        assert call(x_stride=big) == api.ERR_INVALID_ARG
+        assert call(out_stride=big) == api.ERR_INVALID_ARG
+
+
 def test_python_refusals(api):
     t = lambda *s, dtype=torch.float32: torch.zeros(s, dtype=dtype)  # noqa: E731
     i32 = torch.int32
