@@ -226,6 +226,19 @@ def test_offsets_beyond_32_bits(api, B, V):
 
 
 @gpu
+@pytest.mark.parametrize("x", ["fp32", "bf16"])
+@pytest.mark.parametrize("V", [2, 33, 2049, 6147, 50001])
+def test_single_rows_of_any_length(api, x, V):
+    # one row takes no notice of a stride: aligned, it moves in groups of four to its last step
+    c = Case(1, V, x=x, seed=V, prompt=60, output=50, bias=min(6, V))
+    out = torch.full((1, V + 3), 5.0, device="cuda")
+    tokens = api.nvfp4_logits(c.x.cuda(), out=out[:, :V], **c.kwargs())
+    c.check(out[:, :V], tokens)
+    assert torch.all(out[:, V:] == 5.0)
+    assert torch.equal(api.nvfp4_logits(c.x.cuda(), **c.kwargs()), tokens)
+
+
+@gpu
 def test_in_place_and_tokens_only(api):
     c = Case(9, 3001, seed=31, repeat_bias=True, bias=40)
     x = c.x.cuda().contiguous()
