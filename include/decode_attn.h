@@ -380,6 +380,82 @@ typedef struct da_append {
 int decode_attn_append(const da_problem* prob, const da_rope* rope, const da_append* args,
                        void* stream);
 
+/* Norms of the heads of queries and keys before their rotation: each head x of D
+ * dims becomes, in fp32 with one rounding for each operation,
+ *     r = 1 / sqrt(sum x^2 / D + eps),   y = (x * r) * (w + w_add)
+ * with the weights w shared by all heads.  Values are not normed.  A sum of
+ * squares beyond fp32's range makes r zero. */
+typedef struct da_head_norm {
+  const void* q_weight; /* device [D_qk], 16-byte aligned; NULL: queries as they are */
+  const void* k_weight; /* the same for keys                                  */
+  int32_t w_dtype;      /* DA_X_* of both                                     */
+  float w_add;          /* finite: 0, or 1 for weights kept as their distance from 1 */
+  float eps;            /* finite, >= 0                                       */
+} da_head_norm;
+
+/* decode_attn_append with norms and with entries of their own: the norm and the
+ * rotation of a head, and its storage, in the same pass.
+ *   norm    NULL: no norms.  Separate caches only (DA_ERR_UNSUPPORTED for a shared
+ *           latent one, whose norm does not span a head); q_weight needs queries.
+ *   entries int32 [n_tokens] or NULL: token i goes to entry entries[i] of its batch
+ *           row and is rotated by positions[i], as the nodes of a tree of drafted
+ *           tokens need it (decode_attn_tree: node t at entry length + t, at position
+ *           length + its depth).  NULL: entry positions[i].  Contiguous and paged
+ *           layouts (an indexed cache has its slots in rows already).  An entry
+ *           out of [0, capacity) or a negative position sets DA_DEVERR_LENGTH and
+ *           the token is left out.
+ * Everything else is as for decode_attn_append; a token's results depend on that
+ * token alone. */
+int decode_attn_append_norm(const da_problem* prob, const da_rope* rope, const da_head_norm* norm,
+                            const da_append* args, const int32_t* entries, void* stream);
+
+/* ---- moving entries of the caches ------------------------------------ */
+
+/* Nodes of a tree of drafted tokens at most. */
+#define DA_TREE_MAX_NODES 64
+
+/* The caches of a model's layers, all of one geometry (that of the problem given
+ * beside them) and none overlapping another.  k and v are host arrays of device
+ * pointers, each 16-byte aligned; they are read before a call returns. */
+typedef struct da_caches {
+  int32_t n_layers;  /* >= 1                                                  */
+  void* const* k;    /* [n_layers]                                            */
+  void* const* v;    /* [n_layers]; NULL for a shared latent cache            */
+} da_caches;
+
+/* Copy pages (paged layout) or slots (indexed) in the caches of all layers: page
+ * dst[i] becomes what page src[i] is, for i < n (device int32 arrays).  What a fork
+ * of a row needs for its last, partly filled page, and what moves pages together;
+ * which page belongs to whom is the caller's affair.  Pairs with a negative number
+ * and pairs of a page with itself copy nothing.  A page may be a source many times;
+ * one that is a destination may neither be one twice nor be a source of another pair
+ * (its contents are unspecified).  Page ids at or above num_blocks copy nothing and
+ * set DA_DEVERR_INDEX in *err (NULL: not reported; bits are OR-ed, never cleared). */
+int decode_attn_copy_pages(const da_problem* prob, const da_caches* caches, const int32_t* src,
+                           const int32_t* dst, int32_t n, int32_t* err, void* stream);
+
+/* After a tree of drafted tokens has been verified (nvfp4_mm_verify): the entries of
+ * the accepted nodes of each row b move behind its context, in the caches of all
+ * layers.  With L = lengths[b] and m = accepted[b] + 1 nodes (the root and what was
+ * accepted), entry L + nodes[b, i] becomes entry L + i for i < m, all read before any
+ * is written; new_lengths[b] = L + m.  A row whose nodes[b, 0] is negative has no
+ * nodes: m = 0.
+ *   table       as attention reads it (NULL for contiguous).
+ *   lengths     int32 [B], entries before the tree.
+ *   nodes       int32 [B, nodes_width], 1 <= nodes_width <= DA_TREE_MAX_NODES, the
+ *               first m of a row ascending.
+ *   accepted    int32 [B], in [0, nodes_width).
+ *   new_lengths int32 [B] or NULL; overlaps none of the other arrays.
+ * A row is left as it is, with new_lengths[b] = L, where accepted is out of range or
+ * L is (DA_DEVERR_LENGTH; L is clamped to [0, capacity]) or where its nodes do not ascend below
+ * nodes_width, an entry lies beyond its capacity or a page id is out of range
+ * (DA_DEVERR_INDEX), with the bits OR-ed into *err (NULL: not reported).  Entries
+ * that move may not be shared with another row.  The lists are the same for all
+ * layers, so one call, one launch for up to 64 layers, serves a whole model. */
+int decode_attn_compact(const da_problem* prob, const da_caches* caches, const int32_t* table,
+                        const int32_t* lengths, const int32_t* nodes, int32_t nodes_width,
+                        const int32_t* accepted, int32_t* new_lengths, int32_t* err, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

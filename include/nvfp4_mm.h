@@ -212,6 +212,80 @@ typedef struct nvfp4_logits {
  * workspace. */
 int nvfp4_mm_logits(const nvfp4_logits* args, void* stream);
 
+/* ---- verifying drafted tokens ------------------------------------------ */
+
+#define NVFP4_VERIFY_MAX_NODES 64        /* of a request's tree                     */
+#define NVFP4_VERIFY_MAX_VOCAB (1 << 19) /* weights are 44-bit integers, sums 64-bit */
+
+/* A batch of requests with drafted tokens and the target model's logits at each.
+ * Plain data.  Node 0 of a request is its last token, known already; node t >= 1 is a
+ * drafted token that follows its parent's. */
+typedef struct nvfp4_verify {
+  int32_t batch;             /* B >= 0 requests                                  */
+  int32_t nodes;             /* T: 1 .. NVFP4_VERIFY_MAX_NODES, node 0 included  */
+  int32_t vocab;             /* V: 1 .. NVFP4_VERIFY_MAX_VOCAB                   */
+  int32_t x_dtype;           /* NVFP4_X_* of x                                   */
+  const void* x;             /* logits [B, T, V]: of what follows node t         */
+  int64_t x_stride;          /* elements between requests: V .. 2^40 (one: any)  */
+  int64_t x_node_stride;     /* elements between nodes: the same                 */
+  const float* draft;        /* fp32 [B, T, V] or NULL: the probabilities that   */
+                             /* node t's token was drawn from (node 0: not read) */
+  int64_t draft_stride;      /* as x's strides                                   */
+  int64_t draft_node_stride;
+  const int32_t* tokens;     /* int32 [B, T]: node t's token (node 0: not read)  */
+  const int32_t* parents;    /* int32 [B, T]: the parent of node t, below t;     */
+                             /* NULL: t - 1, a chain                             */
+  const int32_t* counts;     /* int32 [B]: nodes that a request has; NULL: T     */
+  const float* temperature;  /* fp32 [B] or NULL (1); 0: greedy                  */
+  const float* uniforms;     /* fp32 [B, T] random numbers in [0, 1), node by node */
+  const float* final_uniforms; /* fp32 [B]: the next token's                     */
+  int32_t* accepted;         /* int32 [B]: drafted tokens accepted               */
+  int32_t* out_nodes;        /* int32 [B, T]: 0, the accepted nodes, then -1     */
+  int32_t* out_tokens;       /* int32 [B, T]: their tokens, the next one, then -1 */
+  int32_t* err;              /* device word for DA_DEVERR_* bits, or NULL        */
+  void* ws;                  /* workspace, 256-byte aligned                      */
+  size_t ws_bytes;
+} nvfp4_verify;
+
+/* Workspace bytes of one call (0: not supported).  Needs no initialisation. */
+size_t nvfp4_mm_verify_workspace_bytes(int32_t batch, int32_t nodes, int32_t vocab);
+
+/* Which drafted tokens stand, and the token after them, so that the tokens are
+ * distributed as the target's own.  With p_i(v) = softmax(x[i] / temperature)[v] and
+ * u_i the uniform of node i, from node i = 0 on:
+ *
+ *   without draft: the children c of i, in order of their numbers, share p_i as it is:
+ *     the first whose p_i(token_c) added to its earlier siblings' exceeds u_i is
+ *     accepted and becomes i (a token that an earlier sibling had counts once);
+ *   with draft (chains only: parents must be NULL): the child c is accepted if
+ *     u_i * draft_c(token_c) < p_i(token_c);
+ *   greedy (temperature 0): the first child whose token is the lowest one with the
+ *     largest logit is accepted.
+ *
+ * Where the walk ends, at node i, the next token is the lowest v with
+ *     sum_{w <= v} r(w) > final_uniform * sum_w r(w)
+ * with r = p_i, less the children's tokens (without draft), or r = max(p_i - draft_c, 0)
+ * if a child c was refused (with draft), or p_i again where that leaves nothing; greedy:
+ * the lowest one with the largest logit.  It is -1 where no token may come (logits all
+ * -inf or NaN).
+ *
+ * p at the drafted tokens is formed in fp64 from an fp32 sum, r as integers of 2^-44 of
+ * the largest p, off by about 2^-38 of their size, whose sums are exact.  A
+ * request's results depend on that request alone.  NaN logits count as -inf; if the
+ * largest is +inf, the tokens that have it share everything.  Temperatures other than 0
+ * are taken within [2^-100, 2^100], negative ones and NaN as 0; uniforms within [0, 1),
+ * NaN as 0; draft values that are negative or NaN: refused, and nothing is taken off p.
+ * A count outside [0, T] is clamped and sets DA_DEVERR_LENGTH; a request of no nodes
+ * gets accepted 0 and rows of -1.  A parent outside [-1, t) or a token
+ * outside [0, V) sets DA_DEVERR_INDEX and the node cannot be accepted (a parent of -1:
+ * the same without the bit).  Bits are OR-ed into *err, never cleared.  Logits of nodes
+ * past a request's count are not read.
+ * Alignment: that of the element types; rows of logits that start on 16-byte (bf16:
+ * 8-byte) boundaries are read in wider accesses.  The three outputs overlap nothing
+ * else.  Two launches.  Errors: DA_ERR_INVALID_ARG, DA_ERR_UNSUPPORTED (sizes),
+ * DA_ERR_WORKSPACE, DA_ERR_CUDA. */
+int nvfp4_mm_verify(const nvfp4_verify* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

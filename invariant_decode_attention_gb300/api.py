@@ -37,7 +37,9 @@ EXPORTS = (
     "decode_attn_run_extra", "decode_attn_forward_extra",
     "nvfp4_mm_workspace_bytes", "nvfp4_mm", "nvfp4_mm_read_error",
     "decode_attn_append", "nvfp4_mm_adapters_workspace_bytes", "nvfp4_mm_adapters",
-    "nvfp4_mm_logits",
+    "nvfp4_mm_logits", "decode_attn_append_norm",
+    "decode_attn_copy_pages", "decode_attn_compact",
+    "nvfp4_mm_verify_workspace_bytes", "nvfp4_mm_verify",
 )
 
 # NVFP4 weight matmul (include/nvfp4_mm.h)
@@ -47,6 +49,8 @@ NVFP4_X_F32, NVFP4_X_BF16 = 0, 1
 # Cache append (include/decode_attn.h) and adapters (include/nvfp4_mm.h)
 X_F32, X_BF16 = 0, 1
 ADAPTER_MAX_RANK, ADAPTER_MAX_K, LOGITS_MAX_BIAS = 128, 1 << 22, 4096
+TREE_MAX_NODES = VERIFY_MAX_NODES = 64
+VERIFY_MAX_VOCAB = 1 << 19
 X_TEST_STALL_DOWN, X_TEST_STALL_UP = 0x100, 0x200  # test hooks (see include/nvfp4_mm.h)
 
 # Size of the fixed device array decode_attn_forward_static uses as scratch.
@@ -126,6 +130,24 @@ class DaAppend(ctypes.Structure):
         ("v", ctypes.c_void_p),
         ("q_out", ctypes.c_void_p),
         ("err", ctypes.c_void_p),
+    ]
+
+
+class DaHeadNorm(ctypes.Structure):
+    _fields_ = [
+        ("q_weight", ctypes.c_void_p),
+        ("k_weight", ctypes.c_void_p),
+        ("w_dtype", ctypes.c_int32),
+        ("w_add", ctypes.c_float),
+        ("eps", ctypes.c_float),
+    ]
+
+
+class DaCaches(ctypes.Structure):
+    _fields_ = [
+        ("n_layers", ctypes.c_int32),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
     ]
 
 
@@ -217,6 +239,12 @@ def lib():
     L.nvfp4_mm_read_error.argtypes = [vp, P(i32), vp]
     L.decode_attn_append.restype = ctypes.c_int
     L.decode_attn_append.argtypes = [vp, vp, vp, vp]  # addresses, or packed bytes
+    L.decode_attn_append_norm.restype = ctypes.c_int
+    L.decode_attn_append_norm.argtypes = [vp, vp, vp, vp, vp, vp]
+    L.decode_attn_copy_pages.restype = ctypes.c_int
+    L.decode_attn_copy_pages.argtypes = [vp, vp, vp, vp, i32, vp, vp]
+    L.decode_attn_compact.restype = ctypes.c_int
+    L.decode_attn_compact.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, vp, vp]
     L.nvfp4_mm_adapters_workspace_bytes.restype = sz
     L.nvfp4_mm_adapters_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
     L.nvfp4_mm_adapters.restype = ctypes.c_int
@@ -224,6 +252,10 @@ def lib():
                                     vp, vp, sz, vp]
     L.nvfp4_mm_logits.restype = ctypes.c_int
     L.nvfp4_mm_logits.argtypes = [vp, vp]
+    L.nvfp4_mm_verify_workspace_bytes.restype = sz
+    L.nvfp4_mm_verify_workspace_bytes.argtypes = [i32, i32, i32]
+    L.nvfp4_mm_verify.restype = ctypes.c_int
+    L.nvfp4_mm_verify.argtypes = [vp, vp]
     _LIB = L
     return L
 
@@ -550,9 +582,10 @@ _I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
-# da_append and nvfp4_logits, field by field, with C's alignment
+# da_append, nvfp4_logits and nvfp4_verify, field by field, with C's alignment
 _APPEND = struct.Struct("@iiPPPqqqPPPPPPP")
 _LOGITS = struct.Struct("@iiiPqPPiPPiPPPPPPiPPiPqPP")
+_VERIFY = struct.Struct("@iiiiPqqPqqPPPPPPPPPPPN")
 
 
 def _where(dev):
@@ -622,6 +655,24 @@ def rope(inv_freq: torch.Tensor, *, offset=0, interleaved=False, gain=1.0) -> Da
     return r
 
 
+def head_norm(q_weight=None, k_weight=None, *, eps, w_add=0.0) -> DaHeadNorm:
+    """Norms of each head of queries and keys (see da_head_norm): fp32 or bf16 [D]
+    weights on the device, of one type, or None: not normed.  The returned
+    description keeps them alive."""
+    some = q_weight if q_weight is not None else k_weight
+    if some is None:
+        raise ValueError("head_norm needs q_weight, k_weight or both")
+    w_dtype = _X_DTYPES.get(some.dtype)
+    if w_dtype is None or some.dim() != 1:
+        raise ValueError("weights must be float32 or bfloat16 vectors")
+    at = (some.get_device(), some.dtype, some.shape)
+    n = DaHeadNorm(_addr(q_weight, "q_weight", *at), _addr(k_weight, "k_weight", *at), w_dtype, w_add,
+                   eps)
+    n.keep = (q_weight, k_weight)
+    n.dev, n.dim = at[0], some.numel()
+    return n
+
+
 def _heads(t, name, dev, dtype, shape):
     """(address, token stride) of projections [n, heads, dim] whose tokens may
     lie apart (a part of a fused projection's rows)."""
@@ -651,10 +702,18 @@ def _cache(t, name, dev, kv_dtype, need):
     return t.data_ptr()
 
 
+def _cache_elements(prob):
+    """Elements of the problem's K (or V) cache."""
+    entries = (prob.num_blocks * prob.page_size if prob.layout == PAGED else
+               prob.batch * prob.width if prob.layout == CONTIGUOUS else prob.num_blocks)
+    return entries * prob.num_kv_heads * prob.head_dim_qk
+
+
 def append(prob: DaProblem, rope, k_new, v_new, k, v, positions, *, rows=None, table=None,
-           q_new=None, q_out=None, err=None, stream=None):
+           q_new=None, q_out=None, err=None, stream=None, norm=None, entries=None):
     """New keys and values, keys rotated, into the caches that ``forward`` reads,
-    and the same tokens' queries rotated (decode_attn_append).
+    and the same tokens' queries rotated (decode_attn_append, or with ``norm`` or
+    ``entries`` decode_attn_append_norm).
 
     prob: the problem given to ``plan`` / ``forward``; rope: from ``rope()`` or
     None; k_new, v_new: fp32 or bf16 [n, H_kv, D] (v_new and v None for a shared
@@ -662,20 +721,21 @@ def append(prob: DaProblem, rope, k_new, v_new, k, v, positions, *, rows=None, t
     rows are taken as they lie; positions: int32 [n]; rows: int32 [n], the batch
     row of each token (None: token i is row i) or, for the indexed layout, its
     slot -- negative: a padded token, nothing is written; table: the page table;
-    err: int32 [1] that device error bits are OR-ed into.  Returns q_out (bf16
-    [n, H_q, D], made when not given; rows of padded tokens are not written) or
-    None without queries.
+    err: int32 [1] that device error bits are OR-ed into; norm: from
+    ``head_norm()``, applied before the rotation; entries: int32 [n], each token's
+    entry in its row's list where that is not its position (the nodes of a tree).
+    Returns q_out (bf16 [n, H_q, D], made when not given; rows of padded tokens are
+    not written) or None without queries.
     """
     dev, dtype, n = k_new.get_device(), k_new.dtype, k_new.shape[0]
     x_dtype = _X_DTYPES.get(dtype)
     if x_dtype is None:
         raise ValueError(f"k_new must be float32 or bfloat16, got {dtype}")
     D, heads, layout, kv_dtype = prob.head_dim_qk, prob.num_kv_heads, prob.layout, prob.kv_dtype
-    entries = (prob.num_blocks * prob.page_size if layout == PAGED else
-               prob.batch * prob.width if layout == CONTIGUOUS else prob.num_blocks)
+    need = _cache_elements(prob)
     shape = (n, heads, D)
     k_ptr, k_stride = _heads(k_new, "k_new", dev, dtype, shape)
-    kc_ptr = _cache(k, "k", dev, kv_dtype, entries * heads * D)
+    kc_ptr = _cache(k, "k", dev, kv_dtype, need)
     if prob.shared_latent:
         if v_new is not None or v is not None:
             raise ValueError("v_new and v: none for a shared latent cache")
@@ -684,7 +744,7 @@ def append(prob: DaProblem, rope, k_new, v_new, k, v, positions, *, rows=None, t
         if v_new is None or v is None:
             raise ValueError("v_new and v: both for separate caches")
         v_ptr, v_stride = _heads(v_new, "v_new", dev, dtype, shape)
-        vc_ptr = _cache(v, "v", dev, kv_dtype, entries * heads * D)
+        vc_ptr = _cache(v, "v", dev, kv_dtype, need)
     q_ptr = q_stride = qo_ptr = 0
     if q_new is not None:
         shape = (n, prob.num_q_heads, D)
@@ -709,8 +769,96 @@ def append(prob: DaProblem, rope, k_new, v_new, k, v, positions, *, rows=None, t
                         _addr(positions, "positions", dev, _I32, (n,)),
                         _addr(rows, "rows", dev, _I32, (n,)), t_ptr, kc_ptr, vc_ptr, qo_ptr,
                         _addr(err, "err", dev, _I32))
-    _call(lib().decode_attn_append, "append", dev, stream, ctypes.addressof(prob), rope_ptr, args)
+    if norm is None and entries is None:
+        _call(lib().decode_attn_append, "append", dev, stream, ctypes.addressof(prob), rope_ptr, args)
+        return q_out
+    norm_ptr = None
+    if norm is not None:
+        if getattr(norm, "dev", dev) != dev:  # not there when filled in by hand
+            raise ValueError(f"the norm's weights are on {_where(norm.dev)}, expected {_where(dev)}")
+        if getattr(norm, "dim", D) != D:
+            raise ValueError(f"the norm's weights have {norm.dim} elements, a head {D}")
+        norm_ptr = ctypes.addressof(norm)
+    _call(lib().decode_attn_append_norm, "append", dev, stream, ctypes.addressof(prob), rope_ptr, norm_ptr,
+          args, _addr(entries, "entries", dev, _I32, (n,)))
     return q_out
+
+
+class Caches:
+    """The caches of a model's layers, for ``copy_pages`` and ``compact``: lists of
+    tensors of the problem's type and size, one a layer (vs None for shared latent
+    caches).  Checked once, here; they must not overlap one another."""
+
+    def __init__(self, prob: DaProblem, ks, vs=None):
+        if bool(prob.shared_latent) != (vs is None) or (vs is not None and len(vs) != len(ks)):
+            raise ValueError("a K and a V cache for each layer, or K alone for shared latent caches")
+        if not ks:
+            raise ValueError("no caches")
+        self.dev = ks[0].get_device()
+        self.need, self.shape = _cache_elements(prob), self._shape(prob)
+        self.keep = (list(ks), None if vs is None else list(vs))
+        k = [_cache(t, "k", self.dev, prob.kv_dtype, self.need) for t in ks]
+        v = [] if vs is None else [_cache(t, "v", self.dev, prob.kv_dtype, self.need) for t in vs]
+        size = {KV_BF16: 2 * self.need, KV_FP8_E4M3: self.need}.get(
+            prob.kv_dtype, self.need // 2 + self.need // 16)
+        at = sorted(k + v)
+        if any(b < a + size for a, b in zip(at, at[1:])):
+            raise ValueError("the caches overlap one another")
+        self._k = (ctypes.c_void_p * len(k))(*k)
+        self._v = (ctypes.c_void_p * len(v))(*v) if v else None
+        self._c = DaCaches(len(k), ctypes.addressof(self._k), ctypes.addressof(self._v) if v else None)
+        self.ptr = ctypes.addressof(self._c)
+
+    @staticmethod
+    def _shape(prob):
+        return (prob.kv_dtype, prob.shared_latent, prob.num_kv_heads, prob.head_dim_qk)
+
+    def of(self, prob):
+        """Address of the list, for a call with this problem."""
+        if self._shape(prob) != self.shape or (
+                _cache_elements(prob) != self.need if prob.kv_dtype == KV_NVFP4 else
+                _cache_elements(prob) > self.need):
+            raise ValueError("the caches were made for another problem")
+        return self.ptr
+
+
+def copy_pages(prob: DaProblem, caches: Caches, src, dst, *, err=None, stream=None):
+    """Page dst[i] of every layer's caches becomes page src[i] (decode_attn_copy_pages).
+
+    src, dst: int32 [n] page ids (slots of an indexed cache); pairs with a negative
+    one copy nothing.  No page may be a destination twice, nor both a destination
+    and another pair's source.  err: int32 [1] that device error bits are OR-ed into.
+    """
+    n, dev = src.shape[0], caches.dev
+    _call(lib().decode_attn_copy_pages, "copy_pages", dev, stream, ctypes.addressof(prob), caches.of(prob),
+          _addr(src, "src", dev, _I32, (n,)), _addr(dst, "dst", dev, _I32, (n,)), n,
+          _addr(err, "err", dev, _I32))
+
+
+def compact(prob: DaProblem, caches: Caches, lengths, nodes, accepted, *, table=None, new_lengths=None,
+            err=None, stream=None):
+    """The entries of each row's accepted nodes moved behind its context, in every
+    layer's caches (decode_attn_compact).
+
+    lengths: int32 [B], entries before the tree; nodes: int32 [B, T] and accepted:
+    int32 [B] as ``nvfp4_verify`` returns them (the root, then accepted[b] nodes in
+    ascending order; negative: none); table: as attention reads it.  Returns
+    new_lengths, int32 [B] (made when not given, not the tensor lengths itself).
+    """
+    dev, B = caches.dev, prob.batch
+    if new_lengths is None:
+        new_lengths = _make((B,), _I32, lengths.device, stream)
+    T = nodes.shape[-1]
+    t_ptr = 0
+    if prob.layout != CONTIGUOUS:
+        if table is None:
+            raise ValueError("a paged or indexed cache needs its table")
+        t_ptr = _addr(table, "table", dev, _I32, (B, prob.width))
+    _call(lib().decode_attn_compact, "compact", dev, stream, ctypes.addressof(prob), caches.of(prob), t_ptr,
+          _addr(lengths, "lengths", dev, _I32, (B,)), _addr(nodes, "nodes", dev, _I32, (B, T)), T,
+          _addr(accepted, "accepted", dev, _I32, (B,)), _addr(new_lengths, "new_lengths", dev, _I32, (B,)),
+          _addr(err, "err", dev, _I32))
+    return new_lengths
 
 
 class Adapters:
@@ -835,3 +983,66 @@ def nvfp4_logits(x, *, prompt=None, prompt_lens=None, output=None, output_lens=N
         _addr(tokens, "tokens", dev, _I32, row), _addr(err, "err", dev, _I32))
     _call(lib().nvfp4_mm_logits, "nvfp4_logits", dev, stream, args)
     return tokens
+
+
+def verify_workspace_bytes(B: int, T: int, V: int) -> int:
+    """Workspace bytes of one ``nvfp4_verify`` call (0: sizes not supported)."""
+    return int(lib().nvfp4_mm_verify_workspace_bytes(B, T, V))
+
+
+def verify_workspace(B: int, T: int, V: int, device="cuda", stream=None) -> torch.Tensor:
+    nb = verify_workspace_bytes(B, T, V)
+    if nb == 0:
+        raise DecodeAttnError(ERR_UNSUPPORTED, f"verify sizes B={B} T={T} V={V}")
+    return _make((nb,), torch.uint8, device, stream)
+
+
+def _logit_nodes(t, name, dev, dtype, shape):
+    """(address, request stride, node stride) of a [B, T, V] tensor whose rows are
+    contiguous."""
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape:
+        row, node, one = t.stride()
+        if one == 1 or shape[2] == 1:
+            return t.data_ptr(), row, node
+    _refuse(t, name, dev, dtype, shape)
+
+
+def nvfp4_verify(x, tokens, uniforms, final_uniforms, *, parents=None, counts=None, draft=None,
+                 temperature=None, accepted=None, nodes=None, out=None, ws=None, err=None, stream=None):
+    """Which drafted tokens of each request stand, and the token after them
+    (nvfp4_mm_verify; the rules are stated there).
+
+    x: fp32 or bf16 [B, T, V], the target's logits of what follows each node (node 0:
+    the request's last token); tokens: int32 [B, T]; uniforms: fp32 [B, T] and
+    final_uniforms: fp32 [B], random numbers in [0, 1); parents: int32 [B, T] (None:
+    chains); counts: int32 [B], nodes that a request has (None: T); draft: fp32
+    [B, T, V], the probabilities that the tokens were drawn from (chains only);
+    temperature: fp32 [B] (None: 1; 0: greedy).  Returns (accepted int32 [B], nodes
+    int32 [B, T], out int32 [B, T]), made when not given: how many drafted tokens
+    stand; node 0 and theirs; their tokens and the next one; -1 behind them.
+    """
+    dev, dtype, shape = x.get_device(), x.dtype, x.shape
+    B, T, V = shape
+    x_dtype = _X_DTYPES.get(dtype)
+    if x_dtype is None:
+        raise ValueError(f"x must be float32 or bfloat16, got {dtype}")
+    if accepted is None:
+        accepted = _make((B,), _I32, x.device, stream)
+    if nodes is None:
+        nodes = _make((B, T), _I32, x.device, stream)
+    if out is None:
+        out = _make((B, T), _I32, x.device, stream)
+    if ws is None:
+        ws = verify_workspace(B, T, V, x.device, stream)
+    row, all_ = (B,), (B, T)
+    args = _VERIFY.pack(
+        B, T, V, x_dtype, *_logit_nodes(x, "x", dev, dtype, shape),
+        *((0, 0, 0) if draft is None else _logit_nodes(draft, "draft", dev, _F32, shape)),
+        _addr(tokens, "tokens", dev, _I32, all_), _addr(parents, "parents", dev, _I32, all_),
+        _addr(counts, "counts", dev, _I32, row), _addr(temperature, "temperature", dev, _F32, row),
+        _addr(uniforms, "uniforms", dev, _F32, all_), _addr(final_uniforms, "final_uniforms", dev, _F32, row),
+        _addr(accepted, "accepted", dev, _I32, row), _addr(nodes, "nodes", dev, _I32, all_),
+        _addr(out, "out", dev, _I32, all_), _addr(err, "err", dev, _I32), _addr(ws, "ws", dev, torch.uint8),
+        ws.numel())
+    _call(lib().nvfp4_mm_verify, "nvfp4_verify", dev, stream, args)
+    return accepted, nodes, out

@@ -10,6 +10,7 @@
 #include "append.cuh"
 #include "common.cuh"
 #include "merge.cuh"
+#include "moves.cuh"
 
 namespace da {
 bool mla_supported(int H_q);
@@ -196,6 +197,63 @@ int check_plan(const da_plan* plan) {
   if (plan->prob.batch > 0) {
     if (!plan->ws || !aligned(plan->ws, 256)) return DA_ERR_WORKSPACE;
     if (plan->ws_bytes < ws_layout(&plan->prob, v.max_splits).total) return DA_ERR_WORKSPACE;
+  }
+  return DA_OK;
+}
+
+long long cache_rows(const da_problem& pr) {
+  return (pr.layout == DA_KV_CONTIGUOUS) ? (long long)pr.batch * pr.width
+         : (pr.layout == DA_KV_PAGED)    ? pr.num_blocks * pr.page_size
+                                         : pr.num_blocks;
+}
+
+bool overlap(const void* a, long long a_bytes, const void* b, long long b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+
+int check_caches(const da_problem* prob, const da_caches* c) {
+  int rc = check_problem(prob);
+  if (rc != DA_OK) return rc;
+  if (!c || c->n_layers < 1) return DA_ERR_INVALID_ARG;
+  Variant var;  // only caches that a kernel of this library reads
+  da_problem one = *prob;
+  one.extra_width = 0;
+  rc = select_variant(&one, &var);
+  if (rc != DA_OK) return rc;
+
+  if (!c->k || (prob->shared_latent != 0) != (c->v == nullptr)) return DA_ERR_INVALID_ARG;
+  for (int i = 0; i < c->n_layers; ++i)
+    if (!c->k[i] || !aligned(c->k[i], 16) || (c->v && (!c->v[i] || !aligned(c->v[i], 16))))
+      return DA_ERR_INVALID_ARG;
+  return DA_OK;
+}
+
+// launch(regions) for all buffers of the caches: what holds elements (NVFP4: codes),
+// then, for NVFP4, the block scales; kMoveRegions buffers at a time.
+template <typename F>
+int for_regions(const da_problem& pr, const da_caches& c, F launch) {
+  const long long elements = (long long)pr.num_kv_heads * pr.head_dim_qk;  // of an entry
+  const bool nvfp4 = pr.kv_dtype == DA_KV_NVFP4;
+  bool report = true;
+  for (int part = 0; part < (nvfp4 ? 2 : 1); ++part) {
+    const long long bytes = part             ? elements / 16
+                            : nvfp4          ? elements / 2
+                            : pr.kv_dtype == DA_KV_BF16 ? elements * 2
+                                                        : elements;
+    if (bytes > (1 << 30)) return DA_ERR_UNSUPPORTED;  // a row's own offsets take 32 bits
+    const long long offset = part ? cache_rows(pr) * (elements / 2) : 0;
+    MoveRegions r;
+    r.n = 0;
+    r.entry_bytes = (int)bytes;
+    for (int i = 0; i < c.n_layers; ++i) {
+      r.base[r.n++] = static_cast<uint8_t*>(c.k[i]) + offset;
+      if (c.v) r.base[r.n++] = static_cast<uint8_t*>(c.v[i]) + offset;
+      if (r.n + 2 <= kMoveRegions && i + 1 < c.n_layers) continue;
+      if (launch(r, report) != cudaSuccess) return DA_ERR_CUDA;
+      report = false;
+      r.n = 0;
+    }
   }
   return DA_OK;
 }
@@ -492,8 +550,8 @@ int decode_attn_copy_plan(const da_plan* plan, int32_t* n_splits, int32_t* split
   return e == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
-int decode_attn_append(const da_problem* prob, const da_rope* rope, const da_append* args,
-                       void* stream) {
+static int append_impl(const da_problem* prob, const da_rope* rope, const da_head_norm* norm,
+                       const da_append* args, const int32_t* entries, void* stream) {
   int rc = check_problem(prob);
   if (rc != DA_OK) return rc;
   if (!args || args->n_tokens < 0) return DA_ERR_INVALID_ARG;
@@ -515,6 +573,17 @@ int decode_attn_append(const da_problem* prob, const da_rope* rope, const da_app
   const da_append& a = *args;
   if (a.n_tokens == 0) return DA_OK;
   const bool latent = prob->shared_latent != 0;
+  const bool norms = norm && (norm->q_weight || norm->k_weight);
+  if (norm) {
+    if ((norm->w_dtype != DA_X_F32 && norm->w_dtype != DA_X_BF16) || !std::isfinite(norm->w_add) ||
+        !std::isfinite(norm->eps) || norm->eps < 0.f)
+      return DA_ERR_INVALID_ARG;
+    if ((norm->q_weight && !aligned(norm->q_weight, 16)) ||
+        (norm->k_weight && !aligned(norm->k_weight, 16)) || (norm->q_weight && !a.q_new))
+      return DA_ERR_INVALID_ARG;
+    if (norms && latent) return DA_ERR_UNSUPPORTED;
+  }
+  if (entries && (prob->layout == DA_KV_INDEXED || !aligned(entries, 4))) return DA_ERR_INVALID_ARG;
   const long long n = a.n_tokens, D = prob->head_dim_qk;
   const long long q_row = prob->num_q_heads * D, kv_row = prob->num_kv_heads * D;
   const long long esize = a.x_dtype == DA_X_BF16 ? 2 : 4;
@@ -590,8 +659,89 @@ int decode_attn_append(const da_problem* prob, const da_rope* rope, const da_app
   }
   L.k_scale = prob->k_scale;
   L.v_scale = prob->v_scale;
+  L.entries = entries;
+  if (norms) {
+    L.q_weight = norm->q_weight;
+    L.k_weight = norm->k_weight;
+    L.w_bf16 = norm->w_dtype == DA_X_BF16;
+    L.w_add = norm->w_add;
+    L.eps = norm->eps;
+  }
   return launch_append(L, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DA_OK
                                                                                  : DA_ERR_CUDA;
+}
+
+int decode_attn_append(const da_problem* prob, const da_rope* rope, const da_append* args,
+                       void* stream) {
+  return append_impl(prob, rope, nullptr, args, nullptr, stream);
+}
+
+int decode_attn_append_norm(const da_problem* prob, const da_rope* rope, const da_head_norm* norm,
+                            const da_append* args, const int32_t* entries, void* stream) {
+  return append_impl(prob, rope, norm, args, entries, stream);
+}
+
+int decode_attn_copy_pages(const da_problem* prob, const da_caches* caches, const int32_t* src,
+                           const int32_t* dst, int32_t n, int32_t* err, void* stream) {
+  const int rc = check_caches(prob, caches);
+  if (rc != DA_OK) return rc;
+  if (n < 0 || prob->layout == DA_KV_CONTIGUOUS) return DA_ERR_INVALID_ARG;
+  if (n == 0) return DA_OK;
+  if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4) || (err && !aligned(err, 4)))
+    return DA_ERR_INVALID_ARG;
+  return for_regions(*prob, *caches, [&](const MoveRegions& r, bool report) {
+    CopyPagesLaunch L;
+    L.regions = r;
+    L.src = src;
+    L.dst = dst;
+    L.err = err;
+    L.num_blocks = prob->num_blocks;
+    L.page_bytes = (long long)r.entry_bytes * (prob->layout == DA_KV_PAGED ? prob->page_size : 1);
+    L.n = n;
+    L.word = L.page_bytes % 16 == 0 ? 16 : 4;
+    L.report = report;
+    return launch_copy_pages(L, static_cast<cudaStream_t>(stream));
+  });
+}
+
+int decode_attn_compact(const da_problem* prob, const da_caches* caches, const int32_t* table,
+                        const int32_t* lengths, const int32_t* nodes, int32_t nodes_width,
+                        const int32_t* accepted, int32_t* new_lengths, int32_t* err, void* stream) {
+  const int rc = check_caches(prob, caches);
+  if (rc != DA_OK) return rc;
+  if (nodes_width < 1 || nodes_width > DA_TREE_MAX_NODES) return DA_ERR_INVALID_ARG;
+  if (prob->batch == 0) return DA_OK;
+  if (!lengths || !nodes || !accepted || (prob->layout != DA_KV_CONTIGUOUS) != (table != nullptr))
+    return DA_ERR_INVALID_ARG;
+  const void* words[6] = {table, lengths, nodes, accepted, new_lengths, err};
+  for (const void* w : words)
+    if (w && !aligned(w, 4)) return DA_ERR_INVALID_ARG;
+  const long long B = prob->batch;
+  if (new_lengths && (overlap(new_lengths, 4 * B, lengths, 4 * B) ||
+                      overlap(new_lengths, 4 * B, accepted, 4 * B) ||
+                      overlap(new_lengths, 4 * B, nodes, 4 * B * nodes_width) ||
+                      (table && overlap(new_lengths, 4 * B, table, 4 * B * prob->width))))
+    return DA_ERR_INVALID_ARG;  // other threads read what it gets
+  return for_regions(*prob, *caches, [&](const MoveRegions& r, bool report) {
+    CompactLaunch L;
+    L.regions = r;
+    L.table = table;
+    L.lengths = lengths;
+    L.nodes = nodes;
+    L.accepted = accepted;
+    L.new_lengths = new_lengths;
+    L.err = err;
+    L.num_blocks = prob->num_blocks;
+    L.capacity = row_capacity(prob->layout, prob->width, prob->page_size);
+    L.B = prob->batch;
+    L.nodes_width = nodes_width;
+    L.layout = prob->layout;
+    L.page_size = prob->page_size;
+    L.width = prob->width;
+    L.word = r.entry_bytes % 16 == 0 ? 16 : 4;
+    L.report = report;
+    return launch_compact(L, static_cast<cudaStream_t>(stream));
+  });
 }
 
 }  // extern "C"

@@ -117,17 +117,18 @@ __device__ __forceinline__ long long entry_of(const AppendLaunch& p, int i, int 
     if (row >= p.num_blocks) *bad |= DA_DEVERR_INDEX;
     return *bad ? -1 : row;
   }
-  if (pos < 0 || pos >= p.capacity) *bad |= DA_DEVERR_LENGTH;
+  const int at = p.entries ? __ldg(p.entries + i) : pos;
+  if (pos < 0 || at < 0 || at >= p.capacity) *bad |= DA_DEVERR_LENGTH;
   if (row >= p.B) *bad |= DA_DEVERR_INDEX;
   if (*bad) return -1;
-  if (p.layout == DA_KV_CONTIGUOUS) return (long long)row * p.width + pos;
-  const int page = pos / p.page_size;
+  if (p.layout == DA_KV_CONTIGUOUS) return (long long)row * p.width + at;
+  const int page = at / p.page_size;
   const int id = __ldg(p.table + (long long)row * p.width + page);
   if (id < 0 || id >= p.num_blocks) {
     *bad |= DA_DEVERR_INDEX;
     return -1;
   }
-  return (long long)id * p.page_size + (pos - page * p.page_size);
+  return (long long)id * p.page_size + (at - page * p.page_size);
 }
 
 // The angle pos * inv_freq in half turns, whole turns taken away: in [-1, 1].
@@ -173,12 +174,35 @@ __device__ __forceinline__ void turn_halves(float (&a)[8], float (&b)[8], const 
   }
 }
 
+// x * r * (w + add) for a chunk of a normed head, one rounding an operation.
+__device__ __forceinline__ void norm_chunk(float (&f)[8], float r, const void* weight, bool w_bf16,
+                                           float add, int chunk) {
+  float w[8];
+  if (w_bf16) {
+    Chunk<__nv_bfloat16> c;
+    c.load(static_cast<const __nv_bfloat16*>(weight) + 8 * chunk);
+    c.get(w);
+  } else {
+    Chunk<float> c;
+    c.load(static_cast<const float*>(weight) + 8 * chunk);
+    c.get(w);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(__fmul_rn(f[e], r), __fadd_rn(w[e], add));
+}
+
 // Warp w of the grid takes part w % parts of token w / parts: units [part *
 // per_part, + per_part) of the token's heads q, k, v, 32 * kBatch at a time.
-template <typename X, int KT, int D>
+//
+// kNorm: queries and keys are normed on the way, y = x / sqrt(mean x^2 + eps) * (w +
+// add).  A head's units lie on neighbouring lanes (eight for 128 dims, four for 64), so
+// its sum of squares is 16 products a lane, in order, and a butterfly of fixed shape;
+// the elements are in registers already, and nothing more is read but the weights.
+template <typename X, int KT, int D, bool kNorm>
 __global__ void __launch_bounds__(kWarps * 32, kResident<X>)
     append_kernel(const AppendLaunch p, int parts, int per_part) {
   constexpr int kUnits = D / 16;                // units of a head
+  static_assert(!kNorm || kUnits == 4 || kUnits == 8, "a head's lanes make a butterfly");
   constexpr int kBatch = kInFlight<X>;
   constexpr bool kBlocks = KT == DA_KV_NVFP4;   // a unit of the cache is always a block of 16
   // gain * (cos, sin) of the token's angles, for each warp: pairs 2i and 2i + 1
@@ -255,13 +279,35 @@ __global__ void __launch_bounds__(kWarps * 32, kResident<X>)
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const int unit = first + u * 32 + lane;
+      float a[8], b[8], r = 1.f;
+      if constexpr (kNorm) {  // all lanes, those past the end too, take part in the sums
+        lo[u].get(a);
+        hi[u].get(b);
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = fmaf(a[e], a[e], sum);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = fmaf(b[e], b[e], sum);
+#pragma unroll
+        for (int m = 1; m < kUnits; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        r = __frsqrt_rn(fmaf(sum, 1.f / D, p.eps));
+      }
       if (unit >= end) continue;
       const int head = unit / kUnits, i = unit - head * kUnits;
       int c0, c1;
       chunks_of(head, i, &c0, &c1);
-      float a[8], b[8];
-      lo[u].get(a);
-      hi[u].get(b);
+      if constexpr (!kNorm) {
+        lo[u].get(a);
+        hi[u].get(b);
+      }
+      const void* weight = nullptr;
+      if constexpr (kNorm) {
+        weight = head < hq ? p.q_weight : head < hk ? p.k_weight : nullptr;
+        if (weight) {
+          norm_chunk(a, r, weight, p.w_bf16, p.w_add, c0);
+          norm_chunk(b, r, weight, p.w_bf16, p.w_add, c1);
+        }
+      }
       if (head < hk) {
         if (!halves) {
           const int r0 = c0 - skip, r1 = c1 - skip;  // pairs 4 r .. 4 r + 3: half a group
@@ -277,16 +323,19 @@ __global__ void __launch_bounds__(kWarps * 32, kResident<X>)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float(&own)[8] = h ? b : a;
-            const int r = (h ? c1 : c0) - skip;
-            if (r < 0 || r >= 2 * groups) continue;
+            const int at = (h ? c1 : c0) - skip;
+            if (at < 0 || at >= 2 * groups) continue;
             Chunk<X> other;
-            other.load(src + 8 * (skip + (r < groups ? r + groups : r - groups)));
+            const int partner = skip + (at < groups ? at + groups : at - groups);
+            other.load(src + 8 * partner);
             float g[8];
             other.get(g);
-            if (r < groups)
-              turn_halves(own, g, turn + r, groups);
+            if constexpr (kNorm)
+              if (weight) norm_chunk(g, r, weight, p.w_bf16, p.w_add, partner);
+            if (at < groups)
+              turn_halves(own, g, turn + at, groups);
             else
-              turn_halves(g, own, turn + (r - groups), groups);
+              turn_halves(g, own, turn + (at - groups), groups);
           }
         }
       }
@@ -336,7 +385,7 @@ __global__ void __launch_bounds__(kWarps * 32, kResident<X>)
   }
 }
 
-template <typename X, int KT, int D>
+template <typename X, int KT, int D, bool kNorm>
 cudaError_t launch_dim(const AppendLaunch& p, int sms, cudaStream_t stream) {
   const int units = (D / 16) * ((p.q_new ? p.H_q : 0) + p.H_kv * (p.v_new ? 2 : 1));
   // a warp takes a whole token once there are enough of them; fewer tokens are
@@ -351,17 +400,21 @@ cudaError_t launch_dim(const AppendLaunch& p, int sms, cudaStream_t stream) {
   parts = (units + per_part - 1) / per_part;
   const long long grid = (p.n_tokens * parts + kWarps - 1) / kWarps;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_after(append_kernel<X, KT, D>, dim3((unsigned)grid), dim3(kWarps * 32), 0, stream, p,
+  return launch_after(append_kernel<X, KT, D, kNorm>, dim3((unsigned)grid), dim3(kWarps * 32), 0, stream, p,
                       (int)parts, per_part);
 }
 
 template <typename X, int KT>
 cudaError_t launch_kv(const AppendLaunch& p, int sms, cudaStream_t stream) {
-  switch (p.D) {
-    case 64: return launch_dim<X, KT, 64>(p, sms, stream);
-    case 128: return launch_dim<X, KT, 128>(p, sms, stream);
+  const bool norm = p.q_weight || p.k_weight;
+  switch (norm ? -p.D : p.D) {
+    case 64: return launch_dim<X, KT, 64, false>(p, sms, stream);
+    case 128: return launch_dim<X, KT, 128, false>(p, sms, stream);
     case 576:
-      if constexpr (KT != DA_KV_NVFP4) return launch_dim<X, KT, 576>(p, sms, stream);
+      if constexpr (KT != DA_KV_NVFP4) return launch_dim<X, KT, 576, false>(p, sms, stream);
+      break;
+    case -64: return launch_dim<X, KT, 64, true>(p, sms, stream);
+    case -128: return launch_dim<X, KT, 128, true>(p, sms, stream);
   }
   return cudaErrorInvalidValue;  // no kernel reads such a cache
 }

@@ -12,6 +12,7 @@ struct AppendLaunch {
   long long k_stride, v_stride, q_stride;  // elements between tokens
   const int32_t* positions;
   const int32_t* rows;  // null: token i is row i
+  const int32_t* entries;  // place in its row's list; null: the position
   const int32_t* table;
   void* k;
   void* v;
@@ -25,6 +26,10 @@ struct AppendLaunch {
   long long capacity;
   int rope_dim, rope_offset, interleaved;
   float gain, k_scale, v_scale;
+  const void* q_weight;  // norms' weights; null: not normed
+  const void* k_weight;
+  int w_bf16;
+  float w_add, eps;
 };
 
 cudaError_t launch_append(const AppendLaunch& p, int sms, cudaStream_t stream);
