@@ -409,10 +409,65 @@ typedef struct da_head_norm {
 int decode_attn_append_norm(const da_problem* prob, const da_rope* rope, const da_head_norm* norm,
                             const da_append* args, const int32_t* entries, void* stream);
 
-/* ---- moving entries of the caches ------------------------------------ */
+/* ---- drafted tokens --------------------------------------------------- */
 
 /* Nodes of a tree of drafted tokens at most. */
 #define DA_TREE_MAX_NODES 64
+
+/* One decode_attn_tree call.  Plain data. */
+typedef struct da_tree {
+  int32_t nodes;          /* T: nodes that a row has room for, 1 .. DA_TREE_MAX_NODES */
+  int32_t window;         /* 0: none; W: a node sees W positions, its own the last    */
+  int32_t sinks;          /* first positions that a window does not hide              */
+  const int32_t* parents; /* int32 [B, T]: node t's parent, below t, or -1: none;     */
+                          /* NULL: t - 1, a chain                                     */
+  const int32_t* counts;  /* int32 [B]: nodes that row b has; NULL: T                 */
+  const void* q;          /* bf16 [B, T, H_q, D], 16-byte aligned                     */
+  const void* k;          /* the caches, as decode_attn_run takes them                */
+  const void* v;
+  const int32_t* table;   /* int32 [B, width] (NULL for contiguous)                   */
+  const int32_t* lengths; /* int32 [B]: entries of row b before its nodes             */
+  void* out;              /* bf16 [B, T, H_q, D], 16-byte aligned                     */
+  float* lse;             /* fp32 [B, T, H_q], natural log                            */
+  int32_t* err;           /* device word for DA_DEVERR_* bits, or NULL                */
+  void* ws;               /* workspace, 256-byte aligned                              */
+  size_t ws_bytes;
+} da_tree;
+
+/* Workspace bytes of a decode_attn_tree call with `nodes` nodes, whatever its window.
+ * Needs no initialisation. */
+int decode_attn_tree_workspace_bytes(const da_problem* prob, int32_t nodes, size_t* bytes);
+
+/* Softmax attention of many query tokens a row: the nodes of a tree of drafted tokens
+ * (a chain of them, a piece of a prompt; with one node a plain decode step, here with a
+ * window as well).  Row b's list has L = lengths[b] entries of context, then its n =
+ * counts[b] nodes, node t at entry L + t (decode_attn_append_norm writes it there).  A
+ * node at depth d -- 0 without a parent, else one more than its parent -- has position
+ * L + d and sees
+ *   - entry j < L of the context if W = 0, or j > L + d - W, or j < sinks;
+ *   - itself, and each of its ancestors, at depth e, if W = 0, or d - e < W, or
+ *     L + e < sinks.
+ * out and lse are as decode_attn_run's, with these entries; a node that sees nothing
+ * (one entry of the list lies beyond the capacity) gets out = 0, lse = -inf.
+ * Entries that a node does not see have no effect on it, whatever they hold, NaN and
+ * infinities included.
+ * Rows past counts[b] of q are not read, those of out and lse left as they are.
+ *
+ * A row's list is cut into splits whose number follows from the row's own list and
+ * number of nodes (and the window): its results are bitwise the same in any batch.
+ *
+ * lengths outside [0, capacity] and counts outside [0, T] are clamped and entries
+ * beyond the capacity are not read: DA_DEVERR_LENGTH.  Page ids and slots out of range are
+ * not read and set DA_DEVERR_INDEX where some node sees an entry of theirs (the row's results are then
+ * unspecified), and so does a parent outside [-1, t), which counts as none.
+ * DA_DEVERR_TIMEOUT: a pipeline wait hit its limit, results are unspecified.  Bits are
+ * OR-ed into *err, never cleared.
+ *
+ * `prob` describes the caches; its batch is the number of rows and its extra_width 0.
+ * Supported: separate caches of all three types, D = 64 or 128, up to 128 query heads a
+ * KV head; (entries of the cache) * H_kv and B * T * H_q up to 2^31.  out and lse overlap
+ * neither q nor each other. */
+int decode_attn_tree(const da_problem* prob, const da_tree* args, void* stream);
 
 /* The caches of a model's layers, all of one geometry (that of the problem given
  * beside them) and none overlapping another.  k and v are host arrays of device

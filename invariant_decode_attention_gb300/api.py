@@ -40,6 +40,7 @@ EXPORTS = (
     "nvfp4_mm_logits", "decode_attn_append_norm",
     "decode_attn_copy_pages", "decode_attn_compact",
     "nvfp4_mm_verify_workspace_bytes", "nvfp4_mm_verify",
+    "decode_attn_tree_workspace_bytes", "decode_attn_tree",
 )
 
 # NVFP4 weight matmul (include/nvfp4_mm.h)
@@ -256,6 +257,10 @@ def lib():
     L.nvfp4_mm_verify_workspace_bytes.argtypes = [i32, i32, i32]
     L.nvfp4_mm_verify.restype = ctypes.c_int
     L.nvfp4_mm_verify.argtypes = [vp, vp]
+    L.decode_attn_tree_workspace_bytes.restype = ctypes.c_int
+    L.decode_attn_tree_workspace_bytes.argtypes = [P(DaProblem), i32, P(sz)]
+    L.decode_attn_tree.restype = ctypes.c_int
+    L.decode_attn_tree.argtypes = [vp, vp, vp]
     _LIB = L
     return L
 
@@ -582,10 +587,11 @@ _I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
-# da_append, nvfp4_logits and nvfp4_verify, field by field, with C's alignment
+# da_append, nvfp4_logits, nvfp4_verify and da_tree, field by field, with C's alignment
 _APPEND = struct.Struct("@iiPPPqqqPPPPPPP")
 _LOGITS = struct.Struct("@iiiPqPPiPPiPPPPPPiPPiPqPP")
 _VERIFY = struct.Struct("@iiiiPqqPqqPPPPPPPPPPPN")
+_TREE = struct.Struct("@iiiPPPPPPPPPPPN")
 
 
 def _where(dev):
@@ -782,6 +788,60 @@ def append(prob: DaProblem, rope, k_new, v_new, k, v, positions, *, rows=None, t
     _call(lib().decode_attn_append_norm, "append", dev, stream, ctypes.addressof(prob), rope_ptr, norm_ptr,
           args, _addr(entries, "entries", dev, _I32, (n,)))
     return q_out
+
+
+def tree_workspace_bytes(prob: DaProblem, nodes: int) -> int:
+    """Workspace bytes of one ``tree`` call with up to ``nodes`` nodes a row."""
+    n = ctypes.c_size_t()
+    _check(lib().decode_attn_tree_workspace_bytes(ctypes.byref(prob), nodes, ctypes.byref(n)),
+           "tree_workspace_bytes")
+    return n.value
+
+
+def tree_workspace(prob: DaProblem, nodes: int, device="cuda", stream=None) -> torch.Tensor:
+    return _make((tree_workspace_bytes(prob, nodes),), torch.uint8, device, stream)
+
+
+def tree(prob: DaProblem, q, k, v, lengths, *, parents=None, counts=None, table=None, window=0, sinks=0,
+         out=None, lse=None, ws=None, err=None, stream=None):
+    """Attention of each row's tree of drafted tokens over its context and their
+    ancestors (decode_attn_tree; what a node sees is stated there).
+
+    q: bf16 [B, T, H_q, D], T up to TREE_MAX_NODES; k, v: the caches, the nodes' entries
+    written already (``append`` with ``entries``); lengths: int32 [B], entries
+    before the nodes; parents: int32 [B, T], earlier nodes or -1 (None: chains);
+    counts: int32 [B] nodes a row has (None: T); window: positions that a node sees (0:
+    all), sinks: first positions that stay visible; ws: from ``tree_workspace``; err:
+    int32 [1] that device error bits are OR-ed into.  Returns (out bf16 [B, T, H_q, D],
+    lse fp32 [B, T, H_q]), made when not given; rows past a row's count are not
+    written.  A row's bits depend on that row alone.
+    """
+    dev, layout, kv_dtype = q.get_device(), prob.layout, prob.kv_dtype
+    B, T, D = prob.batch, q.shape[1], prob.head_dim_qk
+    shape = (B, T, prob.num_q_heads, D)
+    q_ptr = _addr(q, "q", dev, _BF16, shape)
+    if v is None:
+        raise ValueError("tree attention takes separate K and V caches")
+    need = _cache_elements(prob)
+    if layout == CONTIGUOUS:
+        if table is not None:
+            raise ValueError("a contiguous cache has no table")
+    elif table is None:
+        raise ValueError("a paged or indexed cache needs its table")
+    if out is None:
+        out = _make(shape, _BF16, q.device, stream)
+    if lse is None:
+        lse = _make(shape[:3], _F32, q.device, stream)
+    if ws is None:
+        ws = tree_workspace(prob, T, q.device, stream)
+    args = _TREE.pack(T, window, sinks, _addr(parents, "parents", dev, _I32, (B, T)),
+                      _addr(counts, "counts", dev, _I32, (B,)), q_ptr, _cache(k, "k", dev, kv_dtype, need),
+                      _cache(v, "v", dev, kv_dtype, need), _addr(table, "table", dev, _I32, (B, prob.width)),
+                      _addr(lengths, "lengths", dev, _I32, (B,)), _addr(out, "out", dev, _BF16, shape),
+                      _addr(lse, "lse", dev, _F32, shape[:3]), _addr(err, "err", dev, _I32),
+                      _addr(ws, "ws", dev, torch.uint8), ws.numel())
+    _call(lib().decode_attn_tree, "tree", dev, stream, ctypes.addressof(prob), args)
+    return out, lse
 
 
 class Caches:

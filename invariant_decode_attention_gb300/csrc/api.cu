@@ -11,6 +11,7 @@
 #include "common.cuh"
 #include "merge.cuh"
 #include "moves.cuh"
+#include "tree.cuh"
 
 namespace da {
 bool mla_supported(int H_q);
@@ -256,6 +257,44 @@ int for_regions(const da_problem& pr, const da_caches& c, F launch) {
     }
   }
   return DA_OK;
+}
+
+// What the tree attention takes: separate K and V, D = 64 or 128, any group up to 128.
+int check_tree_problem(const da_problem* prob, int32_t nodes) {
+  const int rc = check_problem(prob);
+  if (rc != DA_OK) return rc;
+  if (nodes < 1) return DA_ERR_INVALID_ARG;
+  if (nodes > DA_TREE_MAX_NODES || prob->shared_latent || prob->extra_width ||
+      prob->head_dim_qk != prob->head_dim_v || (prob->head_dim_qk != 64 && prob->head_dim_qk != 128) ||
+      prob->num_q_heads / prob->num_kv_heads > 128)
+    return DA_ERR_UNSUPPORTED;
+  const long long cap = row_capacity(prob->layout, prob->width, prob->page_size);
+  if (cap > 0x7fffff00LL) return DA_ERR_UNSUPPORTED;  // entries and positions in 32 bits
+  // what a copy of scattered rows counts in 32 bits: (entry, head) pairs
+  if (cache_rows(*prob) > 0x7fffffffLL / prob->num_kv_heads) return DA_ERR_UNSUPPORTED;
+  if ((long long)prob->batch * nodes * prob->num_q_heads > (1LL << 31)) return DA_ERR_UNSUPPORTED;
+  return DA_OK;
+}
+
+// Splits that a row of the problem can have at most.
+int tree_max_splits(const da_problem* prob) {
+  const long long cap = row_capacity(prob->layout, prob->width, prob->page_size);
+  const long long tiles = (cap + kTreeTile - 1) / kTreeTile;
+  const long long n = (tiles + kTreeLeastTiles - 1) / kTreeLeastTiles;
+  return (int)std::min<long long>(std::max<long long>(n, 1), kTreeMaxSplits);
+}
+
+struct TreeWs {
+  size_t lse_part, total;  // the outputs' partials lie at the start
+};
+
+TreeWs tree_ws(const da_problem* prob, int32_t nodes) {
+  const int splits = tree_max_splits(prob);
+  const size_t rows = splits > 1 ? (size_t)prob->batch * splits * nodes * prob->num_q_heads : 0;
+  TreeWs w;
+  w.lse_part = align256(4 * rows * prob->head_dim_v);
+  w.total = std::max<size_t>(256, w.lse_part + align256(4 * rows));
+  return w;
 }
 
 }  // namespace
@@ -742,6 +781,86 @@ int decode_attn_compact(const da_problem* prob, const da_caches* caches, const i
     L.report = report;
     return launch_compact(L, static_cast<cudaStream_t>(stream));
   });
+}
+
+int decode_attn_tree_workspace_bytes(const da_problem* prob, int32_t nodes, size_t* bytes) {
+  const int rc = check_tree_problem(prob, nodes);
+  if (rc != DA_OK) return rc;
+  if (!bytes) return DA_ERR_INVALID_ARG;
+  *bytes = tree_ws(prob, nodes).total;
+  return DA_OK;
+}
+
+int decode_attn_tree(const da_problem* prob, const da_tree* args, void* stream) {
+  if (!args) return DA_ERR_INVALID_ARG;
+  const da_tree& a = *args;
+  const int rc = check_tree_problem(prob, a.nodes);
+  if (rc != DA_OK) return rc;
+  if (a.window < 0 || a.sinks < 0) return DA_ERR_INVALID_ARG;
+  if (prob->batch == 0) return DA_OK;
+  if (!a.q || !a.k || !a.v || !a.lengths || !a.out || !a.lse ||
+      (prob->layout != DA_KV_CONTIGUOUS) != (a.table != nullptr))
+    return DA_ERR_INVALID_ARG;
+  const void* wide[4] = {a.q, a.k, a.v, a.out};
+  for (const void* w : wide)
+    if (!aligned(w, 16)) return DA_ERR_INVALID_ARG;
+  const void* words[6] = {a.lengths, a.lse, a.table, a.parents, a.counts, a.err};
+  for (const void* w : words)
+    if (!aligned(w, 4)) return DA_ERR_INVALID_ARG;
+  const TreeWs ws = tree_ws(prob, a.nodes);
+  if (!a.ws || !aligned(a.ws, 256) || a.ws_bytes < ws.total) return DA_ERR_WORKSPACE;
+  const long long rows = (long long)prob->batch * a.nodes * prob->num_q_heads;
+  const long long out_bytes = rows * prob->head_dim_v * 2;
+  // units of work read all of a row's queries, at any time
+  if (overlap(a.out, out_bytes, a.q, out_bytes) || overlap(a.lse, rows * 4, a.q, out_bytes) ||
+      overlap(a.out, out_bytes, a.lse, rows * 4))
+    return DA_ERR_INVALID_ARG;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DA_ERR_CUDA;
+  const int sms = sm_count(dev);
+  if (sms <= 0) return DA_ERR_CUDA;
+  TreeLaunch L;
+  std::memset(&L, 0, sizeof(L));
+  L.q = static_cast<const __nv_bfloat16*>(a.q);
+  L.k = a.k;
+  L.v = a.v;
+  L.table = a.table;
+  L.lengths = a.lengths;
+  L.counts = a.counts;
+  L.parents = a.parents;
+  L.out = static_cast<__nv_bfloat16*>(a.out);
+  L.lse = a.lse;
+  L.err = a.err;
+  L.o_part = static_cast<float*>(a.ws);
+  L.lse_part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + ws.lse_part);
+  L.num_blocks = prob->num_blocks;
+  L.kv_rows = cache_rows(*prob);
+  L.B = prob->batch;
+  L.T = a.nodes;
+  L.H_q = prob->num_q_heads;
+  L.H_kv = prob->num_kv_heads;
+  L.G = L.H_q / L.H_kv;
+  L.D = prob->head_dim_qk;
+  L.layout = prob->layout;
+  L.page_size = prob->page_size;
+  L.width = prob->width;
+  L.capacity = (int)row_capacity(prob->layout, prob->width, prob->page_size);
+  L.kv_type = prob->kv_dtype;
+  // (a window that reaches over everything is none)
+  L.window = (long long)a.window >= (long long)L.capacity + DA_TREE_MAX_NODES ? 0 : a.window;
+  L.sinks = a.sinks;
+  L.max_splits = tree_max_splits(prob);
+  L.scale_log2 = prob->scale * kLog2e;
+  L.v_scale = 1.f;
+  if (prob->kv_dtype != DA_KV_BF16) {
+    L.scale_log2 *= prob->k_scale;
+    L.v_scale = prob->v_scale;
+  }
+  L.test_stall = (prob->flags & DA_FLAG_TEST_STALL) != 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_tree(L, sms, s);
+  if (e == cudaSuccess && L.max_splits > 1) e = launch_tree_combine(L, s);
+  return e == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 }  // extern "C"

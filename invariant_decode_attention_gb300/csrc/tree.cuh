@@ -1,0 +1,89 @@
+// Launch descriptor and row geometry of the tree attention (tree.cu).
+#pragma once
+
+#include "common.cuh"
+
+namespace da {
+
+constexpr int kTreeTile = 64;       // entries of a tile
+constexpr int kTreeMaxSplits = 64;  // pieces of a row's list at most
+constexpr int kTreeSuper = 256;     // (node, head) rows of a unit at most
+
+struct TreeLaunch {
+  const __nv_bfloat16* q;
+  const void* k;
+  const void* v;
+  const int32_t* table;
+  const int32_t* lengths;
+  const int32_t* counts;   // null: T
+  const int32_t* parents;  // null: a chain
+  __nv_bfloat16* out;
+  float* lse;
+  int32_t* err;
+  float* lse_part;  // [B * max_splits][T][H_q], log2 units
+  float* o_part;    // [B * max_splits][T][H_q][D]
+  long long num_blocks;
+  long long kv_rows;  // entries in a cache (NVFP4: its block scales follow its codes)
+  int B, T, H_q, H_kv, G, D;
+  int layout, page_size, width, capacity, kv_type;
+  int window;  // 0: none
+  int sinks;
+  int max_splits;    // of this problem: the partials' stride
+  float scale_log2;  // softmax scale * log2(e) * k_scale
+  float v_scale;
+  int test_stall;
+};
+
+cudaError_t launch_tree(const TreeLaunch& p, int sms, cudaStream_t stream);
+cudaError_t launch_tree_combine(const TreeLaunch& p, cudaStream_t stream);
+
+// Tiles of a split at least, for a row of `rows` (node, head) pairs a KV head.  A split
+// costs its rows' fp32 partials, written and read again, so that many rows want long
+// splits; few rows want short ones, which more SMs share.
+__host__ __device__ inline int tree_min_tiles(int rows) { return rows <= 32 ? 8 : 16; }
+constexpr int kTreeLeastTiles = 8;
+
+#ifdef __CUDACC__
+
+// What a row attends to.  It follows from the row's own length, number of nodes and
+// the call's window alone.
+struct TreeRow {
+  int length, nodes;   // clamped
+  int end;             // entries of the row's list
+  int hole_from, hole_to;  // entries that no node sees (hole_from < hole_to), or none
+  int head_tiles, skip;  // tile i of the list is tile i (+ skip from head_tiles on)
+  int tiles, per_split, splits, supers;
+};
+
+__device__ __forceinline__ TreeRow tree_row(const TreeLaunch& p, int b) {
+  TreeRow r;
+  r.length = clamp_len(__ldg(p.lengths + b), p.capacity);
+  r.nodes = p.counts ? clamp_len(__ldg(p.counts + b), p.T) : p.T;
+  r.end = min(r.length + r.nodes, p.capacity);
+  r.hole_from = r.hole_to = 0;
+  r.head_tiles = r.skip = 0;
+  const int all = (r.end + kTreeTile - 1) / kTreeTile;
+  if (p.window) {  // the first node sees furthest back: its depth is 0
+    const int first = min(r.length - p.window + 1, r.end);
+    if (first > p.sinks) {
+      r.hole_from = p.sinks;
+      r.hole_to = first;
+      r.head_tiles = (p.sinks + kTreeTile - 1) / kTreeTile;
+      r.skip = max(0, first / kTreeTile - r.head_tiles);
+    }
+  }
+  r.tiles = all - r.skip;
+  const int rows = r.nodes * p.G;
+  r.per_split = max(tree_min_tiles(rows), (r.tiles + kTreeMaxSplits - 1) / kTreeMaxSplits);
+  r.splits = max(1, (r.tiles + r.per_split - 1) / r.per_split);
+  r.supers = (rows + kTreeSuper - 1) / kTreeSuper;
+  return r;
+}
+
+__device__ __forceinline__ int tree_tile(const TreeRow& r, int i) {
+  return i < r.head_tiles ? i : i + r.skip;
+}
+
+#endif  // __CUDACC__
+
+}  // namespace da
