@@ -1,9 +1,13 @@
 // Attention of a tree of drafted tokens over the caches: every node of a row attends
 // to the row's context and to its own ancestors.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <cstring>
 
 #include "merge.cuh"
+#include "tcgen05.cuh"
 #include "tree.cuh"
 
 namespace da {
@@ -113,7 +117,7 @@ __device__ void attend_plainly(const TreeLaunch& p, const TreeRow& r, int b, int
       s *= p.scale_log2;
       const float m_new = s > m ? s : m;  // (a NaN moves nothing and stays in the sum)
       const float alpha = m_new == m ? 1.f : ex2(m - m_new);
-      const float w = s == m_new ? 1.f : ex2(s - m_new);
+      const float w = ex2(s - (m_new == -INFINITY ? 0.f : m_new));
       l = fmaf(l, alpha, w);
 #pragma unroll
       for (int e = 0; e < N; ++e) o[e] = fmaf(o[e], alpha, w * v[e]);
@@ -125,39 +129,817 @@ __device__ void attend_plainly(const TreeLaunch& p, const TreeRow& r, int b, int
   *l_out = l;
 }
 
-constexpr int kWarps = 8;
+// ------------------------------------------------------------------ shapes
 
-// A warp for each (split, row, node, head).
+constexpr int kT = kTreeTile;
+constexpr int kRows = 128;         // rows of an MMA: TMEM lanes
+constexpr int kRegion = kT * 128;  // 64 rows of 128 bytes, swizzled
+constexpr int kMaxStages = 12;
+constexpr float kRescaleLog2 = 8.f;
+
+// Shared memory.  KT: the cache's type; quantized caches pass raw stages of cache bytes
+// and are widened to f16 into the operand stages.
 template <int KT, int D>
-__global__ void __launch_bounds__(kWarps * 32) tree_kernel(const TreeLaunch p) {
-  constexpr int N = D / 32;
-  wait_prior_grid();
+struct Lay {
+  static constexpr bool Q8 = KT != DA_KV_BF16;
+  static constexpr int kTile = (D / 64) * kRegion;  // K (or V) of a tile, 16-bit elements
+  static constexpr int kStage = 2 * kTile;
+  static constexpr int kStages = (Q8 ? 4 : 6) * (128 / D);
+  static constexpr int kCodeRow = KT == DA_KV_NVFP4 ? D / 2 : D;  // code bytes of a head's row
+  static constexpr int kScaleRow = KT == DA_KV_NVFP4 ? D / 16 : 0;
+  static constexpr int kRaw = 2 * kT * (kCodeRow + kScaleRow);
+  static constexpr int kRawStage = (kRaw + 1023) / 1024 * 1024;
+  static constexpr int kRawStages = !Q8 ? 0 : D == 64 ? 8 : KT == DA_KV_NVFP4 ? 6 : 5;
+  static constexpr int kRawOffset = kStages * kStage;
+  static constexpr int kBarOffset = kRawOffset + kRawStages * kRawStage;
+  // barriers
+  static constexpr int kFull = 0, kEmpty = kFull + kStages, kRawFull = kEmpty + kStages,
+                       kRawEmpty = kRawFull + kRawStages, kQFull = kRawEmpty + kRawStages, kSFull = kQFull + 2,
+                       kPFull = kSFull + 2, kPVDone = kPFull + 2, kDrain = kPVDone + 2, kStall = kDrain + 1,
+                       kBars = kStall + 1;
+  static constexpr int kSlots = kBarOffset + kBars * 8;      // TMEM address, abort flag
+  static constexpr int kStats = (kSlots + 8 + 15) / 16 * 16;  // m and l of 2 x 128 rows
+  static constexpr int kSizes = kStats + 2 * 2 * kRows * 4;   // length and nodes of each row
+  static constexpr int kFirst = kSizes + kTreeRows * 8;       // first unit of each row
+  static constexpr int kBytes = kFirst + (kTreeRows + 1) * 4;
+  // warps 0-3 and 4-7 softmax and output, 8 and 9 MMAs, 10 copies, (11 none), 12-15 conversion
+  static constexpr int kThreads = Q8 ? 512 : 352;
+  static_assert(kBytes <= 232448, "fits a block's shared memory");
+  static_assert(kBytes > 232448 / 2, "one block an SM (TMEM is taken whole)");
+};
+
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kSCol = 0;    // S of the two streams, 64 columns each; P over its first 32
+constexpr uint32_t kOCol = 128;  // their O
+constexpr uint32_t kQCol = 384;  // their Q, two elements a column
+
+struct Maps {
+  CUtensorMap k3, v3;  // [entries][H_kv][row], boxes of 16 to 64 entries
+  CUtensorMap k2, v2;  // [entries * H_kv][row], single rows (gathers)
+};
+
+struct Ctx {
+  uint8_t* smem;
+  uint32_t sbase, bars;
+  volatile int* abort_flag;
+  int32_t* err;
+  const int2* sizes;
+  const int* first;
+  int units;
+};
+
+__device__ __forceinline__ void report(int32_t* err, int bits) {
+  if (err) atomicOr(err, bits);
+}
+
+// Bounded wait that also gives up when another role has.
+__device__ __forceinline__ bool wait_bar(const Ctx& c, int i, uint32_t parity,
+                                         unsigned long long limit_ns = kWaitLimitNs) {
+  const uint32_t bar = c.bars + 8 * i;
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      if (*c.abort_flag) return false;
+      if (globaltimer_ns() - t0 > limit_ns) {
+        report(c.err, DA_DEVERR_TIMEOUT);
+        *c.abort_flag = 1;
+        return false;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ bool wait_warp(const Ctx& c, int i, uint32_t parity) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = wait_bar(c, i, parity) ? 1 : 0;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+__device__ __forceinline__ void arrive_warp(const Ctx& c, int i) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(c.bars + 8 * i);
+}
+
+__device__ __forceinline__ void fence_proxy_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// A unit of work: tiles [begin, end) of row b's list, KV head h, (node, head) rows
+// row0 .. row0 + rows - 1 of the row's.
+struct Unit {
+  TreeRow r;
+  int b, h, split, begin, end, row0, rows;
+  bool wide;  // more than 128 rows: each stream has its own, over all tiles
+  // Else both streams have the same rows, and each takes every other tile.
+  __device__ __forceinline__ int tiles() const { return end - begin; }
+  __device__ __forceinline__ bool takes(int stream, int i) const { return wide || (i & 1) == stream; }
+  __device__ __forceinline__ bool works(int stream) const { return tiles() > (wide ? 0 : stream); }
+};
+
+__device__ __forceinline__ Unit unit_of(const TreeLaunch& p, const Ctx& c, int u) {
+  int lo = 0, hi = p.rows;  // the row with first[row] <= u < first[row + 1]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (c.first[mid] <= u)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  Unit x;
+  const int2 size = c.sizes[lo];
+  x.r = tree_row(p, size.x, size.y);
+  x.b = p.row0 + lo;
+  u -= c.first[lo];
+  x.row0 = u % x.r.supers * kTreeSuper;
+  u /= x.r.supers;
+  x.h = u % p.H_kv;
+  x.split = u / p.H_kv;
+  x.begin = x.split * x.r.per_split;
+  x.end = min(x.begin + x.r.per_split, x.r.tiles);
+  x.rows = min(kTreeSuper, x.r.nodes * p.G - x.row0);
+  x.wide = x.rows > kRows;
+  return x;
+}
+
+// Low n bits.
+__device__ __forceinline__ unsigned long long low_bits(int n) {
+  return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+
+// Bits of the tile's entries (from j0 on) that no node of the row sees.
+__device__ __forceinline__ unsigned long long hidden_bits(const TreeRow& r, int j0) {
+  unsigned long long hid = ~low_bits(r.end - j0);
+  if (r.hole_to > j0) hid |= low_bits(r.hole_to - j0) & ~low_bits(r.hole_from - j0);
+  return hid;
+}
+
+// ------------------------------------------------------------------ copies
+
+__device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap* tm, int c0, int c1, int c2,
+                                         uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* tm, int col, const int (&r)[4],
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(col), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
+      : "memory");
+}
+
+// One warp.  box > 0: the list's entries lie `box` at a time (64, 32 or 16) in
+// consecutive cache rows, one copy each for K and V (and 64 dims); the lookups of eight
+// tiles are made at once, lane l those of group l % 4 of tile l / 4, a batch ahead of
+// the copies that use them.  box = 0: gathers of four rows, lane l < 16 those of entries
+// 4 l .. 4 l + 3, looked up a tile ahead.  Entries that no node sees, and those whose page is out
+// of range, are not looked up; cache row 0 is copied instead, so that no stage byte is
+// left uninitialised (their weights are zero and their values made zero).
+template <int KT, int D>
+__device__ void producer(const TreeLaunch& p, const Ctx& c, const Maps& m, int box) {
+  using L = Lay<KT, D>;
+  constexpr int kNS = L::Q8 ? L::kRawStages : L::kStages;
+  constexpr int kFullB = L::Q8 ? L::kRawFull : L::kFull, kEmptyB = L::Q8 ? L::kRawEmpty : L::kEmpty;
+  constexpr int kHalves = L::Q8 ? 1 : D / 64;      // copies of a row
+  constexpr uint32_t kTx = L::Q8 ? 2 * kT * L::kCodeRow : L::kStage;
   const int lane = threadIdx.x & 31;
-  const long long task = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int hq = (int)(task % p.H_q), t = (int)(task / p.H_q % p.T);
-  const int s = (int)(task / p.H_q / p.T % p.max_splits);
-  const long long b = task / p.H_q / p.T / p.max_splits;
-  if (b >= p.B) return;
-  const TreeRow r = tree_row(p, (int)b);
-  if (t >= r.nodes || s >= r.splits) return;
-  float m, l, o[N];
-  attend_plainly<KT, D>(p, r, (int)b, t, hq, s * r.per_split, min((s + 1) * r.per_split, r.tiles), lane, &m, &l, o);
-  const float inv = (l > 0.f ? 1.f / l : l != l ? l : 0.f) * p.v_scale;
-  const float lse = l > 0.f || l != l ? m + lg2(l) : -INFINITY;
-  const long long row = (b * p.T + t) * p.H_q + hq, slot = ((b * p.max_splits + s) * p.T + t) * p.H_q + hq;
+  bool bad = false;
+  // whether some node sees one of the entries j .. j + n - 1 (n within a tile's group)
+  auto seen = [&](const TreeRow& r, int j, int n) {
+    return j < r.end && !(j >= r.hole_from && j + n <= r.hole_to);
+  };
+  // table word for entry j of a row (0 where there is none to look up)
+  auto word_of = [&](const Unit& x, int j, int n) -> int {
+    if (p.layout == DA_KV_CONTIGUOUS || !seen(x.r, j, n)) return 0;
+    return __ldg(p.table + (long long)x.b * p.width + (p.layout == DA_KV_PAGED ? j / p.page_size : j));
+  };
+  auto row_of = [&](const Unit& x, int j, int n, int word) -> int {
+    if (!seen(x.r, j, n)) return 0;
+    if (p.layout == DA_KV_CONTIGUOUS) return x.b * p.width + j;
+    if (word < 0 || word >= p.num_blocks) {
+      bad = true;
+      return 0;
+    }
+    return p.layout == DA_KV_PAGED ? word * p.page_size + j % p.page_size : word;
+  };
+  const int groups = box ? kT / box : 0;
+  // this lane's word for tiles 8 bt .. 8 bt + 7 of a unit
+  auto batch = [&](const Unit& x, int bt) -> int {
+    const int i = x.begin + 8 * bt + (lane >> 2);
+    if (i >= x.end || (lane & 3) >= groups) return 0;
+    return word_of(x, tree_tile(x.r, i) * kT + (lane & 3) * box, box);
+  };
+  uint32_t g = 0;
+  bool alive = true;
+  Unit x = unit_of(p, c, blockIdx.x);
+  int first_words = box ? batch(x, 0) : 0;
+  for (int u = blockIdx.x; u < c.units && alive; u += gridDim.x) {
+    const bool more = u + (int)gridDim.x < c.units;
+    const Unit next = more ? unit_of(p, c, u + gridDim.x) : x;
+    const int n = x.tiles(), last_batch = (n - 1) / 8;
+    int words = first_words, ahead = 0;
+    if (box && n > 8) ahead = batch(x, 1);
+    if (box && more && n <= 8) first_words = batch(next, 0);
+    int wg[4] = {0, 0, 0, 0}, wg_next[4] = {0, 0, 0, 0};
+    if (!box && lane < 16 && n > 0)
+      for (int e = 0; e < 4; ++e) wg[e] = word_of(x, tree_tile(x.r, x.begin) * kT + lane * 4 + e, 1);
+    for (int i = 0; i < n; ++i, ++g) {
+      const int j0 = tree_tile(x.r, x.begin + i) * kT, st = g % kNS;
+      if (box) {
+        if (i > 0 && (i & 7) == 0) {
+          words = ahead;
+          if ((i >> 3) < last_batch) ahead = batch(x, (i >> 3) + 1);
+          if ((i >> 3) == last_batch && more) first_words = batch(next, 0);
+        }
+      } else if (lane < 16 && i + 1 < n) {
+        const int j1 = tree_tile(x.r, x.begin + i + 1) * kT;
+        for (int e = 0; e < 4; ++e) wg_next[e] = word_of(x, j1 + lane * 4 + e, 1);
+      }
+      if (!wait_warp(c, kEmptyB + st, ((g / kNS) & 1) ^ 1)) {
+        alive = false;
+        break;
+      }
+      const uint32_t full = c.bars + 8 * (kFullB + st);
+      if (lane == 0) mbar_arrive_expect_tx(full, kTx);
+      __syncwarp();
+      const uint32_t kdst = c.sbase + (L::Q8 ? L::kRawOffset + st * L::kRawStage : st * L::kStage);
+      const uint32_t vdst = kdst + (L::Q8 ? kT * L::kCodeRow : L::kTile);
+      constexpr int kRowBytes = L::Q8 ? L::kCodeRow : 128;  // of a row in the stage (of a half)
+      int row[4] = {0, 0, 0, 0};  // cache rows of this lane's group, or of its four entries
+      if (box) {
+        const int grp = lane & 3;
+        if ((lane >> 2) == (i & 7) && grp < groups) {
+          row[0] = row_of(x, j0 + grp * box, box, words);
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
-    if (r.splits == 1)
-      p.out[row * D + lane * N + e] = __float2bfloat16_rn(o[e] * inv);
-    else
-      p.o_part[slot * D + lane * N + e] = o[e] * inv;
+          for (int half = 0; half < kHalves; ++half) {
+            const uint32_t off = half * kRegion + grp * box * kRowBytes;
+            tma_box3(kdst + off, &m.k3, 64 * half, x.h, row[0], full);
+            tma_box3(vdst + off, &m.v3, 64 * half, x.h, row[0], full);
+          }
+        }
+      } else if (lane < 16) {
+        int at[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          row[e] = row_of(x, j0 + lane * 4 + e, 1, wg[e]);
+          at[e] = row[e] * p.H_kv + x.h;
+          wg[e] = wg_next[e];
+        }
+#pragma unroll
+        for (int half = 0; half < kHalves; ++half) {
+          const uint32_t off = half * kRegion + lane * 4 * kRowBytes;
+          tma_gather4(kdst + off, &m.k2, 64 * half, at, full);
+          tma_gather4(vdst + off, &m.v2, 64 * half, at, full);
+        }
+      }
+      if constexpr (KT == DA_KV_NVFP4) {
+        // block scales of entries 2 lane and 2 lane + 1: K's rows, then V's
+        const long long blocks = p.kv_rows * p.H_kv * (D / 2);
+        const uint32_t sdst = kdst + 2 * kT * L::kCodeRow;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int k = 2 * lane + e;
+          long long at;
+          if (box) {
+            const int base = __shfl_sync(0xffffffffu, row[0], (i & 7) * 4 + k / box);
+            at = min((long long)base + k % box, p.kv_rows - 1);
+          } else {
+            const int a = __shfl_sync(0xffffffffu, row[e], k >> 2);
+            const int b = __shfl_sync(0xffffffffu, row[2 + e], k >> 2);
+            at = min((long long)((k & 2) ? b : a), p.kv_rows - 1);
+          }
+          if (p.kv_rows > 0) {
+            const long long off = blocks + (at * p.H_kv + x.h) * L::kScaleRow;
+            const uint32_t to = sdst + k * L::kScaleRow;
+            if constexpr (L::kScaleRow == 8) {
+              cp_async8(to, static_cast<const uint8_t*>(p.k) + off);
+              cp_async8(to + kT * L::kScaleRow, static_cast<const uint8_t*>(p.v) + off);
+            } else {
+              cp_async4(to, static_cast<const uint8_t*>(p.k) + off);
+              cp_async4(to + kT * L::kScaleRow, static_cast<const uint8_t*>(p.v) + off);
+            }
+          }
+        }
+        cp_async_mbar_arrive(full);
+      }
+    }
+    x = next;
   }
+  if (__any_sync(0xffffffffu, bad) && lane == 0) report(p.err, DA_DEVERR_INDEX);
+  if constexpr (KT == DA_KV_NVFP4) cp_async_wait_all();
+  // leave no copy in flight (after a time-out; else every stage was consumed)
   if (lane == 0) {
-    if (r.splits == 1)
-      p.lse[row] = lse * kLn2;
-    else
-      p.lse_part[slot] = lse;
+    for (int st = 0; st < kNS; ++st) {
+      const int last = (int)g - 1 - (((int)g - 1 - st) % kNS + kNS) % kNS;
+      if (last >= 0 && !mbar_wait(c.bars + 8 * (kFullB + st), (last / kNS) & 1)) report(p.err, DA_DEVERR_TIMEOUT);
+    }
   }
+}
+
+// ------------------------------------------------------------------ conversion
+// Four warps.  E4M3 values are f16 values, and so are NVFP4 elements (a code times its
+// block scale, multiplied in f16), so K and V become f16 without error.
+template <int KT, int D>
+__device__ void converter(const TreeLaunch& p, const Ctx& c) {
+  using L = Lay<KT, D>;
+  constexpr int kPieces = D / 16;               // 16-dim pieces of a row
+  constexpr int kStep = 128 / kPieces;          // rows between a thread's
+  const int ct = threadIdx.x - 12 * 32;
+  const int jj = ct % kPieces, r0 = ct / kPieces;
+  uint32_t g = 0;
+  for (int u = blockIdx.x; u < c.units; u += gridDim.x) {
+    const Unit x = unit_of(p, c, u);
+    for (int i = 0; i < x.tiles(); ++i, ++g) {
+      const int rs = g % L::kRawStages, os = g % L::kStages;
+      if (!wait_warp(c, L::kRawFull + rs, (g / L::kRawStages) & 1)) return;
+      if (!wait_warp(c, L::kEmpty + os, ((g / L::kStages) & 1) ^ 1)) return;
+      const uint8_t* raw = c.smem + L::kRawOffset + rs * L::kRawStage;
+      uint8_t* op = c.smem + os * L::kStage;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll
+        for (int q = 0; q < kT / kStep; ++q) {
+          const int row = r0 + kStep * q;
+          uint32_t h[8];  // dims 16 jj .. 16 jj + 15
+          const uint8_t* codes = raw + kv * kT * L::kCodeRow + row * L::kCodeRow;
+          if constexpr (KT == DA_KV_NVFP4) {
+            const uint2 w = *reinterpret_cast<const uint2*>(codes + jj * 8);
+            const uint32_t block = raw[2 * kT * L::kCodeRow + (kv * kT + row) * L::kScaleRow + jj];
+            const uint32_t s2 = __byte_perm(e4m3x2_to_f16x2(block), 0, 0x1010);
+            uint32_t lo[4], hi[4];
+            e2m1x8_to_f16x2(w.x, lo);
+            e2m1x8_to_f16x2(w.y, hi);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              h[e] = hmul2(lo[e], s2);
+              h[4 + e] = hmul2(hi[e], s2);
+            }
+          } else {
+            const uint4 w = *reinterpret_cast<const uint4*>(codes + jj * 16);
+            const uint32_t wb[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              h[2 * e] = e4m3x2_to_f16x2(wb[e]);
+              h[2 * e + 1] = e4m3x2_to_f16x2(wb[e] >> 16);
+            }
+          }
+          // region jj / 4, chunks 2 (jj % 4) and + 1, in an order that spreads the banks
+          uint8_t* to = op + kv * L::kTile + (jj >> 2) * kRegion + row * 128;
+          const int ch = 2 * (jj & 3), sw = (jj >> 2) & 1;
+          const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+          *reinterpret_cast<uint4*>(to + (((ch + sw) ^ (row & 7)) << 4)) = sw ? hi : lo;
+          *reinterpret_cast<uint4*>(to + (((ch + 1 - sw) ^ (row & 7)) << 4)) = sw ? lo : hi;
+        }
+      }
+      fence_proxy_async();
+      arrive_warp(c, L::kFull + os);
+      arrive_warp(c, L::kRawEmpty + rs);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ MMAs
+// One thread for each stream: S = Q K^T of its next tile (Q in tensor memory), then, once
+// the softmax has put P over S, O += P V.  The next S overwrites P, so it waits for the
+// P V before; the other stream's MMAs fill that time.
+template <int KT, int D>
+__device__ void issue(const TreeLaunch& p, const Ctx& c, uint32_t tmem, int stream) {
+  using L = Lay<KT, D>;
+  constexpr uint32_t kIdescS = L::Q8 ? umma::idesc_f16_f32(kRows, kT, false) : umma::idesc_bf16_f32(kRows, kT, false);
+  constexpr uint32_t kIdescO = L::Q8 ? umma::idesc_f16_f32(kRows, D, true) : umma::idesc_bf16_f32(kRows, D, true);
+  const uint64_t k0 = umma::smem_desc(c.sbase, 16, 1024, umma::kSwizzle128B);
+  // V with its dims contiguous: 64-dim regions kRegion apart, 8-entry groups 1024 bytes
+  const uint64_t v0 = umma::smem_desc(c.sbase + L::kTile, kRegion, 1024, umma::kSwizzle128B);
+  const uint32_t s_col = tmem + kSCol + stream * kT, o_col = tmem + kOCol + stream * D;
+  const uint32_t q_col = tmem + kQCol + stream * 64;
+  if (p.test_stall && stream == 0 && !wait_bar(c, L::kStall, 0, kTestStallNs)) return;
+  uint32_t g = 0, mine = 0, nq = 0;  // tiles of the CTA, of the stream; units of the stream
+  for (int u = blockIdx.x; u < c.units; u += gridDim.x) {
+    const Unit x = unit_of(p, c, u);
+    if (x.works(stream)) {
+      if (!wait_bar(c, L::kQFull + stream, nq & 1)) return;
+      ++nq;
+    }
+    bool start = true;
+    for (int i = 0; i < x.tiles(); ++i, ++g) {
+      if (!x.takes(stream, i)) continue;
+      const int st = g % L::kStages;
+      if (!wait_bar(c, L::kFull + st, (g / L::kStages) & 1)) return;
+      if (mine && !wait_bar(c, L::kPVDone + stream, (mine - 1) & 1)) return;
+      fence_proxy_async();
+      umma::fence_after_sync();
+      const uint64_t stage = (uint64_t)((st * L::kStage) >> 4);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        umma::mma_bf16_ta(s_col, q_col + k * 8, k0 + stage + (uint64_t)(((k / 4) * kRegion + (k % 4) * 32) >> 4),
+                          kIdescS, k ? 1u : 0u);
+      umma::commit(c.bars + 8 * (L::kSFull + stream));
+      if (!wait_bar(c, L::kPFull + stream, mine & 1)) return;
+      umma::fence_after_sync();
+#pragma unroll
+      for (int k = 0; k < kT / 16; ++k)
+        umma::mma_bf16_ta(o_col, s_col + k * 8, v0 + stage + (uint64_t)((k * 2048) >> 4), kIdescO,
+                          (start && k == 0) ? 0u : 1u);
+      umma::commit(c.bars + 8 * (L::kPVDone + stream));
+      umma::commit(c.bars + 8 * (L::kEmpty + st));  // (two arrivals free a stage)
+      if (!x.wide) umma::commit(c.bars + 8 * (L::kEmpty + st));
+      start = false;
+      ++mine;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ softmax and output
+
+// Bits of the nodes that a node with these ancestors sees (see decode_attn.h): the i-th of
+// them from below is at depth i.
+__device__ __forceinline__ unsigned long long windowed(const TreeLaunch& p, const TreeRow& r,
+                                                       unsigned long long anc, int depth) {
+  if (!p.window || p.window > depth) return anc;
+  unsigned long long keep = anc, left = anc;
+  for (int i = 0; i <= depth - p.window; ++i, left &= left - 1)
+    if (r.length + i >= p.sinks) keep &= ~(left & (0 - left));
+  return keep;
+}
+
+// Four warps a stream; a thread has one row, a TMEM lane.  Its scores' running reference
+// value moves only when one exceeds it by more than 2^8 (then its O is rescaled).
+template <int KT, int D>
+__device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem, int stream) {
+  using L = Lay<KT, D>;
+  const int lane = threadIdx.x & 31, tid = threadIdx.x & 127, warp = tid >> 5;
+  const uint32_t base = tmem + ((uint32_t)(warp * 32) << 16);
+  const uint32_t s_col = base + kSCol + stream * kT, o_col = base + kOCol + stream * D;
+  const uint32_t q_col = base + kQCol + stream * 64;
+  float* stats = reinterpret_cast<float*>(c.smem + L::kStats);  // [stream][m, l][128]
+  uint32_t g = 0, mine = 0;
+  for (int u = blockIdx.x; u < c.units; u += gridDim.x) {
+    const Unit x = unit_of(p, c, u);
+    const TreeRow& r = x.r;
+    const int idx = x.row0 + (x.wide ? stream * kRows : 0) + tid;  // (node, head) row
+    const bool live = idx < x.row0 + x.rows;
+    const int t = live ? idx / p.G : 0, head = x.h * p.G + (live ? idx % p.G : 0);
+    const long long q_row = ((long long)x.b * p.T + t) * p.H_q + head;
+    float row_scale = p.scale_log2;
+    bool ok = true;
+    if (x.works(stream)) {
+      // ---- Q into tensor memory: bf16 as it is, or f16 scaled by a power of two
+      uint4 w[D / 8];
+      const uint4* from = reinterpret_cast<const uint4*>(p.q + q_row * D);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) w[i] = live ? __ldg(from + i) : make_uint4(0, 0, 0, 0);
+      float sc = 1.f;
+      if constexpr (L::Q8) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) most = bf16x8_absmax_bits(most, w[i]);
+        const int e = q_prescale_exp(bf16_absmax_value(most));
+        sc = exp2_int(e);
+        row_scale *= exp2_int(-e);
+      }
+#pragma unroll
+      for (int half = 0; half < D / 64; ++half) {
+        uint32_t q32[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t v[4] = {w[half * 8 + i].x, w[half * 8 + i].y, w[half * 8 + i].z, w[half * 8 + i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (L::Q8) {
+              const __half2 hh = __floats2half2_rn(bf16_lo(v[e]) * sc, bf16_hi(v[e]) * sc);
+              q32[4 * i + e] = *reinterpret_cast<const uint32_t*>(&hh);
+            } else {
+              q32[4 * i + e] = v[e];
+            }
+          }
+        }
+        umma::st_32x32b_x32_u(q_col + half * 32, q32);
+      }
+      umma::wait_st();
+      umma::fence_before_sync();
+      arrive_warp(c, L::kQFull + stream);
+    }
+    // ---- what the row sees, if the unit's last tile reaches the nodes or there is a window
+    const bool edge = p.window || (x.tiles() > 0 && (tree_tile(r, x.end - 1) + 1) * kT > r.length);
+    unsigned long long anc = 0;
+    int depth = 0;
+    if (edge && live) {
+      anc = windowed(p, r, ancestors(p, x.b, t, &depth), depth);
+      anc &= low_bits(r.end - r.length);
+    }
+    float m_used = -INFINITY, l = 0.f;
+    bool start = true;
+    for (int i = 0; i < x.tiles(); ++i, ++g) {
+      if (!x.takes(stream, i)) continue;
+      if (!wait_warp(c, L::kSFull + stream, mine & 1)) {
+        ok = false;
+        break;
+      }
+      umma::fence_after_sync();
+      float s[kT];
+      umma::ld_32x32b_x32(s_col, *reinterpret_cast<float(*)[32]>(s));
+      umma::ld_32x32b_x32(s_col + 32, *reinterpret_cast<float(*)[32]>(s + 32));
+      umma::wait_ld();
+      const int j0 = tree_tile(r, x.begin + i) * kT;
+      const bool all = j0 + kT <= r.length && (!p.window || j0 + kT <= p.sinks || j0 >= r.length + r.nodes - p.window);
+      float mt = -INFINITY;
+      if (all) {
+#pragma unroll
+        for (int k = 0; k < kT; ++k) mt = fmaxf(mt, s[k]);
+        // (a negative scale turns the order around)
+        if (row_scale < 0.f) {
+          mt = INFINITY;
+#pragma unroll
+          for (int k = 0; k < kT; ++k) mt = fminf(mt, s[k]);
+        }
+        mt *= row_scale;
+#pragma unroll
+        for (int k = 0; k < kT; ++k) s[k] *= row_scale;
+      } else {
+        unsigned long long vis = low_bits(r.length - j0);
+        if (p.window) vis &= ~low_bits(r.length + depth - p.window + 1 - j0) | low_bits(p.sinks - j0);
+        const int shift = r.length - j0;  // of node 0 in the tile
+        if (shift > -64 && shift < 64) vis |= shift >= 0 ? anc << shift : anc >> -shift;
+        if (!live) vis = 0;
+#pragma unroll
+        for (int k = 0; k < kT; ++k) {
+          s[k] = (vis >> k & 1) ? s[k] * row_scale : -INFINITY;
+          mt = fmaxf(mt, s[k]);
+        }
+      }
+      const bool move = mt > m_used + kRescaleLog2 || (m_used == -INFINITY && mt > -INFINITY);
+      const float m_new = move ? mt : m_used;
+      const float alpha = (move && m_used > -INFINITY) ? ex2(m_used - m_new) : 1.f;
+      const float ref = m_new == -INFINITY ? 0.f : m_new;
+      float sum = 0.f;
+      uint32_t pk[kT / 2];
+#pragma unroll
+      for (int k = 0; k < kT; k += 2) {
+        const float p0 = ex2(s[k] - ref), p1 = ex2(s[k + 1] - ref);
+        sum += p0;
+        sum += p1;
+        if constexpr (L::Q8) {
+          const __half2 h = __floats2half2_rn(p0, p1);
+          pk[k / 2] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+          pk[k / 2] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+      l = fmaf(l, alpha, sum);
+      umma::st_32x32b_x32_u(s_col, pk);
+      // (S was issued after the stream's P V before it, so O stands still)
+      if (!start && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          float o[32];
+          umma::ld_32x32b_x32(o_col + ch * 32, o);
+          umma::wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] *= alpha;
+          umma::st_32x32b_x32(o_col + ch * 32, o);
+        }
+      }
+      m_used = m_new;
+      // values of entries that no node sees: zero times what lies there could be a NaN
+      const unsigned long long hid = hidden_bits(r, j0);
+      if (hid) {
+        const int st = g % L::kStages, k = tid >> 1;
+        if (!wait_warp(c, L::kFull + st, (g / L::kStages) & 1)) {  // (it has been: this orders the stores)
+          ok = false;
+          break;
+        }
+        if (hid >> k & 1) {
+          uint8_t* v = c.smem + st * L::kStage + L::kTile + k * 128 + (D == 128 ? (tid & 1) * kRegion : (tid & 1) * 64);
+#pragma unroll
+          for (int e = 0; e < (D == 128 ? 8 : 4); ++e) reinterpret_cast<uint4*>(v)[e] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
+      }
+      umma::wait_st();
+      umma::fence_before_sync();
+      arrive_warp(c, L::kPFull + stream);
+      start = false;
+      ++mine;
+    }
+    // ---- output
+    if (ok && x.works(stream)) ok = wait_warp(c, L::kPVDone + stream, (mine - 1) & 1);
+    stats[stream * 2 * kRows + tid] = m_used;
+    stats[stream * 2 * kRows + kRows + tid] = l;
+    // all eight warps leave together, or none
+    if (named_bar_or(1, 256, !ok)) return;
+    umma::fence_after_sync();
+    float M = m_used, sum = l, f[2] = {1.f, 1.f};
+    bool has[2] = {stream == 0, stream == 1};  // streams whose O this thread adds up
+    if (!x.wide) {
+      const float* other = stats + (stream ^ 1) * 2 * kRows;
+      const float m2 = other[tid], l2 = other[kRows + tid];
+      M = fmaxf(m_used, m2);
+      const float f_own = m_used == -INFINITY ? 0.f : ex2(m_used - M), f_other = m2 == -INFINITY ? 0.f : ex2(m2 - M);
+      f[stream] = f_own;
+      f[stream ^ 1] = f_other;
+      // in the same order in both streams
+      sum = stream == 0 ? fmaf(f_own, l, f_other * l2) : fmaf(f_other, l2, f_own * l);
+      has[0] = x.tiles() > 0;
+      has[1] = x.tiles() > 1;
+    }
+    const bool single = r.splits == 1;
+    const long long out_row = ((long long)x.b * p.T + t) * p.H_q + head;
+    const long long slot = (((long long)x.b * p.max_splits + x.split) * p.T + t) * p.H_q + head;
+    const float inv = (sum > 0.f ? 1.f / sum : sum != sum ? sum : 0.f) * p.v_scale;
+    const int ch0 = x.wide ? 0 : stream * (D / 64), ch1 = x.wide ? D / 32 : ch0 + D / 64;
+    bool odd = sum != sum;  // something that is not finite
+#pragma unroll 1
+    for (int ch = ch0; ch < ch1; ++ch) {
+      float o[32];
+      if (!x.wide && has[1]) {
+        float o1[32];
+        umma::ld_32x32b_x32(base + kOCol + ch * 32, o);
+        umma::ld_32x32b_x32(base + kOCol + D + ch * 32, o1);
+        umma::wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = fmaf(f[0], o[k], f[1] * o1[k]);
+      } else if (x.wide || has[0]) {
+        umma::ld_32x32b_x32((x.wide ? o_col : base + kOCol) + ch * 32, o);
+        umma::wait_ld();
+      }
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        o[k] = x.tiles() > 0 ? o[k] * inv : 0.f;
+        odd |= !(fabsf(o[k]) < INFINITY);
+      }
+      if (live && single) {
+        uint4* to = reinterpret_cast<uint4*>(p.out + out_row * D + ch * 32);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(o[8 * k + 2 * e], o[8 * k + 2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          to[k] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      } else if (live) {
+        float4* to = reinterpret_cast<float4*>(p.o_part + slot * D + ch * 32);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) to[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+      }
+      __syncwarp();
+    }
+    float lse = sum > 0.f || sum != sum ? M + lg2(sum) : -INFINITY;
+    if (live && (x.wide || stream == 0)) {
+      if (single)
+        p.lse[out_row] = lse * kLn2;
+      else
+        p.lse_part[slot] = lse;
+    }
+    // A value that some node sees and another does not may have been infinite or NaN: zero
+    // times it has spoiled the other's sum.  Such rows are formed again, entry by entry.
+    for (uint32_t again = __ballot_sync(0xffffffffu, live && odd); again; again &= again - 1) {
+      const int src = __ffs((int)again) - 1;
+      const int at = __shfl_sync(0xffffffffu, t, src), hq = __shfl_sync(0xffffffffu, head, src);
+      float m2, l2, o[D / 32];
+      attend_plainly<KT, D>(p, r, x.b, at, hq, x.begin, x.end, lane, &m2, &l2, o);
+      const float inv2 = (l2 > 0.f ? 1.f / l2 : l2 != l2 ? l2 : 0.f) * p.v_scale;
+      const float lse2 = l2 > 0.f || l2 != l2 ? m2 + lg2(l2) : -INFINITY;
+      const long long row2 = ((long long)x.b * p.T + at) * p.H_q + hq;
+      const long long slot2 = (((long long)x.b * p.max_splits + x.split) * p.T + at) * p.H_q + hq;
+      if (x.wide || (lane >> 4) == stream) {  // this stream's dims
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) {
+          const int d = lane * (D / 32) + e;
+          if (single)
+            p.out[row2 * D + d] = __float2bfloat16_rn(o[e] * inv2);
+          else
+            p.o_part[slot2 * D + d] = o[e] * inv2;
+        }
+      }
+      if (lane == 0 && (x.wide || stream == 0)) {
+        if (single)
+          p.lse[row2] = lse2 * kLn2;
+        else
+          p.lse_part[slot2] = lse2;
+      }
+      __syncwarp();
+    }
+    umma::fence_before_sync();
+    named_bar_sync(1, 256);  // O and the statistics have been read
+    umma::fence_after_sync();
+  }
+}
+
+template <int KT, int D>
+__global__ void __launch_bounds__(Lay<KT, D>::kThreads, 1)
+    tree_kernel(const TreeLaunch p, const __grid_constant__ Maps maps, int box) {
+  using L = Lay<KT, D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Ctx c;
+  c.smem = smem;
+  c.sbase = smem_addr(smem);
+  c.bars = c.sbase + L::kBarOffset;
+  c.abort_flag = reinterpret_cast<volatile int*>(smem + L::kSlots + 4);
+  c.err = p.err;
+  int2* sizes = reinterpret_cast<int2*>(smem + L::kSizes);
+  int* first = reinterpret_cast<int*>(smem + L::kFirst);
+  c.sizes = sizes;
+  c.first = first;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kBars; ++i) {
+      uint32_t count = 1;  // tcgen05.commit, or the producer's expect_tx arrive
+      if (i >= L::kFull && i < L::kFull + L::kStages && L::Q8) count = 4;
+      if (i >= L::kEmpty && i < L::kEmpty + L::kStages) count = 2;
+      if (i >= L::kRawFull && i < L::kRawFull + L::kRawStages && KT == DA_KV_NVFP4) count = 33;
+      if (i >= L::kRawEmpty && i < L::kRawEmpty + L::kRawStages) count = 4;
+      if ((i >= L::kQFull && i < L::kQFull + 2) || (i >= L::kPFull && i < L::kPFull + 2)) count = 4;
+      if (i == L::kDrain) count = 2;
+      mbar_init(c.bars + 8 * i, count);
+    }
+    *c.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    umma::tmem_alloc(c.sbase + L::kSlots, kTmemCols);
+    umma::tmem_relinquish();
+  }
+  wait_prior_grid();
+  allow_next_grid();
+  // ---- the rows' units, counted by every CTA for itself
+  int bad = 0;
+  for (int i = threadIdx.x; i < p.rows; i += L::kThreads) {
+    const int2 s = tree_size(p, p.row0 + i, &bad);
+    const TreeRow r = tree_row(p, s.x, s.y);
+    sizes[i] = s;
+    first[i + 1] = r.splits * r.supers * p.H_kv;
+  }
+  if (blockIdx.x == 0) {  // inputs that are out of range
+    if (p.parents)
+      for (int i = threadIdx.x; i < p.rows * p.T; i += L::kThreads) {
+        const int t = i % p.T, up = __ldg(p.parents + (long long)p.row0 * p.T + i);
+        if (t < (p.counts ? __ldg(p.counts + p.row0 + i / p.T) : p.T) && (up < -1 || up >= t)) bad |= DA_DEVERR_INDEX;
+      }
+    if (bad) report(p.err, bad);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int sum = 0;
+    for (int i0 = 0; i0 < p.rows; i0 += 32) {
+      int v = i0 + lane < p.rows ? first[i0 + lane + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+      }
+      if (i0 + lane < p.rows) first[i0 + lane + 1] = sum + v;
+      sum += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) first[0] = 0;
+  }
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  c.units = first[p.rows];
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kSlots);
+  const bool aligned = (c.sbase & 1023u) == 0;  // as the swizzled layouts need it
+  if (!aligned && threadIdx.x == 0) report(p.err, DA_DEVERR_TIMEOUT);
+
+  if ((int)blockIdx.x < c.units && aligned) {
+    if (warp < 8) {
+      softmax_warps<KT, D>(p, c, tmem, warp >> 2);
+    } else if (warp < 10) {
+      if (lane == 0) {
+        issue<KT, D>(p, c, tmem, warp - 8);
+        umma::commit(c.bars + 8 * L::kDrain);  // arrives when all MMAs of this thread are done
+      }
+    } else if (warp == 10) {
+      producer<KT, D>(p, c, maps, box);
+    } else if (warp >= 12) {
+      if constexpr (L::Q8) converter<KT, D>(p, c);
+    }
+    __syncwarp();
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    if (warp == 8 && lane == 0) {
+      const unsigned long long t0 = globaltimer_ns();
+      while (!mbar_try_wait(c.bars + 8 * L::kDrain, 0)) {
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+          report(p.err, DA_DEVERR_TIMEOUT);
+          break;
+        }
+      }
+    }
+    __syncwarp();
+  }
+  if (warp == 8) umma::tmem_dealloc(tmem, kTmemCols);
 }
 
 constexpr int kCombineWarps = 4;
@@ -176,7 +958,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
   if (task >= p.B * per) return;
   const int b = (int)(task / per);
   const long long th = task - b * per;
-  const TreeRow r = tree_row(p, b);
+  int bad = 0;  // (reported by the kernel before)
+  const int2 size = tree_size(p, b, &bad);
+  const TreeRow r = tree_row(p, size.x, size.y);
   if (th / p.H_q >= r.nodes || r.splits <= 1) return;
   const long long slot = (long long)b * p.max_splits * per + th;
   float part[kBatch][N], acc[N];
@@ -222,21 +1006,95 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
   if (lane == 0) p.lse[task] = lse;
 }
 
+// ------------------------------------------------------------------ launches
+
+// Stands in for an empty cache in a tensor map (nothing of it is used).
+__device__ __align__(128) __nv_bfloat16 g_nothing[128];
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+bool encode(CUtensorMap* tm, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box, bool bytes) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn) return false;
+  const cuuint32_t elem[3] = {1, 1, 1};
+  return fn(tm, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+            const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int KT, int D>
+cudaError_t launch_shape(const TreeLaunch& p0, int sms, cudaStream_t stream) {
+  using L = Lay<KT, D>;
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(tree_kernel<KT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  if (attr != cudaSuccess) return attr;
+  TreeLaunch p = p0;
+  // entries that lie together for sure, as many as a copy takes
+  const int box = p.layout == DA_KV_CONTIGUOUS                          ? 64
+                  : p.layout == DA_KV_INDEXED || p.page_size % 16 != 0 ? 0
+                  : p.page_size % 64 == 0                               ? 64
+                  : p.page_size % 32 == 0                               ? 32
+                                                                        : 16;
+  const void* k = p.k;
+  const void* v = p.v;
+  cuuint64_t rows = (cuuint64_t)p.kv_rows, heads = (cuuint64_t)p.H_kv;
+  if (rows < 1) {
+    void* z = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&z, g_nothing);
+    if (e != cudaSuccess) return e;
+    k = v = z;
+    rows = heads = 1;
+  }
+  const cuuint64_t row = L::Q8 ? L::kCodeRow : D, size = L::Q8 ? 1 : 2;
+  const cuuint32_t across = L::Q8 ? L::kCodeRow : 64;
+  Maps m;
+  std::memset(&m, 0, sizeof(m));
+  if (box) {
+    const cuuint64_t dims[3] = {row, heads, rows}, strides[2] = {row * size, heads * row * size};
+    const cuuint32_t bx[3] = {across, 1, (cuuint32_t)box};
+    if (!encode(&m.k3, k, 3, dims, strides, bx, L::Q8) || !encode(&m.v3, v, 3, dims, strides, bx, L::Q8))
+      return cudaErrorInvalidValue;
+  } else {
+    const cuuint64_t dims[2] = {row, rows * heads}, strides[1] = {row * size};
+    const cuuint32_t bx[2] = {across, 1};
+    if (!encode(&m.k2, k, 2, dims, strides, bx, L::Q8) || !encode(&m.v2, v, 2, dims, strides, bx, L::Q8))
+      return cudaErrorInvalidValue;
+  }
+  const int supers = (p.T * p.G + kTreeSuper - 1) / kTreeSuper;
+  for (p.row0 = 0; p.row0 < p.B; p.row0 += kTreeRows) {
+    p.rows = std::min(kTreeRows, p.B - p.row0);
+    const long long most = (long long)p.rows * p.max_splits * p.H_kv * supers;
+    const cudaError_t e = launch_after(tree_kernel<KT, D>, dim3((unsigned)std::min<long long>(most, sms)),
+                                       dim3(L::kThreads), (size_t)L::kBytes, stream, p, m, box);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
 template <int KT>
-cudaError_t launch_kt(const TreeLaunch& p, cudaStream_t stream) {
-  const long long warps = (long long)p.B * p.max_splits * p.T * p.H_q;
-  const unsigned grid = (unsigned)((warps + kWarps - 1) / kWarps);
-  return p.D == 64 ? launch_after(tree_kernel<KT, 64>, dim3(grid), dim3(kWarps * 32), 0, stream, p)
-                   : launch_after(tree_kernel<KT, 128>, dim3(grid), dim3(kWarps * 32), 0, stream, p);
+cudaError_t launch_kt(const TreeLaunch& p, int sms, cudaStream_t stream) {
+  return p.D == 64 ? launch_shape<KT, 64>(p, sms, stream) : launch_shape<KT, 128>(p, sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_tree(const TreeLaunch& p, int sms, cudaStream_t stream) {
   switch (p.kv_type) {
-    case DA_KV_FP8_E4M3: return launch_kt<DA_KV_FP8_E4M3>(p, stream);
-    case DA_KV_NVFP4: return launch_kt<DA_KV_NVFP4>(p, stream);
-    default: return launch_kt<DA_KV_BF16>(p, stream);
+    case DA_KV_FP8_E4M3: return launch_kt<DA_KV_FP8_E4M3>(p, sms, stream);
+    case DA_KV_NVFP4: return launch_kt<DA_KV_NVFP4>(p, sms, stream);
+    default: return launch_kt<DA_KV_BF16>(p, sms, stream);
   }
 }
 

@@ -32,7 +32,10 @@ struct TreeLaunch {
   float scale_log2;  // softmax scale * log2(e) * k_scale
   float v_scale;
   int test_stall;
+  int row0, rows;  // the rows of this launch
 };
+
+constexpr int kTreeRows = 1024;  // rows of a launch at most
 
 cudaError_t launch_tree(const TreeLaunch& p, int sms, cudaStream_t stream);
 cudaError_t launch_tree_combine(const TreeLaunch& p, cudaStream_t stream);
@@ -55,10 +58,10 @@ struct TreeRow {
   int tiles, per_split, splits, supers;
 };
 
-__device__ __forceinline__ TreeRow tree_row(const TreeLaunch& p, int b) {
+__device__ __forceinline__ TreeRow tree_row(const TreeLaunch& p, int length, int nodes) {
   TreeRow r;
-  r.length = clamp_len(__ldg(p.lengths + b), p.capacity);
-  r.nodes = p.counts ? clamp_len(__ldg(p.counts + b), p.T) : p.T;
+  r.length = length;
+  r.nodes = nodes;
   r.end = min(r.length + r.nodes, p.capacity);
   r.hole_from = r.hole_to = 0;
   r.head_tiles = r.skip = 0;
@@ -78,6 +81,14 @@ __device__ __forceinline__ TreeRow tree_row(const TreeLaunch& p, int b) {
   r.splits = max(1, (r.tiles + r.per_split - 1) / r.per_split);
   r.supers = (rows + kTreeSuper - 1) / kTreeSuper;
   return r;
+}
+
+// The length and number of nodes of row b, clamped; *bad gets the error bit.
+__device__ __forceinline__ int2 tree_size(const TreeLaunch& p, int b, int* bad) {
+  const int length = __ldg(p.lengths + b), nodes = p.counts ? __ldg(p.counts + b) : p.T;
+  const int2 s = make_int2(clamp_len(length, p.capacity), clamp_len(nodes, p.T));
+  if (s.x != length || s.y != nodes || s.x + s.y > p.capacity) *bad |= DA_DEVERR_LENGTH;
+  return s;
 }
 
 __device__ __forceinline__ int tree_tile(const TreeRow& r, int i) {
