@@ -136,6 +136,9 @@ constexpr int kRows = 128;         // rows of an MMA: TMEM lanes
 constexpr int kRegion = kT * 128;  // 64 rows of 128 bytes, swizzled
 constexpr int kMaxStages = 12;
 constexpr float kRescaleLog2 = 8.f;
+// f16 weights: the largest is 2^7 or more (and at most 2^15), so that what f16 cannot hold
+// below 2^-25 is less than 2^-32 of it.
+constexpr float kHeadLog2 = 7.f;
 
 // Shared memory.  KT: the cache's type; quantized caches pass raw stages of cache bytes
 // and are widened to f16 into the operand stages.
@@ -674,6 +677,7 @@ __device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem, 
           mt = fmaxf(mt, s[k]);
         }
       }
+      if constexpr (L::Q8) mt -= kHeadLog2;
       const bool move = mt > m_used + kRescaleLog2 || (m_used == -INFINITY && mt > -INFINITY);
       const float m_new = move ? mt : m_used;
       const float alpha = (move && m_used > -INFINITY) ? ex2(m_used - m_new) : 1.f;
@@ -979,9 +983,15 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
     }
   };
   load(0);
-  const float lse = merge_weights(p.lse_part + slot, per, r.splits, coef[warp], lane);
+  float lse = merge_weights(p.lse_part + slot, per, r.splits, coef[warp], lane);
+  bool nan = false;  // (the merge would count such a part as empty)
+  for (int i = lane; i < r.splits; i += 32) {
+    const float part_lse = __ldcg(p.lse_part + slot + i * per);
+    nan |= part_lse != part_lse;
+  }
+  if (__any_sync(0xffffffffu, nan)) lse = NAN;
 #pragma unroll
-  for (int e = 0; e < N; ++e) acc[e] = 0.f;
+  for (int e = 0; e < N; ++e) acc[e] = lse != lse ? NAN : 0.f;
   for (int s0 = 0; s0 < r.splits; s0 += kBatch) {
     if (s0) load(s0);
 #pragma unroll
