@@ -134,7 +134,6 @@ __device__ void attend_plainly(const TreeLaunch& p, const TreeRow& r, int b, int
 constexpr int kT = kTreeTile;
 constexpr int kRows = 128;         // rows of an MMA: TMEM lanes
 constexpr int kRegion = kT * 128;  // 64 rows of 128 bytes, swizzled
-constexpr int kMaxStages = 12;
 constexpr float kRescaleLog2 = 8.f;
 // f16 weights: the largest is 2^7 or more (and at most 2^15), so that what f16 cannot hold
 // below 2^-25 is less than 2^-32 of it.
@@ -147,34 +146,40 @@ struct Lay {
   static constexpr bool Q8 = KT != DA_KV_BF16;
   static constexpr int kTile = (D / 64) * kRegion;  // K (or V) of a tile, 16-bit elements
   static constexpr int kStage = 2 * kTile;
-  static constexpr int kStages = (Q8 ? 4 : 6) * (128 / D);
+  static constexpr int kStages = (Q8 ? 3 : 5) * (128 / D);
   static constexpr int kCodeRow = KT == DA_KV_NVFP4 ? D / 2 : D;  // code bytes of a head's row
   static constexpr int kScaleRow = KT == DA_KV_NVFP4 ? D / 16 : 0;
   static constexpr int kRaw = 2 * kT * (kCodeRow + kScaleRow);
   static constexpr int kRawStage = (kRaw + 1023) / 1024 * 1024;
   static constexpr int kRawStages = !Q8 ? 0 : D == 64 ? 8 : KT == DA_KV_NVFP4 ? 6 : 5;
-  static constexpr int kRawOffset = kStages * kStage;
+  // The second stream's Q, if it has its own (64 dims of 128 rows a region, swizzled);
+  // between units also 4 KB for each softmax warp, through which Q and the output pass
+  static constexpr int kQ1 = kStages * kStage;
+  static constexpr int kQRegion = kRows * 128;
+  static constexpr int kRawOffset = kQ1 + 2 * kQRegion;
   static constexpr int kBarOffset = kRawOffset + kRawStages * kRawStage;
   // barriers
   static constexpr int kFull = 0, kEmpty = kFull + kStages, kRawFull = kEmpty + kStages,
                        kRawEmpty = kRawFull + kRawStages, kQFull = kRawEmpty + kRawStages, kSFull = kQFull + 2,
-                       kPFull = kSFull + 2, kPVDone = kPFull + 2, kDrain = kPVDone + 2, kStall = kDrain + 1,
+                       kSFree = kSFull + 2, kPFull = kSFree + 2, kPVDone = kPFull + 2, kDrain = kPVDone + 2, kStall = kDrain + 1,
                        kBars = kStall + 1;
   static constexpr int kSlots = kBarOffset + kBars * 8;      // TMEM address, abort flag
   static constexpr int kStats = (kSlots + 8 + 15) / 16 * 16;  // m and l of 2 x 128 rows
-  static constexpr int kSizes = kStats + 2 * 2 * kRows * 4;   // length and nodes of each row
+  static constexpr int kScales = kStats + 2 * 2 * kRows * 4;  // softmax scales of 128 rows
+  static constexpr int kSizes = kScales + kRows * 4;          // length and nodes of each row
   static constexpr int kFirst = kSizes + kTreeRows * 8;       // first unit of each row
   static constexpr int kBytes = kFirst + (kTreeRows + 1) * 4;
-  // warps 0-3 and 4-7 softmax and output, 8 and 9 MMAs, 10 copies, (11 none), 12-15 conversion
-  static constexpr int kThreads = Q8 ? 512 : 352;
+  // warps 0-3 and 4-7 softmax and output, 8 and 9 MMAs, 10 and 11 copies, 12-15 conversion
+  static constexpr int kThreads = Q8 ? 512 : 384;
   static_assert(kBytes <= 232448, "fits a block's shared memory");
   static_assert(kBytes > 232448 / 2, "one block an SM (TMEM is taken whole)");
 };
 
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSCol = 0;    // S of the two streams, 64 columns each; P over its first 32
+constexpr uint32_t kSCol = 0;    // S of the two streams, 64 columns each
 constexpr uint32_t kOCol = 128;  // their O
-constexpr uint32_t kQCol = 384;  // their Q, two elements a column
+constexpr uint32_t kQCol = 384;  // Q of the first or of both, two elements a column
+constexpr uint32_t kPCol = 448;  // their P, 32 columns each
 
 struct Maps {
   CUtensorMap k3, v3;  // [entries][H_kv][row], boxes of 16 to 64 entries
@@ -193,6 +198,18 @@ struct Ctx {
 
 __device__ __forceinline__ void report(int32_t* err, int bits) {
   if (err) atomicOr(err, bits);
+}
+
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // Bounded wait that also gives up when another role has.
@@ -298,7 +315,8 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* tm,
       : "memory");
 }
 
-// One warp.  box > 0: the list's entries lie `box` at a time (64, 32 or 16) in
+// Two warps; warp w fills the stages of its parity (a copy costs its thread some 200
+// cycles to issue).  box > 0: the list's entries lie `box` at a time (64, 32 or 16) in
 // consecutive cache rows, one copy each for K and V (and 64 dims); the lookups of eight
 // tiles are made at once, lane l those of group l % 4 of tile l / 4, a batch ahead of
 // the copies that use them.  box = 0: gathers of four rows, lane l < 16 those of entries
@@ -313,88 +331,83 @@ __device__ void producer(const TreeLaunch& p, const Ctx& c, const Maps& m, int b
   constexpr int kHalves = L::Q8 ? 1 : D / 64;      // copies of a row
   constexpr uint32_t kTx = L::Q8 ? 2 * kT * L::kCodeRow : L::kStage;
   const int lane = threadIdx.x & 31;
+  const uint32_t pw = (threadIdx.x >> 5) & 1;
   bool bad = false;
-  // whether some node sees one of the entries j .. j + n - 1 (n within a tile's group)
-  auto seen = [&](const TreeRow& r, int j, int n) {
-    return j < r.end && !(j >= r.hole_from && j + n <= r.hole_to);
-  };
-  // table word for entry j of a row (0 where there is none to look up)
-  auto word_of = [&](const Unit& x, int j, int n) -> int {
-    if (p.layout == DA_KV_CONTIGUOUS || !seen(x.r, j, n)) return 0;
-    return __ldg(p.table + (long long)x.b * p.width + (p.layout == DA_KV_PAGED ? j / p.page_size : j));
-  };
-  auto row_of = [&](const Unit& x, int j, int n, int word) -> int {
-    if (!seen(x.r, j, n)) return 0;
+  // cache row of entry j, the first of n of a tile's (0 where no node sees one of them)
+  auto look_up = [&](const Unit& x, int j, int n) -> int {
+    if (j >= x.r.end || (j >= x.r.hole_from && j + n <= x.r.hole_to)) return 0;
     if (p.layout == DA_KV_CONTIGUOUS) return x.b * p.width + j;
+    const int at = p.layout == DA_KV_PAGED ? j / p.page_size : j;
+    const int word = __ldg(p.table + (long long)x.b * p.width + at);
     if (word < 0 || word >= p.num_blocks) {
       bad = true;
       return 0;
     }
-    return p.layout == DA_KV_PAGED ? word * p.page_size + j % p.page_size : word;
+    return p.layout == DA_KV_PAGED ? word * p.page_size + (j - at * p.page_size) : word;
   };
   const int groups = box ? kT / box : 0;
-  // this lane's word for tiles 8 bt .. 8 bt + 7 of a unit
+  // this lane's row for tiles 8 bt .. 8 bt + 7 of a unit
   auto batch = [&](const Unit& x, int bt) -> int {
     const int i = x.begin + 8 * bt + (lane >> 2);
     if (i >= x.end || (lane & 3) >= groups) return 0;
-    return word_of(x, tree_tile(x.r, i) * kT + (lane & 3) * box, box);
+    return look_up(x, tree_tile(x.r, i) * kT + (lane & 3) * box, box);
   };
   uint32_t g = 0;
   bool alive = true;
   Unit x = unit_of(p, c, blockIdx.x);
-  int first_words = box ? batch(x, 0) : 0;
+  int first_rows = box ? batch(x, 0) : 0;
   for (int u = blockIdx.x; u < c.units && alive; u += gridDim.x) {
     const bool more = u + (int)gridDim.x < c.units;
     const Unit next = more ? unit_of(p, c, u + gridDim.x) : x;
     const int n = x.tiles(), last_batch = (n - 1) / 8;
-    int words = first_words, ahead = 0;
+    int rows = first_rows, ahead = 0;
     if (box && n > 8) ahead = batch(x, 1);
-    if (box && more && n <= 8) first_words = batch(next, 0);
-    int wg[4] = {0, 0, 0, 0}, wg_next[4] = {0, 0, 0, 0};
+    if (box && more && n <= 8) first_rows = batch(next, 0);
+    int rg[4] = {0, 0, 0, 0}, rg_next[4] = {0, 0, 0, 0};
     if (!box && lane < 16 && n > 0)
-      for (int e = 0; e < 4; ++e) wg[e] = word_of(x, tree_tile(x.r, x.begin) * kT + lane * 4 + e, 1);
+      for (int e = 0; e < 4; ++e) rg[e] = look_up(x, tree_tile(x.r, x.begin) * kT + lane * 4 + e, 1);
     for (int i = 0; i < n; ++i, ++g) {
-      const int j0 = tree_tile(x.r, x.begin + i) * kT, st = g % kNS;
+      const uint32_t st = g % kNS, full = c.bars + 8 * (kFullB + st);
       if (box) {
         if (i > 0 && (i & 7) == 0) {
-          words = ahead;
+          rows = ahead;
           if ((i >> 3) < last_batch) ahead = batch(x, (i >> 3) + 1);
-          if ((i >> 3) == last_batch && more) first_words = batch(next, 0);
+          if ((i >> 3) == last_batch && more) first_rows = batch(next, 0);
         }
-      } else if (lane < 16 && i + 1 < n) {
-        const int j1 = tree_tile(x.r, x.begin + i + 1) * kT;
-        for (int e = 0; e < 4; ++e) wg_next[e] = word_of(x, j1 + lane * 4 + e, 1);
+        if ((st & 1) != pw) continue;  // the other warp's
+      } else {
+        if (lane < 16 && i + 1 < n) {
+          const int j1 = tree_tile(x.r, x.begin + i + 1) * kT;
+          for (int e = 0; e < 4; ++e) rg_next[e] = look_up(x, j1 + lane * 4 + e, 1);
+        }
+        if ((st & 1) != pw) {
+          for (int e = 0; e < 4; ++e) rg[e] = rg_next[e];
+          continue;
+        }
       }
       if (!wait_warp(c, kEmptyB + st, ((g / kNS) & 1) ^ 1)) {
         alive = false;
         break;
       }
-      const uint32_t full = c.bars + 8 * (kFullB + st);
       if (lane == 0) mbar_arrive_expect_tx(full, kTx);
       __syncwarp();
       const uint32_t kdst = c.sbase + (L::Q8 ? L::kRawOffset + st * L::kRawStage : st * L::kStage);
       const uint32_t vdst = kdst + (L::Q8 ? kT * L::kCodeRow : L::kTile);
       constexpr int kRowBytes = L::Q8 ? L::kCodeRow : 128;  // of a row in the stage (of a half)
-      int row[4] = {0, 0, 0, 0};  // cache rows of this lane's group, or of its four entries
       if (box) {
         const int grp = lane & 3;
         if ((lane >> 2) == (i & 7) && grp < groups) {
-          row[0] = row_of(x, j0 + grp * box, box, words);
 #pragma unroll
           for (int half = 0; half < kHalves; ++half) {
             const uint32_t off = half * kRegion + grp * box * kRowBytes;
-            tma_box3(kdst + off, &m.k3, 64 * half, x.h, row[0], full);
-            tma_box3(vdst + off, &m.v3, 64 * half, x.h, row[0], full);
+            tma_box3(kdst + off, &m.k3, 64 * half, x.h, rows, full);
+            tma_box3(vdst + off, &m.v3, 64 * half, x.h, rows, full);
           }
         }
       } else if (lane < 16) {
         int at[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          row[e] = row_of(x, j0 + lane * 4 + e, 1, wg[e]);
-          at[e] = row[e] * p.H_kv + x.h;
-          wg[e] = wg_next[e];
-        }
+        for (int e = 0; e < 4; ++e) at[e] = rg[e] * p.H_kv + x.h;
 #pragma unroll
         for (int half = 0; half < kHalves; ++half) {
           const uint32_t off = half * kRegion + lane * 4 * kRowBytes;
@@ -411,12 +424,12 @@ __device__ void producer(const TreeLaunch& p, const Ctx& c, const Maps& m, int b
           const int k = 2 * lane + e;
           long long at;
           if (box) {
-            const int base = __shfl_sync(0xffffffffu, row[0], (i & 7) * 4 + k / box);
+            const int base = __shfl_sync(0xffffffffu, rows, (i & 7) * 4 + k / box);
             at = min((long long)base + k % box, p.kv_rows - 1);
           } else {
-            const int a = __shfl_sync(0xffffffffu, row[e], k >> 2);
-            const int b = __shfl_sync(0xffffffffu, row[2 + e], k >> 2);
-            at = min((long long)((k & 2) ? b : a), p.kv_rows - 1);
+            const int a = __shfl_sync(0xffffffffu, rg[e], k >> 2);
+            const int b = __shfl_sync(0xffffffffu, rg[2 + e], k >> 2);
+            at = (k & 2) ? b : a;
           }
           if (p.kv_rows > 0) {
             const long long off = blocks + (at * p.H_kv + x.h) * L::kScaleRow;
@@ -432,16 +445,20 @@ __device__ void producer(const TreeLaunch& p, const Ctx& c, const Maps& m, int b
         }
         cp_async_mbar_arrive(full);
       }
+      if (!box)
+        for (int e = 0; e < 4; ++e) rg[e] = rg_next[e];
     }
     x = next;
   }
   if (__any_sync(0xffffffffu, bad) && lane == 0) report(p.err, DA_DEVERR_INDEX);
   if constexpr (KT == DA_KV_NVFP4) cp_async_wait_all();
-  // leave no copy in flight (after a time-out; else every stage was consumed)
+  // Leave no copy in flight (after a time-out; else every stage was consumed): each of this
+  // warp's stages has its last tile before g, which is the first that it did not copy.
   if (lane == 0) {
-    for (int st = 0; st < kNS; ++st) {
-      const int last = (int)g - 1 - (((int)g - 1 - st) % kNS + kNS) % kNS;
-      if (last >= 0 && !mbar_wait(c.bars + 8 * (kFullB + st), (last / kNS) & 1)) report(p.err, DA_DEVERR_TIMEOUT);
+    for (uint32_t st = pw; st < kNS; st += 2) {
+      if (g <= st) continue;
+      const uint32_t last = g - 1 - (g - 1 - st) % kNS;
+      if (!mbar_wait(c.bars + 8 * (kFullB + st), (last / kNS) & 1)) report(p.err, DA_DEVERR_TIMEOUT);
     }
   }
 }
@@ -509,9 +526,10 @@ __device__ void converter(const TreeLaunch& p, const Ctx& c) {
 }
 
 // ------------------------------------------------------------------ MMAs
-// One thread for each stream: S = Q K^T of its next tile (Q in tensor memory), then, once
-// the softmax has put P over S, O += P V.  The next S overwrites P, so it waits for the
-// P V before; the other stream's MMAs fill that time.
+// One thread for each stream.  S = Q K^T of its next tile as soon as the softmax has read
+// the one before, O += P V as soon as it has written P: whichever can go first, so that
+// the softmax finds the next scores waiting.  Q lies in tensor memory, shared by both
+// streams, or, for the second of a wide unit, in shared memory.
 template <int KT, int D>
 __device__ void issue(const TreeLaunch& p, const Ctx& c, uint32_t tmem, int stream) {
   using L = Lay<KT, D>;
@@ -520,42 +538,83 @@ __device__ void issue(const TreeLaunch& p, const Ctx& c, uint32_t tmem, int stre
   const uint64_t k0 = umma::smem_desc(c.sbase, 16, 1024, umma::kSwizzle128B);
   // V with its dims contiguous: 64-dim regions kRegion apart, 8-entry groups 1024 bytes
   const uint64_t v0 = umma::smem_desc(c.sbase + L::kTile, kRegion, 1024, umma::kSwizzle128B);
+  const uint64_t q1 = umma::smem_desc(c.sbase + L::kQ1, 16, 1024, umma::kSwizzle128B);
   const uint32_t s_col = tmem + kSCol + stream * kT, o_col = tmem + kOCol + stream * D;
-  const uint32_t q_col = tmem + kQCol + stream * 64;
+  const uint32_t p_col = tmem + kPCol + stream * 32;
   if (p.test_stall && stream == 0 && !wait_bar(c, L::kStall, 0, kTestStallNs)) return;
-  uint32_t g = 0, mine = 0, nq = 0;  // tiles of the CTA, of the stream; units of the stream
+  uint32_t g = 0, mine = 0;       // tiles of the CTA before this unit; S issued by the stream
+  uint32_t nq = 0;                // units that the stream has had work in
+  auto ready = [&](int i, uint32_t parity) { return mbar_test_wait(c.bars + 8 * i, parity); };
   for (int u = blockIdx.x; u < c.units; u += gridDim.x) {
     const Unit x = unit_of(p, c, u);
-    if (x.works(stream)) {
+    const int n = x.tiles(), step = x.wide ? 1 : 2, first = x.wide ? 0 : stream;
+    const bool own_q = x.wide && stream == 1;
+    if (x.works(stream)) {  // (Q is there: all units before are done with)
       if (!wait_bar(c, L::kQFull + stream, nq & 1)) return;
       ++nq;
     }
-    bool start = true;
-    for (int i = 0; i < x.tiles(); ++i, ++g) {
-      if (!x.takes(stream, i)) continue;
-      const int st = g % L::kStages;
-      if (!wait_bar(c, L::kFull + st, (g / L::kStages) & 1)) return;
-      if (mine && !wait_bar(c, L::kPVDone + stream, (mine - 1) & 1)) return;
-      fence_proxy_async();
-      umma::fence_after_sync();
-      const uint64_t stage = (uint64_t)((st * L::kStage) >> 4);
+    const uint32_t base = mine;  // the stream's number of the unit's first tile
+    const int total = n > first ? (n - first + step - 1) / step : 0;
+    int s_done = 0, o_done = 0;  // of the stream's tiles of the unit
+    uint32_t idle = 0;
+    unsigned long long t0 = 0;
+    while (o_done < total) {
+      bool went = false;
+      if (s_done < total && s_done <= o_done + 1) {
+        const uint32_t t = g + first + s_done * step, st = t % L::kStages;
+        // the tile is there, and the scores before it have been read.  (The stage's tile
+        // before may have been the other stream's: only once it is used up does the parity
+        // of "full" mean this tile.)
+        if ((t < L::kStages || ready(L::kEmpty + st, ((t / L::kStages) & 1) ^ 1)) &&
+            ready(L::kFull + st, (t / L::kStages) & 1) &&
+            (mine == 0 || ready(L::kSFree + stream, (mine - 1) & 1))) {
+          umma::fence_after_sync();
+          const uint64_t kd = k0 + (uint64_t)((st * L::kStage) >> 4);
+          if (own_q) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        umma::mma_bf16_ta(s_col, q_col + k * 8, k0 + stage + (uint64_t)(((k / 4) * kRegion + (k % 4) * 32) >> 4),
-                          kIdescS, k ? 1u : 0u);
-      umma::commit(c.bars + 8 * (L::kSFull + stream));
-      if (!wait_bar(c, L::kPFull + stream, mine & 1)) return;
-      umma::fence_after_sync();
+            for (int k = 0; k < D / 16; ++k)
+              umma::mma_bf16(s_col, q1 + (uint64_t)(((k / 4) * L::kQRegion + (k % 4) * 32) >> 4),
+                             kd + (uint64_t)(((k / 4) * kRegion + (k % 4) * 32) >> 4), kIdescS, k ? 1u : 0u);
+          } else {
 #pragma unroll
-      for (int k = 0; k < kT / 16; ++k)
-        umma::mma_bf16_ta(o_col, s_col + k * 8, v0 + stage + (uint64_t)((k * 2048) >> 4), kIdescO,
-                          (start && k == 0) ? 0u : 1u);
-      umma::commit(c.bars + 8 * (L::kPVDone + stream));
-      umma::commit(c.bars + 8 * (L::kEmpty + st));  // (two arrivals free a stage)
-      if (!x.wide) umma::commit(c.bars + 8 * (L::kEmpty + st));
-      start = false;
-      ++mine;
+            for (int k = 0; k < D / 16; ++k)
+              umma::mma_bf16_ta(s_col, tmem + kQCol + k * 8,
+                                kd + (uint64_t)(((k / 4) * kRegion + (k % 4) * 32) >> 4), kIdescS, k ? 1u : 0u);
+          }
+          umma::commit(c.bars + 8 * (L::kSFull + stream));
+          ++s_done;
+          ++mine;
+          went = true;
+        }
+      }
+      if (o_done < s_done && ready(L::kPFull + stream, (base + o_done) & 1)) {
+        umma::fence_after_sync();
+        const uint32_t t = g + first + o_done * step, st = t % L::kStages;
+        const uint64_t vd = v0 + (uint64_t)((st * L::kStage) >> 4);
+#pragma unroll
+        for (int k = 0; k < kT / 16; ++k)
+          umma::mma_bf16_ta(o_col, p_col + k * 8, vd + (uint64_t)((k * 2048) >> 4), kIdescO,
+                            (o_done == 0 && k == 0) ? 0u : 1u);
+        umma::commit(c.bars + 8 * (L::kPVDone + stream));
+        umma::commit(c.bars + 8 * (L::kEmpty + st));  // (two arrivals free a stage)
+        if (!x.wide) umma::commit(c.bars + 8 * (L::kEmpty + st));
+        ++o_done;
+        went = true;
+      }
+      if (went) {
+        idle = 0;
+      } else if ((++idle & 63u) == 0) {
+        if (*c.abort_flag) return;
+        const unsigned long long now = globaltimer_ns();
+        if (idle == 64) t0 = now;
+        if (now - t0 > kWaitLimitNs) {
+          report(c.err, DA_DEVERR_TIMEOUT);
+          *c.abort_flag = 1;
+          return;
+        }
+      }
     }
+    g += n;
   }
 }
 
@@ -572,63 +631,151 @@ __device__ __forceinline__ unsigned long long windowed(const TreeLaunch& p, cons
   return keep;
 }
 
+// The row of a unit that thread `tid` of a stream has.
+struct Lane {
+  int t, head;   // node, query head
+  uint32_t row;  // of q, out and lse
+  bool live;
+};
+
+__device__ __forceinline__ Lane lane_of(const TreeLaunch& p, const Unit& x, int stream, int tid) {
+  Lane y;
+  const int idx = x.row0 + (x.wide ? stream * kRows : 0) + tid;
+  y.live = idx < x.row0 + x.rows;
+  y.t = y.live ? idx / p.G : 0;
+  y.head = x.h * p.G + (y.live ? idx - y.t * p.G : 0);
+  y.row = ((uint32_t)x.b * p.T + y.t) * p.H_q + y.head;
+  return y;
+}
+
+// Bytes of 16-byte chunk `ch` of row `row` in 32 rows of 128 bytes whose chunks are swapped so
+// that neither a warp's rows nor its columns meet in a bank.
+__device__ __forceinline__ uint32_t chunk_at(int row, int ch) { return row * 128 + ((ch ^ (row & 7)) << 4); }
+
+// A unit's Q to where its MMAs read it: bf16 as it is, or f16 scaled by a power of two;
+// the first stream's into tensor memory, by way of `stage`, 4 KB of this warp's, the
+// second's (wide units) into its place in shared memory.  Whole rows are loaded by eight
+// lanes each (a thread that loads its own row keeps the L1 busy for 4000 cycles a unit).
+template <int KT, int D>
+__device__ __forceinline__ float put_q(const TreeLaunch& p, const Ctx& c, const Lane& y, int stream, uint32_t q_col,
+                                       uint8_t* stage) {
+  using L = Lay<KT, D>;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+  const uint32_t live = __ballot_sync(0xffffffffu, y.live);
+  constexpr int kHalves = D / 64;
+  uint4 w[kHalves][8];  // this lane's pieces of rows 4 i + lane / 8
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int rr = 4 * i + (lane >> 3);
+    const uint32_t row = __shfl_sync(0xffffffffu, y.row, rr);
+    const uint4* from = reinterpret_cast<const uint4*>(p.q + (size_t)row * D) + (lane & 7);
+#pragma unroll
+    for (int half = 0; half < kHalves; ++half)
+      w[half][i] = (live >> rr & 1) ? __ldg(from + half * 8) : make_uint4(0, 0, 0, 0);
+  }
+  uint4 own[kHalves][8];  // this lane's row
+#pragma unroll
+  for (int half = 0; half < kHalves; ++half) {
+    uint8_t* at = stream ? c.smem + L::kQ1 + half * L::kQRegion + warp * 4096 : stage;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(at + chunk_at(4 * i + (lane >> 3), lane & 7)) = w[half][i];
+    if (stream && !L::Q8) continue;  // it is where it belongs
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) own[half][i] = *reinterpret_cast<const uint4*>(at + chunk_at(lane, i));
+  }
+  float sc = 1.f, row_scale = p.scale_log2;
+  if constexpr (L::Q8) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int half = 0; half < kHalves; ++half)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) most = bf16x8_absmax_bits(most, own[half][i]);
+    const int e = q_prescale_exp(bf16_absmax_value(most));
+    sc = exp2_int(e);
+    row_scale *= exp2_int(-e);
+  }
+  if (!stream || L::Q8) {
+#pragma unroll
+    for (int half = 0; half < kHalves; ++half) {
+      uint32_t q32[32];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t v[4] = {own[half][i].x, own[half][i].y, own[half][i].z, own[half][i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (L::Q8) {
+            const __half2 hh = __floats2half2_rn(bf16_lo(v[e]) * sc, bf16_hi(v[e]) * sc);
+            q32[4 * i + e] = *reinterpret_cast<const uint32_t*>(&hh);
+          } else {
+            q32[4 * i + e] = v[e];
+          }
+        }
+      }
+      if (!stream) {
+        umma::st_32x32b_x32_u(q_col + half * 32, q32);
+      } else {
+        uint8_t* at = c.smem + L::kQ1 + half * L::kQRegion + warp * 4096;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(at + chunk_at(lane, i)) =
+              make_uint4(q32[4 * i], q32[4 * i + 1], q32[4 * i + 2], q32[4 * i + 3]);
+      }
+    }
+  }
+  if (!stream) {
+    umma::wait_st();
+    umma::fence_before_sync();
+  } else {
+    fence_proxy_async();
+  }
+  arrive_warp(c, L::kQFull + stream);
+  return row_scale;
+}
+
 // Four warps a stream; a thread has one row, a TMEM lane.  Its scores' running reference
-// value moves only when one exceeds it by more than 2^8 (then its O is rescaled).
+// value moves only when one exceeds it by more than 2^8 (then its O is rescaled).  The
+// next unit's Q goes out before this one's output is written.
 template <int KT, int D>
 __device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem, int stream) {
   using L = Lay<KT, D>;
   const int lane = threadIdx.x & 31, tid = threadIdx.x & 127, warp = tid >> 5;
   const uint32_t base = tmem + ((uint32_t)(warp * 32) << 16);
   const uint32_t s_col = base + kSCol + stream * kT, o_col = base + kOCol + stream * D;
-  const uint32_t q_col = base + kQCol + stream * 64;
+  const uint32_t p_col = base + kPCol + stream * 32;
   float* stats = reinterpret_cast<float*>(c.smem + L::kStats);  // [stream][m, l][128]
   uint32_t g = 0, mine = 0;
-  for (int u = blockIdx.x; u < c.units; u += gridDim.x) {
-    const Unit x = unit_of(p, c, u);
-    const TreeRow& r = x.r;
-    const int idx = x.row0 + (x.wide ? stream * kRows : 0) + tid;  // (node, head) row
-    const bool live = idx < x.row0 + x.rows;
-    const int t = live ? idx / p.G : 0, head = x.h * p.G + (live ? idx % p.G : 0);
-    const long long q_row = ((long long)x.b * p.T + t) * p.H_q + head;
-    float row_scale = p.scale_log2;
-    bool ok = true;
-    if (x.works(stream)) {
-      // ---- Q into tensor memory: bf16 as it is, or f16 scaled by a power of two
-      uint4 w[D / 8];
-      const uint4* from = reinterpret_cast<const uint4*>(p.q + q_row * D);
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) w[i] = live ? __ldg(from + i) : make_uint4(0, 0, 0, 0);
-      float sc = 1.f;
-      if constexpr (L::Q8) {
-        uint32_t most = 0;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) most = bf16x8_absmax_bits(most, w[i]);
-        const int e = q_prescale_exp(bf16_absmax_value(most));
-        sc = exp2_int(e);
-        row_scale *= exp2_int(-e);
-      }
-#pragma unroll
-      for (int half = 0; half < D / 64; ++half) {
-        uint32_t q32[32];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t v[4] = {w[half * 8 + i].x, w[half * 8 + i].y, w[half * 8 + i].z, w[half * 8 + i].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if constexpr (L::Q8) {
-              const __half2 hh = __floats2half2_rn(bf16_lo(v[e]) * sc, bf16_hi(v[e]) * sc);
-              q32[4 * i + e] = *reinterpret_cast<const uint32_t*>(&hh);
-            } else {
-              q32[4 * i + e] = v[e];
-            }
-          }
-        }
-        umma::st_32x32b_x32_u(q_col + half * 32, q32);
-      }
-      umma::wait_st();
-      umma::fence_before_sync();
-      arrive_warp(c, L::kQFull + stream);
+  float* scales = reinterpret_cast<float*>(c.smem + L::kScales);
+  // (the first stream's warps share the second half of the space, which holds the
+  // second's rows of the upper dims only once theirs have passed)
+  uint8_t* stage = c.smem + L::kQ1 + (stream ? 0 : L::kQRegion) + warp * 4096;
+  Unit x = unit_of(p, c, blockIdx.x);
+  Lane y = lane_of(p, x, stream, tid);
+  float row_scale = p.scale_log2;
+  // Q of unit x: the first stream's part before, the second's after a barrier of both
+  auto first_q = [&] {
+    if (stream == 0 && x.tiles() > 0) {
+      row_scale = put_q<KT, D>(p, c, y, 0, base + kQCol, stage);
+      if (!x.wide && x.works(1)) arrive_warp(c, L::kQFull + 1);
+      if (L::Q8) scales[tid] = row_scale;
     }
+  };
+  auto second_q = [&] {
+    if (stream == 0 || x.tiles() == 0) return;
+    if (x.wide)
+      row_scale = put_q<KT, D>(p, c, y, 1, 0, stage);
+    else if (L::Q8)
+      row_scale = scales[tid];
+  };
+  first_q();
+  named_bar_sync(1, 256);
+  second_q();
+  for (int u = blockIdx.x; u < c.units; u += gridDim.x) {
+    const TreeRow r = x.r;
+    const bool live = y.live;
+    const int t = y.t, head = y.head;
+    bool ok = true;
     // ---- what the row sees, if the unit's last tile reaches the nodes or there is a window
     const bool edge = p.window || (x.tiles() > 0 && (tree_tile(r, x.end - 1) + 1) * kT > r.length);
     unsigned long long anc = 0;
@@ -650,45 +797,46 @@ __device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem, 
       umma::ld_32x32b_x32(s_col, *reinterpret_cast<float(*)[32]>(s));
       umma::ld_32x32b_x32(s_col + 32, *reinterpret_cast<float(*)[32]>(s + 32));
       umma::wait_ld();
+      umma::fence_before_sync();
+      arrive_warp(c, L::kSFree + stream);
       const int j0 = tree_tile(r, x.begin + i) * kT;
       const bool all = j0 + kT <= r.length && (!p.window || j0 + kT <= p.sinks || j0 >= r.length + r.nodes - p.window);
-      float mt = -INFINITY;
-      if (all) {
-#pragma unroll
-        for (int k = 0; k < kT; ++k) mt = fmaxf(mt, s[k]);
-        // (a negative scale turns the order around)
-        if (row_scale < 0.f) {
-          mt = INFINITY;
-#pragma unroll
-          for (int k = 0; k < kT; ++k) mt = fminf(mt, s[k]);
-        }
-        mt *= row_scale;
+      const float factor = row_scale > 0.f ? row_scale : 1.f;
+      if (row_scale <= 0.f) {  // (the largest score is not the largest product then)
 #pragma unroll
         for (int k = 0; k < kT; ++k) s[k] *= row_scale;
-      } else {
+      }
+      if (!all) {
         unsigned long long vis = low_bits(r.length - j0);
         if (p.window) vis &= ~low_bits(r.length + depth - p.window + 1 - j0) | low_bits(p.sinks - j0);
         const int shift = r.length - j0;  // of node 0 in the tile
         if (shift > -64 && shift < 64) vis |= shift >= 0 ? anc << shift : anc >> -shift;
         if (!live) vis = 0;
 #pragma unroll
-        for (int k = 0; k < kT; ++k) {
-          s[k] = (vis >> k & 1) ? s[k] * row_scale : -INFINITY;
-          mt = fmaxf(mt, s[k]);
-        }
+        for (int k = 0; k < kT; ++k)
+          if (!(vis >> k & 1)) s[k] = -INFINITY;
       }
+      float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int k = 4; k < kT; ++k) m4[k & 3] = fmaxf(m4[k & 3], s[k]);
+      float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * factor;
       if constexpr (L::Q8) mt -= kHeadLog2;
       const bool move = mt > m_used + kRescaleLog2 || (m_used == -INFINITY && mt > -INFINITY);
       const float m_new = move ? mt : m_used;
       const float alpha = (move && m_used > -INFINITY) ? ex2(m_used - m_new) : 1.f;
       const float ref = m_new == -INFINITY ? 0.f : m_new;
-      float sum = 0.f;
+      // 2^(s scale - ref), in pairs; four sums
+      const uint64_t factor2 = pack2(factor, factor), ref2 = pack2(-ref, -ref);
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
       uint32_t pk[kT / 2];
 #pragma unroll
       for (int k = 0; k < kT; k += 2) {
-        const float p0 = ex2(s[k] - ref), p1 = ex2(s[k + 1] - ref);
-        sum += p0;
-        sum += p1;
+        float p0, p1;
+        unpack2(ffma2(pack2(s[k], s[k + 1]), factor2, ref2), p0, p1);
+        p0 = ex2(p0);
+        p1 = ex2(p1);
+        sum[k & 2] += p0;
+        sum[(k & 2) + 1] += p1;
         if constexpr (L::Q8) {
           const __half2 h = __floats2half2_rn(p0, p1);
           pk[k / 2] = *reinterpret_cast<const uint32_t*>(&h);
@@ -697,9 +845,14 @@ __device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem, 
           pk[k / 2] = *reinterpret_cast<const uint32_t*>(&h);
         }
       }
-      l = fmaf(l, alpha, sum);
-      umma::st_32x32b_x32_u(s_col, pk);
-      // (S was issued after the stream's P V before it, so O stands still)
+      l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+      // the stream's P V before has read its P, and O stands still
+      if (!start && !wait_warp(c, L::kPVDone + stream, (mine - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      umma::fence_after_sync();
+      umma::st_32x32b_x32_u(p_col, pk);
       if (!start && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
         for (int ch = 0; ch < D / 32; ++ch) {
@@ -740,37 +893,32 @@ __device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem, 
     // all eight warps leave together, or none
     if (named_bar_or(1, 256, !ok)) return;
     umma::fence_after_sync();
-    float M = m_used, sum = l, f[2] = {1.f, 1.f};
-    bool has[2] = {stream == 0, stream == 1};  // streams whose O this thread adds up
+    float M = m_used, sum = l, f0 = 1.f, f1 = 1.f;  // the streams' weights (narrow units)
     if (!x.wide) {
-      const float* other = stats + (stream ^ 1) * 2 * kRows;
-      const float m2 = other[tid], l2 = other[kRows + tid];
-      M = fmaxf(m_used, m2);
-      const float f_own = m_used == -INFINITY ? 0.f : ex2(m_used - M), f_other = m2 == -INFINITY ? 0.f : ex2(m2 - M);
-      f[stream] = f_own;
-      f[stream ^ 1] = f_other;
-      // in the same order in both streams
-      sum = stream == 0 ? fmaf(f_own, l, f_other * l2) : fmaf(f_other, l2, f_own * l);
-      has[0] = x.tiles() > 0;
-      has[1] = x.tiles() > 1;
+      const float m0 = stats[tid], m1 = stats[2 * kRows + tid];
+      M = fmaxf(m0, m1);
+      f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M);
+      f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+      sum = fmaf(f0, stats[kRows + tid], f1 * stats[3 * kRows + tid]);
     }
     const bool single = r.splits == 1;
-    const long long out_row = ((long long)x.b * p.T + t) * p.H_q + head;
-    const long long slot = (((long long)x.b * p.max_splits + x.split) * p.T + t) * p.H_q + head;
+    // rows of the partials against those of q and out
+    const long long to_slot = (((long long)x.b * p.max_splits + x.split) - x.b) * p.T * p.H_q;
     const float inv = (sum > 0.f ? 1.f / sum : sum != sum ? sum : 0.f) * p.v_scale;
     const int ch0 = x.wide ? 0 : stream * (D / 64), ch1 = x.wide ? D / 32 : ch0 + D / 64;
+    const uint32_t lives = __ballot_sync(0xffffffffu, live);
     bool odd = sum != sum;  // something that is not finite
 #pragma unroll 1
-    for (int ch = ch0; ch < ch1; ++ch) {
+    for (int ch = lives ? ch0 : ch1; ch < ch1; ++ch) {
       float o[32];
-      if (!x.wide && has[1]) {
+      if (!x.wide && x.tiles() > 1) {
         float o1[32];
         umma::ld_32x32b_x32(base + kOCol + ch * 32, o);
         umma::ld_32x32b_x32(base + kOCol + D + ch * 32, o1);
         umma::wait_ld();
 #pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] = fmaf(f[0], o[k], f[1] * o1[k]);
-      } else if (x.wide || has[0]) {
+        for (int k = 0; k < 32; ++k) o[k] = fmaf(f0, o[k], f1 * o1[k]);
+      } else if (x.tiles() > 0) {  // (a lone tile is the first stream's)
         umma::ld_32x32b_x32((x.wide ? o_col : base + kOCol) + ch * 32, o);
         umma::wait_ld();
       }
@@ -779,34 +927,37 @@ __device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem, 
         o[k] = x.tiles() > 0 ? o[k] * inv : 0.f;
         odd |= !(fabsf(o[k]) < INFINITY);
       }
-      if (live && single) {
-        uint4* to = reinterpret_cast<uint4*>(p.out + out_row * D + ch * 32);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(o[8 * k + 2 * e], o[8 * k + 2 * e + 1]);
-            w[e] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          to[k] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      } else if (live) {
-        float4* to = reinterpret_cast<float4*>(p.o_part + slot * D + ch * 32);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) to[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-      }
       __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        *reinterpret_cast<float4*>(stage + chunk_at(lane, k)) =
+            make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {  // eight lanes write a row
+        const int rr = 4 * k + (lane >> 3);
+        const uint32_t row = __shfl_sync(0xffffffffu, y.row, rr);
+        if (!(lives >> rr & 1)) continue;
+        const float4 v = *reinterpret_cast<const float4*>(stage + chunk_at(rr, lane & 7));
+        if (single) {
+          const __nv_bfloat162 h0 = __floats2bfloat162_rn(v.x, v.y), h1 = __floats2bfloat162_rn(v.z, v.w);
+          reinterpret_cast<uint2*>(p.out + (size_t)row * D + ch * 32)[lane & 7] =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+        } else {
+          reinterpret_cast<float4*>(p.o_part + (to_slot + row) * D + ch * 32)[lane & 7] = v;
+        }
+      }
     }
-    float lse = sum > 0.f || sum != sum ? M + lg2(sum) : -INFINITY;
+    const float lse = sum > 0.f || sum != sum ? M + lg2(sum) : -INFINITY;
     if (live && (x.wide || stream == 0)) {
       if (single)
-        p.lse[out_row] = lse * kLn2;
+        p.lse[y.row] = lse * kLn2;
       else
-        p.lse_part[slot] = lse;
+        p.lse_part[to_slot + y.row] = lse;
     }
     // A value that some node sees and another does not may have been infinite or NaN: zero
     // times it has spoiled the other's sum.  Such rows are formed again, entry by entry.
+    __syncwarp();
     for (uint32_t again = __ballot_sync(0xffffffffu, live && odd); again; again &= again - 1) {
       const int src = __ffs((int)again) - 1;
       const int at = __shfl_sync(0xffffffffu, t, src), hq = __shfl_sync(0xffffffffu, head, src);
@@ -814,8 +965,7 @@ __device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem, 
       attend_plainly<KT, D>(p, r, x.b, at, hq, x.begin, x.end, lane, &m2, &l2, o);
       const float inv2 = (l2 > 0.f ? 1.f / l2 : l2 != l2 ? l2 : 0.f) * p.v_scale;
       const float lse2 = l2 > 0.f || l2 != l2 ? m2 + lg2(l2) : -INFINITY;
-      const long long row2 = ((long long)x.b * p.T + at) * p.H_q + hq;
-      const long long slot2 = (((long long)x.b * p.max_splits + x.split) * p.T + at) * p.H_q + hq;
+      const long long row2 = ((long long)x.b * p.T + at) * p.H_q + hq, slot2 = to_slot + row2;
       if (x.wide || (lane >> 4) == stream) {  // this stream's dims
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) {
@@ -834,9 +984,16 @@ __device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem, 
       }
       __syncwarp();
     }
+    // ---- the next unit
+    if (u + (int)gridDim.x < c.units) {
+      x = unit_of(p, c, u + gridDim.x);
+      y = lane_of(p, x, stream, tid);
+      first_q();  // (all MMAs of this unit are done)
+    }
     umma::fence_before_sync();
     named_bar_sync(1, 256);  // O and the statistics have been read
     umma::fence_after_sync();
+    if (u + (int)gridDim.x < c.units) second_q();
   }
 }
 
@@ -863,7 +1020,9 @@ __global__ void __launch_bounds__(Lay<KT, D>::kThreads, 1)
       if (i >= L::kEmpty && i < L::kEmpty + L::kStages) count = 2;
       if (i >= L::kRawFull && i < L::kRawFull + L::kRawStages && KT == DA_KV_NVFP4) count = 33;
       if (i >= L::kRawEmpty && i < L::kRawEmpty + L::kRawStages) count = 4;
-      if ((i >= L::kQFull && i < L::kQFull + 2) || (i >= L::kPFull && i < L::kPFull + 2)) count = 4;
+      if ((i >= L::kQFull && i < L::kQFull + 2) || (i >= L::kSFree && i < L::kSFree + 2) ||
+          (i >= L::kPFull && i < L::kPFull + 2))
+        count = 4;
       if (i == L::kDrain) count = 2;
       mbar_init(c.bars + 8 * i, count);
     }
@@ -923,9 +1082,9 @@ __global__ void __launch_bounds__(Lay<KT, D>::kThreads, 1)
         issue<KT, D>(p, c, tmem, warp - 8);
         umma::commit(c.bars + 8 * L::kDrain);  // arrives when all MMAs of this thread are done
       }
-    } else if (warp == 10) {
+    } else if (warp < 12) {
       producer<KT, D>(p, c, maps, box);
-    } else if (warp >= 12) {
+    } else {
       if constexpr (L::Q8) converter<KT, D>(p, c);
     }
     __syncwarp();

@@ -35,7 +35,7 @@ struct TreeLaunch {
   int row0, rows;  // the rows of this launch
 };
 
-constexpr int kTreeRows = 1024;  // rows of a launch at most
+constexpr int kTreeRows = 512;  // rows of a launch at most
 
 cudaError_t launch_tree(const TreeLaunch& p, int sms, cudaStream_t stream);
 cudaError_t launch_tree_combine(const TreeLaunch& p, cudaStream_t stream);
