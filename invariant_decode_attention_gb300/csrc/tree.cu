@@ -36,7 +36,7 @@ __device__ __forceinline__ unsigned long long ancestors(const TreeLaunch& p, int
 // Cache row of entry j of row b, or -1: its page or slot is out of range.
 __device__ __forceinline__ long long cache_row(const TreeLaunch& p, int b, int j) {
   if (p.layout == DA_KV_CONTIGUOUS) return (long long)b * p.width + j;
-  const int at = p.layout == DA_KV_PAGED ? j / p.page_size : j;
+  const int at = p.layout == DA_KV_PAGED ? quotient(j, p.by_page) : j;
   const int id = __ldg(p.table + (long long)b * p.width + at);
   if (id < 0 || id >= p.num_blocks) return -1;
   return p.layout == DA_KV_PAGED ? (long long)id * p.page_size + (j - at * p.page_size) : id;
@@ -73,7 +73,7 @@ __device__ __forceinline__ void cache_values(const TreeLaunch& p, const void* ca
 // row's list, straight from the formula, entry by entry; lane l has dims [l D/32, + D/32).
 // m: reference value (log2), l: sum, o: the weighted sum.
 template <int KT, int D>
-__device__ void attend_plainly(const TreeLaunch& p, const TreeRow& r, int b, int t, int hq, int begin,
+__device__ __noinline__ void attend_plainly(const TreeLaunch& p, const TreeRow& r, int b, int t, int hq, int begin,
                                int end, int lane, float* m_out, float* l_out, float (&o)[D / 32]) {
   constexpr int N = D / 32;
   int depth;
@@ -139,47 +139,46 @@ constexpr float kRescaleLog2 = 8.f;
 // below 2^-25 is less than 2^-32 of it.
 constexpr float kHeadLog2 = 7.f;
 
-// Shared memory.  KT: the cache's type; quantized caches pass raw stages of cache bytes
-// and are widened to f16 into the operand stages.
+// Shared memory of a block; two blocks share an SM.  KT: the cache's type; quantized caches
+// pass raw stages of cache bytes and are widened to f16 into the operand stages.
 template <int KT, int D>
 struct Lay {
   static constexpr bool Q8 = KT != DA_KV_BF16;
   static constexpr int kTile = (D / 64) * kRegion;  // K (or V) of a tile, 16-bit elements
   static constexpr int kStage = 2 * kTile;
-  static constexpr int kStages = (Q8 ? 3 : 5) * (128 / D);
+  static constexpr int kStages = (Q8 ? 2 : 3) * (128 / D);
   static constexpr int kCodeRow = KT == DA_KV_NVFP4 ? D / 2 : D;  // code bytes of a head's row
   static constexpr int kScaleRow = KT == DA_KV_NVFP4 ? D / 16 : 0;
   static constexpr int kRaw = 2 * kT * (kCodeRow + kScaleRow);
   static constexpr int kRawStage = (kRaw + 1023) / 1024 * 1024;
-  static constexpr int kRawStages = !Q8 ? 0 : D == 64 ? 8 : KT == DA_KV_NVFP4 ? 6 : 5;
-  // The second stream's Q, if it has its own (64 dims of 128 rows a region, swizzled);
-  // between units also 4 KB for each softmax warp, through which Q and the output pass
-  static constexpr int kQ1 = kStages * kStage;
-  static constexpr int kQRegion = kRows * 128;
-  static constexpr int kRawOffset = kQ1 + 2 * kQRegion;
-  static constexpr int kBarOffset = kRawOffset + kRawStages * kRawStage;
+  static constexpr int kRawStages = !Q8 ? 0 : (KT == DA_KV_NVFP4 ? 3 : 2) * (128 / D);
+  static constexpr int kRawOffset = kStages * kStage;
+  static constexpr int kPass = kRawOffset + kRawStages * kRawStage;  // 2 KB for each softmax warp
+  static constexpr int kBarOffset = kPass + 4 * 2048;
   // barriers
   static constexpr int kFull = 0, kEmpty = kFull + kStages, kRawFull = kEmpty + kStages,
-                       kRawEmpty = kRawFull + kRawStages, kQFull = kRawEmpty + kRawStages, kSFull = kQFull + 2,
-                       kSFree = kSFull + 2, kPFull = kSFree + 2, kPVDone = kPFull + 2, kDrain = kPVDone + 2, kStall = kDrain + 1,
-                       kBars = kStall + 1;
-  static constexpr int kSlots = kBarOffset + kBars * 8;      // TMEM address, abort flag
-  static constexpr int kStats = (kSlots + 8 + 15) / 16 * 16;  // m and l of 2 x 128 rows
-  static constexpr int kScales = kStats + 2 * 2 * kRows * 4;  // softmax scales of 128 rows
-  static constexpr int kSizes = kScales + kRows * 4;          // length and nodes of each row
-  static constexpr int kFirst = kSizes + kTreeRows * 8;       // first unit of each row
+                       kRawEmpty = kRawFull + kRawStages, kQFull = kRawEmpty + kRawStages, kSFull = kQFull + 1,
+                       kSFree = kSFull + 1, kPFull = kSFree + 1, kPVDone = kPFull + 1, kDrain = kPVDone + 1,
+                       kStall = kDrain + 1, kBars = kStall + 1;
+  static constexpr int kSlots = kBarOffset + kBars * 8;         // TMEM address, abort flag
+  static constexpr int kSizes = (kSlots + 8 + 15) / 16 * 16;    // length, nodes and splits of each row
+  static constexpr int kFirst = kSizes + kTreeRows * 8;         // first unit of each row
   static constexpr int kBytes = kFirst + (kTreeRows + 1) * 4;
-  // warps 0-3 and 4-7 softmax and output, 8 and 9 MMAs, 10 and 11 copies, 12-15 conversion
-  static constexpr int kThreads = Q8 ? 512 : 384;
-  static_assert(kBytes <= 232448, "fits a block's shared memory");
-  static_assert(kBytes > 232448 / 2, "one block an SM (TMEM is taken whole)");
+  // warps 0-3 softmax, Q and output, 4 and 5 MMAs, 6 and 7 copies, 8-11 conversion.  With
+  // these the threads' registers are split by role; the shares add up to what the block was
+  // launched with, 384 * 80 = 128 * (128 + 56 + 56).
+  static constexpr int kThreads = Q8 ? 384 : 256;
+  static constexpr int kSoftmaxRegs = 128, kIssueRegs = 56, kConvertRegs = 56;
+  static_assert(!Q8 || 128 * (kSoftmaxRegs + kIssueRegs + kConvertRegs) <= kThreads * 80, "register split");
+  static_assert(2 * (kBytes + 1024) <= 228 * 1024, "two blocks an SM");
+  // tensor memory: S, O, Q (two elements a column) and, for 64 dims, P; for 128 dims P lies
+  // in shared memory, over the K tile that its scores came from
+  static constexpr uint32_t kSCol = 0, kOCol = 64, kQCol = kOCol + D, kPCol = kQCol + D / 2;
+  static constexpr bool kPInTmem = D == 64;
+  static_assert(kPCol + (kPInTmem ? 32 : 0) <= 256, "half of the tensor memory");
 };
 
-constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSCol = 0;    // S of the two streams, 64 columns each
-constexpr uint32_t kOCol = 128;  // their O
-constexpr uint32_t kQCol = 384;  // Q of the first or of both, two elements a column
-constexpr uint32_t kPCol = 448;  // their P, 32 columns each
+constexpr uint32_t kTmemCols = 256;
 
 struct Maps {
   CUtensorMap k3, v3;  // [entries][H_kv][row], boxes of 16 to 64 entries
@@ -198,18 +197,6 @@ struct Ctx {
 
 __device__ __forceinline__ void report(int32_t* err, int bits) {
   if (err) atomicOr(err, bits);
-}
-
-__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 
 // Bounded wait that also gives up when another role has.
@@ -242,6 +229,16 @@ __device__ __forceinline__ void arrive_warp(const Ctx& c, int i) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(c.bars + 8 * i);
 }
 
+// 16 columns of tensor memory from registers (32 lanes)
+__device__ __forceinline__ void st_16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -251,11 +248,7 @@ __device__ __forceinline__ void fence_proxy_async() {
 struct Unit {
   TreeRow r;
   int b, h, split, begin, end, row0, rows;
-  bool wide;  // more than 128 rows: each stream has its own, over all tiles
-  // Else both streams have the same rows, and each takes every other tile.
   __device__ __forceinline__ int tiles() const { return end - begin; }
-  __device__ __forceinline__ bool takes(int stream, int i) const { return wide || (i & 1) == stream; }
-  __device__ __forceinline__ bool works(int stream) const { return tiles() > (wide ? 0 : stream); }
 };
 
 __device__ __forceinline__ Unit unit_of(const TreeLaunch& p, const Ctx& c, int u) {
@@ -269,17 +262,21 @@ __device__ __forceinline__ Unit unit_of(const TreeLaunch& p, const Ctx& c, int u
   }
   Unit x;
   const int2 size = c.sizes[lo];
-  x.r = tree_row(p, size.x, size.y);
+  x.r = tree_row(p, size.x, size.y & 0xff, size.y >> 8);
   x.b = p.row0 + lo;
   u -= c.first[lo];
-  x.row0 = u % x.r.supers * kTreeSuper;
-  u /= x.r.supers;
-  x.h = u % p.H_kv;
-  x.split = u / p.H_kv;
+  x.row0 = 0;
+  const int supers = (x.r.nodes * p.G + kTreeSuper - 1) / kTreeSuper;
+  if (supers > 1) {
+    const int v = u / supers;
+    x.row0 = (u - v * supers) * kTreeSuper;
+    u = v;
+  }
+  x.split = quotient(u, p.by_heads);
+  x.h = u - x.split * p.H_kv;
   x.begin = x.split * x.r.per_split;
   x.end = min(x.begin + x.r.per_split, x.r.tiles);
   x.rows = min(kTreeSuper, x.r.nodes * p.G - x.row0);
-  x.wide = x.rows > kRows;
   return x;
 }
 
@@ -337,7 +334,7 @@ __device__ void producer(const TreeLaunch& p, const Ctx& c, const Maps& m, int b
   auto look_up = [&](const Unit& x, int j, int n) -> int {
     if (j >= x.r.end || (j >= x.r.hole_from && j + n <= x.r.hole_to)) return 0;
     if (p.layout == DA_KV_CONTIGUOUS) return x.b * p.width + j;
-    const int at = p.layout == DA_KV_PAGED ? j / p.page_size : j;
+    const int at = p.layout == DA_KV_PAGED ? quotient(j, p.by_page) : j;
     const int word = __ldg(p.table + (long long)x.b * p.width + at);
     if (word < 0 || word >= p.num_blocks) {
       bad = true;
@@ -471,7 +468,7 @@ __device__ void converter(const TreeLaunch& p, const Ctx& c) {
   using L = Lay<KT, D>;
   constexpr int kPieces = D / 16;               // 16-dim pieces of a row
   constexpr int kStep = 128 / kPieces;          // rows between a thread's
-  const int ct = threadIdx.x - 12 * 32;
+  const int ct = threadIdx.x - 8 * 32;
   const int jj = ct % kPieces, r0 = ct / kPieces;
   uint32_t g = 0;
   for (int u = blockIdx.x; u < c.units; u += gridDim.x) {
@@ -526,95 +523,62 @@ __device__ void converter(const TreeLaunch& p, const Ctx& c) {
 }
 
 // ------------------------------------------------------------------ MMAs
-// One thread for each stream.  S = Q K^T of its next tile as soon as the softmax has read
-// the one before, O += P V as soon as it has written P: whichever can go first, so that
-// the softmax finds the next scores waiting.  Q lies in tensor memory, shared by both
-// streams, or, for the second of a wide unit, in shared memory.
+// Two threads: one issues S = Q K^T of a tile as soon as it is there and the softmax has
+// read the scores before it, so that the softmax finds the next ones waiting; the other
+// O += P V when the softmax has written P.
 template <int KT, int D>
-__device__ void issue(const TreeLaunch& p, const Ctx& c, uint32_t tmem, int stream) {
+__device__ void issue_s(const TreeLaunch& p, const Ctx& c, uint32_t tmem) {
   using L = Lay<KT, D>;
-  constexpr uint32_t kIdescS = L::Q8 ? umma::idesc_f16_f32(kRows, kT, false) : umma::idesc_bf16_f32(kRows, kT, false);
-  constexpr uint32_t kIdescO = L::Q8 ? umma::idesc_f16_f32(kRows, D, true) : umma::idesc_bf16_f32(kRows, D, true);
+  constexpr uint32_t kIdesc = L::Q8 ? umma::idesc_f16_f32(kRows, kT, false) : umma::idesc_bf16_f32(kRows, kT, false);
   const uint64_t k0 = umma::smem_desc(c.sbase, 16, 1024, umma::kSwizzle128B);
+  if (p.test_stall && !wait_bar(c, L::kStall, 0, kTestStallNs)) return;
+  uint32_t g = 0, nu = 0;
+  for (int u = blockIdx.x; u < c.units; u += gridDim.x) {
+    const int n = unit_of(p, c, u).tiles();
+    if (n == 0) continue;
+    if (!wait_bar(c, L::kQFull, nu++ & 1)) return;
+    for (int i = 0; i < n; ++i, ++g) {
+      const uint32_t st = g % L::kStages;
+      const uint64_t kd = k0 + (uint64_t)((st * L::kStage) >> 4);
+      if (!wait_bar(c, L::kFull + st, (g / L::kStages) & 1)) return;
+      if (g && !wait_bar(c, L::kSFree, (g - 1) & 1)) return;
+      umma::fence_after_sync();
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        umma::mma_bf16_ta(tmem + L::kSCol, tmem + L::kQCol + k * 8,
+                          kd + (uint64_t)(((k / 4) * kRegion + (k % 4) * 32) >> 4), kIdesc, k ? 1u : 0u);
+      umma::commit(c.bars + 8 * L::kSFull);
+    }
+  }
+}
+
+template <int KT, int D>
+__device__ void issue_pv(const TreeLaunch& p, const Ctx& c, uint32_t tmem) {
+  using L = Lay<KT, D>;
+  constexpr uint32_t kIdesc = L::Q8 ? umma::idesc_f16_f32(kRows, D, true) : umma::idesc_bf16_f32(kRows, D, true);
+  const uint64_t p0 = umma::smem_desc(c.sbase, 16, 1024, umma::kSwizzle128B);
   // V with its dims contiguous: 64-dim regions kRegion apart, 8-entry groups 1024 bytes
   const uint64_t v0 = umma::smem_desc(c.sbase + L::kTile, kRegion, 1024, umma::kSwizzle128B);
-  const uint64_t q1 = umma::smem_desc(c.sbase + L::kQ1, 16, 1024, umma::kSwizzle128B);
-  const uint32_t s_col = tmem + kSCol + stream * kT, o_col = tmem + kOCol + stream * D;
-  const uint32_t p_col = tmem + kPCol + stream * 32;
-  if (p.test_stall && stream == 0 && !wait_bar(c, L::kStall, 0, kTestStallNs)) return;
-  uint32_t g = 0, mine = 0;       // tiles of the CTA before this unit; S issued by the stream
-  uint32_t nq = 0;                // units that the stream has had work in
-  auto ready = [&](int i, uint32_t parity) { return mbar_test_wait(c.bars + 8 * i, parity); };
+  uint32_t g = 0;
   for (int u = blockIdx.x; u < c.units; u += gridDim.x) {
-    const Unit x = unit_of(p, c, u);
-    const int n = x.tiles(), step = x.wide ? 1 : 2, first = x.wide ? 0 : stream;
-    const bool own_q = x.wide && stream == 1;
-    if (x.works(stream)) {  // (Q is there: all units before are done with)
-      if (!wait_bar(c, L::kQFull + stream, nq & 1)) return;
-      ++nq;
+    const int n = unit_of(p, c, u).tiles();
+    for (int i = 0; i < n; ++i, ++g) {
+      const uint32_t st = g % L::kStages;
+      const uint64_t at = (uint64_t)((st * L::kStage) >> 4);
+      if (!wait_bar(c, L::kPFull, g & 1)) return;
+      umma::fence_after_sync();
+#pragma unroll
+      for (int k = 0; k < kT / 16; ++k) {
+        const uint64_t vd = v0 + at + (uint64_t)((k * 2048) >> 4);
+        const uint32_t more = k ? 1u : i > 0;
+        if constexpr (L::kPInTmem)
+          umma::mma_bf16_ta(tmem + L::kOCol, tmem + L::kPCol + k * 8, vd, kIdesc, more);
+        else
+          umma::mma_bf16(tmem + L::kOCol, p0 + at + (uint64_t)((k * 32) >> 4), vd, kIdesc, more);
+      }
+      umma::commit(c.bars + 8 * L::kPVDone);
+      umma::commit(c.bars + 8 * (L::kEmpty + st));
     }
-    const uint32_t base = mine;  // the stream's number of the unit's first tile
-    const int total = n > first ? (n - first + step - 1) / step : 0;
-    int s_done = 0, o_done = 0;  // of the stream's tiles of the unit
-    uint32_t idle = 0;
-    unsigned long long t0 = 0;
-    while (o_done < total) {
-      bool went = false;
-      if (s_done < total && s_done <= o_done + 1) {
-        const uint32_t t = g + first + s_done * step, st = t % L::kStages;
-        // the tile is there, and the scores before it have been read.  (The stage's tile
-        // before may have been the other stream's: only once it is used up does the parity
-        // of "full" mean this tile.)
-        if ((t < L::kStages || ready(L::kEmpty + st, ((t / L::kStages) & 1) ^ 1)) &&
-            ready(L::kFull + st, (t / L::kStages) & 1) &&
-            (mine == 0 || ready(L::kSFree + stream, (mine - 1) & 1))) {
-          umma::fence_after_sync();
-          const uint64_t kd = k0 + (uint64_t)((st * L::kStage) >> 4);
-          if (own_q) {
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              umma::mma_bf16(s_col, q1 + (uint64_t)(((k / 4) * L::kQRegion + (k % 4) * 32) >> 4),
-                             kd + (uint64_t)(((k / 4) * kRegion + (k % 4) * 32) >> 4), kIdescS, k ? 1u : 0u);
-          } else {
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              umma::mma_bf16_ta(s_col, tmem + kQCol + k * 8,
-                                kd + (uint64_t)(((k / 4) * kRegion + (k % 4) * 32) >> 4), kIdescS, k ? 1u : 0u);
-          }
-          umma::commit(c.bars + 8 * (L::kSFull + stream));
-          ++s_done;
-          ++mine;
-          went = true;
-        }
-      }
-      if (o_done < s_done && ready(L::kPFull + stream, (base + o_done) & 1)) {
-        umma::fence_after_sync();
-        const uint32_t t = g + first + o_done * step, st = t % L::kStages;
-        const uint64_t vd = v0 + (uint64_t)((st * L::kStage) >> 4);
-#pragma unroll
-        for (int k = 0; k < kT / 16; ++k)
-          umma::mma_bf16_ta(o_col, p_col + k * 8, vd + (uint64_t)((k * 2048) >> 4), kIdescO,
-                            (o_done == 0 && k == 0) ? 0u : 1u);
-        umma::commit(c.bars + 8 * (L::kPVDone + stream));
-        umma::commit(c.bars + 8 * (L::kEmpty + st));  // (two arrivals free a stage)
-        if (!x.wide) umma::commit(c.bars + 8 * (L::kEmpty + st));
-        ++o_done;
-        went = true;
-      }
-      if (went) {
-        idle = 0;
-      } else if ((++idle & 63u) == 0) {
-        if (*c.abort_flag) return;
-        const unsigned long long now = globaltimer_ns();
-        if (idle == 64) t0 = now;
-        if (now - t0 > kWaitLimitNs) {
-          report(c.err, DA_DEVERR_TIMEOUT);
-          *c.abort_flag = 1;
-          return;
-        }
-      }
-    }
-    g += n;
   }
 }
 
@@ -631,187 +595,140 @@ __device__ __forceinline__ unsigned long long windowed(const TreeLaunch& p, cons
   return keep;
 }
 
-// The row of a unit that thread `tid` of a stream has.
+// The row of a unit that a thread has.
 struct Lane {
   int t, head;   // node, query head
   uint32_t row;  // of q, out and lse
   bool live;
 };
 
-__device__ __forceinline__ Lane lane_of(const TreeLaunch& p, const Unit& x, int stream, int tid) {
+__device__ __forceinline__ Lane lane_of(const TreeLaunch& p, const Unit& x, int at) {
   Lane y;
-  const int idx = x.row0 + (x.wide ? stream * kRows : 0) + tid;
-  y.live = idx < x.row0 + x.rows;
-  y.t = y.live ? idx / p.G : 0;
+  y.live = at < x.rows;
+  const int idx = x.row0 + at;
+  y.t = y.live ? quotient(idx, p.by_group) : 0;
   y.head = x.h * p.G + (y.live ? idx - y.t * p.G : 0);
   y.row = ((uint32_t)x.b * p.T + y.t) * p.H_q + y.head;
   return y;
 }
 
-// Bytes of 16-byte chunk `ch` of row `row` in 32 rows of 128 bytes whose chunks are swapped so
+// Byte of 16-byte chunk `ch` of row `row` in 32 rows of 64 bytes whose chunks are swapped so
 // that neither a warp's rows nor its columns meet in a bank.
-__device__ __forceinline__ uint32_t chunk_at(int row, int ch) { return row * 128 + ((ch ^ (row & 7)) << 4); }
+__device__ __forceinline__ uint32_t chunk_at(int row, int ch) { return row * 64 + ((ch ^ ((row >> 1) & 3)) << 4); }
 
-// A unit's Q to where its MMAs read it: bf16 as it is, or f16 scaled by a power of two;
-// the first stream's into tensor memory, by way of `stage`, 4 KB of this warp's, the
-// second's (wide units) into its place in shared memory.  Whole rows are loaded by eight
-// lanes each (a thread that loads its own row keeps the L1 busy for 4000 cycles a unit).
+// A warp's 32 rows of Q into tensor memory: bf16 as they are, or f16 scaled by a power of
+// two.  Four lanes load a row, 32 dims at a time, and it changes hands by way of `pass` (a
+// thread that loads its own row keeps the L1 busy for several times as long).  Returns
+// the row's softmax scale.
 template <int KT, int D>
-__device__ __forceinline__ float put_q(const TreeLaunch& p, const Ctx& c, const Lane& y, int stream, uint32_t q_col,
-                                       uint8_t* stage) {
+__device__ __forceinline__ float put_q(const TreeLaunch& p, const Lane& y, int lane, uint32_t q_col, uint8_t* pass) {
   using L = Lay<KT, D>;
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+  constexpr int kParts = D / 32;
   const uint32_t live = __ballot_sync(0xffffffffu, y.live);
-  constexpr int kHalves = D / 64;
-  uint4 w[kHalves][8];  // this lane's pieces of rows 4 i + lane / 8
+  uint4 w[kParts][4];  // this lane's pieces of rows 8 i + lane / 4
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int rr = 4 * i + (lane >> 3);
-    const uint32_t row = __shfl_sync(0xffffffffu, y.row, rr);
-    const uint4* from = reinterpret_cast<const uint4*>(p.q + (size_t)row * D) + (lane & 7);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t row = __shfl_sync(0xffffffffu, y.row, 8 * i + (lane >> 2));
+    const uint4* from = reinterpret_cast<const uint4*>(p.q + (size_t)row * D) + (lane & 3);
+    const bool there = live >> (8 * i + (lane >> 2)) & 1;
 #pragma unroll
-    for (int half = 0; half < kHalves; ++half)
-      w[half][i] = (live >> rr & 1) ? __ldg(from + half * 8) : make_uint4(0, 0, 0, 0);
-  }
-  uint4 own[kHalves][8];  // this lane's row
-#pragma unroll
-  for (int half = 0; half < kHalves; ++half) {
-    uint8_t* at = stream ? c.smem + L::kQ1 + half * L::kQRegion + warp * 4096 : stage;
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(at + chunk_at(4 * i + (lane >> 3), lane & 7)) = w[half][i];
-    if (stream && !L::Q8) continue;  // it is where it belongs
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) own[half][i] = *reinterpret_cast<const uint4*>(at + chunk_at(lane, i));
+    for (int part = 0; part < kParts; ++part) w[part][i] = there ? __ldg(from + 4 * part) : make_uint4(0, 0, 0, 0);
   }
   float sc = 1.f, row_scale = p.scale_log2;
   if constexpr (L::Q8) {
     uint32_t most = 0;
 #pragma unroll
-    for (int half = 0; half < kHalves; ++half)
+    for (int i = 0; i < 4; ++i) {
+      uint32_t top = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) most = bf16x8_absmax_bits(most, own[half][i]);
+      for (int part = 0; part < kParts; ++part) top = bf16x8_absmax_bits(top, w[part][i]);
+      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // row 8 i + j lies with lanes 4 j .. 4 j + 3
+      const uint32_t v = __shfl_sync(0xffffffffu, top, (lane & 7) * 4);
+      if (i == lane >> 3) most = v;
+    }
     const int e = q_prescale_exp(bf16_absmax_value(most));
     sc = exp2_int(e);
     row_scale *= exp2_int(-e);
   }
-  if (!stream || L::Q8) {
 #pragma unroll
-    for (int half = 0; half < kHalves; ++half) {
-      uint32_t q32[32];
+  for (int part = 0; part < kParts; ++part) {
+    __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t v[4] = {own[half][i].x, own[half][i].y, own[half][i].z, own[half][i].w};
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(pass + chunk_at(8 * i + (lane >> 2), lane & 3)) = w[part][i];
+    __syncwarp();
+    uint32_t q16[16];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (L::Q8) {
-            const __half2 hh = __floats2half2_rn(bf16_lo(v[e]) * sc, bf16_hi(v[e]) * sc);
-            q32[4 * i + e] = *reinterpret_cast<const uint32_t*>(&hh);
-          } else {
-            q32[4 * i + e] = v[e];
-          }
+    for (int i = 0; i < 4; ++i) {
+      const uint4 own = *reinterpret_cast<const uint4*>(pass + chunk_at(lane, i));
+      const uint32_t v[4] = {own.x, own.y, own.z, own.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (L::Q8) {
+          const __half2 hh = __floats2half2_rn(bf16_lo(v[e]) * sc, bf16_hi(v[e]) * sc);
+          q16[4 * i + e] = *reinterpret_cast<const uint32_t*>(&hh);
+        } else {
+          q16[4 * i + e] = v[e];
         }
       }
-      if (!stream) {
-        umma::st_32x32b_x32_u(q_col + half * 32, q32);
-      } else {
-        uint8_t* at = c.smem + L::kQ1 + half * L::kQRegion + warp * 4096;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<uint4*>(at + chunk_at(lane, i)) =
-              make_uint4(q32[4 * i], q32[4 * i + 1], q32[4 * i + 2], q32[4 * i + 3]);
-      }
     }
+    st_16(q_col + part * 16, q16);
   }
-  if (!stream) {
-    umma::wait_st();
-    umma::fence_before_sync();
-  } else {
-    fence_proxy_async();
-  }
-  arrive_warp(c, L::kQFull + stream);
+  umma::wait_st();
   return row_scale;
 }
 
-// Four warps a stream; a thread has one row, a TMEM lane.  Its scores' running reference
-// value moves only when one exceeds it by more than 2^8 (then its O is rescaled).  The
-// next unit's Q goes out before this one's output is written.
+// Four warps; a thread has one row, a TMEM lane.  Its scores' running reference value moves
+// only when one exceeds it by more than 2^8 (then its O is rescaled).  Between units a warp
+// brings in its rows' Q and writes its rows' output, by itself; the SM's other block fills
+// that time.
 template <int KT, int D>
-__device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem, int stream) {
+__device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem) {
   using L = Lay<KT, D>;
-  const int lane = threadIdx.x & 31, tid = threadIdx.x & 127, warp = tid >> 5;
+  const int tid = threadIdx.x & 127, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = tmem + ((uint32_t)(warp * 32) << 16);
-  const uint32_t s_col = base + kSCol + stream * kT, o_col = base + kOCol + stream * D;
-  const uint32_t p_col = base + kPCol + stream * 32;
-  float* stats = reinterpret_cast<float*>(c.smem + L::kStats);  // [stream][m, l][128]
-  uint32_t g = 0, mine = 0;
-  float* scales = reinterpret_cast<float*>(c.smem + L::kScales);
-  // (the first stream's warps share the second half of the space, which holds the
-  // second's rows of the upper dims only once theirs have passed)
-  uint8_t* stage = c.smem + L::kQ1 + (stream ? 0 : L::kQRegion) + warp * 4096;
-  Unit x = unit_of(p, c, blockIdx.x);
-  Lane y = lane_of(p, x, stream, tid);
-  float row_scale = p.scale_log2;
-  // Q of unit x: the first stream's part before, the second's after a barrier of both
-  auto first_q = [&] {
-    if (stream == 0 && x.tiles() > 0) {
-      row_scale = put_q<KT, D>(p, c, y, 0, base + kQCol, stage);
-      if (!x.wide && x.works(1)) arrive_warp(c, L::kQFull + 1);
-      if (L::Q8) scales[tid] = row_scale;
-    }
-  };
-  auto second_q = [&] {
-    if (stream == 0 || x.tiles() == 0) return;
-    if (x.wide)
-      row_scale = put_q<KT, D>(p, c, y, 1, 0, stage);
-    else if (L::Q8)
-      row_scale = scales[tid];
-  };
-  first_q();
-  named_bar_sync(1, 256);
-  second_q();
+  const uint32_t s_col = base + L::kSCol, o_col = base + L::kOCol;
+  uint8_t* pass = c.smem + L::kPass + warp * 2048;
+  uint32_t g = 0;
   for (int u = blockIdx.x; u < c.units; u += gridDim.x) {
-    const TreeRow r = x.r;
-    const bool live = y.live;
-    const int t = y.t, head = y.head;
-    bool ok = true;
+    const Unit x = unit_of(p, c, u);
+    const Lane y = lane_of(p, x, tid);
+    const int length = x.r.length, end = x.end;
+    // ---- Q (all MMAs of the unit before are done)
+    const float row_scale = put_q<KT, D>(p, y, lane, base + L::kQCol, pass);
+    umma::fence_before_sync();
+    if (x.tiles() > 0) arrive_warp(c, L::kQFull);
     // ---- what the row sees, if the unit's last tile reaches the nodes or there is a window
-    const bool edge = p.window || (x.tiles() > 0 && (tree_tile(r, x.end - 1) + 1) * kT > r.length);
     unsigned long long anc = 0;
     int depth = 0;
-    if (edge && live) {
-      anc = windowed(p, r, ancestors(p, x.b, t, &depth), depth);
-      anc &= low_bits(r.end - r.length);
+    if (y.live && x.tiles() > 0 && (p.window || (tree_tile(x.r, end - 1) + 1) * kT > length)) {
+      anc = windowed(p, x.r, ancestors(p, x.b, y.t, &depth), depth);
+      anc &= low_bits(x.r.end - length);
     }
     float m_used = -INFINITY, l = 0.f;
-    bool start = true;
-    for (int i = 0; i < x.tiles(); ++i, ++g) {
-      if (!x.takes(stream, i)) continue;
-      if (!wait_warp(c, L::kSFull + stream, mine & 1)) {
-        ok = false;
-        break;
-      }
+    for (int i = x.begin; i < end; ++i, ++g) {
+      if (!wait_warp(c, L::kSFull, g & 1)) return;
       umma::fence_after_sync();
       float s[kT];
       umma::ld_32x32b_x32(s_col, *reinterpret_cast<float(*)[32]>(s));
       umma::ld_32x32b_x32(s_col + 32, *reinterpret_cast<float(*)[32]>(s + 32));
       umma::wait_ld();
       umma::fence_before_sync();
-      arrive_warp(c, L::kSFree + stream);
-      const int j0 = tree_tile(r, x.begin + i) * kT;
-      const bool all = j0 + kT <= r.length && (!p.window || j0 + kT <= p.sinks || j0 >= r.length + r.nodes - p.window);
+      arrive_warp(c, L::kSFree);
+      const int j0 = tree_tile(x.r, i) * kT;
+      const bool all = j0 + kT <= length && (!p.window || j0 + kT <= p.sinks || j0 >= length + x.r.nodes - p.window);
       const float factor = row_scale > 0.f ? row_scale : 1.f;
       if (row_scale <= 0.f) {  // (the largest score is not the largest product then)
 #pragma unroll
         for (int k = 0; k < kT; ++k) s[k] *= row_scale;
       }
       if (!all) {
-        unsigned long long vis = low_bits(r.length - j0);
-        if (p.window) vis &= ~low_bits(r.length + depth - p.window + 1 - j0) | low_bits(p.sinks - j0);
-        const int shift = r.length - j0;  // of node 0 in the tile
+        unsigned long long vis = low_bits(length - j0);
+        if (p.window) vis &= ~low_bits(length + depth - p.window + 1 - j0) | low_bits(p.sinks - j0);
+        const int shift = length - j0;  // of node 0 in the tile
         if (shift > -64 && shift < 64) vis |= shift >= 0 ? anc << shift : anc >> -shift;
-        if (!live) vis = 0;
+        if (!y.live) vis = 0;
 #pragma unroll
         for (int k = 0; k < kT; ++k)
           if (!(vis >> k & 1)) s[k] = -INFINITY;
@@ -846,14 +763,20 @@ __device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem, 
         }
       }
       l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
-      // the stream's P V before has read its P, and O stands still
-      if (!start && !wait_warp(c, L::kPVDone + stream, (mine - 1) & 1)) {
-        ok = false;
-        break;
+      m_used = m_new;
+      const uint32_t st = g % L::kStages;
+      if constexpr (!L::kPInTmem) {  // over the tile's K, which S has read: 64 weights, 128 bytes a row
+        uint8_t* to = c.smem + st * L::kStage + tid * 128;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<uint4*>(to + ((k ^ (tid & 7)) << 4)) =
+              make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
       }
+      // the P V before has been done: O stands still
+      if (g && !wait_warp(c, L::kPVDone, (g - 1) & 1)) return;
       umma::fence_after_sync();
-      umma::st_32x32b_x32_u(p_col, pk);
-      if (!start && __any_sync(0xffffffffu, alpha != 1.f)) {
+      if constexpr (L::kPInTmem) umma::st_32x32b_x32_u(base + L::kPCol, pk);
+      if (i > x.begin && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
         for (int ch = 0; ch < D / 32; ++ch) {
           float o[32];
@@ -864,92 +787,70 @@ __device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem, 
           umma::st_32x32b_x32(o_col + ch * 32, o);
         }
       }
-      m_used = m_new;
       // values of entries that no node sees: zero times what lies there could be a NaN
-      const unsigned long long hid = hidden_bits(r, j0);
+      const unsigned long long hid = hidden_bits(x.r, j0);
       if (hid) {
-        const int st = g % L::kStages, k = tid >> 1;
-        if (!wait_warp(c, L::kFull + st, (g / L::kStages) & 1)) {  // (it has been: this orders the stores)
-          ok = false;
-          break;
-        }
+        const int k = tid >> 1;
+        if (!wait_warp(c, L::kFull + st, (g / L::kStages) & 1)) return;  // (it has been: this orders the stores)
         if (hid >> k & 1) {
           uint8_t* v = c.smem + st * L::kStage + L::kTile + k * 128 + (D == 128 ? (tid & 1) * kRegion : (tid & 1) * 64);
 #pragma unroll
           for (int e = 0; e < (D == 128 ? 8 : 4); ++e) reinterpret_cast<uint4*>(v)[e] = make_uint4(0, 0, 0, 0);
         }
-        fence_proxy_async();
       }
+      if (!L::kPInTmem || hid) fence_proxy_async();
       umma::wait_st();
       umma::fence_before_sync();
-      arrive_warp(c, L::kPFull + stream);
-      start = false;
-      ++mine;
+      arrive_warp(c, L::kPFull);
     }
     // ---- output
-    if (ok && x.works(stream)) ok = wait_warp(c, L::kPVDone + stream, (mine - 1) & 1);
-    stats[stream * 2 * kRows + tid] = m_used;
-    stats[stream * 2 * kRows + kRows + tid] = l;
-    // all eight warps leave together, or none
-    if (named_bar_or(1, 256, !ok)) return;
+    if (x.tiles() > 0 && !wait_warp(c, L::kPVDone, (g - 1) & 1)) return;
     umma::fence_after_sync();
-    float M = m_used, sum = l, f0 = 1.f, f1 = 1.f;  // the streams' weights (narrow units)
-    if (!x.wide) {
-      const float m0 = stats[tid], m1 = stats[2 * kRows + tid];
-      M = fmaxf(m0, m1);
-      f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M);
-      f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
-      sum = fmaf(f0, stats[kRows + tid], f1 * stats[3 * kRows + tid]);
-    }
-    const bool single = r.splits == 1;
+    const bool single = x.r.splits == 1;
     // rows of the partials against those of q and out
     const long long to_slot = (((long long)x.b * p.max_splits + x.split) - x.b) * p.T * p.H_q;
-    const float inv = (sum > 0.f ? 1.f / sum : sum != sum ? sum : 0.f) * p.v_scale;
-    const int ch0 = x.wide ? 0 : stream * (D / 64), ch1 = x.wide ? D / 32 : ch0 + D / 64;
-    const uint32_t lives = __ballot_sync(0xffffffffu, live);
-    bool odd = sum != sum;  // something that is not finite
+    const uint32_t lives = __ballot_sync(0xffffffffu, y.live);
+    const float inv = (l > 0.f ? 1.f / l : l != l ? l : 0.f) * p.v_scale;
+    bool odd = l != l;  // something that is not finite
 #pragma unroll 1
-    for (int ch = lives ? ch0 : ch1; ch < ch1; ++ch) {
-      float o[32];
-      if (!x.wide && x.tiles() > 1) {
-        float o1[32];
-        umma::ld_32x32b_x32(base + kOCol + ch * 32, o);
-        umma::ld_32x32b_x32(base + kOCol + D + ch * 32, o1);
-        umma::wait_ld();
+    for (int ch = lives ? 0 : D / 16; ch < D / 16; ++ch) {
+      float o[16];
+      umma::ld_32x32b_x16(o_col + ch * 16, o);
+      umma::wait_ld();
+      float top = 0.f;  // (a sum of magnitudes: infinite or NaN if one of them is)
 #pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] = fmaf(f0, o[k], f1 * o1[k]);
-      } else if (x.tiles() > 0) {  // (a lone tile is the first stream's)
-        umma::ld_32x32b_x32((x.wide ? o_col : base + kOCol) + ch * 32, o);
-        umma::wait_ld();
-      }
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
+      for (int k = 0; k < 16; ++k) {
         o[k] = x.tiles() > 0 ? o[k] * inv : 0.f;
-        odd |= !(fabsf(o[k]) < INFINITY);
+        top += fabsf(o[k]);
       }
+      odd |= !(top < INFINITY);
       __syncwarp();
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        *reinterpret_cast<float4*>(stage + chunk_at(lane, k)) =
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<float4*>(pass + chunk_at(lane, k)) =
             make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
       __syncwarp();
+      uint32_t row[4];
+      float4 v[4];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {  // eight lanes write a row
-        const int rr = 4 * k + (lane >> 3);
-        const uint32_t row = __shfl_sync(0xffffffffu, y.row, rr);
-        if (!(lives >> rr & 1)) continue;
-        const float4 v = *reinterpret_cast<const float4*>(stage + chunk_at(rr, lane & 7));
+      for (int k = 0; k < 4; ++k) {  // four lanes write a row
+        row[k] = __shfl_sync(0xffffffffu, y.row, 8 * k + (lane >> 2));
+        v[k] = *reinterpret_cast<const float4*>(pass + chunk_at(8 * k + (lane >> 2), lane & 3));
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool mine = lives >> (8 * k + (lane >> 2)) & 1;
         if (single) {
-          const __nv_bfloat162 h0 = __floats2bfloat162_rn(v.x, v.y), h1 = __floats2bfloat162_rn(v.z, v.w);
-          reinterpret_cast<uint2*>(p.out + (size_t)row * D + ch * 32)[lane & 7] =
-              make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-        } else {
-          reinterpret_cast<float4*>(p.o_part + (to_slot + row) * D + ch * 32)[lane & 7] = v;
+          const __nv_bfloat162 h0 = __floats2bfloat162_rn(v[k].x, v[k].y), h1 = __floats2bfloat162_rn(v[k].z, v[k].w);
+          const uint2 h = make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+          if (mine) reinterpret_cast<uint2*>(p.out + (size_t)row[k] * D + ch * 16)[lane & 3] = h;
+        } else if (mine) {
+          reinterpret_cast<float4*>(p.o_part + (to_slot + row[k]) * D + ch * 16)[lane & 3] = v[k];
         }
       }
     }
-    const float lse = sum > 0.f || sum != sum ? M + lg2(sum) : -INFINITY;
-    if (live && (x.wide || stream == 0)) {
+    if (y.live) {
+      const float lse = l > 0.f || l != l ? m_used + lg2(l) : -INFINITY;
       if (single)
         p.lse[y.row] = lse * kLn2;
       else
@@ -958,47 +859,46 @@ __device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem, 
     // A value that some node sees and another does not may have been infinite or NaN: zero
     // times it has spoiled the other's sum.  Such rows are formed again, entry by entry.
     __syncwarp();
-    for (uint32_t again = __ballot_sync(0xffffffffu, live && odd); again; again &= again - 1) {
+    for (uint32_t again = __ballot_sync(0xffffffffu, y.live && odd); again; again &= again - 1) {
       const int src = __ffs((int)again) - 1;
-      const int at = __shfl_sync(0xffffffffu, t, src), hq = __shfl_sync(0xffffffffu, head, src);
+      const int t = __shfl_sync(0xffffffffu, y.t, src), head = __shfl_sync(0xffffffffu, y.head, src);
+      const uint32_t row = __shfl_sync(0xffffffffu, y.row, src);
       float m2, l2, o[D / 32];
-      attend_plainly<KT, D>(p, r, x.b, at, hq, x.begin, x.end, lane, &m2, &l2, o);
+      attend_plainly<KT, D>(p, x.r, x.b, t, head, x.begin, x.end, lane, &m2, &l2, o);
       const float inv2 = (l2 > 0.f ? 1.f / l2 : l2 != l2 ? l2 : 0.f) * p.v_scale;
       const float lse2 = l2 > 0.f || l2 != l2 ? m2 + lg2(l2) : -INFINITY;
-      const long long row2 = ((long long)x.b * p.T + at) * p.H_q + hq, slot2 = to_slot + row2;
-      if (x.wide || (lane >> 4) == stream) {  // this stream's dims
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) {
-          const int d = lane * (D / 32) + e;
-          if (single)
-            p.out[row2 * D + d] = __float2bfloat16_rn(o[e] * inv2);
-          else
-            p.o_part[slot2 * D + d] = o[e] * inv2;
-        }
-      }
-      if (lane == 0 && (x.wide || stream == 0)) {
+      for (int e = 0; e < D / 32; ++e) {
+        const int d = lane * (D / 32) + e;
         if (single)
-          p.lse[row2] = lse2 * kLn2;
+          p.out[(size_t)row * D + d] = __float2bfloat16_rn(o[e] * inv2);
         else
-          p.lse_part[slot2] = lse2;
+          p.o_part[(to_slot + row) * D + d] = o[e] * inv2;
+      }
+      if (lane == 0) {
+        if (single)
+          p.lse[row] = lse2 * kLn2;
+        else
+          p.lse_part[to_slot + row] = lse2;
       }
       __syncwarp();
     }
-    // ---- the next unit
-    if (u + (int)gridDim.x < c.units) {
-      x = unit_of(p, c, u + gridDim.x);
-      y = lane_of(p, x, stream, tid);
-      first_q();  // (all MMAs of this unit are done)
-    }
     umma::fence_before_sync();
-    named_bar_sync(1, 256);  // O and the statistics have been read
-    umma::fence_after_sync();
-    if (u + (int)gridDim.x < c.units) second_q();
   }
 }
 
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int N>
+__device__ __forceinline__ void leave_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 template <int KT, int D>
-__global__ void __launch_bounds__(Lay<KT, D>::kThreads, 1)
+__global__ void __launch_bounds__(Lay<KT, D>::kThreads, 2)
     tree_kernel(const TreeLaunch p, const __grid_constant__ Maps maps, int box) {
   using L = Lay<KT, D>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -1017,19 +917,16 @@ __global__ void __launch_bounds__(Lay<KT, D>::kThreads, 1)
     for (int i = 0; i < L::kBars; ++i) {
       uint32_t count = 1;  // tcgen05.commit, or the producer's expect_tx arrive
       if (i >= L::kFull && i < L::kFull + L::kStages && L::Q8) count = 4;
-      if (i >= L::kEmpty && i < L::kEmpty + L::kStages) count = 2;
       if (i >= L::kRawFull && i < L::kRawFull + L::kRawStages && KT == DA_KV_NVFP4) count = 33;
       if (i >= L::kRawEmpty && i < L::kRawEmpty + L::kRawStages) count = 4;
-      if ((i >= L::kQFull && i < L::kQFull + 2) || (i >= L::kSFree && i < L::kSFree + 2) ||
-          (i >= L::kPFull && i < L::kPFull + 2))
-        count = 4;
+      if (i == L::kQFull || i == L::kSFree || i == L::kPFull) count = 4;
       if (i == L::kDrain) count = 2;
       mbar_init(c.bars + 8 * i, count);
     }
     *c.abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (warp == 4) {
     umma::tmem_alloc(c.sbase + L::kSlots, kTmemCols);
     umma::tmem_relinquish();
   }
@@ -1040,7 +937,7 @@ __global__ void __launch_bounds__(Lay<KT, D>::kThreads, 1)
   for (int i = threadIdx.x; i < p.rows; i += L::kThreads) {
     const int2 s = tree_size(p, p.row0 + i, &bad);
     const TreeRow r = tree_row(p, s.x, s.y);
-    sizes[i] = s;
+    sizes[i] = make_int2(s.x, s.y | r.splits << 8);
     first[i + 1] = r.splits * r.supers * p.H_kv;
   }
   if (blockIdx.x == 0) {  // inputs that are out of range
@@ -1075,23 +972,31 @@ __global__ void __launch_bounds__(Lay<KT, D>::kThreads, 1)
   if (!aligned && threadIdx.x == 0) report(p.err, DA_DEVERR_TIMEOUT);
 
   if ((int)blockIdx.x < c.units && aligned) {
-    if (warp < 8) {
-      softmax_warps<KT, D>(p, c, tmem, warp >> 2);
-    } else if (warp < 10) {
-      if (lane == 0) {
-        issue<KT, D>(p, c, tmem, warp - 8);
+    if (warp < 4) {
+      if constexpr (L::Q8) take_registers<L::kSoftmaxRegs>();
+      softmax_warps<KT, D>(p, c, tmem);
+    } else if (warp < 8) {
+      if constexpr (L::Q8) leave_registers<L::kIssueRegs>();
+      if (warp >= 6) {
+        producer<KT, D>(p, c, maps, box);
+      } else if (lane == 0) {
+        if (warp == 4)
+          issue_s<KT, D>(p, c, tmem);
+        else
+          issue_pv<KT, D>(p, c, tmem);
         umma::commit(c.bars + 8 * L::kDrain);  // arrives when all MMAs of this thread are done
       }
-    } else if (warp < 12) {
-      producer<KT, D>(p, c, maps, box);
     } else {
-      if constexpr (L::Q8) converter<KT, D>(p, c);
+      if constexpr (L::Q8) {
+        leave_registers<L::kConvertRegs>();
+        converter<KT, D>(p, c);
+      }
     }
     __syncwarp();
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
-    if (warp == 8 && lane == 0) {
+    if (warp == 4 && lane == 0) {
       const unsigned long long t0 = globaltimer_ns();
       while (!mbar_try_wait(c.bars + 8 * L::kDrain, 0)) {
         if (globaltimer_ns() - t0 > kWaitLimitNs) {
@@ -1102,7 +1007,7 @@ __global__ void __launch_bounds__(Lay<KT, D>::kThreads, 1)
     }
     __syncwarp();
   }
-  if (warp == 8) umma::tmem_dealloc(tmem, kTmemCols);
+  if (warp == 4) umma::tmem_dealloc(tmem, kTmemCols);
 }
 
 constexpr int kCombineWarps = 4;
@@ -1242,10 +1147,13 @@ cudaError_t launch_shape(const TreeLaunch& p0, int sms, cudaStream_t stream) {
       return cudaErrorInvalidValue;
   }
   const int supers = (p.T * p.G + kTreeSuper - 1) / kTreeSuper;
+  p.by_heads = fast_div(p.H_kv);
+  p.by_group = fast_div(p.G);
+  p.by_page = fast_div(std::max(p.page_size, 1));
   for (p.row0 = 0; p.row0 < p.B; p.row0 += kTreeRows) {
     p.rows = std::min(kTreeRows, p.B - p.row0);
     const long long most = (long long)p.rows * p.max_splits * p.H_kv * supers;
-    const cudaError_t e = launch_after(tree_kernel<KT, D>, dim3((unsigned)std::min<long long>(most, sms)),
+    const cudaError_t e = launch_after(tree_kernel<KT, D>, dim3((unsigned)std::min<long long>(most, 2 * sms)),
                                        dim3(L::kThreads), (size_t)L::kBytes, stream, p, m, box);
     if (e != cudaSuccess) return e;
   }

@@ -7,7 +7,23 @@ namespace da {
 
 constexpr int kTreeTile = 64;       // entries of a tile
 constexpr int kTreeMaxSplits = 64;  // pieces of a row's list at most
-constexpr int kTreeSuper = 256;     // (node, head) rows of a unit at most
+constexpr int kTreeSuper = 128;     // (node, head) rows of a unit at most
+
+// n / d for n below 2^31 by a multiplication: a unit's place is found with several
+// divisions, of 40 or so dependent instructions each otherwise.
+struct FastDiv {
+  uint32_t d, mul, shift;
+};
+
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f = {d, 0, 0};
+  if (d > 1) {
+    while ((1u << f.shift) < d) ++f.shift;
+    f.mul = (uint32_t)((1ull << (31 + f.shift)) / d + 1);
+    --f.shift;
+  }
+  return f;
+}
 
 struct TreeLaunch {
   const __nv_bfloat16* q;
@@ -33,9 +49,10 @@ struct TreeLaunch {
   float v_scale;
   int test_stall;
   int row0, rows;  // the rows of this launch
+  FastDiv by_heads, by_group, by_page;  // H_kv, G, page_size
 };
 
-constexpr int kTreeRows = 512;  // rows of a launch at most
+constexpr int kTreeRows = 256;  // rows of a launch at most
 
 cudaError_t launch_tree(const TreeLaunch& p, int sms, cudaStream_t stream);
 cudaError_t launch_tree_combine(const TreeLaunch& p, cudaStream_t stream);
@@ -48,6 +65,10 @@ constexpr int kTreeLeastTiles = 8;
 
 #ifdef __CUDACC__
 
+__device__ __forceinline__ int quotient(int n, const FastDiv& f) {
+  return f.d == 1 ? n : (int)(__umulhi((uint32_t)n, f.mul) >> f.shift);
+}
+
 // What a row attends to.  It follows from the row's own length, number of nodes and
 // the call's window alone.
 struct TreeRow {
@@ -58,7 +79,8 @@ struct TreeRow {
   int tiles, per_split, splits, supers;
 };
 
-__device__ __forceinline__ TreeRow tree_row(const TreeLaunch& p, int length, int nodes) {
+// `splits`: their number where it is known.
+__device__ __forceinline__ TreeRow tree_row(const TreeLaunch& p, int length, int nodes, int splits = 0) {
   TreeRow r;
   r.length = length;
   r.nodes = nodes;
@@ -78,7 +100,7 @@ __device__ __forceinline__ TreeRow tree_row(const TreeLaunch& p, int length, int
   r.tiles = all - r.skip;
   const int rows = r.nodes * p.G;
   r.per_split = max(tree_min_tiles(rows), (r.tiles + kTreeMaxSplits - 1) / kTreeMaxSplits);
-  r.splits = max(1, (r.tiles + r.per_split - 1) / r.per_split);
+  r.splits = splits ? splits : max(1, (r.tiles + r.per_split - 1) / r.per_split);
   r.supers = (rows + kTreeSuper - 1) / kTreeSuper;
   return r;
 }
