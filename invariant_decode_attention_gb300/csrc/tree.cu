@@ -139,6 +139,14 @@ constexpr float kRescaleLog2 = 8.f;
 // below 2^-25 is less than 2^-32 of it.
 constexpr float kHeadLog2 = 7.f;
 
+// A unit of work: tiles [begin, end) of row b's list, KV head h, (node, head) rows
+// row0 .. row0 + rows - 1 of the row's.
+struct Unit {
+  TreeRow r;
+  int b, h, split, begin, end, row0, rows;
+  __device__ __forceinline__ int tiles() const { return end - begin; }
+};
+
 // Shared memory of a block; two blocks share an SM.  KT: the cache's type; quantized caches
 // pass raw stages of cache bytes and are widened to f16 into the operand stages.
 template <int KT, int D>
@@ -163,7 +171,9 @@ struct Lay {
   static constexpr int kSlots = kBarOffset + kBars * 8;         // TMEM address, abort flag
   static constexpr int kSizes = (kSlots + 8 + 15) / 16 * 16;    // length, nodes and splits of each row
   static constexpr int kFirst = kSizes + kTreeRows * 8;         // first unit of each row
-  static constexpr int kBytes = kFirst + (kTreeRows + 1) * 4;
+  // this and the next unit of each softmax warp
+  static constexpr int kUnits = (kFirst + (kTreeRows + 1) * 4 + 15) / 16 * 16;
+  static constexpr int kBytes = kUnits + 4 * 2 * (int)sizeof(Unit);
   // warps 0-3 softmax, Q and output, 4 and 5 MMAs, 6 and 7 copies, 8-11 conversion.  With
   // these the threads' registers are split by role; the shares add up to what the block was
   // launched with, 384 * 80 = 128 * (128 + 56 + 56).
@@ -242,14 +252,6 @@ __device__ __forceinline__ void st_16(uint32_t taddr, const uint32_t (&r)[16]) {
 __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
-
-// A unit of work: tiles [begin, end) of row b's list, KV head h, (node, head) rows
-// row0 .. row0 + rows - 1 of the row's.
-struct Unit {
-  TreeRow r;
-  int b, h, split, begin, end, row0, rows;
-  __device__ __forceinline__ int tiles() const { return end - begin; }
-};
 
 __device__ __forceinline__ Unit unit_of(const TreeLaunch& p, const Ctx& c, int u) {
   int lo = 0, hi = p.rows;  // the row with first[row] <= u < first[row + 1]
@@ -690,24 +692,35 @@ __device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem) 
   const uint32_t base = tmem + ((uint32_t)(warp * 32) << 16);
   const uint32_t s_col = base + L::kSCol, o_col = base + L::kOCol;
   uint8_t* pass = c.smem + L::kPass + warp * 2048;
-  uint32_t g = 0;
-  for (int u = blockIdx.x; u < c.units; u += gridDim.x) {
-    const Unit x = unit_of(p, c, u);
-    const Lane y = lane_of(p, x, tid);
-    const int length = x.r.length, end = x.end;
-    // ---- Q (all MMAs of the unit before are done)
-    const float row_scale = put_q<KT, D>(p, y, lane, base + L::kQCol, pass);
+  // A unit's description stays in shared memory: the loop over tiles has no register for
+  // what is needed before and behind it.
+  Unit* units = reinterpret_cast<Unit*>(c.smem + L::kUnits) + 2 * warp;
+  auto begin_unit = [&](int u, Unit* to) -> float {
+    const Unit z = unit_of(p, c, u);
+    if (lane == 0) *to = z;
+    __syncwarp();
+    const float scale = put_q<KT, D>(p, lane_of(p, z, tid), lane, base + L::kQCol, pass);
     umma::fence_before_sync();
-    if (x.tiles() > 0) arrive_warp(c, L::kQFull);
+    if (z.tiles() > 0) arrive_warp(c, L::kQFull);
+    return scale;
+  };
+  uint32_t g = 0;
+  float row_scale = begin_unit(blockIdx.x, units);
+  for (int u = blockIdx.x, slot = 0; u < c.units; u += gridDim.x, slot ^= 1) {
+    const Unit* x = units + slot;
+    const int begin = x->begin, end = x->end, length = x->r.length, head = x->r.head_tiles, skip = x->r.skip;
+    const bool live = tid < x->rows;
+    // tiles from here on are seen whole, up to the end of the context
+    const int whole = p.window ? length + x->r.nodes - p.window : 0;
     // ---- what the row sees, if the unit's last tile reaches the nodes or there is a window
     unsigned long long anc = 0;
     int depth = 0;
-    if (y.live && x.tiles() > 0 && (p.window || (tree_tile(x.r, end - 1) + 1) * kT > length)) {
-      anc = windowed(p, x.r, ancestors(p, x.b, y.t, &depth), depth);
-      anc &= low_bits(x.r.end - length);
+    if (live && end > begin && (p.window || ((end - 1 < head ? end : end + skip) * kT > length))) {
+      anc = windowed(p, x->r, ancestors(p, x->b, quotient(x->row0 + tid, p.by_group), &depth), depth);
+      anc &= low_bits(x->r.end - length);
     }
     float m_used = -INFINITY, l = 0.f;
-    for (int i = x.begin; i < end; ++i, ++g) {
+    for (int i = begin; i < end; ++i, ++g) {
       if (!wait_warp(c, L::kSFull, g & 1)) return;
       umma::fence_after_sync();
       float s[kT];
@@ -716,8 +729,8 @@ __device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem) 
       umma::wait_ld();
       umma::fence_before_sync();
       arrive_warp(c, L::kSFree);
-      const int j0 = tree_tile(x.r, i) * kT;
-      const bool all = j0 + kT <= length && (!p.window || j0 + kT <= p.sinks || j0 >= length + x.r.nodes - p.window);
+      const int j0 = (i < head ? i : i + skip) * kT;
+      const bool all = j0 + kT <= length && (j0 >= whole || j0 + kT <= p.sinks);
       const float factor = row_scale > 0.f ? row_scale : 1.f;
       if (row_scale <= 0.f) {  // (the largest score is not the largest product then)
 #pragma unroll
@@ -728,7 +741,7 @@ __device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem) 
         if (p.window) vis &= ~low_bits(length + depth - p.window + 1 - j0) | low_bits(p.sinks - j0);
         const int shift = length - j0;  // of node 0 in the tile
         if (shift > -64 && shift < 64) vis |= shift >= 0 ? anc << shift : anc >> -shift;
-        if (!y.live) vis = 0;
+        if (!live) vis = 0;
 #pragma unroll
         for (int k = 0; k < kT; ++k)
           if (!(vis >> k & 1)) s[k] = -INFINITY;
@@ -776,7 +789,7 @@ __device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem) 
       if (g && !wait_warp(c, L::kPVDone, (g - 1) & 1)) return;
       umma::fence_after_sync();
       if constexpr (L::kPInTmem) umma::st_32x32b_x32_u(base + L::kPCol, pk);
-      if (i > x.begin && __any_sync(0xffffffffu, alpha != 1.f)) {
+      if (i > begin && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
         for (int ch = 0; ch < D / 32; ++ch) {
           float o[32];
@@ -788,7 +801,7 @@ __device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem) 
         }
       }
       // values of entries that no node sees: zero times what lies there could be a NaN
-      const unsigned long long hid = hidden_bits(x.r, j0);
+      const unsigned long long hid = all ? 0 : hidden_bits(x->r, j0);
       if (hid) {
         const int k = tid >> 1;
         if (!wait_warp(c, L::kFull + st, (g / L::kStages) & 1)) return;  // (it has been: this orders the stores)
@@ -803,13 +816,16 @@ __device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem) 
       umma::fence_before_sync();
       arrive_warp(c, L::kPFull);
     }
-    // ---- output
-    if (x.tiles() > 0 && !wait_warp(c, L::kPVDone, (g - 1) & 1)) return;
+    // ---- the next unit's Q, whose scores can then be formed, and this one's output
+    if (end > begin && !wait_warp(c, L::kPVDone, (g - 1) & 1)) return;
     umma::fence_after_sync();
-    const bool single = x.r.splits == 1;
+    if (u + (int)gridDim.x < c.units) row_scale = begin_unit(u + gridDim.x, units + (slot ^ 1));
+    const Unit done = *x;
+    const Lane mine = lane_of(p, done, tid);
+    const bool single = done.r.splits == 1;
     // rows of the partials against those of q and out
-    const long long to_slot = (((long long)x.b * p.max_splits + x.split) - x.b) * p.T * p.H_q;
-    const uint32_t lives = __ballot_sync(0xffffffffu, y.live);
+    const long long to_slot = (((long long)done.b * p.max_splits + done.split) - done.b) * p.T * p.H_q;
+    const uint32_t lives = __ballot_sync(0xffffffffu, mine.live);
     const float inv = (l > 0.f ? 1.f / l : l != l ? l : 0.f) * p.v_scale;
     bool odd = l != l;  // something that is not finite
 #pragma unroll 1
@@ -820,7 +836,7 @@ __device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem) 
       float top = 0.f;  // (a sum of magnitudes: infinite or NaN if one of them is)
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        o[k] = x.tiles() > 0 ? o[k] * inv : 0.f;
+        o[k] = done.tiles() > 0 ? o[k] * inv : 0.f;
         top += fabsf(o[k]);
       }
       odd |= !(top < INFINITY);
@@ -834,37 +850,37 @@ __device__ void softmax_warps(const TreeLaunch& p, const Ctx& c, uint32_t tmem) 
       float4 v[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {  // four lanes write a row
-        row[k] = __shfl_sync(0xffffffffu, y.row, 8 * k + (lane >> 2));
+        row[k] = __shfl_sync(0xffffffffu, mine.row, 8 * k + (lane >> 2));
         v[k] = *reinterpret_cast<const float4*>(pass + chunk_at(8 * k + (lane >> 2), lane & 3));
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const bool mine = lives >> (8 * k + (lane >> 2)) & 1;
+        const bool there = lives >> (8 * k + (lane >> 2)) & 1;
         if (single) {
           const __nv_bfloat162 h0 = __floats2bfloat162_rn(v[k].x, v[k].y), h1 = __floats2bfloat162_rn(v[k].z, v[k].w);
           const uint2 h = make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-          if (mine) reinterpret_cast<uint2*>(p.out + (size_t)row[k] * D + ch * 16)[lane & 3] = h;
-        } else if (mine) {
+          if (there) reinterpret_cast<uint2*>(p.out + (size_t)row[k] * D + ch * 16)[lane & 3] = h;
+        } else if (there) {
           reinterpret_cast<float4*>(p.o_part + (to_slot + row[k]) * D + ch * 16)[lane & 3] = v[k];
         }
       }
     }
-    if (y.live) {
+    if (mine.live) {
       const float lse = l > 0.f || l != l ? m_used + lg2(l) : -INFINITY;
       if (single)
-        p.lse[y.row] = lse * kLn2;
+        p.lse[mine.row] = lse * kLn2;
       else
-        p.lse_part[to_slot + y.row] = lse;
+        p.lse_part[to_slot + mine.row] = lse;
     }
     // A value that some node sees and another does not may have been infinite or NaN: zero
     // times it has spoiled the other's sum.  Such rows are formed again, entry by entry.
     __syncwarp();
-    for (uint32_t again = __ballot_sync(0xffffffffu, y.live && odd); again; again &= again - 1) {
+    for (uint32_t again = __ballot_sync(0xffffffffu, mine.live && odd); again; again &= again - 1) {
       const int src = __ffs((int)again) - 1;
-      const int t = __shfl_sync(0xffffffffu, y.t, src), head = __shfl_sync(0xffffffffu, y.head, src);
-      const uint32_t row = __shfl_sync(0xffffffffu, y.row, src);
+      const int t = __shfl_sync(0xffffffffu, mine.t, src), head = __shfl_sync(0xffffffffu, mine.head, src);
+      const uint32_t row = __shfl_sync(0xffffffffu, mine.row, src);
       float m2, l2, o[D / 32];
-      attend_plainly<KT, D>(p, x.r, x.b, t, head, x.begin, x.end, lane, &m2, &l2, o);
+      attend_plainly<KT, D>(p, done.r, done.b, t, head, done.begin, done.end, lane, &m2, &l2, o);
       const float inv2 = (l2 > 0.f ? 1.f / l2 : l2 != l2 ? l2 : 0.f) * p.v_scale;
       const float lse2 = l2 > 0.f || l2 != l2 ? m2 + lg2(l2) : -INFINITY;
 #pragma unroll
