@@ -269,9 +269,9 @@ size_t nvfp4_mm_verify_workspace_bytes(int32_t batch, int32_t nodes, int32_t voc
  * the lowest one with the largest logit.  It is -1 where no token may come (logits all
  * -inf or NaN).
  *
- * p at the drafted tokens is formed in fp64 from an fp32 sum, r as integers of 2^-44 of
- * the largest p, off by about 2^-38 of their size, whose sums are exact.  A
- * request's results depend on that request alone.  NaN logits count as -inf; if the
+ * exp((x - max) / temperature) is an integer of units of 2^-44, off by about 2^-38 of its
+ * size, so that the sums for the next token are exact; p at the drafted tokens is that over
+ * an fp32 sum.  A request's results depend on that request alone.  NaN logits count as -inf; if the
  * largest is +inf, the tokens that have it share everything.  Temperatures other than 0
  * are taken within [2^-100, 2^100], negative ones and NaN as 0; uniforms within [0, 1),
  * NaN as 0; draft values that are negative or NaN: refused, and nothing is taken off p.

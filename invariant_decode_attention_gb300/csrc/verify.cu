@@ -13,8 +13,8 @@
 // one.  So weights are integers, 2^44 exp((x - max) / temperature) off by about 2^-38 of their
 // size: their sums are exact in any order, and how a row is cut does not show.  The
 // exponential is formed for that in two fp32 terms: x - max and its product with
-// log2(e) / temperature without error, 2^(j / 64) from a table, and five terms of the
-// series of exp for the rest, whose argument is below 2^-7.5.
+// log2(e) / temperature without error, 2^(j / 128) from a table, and five terms of the
+// series of exp for the rest, whose argument is below 2^-8.5.
 #include <algorithm>
 #include <cmath>
 
@@ -32,7 +32,8 @@ constexpr int kThreads = 512;                       // of walk_kernel
 constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;                         // CTAs of a request at most
 constexpr int kNodes = NVFP4_VERIFY_MAX_NODES;
-constexpr int kBlock = 32 * kVec;                   // tokens a warp takes at once
+constexpr int kBlock = 32 * kVec;                   // tokens of a warp's load
+constexpr int kAhead = 4;                           // loads of a thread in flight
 static_assert(kNodes == 64, "two nodes a lane");
 
 struct Part {  // of a row's chunk
@@ -69,34 +70,80 @@ __device__ __forceinline__ const void* row_of(const Args& a, int b, int t) {
   return static_cast<const char*>(a.x) + (b * a.x_row + t * a.x_node) * (BF16 ? 2 : 4);
 }
 
-// Whether groups of kVec tokens of a row lie on their natural boundaries.
-template <bool BF16>
-__device__ __forceinline__ bool in_step(const void* row) {
-  return (reinterpret_cast<uintptr_t>(row) & (BF16 ? 7 : 15)) == 0;
-}
-
 template <bool BF16>
 __device__ __forceinline__ float one(const void* row, long long v) {
   return BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(row)[v])
               : static_cast<const float*>(row)[v];
 }
 
-// Tokens v .. v + 3 of a row, -inf past its end.  The same tokens for the same
-// thread wherever the row lies.
 template <bool BF16>
-__device__ __forceinline__ void load4(const void* row, int v, int V, bool whole, float (&f)[kVec]) {
-  if (whole && v + kVec <= V) {
-    if (BF16) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(row) + v));
-      f[0] = bf16_lo(w.x), f[1] = bf16_hi(w.x), f[2] = bf16_lo(w.y), f[3] = bf16_hi(w.y);
-    } else {
-      const float4 w = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(row) + v));
-      f[0] = w.x, f[1] = w.y, f[2] = w.z, f[3] = w.w;
-    }
+struct Word {
+  using type = float4;
+};
+template <>
+struct Word<true> {
+  using type = uint2;
+};
+
+// The bytes from `skew` on of two words that follow each other.
+__device__ __forceinline__ uint2 joined(uint2 w, uint2 n, int skew) {
+  const uint32_t w0 = skew & 4 ? w.y : w.x, w1 = skew & 4 ? n.x : w.y, w2 = skew & 4 ? n.y : n.x;
+  return skew & 2 ? make_uint2(__funnelshift_r(w0, w1, 16), __funnelshift_r(w1, w2, 16)) : make_uint2(w0, w1);
+}
+
+__device__ __forceinline__ float4 joined(float4 w, float4 n, int skew) {
+  return skew == 4   ? make_float4(w.y, w.z, w.w, n.x)
+         : skew == 8 ? make_float4(w.z, w.w, n.x, n.y)
+                     : make_float4(w.w, n.x, n.y, n.z);
+}
+
+// Bytes by which groups of kVec tokens of a row lie behind their natural boundaries.
+template <bool BF16>
+__device__ __forceinline__ int skew_of(const void* row) {
+  return (int)(reinterpret_cast<uintptr_t>(row) & (BF16 ? 7 : 15));
+}
+
+// Groups of four tokens from v, v + step, ... on, -inf at and past `end`: the same tokens
+// for the same thread wherever the row lies.  All loads go out together.  A group off its
+// boundary is put together from the two aligned words that hold it (each has some of its
+// bytes, so that both may be read).
+template <bool BF16, int N>
+__device__ __forceinline__ void load4(const void* row, int v, int step, int end, int skew, float (&f)[N][kVec]) {
+  using W = typename Word<BF16>::type;
+  if (v + (N - 1) * step + kVec > end) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        const int at = v + i * step + e;
+        f[i][e] = at < end ? one<BF16>(row, at) : -INFINITY;
+      }
     return;
   }
+  const W* at = reinterpret_cast<const W*>(static_cast<const char*>(row) + (BF16 ? 2ll : 4ll) * v - skew);
+  step >>= 2;
+  W w[N];
+  if (skew == 0) {
 #pragma unroll
-  for (int e = 0; e < kVec; ++e) f[e] = v + e < V ? one<BF16>(row, v + e) : -INFINITY;
+    for (int i = 0; i < N; ++i) w[i] = __ldg(at + i * step);
+  } else {
+    W n[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      w[i] = __ldg(at + i * step);
+      n[i] = __ldg(at + i * step + 1);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = joined(w[i], n[i], skew);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if constexpr (BF16) {
+      f[i][0] = bf16_lo(w[i].x), f[i][1] = bf16_hi(w[i].x), f[i][2] = bf16_lo(w[i].y), f[i][3] = bf16_hi(w[i].y);
+    } else {
+      f[i][0] = w[i].x, f[i][1] = w[i].y, f[i][2] = w[i].z, f[i][3] = w[i].w;
+    }
+  }
 }
 
 template <bool BF16>
@@ -112,12 +159,11 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const Args a) {
   if (t >= count_of(a, b, &bad)) return;
   const float tau = temperature_of(a, b);
   const void* row = row_of<BF16>(a, b, t);
-  const bool whole = in_step<BF16>(row);
+  const int skew = skew_of<BF16>(row);
   const int v0 = chunk * kChunk + threadIdx.x * kVec;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float f[kLoads][kVec];
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i) load4<BF16>(row, v0 + i * kRowThreads * kVec, a.V, whole, f[i]);
+  load4<BF16, kLoads>(row, v0, kRowThreads * kVec, a.V, skew, f);
   float m = -INFINITY;  // (a NaN is none: it counts as -inf)
 #pragma unroll
   for (int i = 0; i < kLoads; ++i)
@@ -168,69 +214,80 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const Args a) {
   }
 }
 
-// round(2^62 * 2^(j / 64)), j = -32 .. 32
-__device__ const unsigned long long kPowers[65] = {
-    0x2d413cccfe779921ull, 0x2dbf6478ca345de4ull, 0x2e3eebd1d8bee7baull, 0x2ebfd6ac84cf917full,
-    0x2f4228e7d6030db0ull, 0x2fc5e66d9e9cc421ull, 0x304b1332999c2516ull, 0x30d1b3368925d902ull,
-    0x3159ca845541b6b7ull, 0x31e35d322aee6c57ull, 0x326e6f619b8bc9e9ull, 0x32fb053fbc9c9f17ull,
-    0x3389230547e12039ull, 0x3418ccf6bbcac965ull, 0x34aa07647c4ab917ull, 0x353cd6aaf3fb7e88ull,
-    0x35d13f32b5a75abdull, 0x366745709e2bf5edull, 0x36feede5f6bc8dd5ull, 0x37983d209783a449ull,
-    0x383337bb0aa53844ull, 0x38cfe25cafa29694ull, 0x396e41b9df20d22aull, 0x3a0e5a940f12f71aull,
-    0x3ab031b9f7490e4cull, 0x3b53cc07b6650ae1ull, 0x3bf92e66f736bd73ull, 0x3ca05dcf167fec4eull,
-    0x3d495f454921b30bull, 0x3df437dcc2b44eeeull, 0x3ea0ecb6dc8a80cfull, 0x3f4f83033d21b05dull,
-    0x4000000000000000ull, 0x40b268f9de0183baull, 0x4166c34c5615d0ecull, 0x421d1461d66f2023ull,
-    0x42d561b3e6243d8aull, 0x438fb0cb4f468808ull, 0x444c0740496d4294ull, 0x450a6abaa4b77ecdull,
-    0x45cae0f1f545eb73ull, 0x468d6fadbf2dd4f3ull, 0x47521cc5a2e6a9e0ull, 0x4818ee218a3358eeull,
-    0x48e1e9b9d588e19bull, 0x49ad159789f37496ull, 0x4a7a77d47f7b84b1ull, 0x4b4a169b900c2d00ull,
-    0x4c1bf828c6dc54b8ull, 0x4cf022c9905bfd32ull, 0x4dc69cdceaa72a9cull, 0x4e9f6cd3967fdba8ull,
-    0x4f7a993048d088d7ull, 0x50582887dcb8a7e1ull, 0x513821818624b40cull, 0x521a8ad704f3404full,
-    0x52ff6b54d8a89c75ull, 0x53e6c9da74b29ab5ull, 0x54d0ad5a753e077cull, 0x55bd1cdad49f699cull,
-    0x56ac1f752150a563ull, 0x579dbc56b48521baull, 0x5891fac0e95612c8ull, 0x5988e20954889245ull,
-    0x5a827999fcef3242ull
+// round(2^62 * 2^(j / 128)), j = 0 .. 127
+__device__ const unsigned long long kPowers[128] = {
+    0x4000000000000000ull, 0x4058f6a7ecccd5b6ull, 0x40b268f9de0183baull, 0x410c57a1b9fe12f6ull,
+    0x4166c34c5615d0ecull, 0x41c1aca777db771bull, 0x421d1461d66f2023ull, 0x4278fb2b1bce0d15ull,
+    0x42d561b3e6243d8aull, 0x433248adc91fdd02ull, 0x438fb0cb4f468808ull, 0x43ed9abffb4c6bc9ull,
+    0x444c0740496d4294ull, 0x44aaf701b0c72feeull, 0x450a6abaa4b77ecdull, 0x456a632296394492ull,
+    0x45cae0f1f545eb73ull, 0x462be4e23237a6efull, 0x468d6fadbf2dd4f3ull, 0x46ef821011734e6bull,
+    0x47521cc5a2e6a9e0ull, 0x47b5408bf36472e2ull, 0x4818ee218a3358eeull, 0x487d2645f7725895ull,
+    0x48e1e9b9d588e19bull, 0x4947393eca98fcd6ull, 0x49ad159789f37496ull, 0x4a137f87d58e025bull,
+    0x4a7a77d47f7b84b1ull, 0x4ae1ff436b663ff7ull, 0x4b4a169b900c2d00ull, 0x4bb2bea4f8bd5847ull,
+    0x4c1bf828c6dc54b8ull, 0x4c85c3f13360c4d5ull, 0x4cf022c9905bfd32ull, 0x4d5b157e4a7fc325ull,
+    0x4dc69cdceaa72a9cull, 0x4e32b9b417619617ull, 0x4e9f6cd3967fdba8ull, 0x4f0cb70c4ea39210ull,
+    0x4f7a993048d088d7ull, 0x4fe91412b2006e83ull, 0x50582887dcb8a7e1ull, 0x50c7d76542a25b72ull,
+    0x513821818624b40cull, 0x51a907b474015dc9ull, 0x521a8ad704f3404full, 0x528cabc35f4f799dull,
+    0x52ff6b54d8a89c75ull, 0x5372ca67f774358full, 0x53e6c9da74b29ab5ull, 0x545b6a8b3d990704ull,
+    0x54d0ad5a753e077cull, 0x5546932976483b15ull, 0x55bd1cdad49f699cull, 0x56344b525f1ff495ull,
+    0x56ac1f752150a563ull, 0x57249a29651adc07ull, 0x579dbc56b48521baull, 0x581786e5db7022c2ull,
+    0x5891fac0e95612c8ull, 0x590d18d3330c7f1eull, 0x5988e20954889245ull, 0x5a05575132a5cc20ull,
+    0x5a827999fcef3242ull, 0x5b0049d42f6afbb6ull, 0x5b7ec8f19468bbc9ull, 0x5bfdf7e546520f3eull,
+    0x5c7dd7a3b17dcf75ull, 0x5cfe69229605cef5ull, 0x5d7fad59099f22feull, 0x5e01a53f7974fd86ull,
+    0x5e8451cfac061b5full, 0x5f07b404c304c9f1ull, 0x5f8bccdb3d398841ull, 0x60109d50f86846d8ull,
+    0x6096266533384a2bull, 0x611c69188f1eb339ull, 0x61a3666d124bb204ull, 0x622b1f66299a6599ull,
+    0x62b39508aa836d6full, 0x633cc85ad5122fbdull, 0x63c6ba6455dcd8aeull, 0x64516c2e47ff1623ull,
+    0x64dcdec3371793d1ull, 0x6569132f21483ba7ull, 0x65f60a7f79393e2eull, 0x6683c5c3281ee6e9ull,
+    0x6712460a8fc24072ull, 0x67a18c678c8c8c61ull, 0x683199ed779592caull, 0x68c26fb128b4cd63ull,
+    0x69540ec8f895722dull, 0x69e6784cc2cd61bdull, 0x6a79ad55e7f6fd10ull, 0x6b0daeff4fcde703ull,
+    0x6ba27e656b4eb57aull, 0x6c381ca636d99642ull, 0x6cce8ae13c57ebdbull, 0x6d65ca379564e639ull,
+    0x6dfddbcbed791babull, 0x6e96c0c284192610ull, 0x6f307a412f074892ull, 0x6fcb096f5c782210ull,
+    0x70666f76154a7089ull, 0x7102ad7fff41e9b4ull, 0x719fc4b95f452d29ull, 0x723db6501b9ed447ull,
+    0x72dc8373be41a454ull, 0x737c2d55770fe711ull, 0x741cb5281e25ee34ull, 0x74be1c203627c62bull,
+    0x75606373ee921c97ull, 0x76038c5b260e5eeeull, 0x76a7980f6cca15c2ull, 0x774c87cc06d1812eull,
+    0x77f25ccdee6d7ae6ull, 0x78991853d684a285ull, 0x7940bb9e2cffd89dull, 0x79e947ef1d320d2dull,
+    0x7a92be8a92436616ull, 0x7b3d20b6399fc237ull, 0x7be86fb985689ddcull, 0x7c94acddaeea5d3aull,
+    0x7d41d96db915019dull, 0x7deff6b672f84e24ull, 0x7e9f06067a4360baull, 0x7f4f08ae3dc7c426ull
 };
 
 constexpr int kWeightBits = 44;
 
-struct Scale {  // of the row that is sampled
-  float max, c_hi, c_lo;  // log2(e) / temperature in two terms
+struct Scale {
+  float max;         // of the row
+  float c_hi, c_lo;  // log2(e) / temperature in two terms
 };
 
-__device__ __forceinline__ Scale scale_of(float max, float tau) {
-  const double c = 1.4426950408889634 / (double)tau;
-  Scale s;
-  s.max = max;
-  s.c_hi = (float)c;
-  s.c_lo = (float)(c - (double)s.c_hi);
-  return s;
-}
-
-// 2^44 exp((x - max) / temperature), an integer.
+// 2^44 exp((x - max) / temperature), an integer.  Roundings to integers are additions of
+// 1.5 * 2^23 of the unit: the integer is then what the low bits hold.
 __device__ __forceinline__ unsigned long long weight(float x, const Scale& s,
                                                      const unsigned long long* powers) {
-  if (x == s.max) return 1ull << kWeightBits;
   const float d = __fsub_rn(x, s.max);
   const float p = __fmul_rn(d, s.c_hi);
-  if (!(p > -45.f)) return 0;  // nothing left of it (-inf and NaN among them)
   const float bb = __fsub_rn(d, x);  // the difference's rounding error (two-sum)
   const float d_lo = __fadd_rn(__fsub_rn(x, __fsub_rn(d, bb)), __fsub_rn(-s.max, bb));
   const float p_lo = __fmaf_rn(d, s.c_hi, -p) + __fmaf_rn(d, s.c_lo, __fmul_rn(d_lo, s.c_hi));
-  // p = k + j / 64 + r: k and j by rounding, r exactly
-  const float k = rintf(p);
-  const float f = __fsub_rn(p, k);
-  const float j = rintf(__fmul_rn(f, 64.f));
-  const float r = __fmaf_rn(j, -0.015625f, f);
+  // p = n / 128 + r, r exactly, |r| <= 2^-8
+  constexpr float kInt = 12582912.f;
+  const float t = __fmaf_rn(p, 128.f, kInt);
+  const int n = __float_as_int(t) - __float_as_int(kInt);
+  const float r = __fmaf_rn(__fsub_rn(t, kInt), -0.0078125f, p);
   // z = (r + p_lo) ln 2 in two terms, then exp(z) - 1 = z + z^2 (1/2 + z/6 + z^2/24) + ...
-  constexpr float kL = 0x1.62e4300000000p-1f, kLlo = -0x1.05c6100000000p-29f;
+  constexpr float kL = 0x1.62e43p-1f, kLlo = -0x1.05c61p-29f;
   const float z = __fmul_rn(r, kL);
   const float z_lo = __fmaf_rn(r, kL, -z) + __fmaf_rn(r, kLlo, __fmul_rn(p_lo, kL));
   const float q = __fmul_rn(__fmul_rn(z, z), __fmaf_rn(z, __fmaf_rn(z, 1.f / 24.f, 1.f / 6.f), 0.5f));
-  const float low = __fadd_rn(z_lo, q) + __fmul_rn(z, z_lo);
-  // in units of 2^-46
-  const long long e = __float2ll_rn(__fmul_rn(z, 0x1p46f)) + __float2int_rn(__fmul_rn(low, 0x1p46f));
-  const unsigned long long t = powers[(int)j + 32];
-  const unsigned long long w = t + (unsigned long long)__mul64hi((long long)t, e << 18);
-  const int shift = 62 - kWeightBits - (int)k;  // 18 .. 63
-  return shift > 63 ? 0 : ((w >> (shift - 1)) + 1) >> 1;
+  // e, in units of 2^-39: z to 2^-26, then what is left of it and the rest (below 2^-17)
+  constexpr float kHigh = 12582912.f * 0x1p-26f, kLow = 12582912.f * 0x1p-39f;
+  const float high = __fadd_rn(z, kHigh);
+  const float rest = __fadd_rn(__fadd_rn(__fsub_rn(z, __fsub_rn(high, kHigh)), z_lo), q) + __fmul_rn(z, z_lo);
+  const int e = ((__float_as_int(high) - __float_as_int(kHigh)) << 13) +
+                (__float_as_int(__fadd_rn(rest, kLow)) - __float_as_int(kLow));
+  const unsigned long long power = powers[n & 127];
+  const unsigned long long w = power + (unsigned long long)(((long long)e * (int)(power >> 32)) >> 7);
+  const int shift = 62 - kWeightBits - (n >> 7);  // 18 .. 63
+  const unsigned long long v = ((w >> (shift - 1)) + 1) >> 1;
+  // nothing is left below 2^-45 (nor of -inf and NaN); the largest, which may be infinite, is 1
+  return x == s.max ? 1ull << kWeightBits : p > -45.f ? v : 0;
 }
 
 // floor(u * n) for 0 <= u < 1, up to one unit; n where u >= 1.
@@ -268,19 +325,19 @@ struct Walk {  // what the walk leaves for the sampling
 };
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) walk_kernel(const Args a) {
-  __shared__ float row_max[kNodes];
-  __shared__ double row_sum[kNodes];
+__global__ void __launch_bounds__(kThreads, 2) walk_kernel(const Args a) {
+  __shared__ float row_max[kNodes], factor[2];
+  __shared__ double row_sum[kNodes];  // in units of the weights
   __shared__ int row_best[kNodes], except[kNodes];
   __shared__ Walk walk;
-  __shared__ unsigned long long powers[65], warp_sum[kWarps], cta_sum[3][kCluster];
+  __shared__ unsigned long long powers[128], warp_sum[kWarps], cta_sum[3][kCluster];
   wait_prior_grid();
   cluster_arrive();  // waited for before the first store to another CTA
   uint32_t rank, ranks;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
   const int b = blockIdx.x / ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < 65; i += kThreads) powers[i] = kPowers[i];
+  for (int i = tid; i < 128; i += kThreads) powers[i] = kPowers[i];
   int bad = 0;
   const int n = count_of(a, b, &bad);
   const float tau = temperature_of(a, b);
@@ -297,6 +354,12 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const Args a) {
     return;
   }
 
+  // ---- log2(e) / temperature (one thread: a division in fp64, of which the SM does few)
+  if (tid == kThreads - 1 && tau > 0.f) {
+    const double c = 1.4426950408889634 / (double)tau;
+    factor[0] = (float)c;
+    factor[1] = (float)(c - (double)factor[0]);
+  }
   // ---- each row's parts put together, a warp a row
   for (int t = warp; t < n; t += kWarps) {
     const Part* parts = a.parts + ((long long)b * a.T + t) * a.chunks;
@@ -317,7 +380,7 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const Args a) {
     best = __reduce_min_sync(0xffffffffu, best);
     if (lane == 0) {
       row_max[t] = m;
-      row_sum[t] = sum;
+      row_sum[t] = sum * (double)(1ull << kWeightBits);
       row_best[t] = m > -INFINITY ? best : -1;
     }
   }
@@ -327,7 +390,7 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const Args a) {
   if (warp == 0) {
     int par[2], token[2];
     bool may[2], yes[2];   // a child that may be accepted; one that is, if it is reached
-    double p[2] = {0, 0};  // its token's probability at its parent
+    unsigned long long p[2] = {0, 0};  // its token's weight at its parent
     float u[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -350,11 +413,10 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const Args a) {
       may[h] = true;
       if (tau > 0.f) {
         const float m = row_max[par[h]];
-        const float x = one<BF16>(row_of<BF16>(a, b, par[h]), token[h]);
-        if (x == m && m > -INFINITY)
-          p[h] = 1.0 / row_sum[par[h]];
-        else if (x > -INFINITY && m < INFINITY)
-          p[h] = exp(((double)x - (double)m) / (double)tau) / row_sum[par[h]];
+        if (m > -INFINITY) {
+          const Scale at_parent = {m, factor[0], factor[1]};
+          p[h] = weight(fmaxf(one<BF16>(row_of<BF16>(a, b, par[h]), token[h]), -INFINITY), at_parent, powers);
+        }
       } else {
         yes[h] = token[h] == row_best[par[h]];
       }
@@ -368,7 +430,8 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const Args a) {
         if (may[h] && tau > 0.f) {
           const int t = lane + 32 * h;
           const float q = __ldg(a.draft + b * a.draft_row + t * a.draft_node + token[h]);
-          yes[h] = (double)before * (double)q < p[h];  // (a NaN refuses)
+          // u q < w / sum  (a NaN refuses)
+          yes[h] = (double)before * (double)q * row_sum[par[h]] < (double)p[h];
         }
       }
     } else if (tau > 0.f) {  // an earlier sibling's token has been asked for already
@@ -393,12 +456,12 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const Args a) {
              __ballot_sync(0xffffffffu, yes[0])) & kids;
         if (ok) next = __ffsll((long long)ok) - 1;
       } else {
-        const double limit = __shfl_sync(0xffffffffu, cur < 32 ? u[0] : u[1], cur & 31);
-        double sum = 0;
+        const double limit = (double)__shfl_sync(0xffffffffu, cur < 32 ? u[0] : u[1], cur & 31) * row_sum[cur];
+        unsigned long long sum = 0;
         for (unsigned long long left = kids; left && next < 0; left &= left - 1) {
           const int c = __ffsll((long long)left) - 1;
           sum += __shfl_sync(0xffffffffu, c < 32 ? p[0] : p[1], c & 31);
-          if (limit < sum) next = c;
+          if (limit < (double)sum) next = c;
         }
       }
       if (next < 0) break;
@@ -452,28 +515,33 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const Args a) {
   const void* row = row_of<BF16>(a, b, walk.node);
   // (of the child that was refused)
   const float* q_row = a.draft ? a.draft + b * a.draft_row + (walk.node + 1) * a.draft_node : nullptr;
-  const bool whole = in_step<BF16>(row);
-  const Scale scale = scale_of(walk.max, tau);
+  const int skew = skew_of<BF16>(row);
+  const Scale scale = {walk.max, factor[0], factor[1]};
   const int part = a.slice / kWarps;  // tokens of a warp: a multiple of kBlock
   const int v_first = (int)rank * a.slice + warp * part, v_last = min(v_first + part, a.V);
   int mode = walk.mode;
   unsigned long long whole_sum = 0;  // of the plain weights (kLess)
-  auto less = [&](unsigned long long w, int v) -> unsigned long long {
-    const unsigned long long q = share(__ldg(q_row + v), whole_sum);
-    return w > q ? w - q : 0;
-  };
+  const int q_skew = q_row ? skew_of<false>(q_row) : 0;
   // The sum over the row of weights as `what` says, in every thread; warp_sum keeps the
   // parts of this CTA's warps.
   auto sum_row = [&](int what, int round) -> unsigned long long {
     unsigned long long sum = 0;
-    for (int v = v_first + lane * kVec; v < v_last; v += kBlock) {
-      float f[kVec];
-      load4<BF16>(row, v, a.V, whole, f);
+    for (int v0 = v_first + lane * kVec; v0 < v_last; v0 += kBlock * kAhead) {
+      float f[kAhead][kVec], q[kAhead][kVec];
+      load4<BF16, kAhead>(row, v0, kBlock, v_last, skew, f);
+      if (what == kLess) load4<false, kAhead>(q_row, v0, kBlock, v_last, q_skew, q);
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        const unsigned long long w = weight(f[e], scale, powers);
-        sum += what == kLess ? (v + e < a.V ? less(w, v + e) : 0) : w;
-      }
+      for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+          const unsigned long long w = weight(f[i][e], scale, powers);
+          if (what == kLess) {
+            const unsigned long long less = share(q[i][e], whole_sum);
+            sum += w > less ? w - less : 0;
+          } else {
+            sum += w;
+          }
+        }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -518,41 +586,50 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const Args a) {
   for (int r = 0; r < (int)rank; ++r) before += cta_sum[round][r];
   for (int w = 0; w < warp; ++w) before += warp_sum[w];
   if (limit < before || limit - before >= warp_sum[warp]) return;  // another warp's
-  for (int v0 = v_first; v0 < v_last; v0 += kBlock) {
-    const int v = v0 + lane * kVec;
-    unsigned long long w[kVec], mine = 0;
-    if (v < v_last) {
-      float f[kVec];
-      load4<BF16>(row, v, a.V, whole, f);
+  for (int v0 = v_first; v0 < v_last; v0 += kBlock * kAhead) {
+    float f[kAhead][kVec], q[kAhead][kVec];
+    load4<BF16, kAhead>(row, v0 + lane * kVec, kBlock, v_last, skew, f);
+    if (mode == kLess) load4<false, kAhead>(q_row, v0 + lane * kVec, kBlock, v_last, q_skew, q);
+#pragma unroll 1
+    for (int i = 0; i < kAhead; ++i) {
+      const int v = v0 + i * kBlock + lane * kVec;
+      unsigned long long w[kVec], mine = 0;
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
-        w[e] = weight(f[e], scale, powers);
-        if (mode == kLess) w[e] = v + e < a.V ? less(w[e], v + e) : 0;
+        float x = f[0][e], less = q[0][e];
+#pragma unroll
+        for (int k = 1; k < kAhead; ++k)
+          if (i == k) x = f[k][e], less = q[k][e];
+        w[e] = weight(x, scale, powers);
+        if (mode == kLess) {
+          const unsigned long long off = share(less, whole_sum);
+          w[e] = w[e] > off ? w[e] - off : 0;
+        }
         if (mode == kExcept)
-          for (int i = 0; i < walk.n_except; ++i)
-            if (except[i] == v + e) w[e] = 0;
+          for (int k = 0; k < walk.n_except; ++k)
+            if (except[k] == v + e) w[e] = 0;
         mine += w[e];
       }
-    }
-    unsigned long long upto = mine;  // of this and the lanes before it
+      unsigned long long upto = mine;  // of this and the lanes before it
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
-    }
-    const unsigned long long here = __shfl_sync(0xffffffffu, upto, 31);
-    if (limit - before < here) {
-      unsigned long long at = before + upto - mine;
-      if (mine && limit >= at && limit - at < mine) {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          if (limit >= at && limit - at < w[e]) out[place] = v + e;
-          at += w[e];
-        }
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
       }
-      return;
+      const unsigned long long here = __shfl_sync(0xffffffffu, upto, 31);
+      if (limit - before < here) {
+        unsigned long long at = before + upto - mine;
+        if (mine && limit >= at && limit - at < mine) {
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) {
+            if (limit >= at && limit - at < w[e]) out[place] = v + e;
+            at += w[e];
+          }
+        }
+        return;
+      }
+      before += here;
     }
-    before += here;
   }
 }
 
