@@ -7,6 +7,7 @@ namespace da {
 
 constexpr int kTreeTile = 64;       // entries of a tile
 constexpr int kTreeMaxSplits = 64;  // pieces of a row's list at most
+constexpr int kTreeFew = 16;        // (node, head) rows that tree_few.cu takes
 constexpr int kTreeSuper = 128;     // (node, head) rows of a unit at most
 
 // n / d for n below 2^31 by a multiplication: a unit's place is found with several
@@ -55,6 +56,7 @@ struct TreeLaunch {
 constexpr int kTreeRows = 256;  // rows of a launch at most
 
 cudaError_t launch_tree(const TreeLaunch& p, int sms, cudaStream_t stream);
+cudaError_t launch_tree_few(const TreeLaunch& p, int sms, cudaStream_t stream);
 cudaError_t launch_tree_combine(const TreeLaunch& p, cudaStream_t stream);
 
 // Tiles of a split at least, for a row of `rows` (node, head) pairs a KV head.  A split
