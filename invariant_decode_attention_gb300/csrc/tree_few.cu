@@ -9,32 +9,50 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStep = kT / kWarps;  // entries of a tile that a warp has: the M of an MMA
 
-// What a thread of a warp holds, lane 4 g + q: entries g and g + 8 of K (D / 4 dims, in
-// pieces of 16 bytes or one smaller one), entries 2 q, 2 q + 1, 2 q + 8, 2 q + 9 of V (D / 8
-// dims).
+// What a thread of a warp holds of 16 entries, lane 4 g + q: entries g and g + 8 of K (D / 4
+// dims, in pieces of 16 bytes or one smaller one), entries 2 q, 2 q + 1, 2 q + 8, 2 q + 9 of V
+// (D / 8 dims).
 template <int KT, int D, int NT>
 struct Few {
   static constexpr bool Q8 = KT != DA_KV_BF16;
   static constexpr int kRow = KT == DA_KV_BF16 ? 2 * D : KT == DA_KV_FP8_E4M3 ? D : D / 2;  // bytes of a head's row
   static constexpr int kKWords = kRow / 16, kVWords = kRow / 32;
-  static constexpr int kKPiece = kKWords < 4 ? kKWords : 4, kVPiece = kVWords < 4 ? kVWords : 4;  // words of a load
-  static constexpr int kKDims = kKPiece * 4 * D / kRow, kVDims = kVPiece * 4 * D / kRow;          // dims of a load
+  static constexpr int kKPiece = kKWords < 4 ? kKWords : 4, kVPiece = kVWords < 4 ? kVWords : 4;  // words of a copy
+  static constexpr int kKDims = kKPiece * 4 * D / kRow, kVDims = kVPiece * 4 * D / kRow;          // dims of a copy
   static constexpr int kRows = 8 * NT;
-  static constexpr int kPad = D + 4;
-  static constexpr int kOutBytes = kWarps * kRows * kPad * 4;
-  static constexpr int kResident = NT == 1 ? (Q8 || D == 64 ? 4 : 3) : 2;  // blocks an SM
+  // a warp's stage: K, V, NVFP4 block scales (a word of each of the six entries)
+  static constexpr int kVAt = kStep * kRow, kScalesAt = 2 * kVAt;
+  static constexpr int kStage = kScalesAt + (KT == DA_KV_NVFP4 ? 6 * 128 : 0);
+  static constexpr int kStages = kStage > 4096 ? 2 : kStage > 3000 ? 3 : 4;
+  static constexpr int kBytes = kWarps * kStages * kStage;
+  static constexpr int kResident = NT == 1 && kStage <= 4096 ? 4 : NT == 1 || D == 64 ? 3 : 2;  // blocks an SM
+  // rows of the output that go through a stage at once: all, those of an MMA, or every second
+  static constexpr int kPassRows = kScalesAt >= kRows * D * 4 ? kRows : kScalesAt >= 8 * D * 4 ? 8 : 4;
+  static_assert(kScalesAt >= kPassRows * D * 4, "a stage takes a pass");
+  static_assert(kResident * (kBytes + 6 * 1024) <= 228 * 1024, "resident blocks");
 };
 
-template <int W>
-__device__ __forceinline__ void load_words(const uint8_t* from, uint32_t* w) {
-  if constexpr (W == 4)
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "l"(from));
-  else if constexpr (W == 2)
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(from));
+// Copies B bytes, or zeros.
+template <int B>
+__device__ __forceinline__ void copy_or_zero(uint32_t dst, const uint8_t* src, bool there) {
+  const int n = there ? B : 0;
+  if constexpr (B == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
   else
-    asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(w[0]) : "l"(from));
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(B), "r"(n) : "memory");
+}
+
+template <int W>
+__device__ __forceinline__ void read_words(const uint8_t* from, uint32_t* w) {
+  if constexpr (W == 4) {
+    const uint4 x = *reinterpret_cast<const uint4*>(from);
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  } else if constexpr (W == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(from);
+    w[0] = x.x, w[1] = x.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(from);
+  }
 }
 
 // d += a b, 16 x 8 x 16
@@ -69,54 +87,59 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   }
 }
 
-// 16 entries of K and V, a warp's of a tile, as they lie in the cache.
+// Copies 16 entries, a warp's of a tile, to its stage: every lane what it reads itself, so
+// that nothing but its own wait stands between copy and use.  rows: lane i < 16 has entry i's
+// cache row, or -1 (zeros then).
 template <int KT, int D, int NT>
-struct Held {
+__device__ __forceinline__ void copy_step(const TreeLaunch& p, int h, int rows, uint32_t stage, int lane) {
   using F = Few<KT, D, NT>;
-  uint32_t k[2][F::kKWords], v[4][F::kVWords];
-  uint32_t ks[2], vs[4];  // NVFP4: block scales
+  const int g = lane >> 2, q = lane & 3;
+  const long long scales = p.kv_rows * p.H_kv * F::kRow;  // NVFP4's lie behind the codes
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int row = __shfl_sync(0xffffffffu, rows, g + 8 * e);
+    const bool there = row >= 0;
+    const long long at = (long long)(there ? row : 0) * p.H_kv + h;
+    const uint8_t* k = static_cast<const uint8_t*>(p.k);
+#pragma unroll
+    for (int i = 0; i < F::kKWords; i += F::kKPiece)
+      copy_or_zero<F::kKPiece * 4>(stage + (e * F::kKWords + i) * 128 + lane * (F::kKPiece * 4),
+                                   k + at * F::kRow + q * (F::kKPiece * 4) + 16 * i, there);
+    if constexpr (KT == DA_KV_NVFP4)
+      copy_or_zero<4>(stage + F::kScalesAt + e * 128 + lane * 4, k + scales + at * (D / 16) + (D == 128 ? q / 2 * 4 : 0), there);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int row = __shfl_sync(0xffffffffu, rows, 2 * q + (e & 1) + 4 * (e & 2));
+    const bool there = row >= 0;
+    const long long at = (long long)(there ? row : 0) * p.H_kv + h;
+    const uint8_t* v = static_cast<const uint8_t*>(p.v);
+#pragma unroll
+    for (int i = 0; i < F::kVWords; i += F::kVPiece)
+      copy_or_zero<F::kVPiece * 4>(stage + F::kVAt + (e * F::kVWords + i) * 128 + lane * (F::kVPiece * 4),
+                                   v + at * F::kRow + g * (F::kVPiece * 4) + 32 * i, there);
+    if constexpr (KT == DA_KV_NVFP4)
+      copy_or_zero<4>(stage + F::kScalesAt + (2 + e) * 128 + lane * 4, v + scales + at * (D / 16) + (D == 128 ? g / 4 * 4 : 0),
+                      there);
+  }
+}
 
-  // `rows`: lane half + i has entry i's cache row, or -1 (zeros then)
-  __device__ __forceinline__ void load_k(const TreeLaunch& p, int h, int rows, int half, int lane) {
-    const int q = lane & 3;
+template <int KT, int D, int NT>
+struct HeldK {
+  using F = Few<KT, D, NT>;
+  uint32_t k[2][F::kKWords], ks[2];
+
+  __device__ __forceinline__ void read(const uint8_t* stage, int lane) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int row = __shfl_sync(0xffffffffu, rows, half + (lane >> 2) + 8 * e);
 #pragma unroll
-      for (int i = 0; i < F::kKWords; ++i) k[e][i] = 0;
-      ks[e] = 0;
-      if (row < 0) continue;
-      const long long at = (long long)row * p.H_kv + h;
-      const uint8_t* from = static_cast<const uint8_t*>(p.k) + at * F::kRow + q * (F::kKPiece * 4);
-#pragma unroll
-      for (int i = 0; i < F::kKWords; i += F::kKPiece) load_words<F::kKPiece>(from + 16 * i, k[e] + i);
+      for (int i = 0; i < F::kKWords; i += F::kKPiece)
+        read_words<F::kKPiece>(stage + (e * F::kKWords + i) * 128 + lane * (F::kKPiece * 4), k[e] + i);
       if constexpr (KT == DA_KV_NVFP4) {
-        const uint8_t* s = static_cast<const uint8_t*>(p.k) + p.kv_rows * p.H_kv * F::kRow + at * (D / 16);
-        ks[e] = D == 128 ? __ldg(reinterpret_cast<const uint16_t*>(s) + q) : __ldg(s + q);
+        const int q = lane & 3;
+        ks[e] = *reinterpret_cast<const uint32_t*>(stage + F::kScalesAt + e * 128 + lane * 4) >> (D == 128 ? 16 * (q & 1) : 8 * q);
       }
     }
-    __syncwarp();
-  }
-
-  __device__ __forceinline__ void load_v(const TreeLaunch& p, int h, int rows, int half, int lane) {
-    const int g = lane >> 2;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int row = __shfl_sync(0xffffffffu, rows, half + 2 * (lane & 3) + (e & 1) + 4 * (e & 2));
-#pragma unroll
-      for (int i = 0; i < F::kVWords; ++i) v[e][i] = 0;
-      vs[e] = 0;
-      if (row < 0) continue;
-      const long long at = (long long)row * p.H_kv + h;
-      const uint8_t* from = static_cast<const uint8_t*>(p.v) + at * F::kRow + g * (F::kVPiece * 4);
-#pragma unroll
-      for (int i = 0; i < F::kVWords; i += F::kVPiece) load_words<F::kVPiece>(from + 32 * i, v[e] + i);
-      if constexpr (KT == DA_KV_NVFP4) {
-        const uint8_t* s = static_cast<const uint8_t*>(p.v) + p.kv_rows * p.H_kv * F::kRow + at * (D / 16);
-        vs[e] = __ldg(s + g * (D / 8) / 16);
-      }
-    }
-    __syncwarp();
   }
 
   // A operand of the scores, K's dims of k-step s
@@ -130,11 +153,32 @@ struct Held {
         a[e] = e4m3x2_to_f16x2(k[e][s]);
         a[2 + e] = e4m3x2_to_f16x2(k[e][s] >> 16);
       } else {
-        const uint32_t two = e4m3x2_to_f16x2(ks[e]), scale = __byte_perm(two, 0, s < 4 ? 0x1010 : 0x3232);
+        const uint32_t two = e4m3x2_to_f16x2(D == 128 ? ks[e] & 0xffff : ks[e] & 0xff), scale = __byte_perm(two, 0, s < 4 ? 0x1010 : 0x3232);
         uint32_t h[4];
         e2m1x8_to_f16x2(k[e][s / 2], h);
         a[e] = hmul2(h[2 * (s & 1)], scale);
         a[2 + e] = hmul2(h[2 * (s & 1) + 1], scale);
+      }
+    }
+  }
+
+};
+
+template <int KT, int D, int NT>
+struct HeldV {
+  using F = Few<KT, D, NT>;
+  uint32_t v[4][F::kVWords], vs[4];
+
+  __device__ __forceinline__ void read(const uint8_t* stage, int lane) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+#pragma unroll
+      for (int i = 0; i < F::kVWords; i += F::kVPiece)
+        read_words<F::kVPiece>(stage + F::kVAt + (e * F::kVWords + i) * 128 + lane * (F::kVPiece * 4), v[e] + i);
+      if constexpr (KT == DA_KV_NVFP4) {
+        const int g = lane >> 2;
+        vs[e] = *reinterpret_cast<const uint32_t*>(stage + F::kScalesAt + (2 + e) * 128 + lane * 4) >>
+                8 * (D == 128 ? g & 3 : g / 2);
       }
     }
   }
@@ -161,7 +205,7 @@ struct Held {
         uint32_t h[2][4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const uint32_t scale = __byte_perm(e4m3x2_to_f16x2(vs[2 * pair + e]), 0, 0x1010);
+          const uint32_t scale = __byte_perm(e4m3x2_to_f16x2(vs[2 * pair + e] & 0xff), 0, 0x1010);
           e2m1x8_to_f16x2(v[2 * pair + e][j4], h[e]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) h[e][j] = hmul2(h[e][j], scale);
@@ -176,13 +220,19 @@ struct Held {
   }
 };
 
+// What pairs of dims of lane (g, q) are swapped by, of kPer next to each other.
+template <int kPer>
+__device__ __forceinline__ int swap_of(int g, int q) {
+  return kPer == 8 ? (g >> 1 & 1) * 4 + q : q;
+}
+
 template <int KT, int D, int NT>
 __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident) few_kernel(const TreeLaunch p) {
   using F = Few<KT, D, NT>;
-  extern __shared__ __align__(16) float parts[];  // [kWarps][kRows][kPad]: the warps' sums
+  extern __shared__ __align__(16) uint8_t stages[];  // of warp 0, warp 1, ...
   __shared__ int2 sizes[kTreeRows];
   __shared__ int first[kTreeRows + 1];
-  __shared__ Unit units[kWarps][2];
+  __shared__ Unit units[kWarps][2];  // a warp's unit, and the one that it copies
   __shared__ unsigned long long sees[F::kRows];  // nodes that a row sees
   __shared__ int depths[F::kRows];
   __shared__ float part_m[kWarps][F::kRows], part_l[kWarps][F::kRows];
@@ -198,33 +248,55 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident) few_kerne
   c.units = first[p.rows];
   if ((int)blockIdx.x >= c.units) return;
 
+  // ---- copies run ahead of their use by kStages - 1 tiles, and lookups by one more
+  uint8_t* const mine = stages + warp * (F::kStages * F::kStage);
+  const uint32_t mine_at = smem_addr(mine);
+  Unit* const ahead = &units[warp][1];
   bool bad = false;
-  // cache rows of this warp's entries of tiles i and i + 1 of a unit, lane 16 t + e
-  auto look_up = [&](const Unit* x, int i) -> int {
-    i += lane >> 4;
-    if (i >= x->end) return -1;
-    const int j = tree_tile(x->r, i) * kT + warp * kStep + (lane & 15);
-    if (j >= x->r.end || (j >= x->r.hole_from && j < x->r.hole_to)) return -1;
-    const long long row = cache_row(p, x->b, j);
-    bad |= row < 0;
-    return (int)row;
-  };
-  const Unit first_unit = unit_of(p, c, blockIdx.x);
-  if (lane == 0) units[warp][0] = first_unit;
-  __syncwarp();
-  Held<KT, D, NT> held;
-  int rows = look_up(&units[warp][0], first_unit.begin);
-  held.load_k(p, first_unit.h, rows, 0, lane);
-  held.load_v(p, first_unit.h, rows, 0, lane);
-  for (int u = blockIdx.x, slot = 0; u < c.units; u += gridDim.x, slot ^= 1) {
-    const Unit* x = &units[warp][slot];
-    const Unit* next = &units[warp][slot ^ 1];
-    const bool more = u + (int)gridDim.x < c.units;
-    if (more) {
-      const Unit z = unit_of(p, c, u + gridDim.x);
-      if (lane == 0) units[warp][slot ^ 1] = z;
+  int ahead_u = (int)blockIdx.x - (int)gridDim.x, ahead_i = 0, ahead_end = 0, rows = -1;
+  uint32_t copied = 0;
+  // cache row of this warp's entry `lane` of the next tile to copy
+  auto look_up = [&]() {
+    if (ahead_i >= ahead_end) {
+      do {
+        ahead_u += gridDim.x;
+        if (ahead_u >= c.units) return;
+        const Unit z = unit_of(p, c, ahead_u);
+        ahead_i = z.begin;
+        ahead_end = z.end;
+        __syncwarp();
+        if (lane == 0) *ahead = z;
+        __syncwarp();
+      } while (ahead_i >= ahead_end);
     }
+    const int j = tree_tile(ahead->r, ahead_i) * kT + warp * kStep + (lane & 15);
+    rows = -1;
+    if (j < ahead->r.end && (j < ahead->r.hole_from || j >= ahead->r.hole_to)) {
+      rows = (int)cache_row(p, ahead->b, j);
+      bad |= rows < 0;
+    }
+    ++ahead_i;
     __syncwarp();
+  };
+  auto copy_next = [&]() {
+    if (ahead_u < c.units) {
+      copy_step<KT, D, NT>(p, ahead->h, rows, mine_at + copied % F::kStages * F::kStage, lane);
+      look_up();
+    }
+    ++copied;
+    cp_async_commit();
+  };
+  look_up();
+  for (int i = 0; i < F::kStages - 1; ++i) copy_next();
+  uint32_t used = 0;
+  for (int u = blockIdx.x; u < c.units; u += gridDim.x) {
+    Unit* const x = &units[warp][0];
+    {
+      const Unit z = unit_of(p, c, u);
+      __syncwarp();
+      if (lane == 0) *x = z;
+      __syncwarp();
+    }
     const int n_rows = x->rows, h = x->h, begin = x->begin, end = x->end, length = x->r.length;
     // ---- Q, and what the rows see
     uint32_t qb[NT][D / 16][2];
@@ -287,8 +359,13 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident) few_kerne
       m[nt][0] = m[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
     }
-    for (int i = begin; i < end; ++i) {
+    for (int i = begin; i < end; ++i, ++used) {
+      copy_next();
+      cp_async_wait<F::kStages - 1>();
+      const uint8_t* stage = mine + used % F::kStages * F::kStage;
       // ---- scores: entries g and g + 8, rows 8 nt + 2 q and + 1
+      HeldK<KT, D, NT> held;
+      held.read(stage, lane);
       float s[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -301,21 +378,6 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident) few_kerne
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma_16816<F::Q8>(s[nt], a, qb[nt][k][0], qb[nt][k][1]);
       }
-      // the next tile's K, and behind it the V, of this unit or the next one
-      const int odd = (i - begin) & 1;
-      const bool last = i + 1 == end;
-      int h_next = h;
-      if (last) {
-        if (more) {
-          rows = look_up(next, next->begin);
-          h_next = next->h;
-        }
-      } else if (odd) {
-        rows = look_up(x, i + 1);
-      }
-      const int half = last || odd ? 0 : 16;
-      if (!last || more) held.load_k(p, h_next, rows, half, lane);
-
       const int j0 = tree_tile(x->r, i) * kT;
       const bool all = j0 + kT <= length && (j0 >= whole || j0 + kT <= p.sinks);
       bool move = false;
@@ -381,77 +443,91 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident) few_kerne
         pb[nt][0] = transposed(pack16<F::Q8>(w[0], w[1]));
         pb[nt][1] = transposed(pack16<F::Q8>(w[2], w[3]));
       }
+      HeldV<KT, D, NT> values;
+      values.read(stage, lane);
 #pragma unroll
       for (int j4 = 0; j4 < D / 64; ++j4) {
         uint32_t a[4][4];
-        held.v_operands(j4, a);
+        values.v_operands(j4, a);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) mma_16816<F::Q8>(o[nt][4 * j4 + j], a[j], pb[nt][0], pb[nt][1]);
       }
-      if (!last || more) held.load_v(p, h_next, rows, half, lane);
     }
-    if (end == begin && more) {  // (nothing has brought in the next unit's)
-      rows = look_up(next, next->begin);
-      held.load_k(p, next->h, rows, 0, lane);
-      held.load_v(p, next->h, rows, 0, lane);
-    }
-    // ---- the warps' sums joined, in their order
-    float* mine = parts + warp * F::kRows * F::kPad;
+    // ---- the warps' sums joined, in their order, by way of each one's stage that was used last
+    // (the next copy goes there)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int at = nt * 8 + 2 * q + r;
         float sum = l[nt][r];
 #pragma unroll
         for (int b = 4; b < 32; b <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, b);
         if (g == 0) {
-          part_m[warp][at] = m[nt][r];
-          part_l[warp][at] = sum;
-        }
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          constexpr int kPer = F::kVDims / 2;  // tiles of a piece
-          const int d = (j / kPer) * (8 * F::kVDims) + g * F::kVDims + 2 * (j % kPer);
-          *reinterpret_cast<float2*>(mine + at * F::kPad + d) = make_float2(o[nt][j][r], o[nt][j][2 + r]);
+          part_m[warp][nt * 8 + 2 * q + r] = m[nt][r];
+          part_l[warp][nt * 8 + 2 * q + r] = sum;
         }
       }
-    __syncthreads();
+    const uint32_t free_at = (used + F::kStages - 1) % F::kStages * F::kStage;
     const bool single = x->r.splits == 1;
     const long long to_slot = (((long long)x->b * p.max_splits + x->split) - x->b) * p.T * p.H_q;
-    for (int i = threadIdx.x; i < n_rows * (D / 4); i += kThreads) {
-      const int at = i / (D / 4), d = 4 * (i % (D / 4));
-      float top = -INFINITY, sum = 0.f;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_m[w][at]);
+    for (int pass = 0; pass < F::kRows / F::kPassRows; ++pass) {
+      // row 8 nt + 2 q + r is row `at` of the pass; its dims in pairs, swapped so that a warp's
+      // meet in no bank
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float c_w = part_m[w][at] == top ? 1.f : ex2(part_m[w][at] - top);
-        const float4 o_w = *reinterpret_cast<const float4*>(parts + (w * F::kRows + at) * F::kPad + d);
-        sum = fmaf(part_l[w][at], c_w, sum);
-        v.x = fmaf(o_w.x, c_w, v.x);
-        v.y = fmaf(o_w.y, c_w, v.y);
-        v.z = fmaf(o_w.z, c_w, v.z);
-        v.w = fmaf(o_w.w, c_w, v.w);
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if (F::kPassRows == 8 && nt != pass) continue;
+          if (F::kPassRows == 4 && 2 * nt + r != pass) continue;
+          const int at = F::kPassRows == 4 ? q : F::kPassRows == 8 ? 2 * q + r : 8 * nt + 2 * q + r;
+          float2* to = reinterpret_cast<float2*>(mine + free_at) + at * (D / 2);
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            constexpr int kPer = F::kVDims / 2;  // tiles of a piece
+            to[((j / kPer) * 8 + g) * kPer + (j % kPer ^ swap_of<kPer>(g, q))] = make_float2(o[nt][j][r], o[nt][j][2 + r]);
+          }
+        }
+      __syncthreads();
+      for (int i = threadIdx.x; i < F::kPassRows * (D / 4); i += kThreads) {
+        const int in = i / (D / 4), d = 4 * (i % (D / 4));
+        const int at = F::kPassRows == 4 ? 8 * (pass / 2) + 2 * in + pass % 2 : F::kPassRows == 8 ? 8 * pass + in : in;
+        if (at >= n_rows) continue;
+        constexpr int kPer = F::kVDims / 2;
+        const int pair = d / 2, swap = swap_of<kPer>(pair / kPer % 8, at % 8 / 2);
+        float top = -INFINITY, sum = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_m[w][at]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float c_w = part_m[w][at] == top ? 1.f : ex2(part_m[w][at] - top);
+          const float2* from = reinterpret_cast<const float2*>(stages + w * (F::kStages * F::kStage) + free_at) + in * (D / 2);
+          const float2 o0 = from[pair ^ swap], o1 = from[(pair + 1) ^ swap];
+          sum = fmaf(part_l[w][at], c_w, sum);
+          v.x = fmaf(o0.x, c_w, v.x);
+          v.y = fmaf(o0.y, c_w, v.y);
+          v.z = fmaf(o1.x, c_w, v.z);
+          v.w = fmaf(o1.y, c_w, v.w);
+        }
+        const float inv = (sum > 0.f ? 1.f / sum : sum != sum ? sum : 0.f) * p.v_scale;
+        v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+        const int t = quotient(at, p.by_group);
+        const size_t row = (size_t)((long long)x->b * p.T + t) * p.H_q + h * p.G + (at - t * p.G);
+        if (sum != sum || !(fabsf(v.x) + fabsf(v.y) + fabsf(v.z) + fabsf(v.w) < INFINITY)) atomicOr(&odd_rows, 1u << at);
+        const float lse = sum > 0.f || sum != sum ? top + lg2(sum) : -INFINITY;
+        if (single) {
+          *reinterpret_cast<uint2*>(p.out + row * D + d) = make_uint2(pack16<false>(v.x, v.y), pack16<false>(v.z, v.w));
+          if (d == 0) p.lse[row] = lse * kLn2;
+        } else {
+          *reinterpret_cast<float4*>(p.o_part + (to_slot + (long long)row) * D + d) = v;
+          if (d == 0) p.lse_part[to_slot + (long long)row] = lse;
+        }
       }
-      const float inv = (sum > 0.f ? 1.f / sum : sum != sum ? sum : 0.f) * p.v_scale;
-      v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-      const int t = quotient(at, p.by_group);
-      const size_t row = (size_t)((long long)x->b * p.T + t) * p.H_q + h * p.G + (at - t * p.G);
-      if (sum != sum || !(fabsf(v.x) + fabsf(v.y) + fabsf(v.z) + fabsf(v.w) < INFINITY)) atomicOr(&odd_rows, 1u << at);
-      const float lse = sum > 0.f || sum != sum ? top + lg2(sum) : -INFINITY;
-      if (single) {
-        *reinterpret_cast<uint2*>(p.out + row * D + d) = make_uint2(pack16<false>(v.x, v.y), pack16<false>(v.z, v.w));
-        if (d == 0) p.lse[row] = lse * kLn2;
-      } else {
-        *reinterpret_cast<float4*>(p.o_part + (to_slot + (long long)row) * D + d) = v;
-        if (d == 0) p.lse_part[to_slot + (long long)row] = lse;
-      }
+      __syncthreads();
     }
-    __syncthreads();
     // rows that something infinite or NaN has spoiled: formed again, entry by entry
     uint32_t again = odd_rows;
     for (int n = 0; again; again &= again - 1, ++n) {
@@ -477,8 +553,9 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident) few_kerne
           p.lse_part[to_slot + (long long)row] = lse2;
       }
     }
-    __syncthreads();  // (odd_rows, sees and parts are the next unit's now)
+    __syncthreads();  // (odd_rows and sees are the next unit's now)
   }
+  cp_async_wait<0>();
   if (__any_sync(0xffffffffu, bad) && lane == 0) report(p.err, DA_DEVERR_INDEX);
 }
 
@@ -486,7 +563,7 @@ template <int KT, int D, int NT>
 cudaError_t launch_shape(const TreeLaunch& p0, int sms, cudaStream_t stream) {
   using F = Few<KT, D, NT>;
   static const cudaError_t attr =
-      cudaFuncSetAttribute(few_kernel<KT, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kOutBytes);
+      cudaFuncSetAttribute(few_kernel<KT, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kBytes);
   if (attr != cudaSuccess) return attr;
   TreeLaunch p = p0;
   p.by_heads = fast_div(p.H_kv);
@@ -496,7 +573,7 @@ cudaError_t launch_shape(const TreeLaunch& p0, int sms, cudaStream_t stream) {
     p.rows = p.B - p.row0 < kTreeRows ? p.B - p.row0 : kTreeRows;
     const long long most = (long long)p.rows * p.max_splits * p.H_kv, room = (long long)F::kResident * sms;
     const cudaError_t e = launch_after(few_kernel<KT, D, NT>, dim3((unsigned)(most < room ? most : room)), dim3(kThreads),
-                                       (size_t)F::kOutBytes, stream, p);
+                                       (size_t)F::kBytes, stream, p);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
