@@ -9,9 +9,9 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStep = kT / kWarps;  // entries of a tile that a warp has: the M of an MMA
 
-// What a thread of a warp holds of 16 entries, lane 4 g + q: entries g and g + 8 of K (D / 4
-// dims, in pieces of 16 bytes or one smaller one), entries 2 q, 2 q + 1, 2 q + 8, 2 q + 9 of V
-// (D / 8 dims).
+// What a thread of a warp reads of 16 entries, lane 4 g + q: entries g and g + 8 of K (D / 4
+// dims, in chunks of 16 bytes or half a one), entries 2 q, 2 q + 1, 2 q + 8, 2 q + 9 of V (D / 8
+// dims).
 template <int KT, int D, int NT>
 struct Few {
   static constexpr bool Q8 = KT != DA_KV_BF16;
@@ -20,9 +20,11 @@ struct Few {
   static constexpr int kKPiece = kKWords < 4 ? kKWords : 4, kVPiece = kVWords < 4 ? kVWords : 4;  // words of a copy
   static constexpr int kKDims = kKPiece * 4 * D / kRow, kVDims = kVPiece * 4 * D / kRow;          // dims of a copy
   static constexpr int kRows = 8 * NT;
-  // a warp's stage: K, V, NVFP4 block scales (a word of each of the six entries)
+  // chunk of a row that is lane q's P-th of K: a phase of a read has two rows' even or odd ones
+  static __device__ __forceinline__ int k_chunk(int q, int P) { return kRow >= 128 ? 2 * q + P % 2 + P / 2 * 8 : q; }
+  // a warp's stage: K, V, NVFP4 block scales
   static constexpr int kVAt = kStep * kRow, kScalesAt = 2 * kVAt;
-  static constexpr int kStage = kScalesAt + (KT == DA_KV_NVFP4 ? 6 * 128 : 0);
+  static constexpr int kStage = kScalesAt + (KT == DA_KV_NVFP4 ? 2 * kStep * (D / 16) : 0);
   static constexpr int kStages = kStage > 4096 ? 2 : kStage > 3000 ? 3 : 4;
   static constexpr int kBytes = kWarps * kStages * kStage;
   static constexpr int kResident = NT == 1 && kStage <= 4096 ? 4 : NT == 1 || D == 64 ? 3 : 2;  // blocks an SM
@@ -33,13 +35,20 @@ struct Few {
 };
 
 // Copies B bytes, or zeros.
-template <int B>
+template <int B, bool ALL>
 __device__ __forceinline__ void copy_or_zero(uint32_t dst, const uint8_t* src, bool there) {
-  const int n = there ? B : 0;
-  if constexpr (B == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(B), "r"(n) : "memory");
+  if constexpr (ALL) {
+    if constexpr (B == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(B) : "memory");
+  } else {
+    const int n = there ? B : 0;
+    if constexpr (B == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(B), "r"(n) : "memory");
+  }
 }
 
 template <int W>
@@ -87,40 +96,36 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   }
 }
 
-// Copies 16 entries, a warp's of a tile, to its stage: every lane what it reads itself, so
-// that nothing but its own wait stands between copy and use.  rows: lane i < 16 has entry i's
-// cache row, or -1 (zeros then).
-template <int KT, int D, int NT>
-__device__ __forceinline__ void copy_step(const TreeLaunch& p, int h, int rows, uint32_t stage, int lane) {
+// 16-byte chunk `ch` of entry `row` in a stage, in an order in which a warp's reads spread
+// over the banks.
+template <int R>  // chunks of a row
+__device__ __forceinline__ uint32_t chunk_at(int row, int ch) {
+  return (row * R + (ch ^ (R >= 8 ? row & 7 : R == 4 ? row >> 1 & 3 : row >> 2 & 1))) * 16;
+}
+
+// Copies 16 entries, a warp's of a tile, to its stage, whole rows at a time: a copy costs the
+// SM by the 128-byte lines that it touches.  spots: lane `at` + i has entry i's (cache row,
+// head), or -1 (zeros then); ALL: there is no -1.
+template <int KT, int D, int NT, bool ALL>
+__device__ __forceinline__ void copy_step(const TreeLaunch& p, long long scales, int spots, int at, uint32_t dst, int lane) {
   using F = Few<KT, D, NT>;
-  const int g = lane >> 2, q = lane & 3;
-  const long long scales = p.kv_rows * p.H_kv * F::kRow;  // NVFP4's lie behind the codes
+  constexpr int R = F::kRow / 16;
+  const uint8_t* const k = static_cast<const uint8_t*>(p.k) + lane % R * 16;
+  const uint8_t* const v = static_cast<const uint8_t*>(p.v) + lane % R * 16;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int row = __shfl_sync(0xffffffffu, rows, g + 8 * e);
-    const bool there = row >= 0;
-    const long long at = (long long)(there ? row : 0) * p.H_kv + h;
-    const uint8_t* k = static_cast<const uint8_t*>(p.k);
-#pragma unroll
-    for (int i = 0; i < F::kKWords; i += F::kKPiece)
-      copy_or_zero<F::kKPiece * 4>(stage + (e * F::kKWords + i) * 128 + lane * (F::kKPiece * 4),
-                                   k + at * F::kRow + q * (F::kKPiece * 4) + 16 * i, there);
-    if constexpr (KT == DA_KV_NVFP4)
-      copy_or_zero<4>(stage + F::kScalesAt + e * 128 + lane * 4, k + scales + at * (D / 16) + (D == 128 ? q / 2 * 4 : 0), there);
+  for (int i = 0; i < kStep * R / 32; ++i) {
+    const int row = i * (32 / R) + lane / R;
+    const int spot = __shfl_sync(0xffffffffu, spots, at + row);
+    const unsigned long long off = (unsigned long long)(uint32_t)(ALL ? spot : max(spot, 0)) * F::kRow;
+    const uint32_t to = dst + chunk_at<R>(row, lane % R);
+    copy_or_zero<16, ALL>(to, k + off, spot >= 0);
+    copy_or_zero<16, ALL>(to + F::kVAt, v + off, spot >= 0);
   }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int row = __shfl_sync(0xffffffffu, rows, 2 * q + (e & 1) + 4 * (e & 2));
-    const bool there = row >= 0;
-    const long long at = (long long)(there ? row : 0) * p.H_kv + h;
-    const uint8_t* v = static_cast<const uint8_t*>(p.v);
-#pragma unroll
-    for (int i = 0; i < F::kVWords; i += F::kVPiece)
-      copy_or_zero<F::kVPiece * 4>(stage + F::kVAt + (e * F::kVWords + i) * 128 + lane * (F::kVPiece * 4),
-                                   v + at * F::kRow + g * (F::kVPiece * 4) + 32 * i, there);
-    if constexpr (KT == DA_KV_NVFP4)
-      copy_or_zero<4>(stage + F::kScalesAt + (2 + e) * 128 + lane * 4, v + scales + at * (D / 16) + (D == 128 ? g / 4 * 4 : 0),
-                      there);
+  if constexpr (KT == DA_KV_NVFP4) {  // a row's block scales: K's by lanes 0 to 15, V's by the others
+    const int spot = __shfl_sync(0xffffffffu, spots, at + (lane & 15));
+    const uint8_t* from = static_cast<const uint8_t*>(lane < 16 ? p.k : p.v) + scales +
+                          (unsigned long long)(uint32_t)(ALL ? spot : max(spot, 0)) * (D / 16);
+    copy_or_zero<D / 16, ALL>(dst + F::kScalesAt + lane * (D / 16), from, spot >= 0);
   }
 }
 
@@ -130,14 +135,18 @@ struct HeldK {
   uint32_t k[2][F::kKWords], ks[2];
 
   __device__ __forceinline__ void read(const uint8_t* stage, int lane) {
+    const int g = lane >> 2, q = lane & 3;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
+      const int row = g + 8 * e;
 #pragma unroll
       for (int i = 0; i < F::kKWords; i += F::kKPiece)
-        read_words<F::kKPiece>(stage + (e * F::kKWords + i) * 128 + lane * (F::kKPiece * 4), k[e] + i);
+        read_words<F::kKPiece>(F::kKPiece == 4 ? stage + chunk_at<F::kRow / 16>(row, F::k_chunk(q, i / 4))
+                                               : stage + chunk_at<F::kRow / 16>(row, q / 2) + 8 * (q & 1),
+                               k[e] + i);
       if constexpr (KT == DA_KV_NVFP4) {
-        const int q = lane & 3;
-        ks[e] = *reinterpret_cast<const uint32_t*>(stage + F::kScalesAt + e * 128 + lane * 4) >> (D == 128 ? 16 * (q & 1) : 8 * q);
+        const uint8_t* s = stage + F::kScalesAt + row * (D / 16);
+        ks[e] = D == 128 ? reinterpret_cast<const uint16_t*>(s)[q] : s[q];
       }
     }
   }
@@ -153,7 +162,7 @@ struct HeldK {
         a[e] = e4m3x2_to_f16x2(k[e][s]);
         a[2 + e] = e4m3x2_to_f16x2(k[e][s] >> 16);
       } else {
-        const uint32_t two = e4m3x2_to_f16x2(D == 128 ? ks[e] & 0xffff : ks[e] & 0xff), scale = __byte_perm(two, 0, s < 4 ? 0x1010 : 0x3232);
+        const uint32_t two = e4m3x2_to_f16x2(ks[e]), scale = __byte_perm(two, 0, s < 4 ? 0x1010 : 0x3232);
         uint32_t h[4];
         e2m1x8_to_f16x2(k[e][s / 2], h);
         a[e] = hmul2(h[2 * (s & 1)], scale);
@@ -170,16 +179,16 @@ struct HeldV {
   uint32_t v[4][F::kVWords], vs[4];
 
   __device__ __forceinline__ void read(const uint8_t* stage, int lane) {
+    const int g = lane >> 2, q = lane & 3;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
+      const int row = 2 * q + (e & 1) + 4 * (e & 2);
 #pragma unroll
-      for (int i = 0; i < F::kVWords; i += F::kVPiece)
-        read_words<F::kVPiece>(stage + F::kVAt + (e * F::kVWords + i) * 128 + lane * (F::kVPiece * 4), v[e] + i);
-      if constexpr (KT == DA_KV_NVFP4) {
-        const int g = lane >> 2;
-        vs[e] = *reinterpret_cast<const uint32_t*>(stage + F::kScalesAt + (2 + e) * 128 + lane * 4) >>
-                8 * (D == 128 ? g & 3 : g / 2);
+      for (int i = 0; i < F::kVWords; i += F::kVPiece) {
+        const int byte = g * (F::kVPiece * 4) + 32 * i;  // of the row
+        read_words<F::kVPiece>(stage + F::kVAt + chunk_at<F::kRow / 16>(row, byte / 16) + byte % 16, v[e] + i);
       }
+      if constexpr (KT == DA_KV_NVFP4) vs[e] = stage[F::kScalesAt + (kStep + row) * (D / 16) + g * (D / 8) / 16];
     }
   }
 
@@ -205,7 +214,7 @@ struct HeldV {
         uint32_t h[2][4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const uint32_t scale = __byte_perm(e4m3x2_to_f16x2(vs[2 * pair + e] & 0xff), 0, 0x1010);
+          const uint32_t scale = __byte_perm(e4m3x2_to_f16x2(vs[2 * pair + e]), 0, 0x1010);
           e2m1x8_to_f16x2(v[2 * pair + e][j4], h[e]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) h[e][j] = hmul2(h[e][j], scale);
@@ -248,47 +257,64 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident) few_kerne
   c.units = first[p.rows];
   if ((int)blockIdx.x >= c.units) return;
 
-  // ---- copies run ahead of their use by kStages - 1 tiles, and lookups by one more
+  // ---- copies run ahead of their use by kStages - 1 tiles, lookups by two more
   uint8_t* const mine = stages + warp * (F::kStages * F::kStage);
   const uint32_t mine_at = smem_addr(mine);
   Unit* const ahead = &units[warp][1];
+  const long long scales = p.kv_rows * p.H_kv * F::kRow;  // NVFP4's lie behind the codes
   bool bad = false;
-  int ahead_u = (int)blockIdx.x - (int)gridDim.x, ahead_i = 0, ahead_end = 0, rows = -1;
-  uint32_t copied = 0;
-  // cache row of this warp's entry `lane` of the next tile to copy
+  int ahead_u = (int)blockIdx.x - (int)gridDim.x, ahead_i = 0, ahead_end = 0;
+  int spots = -1, next_spots = -1;  // of two tiles' entries (lanes 0 to 15, 16 to 31), and the two behind them
+  int tiles = 0, next_tiles = 0, half = 0;
+  uint32_t to_stage = 0;
   auto look_up = [&]() {
-    if (ahead_i >= ahead_end) {
-      do {
-        ahead_u += gridDim.x;
-        if (ahead_u >= c.units) return;
-        const Unit z = unit_of(p, c, ahead_u);
-        ahead_i = z.begin;
-        ahead_end = z.end;
-        __syncwarp();
-        if (lane == 0) *ahead = z;
-        __syncwarp();
-      } while (ahead_i >= ahead_end);
+    next_tiles = 0;
+    while (ahead_i >= ahead_end) {
+      ahead_u += gridDim.x;
+      if (ahead_u >= c.units) return;
+      const Unit z = unit_of(p, c, ahead_u);
+      ahead_i = z.begin;
+      ahead_end = z.end;
+      __syncwarp();
+      if (lane == 0) *ahead = z;
+      __syncwarp();
     }
-    const int j = tree_tile(ahead->r, ahead_i) * kT + warp * kStep + (lane & 15);
-    rows = -1;
-    if (j < ahead->r.end && (j < ahead->r.hole_from || j >= ahead->r.hole_to)) {
-      rows = (int)cache_row(p, ahead->b, j);
-      bad |= rows < 0;
+    const int i = ahead_i + (lane >> 4);
+    next_spots = -1;
+    if (i < ahead_end) {
+      const int j = tree_tile(ahead->r, i) * kT + warp * kStep + (lane & 15);
+      if (j < ahead->r.end && (j < ahead->r.hole_from || j >= ahead->r.hole_to)) {
+        const int row = (int)cache_row(p, ahead->b, j);
+        next_spots = row < 0 ? -1 : row * p.H_kv + ahead->h;
+        bad |= row < 0;
+      }
     }
-    ++ahead_i;
+    next_tiles = min(2, ahead_end - ahead_i);
+    ahead_i += 2;
     __syncwarp();
   };
+  auto take_lookup = [&]() {
+    spots = next_spots;
+    tiles = next_tiles;
+    half = 0;
+    if (tiles > 0) look_up();
+  };
   auto copy_next = [&]() {
-    if (ahead_u < c.units) {
-      copy_step<KT, D, NT>(p, ahead->h, rows, mine_at + copied % F::kStages * F::kStage, lane);
-      look_up();
+    if (tiles > 0) {
+      if (__all_sync(0xffffffffu, spots >= 0))
+        copy_step<KT, D, NT, true>(p, scales, spots, half, mine_at + to_stage, lane);
+      else
+        copy_step<KT, D, NT, false>(p, scales, spots, half, mine_at + to_stage, lane);
+      half = 16;
+      if (--tiles == 0) take_lookup();
     }
-    ++copied;
+    to_stage = to_stage == (F::kStages - 1) * F::kStage ? 0 : to_stage + F::kStage;
     cp_async_commit();
   };
   look_up();
+  take_lookup();
   for (int i = 0; i < F::kStages - 1; ++i) copy_next();
-  uint32_t used = 0;
+  uint32_t at_stage = 0, free_at = (F::kStages - 1) * F::kStage;  // the stage in use, and the one before it
   for (int u = blockIdx.x; u < c.units; u += gridDim.x) {
     Unit* const x = &units[warp][0];
     {
@@ -311,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident) few_kerne
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) {
         constexpr int kPer = F::kKDims / 4;  // k-steps of a piece
-        const int d = (s / kPer) * (4 * F::kKDims) + q * F::kKDims + 4 * (s % kPer);
+        const int d = F::k_chunk(q, s / kPer) * F::kKDims + 4 * (s % kPer);
         const uint2 w = live ? __ldg(reinterpret_cast<const uint2*>(from + d)) : make_uint2(0, 0);
         qb[nt][s][0] = w.x;
         qb[nt][s][1] = w.y;
@@ -359,25 +385,35 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident) few_kerne
       m[nt][0] = m[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
     }
-    for (int i = begin; i < end; ++i, ++used) {
-      copy_next();
-      cp_async_wait<F::kStages - 1>();
-      const uint8_t* stage = mine + used % F::kStages * F::kStage;
-      // ---- scores: entries g and g + 8, rows 8 nt + 2 q and + 1
+    for (int i = begin; i < end; ++i) {
+      cp_async_wait<F::kStages - 2>();
+      __syncwarp();
+      const uint8_t* stage = mine + at_stage;
       HeldK<KT, D, NT> held;
       held.read(stage, lane);
-      float s[NT][4];
+      copy_next();  // to the stage of the step before
+      free_at = at_stage;
+      at_stage = at_stage == (F::kStages - 1) * F::kStage ? 0 : at_stage + F::kStage;
+      // ---- scores: entries g and g + 8, rows 8 nt + 2 q and + 1; two sums, as an MMA waits long
+      // for the one before it
+      float s[NT][4], s_odd[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+        for (int e = 0; e < 4; ++e) s[nt][e] = s_odd[nt][e] = 0.f;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         uint32_t a[4];
         held.k_operand(k, a);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_16816<F::Q8>(s[nt], a, qb[nt][k][0], qb[nt][k][1]);
+        for (int nt = 0; nt < NT; ++nt) mma_16816<F::Q8>(k & 1 ? s_odd[nt] : s[nt], a, qb[nt][k][0], qb[nt][k][1]);
       }
+      HeldV<KT, D, NT> values;
+      values.read(stage, lane);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][e] += s_odd[nt][e];
       const int j0 = tree_tile(x->r, i) * kT;
       const bool all = j0 + kT <= length && (j0 >= whole || j0 + kT <= p.sinks);
       bool move = false;
@@ -443,8 +479,6 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident) few_kerne
         pb[nt][0] = transposed(pack16<F::Q8>(w[0], w[1]));
         pb[nt][1] = transposed(pack16<F::Q8>(w[2], w[3]));
       }
-      HeldV<KT, D, NT> values;
-      values.read(stage, lane);
 #pragma unroll
       for (int j4 = 0; j4 < D / 64; ++j4) {
         uint32_t a[4][4];
@@ -469,7 +503,6 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident) few_kerne
           part_l[warp][nt * 8 + 2 * q + r] = sum;
         }
       }
-    const uint32_t free_at = (used + F::kStages - 1) % F::kStages * F::kStage;
     const bool single = x->r.splits == 1;
     const long long to_slot = (((long long)x->b * p.max_splits + x->split) - x->b) * p.T * p.H_q;
 #pragma unroll
