@@ -1,6 +1,5 @@
 // Attention of a tree of drafted tokens over the caches: every node of a row attends
 // to the row's context and to its own ancestors.
-#include <cuda.h>
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -11,6 +10,33 @@
 #include "tree_parts.cuh"
 
 namespace da {
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+}  // namespace
+
+bool tree_tensor_map(CUtensorMap* tm, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                     const cuuint32_t* box, bool bytes, CUtensorMapSwizzle swizzle) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn) return false;
+  const cuuint32_t elem[3] = {1, 1, 1};
+  return fn(tm, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+            const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 // ------------------------------------------------------------------ shapes
@@ -112,20 +138,7 @@ __device__ __forceinline__ void st_16(uint32_t taddr, const uint32_t (&r)[16]) {
       : "memory");
 }
 
-__device__ __forceinline__ void fence_proxy_async() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
 // ------------------------------------------------------------------ copies
-
-__device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap* tm, int c0, int c1, int c2,
-                                         uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-      : "memory");
-}
 
 __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* tm, int col, const int (&r)[4],
                                             uint32_t bar) {
@@ -882,29 +895,6 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
 // Stands in for an empty cache in a tensor map (nothing of it is used).
 __device__ __align__(128) __nv_bfloat16 g_nothing[128];
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }();
-  return fn;
-}
-
-bool encode(CUtensorMap* tm, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-            const cuuint32_t* box, bool bytes) {
-  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
-  if (!fn) return false;
-  const cuuint32_t elem[3] = {1, 1, 1};
-  return fn(tm, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
-            const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int KT, int D>
 cudaError_t launch_shape(const TreeLaunch& p0, int sms, cudaStream_t stream) {
   using L = Lay<KT, D>;
@@ -930,17 +920,18 @@ cudaError_t launch_shape(const TreeLaunch& p0, int sms, cudaStream_t stream) {
   }
   const cuuint64_t row = L::Q8 ? L::kCodeRow : D, size = L::Q8 ? 1 : 2;
   const cuuint32_t across = L::Q8 ? L::kCodeRow : 64;
+  const CUtensorMapSwizzle swizzle = L::Q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
   Maps m;
   std::memset(&m, 0, sizeof(m));
   if (box) {
     const cuuint64_t dims[3] = {row, heads, rows}, strides[2] = {row * size, heads * row * size};
     const cuuint32_t bx[3] = {across, 1, (cuuint32_t)box};
-    if (!encode(&m.k3, k, 3, dims, strides, bx, L::Q8) || !encode(&m.v3, v, 3, dims, strides, bx, L::Q8))
+    if (!tree_tensor_map(&m.k3, k, 3, dims, strides, bx, L::Q8, swizzle) || !tree_tensor_map(&m.v3, v, 3, dims, strides, bx, L::Q8, swizzle))
       return cudaErrorInvalidValue;
   } else {
     const cuuint64_t dims[2] = {row, rows * heads}, strides[1] = {row * size};
     const cuuint32_t bx[2] = {across, 1};
-    if (!encode(&m.k2, k, 2, dims, strides, bx, L::Q8) || !encode(&m.v2, v, 2, dims, strides, bx, L::Q8))
+    if (!tree_tensor_map(&m.k2, k, 2, dims, strides, bx, L::Q8, swizzle) || !tree_tensor_map(&m.v2, v, 2, dims, strides, bx, L::Q8, swizzle))
       return cudaErrorInvalidValue;
   }
   const int supers = (p.T * p.G + kTreeSuper - 1) / kTreeSuper;
@@ -965,7 +956,7 @@ cudaError_t launch_kt(const TreeLaunch& p, int sms, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_tree(const TreeLaunch& p, int sms, cudaStream_t stream) {
-  if (p.T * p.G <= kTreeFew && !p.test_stall) return launch_tree_few(p, sms, stream);
+  if (p.T * p.G <= kTreeFew) return launch_tree_few(p, sms, stream);
   switch (p.kv_type) {
     case DA_KV_FP8_E4M3: return launch_kt<DA_KV_FP8_E4M3>(p, sms, stream);
     case DA_KV_NVFP4: return launch_kt<DA_KV_NVFP4>(p, sms, stream);

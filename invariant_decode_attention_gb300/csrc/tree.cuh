@@ -1,6 +1,8 @@
 // Launch descriptor and row geometry of the tree attention (tree.cu).
 #pragma once
 
+#include <cuda.h>
+
 #include "common.cuh"
 
 namespace da {
@@ -54,6 +56,10 @@ struct TreeLaunch {
 };
 
 constexpr int kTreeRows = 256;  // rows of a launch at most
+
+// A tensor map of bytes or bf16 (rank 2 or 3); false if the driver has none.
+bool tree_tensor_map(CUtensorMap* tm, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                     const cuuint32_t* box, bool bytes, CUtensorMapSwizzle swizzle);
 
 cudaError_t launch_tree(const TreeLaunch& p, int sms, cudaStream_t stream);
 cudaError_t launch_tree_few(const TreeLaunch& p, int sms, cudaStream_t stream);

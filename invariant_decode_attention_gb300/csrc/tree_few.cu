@@ -1,5 +1,7 @@
 // Tree attention of few (node, head) rows a KV head: a plain decode step's, or a short
 // chain's with small groups.
+#include <cstring>
+
 #include "tree_parts.cuh"
 
 namespace da {
@@ -24,9 +26,10 @@ struct Few {
   static __device__ __forceinline__ int k_chunk(int q, int P) { return kRow >= 128 ? 2 * q + P % 2 + P / 2 * 8 : q; }
   // a warp's stage: K, V, NVFP4 block scales
   static constexpr int kVAt = kStep * kRow, kScalesAt = 2 * kVAt;
-  static constexpr int kStage = kScalesAt + (KT == DA_KV_NVFP4 ? 2 * kStep * (D / 16) : 0);
+  static constexpr int kAlign = kRow >= 128 ? 1024 : kRow == 64 ? 512 : 256;  // as the swizzles need it
+  static constexpr int kStage = (kScalesAt + (KT == DA_KV_NVFP4 ? 2 * kStep * (D / 16) : 0) + kAlign - 1) / kAlign * kAlign;
   static constexpr int kStages = kStage > 4096 ? 2 : kStage > 3000 ? 3 : 4;
-  static constexpr int kBytes = kWarps * kStages * kStage;
+  static constexpr int kBytes = kWarps * kStages * kStage + 1024;  // (1024: to align them)
   static constexpr int kResident = NT == 1 && kStage <= 4096 ? 4 : NT == 1 || D == 64 ? 3 : 2;  // blocks an SM
   // rows of the output that go through a stage at once: all, those of an MMA, or every second
   static constexpr int kPassRows = kScalesAt >= kRows * D * 4 ? kRows : kScalesAt >= 8 * D * 4 ? 8 : 4;
@@ -96,18 +99,23 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   }
 }
 
+struct FewMaps {
+  CUtensorMap k, v;  // [entries][H_kv][row], boxes of 16 entries of a head (of 128 bytes at most)
+};
+
 // 16-byte chunk `ch` of entry `row` in a stage, in an order in which a warp's reads spread
-// over the banks.
+// over the banks: the TMA's, 128, 64 or 32 bytes wide.
 template <int R>  // chunks of a row
 __device__ __forceinline__ uint32_t chunk_at(int row, int ch) {
-  return (row * R + (ch ^ (R >= 8 ? row & 7 : R == 4 ? row >> 1 & 3 : row >> 2 & 1))) * 16;
+  if constexpr (R == 16) return (ch >> 3) * (kStep * 128) + row * 128 + ((ch & 7) ^ (row & 7)) * 16;
+  return (row * R + (ch ^ (R == 8 ? row & 7 : R == 4 ? row >> 1 & 3 : row >> 2 & 1))) * 16;
 }
 
 // Copies 16 entries, a warp's of a tile, to its stage, whole rows at a time: a copy costs the
 // SM by the 128-byte lines that it touches.  spots: lane `at` + i has entry i's (cache row,
 // head), or -1 (zeros then); ALL: there is no -1.
 template <int KT, int D, int NT, bool ALL>
-__device__ __forceinline__ void copy_step(const TreeLaunch& p, long long scales, int spots, int at, uint32_t dst, int lane) {
+__device__ __forceinline__ void copy_rows(const TreeLaunch& p, int spots, int at, uint32_t dst, int lane) {
   using F = Few<KT, D, NT>;
   constexpr int R = F::kRow / 16;
   const uint8_t* const k = static_cast<const uint8_t*>(p.k) + lane % R * 16;
@@ -121,12 +129,15 @@ __device__ __forceinline__ void copy_step(const TreeLaunch& p, long long scales,
     copy_or_zero<16, ALL>(to, k + off, spot >= 0);
     copy_or_zero<16, ALL>(to + F::kVAt, v + off, spot >= 0);
   }
-  if constexpr (KT == DA_KV_NVFP4) {  // a row's block scales: K's by lanes 0 to 15, V's by the others
-    const int spot = __shfl_sync(0xffffffffu, spots, at + (lane & 15));
-    const uint8_t* from = static_cast<const uint8_t*>(lane < 16 ? p.k : p.v) + scales +
-                          (unsigned long long)(uint32_t)(ALL ? spot : max(spot, 0)) * (D / 16);
-    copy_or_zero<D / 16, ALL>(dst + F::kScalesAt + lane * (D / 16), from, spot >= 0);
-  }
+}
+
+// NVFP4: the rows' block scales, K's by lanes 0 to 15, V's by the others.
+template <int D>
+__device__ __forceinline__ void copy_scales(const TreeLaunch& p, int spots, int at, uint32_t dst, int lane) {
+  const int spot = __shfl_sync(0xffffffffu, spots, at + (lane & 15));
+  const uint8_t* from = static_cast<const uint8_t*>(lane < 16 ? p.k : p.v) + p.kv_rows * p.H_kv * (D / 2) +
+                        (unsigned long long)(uint32_t)max(spot, 0) * (D / 16);
+  copy_or_zero<D / 16, false>(dst + lane * (D / 16), from, spot >= 0);
 }
 
 template <int KT, int D, int NT>
@@ -236,9 +247,12 @@ __device__ __forceinline__ int swap_of(int g, int q) {
 }
 
 template <int KT, int D, int NT>
-__global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident) few_kernel(const TreeLaunch p) {
+__global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
+    few_kernel(const TreeLaunch p, const __grid_constant__ FewMaps maps, int boxes) {
   using F = Few<KT, D, NT>;
-  extern __shared__ __align__(16) uint8_t stages[];  // of warp 0, warp 1, ...
+  extern __shared__ uint8_t smem[];
+  uint8_t* const stages = smem + (-smem_addr(smem) & 1023u);  // of warp 0, warp 1, ...
+  __shared__ uint64_t bars[kWarps * F::kStages + 1];           // of the TMA's copies; one that nothing arrives at
   __shared__ int2 sizes[kTreeRows];
   __shared__ int first[kTreeRows + 1];
   __shared__ Unit units[kWarps][2];  // a warp's unit, and the one that it copies
@@ -247,6 +261,10 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident) few_kerne
   __shared__ float part_m[kWarps][F::kRows], part_l[kWarps][F::kRows];
   __shared__ uint32_t odd_rows;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i <= kWarps * F::kStages; ++i) mbar_init(smem_addr(bars + i), 1);
+    fence_mbar_init();
+  }
   wait_prior_grid();
   allow_next_grid();
   count_units(p, sizes, first, kThreads);
@@ -256,17 +274,26 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident) few_kerne
   c.first = first;
   c.units = first[p.rows];
   if ((int)blockIdx.x >= c.units) return;
+  if (p.test_stall) {  // the time-out's test: a wait that runs out
+    const unsigned long long t0 = globaltimer_ns();
+    while (!mbar_try_wait(smem_addr(bars + kWarps * F::kStages), 0) && globaltimer_ns() - t0 < kTestStallNs) {
+    }
+    if (threadIdx.x == 0) report(p.err, DA_DEVERR_TIMEOUT);
+    return;
+  }
 
   // ---- copies run ahead of their use by kStages - 1 tiles, lookups by two more
   uint8_t* const mine = stages + warp * (F::kStages * F::kStage);
   const uint32_t mine_at = smem_addr(mine);
   Unit* const ahead = &units[warp][1];
-  const long long scales = p.kv_rows * p.H_kv * F::kRow;  // NVFP4's lie behind the codes
+  const uint32_t full = smem_addr(bars + warp * F::kStages);
+  uint32_t by_tma = 0, parity = 0;  // bits of the stages: what fills them, the phase to wait for
+  bool dead = false;                // a wait ran out
   bool bad = false;
   int ahead_u = (int)blockIdx.x - (int)gridDim.x, ahead_i = 0, ahead_end = 0;
   int spots = -1, next_spots = -1;  // of two tiles' entries (lanes 0 to 15, 16 to 31), and the two behind them
   int tiles = 0, next_tiles = 0, half = 0;
-  uint32_t to_stage = 0;
+  int to_stage = 0;
   auto look_up = [&]() {
     next_tiles = 0;
     while (ahead_i >= ahead_end) {
@@ -300,21 +327,40 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident) few_kerne
     if (tiles > 0) look_up();
   };
   auto copy_next = [&]() {
-    if (tiles > 0) {
-      if (__all_sync(0xffffffffu, spots >= 0))
-        copy_step<KT, D, NT, true>(p, scales, spots, half, mine_at + to_stage, lane);
-      else
-        copy_step<KT, D, NT, false>(p, scales, spots, half, mine_at + to_stage, lane);
+    if (tiles > 0 && !dead) {
+      const uint32_t dst = mine_at + to_stage * F::kStage;
+      const bool all = (__ballot_sync(0xffffffffu, spots >= 0) >> half & 0xffffu) == 0xffffu;
+      if (all && boxes) {  // 16 entries in a row
+        fence_proxy_async();  // (after what was written here by this warp itself)
+        const int spot = __shfl_sync(0xffffffffu, spots, half);
+        if (lane == 0) {
+          const int row = quotient(spot, p.by_heads), h = spot - row * p.H_kv;
+          const uint32_t bar = full + 8 * to_stage;
+          mbar_arrive_expect_tx(bar, 2 * F::kVAt);
+#pragma unroll
+          for (int part = 0; part < (F::kRow + 127) / 128; ++part) {
+            tma_box3(dst + part * (kStep * 128), &maps.k, 64 * part, h, row, bar);
+            tma_box3(dst + F::kVAt + part * (kStep * 128), &maps.v, 64 * part, h, row, bar);
+          }
+        }
+        __syncwarp();
+        by_tma |= 1u << to_stage;
+      } else if (all) {
+        copy_rows<KT, D, NT, true>(p, spots, half, dst, lane);
+      } else {
+        copy_rows<KT, D, NT, false>(p, spots, half, dst, lane);
+      }
+      if constexpr (KT == DA_KV_NVFP4) copy_scales<D>(p, spots, half, dst + F::kScalesAt, lane);
       half = 16;
       if (--tiles == 0) take_lookup();
     }
-    to_stage = to_stage == (F::kStages - 1) * F::kStage ? 0 : to_stage + F::kStage;
+    to_stage = to_stage == F::kStages - 1 ? 0 : to_stage + 1;
     cp_async_commit();
   };
   look_up();
   take_lookup();
   for (int i = 0; i < F::kStages - 1; ++i) copy_next();
-  uint32_t at_stage = 0, free_at = (F::kStages - 1) * F::kStage;  // the stage in use, and the one before it
+  int at_stage = 0, free_stage = F::kStages - 1;  // the stage in use, and the one before it
   for (int u = blockIdx.x; u < c.units; u += gridDim.x) {
     Unit* const x = &units[warp][0];
     {
@@ -387,13 +433,19 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident) few_kerne
     }
     for (int i = begin; i < end; ++i) {
       cp_async_wait<F::kStages - 2>();
+      if (by_tma >> at_stage & 1 && !dead) {
+        dead = __any_sync(0xffffffffu, !mbar_wait(full + 8 * at_stage, parity >> at_stage & 1));
+        by_tma ^= 1u << at_stage;
+        parity ^= 1u << at_stage;
+        if (dead && lane == 0) report(p.err, DA_DEVERR_TIMEOUT);
+      }
       __syncwarp();
-      const uint8_t* stage = mine + at_stage;
+      const uint8_t* stage = mine + at_stage * F::kStage;
       HeldK<KT, D, NT> held;
       held.read(stage, lane);
       copy_next();  // to the stage of the step before
-      free_at = at_stage;
-      at_stage = at_stage == (F::kStages - 1) * F::kStage ? 0 : at_stage + F::kStage;
+      free_stage = at_stage;
+      at_stage = at_stage == F::kStages - 1 ? 0 : at_stage + 1;
       // ---- scores: entries g and g + 8, rows 8 nt + 2 q and + 1; two sums, as an MMA waits long
       // for the one before it
       float s[NT][4], s_odd[NT][4];
@@ -516,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident) few_kerne
           if (F::kPassRows == 8 && nt != pass) continue;
           if (F::kPassRows == 4 && 2 * nt + r != pass) continue;
           const int at = F::kPassRows == 4 ? q : F::kPassRows == 8 ? 2 * q + r : 8 * nt + 2 * q + r;
-          float2* to = reinterpret_cast<float2*>(mine + free_at) + at * (D / 2);
+          float2* to = reinterpret_cast<float2*>(mine + free_stage * F::kStage) + at * (D / 2);
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
             constexpr int kPer = F::kVDims / 2;  // tiles of a piece
@@ -537,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident) few_kerne
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const float c_w = part_m[w][at] == top ? 1.f : ex2(part_m[w][at] - top);
-          const float2* from = reinterpret_cast<const float2*>(stages + w * (F::kStages * F::kStage) + free_at) + in * (D / 2);
+          const float2* from = reinterpret_cast<const float2*>(stages + w * (F::kStages * F::kStage) + free_stage * F::kStage) + in * (D / 2);
           const float2 o0 = from[pair ^ swap], o1 = from[(pair + 1) ^ swap];
           sum = fmaf(part_l[w][at], c_w, sum);
           v.x = fmaf(o0.x, c_w, v.x);
@@ -589,6 +641,8 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident) few_kerne
     __syncthreads();  // (odd_rows and sees are the next unit's now)
   }
   cp_async_wait<0>();
+  for (int st = 0; dead && st < F::kStages; ++st)  // leave no copy in flight
+    if (by_tma >> st & 1) mbar_wait(full + 8 * st, parity >> st & 1);
   if (__any_sync(0xffffffffu, bad) && lane == 0) report(p.err, DA_DEVERR_INDEX);
 }
 
@@ -602,11 +656,26 @@ cudaError_t launch_shape(const TreeLaunch& p0, int sms, cudaStream_t stream) {
   p.by_heads = fast_div(p.H_kv);
   p.by_group = fast_div(p.G);
   p.by_page = fast_div(p.page_size > 1 ? p.page_size : 1);
+  FewMaps m;
+  std::memset(&m, 0, sizeof(m));
+  const int boxes = p.kv_rows > 0 && (p.layout == DA_KV_CONTIGUOUS || (p.layout == DA_KV_PAGED && p.page_size % kStep == 0));
+  if (boxes) {
+    constexpr cuuint32_t kWide = F::kRow < 128 ? F::kRow : 128;  // bytes of a box's row
+    const cuuint64_t heads = (cuuint64_t)p.H_kv, size = F::Q8 ? 1 : 2;
+    const cuuint64_t dims[3] = {F::kRow / size, heads, (cuuint64_t)p.kv_rows}, strides[2] = {F::kRow, heads * F::kRow};
+    const cuuint32_t box[3] = {kWide / (cuuint32_t)size, 1, kStep};
+    const CUtensorMapSwizzle swizzle = kWide == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                       : kWide == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                     : CU_TENSOR_MAP_SWIZZLE_32B;
+    if (!tree_tensor_map(&m.k, p.k, 3, dims, strides, box, F::Q8, swizzle) ||
+        !tree_tensor_map(&m.v, p.v, 3, dims, strides, box, F::Q8, swizzle))
+      return cudaErrorInvalidValue;
+  }
   for (p.row0 = 0; p.row0 < p.B; p.row0 += kTreeRows) {
     p.rows = p.B - p.row0 < kTreeRows ? p.B - p.row0 : kTreeRows;
     const long long most = (long long)p.rows * p.max_splits * p.H_kv, room = (long long)F::kResident * sms;
     const cudaError_t e = launch_after(few_kernel<KT, D, NT>, dim3((unsigned)(most < room ? most : room)), dim3(kThreads),
-                                       (size_t)F::kBytes, stream, p);
+                                       (size_t)F::kBytes, stream, p, m, boxes);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
