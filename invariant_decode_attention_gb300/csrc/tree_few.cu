@@ -9,6 +9,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+// Copies and lookups run less than this many units ahead: four stages' tiles and four more.
+constexpr int kUnitSlots = 8;
 constexpr int kStep = kT / kWarps;  // entries of a tile that a warp has: the M of an MMA
 
 // What a thread of a warp reads of 16 entries, lane 4 g + q: entries g and g + 8 of K (D / 4
@@ -255,11 +257,11 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
   __shared__ uint64_t bars[kWarps * F::kStages + 1];           // of the TMA's copies; one that nothing arrives at
   __shared__ int2 sizes[kTreeRows];
   __shared__ int first[kTreeRows + 1];
-  __shared__ Unit units[kWarps][2];  // a warp's unit, and the one that it copies
+  __shared__ Unit units[kWarps][kUnitSlots];  // a warp's unit, and those behind it up to the one that it copies
   __shared__ unsigned long long sees[F::kRows];  // nodes that a row sees
   __shared__ int depths[F::kRows];
   __shared__ float part_m[kWarps][F::kRows], part_l[kWarps][F::kRows];
-  __shared__ uint32_t odd_rows;
+  __shared__ uint32_t odd_rows[2];  // of every second unit
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
   if (threadIdx.x == 0) {
     for (int i = 0; i <= kWarps * F::kStages; ++i) mbar_init(smem_addr(bars + i), 1);
@@ -285,12 +287,12 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
   // ---- copies run ahead of their use by kStages - 1 tiles, lookups by two more
   uint8_t* const mine = stages + warp * (F::kStages * F::kStage);
   const uint32_t mine_at = smem_addr(mine);
-  Unit* const ahead = &units[warp][1];
+  Unit* ahead = nullptr;
   const uint32_t full = smem_addr(bars + warp * F::kStages);
   uint32_t by_tma = 0, parity = 0;  // bits of the stages: what fills them, the phase to wait for
   bool dead = false;                // a wait ran out
   bool bad = false;
-  int ahead_u = (int)blockIdx.x - (int)gridDim.x, ahead_i = 0, ahead_end = 0;
+  int ahead_u = (int)blockIdx.x - (int)gridDim.x, ahead_n = 0, ahead_i = 0, ahead_end = 0;
   int spots = -1, next_spots = -1;  // of two tiles' entries (lanes 0 to 15, 16 to 31), and the two behind them
   int tiles = 0, next_tiles = 0, half = 0;
   int to_stage = 0;
@@ -302,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
       const Unit z = unit_of(p, c, ahead_u);
       ahead_i = z.begin;
       ahead_end = z.end;
-      __syncwarp();
+      ahead = &units[warp][ahead_n++ % kUnitSlots];
       if (lane == 0) *ahead = z;
       __syncwarp();
     }
@@ -361,25 +363,14 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
   take_lookup();
   for (int i = 0; i < F::kStages - 1; ++i) copy_next();
   int at_stage = 0, free_stage = F::kStages - 1;  // the stage in use, and the one before it
-  for (int u = blockIdx.x; u < c.units; u += gridDim.x) {
-    Unit* const x = &units[warp][0];
-    {
-      const Unit z = unit_of(p, c, u);
-      __syncwarp();
-      if (lane == 0) *x = z;
-      __syncwarp();
-    }
-    const int n_rows = x->rows, h = x->h, begin = x->begin, end = x->end, length = x->r.length;
-    // ---- Q, and what the rows see
-    uint32_t qb[NT][D / 16][2];
-    float scale[NT][2];  // softmax scales of rows 8 nt + 2 q and + 1
+  uint32_t qb[NT][D / 16][2];
+  auto load_q = [&](const Unit* z) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int at = nt * 8 + g;
-      float mine = p.scale_log2;
-      const bool live = at < n_rows;
+      const bool live = at < z->rows;
       const int t = live ? quotient(at, p.by_group) : 0;
-      const __nv_bfloat16* from = p.q + ((size_t)((long long)x->b * p.T + t) * p.H_q + h * p.G + (at - t * p.G)) * D;
+      const __nv_bfloat16* from = p.q + ((size_t)((long long)z->b * p.T + t) * p.H_q + z->h * p.G + (at - t * p.G)) * D;
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) {
         constexpr int kPer = F::kKDims / 4;  // k-steps of a piece
@@ -388,6 +379,29 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
         qb[nt][s][0] = w.x;
         qb[nt][s][1] = w.y;
       }
+    }
+  };
+  // A list without entries (a capacity of 0, which all rows share) is not looked up, and after
+  // a time-out nothing is.
+  auto unit_at = [&](int u, int n) -> const Unit* {
+    Unit* const z = &units[warp][n % kUnitSlots];
+    if (p.capacity == 0 || dead) {
+      const Unit v = unit_of(p, c, u);
+      __syncwarp();
+      if (lane == 0) *z = v;
+      __syncwarp();
+    }
+    return z;
+  };
+  const Unit* x = unit_at(blockIdx.x, 0);
+  load_q(x);
+  for (int u = blockIdx.x, n = 0; u < c.units; u += gridDim.x, ++n) {
+    const int n_rows = x->rows, h = x->h, begin = x->begin, end = x->end, length = x->r.length;
+    // ---- Q as an operand, and what the rows see
+    float scale[NT][2];  // softmax scales of rows 8 nt + 2 q and + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float mine = p.scale_log2;
       if constexpr (F::Q8) {  // f16, scaled by a power of two
         uint32_t top = 0;
 #pragma unroll
@@ -411,14 +425,14 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
       const int at = threadIdx.x;
       int depth = 0;
       unsigned long long anc = 0;
-      if (at < n_rows) {
+      if (at < n_rows && end > begin && (p.window || (tree_tile(x->r, end - 1) + 1) * kT > length)) {
         anc = ancestors(p, x->b, quotient(at, p.by_group), &depth);
         anc = windowed(p, x->r, anc, depth) & low_bits(x->r.end - length);
       }
       sees[at] = anc;
       depths[at] = depth;
     }
-    if (threadIdx.x == 0) odd_rows = 0;
+    if (threadIdx.x == 0) odd_rows[n & 1] = 0;
     __syncthreads();
     const int whole = p.window ? length + x->r.nodes - p.window : 0;
     float o[NT][D / 16][4], m[NT][2], l[NT][2];
@@ -541,6 +555,11 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
           for (int nt = 0; nt < NT; ++nt) mma_16816<F::Q8>(o[nt][4 * j4 + j], a[j], pb[nt][0], pb[nt][1]);
       }
     }
+    const Unit* next = x;
+    if (u + (int)gridDim.x < c.units) {
+      next = unit_at(u + gridDim.x, n + 1);
+      load_q(next);
+    }
     // ---- the warps' sums joined, in their order, by way of each one's stage that was used last
     // (the next copy goes there)
 #pragma unroll
@@ -601,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
         v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
         const int t = quotient(at, p.by_group);
         const size_t row = (size_t)((long long)x->b * p.T + t) * p.H_q + h * p.G + (at - t * p.G);
-        if (sum != sum || !(fabsf(v.x) + fabsf(v.y) + fabsf(v.z) + fabsf(v.w) < INFINITY)) atomicOr(&odd_rows, 1u << at);
+        if (sum != sum || !(fabsf(v.x) + fabsf(v.y) + fabsf(v.z) + fabsf(v.w) < INFINITY)) atomicOr(&odd_rows[n & 1], 1u << at);
         const float lse = sum > 0.f || sum != sum ? top + lg2(sum) : -INFINITY;
         if (single) {
           *reinterpret_cast<uint2*>(p.out + row * D + d) = make_uint2(pack16<false>(v.x, v.y), pack16<false>(v.z, v.w));
@@ -614,9 +633,9 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
       __syncthreads();
     }
     // rows that something infinite or NaN has spoiled: formed again, entry by entry
-    uint32_t again = odd_rows;
-    for (int n = 0; again; again &= again - 1, ++n) {
-      if (n % kWarps != warp) continue;
+    uint32_t again = odd_rows[n & 1];
+    for (int k = 0; again; again &= again - 1, ++k) {
+      if (k % kWarps != warp) continue;
       const int at = __ffs((int)again) - 1, t = quotient(at, p.by_group), head = h * p.G + (at - t * p.G);
       const size_t row = (size_t)((long long)x->b * p.T + t) * p.H_q + head;
       float m2, l2, o2[D / 32];
@@ -638,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
           p.lse_part[to_slot + (long long)row] = lse2;
       }
     }
-    __syncthreads();  // (odd_rows and sees are the next unit's now)
+    x = next;
   }
   cp_async_wait<0>();
   for (int st = 0; dead && st < F::kStages; ++st)  // leave no copy in flight
