@@ -24,6 +24,7 @@ struct Few {
   static constexpr int kKPiece = kKWords < 4 ? kKWords : 4, kVPiece = kVWords < 4 ? kVWords : 4;  // words of a copy
   static constexpr int kKDims = kKPiece * 4 * D / kRow, kVDims = kVPiece * 4 * D / kRow;          // dims of a copy
   static constexpr int kRows = 8 * NT;
+  static constexpr int kPitch = kRow < 128 ? kRow : 128;  // from row to row in a stage
   // chunk of a row that is lane q's P-th of K: a phase of a read has two rows' even or odd ones
   static __device__ __forceinline__ int k_chunk(int q, int P) { return kRow >= 128 ? 2 * q + P % 2 + P / 2 * 8 : q; }
   // a warp's stage: K, V, NVFP4 block scales
@@ -147,18 +148,17 @@ struct HeldK {
   using F = Few<KT, D, NT>;
   uint32_t k[2][F::kKWords], ks[2];
 
-  __device__ __forceinline__ void read(const uint8_t* stage, int lane) {
-    const int g = lane >> 2, q = lane & 3;
+  // `off`: where this lane's first words lie; the others follow from it, as a swizzle only
+  // swaps neighbours here
+  __device__ __forceinline__ void read(const uint8_t* stage, uint32_t off, int q) {
+    const int g = (threadIdx.x & 31) >> 2;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int row = g + 8 * e;
 #pragma unroll
       for (int i = 0; i < F::kKWords; i += F::kKPiece)
-        read_words<F::kKPiece>(F::kKPiece == 4 ? stage + chunk_at<F::kRow / 16>(row, F::k_chunk(q, i / 4))
-                                               : stage + chunk_at<F::kRow / 16>(row, q / 2) + 8 * (q & 1),
-                               k[e] + i);
+        read_words<F::kKPiece>(stage + (off ^ (i & 4 ? 16u : 0u)) + i / 8 * (kStep * 128) + e * 8 * F::kPitch, k[e] + i);
       if constexpr (KT == DA_KV_NVFP4) {
-        const uint8_t* s = stage + F::kScalesAt + row * (D / 16);
+        const uint8_t* s = stage + F::kScalesAt + (g + 8 * e) * (D / 16);
         ks[e] = D == 128 ? reinterpret_cast<const uint16_t*>(s)[q] : s[q];
       }
     }
@@ -191,17 +191,17 @@ struct HeldV {
   using F = Few<KT, D, NT>;
   uint32_t v[4][F::kVWords], vs[4];
 
-  __device__ __forceinline__ void read(const uint8_t* stage, int lane) {
-    const int g = lane >> 2, q = lane & 3;
+  __device__ __forceinline__ void read(const uint8_t* stage, uint32_t off, int q) {
+    const int g = (threadIdx.x & 31) >> 2;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int row = 2 * q + (e & 1) + 4 * (e & 2);
 #pragma unroll
-      for (int i = 0; i < F::kVWords; i += F::kVPiece) {
-        const int byte = g * (F::kVPiece * 4) + 32 * i;  // of the row
-        read_words<F::kVPiece>(stage + F::kVAt + chunk_at<F::kRow / 16>(row, byte / 16) + byte % 16, v[e] + i);
-      }
-      if constexpr (KT == DA_KV_NVFP4) vs[e] = stage[F::kScalesAt + (kStep + row) * (D / 16) + g * (D / 8) / 16];
+      for (int i = 0; i < F::kVWords; i += F::kVPiece)
+        read_words<F::kVPiece>(stage + F::kVAt + (off ^ (F::kRow >= 128 && (e & 1) ? 16u : 0u)) + i / 4 * (kStep * 128) +
+                                   ((e & 1) + 4 * (e & 2)) * F::kPitch,
+                               v[e] + i);
+      if constexpr (KT == DA_KV_NVFP4)
+        vs[e] = stage[F::kScalesAt + (kStep + 2 * q + (e & 1) + 4 * (e & 2)) * (D / 16) + g * (D / 8) / 16];
     }
   }
 
@@ -289,6 +289,8 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
   const uint32_t mine_at = smem_addr(mine);
   Unit* ahead = nullptr;
   const uint32_t full = smem_addr(bars + warp * F::kStages);
+  const uint32_t k_off = chunk_at<F::kRow / 16>(g, F::kKPiece == 4 ? F::k_chunk(q, 0) : q / 2) + (F::kKPiece == 4 ? 0 : 8 * (q & 1));
+  const uint32_t v_off = chunk_at<F::kRow / 16>(2 * q, g * F::kVPiece / 4) + g * F::kVPiece % 4 * 4;
   uint32_t by_tma = 0, parity = 0;  // bits of the stages: what fills them, the phase to wait for
   bool dead = false;                // a wait ran out
   bool bad = false;
@@ -397,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
   load_q(x);
   for (int u = blockIdx.x, n = 0; u < c.units; u += gridDim.x, ++n) {
     const int n_rows = x->rows, h = x->h, begin = x->begin, end = x->end, length = x->r.length;
+    const int head = x->r.head_tiles, skip = x->r.skip;
     // ---- Q as an operand, and what the rows see
     float scale[NT][2];  // softmax scales of rows 8 nt + 2 q and + 1
 #pragma unroll
@@ -456,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
       __syncwarp();
       const uint8_t* stage = mine + at_stage * F::kStage;
       HeldK<KT, D, NT> held;
-      held.read(stage, lane);
+      held.read(stage, k_off, q);
       copy_next();  // to the stage of the step before
       free_stage = at_stage;
       at_stage = at_stage == F::kStages - 1 ? 0 : at_stage + 1;
@@ -475,12 +478,12 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
         for (int nt = 0; nt < NT; ++nt) mma_16816<F::Q8>(k & 1 ? s_odd[nt] : s[nt], a, qb[nt][k][0], qb[nt][k][1]);
       }
       HeldV<KT, D, NT> values;
-      values.read(stage, lane);
+      values.read(stage, v_off, q);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[nt][e] += s_odd[nt][e];
-      const int j0 = tree_tile(x->r, i) * kT;
+      const int j0 = (i < head ? i : i + skip) * kT;
       const bool all = j0 + kT <= length && (j0 >= whole || j0 + kT <= p.sinks);
       bool move = false;
 #pragma unroll
@@ -636,10 +639,10 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
     uint32_t again = odd_rows[n & 1];
     for (int k = 0; again; again &= again - 1, ++k) {
       if (k % kWarps != warp) continue;
-      const int at = __ffs((int)again) - 1, t = quotient(at, p.by_group), head = h * p.G + (at - t * p.G);
-      const size_t row = (size_t)((long long)x->b * p.T + t) * p.H_q + head;
+      const int at = __ffs((int)again) - 1, t = quotient(at, p.by_group), hq = h * p.G + (at - t * p.G);
+      const size_t row = (size_t)((long long)x->b * p.T + t) * p.H_q + hq;
       float m2, l2, o2[D / 32];
-      attend_plainly<KT, D>(p, x->r, x->b, t, head, begin, end, lane, &m2, &l2, o2);
+      attend_plainly<KT, D>(p, x->r, x->b, t, hq, begin, end, lane, &m2, &l2, o2);
       const float inv2 = (l2 > 0.f ? 1.f / l2 : l2 != l2 ? l2 : 0.f) * p.v_scale;
       const float lse2 = l2 > 0.f || l2 != l2 ? m2 + lg2(l2) : -INFINITY;
 #pragma unroll
@@ -677,7 +680,7 @@ cudaError_t launch_shape(const TreeLaunch& p0, int sms, cudaStream_t stream) {
   p.by_page = fast_div(p.page_size > 1 ? p.page_size : 1);
   FewMaps m;
   std::memset(&m, 0, sizeof(m));
-  const int boxes = p.kv_rows > 0 && (p.layout == DA_KV_CONTIGUOUS || (p.layout == DA_KV_PAGED && p.page_size % kStep == 0));
+  const int boxes = F::kRow >= 128 && p.kv_rows > 0 && (p.layout == DA_KV_CONTIGUOUS || (p.layout == DA_KV_PAGED && p.page_size % kStep == 0));
   if (boxes) {
     constexpr cuuint32_t kWide = F::kRow < 128 ? F::kRow : 128;  // bytes of a box's row
     const cuuint64_t heads = (cuuint64_t)p.H_kv, size = F::Q8 ? 1 : 2;
