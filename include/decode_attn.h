@@ -454,7 +454,8 @@ int decode_attn_tree_workspace_bytes(const da_problem* prob, int32_t nodes, size
  * Rows past counts[b] of q are not read, those of out and lse left as they are.
  *
  * A row's list is cut into splits whose number follows from the row's own list and
- * number of nodes (and the window): its results are bitwise the same in any batch.
+ * number of nodes (and the window), and the kernel is chosen by the problem and T: a
+ * row's results are bitwise the same in any batch of calls with the same T.
  *
  * lengths outside [0, capacity] and counts outside [0, T] are clamped and entries
  * beyond the capacity are not read: DA_DEVERR_LENGTH.  Page ids and slots out of range are

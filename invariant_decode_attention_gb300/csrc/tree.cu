@@ -1,5 +1,27 @@
-// Attention of a tree of drafted tokens over the caches: every node of a row attends
-// to the row's context and to its own ancestors.
+// Attention of a tree of drafted tokens over the caches: every node of a row attends to the
+// row's context and to its own ancestors.  For (node t, head h) of row b, over the entries j
+// that t sees,
+//     s_j = scale q . k_j,   out = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m)    (log2 units),
+// in one pass with a running reference value m that moves only when a score exceeds it by 2^8,
+// and a log-sum-exp that joins the splits of a list in their order.
+//
+// All nodes of a row read the same K and V, so the rows of a matrix product are (node, head)
+// pairs: S = Q K^T and O += P V are tcgen05.mma of 128 rows, with S, O and Q in tensor memory
+// and P in shared memory over the K tile that it came from (64 dims: in tensor memory).  Calls
+// with few such pairs go to tree_few.cu.  What a node sees is a 64-bit mask of nodes, found
+// once a unit; whole tiles of context need no mask.
+//
+// Bound: bytes of K and V for one row's nodes; the softmax (a thread a row, 64 exponentials a
+// tile) and the way from MMA to softmax to MMA for full units of 128.  Measured, captured and
+// replayed, bf16, 64-entry tiles: 32 rows of 16 nodes, 32/8 heads, 8192 entries, 171 us = 4.8
+// TB/s (copied once at the measured bandwidth: 120 us); 8 rows of 64 nodes, 64/8 heads, 16384
+// entries, 230 us = 675 TFLOP/s.  Two blocks an SM, one unit each, because everything in a
+// block waits for something: between MMA, softmax and MMA, and for 13,500 cycles between
+// units; one block with two units in flight took 204 and 258 us.  Also measured and not kept,
+// on the first and the second of these: warps of their own for the output (258, 493), K and V
+// in rings of their own with P apart (197, 259), one warp for both MMAs (198, 270), a unit's
+// split chosen for equal units (188, 237: the blocks run in step), copies of Q and output by
+// rows of their own threads (187, 267).
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -956,7 +978,7 @@ cudaError_t launch_kt(const TreeLaunch& p, int sms, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_tree(const TreeLaunch& p, int sms, cudaStream_t stream) {
-  if (p.T * p.G <= kTreeFew) return launch_tree_few(p, sms, stream);
+  if (tree_takes_few(p.kv_type, p.D, p.T * p.G)) return launch_tree_few(p, sms, stream);
   switch (p.kv_type) {
     case DA_KV_FP8_E4M3: return launch_kt<DA_KV_FP8_E4M3>(p, sms, stream);
     case DA_KV_NVFP4: return launch_kt<DA_KV_NVFP4>(p, sms, stream);

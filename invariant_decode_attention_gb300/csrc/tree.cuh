@@ -9,7 +9,6 @@ namespace da {
 
 constexpr int kTreeTile = 64;       // entries of a tile
 constexpr int kTreeMaxSplits = 64;  // pieces of a row's list at most
-constexpr int kTreeFew = 16;        // (node, head) rows that tree_few.cu takes
 constexpr int kTreeSuper = 128;     // (node, head) rows of a unit at most
 
 // n / d for n below 2^31 by a multiplication: a unit's place is found with several
@@ -64,6 +63,15 @@ bool tree_tensor_map(CUtensorMap* tm, const void* base, int rank, const cuuint64
 cudaError_t launch_tree(const TreeLaunch& p, int sms, cudaStream_t stream);
 cudaError_t launch_tree_few(const TreeLaunch& p, int sms, cudaStream_t stream);
 cudaError_t launch_tree_combine(const TreeLaunch& p, cudaStream_t stream);
+
+// Whether tree_few.cu takes a call with this many (node, head) rows a KV head at most, whose
+// cost grows with the rows, where tree.cu's is the same up to 128.  A windowed step of 64 rows
+// with 4096 entries each and 8 KV heads, here against there, in us: 16 rows E4M3 211, 424, bf16
+// 225, 268; 32 rows E4M3 309, 438, NVFP4 342, 625, bf16 321, 282; 24 rows bf16 253, 273; 32 rows
+// of 64 dims, bf16, 208, 233.
+inline bool tree_takes_few(int kv_type, int D, int rows) {
+  return rows <= (kv_type == DA_KV_BF16 && D == 128 ? 24 : 32);
+}
 
 // Tiles of a split at least, for a row of `rows` (node, head) pairs a KV head.  A split
 // costs its rows' fp32 partials, written and read again, so that many rows want long

@@ -1,5 +1,25 @@
-// Tree attention of few (node, head) rows a KV head: a plain decode step's, or a short
-// chain's with small groups.
+// Tree attention of few (node, head) rows a KV head: a plain decode step's, or those of a short
+// chain or small tree.
+//
+// Tiles of 128 rows would be empty for the most part, and their way through tensor memory as
+// long.  Here each warp forms transposed products with m16n8k16: S^T = K Q^T and O^T += V^T P^T,
+// 16 entries of K (or 16 dims of V) on the wide side and 8 rows on the narrow one.  The order of
+// the dims in Q K^T, and of the entries in P V, is free, so a lane takes chunks of a cache row
+// just as they lie in memory, widens them in registers, and holds the right operand: no value
+// changes hands but the weights, by one 8 x 8 transpose.  A row's reference value and sum lie
+// with the lanes that have its weights and its output.
+//
+// A block has a unit of a list (tree.cuh's splits), its four warps 16 entries of each tile; they
+// meet once a unit, to join their sums.  Bound: the instructions that widen and multiply (about
+// 300 a warp and 16 entries) and, for bf16, the cache's bytes.  Measured, captured and replayed,
+// 64 rows of one node with 4096 of 32768 entries in their window: 32/8 heads E4M3 113 us = 4.8
+// TB/s (floor 79), bf16 179 us = 6.0 TB/s (159), NVFP4 120 us (45); 128/8 heads E4M3 211 us.  By
+// tiles of 128 rows the first took 415 us.  Steps: values loaded into registers a step ahead,
+// 196 us; by way of stages in shared memory, three or so steps ahead, 147; whole 128-byte lines
+// a copy instead of the lane's own chunks, 119 (the SM pays by the lines that a copy touches:
+// 64-byte pieces of K cost as much); boxes by the TMA, 113.  Splits of 16 tiles at least instead
+// of 8 make that 105, but a lone row of 4096 entries 21 us instead of 14.  More warps an SM with
+// fewer registers (20, 24) took 145 and 204 us against 141 at that step.
 #include <cstring>
 
 #include "tree_parts.cuh"
@@ -24,6 +44,10 @@ struct Few {
   static constexpr int kKPiece = kKWords < 4 ? kKWords : 4, kVPiece = kVWords < 4 ? kVWords : 4;  // words of a copy
   static constexpr int kKDims = kKPiece * 4 * D / kRow, kVDims = kVPiece * 4 * D / kRow;          // dims of a copy
   static constexpr int kRows = 8 * NT;
+  // Q lies in every warp's registers, or for more than 16 rows in shared memory, where warp w
+  // puts rows 8 w to 8 w + 7
+  static constexpr bool kQShared = NT > 2;
+  static constexpr int kQHeld = kQShared ? 1 : NT;
   static constexpr int kPitch = kRow < 128 ? kRow : 128;  // from row to row in a stage
   // chunk of a row that is lane q's P-th of K: a phase of a read has two rows' even or odd ones
   static __device__ __forceinline__ int k_chunk(int q, int P) { return kRow >= 128 ? 2 * q + P % 2 + P / 2 * 8 : q; }
@@ -37,7 +61,7 @@ struct Few {
   // rows of the output that go through a stage at once: all, those of an MMA, or every second
   static constexpr int kPassRows = kScalesAt >= kRows * D * 4 ? kRows : kScalesAt >= 8 * D * 4 ? 8 : 4;
   static_assert(kScalesAt >= kPassRows * D * 4, "a stage takes a pass");
-  static_assert(kResident * (kBytes + 6 * 1024) <= 228 * 1024, "resident blocks");
+  static_assert(kResident * (kBytes + (kQShared ? 15 : 6) * 1024) <= 228 * 1024, "resident blocks");
 };
 
 // Copies B bytes, or zeros.
@@ -260,6 +284,8 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
   __shared__ Unit units[kWarps][kUnitSlots];  // a warp's unit, and those behind it up to the one that it copies
   __shared__ unsigned long long sees[F::kRows];  // nodes that a row sees
   __shared__ int depths[F::kRows];
+  __shared__ uint2 shared_q[F::kQShared ? NT * (D / 16) * 32 : 1];  // lane by lane
+  __shared__ float shared_scale[F::kRows];
   __shared__ float part_m[kWarps][F::kRows], part_l[kWarps][F::kRows];
   __shared__ uint32_t odd_rows[2];  // of every second unit
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
@@ -365,11 +391,11 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
   take_lookup();
   for (int i = 0; i < F::kStages - 1; ++i) copy_next();
   int at_stage = 0, free_stage = F::kStages - 1;  // the stage in use, and the one before it
-  uint32_t qb[NT][D / 16][2];
+  uint32_t qb[F::kQHeld][D / 16][2];
   auto load_q = [&](const Unit* z) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int at = nt * 8 + g;
+    for (int nt = 0; nt < F::kQHeld; ++nt) {
+      const int at = (F::kQShared ? warp : nt) * 8 + g;
       const bool live = at < z->rows;
       const int t = live ? quotient(at, p.by_group) : 0;
       const __nv_bfloat16* from = p.q + ((size_t)((long long)z->b * p.T + t) * p.H_q + z->h * p.G + (at - t * p.G)) * D;
@@ -403,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
     // ---- Q as an operand, and what the rows see
     float scale[NT][2];  // softmax scales of rows 8 nt + 2 q and + 1
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < F::kQHeld; ++nt) {
       float mine = p.scale_log2;
       if constexpr (F::Q8) {  // f16, scaled by a power of two
         uint32_t top = 0;
@@ -421,8 +447,16 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
           for (int i = 0; i < 2; ++i)
             qb[nt][s][i] = pack16<true>(bf16_lo(qb[nt][s][i]) * sc, bf16_hi(qb[nt][s][i]) * sc);
       }
-      scale[nt][0] = __shfl_sync(0xffffffffu, mine, 8 * q);
-      scale[nt][1] = __shfl_sync(0xffffffffu, mine, 8 * q + 4);
+      if constexpr (F::kQShared) {
+        if (warp < NT) {
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) shared_q[(warp * (D / 16) + s) * 32 + lane] = make_uint2(qb[0][s][0], qb[0][s][1]);
+          if (q == 0) shared_scale[warp * 8 + g] = mine;
+        }
+      } else {
+        scale[nt][0] = __shfl_sync(0xffffffffu, mine, 8 * q);
+        scale[nt][1] = __shfl_sync(0xffffffffu, mine, 8 * q + 4);
+      }
     }
     if (threadIdx.x < F::kRows) {
       const int at = threadIdx.x;
@@ -437,6 +471,12 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
     }
     if (threadIdx.x == 0) odd_rows[n & 1] = 0;
     __syncthreads();
+    if constexpr (F::kQShared) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) scale[nt][r] = shared_scale[8 * nt + 2 * q + r];
+    }
     const int whole = p.window ? length + x->r.nodes - p.window : 0;
     float o[NT][D / 16][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -475,7 +515,14 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
         uint32_t a[4];
         held.k_operand(k, a);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_16816<F::Q8>(k & 1 ? s_odd[nt] : s[nt], a, qb[nt][k][0], qb[nt][k][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          uint2 b;
+          if constexpr (F::kQShared)
+            b = shared_q[(nt * (D / 16) + k) * 32 + lane];
+          else
+            b = make_uint2(qb[nt][k][0], qb[nt][k][1]);
+          mma_16816<F::Q8>(k & 1 ? s_odd[nt] : s[nt], a, b.x, b.y);
+        }
       }
       HeldV<KT, D, NT> values;
       values.read(stage, v_off, q);
@@ -705,7 +752,12 @@ cudaError_t launch_shape(const TreeLaunch& p0, int sms, cudaStream_t stream) {
 
 template <int KT, int D>
 cudaError_t launch_rows(const TreeLaunch& p, int sms, cudaStream_t stream) {
-  return p.T * p.G <= 8 ? launch_shape<KT, D, 1>(p, sms, stream) : launch_shape<KT, D, 2>(p, sms, stream);
+  const int rows = p.T * p.G;
+  if (rows <= 8) return launch_shape<KT, D, 1>(p, sms, stream);
+  if (rows <= 16) return launch_shape<KT, D, 2>(p, sms, stream);
+  if (rows <= 24) return launch_shape<KT, D, 3>(p, sms, stream);
+  if constexpr (KT != DA_KV_BF16 || D != 128) return launch_shape<KT, D, 4>(p, sms, stream);
+  return cudaErrorInvalidValue;
 }
 
 template <int KT>

@@ -191,11 +191,74 @@ def test_against_definition(api, layout, kv, page, heads, T, lengths, counts, wi
     c.check(out, lse)
 
 
+# (heads, T): (node, head) rows a KV head on both sides of every width that a kernel is made for
+ROWS = [((7, 7, 128), 1), ((8, 1, 64), 1), ((32, 8, 128), 2), ((18, 2, 128), 1), ((32, 8, 128), 4), ((34, 2, 64), 1),
+        ((24, 2, 128), 2), ((10, 2, 64), 5), ((15, 3, 128), 5), ((32, 8, 128), 8), ((16, 2, 64), 4), ((11, 1, 128), 3)]
+
+
 @gpu
 @pytest.mark.parametrize("kv", KV)
-def test_peaked_scores(api, kv):
+@pytest.mark.parametrize("heads,T", ROWS)
+@pytest.mark.parametrize("layout,page,window", [("paged", 16, 0), ("paged", 5, 70), ("contiguous", 0, 300), ("indexed", 0, 0)])
+def test_numbers_of_rows(api, kv, heads, T, layout, page, window):
+    c = Case(api, kv=kv, heads=heads, T=T, layout=layout, page=page, lengths=[640, 5, 0, 61], window=window,
+             sinks=5 if window else 0, tree=T > 2, seed=T + page)
+    c.check(*c.run(api))
+
+
+@gpu
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("heads,T", [((8, 2, 64), 3), ((8, 8, 128), 2), ((32, 2, 128), 3)])
+def test_layouts_give_the_same_bits(api, kv, heads, T):
+    """Pages of 16 (copied whole), of 5 and single slots, and a contiguous cache."""
+    H, D = heads[1:]
+    L, rows = [700, 33], []
+    base = Case(api, kv=kv, heads=heads, T=T, layout="contiguous", page=0, lengths=L, seed=21)
+    for layout, page in (("contiguous", 0), ("paged", 16), ("paged", 5), ("indexed", 0)):
+        c = Case(api, kv=kv, heads=heads, T=T, layout=layout, page=page, lengths=L, seed=21)
+        c.q, c.parents = base.q, base.parents
+        for b in range(2):
+            for j in range(L[b] + T):
+                to, at = c.entry(b, j), base.entry(b, j)
+                for mine, its in ((c.kc, base.kc), (c.vc, base.vc)):
+                    if kv != "nvfp4":
+                        mine[to] = its[at]
+                        continue
+                    m, m0 = c.total * H * D // 2, base.total * H * D // 2
+                    mine[:m].view(-1, H * D // 2)[to] = its[:m0].view(-1, H * D // 2)[at]
+                    mine[m:].view(-1, H * D // 16)[to] = its[m0:].view(-1, H * D // 16)[at]
+        rows.append(c.run(api))
+    for out, lse in rows[1:]:
+        assert torch.equal(out, rows[0][0]) and torch.equal(lse, rows[0][1])
+
+
+@gpu
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("heads,T", [((8, 8, 128), 4), ((8, 2, 64), 4), ((48, 2, 128), 1)])
+def test_a_short_row_depends_on_itself_alone(api, kv, heads, T):
+    """Rows of few nodes, alone and in batches of any size and order, and again."""
+    rng = np.random.default_rng(22)
+    lengths = [int(x) for x in rng.integers(0, 2500, 40)]
+    counts = [int(x) for x in rng.integers(1, T + 1, 40)]
+    c = Case(api, kv=kv, heads=heads, T=T, lengths=lengths, counts=counts, window=900, sinks=2, seed=22)
+    out, lse = c.run(api)
+    again = c.run(api)
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+    q, table, parents = c.q.clone(), c.table.clone(), list(c.parents)
+    for rows in ([7], [39, 0], [int(x) for x in rng.permutation(40)], [5] * 3):
+        c.prob.batch = c.B = len(rows)
+        c.q, c.table, c.parents = q[rows], table[rows].contiguous(), [parents[b] for b in rows]
+        c.lengths, c.counts = [lengths[b] for b in rows], [counts[b] for b in rows]
+        got = c.run(api)
+        assert torch.equal(got[0], out[rows]) and torch.equal(got[1], lse[rows])
+
+
+@gpu
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("heads", [(8, 2, 64), (16, 2, 64)])  # 24 rows a KV head, 48: the two kernels
+def test_peaked_scores(api, kv, heads):
     # large scores: the running reference value moves many times
-    c = Case(api, kv=kv, T=6, lengths=[1500, 700], heads=(8, 2, 64), q_gain=12.0, seed=3)
+    c = Case(api, kv=kv, T=6, lengths=[1500, 700], heads=heads, q_gain=12.0, seed=3)
     c.check(*c.run(api))
 
 
@@ -248,11 +311,12 @@ def test_more_rows_than_a_launch_takes(api):
 @gpu
 @pytest.mark.parametrize("kv", KV)
 @pytest.mark.parametrize("window", [0, 150])
-def test_what_lies_in_unseen_places_does_not_matter(api, kv, window):
+@pytest.mark.parametrize("heads", [(8, 2, 64), (16, 2, 64), (2, 2, 128)])
+def test_what_lies_in_unseen_places_does_not_matter(api, kv, window, heads):
     """NaN (and for bf16 infinities) past the end, in the window's hole, in pages of nobody,
     and in a sibling's entry, whose K and V only that node sees."""
     L, T = 1000, 6
-    c = Case(api, kv=kv, T=T, lengths=[L, 30], heads=(8, 2, 64), window=window, sinks=3 if window else 0, seed=9, room=70)
+    c = Case(api, kv=kv, T=T, lengths=[L, 30], heads=heads, window=window, sinks=3 if window else 0, seed=9, room=70)
     c.parents = [[-1, 0, 0, 2, 2, -1]] * 2  # node 1 is seen by itself alone
     clean = c.run(api)
     c.check(*clean)
@@ -394,8 +458,9 @@ def test_streams_and_graphs(api):
 
 @gpu
 @pytest.mark.parametrize("kv", KV)
-def test_time_out_path(api, kv):
-    c = Case(api, kv=kv, T=4, lengths=[700, 90], seed=15)
+@pytest.mark.parametrize("heads", [(8, 2, 128), (32, 2, 128)])
+def test_time_out_path(api, kv, heads):
+    c = Case(api, kv=kv, T=4, lengths=[700, 90], heads=heads, seed=15)
     want = c.run(api)
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     c.prob.flags = api.FLAG_TEST_STALL
@@ -412,11 +477,12 @@ def test_time_out_path(api, kv):
 
 @gpu
 @pytest.mark.parametrize("kv", KV)
-def test_caches_beyond_32_bits(api, kv):
+@pytest.mark.parametrize("H_q,T", [(8, 3), (128, 3)])
+def test_caches_beyond_32_bits(api, kv, H_q, T):
     """A cache of more than 2^32 elements, pages at both ends of it and around 2^31 and 2^32."""
-    H_q, H, D, page = 8, 8, 128, 16
+    H, D, page = 8, 128, 16
     pages = (1 << 18) + 7  # 16384 elements each
-    c = Case(api, kv=kv, heads=(H_q, H, D), T=3, lengths=[120], page=page, seed=16)
+    c = Case(api, kv=kv, heads=(H_q, H, D), T=T, lengths=[120], page=page, seed=16)
     small = c.run(api)
     ids = [0, (1 << 17) - 1, 1 << 17, (1 << 18) - 1, 1 << 18, pages - 2, pages - 1, 77]
     n = c.width
