@@ -326,6 +326,7 @@ template <int KT, int D>
 __device__ void converter(const TreeLaunch& p, const Ctx& c) {
   using L = Lay<KT, D>;
   constexpr int kPieces = D / 16;               // 16-dim pieces of a row
+  constexpr int kTimes = KT == DA_KV_NVFP4 ? 1 : 2;
   constexpr int kStep = 128 / kPieces;          // rows between a thread's
   const int ct = threadIdx.x - 8 * 32;
   const int jj = ct % kPieces, r0 = ct / kPieces;
@@ -338,7 +339,9 @@ __device__ void converter(const TreeLaunch& p, const Ctx& c) {
       if (!wait_warp(c, L::kEmpty + os, ((g / L::kStages) & 1) ^ 1)) return;
       const uint8_t* raw = c.smem + L::kRawOffset + rs * L::kRawStage;
       uint8_t* op = c.smem + os * L::kStage;
-#pragma unroll
+      // (rolled for NVFP4, whose code is long: 517 against 553 us for 64 rows of 16 nodes with 4096
+      // entries each; E4M3 takes 411 rolled, 397 unrolled)
+#pragma unroll kTimes
       for (int kv = 0; kv < 2; ++kv) {
 #pragma unroll
         for (int q = 0; q < kT / kStep; ++q) {

@@ -33,7 +33,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;                         // CTAs of a request at most
 constexpr int kNodes = NVFP4_VERIFY_MAX_NODES;
 constexpr int kBlock = 32 * kVec;                   // tokens of a warp's load
-constexpr int kAhead = 4;                           // loads of a thread in flight
+// Loads of a thread in flight: with 4 the largest calls take 1.3% less, the smallest 12% more.
+constexpr int kAhead = 2;
 static_assert(kNodes == 64, "two nodes a lane");
 
 struct Part {  // of a row's chunk
