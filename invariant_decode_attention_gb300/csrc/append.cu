@@ -198,6 +198,9 @@ __device__ __forceinline__ void norm_chunk(float (&f)[8], float r, const void* w
 // add).  A head's units lie on neighbouring lanes (eight for 128 dims, four for 64), so
 // its sum of squares is 16 products a lane, in order, and a butterfly of fixed shape;
 // the elements are in registers already, and nothing more is read but the weights.
+// Measured: 8192 tokens of 32/8 heads of 128, bf16, 46 us (30 at the measured bandwidth; 0.63
+// of the issue slots used, two tokens a warp, each beginning with its angles and its loads);
+// 64 rows of 8 nodes, fp32 into E4M3, 7.3 us (2.6).
 template <typename X, int KT, int D, bool kNorm>
 __global__ void __launch_bounds__(kWarps * 32, kResident<X>)
     append_kernel(const AppendLaunch p, int parts, int per_part) {
