@@ -17,9 +17,9 @@
 // TB/s (copied once at the measured bandwidth: 120 us); 8 rows of 64 nodes, 64/8 heads, 16384
 // entries, 230 us = 675 TFLOP/s.  Two blocks an SM, one unit each, because everything in a
 // block waits for something: between MMA, softmax and MMA, and for 13,500 cycles between
-// units; one block with two units in flight took 204 and 258 us.  Also measured and not kept,
+// units; one block with two units in flight took 204 us.  Also measured and not kept,
 // on the first and the second of these: warps of their own for the output (258, 493), K and V
-// in rings of their own with P apart (197, 259), one warp for both MMAs (198, 270), a unit's
+// in rings of their own with P apart (197, 259), MMAs issued by an elected lane of a whole warp (198, 270), a unit's
 // split chosen for equal units (188, 237: the blocks run in step), copies of Q and output by
 // rows of their own threads (187, 267).
 #include <cudaTypedefs.h>

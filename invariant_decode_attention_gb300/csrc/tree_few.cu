@@ -53,8 +53,11 @@ struct Few {
   static __device__ __forceinline__ int k_chunk(int q, int P) { return kRow >= 128 ? 2 * q + P % 2 + P / 2 * 8 : q; }
   // a warp's stage: K, V, NVFP4 block scales
   static constexpr int kVAt = kStep * kRow, kScalesAt = 2 * kVAt;
-  static constexpr int kAlign = kRow >= 128 ? 1024 : kRow == 64 ? 512 : 256;  // as the swizzles need it
-  static constexpr int kStage = (kScalesAt + (KT == DA_KV_NVFP4 ? 2 * kStep * (D / 16) : 0) + kAlign - 1) / kAlign * kAlign;
+  static constexpr int kStage = kScalesAt + (KT == DA_KV_NVFP4 ? 2 * kStep * (D / 16) : 0);
+  // Where 16 entries lie together the TMA copies rows of 128 bytes or more; shorter ones go faster
+  // by the lanes' copies (a windowed step of 64 rows: NVFP4 120 against 128 us, 64 dims of E4M3 81
+  // against 89; E4M3 with 128 dims 113 against 118 the other way).
+  static constexpr bool kBoxes = kRow >= 128;
   static constexpr int kStages = kStage > 4096 ? 2 : kStage > 3000 ? 3 : 4;
   static constexpr int kBytes = kWarps * kStages * kStage + 1024;  // (1024: to align them)
   static constexpr int kResident = NT == 1 && kStage <= 4096 ? 4 : NT == 1 || D == 64 ? 3 : 2;  // blocks an SM
@@ -131,7 +134,7 @@ struct FewMaps {
 };
 
 // 16-byte chunk `ch` of entry `row` in a stage, in an order in which a warp's reads spread
-// over the banks: the TMA's, 128, 64 or 32 bytes wide.
+// over the banks: the TMA's of 128 bytes, and the like for shorter rows.
 template <int R>  // chunks of a row
 __device__ __forceinline__ uint32_t chunk_at(int row, int ch) {
   if constexpr (R == 16) return (ch >> 3) * (kStep * 128) + row * 128 + ((ch & 7) ^ (row & 7)) * 16;
@@ -360,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
     if (tiles > 0 && !dead) {
       const uint32_t dst = mine_at + to_stage * F::kStage;
       const bool all = (__ballot_sync(0xffffffffu, spots >= 0) >> half & 0xffffu) == 0xffffu;
-      if (all && boxes) {  // 16 entries in a row
+      if (F::kBoxes && all && boxes) {  // 16 entries in a row
         fence_proxy_async();  // (after what was written here by this warp itself)
         const int spot = __shfl_sync(0xffffffffu, spots, half);
         if (lane == 0) {
@@ -368,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
           const uint32_t bar = full + 8 * to_stage;
           mbar_arrive_expect_tx(bar, 2 * F::kVAt);
 #pragma unroll
-          for (int part = 0; part < (F::kRow + 127) / 128; ++part) {
+          for (int part = 0; part < F::kRow / 128; ++part) {
             tma_box3(dst + part * (kStep * 128), &maps.k, 64 * part, h, row, bar);
             tma_box3(dst + F::kVAt + part * (kStep * 128), &maps.v, 64 * part, h, row, bar);
           }
@@ -727,17 +730,14 @@ cudaError_t launch_shape(const TreeLaunch& p0, int sms, cudaStream_t stream) {
   p.by_page = fast_div(p.page_size > 1 ? p.page_size : 1);
   FewMaps m;
   std::memset(&m, 0, sizeof(m));
-  const int boxes = F::kRow >= 128 && p.kv_rows > 0 && (p.layout == DA_KV_CONTIGUOUS || (p.layout == DA_KV_PAGED && p.page_size % kStep == 0));
-  if (boxes) {
-    constexpr cuuint32_t kWide = F::kRow < 128 ? F::kRow : 128;  // bytes of a box's row
+  int boxes = 0;
+  if constexpr (F::kBoxes) {
+    boxes = p.kv_rows > 0 && (p.layout == DA_KV_CONTIGUOUS || (p.layout == DA_KV_PAGED && p.page_size % kStep == 0));
     const cuuint64_t heads = (cuuint64_t)p.H_kv, size = F::Q8 ? 1 : 2;
     const cuuint64_t dims[3] = {F::kRow / size, heads, (cuuint64_t)p.kv_rows}, strides[2] = {F::kRow, heads * F::kRow};
-    const cuuint32_t box[3] = {kWide / (cuuint32_t)size, 1, kStep};
-    const CUtensorMapSwizzle swizzle = kWide == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                                       : kWide == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                                     : CU_TENSOR_MAP_SWIZZLE_32B;
-    if (!tree_tensor_map(&m.k, p.k, 3, dims, strides, box, F::Q8, swizzle) ||
-        !tree_tensor_map(&m.v, p.v, 3, dims, strides, box, F::Q8, swizzle))
+    const cuuint32_t box[3] = {128 / (cuuint32_t)size, 1, kStep};
+    if (boxes && (!tree_tensor_map(&m.k, p.k, 3, dims, strides, box, F::Q8, CU_TENSOR_MAP_SWIZZLE_128B) ||
+                  !tree_tensor_map(&m.v, p.v, 3, dims, strides, box, F::Q8, CU_TENSOR_MAP_SWIZZLE_128B)))
       return cudaErrorInvalidValue;
   }
   for (p.row0 = 0; p.row0 < p.B; p.row0 += kTreeRows) {
