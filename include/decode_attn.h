@@ -467,7 +467,7 @@ int decode_attn_tree_workspace_bytes(const da_problem* prob, int32_t nodes, size
  * `prob` describes the caches; its batch is the number of rows and its extra_width 0.
  * Supported: separate caches of all three types, D = 64 or 128, up to 128 query heads a
  * KV head; (entries of the cache) * H_kv and B * T * H_q up to 2^31.  out and lse overlap
- * neither q nor each other. */
+ * neither each other nor anything that the call reads, nor the workspace. */
 int decode_attn_tree(const da_problem* prob, const da_tree* args, void* stream);
 
 /* The caches of a model's layers, all of one geometry (that of the problem given

@@ -811,10 +811,19 @@ int decode_attn_tree(const da_problem* prob, const da_tree* args, void* stream) 
   if (!a.ws || !aligned(a.ws, 256) || a.ws_bytes < ws.total) return DA_ERR_WORKSPACE;
   const long long rows = (long long)prob->batch * a.nodes * prob->num_q_heads;
   const long long out_bytes = rows * prob->head_dim_v * 2;
-  // units of work read all of a row's queries, at any time
-  if (overlap(a.out, out_bytes, a.q, out_bytes) || overlap(a.lse, rows * 4, a.q, out_bytes) ||
-      overlap(a.out, out_bytes, a.lse, rows * 4))
-    return DA_ERR_INVALID_ARG;
+  // units of work read all of a row's queries, its entries and sizes, and write partials, at any time
+  const long long elements = cache_rows(*prob) * prob->num_kv_heads * prob->head_dim_qk;
+  const long long cache_bytes = prob->kv_dtype == DA_KV_BF16       ? elements * 2
+                                : prob->kv_dtype == DA_KV_FP8_E4M3 ? elements
+                                                                   : elements / 2 + elements / 16;
+  const long long B = prob->batch;
+  const void* used[8] = {a.q, a.k, a.v, a.lengths, a.counts, a.parents, a.table, a.ws};
+  const long long used_bytes[8] = {out_bytes, cache_bytes, cache_bytes, 4 * B, 4 * B, 4 * B * a.nodes, 4 * B * prob->width,
+                                   (long long)ws.total};
+  for (int i = 0; i < 8; ++i)
+    if (used[i] && (overlap(a.out, out_bytes, used[i], used_bytes[i]) || overlap(a.lse, rows * 4, used[i], used_bytes[i])))
+      return DA_ERR_INVALID_ARG;
+  if (overlap(a.out, out_bytes, a.lse, rows * 4)) return DA_ERR_INVALID_ARG;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DA_ERR_CUDA;
   const int sms = sm_count(dev);

@@ -555,6 +555,11 @@ def test_argument_rules(api):
                dict(err=(1 << 12) + 1), dict(lengths=(1 << 24) + 2), dict(out=1 << 20), dict(lse=(1 << 20) + 4),
                dict(lse=(1 << 26) + 64)):
         assert call(api, p, **kw) == inv, kw
+    # outputs over what other blocks read or write meanwhile
+    out, lse = 1 << 26, 1 << 28
+    for kw in (dict(lengths=out + 64), dict(counts=lse + 8), dict(parents=out + 128), dict(table=lse + 16),
+               dict(k=out), dict(v=out + 4096), dict(k=lse), dict(ws=out), dict(ws=lse)):
+        assert call(api, p, **kw) == inv, kw
     assert call(api, p, nodes=65) == uns
     need = api.tree_workspace_bytes(p, 4)
     for kw in (dict(ws=0), dict(ws=(1 << 30) + 16), dict(ws_bytes=need - 1)):
