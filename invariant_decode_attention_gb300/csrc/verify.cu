@@ -730,7 +730,10 @@ int nvfp4_mm_verify(const nvfp4_verify* args, void* stream) {
   const long long in_bytes[6] = {all, all, all, rows, rows, rows};
   const long long e_x = (long long)size, x_bytes = e_x * ((v.batch > 1 ? (v.batch - 1) * v.x_stride : 0) +
                                                           (v.nodes > 1 ? (v.nodes - 1) * v.x_node_stride : 0) + v.vocab);
+  const long long draft_bytes = 4 * ((v.batch > 1 ? (v.batch - 1) * v.draft_stride : 0) +
+                                     (v.nodes > 1 ? (v.nodes - 1) * v.draft_node_stride : 0) + v.vocab);
   for (int i = 0; i < 3; ++i) {
+    if (v.draft && overlap(outs[i], out_bytes[i], v.draft, draft_bytes)) return DA_ERR_INVALID_ARG;
     if (overlap(outs[i], out_bytes[i], v.x, x_bytes) || overlap(outs[i], out_bytes[i], v.ws, (long long)need))
       return DA_ERR_INVALID_ARG;
     for (int k = 0; k < 6; ++k)

@@ -396,7 +396,8 @@ def test_argument_rules(api):
                dict(xs=99), dict(xn=99), dict(xn=1 << 41), dict(draft=1 << 28, parents=1 << 12),
                dict(draft=1 << 28, ds=400, dn=99), dict(draft=1 << 28, ds=99, dn=100), dict(draft=(1 << 28) + 2, ds=400, dn=100),
                dict(err=2), dict(out=1 << 21), dict(nodes=(1 << 21) + 28), dict(accepted=1 << 22), dict(out=(1 << 25) + 4),
-               dict(out=(1 << 20) + 400), dict(accepted=1 << 27)):
+               dict(out=(1 << 20) + 400), dict(accepted=1 << 27), dict(draft=(1 << 24) - 8, ds=400, dn=100),
+               dict(draft=(1 << 26) - 3000, ds=400, dn=100)):
         assert call(**kw) == inv, kw
     for kw in (dict(T=65), dict(V=(1 << 19) + 1)):
         assert call(**kw) == uns, kw
