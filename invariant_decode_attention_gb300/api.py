@@ -814,7 +814,7 @@ def tree(prob: DaProblem, q, k, v, lengths, *, parents=None, counts=None, table=
     all), sinks: first positions that stay visible; ws: from ``tree_workspace``; err:
     int32 [1] that device error bits are OR-ed into.  Returns (out bf16 [B, T, H_q, D],
     lse fp32 [B, T, H_q]), made when not given; rows past a row's count are not
-    written.  A row's bits depend on that row alone.
+    written.  In calls of one T a row's bits depend on that row alone.
     """
     dev, layout, kv_dtype = q.get_device(), prob.layout, prob.kv_dtype
     B, T, D = prob.batch, q.shape[1], prob.head_dim_qk

@@ -114,6 +114,47 @@ def test_pages_out_of_range(api):
     api.copy_pages(c.prob, c.caches, i32([]), i32([]))
 
 
+@gpu
+@pytest.mark.parametrize("kv", ["e4m3", "nvfp4"])
+def test_caches_beyond_32_bits(api, kv):
+    """Pages and entries on both sides of 2^31 and 2^32 bytes of a buffer, block scales behind them."""
+    heads, D, page, pages = 8, 128, 64, (1 << 18) + 9  # 64 KB of elements a page
+    per = heads * D * page
+    prob = api.problem(batch=1, num_q_heads=heads, num_kv_heads=heads, head_dim_qk=D, layout="paged", scale=0.1,
+                       page_size=page, width=2, num_blocks=pages, kv_dtype=KV.index(kv))
+    m = pages * per
+    size = m if kv == "e4m3" else m // 2 + m // 16
+    k, v = (torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(2))
+    caches = api.Caches(prob, [k], [v])
+    # (parts: elements or codes, block scales)
+    parts = [(0, m, per)] if kv == "e4m3" else [(0, m // 2, per // 2), (m // 2, size, per // 16)]
+    g = torch.Generator().manual_seed(24)
+    ends = [0, (1 << 15) - 1, 1 << 15, (1 << 16) - 1, 1 << 16, (1 << 17) - 1, 1 << 17, pages - 9]
+    to = [pages - 1 - i for i in range(4)] + [1, 2, 3, 4]
+    filled = {}
+    for which, cache in enumerate((k, v)):
+        for lo, hi, n in parts:
+            for i in ends:
+                filled[which, lo, i] = torch.randint(0, 256, (n,), generator=g, dtype=torch.int32).to(torch.uint8).cuda()
+                cache[lo:hi].view(-1, n)[i] = filled[which, lo, i]
+    api.copy_pages(prob, caches, i32(ends), i32(to))
+    # entries 62 to 66 of a row over the last page and one at 2^32 bytes or past it: nodes 0, 2 and 4 of 62 stand
+    row = [pages - 1, 1 << 16]
+    new = api.compact(prob, caches, i32([62]), i32([[0, 2, 4, -1, -1]]), i32([2]), table=i32([row]))
+    assert new.tolist() == [65]
+    for which, cache in enumerate((k, v)):
+        for lo, hi, n in parts:
+            now = cache[lo:hi].view(-1, n)
+            last, next_ = filled[which, lo, ends[0]].view(page, -1).clone(), filled[which, lo, 1 << 16].view(page, -1).clone()
+            last[63] = next_[0]
+            next_[0] = next_[2]
+            assert torch.equal(now[row[0]].view(page, -1), last) and torch.equal(now[row[1]].view(page, -1), next_)
+            for i, j in list(zip(ends, to))[1:]:
+                assert torch.equal(now[j], filled[which, lo, i])
+    del k, v, caches, cache, now
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------ accepted entries
 
 def paths(rng, B, T):

@@ -332,6 +332,24 @@ def test_a_request_depends_on_itself_alone(api):
 
 
 @gpu
+def test_rows_beyond_32_bits(api):
+    """Requests and nodes 2^32 and 2^30 elements apart, of logits and draft's probabilities."""
+    c = Case(B=2, T=3, V=5003, x="bf16", draft=True, seed=23)
+    want = c.run(api)
+    c.check(want)
+    apart = (1 << 32) + 6, (1 << 30) + 2
+    size = apart[0] + 2 * apart[1] + 5003
+    x = torch.empty(size, dtype=torch.bfloat16, device="cuda").as_strided((2, 3, 5003), (*apart, 1))
+    draft = torch.empty(size, device="cuda").as_strided((2, 3, 5003), (*apart, 1))
+    x.copy_(c.x)
+    draft.copy_(c.draft)
+    got = c.run(api, x=x, draft=draft)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    del x, draft
+    torch.cuda.empty_cache()
+
+
+@gpu
 def test_tokens_are_distributed_as_the_targets(api):
     """Accepted or not, the first token has the target's distribution: 2^16 requests that
     differ in their random numbers alone, counts within six standard deviations."""
