@@ -12,13 +12,14 @@
 // A block has a unit of a list (tree.cuh's splits), its four warps 16 entries of each tile; they
 // meet once a unit, to join their sums.  Bound: the instructions that widen and multiply (about
 // 300 a warp and 16 entries) and, for bf16, the cache's bytes.  Measured, captured and replayed,
-// 64 rows of one node with 4096 of 32768 entries in their window: 32/8 heads E4M3 113 us = 4.8
-// TB/s (floor 79), bf16 179 us = 6.0 TB/s (159), NVFP4 120 us (45); 128/8 heads E4M3 211 us.  By
+// 64 rows of one node with 4096 of 32768 entries in their window: 32/8 heads E4M3 111 us = 4.9
+// TB/s (floor 79), bf16 177 us = 6.1 TB/s (159), NVFP4 110 us (45); 128/8 heads E4M3 207 us.  By
 // tiles of 128 rows the first took 415 us.  Steps: values loaded into registers a step ahead,
 // 196 us; by way of stages in shared memory, three or so steps ahead, 147; whole 128-byte lines
 // a copy instead of the lane's own chunks, 119 (the SM pays by the lines that a copy touches:
-// 64-byte pieces of K cost as much); boxes by the TMA, 113.  Splits of 16 tiles at least instead
-// of 8 make that 105, but a lone row of 4096 entries 21 us instead of 14.  More warps an SM with
+// 64-byte pieces of K cost as much); boxes by the TMA, the next
+// unit's Q ahead of its turn, no rescaling before a first score, 111.  Splits of 16 tiles at least instead
+// of 8 took 105 at 113, but a lone row of 4096 entries 21 us instead of 14.  More warps an SM with
 // fewer registers (20, 24) took 145 and 204 us against 141 at that step.
 #include <cstring>
 
@@ -55,8 +56,8 @@ struct Few {
   static constexpr int kVAt = kStep * kRow, kScalesAt = 2 * kVAt;
   static constexpr int kStage = kScalesAt + (KT == DA_KV_NVFP4 ? 2 * kStep * (D / 16) : 0);
   // Where 16 entries lie together the TMA copies rows of 128 bytes or more; shorter ones go faster
-  // by the lanes' copies (a windowed step of 64 rows: NVFP4 120 against 128 us, 64 dims of E4M3 81
-  // against 89; E4M3 with 128 dims 113 against 118 the other way).
+  // by the lanes' copies (a windowed step of 64 rows, when both were measured: NVFP4 120 against 128
+  // us, 64 dims of E4M3 81 against 89; E4M3 with 128 dims 115 against 119 the other way).
   static constexpr bool kBoxes = kRow >= 128;
   static constexpr int kStages = kStage > 4096 ? 2 : kStage > 3000 ? 3 : 4;
   static constexpr int kBytes = kWarps * kStages * kStage + 1024;  // (1024: to align them)
@@ -578,6 +579,8 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
             if (moves) m[nt][r] = most;
             l[nt][r] *= alpha[r];
           }
+          // (no sum stands before a row's first score)
+          if (!__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) continue;
 #pragma unroll
           for (int j = 0; j < D / 16; ++j)
 #pragma unroll
