@@ -797,7 +797,7 @@ __global__ void __launch_bounds__(Lay<KT, D>::kThreads, 2)
   }
   wait_prior_grid();
   allow_next_grid();
-  count_units(p, sizes, first, L::kThreads);
+  count_units<false>(p, sizes, first, L::kThreads);
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();

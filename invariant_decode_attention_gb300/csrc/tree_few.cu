@@ -299,8 +299,17 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
   }
   wait_prior_grid();
   allow_next_grid();
-  count_units(p, sizes, first, kThreads);
+  count_units<true>(p, sizes, first, kThreads);
   __syncthreads();
+  // Rows without a tile have no unit, so that the ring of units holds only such as are copied;
+  // their nodes see nothing.
+  for (int i = blockIdx.x; i < p.rows; i += gridDim.x) {
+    if (sizes[i].y >> 8) continue;
+    const long long heads = (long long)sizes[i].y * p.H_q, row = (long long)(p.row0 + i) * p.T * p.H_q;
+    for (long long k = threadIdx.x; k < heads * (D / 8); k += kThreads)
+      reinterpret_cast<uint4*>(p.out + row * D)[k] = make_uint4(0, 0, 0, 0);
+    for (long long k = threadIdx.x; k < heads; k += kThreads) p.lse[row + k] = -INFINITY;
+  }
   UnitTable c;
   c.sizes = sizes;
   c.first = first;
@@ -330,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
   int to_stage = 0;
   auto look_up = [&]() {
     next_tiles = 0;
-    while (ahead_i >= ahead_end) {
+    if (ahead_i >= ahead_end) {  // (every unit has a tile)
       ahead_u += gridDim.x;
       if (ahead_u >= c.units) return;
       const Unit z = unit_of(p, c, ahead_u);
@@ -413,11 +422,10 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
       }
     }
   };
-  // A list without entries (a capacity of 0, which all rows share) is not looked up, and after
-  // a time-out nothing is.
+  // (after a time-out nothing is looked up)
   auto unit_at = [&](int u, int n) -> const Unit* {
     Unit* const z = &units[warp][n % kUnitSlots];
-    if (p.capacity == 0 || dead) {
+    if (dead) {
       const Unit v = unit_of(p, c, u);
       __syncwarp();
       if (lane == 0) *z = v;

@@ -163,15 +163,19 @@ struct UnitTable {
 
 // The units of the launch's rows, counted by every block for itself: sizes gets each row's
 // length, nodes and splits, first its first unit.  The first block reports what is out of
-// range.  All `threads` threads; the caller synchronizes behind it.
+// range.  All `threads` threads; the caller synchronizes behind it.  A row can have nodes and
+// no tile: it fills its capacity, so that the nodes' own entries lie beyond it, and their
+// window holds no other.  kEmptyApart: such a row gets no unit and no split.
+template <bool kEmptyApart>
 __device__ __forceinline__ void count_units(const TreeLaunch& p, int2* sizes, int* first, int threads) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int bad = 0;
   for (int i = threadIdx.x; i < p.rows; i += threads) {
     const int2 s = tree_size(p, p.row0 + i, &bad);
     const TreeRow r = tree_row(p, s.x, s.y);
-    sizes[i] = make_int2(s.x, s.y | r.splits << 8);
-    first[i + 1] = r.splits * r.supers * p.H_kv;
+    const int splits = kEmptyApart && r.tiles == 0 ? 0 : r.splits;
+    sizes[i] = make_int2(s.x, s.y | splits << 8);
+    first[i + 1] = splits * r.supers * p.H_kv;
   }
   if (blockIdx.x == 0) {  // inputs that are out of range
     if (p.parents)

@@ -426,6 +426,31 @@ def test_a_row_of_capacity_zero(api):
 
 
 @gpu
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("heads,T", [((32, 32, 64), 1), ((64, 32, 128), 3), ((128, 32, 64), 5), ((96, 8, 64), 4)])
+def test_rows_without_a_tile_among_others(api, kv, heads, T):
+    """Full rows with a window of one: their nodes see nothing.  A block has a dozen units
+    of such rows one after another, and some of rows that see something."""
+    lengths = [64] * 300
+    for b, L in ((0, 63), (100, 0), (199, 5), (200, 63), (254, 17), (255, 1), (299, 40)):
+        lengths[b] = L
+    c = Case(api, kv=kv, heads=heads, T=T, layout="contiguous", page=0, lengths=lengths, window=1, room=-T, seed=18)
+    assert c.cap == 64
+    c.lengths[7] = c.lengths[201] = 99  # clamped
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = c.run(api, err=err)
+    assert int(err) == api.DEVERR_LENGTH
+    c.check(out, lse)
+    # all rows of a call
+    c.lengths = [64] * 300
+    out, lse = c.run(api)
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    # and with places left for more nodes
+    c.lengths, c.counts, c.given_counts = list(lengths), [b % (T + 1) for b in range(300)], True
+    c.check(*c.run(api))
+
+
+@gpu
 def test_streams_and_graphs(api):
     a = Case(api, T=5, lengths=[900, 20], seed=13)
     b = Case(api, T=7, lengths=[40, 1500, 3], kv="e4m3", window=64, sinks=4, seed=14)
