@@ -440,8 +440,8 @@ __global__ void __launch_bounds__(kThreads, 2) walk_kernel(const Args a) {
         if (may[h] && tau > 0.f) {
           const int t = lane + 32 * h;
           const float q = __ldg(a.draft + b * a.draft_row + t * a.draft_node + token[h]);
-          // u q < w / sum  (a NaN refuses)
-          yes[h] = (double)before * (double)q * row_sum[par[h]] < (double)p[h];
+          // u q < w / sum  (a NaN or a negative q refuses)
+          yes[h] = q >= 0.f && (double)before * (double)q * row_sum[par[h]] < (double)p[h];
         }
       }
     } else if (tau > 0.f) {  // an earlier sibling's token has been asked for already

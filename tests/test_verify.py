@@ -303,6 +303,27 @@ def test_draft_values_that_are_none(api):
 
 
 @gpu
+@pytest.mark.parametrize("x", ["fp32", "bf16"])
+@pytest.mark.parametrize("T", [2, 40])
+def test_negative_draft_values_refuse(api, x, T):
+    """Whatever the target says of the token, and with nothing taken off p for it."""
+    inf = float("inf")
+    values = (-1.0, -1.0, -1.0, -inf, -1e-45, -3e38, -0.0)
+    c = Case(B=7, T=T, V=900, x=x, draft=True, seed=17)
+    last = T - 1  # the refusal is here, in either half of a warp's nodes
+    c.u[:, :last - 1] = 0.0  # accepted up to there
+    for b, q in enumerate(values):
+        c.draft[b, last, int(c.tokens[b, last])] = q
+    c.u[1, last - 1] = 0.0                             # 0 * q is -0
+    c.x[2, last - 1, int(c.tokens[2, last])] = -inf    # no share of the target's, any q < 0 is less
+    got = c.run(api)
+    assert got[0].tolist() == [last - 1] * 6 + [last]  # (-0 is not negative)
+    # the definition, which refuses at a NaN and takes nothing off p for it
+    c.draft[c.draft < 0] = float("nan")
+    c.check(got)
+
+
+@gpu
 def test_tokens_and_parents_out_of_range(api):
     c = Case(B=5, T=4, V=2000, tree=True, seed=14)
     c.u[:] = 1e-9  # the first child that can be accepted is
