@@ -1220,11 +1220,6 @@ Layout layout_of(int n, int K, int max_rank) {
   return l;
 }
 
-template <typename F>
-cudaError_t allow_smem(F* kernel, int bytes) {  // it holds per device, and is cheap
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
 template <bool BF16, int S>
 cudaError_t launch_down(const Args& g, int sms, cudaStream_t st) {
   // at least so much that a second CTA stays off the SM: one owns tensor memory

@@ -124,6 +124,13 @@ inline cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, dim3 block, 
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Lets a kernel have more dynamic shared memory than needs no consent.  It holds for the
+// current device alone and is cheap, so that every launch asks for it.
+template <typename F>
+inline cudaError_t allow_smem(F* kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 // Host launchers (each in its own translation unit).
 cudaError_t launch_plan(const PlanLaunch& p, cudaStream_t stream);
 cudaError_t launch_split_fma(const Launch& p, int grid, cudaStream_t stream);

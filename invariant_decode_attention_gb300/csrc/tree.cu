@@ -923,8 +923,7 @@ __device__ __align__(128) __nv_bfloat16 g_nothing[128];
 template <int KT, int D>
 cudaError_t launch_shape(const TreeLaunch& p0, int sms, cudaStream_t stream) {
   using L = Lay<KT, D>;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(tree_kernel<KT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  const cudaError_t attr = allow_smem(tree_kernel<KT, D>, L::kBytes);
   if (attr != cudaSuccess) return attr;
   TreeLaunch p = p0;
   // entries that lie together for sure, as many as a copy takes

@@ -732,8 +732,7 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
 template <int KT, int D, int NT>
 cudaError_t launch_shape(const TreeLaunch& p0, int sms, cudaStream_t stream) {
   using F = Few<KT, D, NT>;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(few_kernel<KT, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kBytes);
+  const cudaError_t attr = allow_smem(few_kernel<KT, D, NT>, F::kBytes);
   if (attr != cudaSuccess) return attr;
   TreeLaunch p = p0;
   p.by_heads = fast_div(p.H_kv);
