@@ -645,9 +645,7 @@ int nvfp4_mm(const void* x, int32_t x_dtype, const uint8_t* codes, const uint8_t
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return DA_ERR_CUDA;
   }
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      nvfp4_mm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (attr != cudaSuccess) return DA_ERR_CUDA;
+  if (allow_smem(nvfp4_mm_kernel, kSmemBytes) != cudaSuccess) return DA_ERR_CUDA;
 
   MmArgs a;
   a.codes = codes;

@@ -761,9 +761,7 @@ __global__ void __launch_bounds__(FmaShape<G, D>::kThreads) split_fma_kernel(Lau
 template <int G, int D, bool X, int KT, bool PF = false>
 cudaError_t launch_x(const Launch& p, int grid, cudaStream_t stream) {
   using S = FmaShape<G, D, KT>;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(split_fma_kernel<G, D, X, KT, PF>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes);
+  const cudaError_t attr = allow_smem(split_fma_kernel<G, D, X, KT, PF>, S::kSmemBytes);
   if (attr != cudaSuccess) return attr;
   return launch_after(split_fma_kernel<G, D, X, KT, PF>, dim3(grid), dim3(S::kThreads),
                       S::kSmemBytes, stream, p);
@@ -790,8 +788,7 @@ template <int G, int D>
 int ctas_one() {
   using S = FmaShape<G, D>;
   static int n = [] {
-    cudaFuncSetAttribute(split_fma_kernel<G, D, false, kKvBf16, false>,
-                         cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes);
+    allow_smem(split_fma_kernel<G, D, false, kKvBf16, false>, S::kSmemBytes);
     int c = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&c, split_fma_kernel<G, D, false, kKvBf16, false>,
                                                       S::kThreads,

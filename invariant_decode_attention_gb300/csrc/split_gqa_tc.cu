@@ -1036,10 +1036,7 @@ int copies_for(int G) {
 
 template <int R, int KT>
 cudaError_t set_smem() {
-  static const cudaError_t e =
-      cudaFuncSetAttribute(split_gqa_tc_kernel<R, KT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Lay<KT>::kSmemBytes);
-  return e;
+  return allow_smem(split_gqa_tc_kernel<R, KT>, Lay<KT>::kSmemBytes);
 }
 
 int tc_ctas_per_sm() {

@@ -1046,9 +1046,7 @@ bool encode_rows(CUtensorMap* tm, const void* base, long long rows, int box_rows
 
 template <int KT>
 cudaError_t set_smem() {
-  static const cudaError_t e = cudaFuncSetAttribute(
-      split_mla_kernel<KT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  return e;
+  return allow_smem(split_mla_kernel<KT>, kSmemBytes);
 }
 
 }  // namespace

@@ -100,9 +100,36 @@ def tree(api, kv, D, T, group):
     return api.lib().decode_attn_tree(ctypes.addressof(p), args, None)
 
 
+def forward(api, kv, D, group, page=16, latent=False, extra=False):
+    H = 1 if latent else 2
+    p = api.problem(batch=2, num_q_heads=H * group, num_kv_heads=H, head_dim_qk=D, head_dim_v=512 if latent else D,
+                    layout="paged" if page else "indexed", scale=0.1, page_size=page, width=64, num_blocks=200,
+                    kv_dtype=kv, shared_latent=latent, extra_width=8 if extra else 0, extra_num_blocks=9 if extra else 0)
+    ref, v, table, lengths, more = ctypes.byref(p), 0 if latent else 1 << 22, 1 << 23, 1 << 24, 1 << 25
+    rest = (1 << 30, api.workspace_bytes(p), 1 << 26, 1 << 28, None)
+    if not extra:
+        return api.lib().decode_attn_forward(ref, api.INVARIANT, 1 << 20, 1 << 21, v, table, lengths, *rest)
+    return api.lib().decode_attn_forward_extra(ref, api.INVARIANT, 1 << 20, 1 << 21, v, table, lengths, more,
+                                               0 if latent else more, more, more, *rest)
+
+
+def matmul(api):
+    n, N, K = 40, 256, 2048
+    return api.lib().nvfp4_mm(1 << 20, 1, 1 << 21, 1 << 22, 1.0, n, N, K, 1 << 23, 0, 1 << 30,
+                              api.lib().nvfp4_mm_workspace_bytes(n, N, K), None)
+
+
 # (T, query heads a KV head): every width of the kernel for few rows, and the tiles of 128
 CALLS = [(f"tree kv{kv} D{D} T{T} group {group}", lambda api, a=(kv, D, T, group): tree(api, *a))
          for kv in (0, 1, 2) for D in (64, 128) for T, group in ((1, 4), (4, 4), (6, 4), (8, 4), (16, 4))]
+CALLS += [(f"attention kv{kv} D{D} group {group} page {page}", lambda api, a=(kv, D, group, page): forward(api, *a))
+          for kv in (0, 1, 2) for D in (64, 128) for group in (1, 2, 4, 8) for page in (16, 64)]
+CALLS += [(f"attention kv{kv} group {group}", lambda api, a=(kv, 128, group): forward(api, *a))
+          for kv in (0, 1, 2) for group in (16, 32, 64, 128)]
+CALLS += [(f"latent attention kv{kv}", lambda api, kv=kv: forward(api, kv, 576, 64, latent=True)) for kv in (0, 1)]
+CALLS += [(f"attention of two sources, group {group}", lambda api, group=group: forward(api, 0, 128, group, 0, extra=True))
+          for group in (1, 2, 4)]
+CALLS += [("matmul", matmul)]
 
 
 @pytest.mark.parametrize("call", [c for _, c in CALLS], ids=[n for n, _ in CALLS])
