@@ -23,6 +23,7 @@
 // fewer registers (20, 24) took 145 and 204 us against 141 at that step.
 #include <cstring>
 
+#include "copies.cuh"
 #include "tree_parts.cuh"
 
 namespace da {
@@ -315,13 +316,6 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
   c.first = first;
   c.units = first[p.rows];
   if ((int)blockIdx.x >= c.units) return;
-  if (p.test_stall) {  // the time-out's test: a wait that runs out
-    const unsigned long long t0 = globaltimer_ns();
-    while (!mbar_try_wait(smem_addr(bars + kWarps * F::kStages), 0) && globaltimer_ns() - t0 < kTestStallNs) {
-    }
-    if (threadIdx.x == 0) report(p.err, DA_DEVERR_TIMEOUT);
-    return;
-  }
 
   // ---- copies run ahead of their use by kStages - 1 tiles, lookups by two more
   uint8_t* const mine = stages + warp * (F::kStages * F::kStage);
@@ -330,8 +324,11 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
   const uint32_t full = smem_addr(bars + warp * F::kStages);
   const uint32_t k_off = chunk_at<F::kRow / 16>(g, F::kKPiece == 4 ? F::k_chunk(q, 0) : q / 2) + (F::kKPiece == 4 ? 0 : 8 * (q & 1));
   const uint32_t v_off = chunk_at<F::kRow / 16>(2 * q, g * F::kVPiece / 4) + g * F::kVPiece % 4 * 4;
-  uint32_t by_tma = 0, parity = 0;  // bits of the stages: what fills them, the phase to wait for
-  bool dead = false;                // a wait ran out
+  Copies boxed;  // the TMA's
+  // (all lanes wait: each of them reads what has arrived)
+  auto landed = [&](int stage, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(full + 8 * stage, parity)) != 0;
+  };
   bool bad = false;
   int ahead_u = (int)blockIdx.x - (int)gridDim.x, ahead_n = 0, ahead_i = 0, ahead_end = 0;
   int spots = -1, next_spots = -1;  // of two tiles' entries (lanes 0 to 15, 16 to 31), and the two behind them
@@ -370,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
     if (tiles > 0) look_up();
   };
   auto copy_next = [&]() {
-    if (tiles > 0 && !dead) {
+    if (tiles > 0 && !boxed.lost) {
       const uint32_t dst = mine_at + to_stage * F::kStage;
       const bool all = (__ballot_sync(0xffffffffu, spots >= 0) >> half & 0xffffu) == 0xffffu;
       if (F::kBoxes && all && boxes) {  // 16 entries in a row
@@ -387,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
           }
         }
         __syncwarp();
-        by_tma |= 1u << to_stage;
+        boxed.sent(to_stage);
       } else if (all) {
         copy_rows<KT, D, NT, true>(p, spots, half, dst, lane);
       } else {
@@ -403,6 +400,17 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
   look_up();
   take_lookup();
   for (int i = 0; i < F::kStages - 1; ++i) copy_next();
+  if (p.test_stall) {  // the time-out's test: a wait that runs out, of the first copy if that is the TMA's
+    auto stalled = [&](int, uint32_t) {
+      const unsigned long long t0 = globaltimer_ns();
+      while (!mbar_try_wait(smem_addr(bars + kWarps * F::kStages), 0) && globaltimer_ns() - t0 < kTestStallNs) {
+      }
+      __syncwarp();
+      return false;
+    };
+    boxed.wait(0, stalled);
+    if (!boxed.lost) boxed.lost = !stalled(0, 0);
+  }
   int at_stage = 0, free_stage = F::kStages - 1;  // the stage in use, and the one before it
   uint32_t qb[F::kQHeld][D / 16][2];
   auto load_q = [&](const Unit* z) {
@@ -425,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
   // (after a time-out nothing is looked up)
   auto unit_at = [&](int u, int n) -> const Unit* {
     Unit* const z = &units[warp][n % kUnitSlots];
-    if (dead) {
+    if (boxed.lost) {
       const Unit v = unit_of(p, c, u);
       __syncwarp();
       if (lane == 0) *z = v;
@@ -502,12 +510,7 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
     }
     for (int i = begin; i < end; ++i) {
       cp_async_wait<F::kStages - 2>();
-      if (by_tma >> at_stage & 1 && !dead) {
-        dead = __any_sync(0xffffffffu, !mbar_wait(full + 8 * at_stage, parity >> at_stage & 1));
-        by_tma ^= 1u << at_stage;
-        parity ^= 1u << at_stage;
-        if (dead && lane == 0) report(p.err, DA_DEVERR_TIMEOUT);
-      }
+      boxed.wait(at_stage, landed);
       __syncwarp();
       const uint8_t* stage = mine + at_stage * F::kStage;
       HeldK<KT, D, NT> held;
@@ -648,6 +651,7 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
+          if (boxed.lost) continue;  // (a copy may be on its way there)
           if (F::kPassRows == 8 && nt != pass) continue;
           if (F::kPassRows == 4 && 2 * nt + r != pass) continue;
           const int at = F::kPassRows == 4 ? q : F::kPassRows == 8 ? 2 * q + r : 8 * nt + 2 * q + r;
@@ -724,8 +728,10 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
     x = next;
   }
   cp_async_wait<0>();
-  for (int st = 0; dead && st < F::kStages; ++st)  // leave no copy in flight
-    if (by_tma >> st & 1) mbar_wait(full + 8 * st, parity >> st & 1);
+  if (boxed.lost) {  // leave no copy in flight
+    boxed.drain(F::kStages, landed);
+    if (lane == 0) report(p.err, DA_DEVERR_TIMEOUT);
+  }
   if (__any_sync(0xffffffffu, bad) && lane == 0) report(p.err, DA_DEVERR_INDEX);
 }
 

@@ -501,6 +501,40 @@ def test_time_out_path(api, kv, heads):
 
 
 @gpu
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("layout,page", [("paged", 16), ("contiguous", 0)])
+@pytest.mark.parametrize("T", [1, 5])
+def test_time_out_with_copies_on_their_way(api, kv, layout, page, T):
+    """Few rows, entries copied in boxes: every wait for one runs out, in blocks that have
+    several units each.  Other calls beside it and after it are as ever."""
+    rng = np.random.default_rng(23)
+    c = Case(api, kv=kv, T=T, lengths=[int(x) for x in rng.integers(0, 1500, 200)], heads=(16, 4, 128), layout=layout,
+             page=page, seed=23)
+    b = Case(api, kv=kv, T=T, lengths=[1100, 30, 400], heads=(16, 4, 128), layout=layout, page=page, seed=24)
+    want = [x.run(api) for x in (c, b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    inputs = [(x.prob, x.q.cuda(), x.kc.cuda(), x.vc.cuda(), x.i32(x.lengths)) for x in (c, b)]
+    more = [dict(parents=x.i32(x.parents), table=None if x.table is None else x.table.cuda(), ws=api.tree_workspace(x.prob, T))
+            for x in (c, b)]
+    for _ in range(3):
+        err, none = (torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2))
+        outs = [(torch.full_like(inputs[i][1], 7.0), torch.full(inputs[i][1].shape[:3], 7.0, device="cuda"))
+                for i in (0, 0, 1, 1, 1)]
+        torch.cuda.synchronize()
+        c.prob.flags = api.FLAG_TEST_STALL
+        api.tree(*inputs[0], **more[0], out=outs[0][0], lse=outs[0][1], err=err, stream=streams[0])
+        c.prob.flags = 0
+        for out, lse in outs[2:]:
+            api.tree(*inputs[1], **more[1], out=out, lse=lse, err=none, stream=streams[1])
+        api.tree(*inputs[0], **more[0], out=outs[1][0], lse=outs[1][1], err=none, stream=streams[0])
+        torch.cuda.synchronize()
+        assert int(err) == api.DEVERR_TIMEOUT and int(none) == 0
+        assert (outs[0][0] != 7.0).any()  # the units were gone through
+        for i, (out, lse) in zip((0, 1, 1, 1), outs[1:]):
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+@gpu
 @pytest.mark.parametrize("kv", KV)
 @pytest.mark.parametrize("H_q,T", [(8, 3), (128, 3)])
 def test_caches_beyond_32_bits(api, kv, H_q, T):
