@@ -404,8 +404,8 @@ typedef struct da_head_norm {
  *           layouts (an indexed cache has its slots in rows already).  An entry
  *           out of [0, capacity) or a negative position sets DA_DEVERR_LENGTH and
  *           the token is left out.
- * Everything else is as for decode_attn_append; a token's results depend on that
- * token alone. */
+ * q_out overlaps neither the weights nor entries.  Everything else is as for
+ * decode_attn_append; a token's results depend on that token alone. */
 int decode_attn_append_norm(const da_problem* prob, const da_rope* rope, const da_head_norm* norm,
                             const da_append* args, const int32_t* entries, void* stream);
 

@@ -654,6 +654,11 @@ static int append_impl(const da_problem* prob, const da_rope* rope, const da_hea
     const uintptr_t src_end = src + ((n - 1) * strides[i] + least[i]) * esize;
     if (dst < src_end && src < dst + n * q_row * 2) return DA_ERR_INVALID_ARG;
   }
+  const void* read[3] = {norms ? norm->q_weight : nullptr, norms ? norm->k_weight : nullptr, entries};
+  const long long weight_bytes = norms ? D * (norm->w_dtype == DA_X_BF16 ? 2 : 4) : 0;
+  const long long read_bytes[3] = {weight_bytes, weight_bytes, 4 * n};
+  for (int i = 0; i < 3 && a.q_out; ++i)  // (by the threads of every token)
+    if (read[i] && overlap(a.q_out, n * q_row * 2, read[i], read_bytes[i])) return DA_ERR_INVALID_ARG;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DA_ERR_CUDA;
   const int sms = sm_count(dev);

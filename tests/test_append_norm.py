@@ -301,6 +301,27 @@ def test_argument_rules(api):
     assert call(args=packed(api, n=0)) == api.OK
 
 
+def test_queries_over_weights_or_entries(api):
+    """What the threads of every token read is not to be written by any of them."""
+    prob = api.problem(batch=2, num_q_heads=8, num_kv_heads=2, head_dim_qk=128, layout="paged", scale=0.1, page_size=16,
+                       width=8, num_blocks=20)
+    q_out, end = 1 << 28, (1 << 28) + 2 * 8 * 128 * 2
+
+    def call(dtype=api.X_BF16, entries=0, q_weight=1 << 12, k_weight=1 << 13):
+        n = api.DaHeadNorm(q_weight, k_weight, dtype, 0.0, 1e-6)
+        return api.lib().decode_attn_append_norm(ctypes.addressof(prob), None, ctypes.addressof(n), packed(api),
+                                                 entries or None, None)
+
+    over = [dict(q_weight=q_out), dict(k_weight=end - 16), dict(q_weight=q_out - 256 + 16),
+            dict(dtype=api.X_F32, k_weight=q_out - 512 + 16), dict(entries=end - 4), dict(entries=q_out - 4),
+            dict(entries=q_out + 64)]
+    for kw in over:
+        assert call(**kw) == api.ERR_INVALID_ARG, kw
+    if not torch.cuda.is_available():  # (the addresses are no one's)
+        for kw in (dict(), dict(q_weight=end), dict(k_weight=q_out - 256), dict(entries=q_out - 8), dict(entries=end)):
+            assert call(**kw) == api.ERR_CUDA, kw
+
+
 def test_python_checks(api):
     w = torch.ones(128)
     with pytest.raises(ValueError, match="needs"):
