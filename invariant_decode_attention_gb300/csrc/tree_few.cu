@@ -408,8 +408,15 @@ __global__ void __launch_bounds__(kThreads, Few<KT, D, NT>::kResident)
       __syncwarp();
       return false;
     };
-    boxed.wait(0, stalled);
-    if (!boxed.lost) boxed.lost = !stalled(0, 0);
+    if constexpr (F::kBoxes) {
+      boxed.wait(0, stalled);
+      if (!boxed.lost) boxed.lost = !stalled(0, 0);
+    } else {  // the lanes' own copies have no wait that could run out, and the loops below no test for it
+      stalled(0, 0);
+      cp_async_wait<0>();
+      if (threadIdx.x == 0) report(p.err, DA_DEVERR_TIMEOUT);
+      return;
+    }
   }
   int at_stage = 0, free_stage = F::kStages - 1;  // the stage in use, and the one before it
   uint32_t qb[F::kQHeld][D / 16][2];
