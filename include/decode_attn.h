@@ -452,6 +452,10 @@ int decode_attn_tree_workspace_bytes(const da_problem* prob, int32_t nodes, size
  * Entries that a node does not see have no effect on it, whatever they hold, NaN and
  * infinities included.
  * Rows past counts[b] of q are not read, those of out and lse left as they are.
+ * Weights are rounded to bf16 (bf16 caches) or f16 (the others) before they multiply
+ * the values, also where decode_attn_run keeps fp32 weights (fewer than 16 query heads
+ * a KV head): over bf16 caches an output is off by up to 2^-8 of its weighted sum of
+ * |v| besides its own rounding.  lse is not affected.
  *
  * A row's list is cut into splits whose number follows from the row's own list and
  * number of nodes (and the window), and the kernel is chosen by the problem and T: a

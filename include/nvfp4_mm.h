@@ -270,7 +270,7 @@ size_t nvfp4_mm_verify_workspace_bytes(int32_t batch, int32_t nodes, int32_t voc
  * -inf or NaN).
  *
  * exp((x - max) / temperature) is an integer of units of 2^-44, off by about 2^-38 of its
- * size, so that the sums for the next token are exact; p at the drafted tokens is that over
+ * size (and by half a unit: below 2^-45 it is nothing, and such a token is never drawn), so that the sums for the next token are exact; p at the drafted tokens is that over
  * an fp32 sum.  A request's results depend on that request alone.  NaN logits count as -inf; if the
  * largest is +inf, the tokens that have it share everything.  Temperatures other than 0
  * are taken within [2^-100, 2^100], negative ones and NaN as 0; uniforms within [0, 1),

@@ -11,13 +11,24 @@
 // with few such pairs go to tree_few.cu.  What a node sees is a 64-bit mask of nodes, found
 // once a unit; whole tiles of context need no mask.
 //
+// Weights are rounded before the second product: an MMA takes both operands in one type, so
+// that they are bf16 beside bf16 values (off by 2^-8 of their size at most) and f16 beside f16
+// ones (2^-11; formed with a largest one of 2^7 or more).  The sum that divides them is of the
+// unrounded ones, in fp32.  Over bf16 caches outputs are off by 0.0023 (root mean square,
+// relative), 0.0017 of it by their own rounding; a second term of each weight would take a
+// second product.
+//
 // Bound: bytes of K and V for one row's nodes; the softmax (a thread a row, 64 exponentials a
 // tile) and the way from MMA to softmax to MMA for full units of 128.  Measured, captured and
 // replayed, bf16, 64-entry tiles: 32 rows of 16 nodes, 32/8 heads, 8192 entries, 171 us = 4.8
 // TB/s (copied once at the measured bandwidth: 120 us); 8 rows of 64 nodes, 64/8 heads, 16384
-// entries, 230 us = 675 TFLOP/s.  Two blocks an SM, one unit each, because everything in a
-// block waits for something: between MMA, softmax and MMA, and for 13,500 cycles between
-// units; one block with two units in flight took 204 us.  Also measured and not kept,
+// entries, 230 us = 675 TFLOP/s; 64 rows of 16 nodes, 4096 of 32768 entries in their window,
+// 32/8 heads, E4M3 397 us and NVFP4 513 (81 and 47): two operand stages, each held from the
+// widening of its K to the end of its P V, keep widening and softmax close together.
+//
+// Two blocks an SM, one unit each, because everything in a block waits for something:
+// between MMA, softmax and MMA, and for 13,500 cycles between units; one block with two units
+// in flight took 204 us.  Also measured and not kept,
 // on the first and the second of these: warps of their own for the output (258, 493), K and V
 // in rings of their own with P apart (197, 259), MMAs issued by an elected lane of a whole warp (198, 270), a unit's
 // split chosen for equal units (188, 237: the blocks run in step), copies of Q and output by

@@ -66,9 +66,9 @@ cudaError_t launch_tree_combine(const TreeLaunch& p, cudaStream_t stream);
 
 // Whether tree_few.cu takes a call with this many (node, head) rows a KV head at most, whose
 // cost grows with the rows, where tree.cu's is the same up to 128.  A windowed step of 64 rows
-// with 4096 entries each and 8 KV heads, here against there, in us: 16 rows E4M3 207, 424, bf16
-// 224, 268; 32 rows E4M3 308, 438, NVFP4 311, 625, bf16 321, 281; 24 rows bf16 252, 273; 32 rows
-// of 64 dims, bf16, 199, 233.
+// with 4096 entries each and 8 KV heads, here against there, in us: 16 rows E4M3 206, 424, bf16
+// 223, 268; 32 rows E4M3 306, 438, NVFP4 305, 625, bf16 321, 281; 24 rows bf16 251, 273; 32 rows
+// of 64 dims, bf16, 196, 233.
 inline bool tree_takes_few(int kv_type, int D, int rows) {
   return rows <= (kv_type == DA_KV_BF16 && D == 128 ? 24 : 32);
 }

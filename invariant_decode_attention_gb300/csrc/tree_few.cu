@@ -6,15 +6,16 @@
 // 16 entries of K (or 16 dims of V) on the wide side and 8 rows on the narrow one.  The order of
 // the dims in Q K^T, and of the entries in P V, is free, so a lane takes chunks of a cache row
 // just as they lie in memory, widens them in registers, and holds the right operand: no value
-// changes hands but the weights, by one 8 x 8 transpose.  A row's reference value and sum lie
-// with the lanes that have its weights and its output.
+// changes hands but the weights, by one 8 x 8 transpose, rounded to the values' type as in
+// tree.cu.  A row's reference value and sum lie with the lanes that have its weights and its output.
 //
 // A block has a unit of a list (tree.cuh's splits), its four warps 16 entries of each tile; they
-// meet once a unit, to join their sums.  Bound: the instructions that widen and multiply (about
-// 300 a warp and 16 entries) and, for bf16, the cache's bytes.  Measured, captured and replayed,
-// 64 rows of one node with 4096 of 32768 entries in their window: 32/8 heads E4M3 111 us = 4.9
-// TB/s (floor 79), bf16 177 us = 6.1 TB/s (159), NVFP4 110 us (45); 128/8 heads E4M3 207 us.  By
-// tiles of 128 rows the first took 415 us.  Steps: values loaded into registers a step ahead,
+// meet once a unit, to join their sums.  Bound: for bf16 the cache's bytes; else a warp's way
+// through a tile, about 300 instructions that widen and multiply, most of which wait for the one
+// before (0.53 of the issue slots used, so that their number is not a limit yet).  Measured,
+// captured and replayed, 64 rows of one node with 4096 of 32768 entries in their window: 32/8
+// heads E4M3 110 us = 4.9 TB/s (floor 79), bf16 177 us = 6.1 TB/s (159), NVFP4 108 us (45);
+// 128/8 heads E4M3 206 us.  By tiles of 128 rows the first took 415 us.  Steps: values loaded into registers a step ahead,
 // 196 us; by way of stages in shared memory, three or so steps ahead, 147; whole 128-byte lines
 // a copy instead of the lane's own chunks, 119 (the SM pays by the lines that a copy touches:
 // 64-byte pieces of K cost as much); boxes by the TMA, the next

@@ -19,10 +19,11 @@
 // Measured, captured and replayed: 64 chains of seven drafted tokens, 131072 fp32 logits a
 // node and a draft's probabilities, 112 us (35 at the measured bandwidth); 32 trees of 16
 // nodes, 50001 bf16 logits, 31 us (6); one chain of three, 32000 logits, 11.4 us, two
-// launches and the steps of the walk one after another.  The large call is bound by
-// instructions: rows_kernel takes some 40 us of it, and the walk two passes of weights over
-// the row where it ended, about 110 instructions a weight and pass (0.56 of the issue slots
-// used).  The weights of the first pass held in registers for the second took 123 us: one CTA
+// launches and the steps of the walk one after another.  Of the large
+// call rows_kernel takes some 40 us, the walk the rest: two passes of weights over the row
+// where it ended, about 110 instructions a weight and pass, most of them one after another
+// (0.56 of the issue slots used: less work a weight would help, and so would more weights
+// at once).  The weights of the first pass held in registers for the second took 123 us: one CTA
 // an SM fits then.
 #include <algorithm>
 #include <cmath>
