@@ -5,7 +5,6 @@ is computed and no GPU is used."""
 
 import ctypes
 import os
-import shutil
 import subprocess
 
 import pytest
@@ -79,7 +78,7 @@ def api(tmp_path_factory):
     folder = tmp_path_factory.mktemp("runtime")
     source, path = folder / "runtime.cc", folder / "libstandin.so"
     source.write_text(RUNTIME)
-    include = os.path.join(os.path.dirname(os.path.dirname(shutil.which("nvcc") or B.nvcc())), "include")
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(B.nvcc()))), "include")
     objects = [os.path.join(B.OBJ_DIR, f + ".o") for f in sorted(os.listdir(B.CSRC)) if f.endswith(".cu")]
     if not all(os.path.exists(o) for o in objects):
         B.build()
